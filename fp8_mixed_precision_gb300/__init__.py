@@ -21,6 +21,9 @@ __all__ = [
     "fp8_launch_count", "fp8_profile_begin", "fp8_profile_end", "WeightCache", "LinearContext",
     "fp8_quantize_delayed", "fp8_debug_wait_timeout", "HostPipeline", "amax_partials_buffer",
     "fp8_amax_partials", "fp8_linear_fwd_after_amax", "fp8_linear_bwd_after_amax",
+    "ACTIVATION", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "rmsnorm_buffers", "rmsnorm_workspace",
+    "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd", "GatedContext", "gated_context",
+    "gated_workspace", "fp8_gated_ctx_layout", "GradClip",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +33,9 @@ RECIPE = {"tensorwise": 0, "block": 1, "delayed": 2}
 ROLE = {"act": 0, "weight": 1, "grad": 2}
 FORMAT = {"e4m3": 0, "e5m2": 1}
 SCALING = {"tensor": 0, "1x128_128x128": 1, "1x128_1x128": 2}
+
+ACTIVATION = {"silu": 0, "gelu": 1}
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
@@ -108,6 +114,37 @@ _SIGS.update({
     "fp8_host_pipeline_fork": (_c_int, [_c_p, _c_p]),
     "fp8_host_pipeline_join": (_c_int, [_c_p, _c_p]),
     "fp8_host_pipeline_sync": (_c_int, [_c_p]),
+})
+
+
+class _GradDesc(ctypes.Structure):
+    _fields_ = [("src", _c_p), ("dst", _c_p), ("n", _c_i64), ("dtype", _c_int)]
+
+
+_SIGS.update({
+    "fp8_rmsnorm_fwd": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, ctypes.c_float] +
+                        [_c_p] * 10),
+    "fp8_rmsnorm_workspace_size": (_c_int, [_c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fp8_rmsnorm_bwd": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, _c_p, _c_p,
+                                 _c_p, _c_sz, _c_p]),
+    "fp8_gated_ctx_size": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fp8_gated_ctx_layout": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, _c_p] +
+                             [ctypes.POINTER(_c_p)] * 5),
+    "fp8_gated_workspace_size": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, _c_int,
+                                          ctypes.POINTER(_c_sz)]),
+    "fp8_gated_fwd": (_c_int, [_c_p, _c_i64, _c_i64, _c_p, ctypes.c_int32, _c_int, _c_int, _c_p,
+                               _c_p, _c_p, _c_sz, _c_p]),
+    "fp8_gated_fwd_quantized": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int32, _c_int,
+                                         _c_int, _c_p, _c_p, _c_p]),
+    "fp8_gated_bwd": (_c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, ctypes.c_int32, _c_int, _c_int,
+                               _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "fp8_grad_clip_create": (_c_int, [ctypes.POINTER(_GradDesc), _c_i64, ctypes.POINTER(_c_p)]),
+    "fp8_grad_clip_destroy": (None, [_c_p]),
+    "fp8_grad_clip_table_size": (_c_int, [_c_p, ctypes.POINTER(_c_sz)]),
+    "fp8_grad_clip_table_write": (_c_int, [_c_p, _c_p, _c_sz]),
+    "fp8_grad_clip_workspace_size": (_c_int, [_c_p, ctypes.POINTER(_c_sz)]),
+    "fp8_grad_clip_run": (_c_int, [_c_p, _c_p, ctypes.c_float, _c_p, _c_p, _c_sz, _c_p]),
+    "fp8_grad_norm": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
 })
 
 
@@ -607,3 +644,260 @@ def fp8_linear_bwd_after_amax(dy: torch.Tensor, dy_partials: torch.Tensor, ctx: 
                                            _ptr(ws), ws.numel(), _stream(stream)),
            "fp8_linear_bwd_after_amax")
     return dx, dw
+
+
+# ---------------------------------------------------------------- RMS norm
+def _need(t, name, shape, dtype):
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == tuple(shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+
+
+def rmsnorm_buffers(R: int, C: int, device, residual: bool = True, rowwise: bool = True,
+                    colwise: bool = True, bf16: bool = False) -> dict:
+    """Output buffers of fp8_rmsnorm_fwd for an [R, C] input, to be passed as
+    `out` by callers that keep them between calls (absent outputs are None)."""
+    Rp, nb, rb = -(-R // 16) * 16, -(-C // 128), -(-R // 128)
+
+    def f32(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=device)
+
+    return dict(r=torch.empty((R, C), dtype=torch.bfloat16, device=device) if residual else None,
+                rstd=f32(R), y=torch.empty((R, C), dtype=torch.bfloat16, device=device) if bf16 else None,
+                row=torch.empty((R, C), dtype=torch.uint8, device=device) if rowwise else None,
+                row_scale=f32(R, nb) if rowwise else None,
+                row_scale_inv=f32(R, nb) if rowwise else None,
+                col=torch.empty((C, Rp), dtype=torch.uint8, device=device) if colwise else None,
+                col_scale=f32(C, rb) if colwise else None,
+                col_scale_inv=f32(C, rb) if colwise else None)
+
+
+def rmsnorm_workspace(R: int, C: int, device) -> torch.Tensor:
+    b = _c_sz()
+    _check(lib().fp8_rmsnorm_workspace_size(R, C, ctypes.byref(b)), "fp8_rmsnorm_workspace_size")
+    return _empty_bytes(b.value, device)
+
+
+def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None = None,
+                    eps: float = 1e-6, rowwise: bool = True, colwise: bool = True,
+                    bf16: bool = False, out: dict | None = None, stream=None) -> dict:
+    """Residual addition, RMS norm and FP8 output of a bf16 [R, C] x; w is a
+    bf16 or float32 [C].  Returns dict(r, rstd, y, row, row_scale,
+    row_scale_inv, col, col_scale, col_scale_inv), absent ones None: r is the
+    residual stream bf16(x + residual) (x itself without a residual), row
+    [R, C] and col [C, R rounded up to 16] the E4M3 bytes of the norm in 1x128
+    blocks, y the norm in bf16.  out: buffers of rmsnorm_buffers to write."""
+    _need_bf16_cuda(x, "x")
+    R, C = x.shape
+    if w.dtype not in _DTYPE:
+        raise ValueError("w must be bf16 or float32")
+    _need(w, "w", (C,), w.dtype)
+    if residual is not None:
+        _need(residual, "residual", (R, C), torch.bfloat16)
+    if out is None:
+        out = rmsnorm_buffers(R, C, x.device, residual is not None, rowwise, colwise, bf16)
+    o = out
+    Rp = -(-R // 16) * 16
+    for key, want, shape, dtype in (("r", residual is not None, (R, C), torch.bfloat16),
+                                    ("y", bf16, (R, C), torch.bfloat16),
+                                    ("row", rowwise, (R, C), torch.uint8),
+                                    ("col", colwise, (C, Rp), torch.uint8)):
+        if want:
+            if o[key] is None:
+                raise ValueError(f"out has no buffer for {key}")
+            _need(o[key], key, shape, dtype)
+    _check(lib().fp8_rmsnorm_fwd(
+        _ptr(x), _ptr(residual), _ptr(w), _DTYPE[w.dtype], R, C, eps,
+        _ptr(o["r"]) if residual is not None else None, _ptr(o["rstd"]),
+        _ptr(o["y"]) if bf16 else None, _ptr(o["row"]) if rowwise else None,
+        _ptr(o["col"]) if colwise else None, _ptr(o["row_scale"]), _ptr(o["row_scale_inv"]),
+        _ptr(o["col_scale"]), _ptr(o["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
+    return out if residual is not None else dict(out, r=x)
+
+
+def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: torch.Tensor,
+                    dr: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                    dw: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Returns (dx, dw): dx bf16, the gradient of x and of the residual, dw
+    float32; dr is the gradient that the stream r has from elsewhere."""
+    _need_bf16_cuda(dy, "dy")
+    R, C = dy.shape
+    _need(r, "r", (R, C), torch.bfloat16)
+    _need(rstd, "rstd", (R,), torch.float32)
+    if w.dtype not in _DTYPE:
+        raise ValueError("w must be bf16 or float32")
+    _need(w, "w", (C,), w.dtype)
+    if dr is not None:
+        _need(dr, "dr", (R, C), torch.bfloat16)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dw is None:
+        dw = torch.empty(C, dtype=torch.float32, device=dy.device)
+    _need(dx, "dx", (R, C), torch.bfloat16)
+    _need(dw, "dw", (C,), torch.float32)
+    if ws is None:
+        ws = rmsnorm_workspace(R, C, dy.device)
+    _check(lib().fp8_rmsnorm_bwd(_ptr(dy), _ptr(dr), _ptr(r), _ptr(rstd), _ptr(w), _DTYPE[w.dtype],
+                                 R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
+           "fp8_rmsnorm_bwd")
+    return dx, dw
+
+
+# ---------------------------------------------------------------- gated feed-forward
+@dataclass
+class GatedContext:
+    """What a gated forward pass keeps for its backward pass: the device buffer,
+    its shape, and the activation (set by the forward pass)."""
+    ctx: torch.Tensor
+    N: int
+    K: int
+    F: int
+    act: str = "silu"
+
+
+def gated_context(recipe: str, N: int, K: int, F: int, device) -> GatedContext:
+    b = _c_sz()
+    _check(lib().fp8_gated_ctx_size(RECIPE[recipe], N, K, F, ctypes.byref(b)), "fp8_gated_ctx_size")
+    return GatedContext(_empty_bytes(b.value, device), N, K, F)
+
+
+def gated_workspace(recipe: str, N: int, K: int, F: int, device, train: bool = True) -> torch.Tensor:
+    b = _c_sz()
+    _check(lib().fp8_gated_workspace_size(RECIPE[recipe], N, K, F, int(train), ctypes.byref(b)),
+           "fp8_gated_workspace_size")
+    return _empty_bytes(b.value, device)
+
+
+def fp8_gated_ctx_layout(recipe: str, ctx: GatedContext):
+    """Device pointers inside ctx: (transposed FP8 input, its scale, its
+    scale_inv, G, U)."""
+    p = [_c_p() for _ in range(5)]
+    _check(lib().fp8_gated_ctx_layout(RECIPE[recipe], ctx.N, ctx.K, ctx.F, _ptr(ctx.ctx),
+                                      *[ctypes.byref(q) for q in p]), "fp8_gated_ctx_layout")
+    return tuple(p)
+
+
+def _gated_out(N, K, cache, h, recipe, y, ctx, train, device):
+    if not 0 <= h < len(cache.entries):
+        raise ValueError("no such weight handle")
+    F = cache.entries[h].w.shape[0] // 2
+    if y is None:
+        y = torch.empty((N, F), dtype=torch.bfloat16, device=device)
+    _need(y, "y", (N, F), torch.bfloat16)
+    if train and ctx is None:
+        ctx = gated_context(recipe, N, K, F, device)
+    if train and (ctx.N, ctx.K, ctx.F) != (N, K, F):
+        raise ValueError("ctx was made for another shape")
+    return F, y, ctx if train else None
+
+
+def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act: str = "silu",
+                  train: bool = True, ws: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                  ctx: GatedContext | None = None, stream=None):
+    """H = act(X Wg^T) * (X Wu^T) for the weight [Wg; Wu] of handle h; returns
+    (H, GatedContext), the context None with train=False."""
+    _need_bf16_cuda(x, "x")
+    N, K = x.shape
+    F, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, train, x.device)
+    if ws is None:
+        ws = gated_workspace(recipe, N, K, F, x.device, train=False)
+    _check(lib().fp8_gated_fwd(_ptr(x), N, K, cache.handle, h, RECIPE[recipe], ACTIVATION[act],
+                               _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws), ws.numel(),
+                               _stream(stream)), "fp8_gated_fwd")
+    if train:
+        ctx.act = act
+    return y, ctx
+
+
+def fp8_gated_fwd_quantized(row: torch.Tensor, row_scale_inv: torch.Tensor, cache: WeightCache,
+                            h: int, recipe: str, act: str = "silu", y: torch.Tensor | None = None,
+                            ctx: GatedContext | None = None, stream=None):
+    """fp8_gated_fwd on an input given as E4M3 bytes [N, K] and scale_inv; with
+    ctx its transposed part (fp8_gated_ctx_layout) is already filled."""
+    if not (row.is_cuda and row.dtype == torch.uint8 and row.is_contiguous()):
+        raise ValueError("row must be a contiguous uint8 CUDA tensor")
+    N, K = row.shape
+    _, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, ctx is not None, row.device)
+    _check(lib().fp8_gated_fwd_quantized(_ptr(row), _ptr(row_scale_inv), N, K, cache.handle, h,
+                                         RECIPE[recipe], ACTIVATION[act], _ptr(y),
+                                         None if ctx is None else _ptr(ctx.ctx), _stream(stream)),
+           "fp8_gated_fwd_quantized")
+    if ctx is not None:
+        ctx.act = act
+    return y, ctx
+
+
+def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: int, recipe: str,
+                  need_dx: bool = True, ws: torch.Tensor | None = None,
+                  dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
+    """Returns (dX or None, dW [2F, K]) of the forward pass that made ctx."""
+    _need(dh, "dh", (ctx.N, ctx.F), torch.bfloat16)
+    N, K, F, dev = ctx.N, ctx.K, ctx.F, dh.device
+    if need_dx and dx is None:
+        dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+    if dw is None:
+        dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=dev)
+    if need_dx:
+        _need(dx, "dx", (N, K), torch.bfloat16)
+    _need(dw, "dw", (2 * F, K), torch.bfloat16)
+    if ws is None:
+        ws = gated_workspace(recipe, N, K, F, dev)
+    _check(lib().fp8_gated_bwd(_ptr(dh), N, F, _ptr(ctx.ctx), cache.handle, h, RECIPE[recipe],
+                               ACTIVATION[ctx.act], _ptr(dx) if need_dx else None, _ptr(dw),
+                               _ptr(ws), ws.numel(), _stream(stream)), "fp8_gated_bwd")
+    return (dx if need_dx else None), dw
+
+
+# ---------------------------------------------------------------- gradient clipping
+class GradClip:
+    """Global norm and clipping of a fixed set of gradient tensors (bf16 or
+    float32, contiguous, any sizes).  out: tensors of the same types and sizes
+    that take the clipped gradients; by default the gradients themselves."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError("out must have one tensor per gradient")
+        for g, o in zip(self.grads, self.out):
+            if g.dtype not in _DTYPE:
+                raise ValueError("gradients must be bf16 or float32")
+            _need(g, "gradient", g.shape, g.dtype)
+            _need(o, "out", g.shape, g.dtype)
+        n = len(self.grads)
+        descs = (_GradDesc * max(n, 1))(*[_GradDesc(g.data_ptr(), o.data_ptr(), g.numel(),
+                                                    _DTYPE[g.dtype])
+                                          for g, o in zip(self.grads, self.out)])
+        h = _c_p()
+        _check(lib().fp8_grad_clip_create(descs, n, ctypes.byref(h)), "fp8_grad_clip_create")
+        self._h = h
+        b = _c_sz()
+        _check(lib().fp8_grad_clip_table_size(h, ctypes.byref(b)), "fp8_grad_clip_table_size")
+        host = torch.empty(max(b.value, 16), dtype=torch.uint8)
+        _check(lib().fp8_grad_clip_table_write(h, _ptr(host), host.numel()),
+               "fp8_grad_clip_table_write")
+        dev = self.grads[0].device if n else torch.device("cuda")
+        self._table = host.to(dev)
+        _check(lib().fp8_grad_clip_workspace_size(h, ctypes.byref(b)),
+               "fp8_grad_clip_workspace_size")
+        self._ws = _empty_bytes(b.value, dev)
+        self._norm = torch.empty(1, dtype=torch.float32, device=dev)
+
+    def clip(self, max_norm: float, stream=None):
+        """Scales the gradients to a global norm of at most max_norm; returns
+        (norm, out), the norm as a float32 device tensor of the unclipped
+        gradients.  A norm that is not finite leaves them as they are."""
+        _check(lib().fp8_grad_clip_run(self._h, _ptr(self._table), max_norm, _ptr(self._norm),
+                                       _ptr(self._ws), self._ws.numel(), _stream(stream)),
+               "fp8_grad_clip_run")
+        return self._norm, self.out
+
+    def norm(self, stream=None) -> torch.Tensor:
+        """The global norm alone (float32 device tensor, reused by later calls)."""
+        _check(lib().fp8_grad_norm(self._h, _ptr(self._table), _ptr(self._norm), _ptr(self._ws),
+                                   self._ws.numel(), _stream(stream)), "fp8_grad_norm")
+        return self._norm
+
+    def __del__(self):
+        if getattr(self, "_h", None) is not None and _lib is not None:
+            _lib.fp8_grad_clip_destroy(self._h)
+            self._h = None

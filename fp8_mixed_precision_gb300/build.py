@@ -24,7 +24,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
               "-I" + INCLUDE] + ARCH
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE]
 
-CU_SOURCES = ["quantize.cu", "gemm.cu", "glue.cu", "noalloc.cu"]
+CU_SOURCES = ["quantize.cu", "gemm.cu", "glue.cu", "noalloc.cu", "norm.cu",
+              "gated.cu", "clip.cu"]
 CXX_SOURCES = ["api.cpp"]
 
 

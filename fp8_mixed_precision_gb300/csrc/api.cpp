@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <tuple>
 #include <mutex>
 #include <new>
@@ -686,6 +687,356 @@ fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream
   return from_cuda(launch_grad_accumulate(acc, dW, n, cs(stream)));
 }
 
+// ---------------------------------------------------------------- RMS norm
+namespace {
+bool valid_dtype(int d) { return d == FP8_DTYPE_BF16 || d == FP8_DTYPE_F32; }
+fp8_status check_norm(int64_t rows, int64_t cols, int dtype) {
+  if (rows < 0 || cols < 0 || !valid_dtype(dtype)) return FP8_ERR_INVALID_ARG;
+  if (cols % 16 || rows > (int64_t(1) << 31) - 128) return FP8_ERR_SHAPE;
+  if (cols > kMaxNormCols) return FP8_ERR_UNSUPPORTED;
+  return FP8_OK;
+}
+inline int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+}  // namespace
+
+fp8_status fp8_rmsnorm_fwd(const void *x, const void *residual, const void *w, fp8_dtype w_dtype,
+                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd, void *y,
+                           uint8_t *rowwise_out, uint8_t *colwise_out, float *row_scale,
+                           float *row_scale_inv, float *col_scale, float *col_scale_inv,
+                           fp8_stream_t stream) {
+  fp8_status st = check_norm(rows, cols, w_dtype);
+  if (st != FP8_OK) return st;
+  if (!(eps > 0.0f)) return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if (!y && !rowwise_out && !colwise_out) return FP8_ERR_INVALID_ARG;
+  if ((residual != nullptr) != (r_out != nullptr)) return FP8_ERR_INVALID_ARG;
+  if (!x || !w || (rowwise_out && (!row_scale || !row_scale_inv)) ||
+      (colwise_out && (!col_scale || !col_scale_inv || !rstd)))
+    return FP8_ERR_INVALID_ARG;
+  for (const void *p : {x, residual, w, (const void *)r_out, (const void *)y,
+                        (const void *)rowwise_out, (const void *)colwise_out})
+    if (!aligned16(p)) return FP8_ERR_ALIGN;
+  st = from_cuda(launch_rmsnorm_rows(x, residual, w, w_dtype, rows, cols, eps, r_out, rstd, y,
+                                     rowwise_out, row_scale, row_scale_inv, cs(stream)));
+  if (st != FP8_OK || !colwise_out) return st;
+  return from_cuda(launch_rmsnorm_cols(residual ? r_out : x, rstd, w, w_dtype, rows, cols,
+                                       colwise_out, col_scale, col_scale_inv, cs(stream)));
+}
+
+fp8_status fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_norm(rows, cols, FP8_DTYPE_F32);
+  if (st != FP8_OK) return st;
+  *bytes = rows && cols ? (size_t)norm_bwd_ctas(rows, cols) * (size_t)cols * sizeof(float) : 0;
+  return FP8_OK;
+}
+
+fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const float *rstd,
+                           const void *w, fp8_dtype w_dtype, int64_t rows, int64_t cols, void *dx,
+                           float *dw, void *workspace, size_t workspace_bytes,
+                           fp8_stream_t stream) {
+  fp8_status st = check_norm(rows, cols, w_dtype);
+  if (st != FP8_OK) return st;
+  if (cols == 0) return FP8_OK;
+  if (!dw) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(dw)) return FP8_ERR_ALIGN;
+  if (rows == 0) return from_cuda(cudaMemsetAsync(dw, 0, (size_t)cols * 4, cs(stream)));
+  if (!dy || !r || !rstd || !w || !dx) return FP8_ERR_INVALID_ARG;
+  for (const void *p : {dy, dr, r, w, (const void *)dx, (const void *)workspace})
+    if (!aligned16(p)) return FP8_ERR_ALIGN;
+  size_t need = 0;
+  fp8_rmsnorm_workspace_size(rows, cols, &need);
+  if (workspace_bytes < need || !workspace) return FP8_ERR_WORKSPACE;
+  return from_cuda(launch_rmsnorm_bwd(dy, dr, r, rstd, w, w_dtype, rows, cols, dx, dw,
+                                      static_cast<float *>(workspace), cs(stream)));
+}
+
+// ---------------------------------------------------------------- gated feed-forward
+namespace {
+
+// Context of a gated forward pass: the linear's (transposed FP8 X and its
+// scales, for the token count rounded up to 16), then both projections.
+struct GatedCtx {
+  CtxLayout x;
+  size_t g, u, total;
+};
+GatedCtx gated_ctx(fp8_recipe recipe, int64_t N, int64_t K, int64_t F) {
+  GatedCtx L;
+  L.x = ctx_layout(recipe, round16(N), K);
+  L.g = L.x.total;
+  L.u = L.g + align_up((size_t)N * F * 2);
+  L.total = L.u + align_up((size_t)N * F * 2);
+  return L;
+}
+
+// Workspace regions, by byte offset (forward and backward share the buffer).
+struct GatedWs {
+  size_t xq, xs, xsi, part, fwd;             // forward: rowwise X, its scales, partials
+  size_t row, col, rsi, csi, bpart, gemm, bwd;  // backward: dGU, its scales, partials, GEMM scratch
+};
+GatedWs gated_ws(fp8_recipe recipe, int64_t N, int64_t K, int64_t F) {
+  const fp8_recipe ar = act_recipe(recipe);
+  GatedWs L;
+  Carver a(nullptr);
+  auto at = [](Carver &c, size_t bytes) {
+    const size_t o = c.off;
+    c.take<uint8_t>(bytes);
+    return o;
+  };
+  const size_t part = (size_t)kMaxPartials * sizeof(float);
+  const size_t nx = (size_t)scale_elems(ar, FP8_ROLE_ACT, N, K, 0) * 4;
+  L.xq = at(a, (size_t)N * K);
+  L.xs = at(a, nx);
+  L.xsi = at(a, nx);
+  L.part = at(a, part);
+  L.fwd = a.off;
+  Carver b(nullptr);
+  const int64_t Np = round16(N);
+  L.row = at(b, (size_t)N * 2 * F);
+  L.col = at(b, (size_t)Np * 2 * F);
+  L.rsi = at(b, (size_t)scale_elems(ar, FP8_ROLE_GRAD, N, 2 * F, 0) * 4);
+  L.csi = at(b, (size_t)scale_elems(ar, FP8_ROLE_GRAD, N, 2 * F, 1) * 4);
+  L.bpart = at(b, part);
+  L.gemm = at(b, std::max(gemm_workspace_bytes(N, K, 2 * F, fwd_scaling(ar)),
+                          gemm_workspace_bytes(2 * F, K, Np, wgrad_scaling(ar))));
+  L.bwd = b.off;
+  return L;
+}
+
+fp8_status check_gated(int recipe, int64_t N, int64_t K, int64_t F) {
+  if (!valid_linear_recipe(recipe) || N < 0 || K < 0 || F < 0) return FP8_ERR_INVALID_ARG;
+  if (K % 16 || F % 16 || (recipe == FP8_RECIPE_BLOCK && F % 128)) return FP8_ERR_SHAPE;
+  for (int64_t d : {N, K, F})
+    if (d > (int64_t(1) << 30)) return FP8_ERR_SHAPE;
+  return FP8_OK;
+}
+// The registered weight of a gated call, its handle, recipe, shape and state checked.
+fp8_status gated_entry(fp8_weight_cache *cache, fp8_weight_handle h, int recipe, int act, int64_t N,
+                       const fp8_weight_cache::Entry **out) {
+  if (!cache || h < 0 || (size_t)h >= cache->entries.size() ||
+      (act != FP8_ACT_SILU && act != FP8_ACT_GELU))
+    return FP8_ERR_INVALID_ARG;
+  const auto &e = cache->entries[h];
+  if (e.recipe != recipe) return FP8_ERR_INVALID_ARG;
+  if (e.O % 2) return FP8_ERR_SHAPE;
+  const fp8_status st = check_gated(recipe, N, e.K, e.O / 2);
+  if (st != FP8_OK) return st;
+  if (e.cycle != cache->cycle) return FP8_ERR_STALE;
+  *out = &e;
+  return FP8_OK;
+}
+
+}  // namespace
+
+fp8_status fp8_gated_ctx_size(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_gated(recipe, N, K, F);
+  if (st == FP8_OK) *bytes = gated_ctx(recipe, N, K, F).total;
+  return st;
+}
+
+fp8_status fp8_gated_ctx_layout(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, void *ctx,
+                                uint8_t **xq_col, float **col_scale, float **col_scale_inv,
+                                void **g, void **u) {
+  if (!ctx || !xq_col || !col_scale || !col_scale_inv || !g || !u) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_gated(recipe, N, K, F);
+  if (st != FP8_OK) return st;
+  const GatedCtx L = gated_ctx(recipe, N, K, F);
+  uint8_t *c = static_cast<uint8_t *>(ctx);
+  *xq_col = c + L.x.xq_col;
+  *col_scale = reinterpret_cast<float *>(c + L.x.scale);
+  *col_scale_inv = reinterpret_cast<float *>(c + L.x.scale_inv);
+  *g = c + L.g;
+  *u = c + L.u;
+  return FP8_OK;
+}
+
+fp8_status fp8_gated_workspace_size(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, int train,
+                                    size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_gated(recipe, N, K, F);
+  if (st != FP8_OK) return st;
+  const GatedWs L = gated_ws(recipe, N, K, F);
+  *bytes = train ? std::max(L.fwd, L.bwd) : L.fwd;
+  return FP8_OK;
+}
+
+fp8_status fp8_gated_fwd_quantized(const uint8_t *xq_row, const float *xq_row_scale_inv, int64_t N,
+                                   int64_t K, fp8_weight_cache *cache, fp8_weight_handle h,
+                                   fp8_recipe recipe, fp8_act act, void *H, void *ctx,
+                                   fp8_stream_t stream) {
+  const fp8_weight_cache::Entry *e = nullptr;
+  const fp8_status st = gated_entry(cache, h, recipe, act, N, &e);
+  if (st != FP8_OK) return st;
+  if (e->K != K) return FP8_ERR_INVALID_ARG;
+  if (N == 0) return FP8_OK;
+  if (!xq_row || !xq_row_scale_inv || !H) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(xq_row) || !aligned16(H) || !aligned16(ctx)) return FP8_ERR_ALIGN;
+  const int64_t F = e->O / 2;
+  const GatedCtx L = gated_ctx(recipe, N, K, F);
+  uint8_t *c = static_cast<uint8_t *>(ctx);
+  return from_cuda(launch_gated_fwd(xq_row, xq_row_scale_inv, e->w_row, e->row_scale_inv, N, K, F,
+                                    recipe == FP8_RECIPE_BLOCK, act, H, c ? c + L.g : nullptr,
+                                    c ? c + L.u : nullptr, cs(stream)));
+}
+
+fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *cache,
+                         fp8_weight_handle h, fp8_recipe recipe, fp8_act act, void *H, void *ctx,
+                         void *ws, size_t ws_bytes, fp8_stream_t stream) {
+  const fp8_weight_cache::Entry *e = nullptr;
+  fp8_status st = gated_entry(cache, h, recipe, act, N, &e);
+  if (st != FP8_OK) return st;
+  if (e->K != K) return FP8_ERR_INVALID_ARG;
+  if (N == 0) return FP8_OK;
+  if (!X || !H || !ws) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(H) || !aligned16(ctx) || !aligned16(ws)) return FP8_ERR_ALIGN;
+  const int64_t F = e->O / 2;
+  const GatedWs L = gated_ws(recipe, N, K, F);
+  if (ws_bytes < L.fwd) return FP8_ERR_WORKSPACE;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  uint8_t *col = nullptr;
+  float *cscale = nullptr, *cscale_inv = nullptr;
+  void *g, *u;
+  if (ctx) fp8_gated_ctx_layout(recipe, N, K, F, ctx, &col, &cscale, &cscale_inv, &g, &u);
+  st = from_cuda(launch_quantize(X, N, K, recipe == FP8_RECIPE_BLOCK ? 1 : 0, FP8_FORMAT_E4M3,
+                                 w + L.xq, col, reinterpret_cast<float *>(w + L.xs),
+                                 reinterpret_cast<float *>(w + L.xsi), cscale, cscale_inv,
+                                 reinterpret_cast<float *>(w + L.part), cs(stream)));
+  if (st != FP8_OK) return st;
+  return fp8_gated_fwd_quantized(w + L.xq, reinterpret_cast<float *>(w + L.xsi), N, K, cache, h,
+                                 recipe, act, H, ctx, stream);
+}
+
+fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
+                         fp8_weight_cache *cache, fp8_weight_handle h, fp8_recipe recipe,
+                         fp8_act act, void *dX, void *dW, void *ws, size_t ws_bytes,
+                         fp8_stream_t stream) {
+  const fp8_weight_cache::Entry *e = nullptr;
+  fp8_status st = gated_entry(cache, h, recipe, act, N, &e);
+  if (st != FP8_OK) return st;
+  if (e->O != 2 * F) return FP8_ERR_INVALID_ARG;
+  const int64_t K = e->K;
+  if (!dW) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(dW)) return FP8_ERR_ALIGN;
+  if (N == 0) return from_cuda(cudaMemsetAsync(dW, 0, (size_t)2 * F * K * 2, cs(stream)));
+  if (!dH || !ctx || !ws) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(dH) || !aligned16(ctx) || !aligned16(dX) || !aligned16(ws)) return FP8_ERR_ALIGN;
+  const GatedWs L = gated_ws(recipe, N, K, F);
+  if (ws_bytes < L.bwd) return FP8_ERR_WORKSPACE;
+  const bool block = recipe == FP8_RECIPE_BLOCK;
+  const GatedCtx C = gated_ctx(recipe, N, K, F);
+  const uint8_t *c = static_cast<const uint8_t *>(ctx);
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  float *rsi = reinterpret_cast<float *>(w + L.rsi);
+  float *csi = block ? reinterpret_cast<float *>(w + L.csi) : rsi;  // tensorwise: one scale
+  st = from_cuda(launch_gated_bwd_quantize(dH, c + C.g, c + C.u, N, F, block, act, w + L.row,
+                                           w + L.col, rsi, csi,
+                                           reinterpret_cast<float *>(w + L.bpart), cs(stream)));
+  if (st != FP8_OK) return st;
+  if (dX) {
+    st = from_cuda(launch_gemm(w + L.row, FP8_FORMAT_E5M2, rsi, e->w_col, FP8_FORMAT_E4M3,
+                               e->col_scale_inv, N, K, 2 * F, fwd_scaling(recipe), dX, w + L.gemm,
+                               cs(stream)));
+    if (st != FP8_OK) return st;
+  }
+  return from_cuda(launch_gemm(w + L.col, FP8_FORMAT_E5M2, csi, c + C.x.xq_col, FP8_FORMAT_E4M3,
+                               reinterpret_cast<const float *>(c + C.x.scale_inv), 2 * F, K,
+                               round16(N), wgrad_scaling(recipe), dW, w + L.gemm, cs(stream)));
+}
+
+// ---------------------------------------------------------------- gradient clipping
+struct fp8_grad_clip {
+  std::vector<ClipChunk> table;
+  double elements = 0.0, bytes = 0.0;
+};
+
+fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_grad_clip **out) {
+  if (!out || count < 0 || (count > 0 && !descs)) return FP8_ERR_INVALID_ARG;
+  *out = nullptr;
+  double elements = 0.0, bytes = 0.0;
+  for (int64_t i = 0; i < count; ++i) {
+    const fp8_grad_desc &d = descs[i];
+    if (d.n < 0 || !valid_dtype(d.dtype) || (d.n > 0 && (!d.src || !d.dst)))
+      return FP8_ERR_INVALID_ARG;
+    const uintptr_t size = d.dtype == FP8_DTYPE_F32 ? 4 : 2;
+    if ((reinterpret_cast<uintptr_t>(d.src) | reinterpret_cast<uintptr_t>(d.dst)) % size)
+      return FP8_ERR_ALIGN;
+    elements += (double)d.n;
+    bytes += (double)d.n * (double)size;
+  }
+  // Chunk: a power of two between 2048 and 32768 elements, so that small sets
+  // still spread over the GPU's CTAs and large ones have few chunks.
+  int64_t chunk = 2048;
+  while (chunk < 32768 && elements / (double)chunk > 4096.0) chunk *= 2;
+  try {
+    auto p = std::make_unique<fp8_grad_clip>();
+    p->elements = elements;
+    p->bytes = bytes;
+    for (int64_t i = 0; i < count; ++i) {
+      const fp8_grad_desc &d = descs[i];
+      const int64_t size = d.dtype == FP8_DTYPE_F32 ? 4 : 2;
+      for (int64_t o = 0; o < d.n; o += chunk)
+        p->table.push_back(ClipChunk{static_cast<const uint8_t *>(d.src) + o * size,
+                                     static_cast<uint8_t *>(d.dst) + o * size,
+                                     (int32_t)std::min(chunk, d.n - o), d.dtype == FP8_DTYPE_F32});
+    }
+    *out = p.release();
+  } catch (...) {  // out of host memory
+    return FP8_ERR_INVALID_ARG;
+  }
+  return FP8_OK;
+}
+
+void fp8_grad_clip_destroy(fp8_grad_clip *plan) { delete plan; }
+
+fp8_status fp8_grad_clip_table_size(const fp8_grad_clip *plan, size_t *bytes) {
+  if (!plan || !bytes) return FP8_ERR_INVALID_ARG;
+  *bytes = plan->table.size() * sizeof(ClipChunk);
+  return FP8_OK;
+}
+
+fp8_status fp8_grad_clip_table_write(const fp8_grad_clip *plan, void *host, size_t bytes) {
+  if (!plan || (!host && !plan->table.empty())) return FP8_ERR_INVALID_ARG;
+  if (bytes < plan->table.size() * sizeof(ClipChunk)) return FP8_ERR_WORKSPACE;
+  if (!plan->table.empty())
+    std::memcpy(host, plan->table.data(), plan->table.size() * sizeof(ClipChunk));
+  return FP8_OK;
+}
+
+fp8_status fp8_grad_clip_workspace_size(const fp8_grad_clip *plan, size_t *bytes) {
+  if (!plan || !bytes) return FP8_ERR_INVALID_ARG;
+  *bytes = (size_t)clip_ctas((int64_t)plan->table.size()) * sizeof(float);
+  return FP8_OK;
+}
+
+namespace {
+fp8_status clip_run(const fp8_grad_clip *plan, const void *table, bool write, float max_norm,
+                    float *norm, void *ws, size_t ws_bytes, fp8_stream_t stream) {
+  if (!plan || !norm || (!table && !plan->table.empty()) || !(max_norm > 0.0f))
+    return FP8_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(table) % 8 || reinterpret_cast<uintptr_t>(norm) % 4 ||
+      !aligned16(ws))
+    return FP8_ERR_ALIGN;
+  size_t need = 0;
+  fp8_grad_clip_workspace_size(plan, &need);
+  if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
+  return from_cuda(launch_clip(static_cast<const ClipChunk *>(table), (int64_t)plan->table.size(),
+                               plan->bytes, plan->elements, write, max_norm, norm,
+                               static_cast<float *>(ws), cs(stream)));
+}
+}  // namespace
+
+fp8_status fp8_grad_clip_run(const fp8_grad_clip *plan, const void *table, float max_norm,
+                             float *norm, void *workspace, size_t workspace_bytes,
+                             fp8_stream_t stream) {
+  return clip_run(plan, table, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *norm, void *workspace,
+                         size_t workspace_bytes, fp8_stream_t stream) {
+  return clip_run(plan, table, false, 1.0f, norm, workspace, workspace_bytes, stream);
+}
+
 fp8_status fp8_profile_begin(void) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   for (auto &r : g_prof) {
@@ -894,10 +1245,12 @@ fp8_status fp8_debug_wait_timeout(uint64_t limit_ns, fp8_stream_t stream) {
 }
 
 fp8_status fp8_get_device_status(fp8_stream_t stream) {
-  unsigned s = 0, q = 0;
+  unsigned s = 0, q = 0, n = 0, g = 0;
   if (gemm_read_status(&s, cs(stream)) != cudaSuccess) return FP8_ERR_CUDA;
   if (quant_read_status(&q) != cudaSuccess) return FP8_ERR_CUDA;
-  return (fp8_status)(s ? s : q);
+  if (norm_read_status(&n) != cudaSuccess) return FP8_ERR_CUDA;
+  if (gated_read_status(&g) != cudaSuccess) return FP8_ERR_CUDA;
+  return (fp8_status)(s ? s : q ? q : n ? n : g);
 }
 
 }  // extern "C"

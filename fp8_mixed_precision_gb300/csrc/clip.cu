@@ -1,0 +1,175 @@
+// Global gradient norm over many tensors, and clipping.
+//
+//   norm = sqrt(sum over all tensors of g^2)
+//   coef = min(1, max_norm / (norm + 1e-6)), or 1 when the norm is not finite
+//   out  = g * coef
+//
+// The tensors are cut into chunks of at most `chunk` elements; a table of
+// chunks in device memory (pointer, pointer, count, type) lets one launch
+// cover tensors of any number and size.  Bound by memory: the first pass reads
+// every gradient once, the second reads it again (from L2 where it still is)
+// and writes it once.  Sums are fp32 per thread and fp64 over the CTAs, in an
+// order that depends on the table and the GPU alone.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fp8lin {
+namespace {
+
+constexpr int kClipThreads = 512;
+
+__device__ __forceinline__ bool vec_ok(const ClipChunk &c) {
+  return ((reinterpret_cast<uintptr_t>(c.src) | reinterpret_cast<uintptr_t>(c.dst)) & 15) == 0;
+}
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+  v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+  v[4] = bf16lo(w.z); v[5] = bf16hi(w.z); v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ float load1(const ClipChunk &c, int i) {
+  return c.f32 ? static_cast<const float *>(c.src)[i]
+               : bf16lo(static_cast<const uint16_t *>(c.src)[i]);
+}
+
+// Sum over the CTA's 512 threads, in a fixed order; thread 0 has the result.
+__device__ __forceinline__ float block_sum(float v) {
+  __shared__ float red[kClipThreads / 32];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+  if (threadIdx.x == 0)
+    for (int k = 0; k < kClipThreads / 32; ++k) v += red[k];
+  return v;
+}
+
+__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const ClipChunk *__restrict__ table,
+                                                                 int64_t chunks,
+                                                                 float *__restrict__ partials) {
+  pdl_wait_then_release();
+  float a[4] = {};
+  for (int64_t id = blockIdx.x; id < chunks; id += gridDim.x) {
+    const ClipChunk c = table[id];
+    int done = 0;
+    if (vec_ok(c)) {
+      const uint4 *p = static_cast<const uint4 *>(c.src);
+      const int per = c.f32 ? 4 : 8, nv = c.n / per;
+      for (int i = threadIdx.x; i < nv; i += kClipThreads) {
+        const uint4 w = p[i];
+        if (c.f32) {
+          const float x = __uint_as_float(w.x), y = __uint_as_float(w.y);
+          const float z = __uint_as_float(w.z), q = __uint_as_float(w.w);
+          a[0] = fmaf(x, x, a[0]);
+          a[1] = fmaf(y, y, a[1]);
+          a[2] = fmaf(z, z, a[2]);
+          a[3] = fmaf(q, q, a[3]);
+        } else {
+          float v[8];
+          unpack8(w, v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a[k & 3] = fmaf(v[k], v[k], a[k & 3]);
+        }
+      }
+      done = nv * per;
+    }
+    for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {
+      const float v = load1(c, i);
+      a[0] = fmaf(v, v, a[0]);
+    }
+  }
+  const float s = block_sum((a[0] + a[1]) + (a[2] + a[3]));
+  if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+
+// Every CTA forms the norm from the partials, in the same order.
+__device__ __forceinline__ float norm_of(const float *partials, int n) {
+  __shared__ double red[kClipThreads / 32];
+  __shared__ float norm;
+  double s = 0.0;
+  for (int k = threadIdx.x; k < n; k += kClipThreads) s += (double)partials[k];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int k = 0; k < kClipThreads / 32; ++k) s += red[k];
+    norm = (float)sqrt(s);
+  }
+  __syncthreads();
+  return norm;
+}
+
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const ClipChunk *__restrict__ table,
+                                                                  int64_t chunks,
+                                                                  const float *__restrict__ partials,
+                                                                  int n_partials, float max_norm,
+                                                                  float *__restrict__ norm_out) {
+  pdl_wait_then_release();
+  const float norm = norm_of(partials, n_partials);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  const float coef = isfinite(norm) ? fminf(1.0f, __fdiv_rn(max_norm, norm + 1e-6f)) : 1.0f;
+  // last chunk first: what the first pass read last may still be in L2
+  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const ClipChunk c = table[chunks - 1 - k];
+    if (c.dst == c.src && coef == 1.0f) continue;  // in place and nothing to change
+    int done = 0;
+    if (vec_ok(c)) {
+      const uint4 *p = static_cast<const uint4 *>(c.src);
+      uint4 *q = static_cast<uint4 *>(c.dst);
+      const int per = c.f32 ? 4 : 8, nv = c.n / per;
+      for (int i = threadIdx.x; i < nv; i += kClipThreads) {
+        uint4 w = p[i];
+        if (coef == 1.0f) {
+        } else if (c.f32) {
+          w.x = __float_as_uint(__fmul_rn(__uint_as_float(w.x), coef));
+          w.y = __float_as_uint(__fmul_rn(__uint_as_float(w.y), coef));
+          w.z = __float_as_uint(__fmul_rn(__uint_as_float(w.z), coef));
+          w.w = __float_as_uint(__fmul_rn(__uint_as_float(w.w), coef));
+        } else {
+          float v[8];
+          unpack8(w, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], coef);
+          w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        }
+        q[i] = w;
+      }
+      done = nv * per;
+    }
+    for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {
+      const float v = load1(c, i);
+      if (c.f32)
+        static_cast<float *>(c.dst)[i] = coef == 1.0f ? v : __fmul_rn(v, coef);
+      else
+        static_cast<__nv_bfloat16 *>(c.dst)[i] =
+            __float2bfloat16_rn(coef == 1.0f ? v : __fmul_rn(v, coef));
+    }
+  }
+}
+
+}  // namespace
+
+int clip_ctas(int64_t chunks) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)num_sms() * 4));
+}
+
+cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,
+                        bool write, float max_norm, float *norm, float *partials, cudaStream_t st) {
+  const int grid = clip_ctas(chunks);
+  {
+    LaunchScope ls("clip_norm", st, in_bytes, 2.0 * elements, (int64_t)elements);
+    const cudaError_t e = launch_kernel(clip_norm_kernel, dim3((unsigned)grid), dim3(kClipThreads),
+                                        0, st, table, chunks, partials);
+    if (e != cudaSuccess) return e;
+  }
+  LaunchScope ls("clip_scale", st, write ? 2.0 * in_bytes : 0.0, elements, (int64_t)elements);
+  return launch_kernel(clip_scale_kernel, dim3(write ? (unsigned)grid : 1u), dim3(kClipThreads), 0,
+                       st, table, write ? chunks : (int64_t)0, (const float *)partials, grid,
+                       max_norm, norm);
+}
+
+}  // namespace fp8lin

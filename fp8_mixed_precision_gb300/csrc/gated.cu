@@ -1,0 +1,723 @@
+// Gated feed-forward on FP8 operands: both projections, the activation and
+// the product in one kernel, and the backward pass's fused derivative and
+// E5M2 cast.
+//
+//   W = [Wg; Wu] [2F, K],  G = X Wg^T,  U = X Wu^T,  H = act(G) * U
+//   dG = (dH * U) * act'(G),  dU = dH * act(G)
+//   act: silu, g s with s = 1 / (1 + e^-g), or the exact-erf GELU
+//
+// Forward: persistent CTAs (one per SM), one 128-token x 128-column tile of H
+// at a time.  The B operand of the tile's MMAs is 128 rows of Wg followed by
+// the same 128 rows of Wu, so one 128 x 256 accumulator holds G and U of the
+// same outputs and an epilogue warp reads both from its own TMEM lanes; H is
+// formed from the fp32 accumulators and rounded once.  Training keeps G and U
+// as bf16 (the framework's GEMM outputs are bf16), which the backward pass
+// reads.
+//   warp 0      TMA producer: A (128 tokens) and B (2 x 128 weight rows),
+//               128 bytes along K, 128B swizzle, ring of full/empty mbarriers
+//   warp 1      TMEM allocator and tcgen05.mma issuer (kind::f8f6f4)
+//   warps 2-9   epilogue; warp w reads lanes 32*(w%4)..+31 and columns
+//               64*((w-2)/4)..+63 of both halves
+// Tensor scaling keeps one accumulator over K; block scaling (1x128 tokens,
+// 128x128 weights) promotes every 128-deep partial into fp32 registers.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "pipe.cuh"
+#include "ptx.cuh"
+
+namespace fp8lin {
+namespace {
+
+using gelu2::dup;
+using gelu2::fma2;
+using gelu2::mul2;
+using gelu2::pk;
+using gelu2::upk;
+
+__device__ unsigned g_gated_status;
+
+constexpr int BM = 128, BK = 128, BF = 128;  // tokens, K bytes, columns of H per tile
+constexpr int BN = 2 * BF;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemBudget = 227 * 1024;
+constexpr int kMaxStages = 8;
+
+// silu and its derivative, from the hardware's base-2 exponential and
+// reciprocal (each within 2 ulp of fp32).
+__device__ __forceinline__ float sigmoid_f(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(e, 1.0f)));
+  return s;
+}
+template <int ACT>
+__device__ __forceinline__ void act2(float g0, float g1, float &a0, float &a1) {
+  if (ACT == FP8_ACT_SILU) {
+    a0 = __fmul_rn(g0, sigmoid_f(g0));
+    a1 = __fmul_rn(g1, sigmoid_f(g1));
+  } else {
+    gelu_f2(g0, g1, a0, a1);
+  }
+}
+// act and act' of two values
+template <int ACT>
+__device__ __forceinline__ void act_grad2(float g0, float g1, float &a0, float &a1, float &d0,
+                                          float &d1) {
+  if (ACT == FP8_ACT_SILU) {
+    const float s0 = sigmoid_f(g0), s1 = sigmoid_f(g1);
+    a0 = __fmul_rn(g0, s0);
+    a1 = __fmul_rn(g1, s1);
+    d0 = __fmul_rn(s0, fmaf(g0, 1.0f - s0, 1.0f));
+    d1 = __fmul_rn(s1, fmaf(g1, 1.0f - s1, 1.0f));
+  } else {
+    gelu_f2(g0, g1, a0, a1);
+    gelu_grad_f2(g0, g1, d0, d1);
+  }
+}
+
+struct GatedCtl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kCtlBytes = (int)((sizeof(GatedCtl) + 127) / 128 * 128);
+
+template <bool SAVE>
+struct GCfg {
+  static constexpr int kEpi = 8;
+  static constexpr int kThreads = 32 * (2 + kEpi);
+  static constexpr int kStageA = BM * BK, kStageB = BN * BK;
+  static constexpr int kStageBytes = kStageA + kStageB;
+  static constexpr int kSlabBytes = 32 * 128;  // 32 tokens x 64 bf16 columns
+  static constexpr int kSlabs = SAVE ? 2 : 1;  // per epilogue warp
+  static constexpr int kOutBytes = kEpi * kSlabs * kSlabBytes;
+  static constexpr int kRing = kSmemBudget - 1024 - kOutBytes - kCtlBytes;
+  static constexpr int kStages = kRing / kStageBytes;
+  static constexpr size_t kSmemBytes =
+      1024 + (size_t)kStages * kStageBytes + kOutBytes + kCtlBytes;
+  static_assert(kStages >= 2 && kStages <= kMaxStages, "operand ring");
+};
+
+struct GatedArgs {
+  int64_t N, F;
+  int tiles_m, tiles_f, kbs;
+  int64_t units;
+  const float *x_sinv, *w_sinv;
+  int64_t lds;  // row stride (floats) of both block scale arrays
+  uint32_t idesc;
+  int group_m;  // > 0: units run in groups of group_m token tiles
+};
+
+__device__ __forceinline__ void decode_unit(const GatedArgs &g, int64_t u64, int &tm, int &tf) {
+  const uint32_t u = (uint32_t)u64, tiles_f = (uint32_t)g.tiles_f;
+  if (g.group_m > 0) {
+    const uint32_t gmax = (uint32_t)g.group_m, per_group = gmax * tiles_f;
+    const uint32_t m0 = u / per_group * gmax, rem = u % per_group;
+    const uint32_t gm = min(gmax, (uint32_t)g.tiles_m - m0);
+    tm = (int)(m0 + rem % gm);
+    tf = (int)(rem / gm);
+  } else {
+    tm = (int)(u / tiles_f);
+    tf = (int)(u % tiles_f);
+  }
+}
+
+// 32 packed bf16 pairs (64 columns) of one token into a 32 x 64 slab (128-byte
+// rows, 128-byte swizzle, as the TMA store expects).
+__device__ __forceinline__ void stage64(uint8_t *slab, int row, const uint32_t (&w)[32]) {
+  uint8_t *rp = slab + row * 128;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4 *>(rp + ((c ^ (row & 7)) * 16)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+
+template <int SCALING, int ACT, bool SAVE>
+__global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
+    gated_fwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmG,
+                     const __grid_constant__ CUtensorMap tmU, const GatedArgs g) {
+  using C = GCfg<SAVE>;
+  constexpr bool kTensor = SCALING == FP8_SCALING_TENSOR;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *out_stage = smem + (size_t)kStages * C::kStageBytes;
+  GatedCtl *ctl = reinterpret_cast<GatedCtl *>(out_stage + C::kOutBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&ctl->full[s], 1);
+      ptx::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ctl->acc_full[b], 1);
+      ptx::mbar_init(&ctl->acc_empty[b], C::kEpi);
+    }
+    ptx::mbar_init(&ctl->mma_done, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmX);
+    ptx::tma_prefetch_desc(&tmW);
+    ptx::tma_prefetch_desc(&tmH);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&ctl->tmem_base, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  pdl_wait();  // dependents launch as this grid exits
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int *abort = &ctl->abort;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return pipe::wait_bar(bar, parity, abort, &g_gated_status);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_phase[kStages];
+      for (int s = 0; s < kStages; ++s) last_phase[s] = -1;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+        int tm, tf;
+        decode_unit(g, u, tm, tf);
+        for (int kb = 0; kb < g.kbs; ++kb) {
+          if (!wait(&ctl->empty[stage], phase ^ 1)) { ok = false; break; }
+          uint8_t *sa = smem + (size_t)stage * C::kStageBytes;
+          ptx::mbar_arrive_expect_tx(&ctl->full[stage], C::kStageBytes);
+          ptx::tma_load_2d(sa, &tmX, &ctl->full[stage], kb * BK, tm * BM);
+          // gate rows, then the up rows of the same columns (past the weight: zeros)
+          ptx::tma_load_2d(sa + C::kStageA, &tmW, &ctl->full[stage], kb * BK, tf * BF);
+          ptx::tma_load_2d(sa + C::kStageA + BF * BK, &tmW, &ctl->full[stage], kb * BK,
+                           (int)g.F + tf * BF);
+          last_phase[stage] = (int)phase;
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok)  // let every issued copy land before the CTA can exit
+        for (int s = 0; s < kStages; ++s)
+          if (last_phase[s] >= 0)
+            pipe::drain_wait(&ctl->full[s], (uint32_t)last_phase[s], &g_gated_status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, nacc = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+        for (int kb = 0; kb < g.kbs; ++kb) {
+          const bool first = !kTensor || kb == 0, last = !kTensor || kb == g.kbs - 1;
+          if (first) {
+            if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) { ok = false; break; }
+            ptx::tc_fence_after();
+          }
+          if (!wait(&ctl->full[stage], phase)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t a_addr = ptx::smem_u32(smem + (size_t)stage * C::kStageBytes);
+          const uint64_t adesc = ptx::smem_desc_sw128(a_addr);
+          const uint64_t bdesc = ptx::smem_desc_sw128(a_addr + C::kStageA);
+          const uint32_t d = tmem + (nacc & 1) * BN;
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            ptx::mma_f8f6f4(d, adesc + 2 * k, bdesc + 2 * k, g.idesc, (!first || k > 0) ? 1u : 0u);
+          ptx::mma_commit(&ctl->empty[stage]);
+          if (last) {
+            ptx::mma_commit(&ctl->acc_full[nacc & 1]);
+            ++nacc;
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
+      ptx::mma_commit(&ctl->mma_done);
+      pipe::drain_wait(&ctl->mma_done, 0, &g_gated_status);
+    }
+  } else {
+    const int ew = warp - 2, q = warp & 3, h = ew >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 64);
+    uint32_t nacc = 0, nout = 0;
+    uint8_t *slabs = out_stage + (size_t)ew * C::kSlabs * C::kSlabBytes;
+    float s_tensor = 0.0f;
+    if (kTensor) s_tensor = __fmul_rn(g.x_sinv[0], g.w_sinv[0]);
+    auto release_acc = [&](uint32_t ab) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
+    };
+    auto emit = [&](const CUtensorMap *map, const uint32_t (&w)[32], int col0, int row0) {
+      uint8_t *slab = slabs + (nout % C::kSlabs) * C::kSlabBytes;
+      if (lane == 0) ptx::bulk_wait_read<C::kSlabs - 1>();
+      __syncwarp();
+      stage64(slab, lane, w);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_2d(map, slab, col0, row0);
+        ptx::bulk_commit();
+      }
+      ++nout;
+    };
+    for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {
+      int tm, tf;
+      decode_unit(g, u, tm, tf);
+      const int row0 = tm * BM + q * 32, col0 = tf * BF + h * 64;
+      const bool stored = row0 < g.N && col0 < g.F;  // otherwise the slab is wholly outside
+      uint32_t hp[32], gp[SAVE ? 32 : 1], up[SAVE ? 32 : 1];
+      // columns 32 half .. +31 of this warp's 64, as G and U
+      auto finish = [&](int half, const float (&G)[32], const float (&U)[32]) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float a0, a1;
+          act2<ACT>(G[2 * j], G[2 * j + 1], a0, a1);
+          hp[16 * half + j] =
+              pack_bf16x2(__fmul_rn(a0, U[2 * j]), __fmul_rn(a1, U[2 * j + 1]));
+          if constexpr (SAVE) {
+            gp[16 * half + j] = pack_bf16x2(G[2 * j], G[2 * j + 1]);
+            up[16 * half + j] = pack_bf16x2(U[2 * j], U[2 * j + 1]);
+          }
+        }
+      };
+      if constexpr (kTensor) {
+        const uint32_t ab = nacc & 1;
+        if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t rg[32], ru[32];
+          ptx::tmem_ld32(tl + ab * BN + 32 * half, rg);
+          ptx::tmem_ld32(tl + ab * BN + BF + 32 * half, ru);
+          ptx::tmem_ld_wait();
+          if (half == 1) release_acc(ab);
+          float G[32], U[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            G[j] = __fmul_rn(__uint_as_float(rg[j]), s_tensor);
+            U[j] = __fmul_rn(__uint_as_float(ru[j]), s_tensor);
+          }
+          finish(half, G, U);
+        }
+        ++nacc;
+      } else {
+        uint64_t acc[64];  // pairs: G columns 0..63, then U columns 0..63
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = 0;
+        const int64_t m = (int64_t)row0 + lane;
+        const float *xrow = g.x_sinv + (m < g.N ? m : g.N - 1) * g.lds;
+        const float *wg = g.w_sinv + (int64_t)tf * g.lds;  // F is a multiple of 128
+        const float *wu = wg + (g.F / BF) * g.lds;
+        bool ok = true;
+        float xs = xrow[0], gs = wg[0], us = wu[0];
+        for (int kb = 0; kb < g.kbs; ++kb) {
+          const uint32_t ab = nacc & 1;
+          const uint64_t sg = dup(__fmul_rn(xs, gs)), su = dup(__fmul_rn(xs, us));
+          if (kb + 1 < g.kbs) {
+            xs = xrow[kb + 1];
+            gs = wg[kb + 1];
+            us = wu[kb + 1];
+          }
+          if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) { ok = false; break; }
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {  // 16 columns at a time: G, then U
+            uint32_t raw[16];
+            ptx::tmem_ld16(tl + ab * BN + (c >> 2) * BF + 16 * (c & 3), raw);
+            ptx::tmem_ld_wait();
+            if (c == 7) release_acc(ab);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[8 * c + j] = fma2(pk(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
+                                    c < 4 ? sg : su, acc[8 * c + j]);
+          }
+          ++nacc;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float G[32], U[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            upk(acc[16 * half + j], G[2 * j], G[2 * j + 1]);
+            upk(acc[32 + 16 * half + j], U[2 * j], U[2 * j + 1]);
+          }
+          finish(half, G, U);
+        }
+      }
+      if (stored) {
+        emit(&tmH, hp, col0, row0);
+        if constexpr (SAVE) {
+          emit(&tmG, gp, col0, row0);
+          emit(&tmU, up, col0, row0);
+        }
+      }
+    }
+    if (lane == 0) ptx::bulk_wait<0>();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+struct GatedBwd {
+  const uint4 *dh, *g, *u;  // bf16 [N, F]
+  int64_t N, F, ldn;        // ldn: tokens per row of the transposed layout (N rounded up to 16)
+  uint8_t *row;             // E5M2 [N, 2F]
+  uint8_t *col;             // E5M2 [2F, ldn]
+  float *row_scale_inv, *col_scale_inv;  // block scaling
+  float *scale_inv;                      // tensor scaling (1)
+  const float *partials;                 // tensor scaling: maxima of the first pass
+  int n_partials;
+};
+
+// dG and dU of eight elements.
+template <int ACT>
+__device__ __forceinline__ void dgu8(uint4 dh, uint4 g, uint4 u, float (&dg)[8], float (&du)[8]) {
+  const uint32_t hw[4] = {dh.x, dh.y, dh.z, dh.w}, gw[4] = {g.x, g.y, g.z, g.w},
+                 uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a0, a1, d0, d1;
+    act_grad2<ACT>(bf16lo(gw[k]), bf16hi(gw[k]), a0, a1, d0, d1);
+    const float h0 = bf16lo(hw[k]), h1 = bf16hi(hw[k]);
+    dg[2 * k] = __fmul_rn(__fmul_rn(h0, bf16lo(uw[k])), d0);
+    dg[2 * k + 1] = __fmul_rn(__fmul_rn(h1, bf16hi(uw[k])), d1);
+    du[2 * k] = __fmul_rn(h0, a0);
+    du[2 * k + 1] = __fmul_rn(h1, a1);
+  }
+}
+
+constexpr int kAmaxThreads = 256;
+// Tensor scaling, first pass: per-CTA maximum of |dG| and |dU| (NaN ignored).
+template <int ACT>
+__global__ void __launch_bounds__(kAmaxThreads)
+    gated_bwd_amax_kernel(const uint4 *__restrict__ dh, const uint4 *__restrict__ g,
+                          const uint4 *__restrict__ u, int64_t n8, float *__restrict__ partials) {
+  pdl_wait_then_release();
+  float m = 0.0f;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += stride) {
+    float dg[8], du[8];
+    dgu8<ACT>(dh[i], g[i], u[i], dg, du);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = amax_acc(amax_acc(m, dg[k]), du[k]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  __shared__ float red[kAmaxThreads / 32];
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kAmaxThreads / 32; ++k) m = fmaxf(m, red[k]);
+    partials[blockIdx.x] = m;
+  }
+}
+
+constexpr int kBwdThreads = 512;
+struct __align__(128) BSmem {
+  uint16_t in[3][128 * 128];   // dH, G, U tiles (TMA destinations)
+  uint32_t tile[2][128 * 32];  // FP8 bytes of dG and dU for the transposed layout
+  float colred[16][2][128];    // per-warp column maxima
+  float colsc[2][128];
+  float red[16];
+  float tscale;
+  uint64_t full;
+};
+
+__device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
+
+// One 128-token x 128-column tile of dH, G, U per iteration: dG and dU are
+// formed once, in registers, and leave as E5M2 in both layouts, each with its
+// own 1x128 blocks (block scaling) or one scale (tensor scaling).
+template <bool BLOCK, int ACT>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    gated_bwd_cast_kernel(const __grid_constant__ CUtensorMap tmD,
+                          const __grid_constant__ CUtensorMap tmG,
+                          const __grid_constant__ CUtensorMap tmU, GatedBwd p) {
+  extern __shared__ __align__(1024) uint8_t b_smem_raw[];
+  BSmem &S = *reinterpret_cast<BSmem *>(b_smem_raw);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int cg = t & 15, rr = t >> 4;  // 8 columns, rows rr + 32 i
+  const int64_t tiles_r = (p.N + 127) / 128, tiles_c = (p.F + 127) / 128;
+  const int64_t ntiles = tiles_r * tiles_c;
+  const int64_t F2 = 2 * p.F;
+  if (t == 0) {
+    ptx::mbar_init(&S.full, 1);
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmD);
+    ptx::tma_prefetch_desc(&tmG);
+    ptx::tma_prefetch_desc(&tmU);
+  }
+  __syncthreads();
+  pdl_wait_then_release();
+  auto prefetch = [&](int64_t id) {
+    if (t != 0 || id >= ntiles) return;
+    const int x = (int)(id % tiles_c) * 128, y = (int)(id / tiles_c) * 128;
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive_expect_tx(&S.full, 3u * 128 * 128 * 2);
+    ptx::tma_load_2d(S.in[0], &tmD, &S.full, x, y);
+    ptx::tma_load_2d(S.in[1], &tmG, &S.full, x, y);
+    ptx::tma_load_2d(S.in[2], &tmU, &S.full, x, y);
+  };
+  int64_t id = blockIdx.x;
+  prefetch(id);
+  float ts = 1.0f;
+  if constexpr (!BLOCK) {
+    float m = 0.0f;
+    for (int k = t; k < p.n_partials; k += kBwdThreads) m = fmaxf(m, p.partials[k]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) S.red[warp] = m;
+    __syncthreads();
+    if (t == 0) {
+      for (int k = 1; k < 16; ++k) m = fmaxf(m, S.red[k]);
+      float s, si;
+      scale_from_amax(m, kE5M2Max, s, si);
+      S.tscale = s;
+      if (blockIdx.x == 0) p.scale_inv[0] = si;
+    }
+    __syncthreads();
+    ts = S.tscale;
+  }
+  volatile int no_abort = 0;
+  for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
+    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    const int64_t r0 = tr * 128, c0 = tc * 128;
+    const int rows_here = (int)(p.N - r0 < 128 ? p.N - r0 : 128);
+    const int cols_here = (int)(p.F - c0 < 128 ? p.F - c0 : 128);
+    const bool col_ok = 8 * cg < cols_here;
+    pipe::wait_bar(&S.full, k & 1, &no_abort, &g_gated_status);  // on expiry: recorded, carry on
+    float v[2][4][8];  // [dG, dU][row][column]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int o = (rr + 32 * i) * 128 + 8 * cg;
+      dgu8<ACT>(*reinterpret_cast<const uint4 *>(&S.in[0][o]),
+                *reinterpret_cast<const uint4 *>(&S.in[1][o]),
+                *reinterpret_cast<const uint4 *>(&S.in[2][o]), v[0][i], v[1][i]);
+    }
+    __syncthreads();  // the buffers are read, and the last tile's transpose too
+    prefetch(id + gridDim.x);
+    float rs[2][4];
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float cm[8] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float m = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            m = amax_acc(m, v[z][i][j]);
+            cm[j] = amax_acc(cm[j], v[z][i][j]);
+          }
+#pragma unroll
+          for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float si;
+          scale_from_amax(m, kE5M2Max, rs[z][i], si);
+          const int64_t row = r0 + rr + 32 * i;
+          if (cg == 0 && row < p.N)
+            p.row_scale_inv[row * (2 * tiles_c) + z * tiles_c + tc] = si;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+        if (lane < 16)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) S.colred[warp][z][8 * cg + j] = cm[j];
+      }
+      __syncthreads();
+      if (t < 256) {
+        const int z = t >> 7, c = t & 127;
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) m = fmaxf(m, S.colred[w][z][c]);
+        float s, si;
+        scale_from_amax(m, kE5M2Max, s, si);
+        S.colsc[z][c] = s;
+        if (c < cols_here) p.col_scale_inv[(z * p.F + c0 + c) * tiles_r + tr] = si;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      float cs[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cs[j] = BLOCK ? S.colsc[z][8 * cg + j] : ts;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = rr + 32 * i;
+        const float s = BLOCK ? rs[z][i] : ts;
+        uint2 q;
+        q.x = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][0], s), __fmul_rn(v[z][i][1], s),
+                                    __fmul_rn(v[z][i][2], s), __fmul_rn(v[z][i][3], s));
+        q.y = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][4], s), __fmul_rn(v[z][i][5], s),
+                                    __fmul_rn(v[z][i][6], s), __fmul_rn(v[z][i][7], s));
+        if (col_ok && r < rows_here)
+          *reinterpret_cast<uint2 *>(p.row + (r0 + r) * F2 + z * p.F + c0 + 8 * cg) = q;
+        if (BLOCK) {
+          q.x = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][0], cs[0]), __fmul_rn(v[z][i][1], cs[1]),
+                                      __fmul_rn(v[z][i][2], cs[2]), __fmul_rn(v[z][i][3], cs[3]));
+          q.y = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][4], cs[4]), __fmul_rn(v[z][i][5], cs[5]),
+                                      __fmul_rn(v[z][i][6], cs[6]), __fmul_rn(v[z][i][7], cs[7]));
+        }
+        *reinterpret_cast<uint2 *>(&S.tile[z][r * 32 + ((2 * cg) ^ swz(r))]) = q;
+      }
+    }
+    __syncthreads();
+    {
+      // tokens past N are zeros (the TMA load's fill, and dH = 0 gives 0 there)
+      const int z = t >> 8, seg = t & 7, w = (t >> 3) & 31;
+      if (4 * w < cols_here && 16 * seg < rows_here) {
+        uint32_t a[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = seg * 16 + i;
+          a[i] = S.tile[z][r * 32 + (w ^ swz(r))];
+        }
+        uint32_t o[4][4];
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          const uint32_t t0 = __byte_perm(a[4 * gq + 0], a[4 * gq + 1], 0x5140);
+          const uint32_t t1 = __byte_perm(a[4 * gq + 0], a[4 * gq + 1], 0x7362);
+          const uint32_t t2 = __byte_perm(a[4 * gq + 2], a[4 * gq + 3], 0x5140);
+          const uint32_t t3 = __byte_perm(a[4 * gq + 2], a[4 * gq + 3], 0x7362);
+          o[0][gq] = __byte_perm(t0, t2, 0x5410);
+          o[1][gq] = __byte_perm(t0, t2, 0x7632);
+          o[2][gq] = __byte_perm(t1, t3, 0x5410);
+          o[3][gq] = __byte_perm(t1, t3, 0x7632);
+        }
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          *reinterpret_cast<uint4 *>(p.col + (z * p.F + c0 + 4 * w + jj) * p.ldn + r0 + 16 * seg) =
+              make_uint4(o[jj][0], o[jj][1], o[jj][2], o[jj][3]);
+      }
+    }
+  }
+}
+
+template <typename Kernel>
+cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+template <int SCALING, int ACT, bool SAVE>
+cudaError_t launch_fwd(const CUtensorMap (&m)[5], const GatedArgs &g, cudaStream_t st) {
+  using C = GCfg<SAVE>;
+  static bool done[64];
+  const cudaError_t e = opt_in_smem(gated_fwd_kernel<SCALING, ACT, SAVE>, C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(g.units, num_sms());
+  return launch_kernel(gated_fwd_kernel<SCALING, ACT, SAVE>, dim3((unsigned)grid), dim3(C::kThreads),
+                       C::kSmemBytes, st, m[0], m[1], m[2], m[3], m[4], g);
+}
+template <int SCALING, int ACT>
+cudaError_t launch_fwd_save(const CUtensorMap (&m)[5], const GatedArgs &g, bool save,
+                            cudaStream_t st) {
+  return save ? launch_fwd<SCALING, ACT, true>(m, g, st) : launch_fwd<SCALING, ACT, false>(m, g, st);
+}
+
+template <bool BLOCK, int ACT>
+cudaError_t launch_cast(const CUtensorMap (&m)[3], const GatedBwd &p, cudaStream_t st) {
+  static bool done[64];
+  const cudaError_t e = opt_in_smem(gated_bwd_cast_kernel<BLOCK, ACT>, sizeof(BSmem), done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((p.N + 127) / 128) * ((p.F + 127) / 128);
+  const int64_t grid = std::min<int64_t>(tiles, num_sms());
+  LaunchScope ls(BLOCK ? "gated_bwd_cast_block" : "gated_bwd_cast_tensor", st, 10.0 * p.N * p.F, 0.0,
+                 p.N, p.F);
+  return launch_kernel(gated_bwd_cast_kernel<BLOCK, ACT>, dim3((unsigned)grid), dim3(kBwdThreads),
+                       sizeof(BSmem), st, m[0], m[1], m[2], p);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
+                             const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
+                             int act, void *H, void *G, void *U, cudaStream_t st) {
+  const bool save = G != nullptr;
+  CUtensorMap m[5];
+  if (!make_u8_map(&m[0], xq, N, K, BM) || !make_u8_map(&m[1], wq, 2 * F, K, BF) ||
+      !make_bf16_slab_map(&m[2], H, N, F))
+    return cudaErrorInvalidValue;
+  m[3] = m[4] = m[2];
+  if (save && (!make_bf16_slab_map(&m[3], G, N, F) || !make_bf16_slab_map(&m[4], U, N, F)))
+    return cudaErrorInvalidValue;
+  GatedArgs g;
+  g.N = N;
+  g.F = F;
+  g.tiles_m = (int)((N + BM - 1) / BM);
+  g.tiles_f = (int)((F + BF - 1) / BF);
+  g.kbs = (int)((K + BK - 1) / BK);
+  g.units = (int64_t)g.tiles_m * g.tiles_f;
+  if (g.units >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  g.x_sinv = x_sinv;
+  g.w_sinv = w_sinv;
+  g.lds = g.kbs;
+  g.idesc = ptx::idesc_f8f6f4(FP8_FORMAT_E4M3, FP8_FORMAT_E4M3, BM, BN);
+  // deep K: 16 token tiles share the weight tiles that L2 holds
+  g.group_m = g.kbs >= 16 ? std::min(16, g.tiles_m) : 0;
+  LaunchScope ls(block ? "gated_fwd_block" : "gated_fwd_tensor", st,
+                 (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F, 4.0 * N * K * F, N, F, K);
+  if (block)
+    return act == FP8_ACT_SILU ? launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_SILU>(m, g, save, st)
+                               : launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(m, g, save, st);
+  return act == FP8_ACT_SILU ? launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_SILU>(m, g, save, st)
+                             : launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_GELU>(m, g, save, st);
+}
+
+cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void *U, int64_t N,
+                                      int64_t F, bool block, int act, uint8_t *row, uint8_t *col,
+                                      float *row_scale_inv, float *col_scale_inv, float *partials,
+                                      cudaStream_t st) {
+  CUtensorMap m[3];
+  if (!make_bf16_tile_map(&m[0], dH, N, F, 128, 128) || !make_bf16_tile_map(&m[1], G, N, F, 128, 128) ||
+      !make_bf16_tile_map(&m[2], U, N, F, 128, 128))
+    return cudaErrorInvalidValue;
+  GatedBwd p{static_cast<const uint4 *>(dH), static_cast<const uint4 *>(G),
+             static_cast<const uint4 *>(U), N, F, (N + 15) / 16 * 16, row, col, row_scale_inv,
+             col_scale_inv, row_scale_inv, partials, 0};
+  if (block)
+    return act == FP8_ACT_SILU ? launch_cast<true, FP8_ACT_SILU>(m, p, st)
+                               : launch_cast<true, FP8_ACT_GELU>(m, p, st);
+  const int64_t n8 = N * F / 8;
+  static int bps[2][64];
+  const int i = act == FP8_ACT_SILU ? 0 : 1;
+  auto kernel = i == 0 ? gated_bwd_amax_kernel<FP8_ACT_SILU> : gated_bwd_amax_kernel<FP8_ACT_GELU>;
+  const int64_t resident = (int64_t)blocks_per_sm(kernel, kAmaxThreads, bps[i]) * num_sms();
+  p.n_partials = (int)std::max<int64_t>(
+      1, std::min<int64_t>({(n8 + kAmaxThreads - 1) / kAmaxThreads, resident, kMaxPartials}));
+  {
+    LaunchScope ls("gated_bwd_amax", st, 6.0 * N * F, 0.0, N, F);
+    const cudaError_t e =
+        launch_kernel(kernel, dim3((unsigned)p.n_partials), dim3(kAmaxThreads), 0, st, p.dh, p.g, p.u,
+                      n8, partials);
+    if (e != cudaSuccess) return e;
+  }
+  return act == FP8_ACT_SILU ? launch_cast<false, FP8_ACT_SILU>(m, p, st)
+                             : launch_cast<false, FP8_ACT_GELU>(m, p, st);
+}
+
+cudaError_t gated_read_status(unsigned *status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_gated_status, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_gated_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace fp8lin

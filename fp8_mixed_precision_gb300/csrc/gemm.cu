@@ -1208,6 +1208,13 @@ bool make_bf16_tile_map(CUtensorMap *m, const void *base, int64_t rows, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_u8_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows) {
+  return make_map(m, base, rows, cols, box_rows);
+}
+bool make_bf16_slab_map(CUtensorMap *m, void *base, int64_t rows, int64_t cols) {
+  return make_out_map(m, base, rows, cols, false);
+}
+
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int scaling) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   const Plan p = make_plan(M, N, K, scaling);

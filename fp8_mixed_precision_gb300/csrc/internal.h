@@ -88,7 +88,9 @@ int tensorwise_partials_count(int64_t rows, int64_t cols);
 
 // mode: 0 tensorwise, 1 1x128 blocks, 2 128x128 tiles; fmt: fp8_format.
 // Tensorwise with amax_done: the first pass already wrote `partials`
-// (launch_amax_partials on the same tensor); only the cast runs.
+// (launch_amax_partials on the same tensor); only the cast runs.  rows need
+// not be a multiple of 16 here: out_col then has rows of rows rounded up to
+// 16 bytes, filled up with zeros.
 cudaError_t launch_quantize(const void *x, int64_t rows, int64_t cols, int mode, int fmt,
                             uint8_t *out_row, uint8_t *out_col, float *row_scale,
                             float *row_scale_inv, float *col_scale, float *col_scale_inv,
@@ -129,6 +131,55 @@ cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const 
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, cudaStream_t st);
 // Reads and clears the GEMM kernels' device status word (0 = ok).
 cudaError_t gemm_read_status(unsigned *status, cudaStream_t st);
+
+// Operand and output tiles of the GEMM kernels: u8 [rows, cols] boxes of
+// box_rows rows x 128 bytes, and bf16 [rows, cols] boxes of 32 rows x 64
+// columns, both 128-byte swizzled.
+bool make_u8_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows);
+bool make_bf16_slab_map(CUtensorMap *m, void *base, int64_t rows, int64_t cols);
+
+// Root-mean-square norm (norm.cu).  cols: a multiple of 16, at most
+// kMaxNormCols (a row is held in the registers of one CTA).
+constexpr int64_t kMaxNormCols = 16384;
+cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, int w_f32,
+                                int64_t rows, int64_t cols, float eps, void *r, float *rstd,
+                                void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
+                                cudaStream_t st);
+cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const void *w, int w_f32,
+                                int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
+                                float *col_scale_inv, cudaStream_t st);
+// partials: norm_bwd_ctas(rows, cols) x cols floats.
+int norm_bwd_ctas(int64_t rows, int64_t cols);
+cudaError_t launch_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const float *rstd,
+                               const void *w, int w_f32, int64_t rows, int64_t cols, void *dx,
+                               float *dw, float *partials, cudaStream_t st);
+cudaError_t norm_read_status(unsigned *status);
+
+// Gated feed-forward (gated.cu).  Any number of tokens N; G and U null: no
+// backward pass follows.
+cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
+                             const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
+                             int act, void *H, void *G, void *U, cudaStream_t st);
+// dG and dU, E5M2, as one [N, 2F] tensor and its transpose [2F, N rounded up
+// to 16].  Tensor scaling: row_scale_inv takes the one scale, partials
+// kMaxPartials floats.
+cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void *U, int64_t N,
+                                      int64_t F, bool block, int act, uint8_t *row, uint8_t *col,
+                                      float *row_scale_inv, float *col_scale_inv, float *partials,
+                                      cudaStream_t st);
+cudaError_t gated_read_status(unsigned *status);
+
+// Gradient clipping (clip.cu): one chunk of one tensor.
+struct ClipChunk {
+  const void *src;
+  void *dst;
+  int32_t n;    // elements
+  int32_t f32;  // 1: fp32, 0: bf16
+};
+int clip_ctas(int64_t chunks);  // partial sums the first pass writes
+// write = false: the norm alone.
+cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,
+                        bool write, float max_norm, float *norm, float *partials, cudaStream_t st);
 
 cudaError_t launch_gelu_fwd(const void *H, void *A, int64_t n, cudaStream_t st);
 cudaError_t launch_gelu_bwd(const void *dA, const void *H, void *dH, int64_t n, cudaStream_t st);

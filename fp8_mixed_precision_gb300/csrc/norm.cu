@@ -1,0 +1,570 @@
+// Root-mean-square norm of the residual stream, with the residual's addition
+// and an E4M3 output in 1x128 blocks, and its backward pass.
+//
+//   r = bf16(x + residual)          (no residual: r = x)
+//   rstd = 1 / sqrt(mean(r^2) + eps)
+//   y = (r * rstd) * w              fp32, quantized without another rounding
+//   backward, with g = dy * w and c = mean(g * r) over a row's C columns:
+//     dx = dr + rstd * g - r * (rstd^3 * c)      (x and the residual share it)
+//     dw = sum over rows of (dy * r) * rstd
+//
+// All arithmetic and sums are fp32; r and dx are rounded to bf16 once, as the
+// framework keeps activations and gradients.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fp8lin {
+namespace {
+
+__device__ unsigned g_norm_status;
+constexpr uint64_t kNWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kNormThreads = 256;
+
+// Norm weight: bf16 or fp32, eight consecutive values.
+struct NormW {
+  const void *w;
+  int f32;
+};
+__device__ __forceinline__ void load_w8(const NormW &w, int64_t c, float (&v)[8]) {
+  if (w.f32) {
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w.w) + c);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w.w) + c));
+    v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
+    v[4] = bf16lo(a.z); v[5] = bf16hi(a.z); v[6] = bf16lo(a.w); v[7] = bf16hi(a.w);
+  }
+}
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+  v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+  v[4] = bf16lo(w.z); v[5] = bf16hi(w.z); v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+// y = (r * rstd) * w, the one place where the forward pass forms it.
+__device__ __forceinline__ void norm8(uint4 r, float rstd, const float (&w)[8], float (&y)[8]) {
+  float v[8];
+  unpack8(r, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(__fmul_rn(v[k], rstd), w[k]);
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct NormFwd {
+  const uint4 *x, *res;  // bf16 [R, C]; res may be null
+  NormW w;
+  int64_t R, C;
+  float eps;
+  uint4 *r;      // bf16 [R, C]; written when res is given
+  float *rstd;   // [R] or null
+  uint4 *y;      // bf16 [R, C] or null
+  uint8_t *row;  // E4M3 [R, C] or null
+  float *row_scale, *row_scale_inv;
+};
+
+// Rows: a group of WPR warps holds one row in registers (VPT vectors of 8
+// elements per thread), so x and the residual are read once and everything
+// that the row alone determines is written from there.
+template <int VPT, int WPR>
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
+    rmsnorm_rows_kernel(NormFwd a) {
+  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
+  constexpr int kRows = kWarps / WPR;  // rows per CTA
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wir = warp % WPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
+  const bool live = row < a.R;
+  const int nv = (int)(a.C / 8);
+  const int64_t base = row * nv;
+  uint4 rv[VPT];
+  float ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = (j * WPR + wir) * 32 + lane;
+    rv[j] = make_uint4(0, 0, 0, 0);
+    if (live && v < nv) rv[j] = a.x[base + v];
+  }
+  if (a.res) {
+    uint4 sv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      sv[j] = make_uint4(0, 0, 0, 0);
+      if (live && v < nv) sv[j] = a.res[base + v];
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      float p[8], q[8];
+      unpack8(rv[j], p);
+      unpack8(sv[j], q);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] += q[k];
+      rv[j] = pack8(p);
+      if (live && v < nv) a.r[base + v] = rv[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float p[8];
+    unpack8(rv[j], p);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(p[k], p[k], ss);
+  }
+  ss = warp_sum(ss);
+  if constexpr (WPR > 1) {
+    __shared__ float red[kWarps];
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) ss += red[(warp / WPR) * WPR + k];
+  }
+  if (!live) return;
+  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.C), a.eps));
+  if (a.rstd && wir == 0 && lane == 0) a.rstd[row] = rstd;
+  const int64_t nb = (a.C + 127) / 128;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = (j * WPR + wir) * 32 + lane;
+    const bool in = v < nv;
+    if (__all_sync(0xffffffffu, !in)) break;
+    float w8[8] = {}, y[8];
+    if (in) load_w8(a.w, (int64_t)v * 8, w8);
+    norm8(rv[j], rstd, w8, y);
+    if (a.y && in) a.y[base + v] = pack8(y);
+    if (a.row) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = amax_acc(m, y[k]);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float s, si;
+      scale_from_amax(m, kE4M3Max, s, si);
+      if (in) {
+        uint2 q;
+        q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[0], s), __fmul_rn(y[1], s), __fmul_rn(y[2], s),
+                                    __fmul_rn(y[3], s));
+        q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[4], s), __fmul_rn(y[5], s), __fmul_rn(y[6], s),
+                                    __fmul_rn(y[7], s));
+        *reinterpret_cast<uint2 *>(a.row + row * a.C + (int64_t)v * 8) = q;
+        if ((lane & 15) == 0) {
+          a.row_scale[row * nb + v / 16] = s;
+          a.row_scale_inv[row * nb + v / 16] = si;
+        }
+      }
+    }
+  }
+}
+
+struct NormCols {
+  NormW w;
+  int64_t R, C, ldr;  // ldr: tokens per row of the transposed layout (R rounded up to 16)
+  const float *rstd;
+  uint8_t *col;  // E4M3 [C, ldr]
+  float *col_scale, *col_scale_inv;
+};
+
+struct __align__(128) CSmem {
+  uint16_t in[2][128 * 128];
+  uint32_t tile[128 * 32];
+  float colred[8][128];
+  float colsc[128];
+  uint64_t full[2];
+};
+
+// Bounded wait for a tile; on expiry the status word records FP8_ERR_TIMEOUT
+// and the caller carries on (its results are then invalid).
+__device__ __forceinline__ void wait_tile(uint64_t *bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    if ((it & 63) == 0 && ptx::globaltimer() - t0 > kNWaitLimitNs) {
+      atomicCAS(&g_norm_status, 0u, (unsigned)FP8_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
+
+// Transposed copy: 128 tokens x 128 columns per iteration.  r comes back by
+// TMA, y is formed again from r, rstd and w, each column's maximum over its
+// 128 tokens gives its scale, and the bytes go through a swizzled tile so
+// that 16 tokens leave in one store.  Tokens past R are zeros.
+__global__ void __launch_bounds__(kNormThreads, 2)
+    rmsnorm_cols_kernel(const __grid_constant__ CUtensorMap tmr, NormCols p) {
+  extern __shared__ __align__(1024) uint8_t n_smem_raw[];
+  CSmem &S = *reinterpret_cast<CSmem *>(n_smem_raw);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int cg = t & 15, rr = t >> 4;
+  const int64_t tiles_r = (p.R + 127) / 128, tiles_c = (p.C + 127) / 128;
+  const int64_t ntiles = tiles_r * tiles_c;
+  if (t == 0) {
+    ptx::mbar_init(&S.full[0], 1);
+    ptx::mbar_init(&S.full[1], 1);
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmr);
+  }
+  __syncthreads();
+  pdl_wait_then_release();
+  auto prefetch = [&](int64_t id, int b) {
+    if (t != 0 || id >= ntiles) return;
+    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive_expect_tx(&S.full[b], 128u * 128 * 2);
+    ptx::tma_load_2d(S.in[b], &tmr, &S.full[b], (int)(tc * 128), (int)(tr * 128));
+  };
+  int64_t id = blockIdx.x;
+  prefetch(id, 0);
+  prefetch(id + gridDim.x, 1);
+  for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
+    const int b = k & 1;
+    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    const int64_t r0 = tr * 128, c0 = tc * 128;
+    const int rows_here = (int)(p.R - r0 < 128 ? p.R - r0 : 128);
+    const int cols_here = (int)(p.C - c0 < 128 ? p.C - c0 : 128);
+    float w8[8] = {};
+    if (8 * cg < cols_here) load_w8(p.w, c0 + 8 * cg, w8);
+    float rs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = rr + 16 * i;
+      rs[i] = r < rows_here ? p.rstd[r0 + r] : 0.0f;
+    }
+    wait_tile(&S.full[b], (k >> 1) & 1);
+    __syncthreads();
+    uint4 xw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      xw[i] = *reinterpret_cast<const uint4 *>(&S.in[b][(rr + 16 * i) * 128 + 8 * cg]);
+    float cm[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float y[8];
+      norm8(xw[i], rs[i], w8, y);
+      if (rr + 16 * i < rows_here)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cm[j] = amax_acc(cm[j], y[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+    if (lane < 16)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) S.colred[warp][8 * cg + j] = cm[j];
+    __syncthreads();
+    prefetch(id + 2 * (int64_t)gridDim.x, b);  // every thread holds its elements
+    if (t < 128) {
+      float m = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = fmaxf(m, S.colred[w][t]);
+      float s, si;
+      scale_from_amax(m, kE4M3Max, s, si);
+      S.colsc[t] = s;
+      if (t < cols_here) {
+        p.col_scale[(c0 + t) * tiles_r + tr] = s;
+        p.col_scale_inv[(c0 + t) * tiles_r + tr] = si;
+      }
+    }
+    __syncthreads();
+    float cs[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cs[j] = S.colsc[8 * cg + j];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = rr + 16 * i;
+      float y[8];
+      norm8(xw[i], rs[i], w8, y);
+      uint2 q = make_uint2(0, 0);
+      if (r < rows_here) {
+        q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[0], cs[0]), __fmul_rn(y[1], cs[1]),
+                                    __fmul_rn(y[2], cs[2]), __fmul_rn(y[3], cs[3]));
+        q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[4], cs[4]), __fmul_rn(y[5], cs[5]),
+                                    __fmul_rn(y[6], cs[6]), __fmul_rn(y[7], cs[7]));
+      }
+      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = q;
+    }
+    __syncthreads();
+    const int seg = t & 7, w = t >> 3;  // rows seg*16..+15, columns 4w..4w+3
+    if (4 * w < cols_here && 16 * seg < rows_here) {
+      uint32_t a[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = seg * 16 + i;
+        a[i] = S.tile[r * 32 + (w ^ swz(r))];
+      }
+      uint32_t o[4][4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t t0 = __byte_perm(a[4 * g + 0], a[4 * g + 1], 0x5140);
+        const uint32_t t1 = __byte_perm(a[4 * g + 0], a[4 * g + 1], 0x7362);
+        const uint32_t t2 = __byte_perm(a[4 * g + 2], a[4 * g + 3], 0x5140);
+        const uint32_t t3 = __byte_perm(a[4 * g + 2], a[4 * g + 3], 0x7362);
+        o[0][g] = __byte_perm(t0, t2, 0x5410);
+        o[1][g] = __byte_perm(t0, t2, 0x7632);
+        o[2][g] = __byte_perm(t1, t3, 0x5410);
+        o[3][g] = __byte_perm(t1, t3, 0x7632);
+      }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+        *reinterpret_cast<uint4 *>(p.col + (c0 + 4 * w + jj) * p.ldr + r0 + 16 * seg) =
+            make_uint4(o[jj][0], o[jj][1], o[jj][2], o[jj][3]);
+    }
+  }
+}
+
+struct NormBwd {
+  const uint4 *dy, *dr, *r;  // bf16 [R, C]; dr may be null
+  const float *rstd;
+  NormW w;
+  int64_t R, C;
+  uint4 *dx;        // bf16 [R, C]
+  float *partials;  // [gridDim.x, C] sums of this CTA's rows
+};
+
+// Backward: a group of WPR warps per row, rows in a grid-stride loop; each
+// thread keeps the dw sums of its own columns over all rows of its group.
+template <int VPT, int WPR>
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
+    rmsnorm_bwd_kernel(NormBwd a) {
+  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
+  constexpr int kRows = kWarps / WPR;
+  __shared__ float red[2][kWarps];
+  extern __shared__ float dwsum[];  // kRows > 1: [kRows - 1][C] sums of the other groups
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wir = warp % WPR, grp = warp / WPR;
+  const int nv = (int)(a.C / 8);
+  float dw[VPT][8] = {};
+  const float inv_c = __fdiv_rn(1.0f, (float)a.C);
+  int buf = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.R;
+       row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + grp;
+    const bool live = row < a.R;
+    const int64_t base = row * nv;
+    uint4 dyv[VPT], rv[VPT], drv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      const bool in = live && v < nv;
+      dyv[j] = rv[j] = drv[j] = make_uint4(0, 0, 0, 0);
+      if (in) dyv[j] = a.dy[base + v];
+      if (in) rv[j] = a.r[base + v];
+      if (in && a.dr) drv[j] = a.dr[base + v];
+    }
+    const float rstd = live ? a.rstd[row] : 0.0f;
+    float c = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      float w8[8] = {}, d[8], r[8];
+      if (v < nv) load_w8(a.w, (int64_t)v * 8, w8);
+      unpack8(dyv[j], d);
+      unpack8(rv[j], r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        c = fmaf(d[k] * w8[k], r[k], c);
+        dw[j][k] = fmaf(d[k] * r[k], rstd, dw[j][k]);
+      }
+    }
+    c = warp_sum(c);
+    if constexpr (WPR > 1) {
+      if (lane == 0) red[buf][warp] = c;
+      __syncthreads();
+      c = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) c += red[buf][grp * WPR + k];
+      buf ^= 1;  // the other half next time: one barrier per row
+    }
+    const float c3 = c * inv_c * rstd * rstd * rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      if (live && v < nv) {
+        float w8[8], d[8], r[8], e[8];
+        load_w8(a.w, (int64_t)v * 8, w8);
+        unpack8(dyv[j], d);
+        unpack8(rv[j], r);
+        unpack8(drv[j], e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = fmaf(-r[k], c3, fmaf(d[k] * w8[k], rstd, e[k]));
+        a.dx[base + v] = pack8(e);
+      }
+    }
+  }
+  // this CTA's column sums: the groups in order
+  if constexpr (kRows > 1) {
+    if (grp > 0)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = (j * WPR + wir) * 32 + lane;
+        if (v < nv)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dwsum[(int64_t)(grp - 1) * a.C + v * 8 + k] = dw[j][k];
+      }
+    __syncthreads();
+  }
+  if (grp == 0)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      if (v < nv) {
+        for (int g = 1; g < kRows; ++g)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dw[j][k] += dwsum[(int64_t)(g - 1) * a.C + v * 8 + k];
+        float4 *dst = reinterpret_cast<float4 *>(a.partials + (int64_t)blockIdx.x * a.C + v * 8);
+        dst[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+        dst[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+      }
+    }
+}
+
+// dw[c] = sum of the CTAs' partials in a fixed order: 32 columns x 8 parts of
+// the CTAs per block, the parts joined in order.
+__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ partials, int n,
+                                                         int64_t C, float *__restrict__ dw) {
+  pdl_wait_then_release();
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < C)
+    for (int k = warp; k < n; k += 8) s += partials[(int64_t)k * C + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < C) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += part[k][lane];
+    dw[c] = s;
+  }
+}
+
+template <int VPT, int WPR>
+cudaError_t launch_rows(const NormFwd &a, cudaStream_t st) {
+  constexpr int kThreads = WPR > 8 ? 32 * WPR : kNormThreads;
+  constexpr int kRows = kThreads / 32 / WPR;
+  return launch_kernel(rmsnorm_rows_kernel<VPT, WPR>, dim3((unsigned)((a.R + kRows - 1) / kRows)),
+                       dim3(kThreads), 0, st, a);
+}
+
+template <int VPT, int WPR>
+cudaError_t launch_bwd(NormBwd a, int grid, cudaStream_t st) {
+  constexpr int kThreads = WPR > 8 ? 32 * WPR : kNormThreads;
+  constexpr int kRows = kThreads / 32 / WPR;
+  const size_t smem = (size_t)(kRows - 1) * a.C * 4;
+  return launch_kernel(rmsnorm_bwd_kernel<VPT, WPR>, dim3((unsigned)grid), dim3(kThreads), smem, st,
+                       a);
+}
+
+// Warps per row of the backward pass for C columns, at two vectors (16
+// elements) per thread: 32 warps hold kMaxNormCols columns.
+int bwd_warps(int64_t C) {
+  int wpr = 1;
+  while ((int64_t)wpr * 512 < C) wpr *= 2;
+  return wpr;
+}
+
+}  // namespace
+
+// CTAs of the backward pass: a function of the shape alone, so that the order
+// of the dw sums is too.
+int norm_bwd_ctas(int64_t rows, int64_t cols) {
+  const int wpr = bwd_warps(cols);
+  const int64_t per_cta = wpr >= 8 ? 1 : 8 / wpr;
+  const int64_t most = wpr <= 8 ? 152 * 4 : wpr == 16 ? 152 * 2 : 152;
+  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + per_cta - 1) / per_cta, most));
+}
+
+cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, int w_f32,
+                                int64_t rows, int64_t cols, float eps, void *r, float *rstd,
+                                void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
+                                cudaStream_t st) {
+  NormFwd a{static_cast<const uint4 *>(x), static_cast<const uint4 *>(res), {w, w_f32}, rows, cols,
+            eps, static_cast<uint4 *>(r), rstd, static_cast<uint4 *>(y), row, row_scale,
+            row_scale_inv};
+  const double n = (double)rows * cols;
+  LaunchScope ls("rmsnorm_rows", st,
+                 n * (2 + (res ? 4 : 0) + (y ? 2 : 0) + (row ? 1 : 0)) +
+                     rows * 8.0 * ((cols + 127) / 128),
+                 4 * n, rows, cols);
+  const int64_t nv = cols / 8;
+  if (nv <= 32) return launch_rows<1, 1>(a, st);
+  if (nv <= 64) return launch_rows<2, 1>(a, st);
+  if (nv <= 128) return launch_rows<4, 1>(a, st);
+  if (nv <= 256) return launch_rows<4, 2>(a, st);
+  if (nv <= 512) return launch_rows<4, 4>(a, st);
+  if (nv <= 1024) return launch_rows<4, 8>(a, st);
+  return launch_rows<4, 16>(a, st);  // up to kMaxNormCols
+}
+
+cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const void *w, int w_f32,
+                                int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
+                                float *col_scale_inv, cudaStream_t st) {
+  CUtensorMap tm;
+  if (!make_bf16_tile_map(&tm, r, rows, cols, 128, 128)) return cudaErrorInvalidValue;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        rmsnorm_cols_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(CSmem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  NormCols p{{w, w_f32}, rows, cols, (rows + 15) / 16 * 16, rstd, col, col_scale, col_scale_inv};
+  const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+  const int64_t grid = std::min<int64_t>(tiles, (int64_t)num_sms() * 2);
+  LaunchScope ls("rmsnorm_cols", st,
+                 3.0 * rows * cols + 4.0 * rows + 8.0 * cols * ((rows + 127) / 128),
+                 2.0 * rows * cols, rows, cols);
+  return launch_kernel(rmsnorm_cols_kernel, dim3((unsigned)grid), dim3(kNormThreads),
+                       sizeof(CSmem), st, tm, p);
+}
+
+cudaError_t launch_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const float *rstd,
+                               const void *w, int w_f32, int64_t rows, int64_t cols, void *dx,
+                               float *dw, float *partials, cudaStream_t st) {
+  NormBwd a{static_cast<const uint4 *>(dy), static_cast<const uint4 *>(dr),
+            static_cast<const uint4 *>(r), rstd, {w, w_f32}, rows, cols, static_cast<uint4 *>(dx),
+            partials};
+  const int grid = norm_bwd_ctas(rows, cols);
+  {
+    LaunchScope ls("rmsnorm_bwd", st, (dr ? 8.0 : 6.0) * rows * cols + 4.0 * rows,
+                   8.0 * rows * cols, rows, cols);
+    cudaError_t e;
+    switch (bwd_warps(cols)) {
+      case 1: e = launch_bwd<2, 1>(a, grid, st); break;
+      case 2: e = launch_bwd<2, 2>(a, grid, st); break;
+      case 4: e = launch_bwd<2, 4>(a, grid, st); break;
+      case 8: e = launch_bwd<2, 8>(a, grid, st); break;
+      case 16: e = launch_bwd<2, 16>(a, grid, st); break;
+      default: e = launch_bwd<2, 32>(a, grid, st); break;
+    }
+    if (e != cudaSuccess) return e;
+  }
+  LaunchScope ls("rmsnorm_dw", st, 4.0 * grid * cols + 4.0 * cols, (double)grid * cols, grid, cols);
+  return launch_kernel(rmsnorm_dw_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st,
+                       (const float *)partials, grid, cols, dw);
+}
+
+cudaError_t norm_read_status(unsigned *status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_norm_status, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace fp8lin

@@ -109,8 +109,9 @@ struct QParams {
   const uint16_t *x;
   const uint16_t *x2;  // fused GELU backward: H (x holds dA)
   int64_t R, C;
+  int64_t ldc;       // bytes per row of out_col: R rounded up to 16, zeros past R
   uint8_t *out_row;  // [R, C] or null
-  uint8_t *out_col;  // [C, R] or null
+  uint8_t *out_col;  // [C, ldc] or null
   float *row_scale, *row_scale_inv;
   float *col_scale, *col_scale_inv;
   const float *partials;  // tensorwise: per-CTA amax of pass 1
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
         }
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-          *reinterpret_cast<uint4 *>(p.out_col + (c0 + 4 * w + jj) * p.R + r0 + 16 * seg) =
+          *reinterpret_cast<uint4 *>(p.out_col + (c0 + 4 * w + jj) * p.ldc + r0 + 16 * seg) =
               make_uint4(o[jj][0], o[jj][1], o[jj][2], o[jj][3]);
       }
     }
@@ -665,6 +666,7 @@ cudaError_t launch_quantize(const void *x, int64_t rows, int64_t cols, int mode,
   p.x2 = nullptr;
   p.R = rows;
   p.C = cols;
+  p.ldc = (rows + 15) / 16 * 16;
   p.out_row = out_row;
   p.out_col = out_col;
   p.row_scale = row_scale;
@@ -701,6 +703,7 @@ cudaError_t launch_quantize_delayed(const void *x, int64_t rows, int64_t cols, i
   p.x2 = nullptr;
   p.R = rows;
   p.C = cols;
+  p.ldc = (rows + 15) / 16 * 16;
   p.out_row = out_row;
   p.out_col = out_col;
   p.row_scale = scale;
@@ -731,6 +734,7 @@ cudaError_t launch_gelu_quantize(const void *H, const void *H2, int64_t rows, in
   p.x2 = static_cast<const uint16_t *>(H2);
   p.R = rows;
   p.C = cols;
+  p.ldc = (rows + 15) / 16 * 16;
   p.out_row = out_row;
   p.out_col = out_col;
   p.row_scale = row_scale;

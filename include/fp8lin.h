@@ -11,6 +11,9 @@
  *   weight cache - is_first_microbatch semantics ("FP8 weight caching shows no
  *                 speedup ... under Float8BlockScaling", TransformerEngine
  *                 issue #2852, opening post and maintainer reply);
+ *   gated MLP   - RMS norm with the residual's addition and an FP8 output, the
+ *                 gated feed-forward on FP8 operands, and global gradient
+ *                 norm clipping, each with its backward pass where it has one;
  *   FP8 GEMMs   - fprop, dgrad and wgrad on tcgen05 tensor cores with fp32
  *                 accumulation and BF16 output (use_fast_accum=False in the
  *                 reconstruction's implementation paragraph).
@@ -27,6 +30,9 @@
  *     dimension need not be a multiple of 128: the last 128-block of a row,
  *     column or tile is then shorter ("ragged tail") and its amax covers the
  *     elements present.  A zero dimension makes the call a no-op (FP8_OK).
+ *     The norm and the gated feed-forward take any number of tokens; their
+ *     transposed FP8 layouts have rows of the token count rounded up to a
+ *     multiple of 16, filled up with zero bytes.
  *   - bf16 tensors are passed as `const void*` (IEEE bfloat16 bit patterns).
  *   - Every call enqueues work on `stream` (a cudaStream_t; NULL = legacy
  *     default stream) and returns without synchronising, except
@@ -336,6 +342,125 @@ fp8_status fp8_linear_bwd_quantized(const uint8_t *gq_row, const float *gq_row_s
 fp8_status fp8_gelu_fwd(const void *H, void *A, int64_t n, fp8_stream_t stream);
 fp8_status fp8_gelu_bwd(const void *dA, const void *H, void *dH, int64_t n, fp8_stream_t stream);
 fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream_t stream);
+
+/* ------------------------------------------------------------------ RMS norm
+ * fp8_rmsnorm_fwd: the residual stream's addition, its root-mean-square norm
+ * and the norm's FP8 output, for a bf16 [rows, cols] x:
+ *   r = bf16(x + residual) (residual NULL: r = x), rstd = (mean(r^2) + eps)^-1/2,
+ *   y = (r * rstd) * w in fp32; y is quantized as it is (E4M3, activation role
+ *   of the block recipe, 1x128 blocks, scale rule as above) and/or rounded to
+ *   bf16.  Squares and sums are fp32.
+ *   rows           any number of tokens; cols: a multiple of 16, at most 16384
+ *   w              device bf16 or fp32 [cols], as w_dtype says
+ *   eps            positive
+ *   r_out          device bf16 [rows, cols]; given exactly when residual is.
+ *                  May be x or residual itself (in place).
+ *   rstd           device f32 [rows], or NULL; required with colwise_out and
+ *                  for a backward pass
+ *   y              device bf16 [rows, cols] or NULL
+ *   rowwise_out    device u8 [rows, cols] or NULL, with row_scale,
+ *                  row_scale_inv f32 [rows, ceil(cols/128)]
+ *   colwise_out    device u8 [cols, rows rounded up to 16] or NULL (bytes past
+ *                  `rows` are written as zeros), with col_scale, col_scale_inv
+ *                  f32 [cols, ceil(rows/128)].  Not all three outputs NULL.
+ * fp8_rmsnorm_bwd: from dy = dL/dy (bf16), r and rstd of the forward pass and
+ *   dr = dL/dr (bf16, the stream's own gradient, or NULL for none), with
+ *   g = dy * w and c = mean(g * r) over a row:
+ *   dx = dr + rstd * g - r * rstd^3 * c   (bf16; x and residual share it; may
+ *        be dy or dr itself)
+ *   dw = sum over rows of dy * r * rstd   (f32 [cols]; zeros when rows = 0)
+ *   The FP8 cast and its scales are constants of the backward (detached).
+ *   workspace: fp8_rmsnorm_workspace_size bytes.  Deterministic.
+ * Errors: INVALID_ARG, SHAPE, UNSUPPORTED (cols > 16384), ALIGN, WORKSPACE, CUDA. */
+typedef enum { FP8_DTYPE_BF16 = 0, FP8_DTYPE_F32 = 1 } fp8_dtype;
+
+fp8_status fp8_rmsnorm_fwd(const void *x, const void *residual, const void *w, fp8_dtype w_dtype,
+                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd, void *y,
+                           uint8_t *rowwise_out, uint8_t *colwise_out, float *row_scale,
+                           float *row_scale_inv, float *col_scale, float *col_scale_inv,
+                           fp8_stream_t stream);
+fp8_status fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes);
+fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const float *rstd,
+                           const void *w, fp8_dtype w_dtype, int64_t rows, int64_t cols, void *dx,
+                           float *dw, void *workspace, size_t workspace_bytes, fp8_stream_t stream);
+
+/* ------------------------------------------------------------------ gated feed-forward
+ * H[N, F] = act(X Wg^T) * (X Wu^T), the weight registered in a weight cache as
+ * one W = [Wg; Wu] [2F, K].  X is quantized as fp8_linear_fwd's; both
+ * projections, the activation and the product are one kernel, H is formed from
+ * the fp32 accumulators and rounded once to bf16.
+ *   N   any number of tokens;  K, F multiples of 16, under the block recipe F a
+ *       multiple of 128 (the weight's 128x128 tiles must not straddle Wg and Wu)
+ *   ctx device buffer of fp8_gated_ctx_size bytes for the backward pass (the
+ *       transposed FP8 X and its scales, and both projections as bf16), or NULL
+ *       when none follows
+ *   ws  device scratch of fp8_gated_workspace_size bytes (train = 0: enough for
+ *       the forward pass alone)
+ * fp8_gated_fwd_quantized: X given as its rowwise bytes and scale_inv (e.g.
+ *   from fp8_rmsnorm_fwd); with ctx the caller has already filled its transposed
+ *   part (fp8_gated_ctx_layout says where).
+ * fp8_gated_bwd: with G and U as the forward pass kept them (bf16),
+ *   dG = (dH * U) * act'(G), dU = dH * act(G) in fp32, cast to E5M2 in both
+ *   layouts as one [N, 2F] tensor; dX = dGU W (or NULL), dW = dGU^T X [2F, K],
+ *   the forward's rounded W and X reused (bf16; dW zeros when N = 0).
+ * act: silu(g) = g / (1 + e^-g), or GELU in its exact erf form.
+ * Weight-cache and recipe rules as fp8_linear_fwd / bwd (delayed recipe: its
+ * activations and gradients use current tensorwise scaling).
+ * Errors: INVALID_ARG, SHAPE, ALIGN, STALE, WORKSPACE, CUDA. */
+typedef enum { FP8_ACT_SILU = 0, FP8_ACT_GELU = 1 } fp8_act;
+
+fp8_status fp8_gated_ctx_size(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, size_t *bytes);
+fp8_status fp8_gated_ctx_layout(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, void *ctx,
+                                uint8_t **xq_col, float **col_scale, float **col_scale_inv,
+                                void **g, void **u);
+fp8_status fp8_gated_workspace_size(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, int train,
+                                    size_t *bytes);
+fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *cache,
+                         fp8_weight_handle h, fp8_recipe recipe, fp8_act act, void *H, void *ctx,
+                         void *ws, size_t ws_bytes, fp8_stream_t stream);
+fp8_status fp8_gated_fwd_quantized(const uint8_t *xq_row, const float *xq_row_scale_inv, int64_t N,
+                                   int64_t K, fp8_weight_cache *cache, fp8_weight_handle h,
+                                   fp8_recipe recipe, fp8_act act, void *H, void *ctx,
+                                   fp8_stream_t stream);
+fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
+                         fp8_weight_cache *cache, fp8_weight_handle h, fp8_recipe recipe,
+                         fp8_act act, void *dX, void *dW, void *ws, size_t ws_bytes,
+                         fp8_stream_t stream);
+
+/* ------------------------------------------------------------------ gradient clipping
+ * Global norm of a set of gradient tensors and clipping by it:
+ *   norm = sqrt(sum of g^2 over all tensors), coef = min(1, max_norm / (norm + 1e-6)),
+ *   dst = g * coef.  A norm that is not finite (an inf or NaN gradient, or squares
+ *   past the fp32 range) leaves coef at 1, so the caller reads `norm` and decides.
+ * A plan is a host object made once for a set of tensors (their addresses and
+ * sizes).  Its table goes into caller-owned device memory: write it into host
+ * memory of fp8_grad_clip_table_size bytes, copy that to the device (8-byte
+ * aligned) and pass it to every call.
+ *   src, dst   device tensors of n elements, dst = src clips in place; any
+ *              alignment of the element type (16-byte aligned ones are faster)
+ *   max_norm   positive; infinity leaves every gradient as it is
+ *   norm       device f32 [1]
+ *   workspace  fp8_grad_clip_workspace_size bytes
+ * fp8_grad_norm: the norm alone; nothing else is written.
+ * Deterministic for a plan on a GPU.
+ * Errors: INVALID_ARG, ALIGN, WORKSPACE, CUDA. */
+typedef struct {
+  const void *src;
+  void *dst;
+  int64_t n;
+  fp8_dtype dtype; /* of src and dst */
+} fp8_grad_desc;
+typedef struct fp8_grad_clip fp8_grad_clip;
+fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_grad_clip **out);
+void fp8_grad_clip_destroy(fp8_grad_clip *plan);
+fp8_status fp8_grad_clip_table_size(const fp8_grad_clip *plan, size_t *bytes);
+fp8_status fp8_grad_clip_table_write(const fp8_grad_clip *plan, void *host, size_t bytes);
+fp8_status fp8_grad_clip_workspace_size(const fp8_grad_clip *plan, size_t *bytes);
+fp8_status fp8_grad_clip_run(const fp8_grad_clip *plan, const void *table, float max_norm,
+                             float *norm, void *workspace, size_t workspace_bytes,
+                             fp8_stream_t stream);
+fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *norm, void *workspace,
+                         size_t workspace_bytes, fp8_stream_t stream);
 
 /* ------------------------------------------------------------------ host-buffer steps
  * One forward + backward of an isolated FP8 linear (fp8_linear_fwd then
