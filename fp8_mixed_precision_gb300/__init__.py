@@ -23,7 +23,7 @@ __all__ = [
     "fp8_amax_partials", "fp8_linear_fwd_after_amax", "fp8_linear_bwd_after_amax",
     "ACTIVATION", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "rmsnorm_buffers", "rmsnorm_workspace",
     "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd", "GatedContext", "gated_context",
-    "gated_workspace", "fp8_gated_ctx_layout", "GradClip",
+    "gated_workspace", "fp8_gated_ctx_layout", "GradClip", "NormBuffers",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -123,7 +123,7 @@ class _GradDesc(ctypes.Structure):
 
 _SIGS.update({
     "fp8_rmsnorm_fwd": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, ctypes.c_float] +
-                        [_c_p] * 10),
+                        [_c_p] * 11),
     "fp8_rmsnorm_workspace_size": (_c_int, [_c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
     "fp8_rmsnorm_bwd": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, _c_p, _c_p,
                                  _c_p, _c_sz, _c_p]),
@@ -188,12 +188,17 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t of `stream`, by default of the current stream (read
+    without building a torch Stream object, which takes 3 us on this CPU)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need_bf16_cuda(t, name):
@@ -648,12 +653,39 @@ def fp8_linear_bwd_after_amax(dy: torch.Tensor, dy_partials: torch.Tensor, ctx: 
 
 # ---------------------------------------------------------------- RMS norm
 def _need(t, name, shape, dtype):
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == tuple(shape)):
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
 
 
+class NormBuffers(dict):
+    """Output buffers of fp8_rmsnorm_fwd.  Their shapes are checked on the first
+    call that writes them and again after an entry has been replaced."""
+
+    checked = None
+
+    def __setitem__(self, key, value):
+        super().__setitem__(key, value)
+        self.checked = None
+
+    def check(self, R, C, wanted):
+        """wanted: (r, rowwise, colwise, y) to be written for an [R, C] input."""
+        nb, rb = -(-C // 128), -(-R // 128)
+        r, row, col, y = wanted
+        bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+        for key, want, shape, dtype in (
+                ("rstd", True, (R,), f32), ("rstd_lo", col, (R,), f32), ("r", r, (R, C), bf16), ("y", y, (R, C), bf16),
+                ("row", row, (R, C), u8), ("row_scale", row, (R, nb), f32),
+                ("row_scale_inv", row, (R, nb), f32), ("col", col, (C, -(-R // 16) * 16), u8),
+                ("col_scale", col, (C, rb), f32), ("col_scale_inv", col, (C, rb), f32)):
+            if want:
+                if self.get(key) is None:
+                    raise ValueError(f"out has no buffer for {key}")
+                _need(self[key], key, shape, dtype)
+        self.checked = (R, C, wanted)
+
+
 def rmsnorm_buffers(R: int, C: int, device, residual: bool = True, rowwise: bool = True,
-                    colwise: bool = True, bf16: bool = False) -> dict:
+                    colwise: bool = True, bf16: bool = False) -> NormBuffers:
     """Output buffers of fp8_rmsnorm_fwd for an [R, C] input, to be passed as
     `out` by callers that keep them between calls (absent outputs are None)."""
     Rp, nb, rb = -(-R // 16) * 16, -(-C // 128), -(-R // 128)
@@ -661,14 +693,14 @@ def rmsnorm_buffers(R: int, C: int, device, residual: bool = True, rowwise: bool
     def f32(*shape):
         return torch.empty(shape, dtype=torch.float32, device=device)
 
-    return dict(r=torch.empty((R, C), dtype=torch.bfloat16, device=device) if residual else None,
-                rstd=f32(R), y=torch.empty((R, C), dtype=torch.bfloat16, device=device) if bf16 else None,
-                row=torch.empty((R, C), dtype=torch.uint8, device=device) if rowwise else None,
-                row_scale=f32(R, nb) if rowwise else None,
-                row_scale_inv=f32(R, nb) if rowwise else None,
-                col=torch.empty((C, Rp), dtype=torch.uint8, device=device) if colwise else None,
-                col_scale=f32(C, rb) if colwise else None,
-                col_scale_inv=f32(C, rb) if colwise else None)
+    return NormBuffers(
+        r=torch.empty((R, C), dtype=torch.bfloat16, device=device) if residual else None,
+        rstd=f32(R), rstd_lo=f32(R) if colwise else None,
+        y=torch.empty((R, C), dtype=torch.bfloat16, device=device) if bf16 else None,
+        row=torch.empty((R, C), dtype=torch.uint8, device=device) if rowwise else None,
+        row_scale=f32(R, nb) if rowwise else None, row_scale_inv=f32(R, nb) if rowwise else None,
+        col=torch.empty((C, Rp), dtype=torch.uint8, device=device) if colwise else None,
+        col_scale=f32(C, rb) if colwise else None, col_scale_inv=f32(C, rb) if colwise else None)
 
 
 def rmsnorm_workspace(R: int, C: int, device) -> torch.Tensor:
@@ -681,7 +713,7 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
                     eps: float = 1e-6, rowwise: bool = True, colwise: bool = True,
                     bf16: bool = False, out: dict | None = None, stream=None) -> dict:
     """Residual addition, RMS norm and FP8 output of a bf16 [R, C] x; w is a
-    bf16 or float32 [C].  Returns dict(r, rstd, y, row, row_scale,
+    bf16 or float32 [C].  Returns dict(r, rstd, rstd_lo, y, row, row_scale,
     row_scale_inv, col, col_scale, col_scale_inv), absent ones None: r is the
     residual stream bf16(x + residual) (x itself without a residual), row
     [R, C] and col [C, R rounded up to 16] the E4M3 bytes of the norm in 1x128
@@ -695,22 +727,17 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
         _need(residual, "residual", (R, C), torch.bfloat16)
     if out is None:
         out = rmsnorm_buffers(R, C, x.device, residual is not None, rowwise, colwise, bf16)
-    o = out
-    Rp = -(-R // 16) * 16
-    for key, want, shape, dtype in (("r", residual is not None, (R, C), torch.bfloat16),
-                                    ("y", bf16, (R, C), torch.bfloat16),
-                                    ("row", rowwise, (R, C), torch.uint8),
-                                    ("col", colwise, (C, Rp), torch.uint8)):
-        if want:
-            if o[key] is None:
-                raise ValueError(f"out has no buffer for {key}")
-            _need(o[key], key, shape, dtype)
+    if not isinstance(out, NormBuffers):
+        out = NormBuffers(out)
+    wanted = (residual is not None, rowwise, colwise, bf16)
+    if out.checked != (R, C, wanted):
+        out.check(R, C, wanted)
     _check(lib().fp8_rmsnorm_fwd(
-        _ptr(x), _ptr(residual), _ptr(w), _DTYPE[w.dtype], R, C, eps,
-        _ptr(o["r"]) if residual is not None else None, _ptr(o["rstd"]),
-        _ptr(o["y"]) if bf16 else None, _ptr(o["row"]) if rowwise else None,
-        _ptr(o["col"]) if colwise else None, _ptr(o["row_scale"]), _ptr(o["row_scale_inv"]),
-        _ptr(o["col_scale"]), _ptr(o["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
+        x.data_ptr(), _ptr(residual), w.data_ptr(), _DTYPE[w.dtype], R, C, eps,
+        _ptr(out["r"]) if residual is not None else None, out["rstd"].data_ptr(),
+        _ptr(out["rstd_lo"]) if colwise else None, _ptr(out["y"]) if bf16 else None, _ptr(out["row"]) if rowwise else None,
+        _ptr(out["col"]) if colwise else None, _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]),
+        _ptr(out["col_scale"]), _ptr(out["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
     return out if residual is not None else dict(out, r=x)
 
 

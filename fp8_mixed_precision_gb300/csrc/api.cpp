@@ -700,8 +700,8 @@ inline int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 }  // namespace
 
 fp8_status fp8_rmsnorm_fwd(const void *x, const void *residual, const void *w, fp8_dtype w_dtype,
-                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd, void *y,
-                           uint8_t *rowwise_out, uint8_t *colwise_out, float *row_scale,
+                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd,
+                           float *rstd_lo, void *y, uint8_t *rowwise_out, uint8_t *colwise_out, float *row_scale,
                            float *row_scale_inv, float *col_scale, float *col_scale_inv,
                            fp8_stream_t stream) {
   fp8_status st = check_norm(rows, cols, w_dtype);
@@ -711,16 +711,17 @@ fp8_status fp8_rmsnorm_fwd(const void *x, const void *residual, const void *w, f
   if (!y && !rowwise_out && !colwise_out) return FP8_ERR_INVALID_ARG;
   if ((residual != nullptr) != (r_out != nullptr)) return FP8_ERR_INVALID_ARG;
   if (!x || !w || (rowwise_out && (!row_scale || !row_scale_inv)) ||
-      (colwise_out && (!col_scale || !col_scale_inv || !rstd)))
+      (colwise_out && (!col_scale || !col_scale_inv || !rstd || !rstd_lo)))
     return FP8_ERR_INVALID_ARG;
   for (const void *p : {x, residual, w, (const void *)r_out, (const void *)y,
                         (const void *)rowwise_out, (const void *)colwise_out})
     if (!aligned16(p)) return FP8_ERR_ALIGN;
-  st = from_cuda(launch_rmsnorm_rows(x, residual, w, w_dtype, rows, cols, eps, r_out, rstd, y,
-                                     rowwise_out, row_scale, row_scale_inv, cs(stream)));
+  st = from_cuda(launch_rmsnorm_rows(x, residual, w, w_dtype, rows, cols, eps, r_out, rstd,
+                                     rstd_lo, y, rowwise_out, row_scale, row_scale_inv,
+                                     cs(stream)));
   if (st != FP8_OK || !colwise_out) return st;
-  return from_cuda(launch_rmsnorm_cols(residual ? r_out : x, rstd, w, w_dtype, rows, cols,
-                                       colwise_out, col_scale, col_scale_inv, cs(stream)));
+  return from_cuda(launch_rmsnorm_cols(residual ? r_out : x, rstd, rstd_lo, w, w_dtype, rows,
+                                       cols, colwise_out, col_scale, col_scale_inv, cs(stream)));
 }
 
 fp8_status fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes) {

@@ -32,6 +32,38 @@ __device__ __forceinline__ float load1(const ClipChunk &c, int i) {
                : bf16lo(static_cast<const uint16_t *>(c.src)[i]);
 }
 
+// Squares of a vector's elements, into four sums.
+__device__ __forceinline__ void add_squares(uint4 w, int f32, float (&a)[4]) {
+  if (f32) {
+    const float x = __uint_as_float(w.x), y = __uint_as_float(w.y);
+    const float z = __uint_as_float(w.z), q = __uint_as_float(w.w);
+    a[0] = fmaf(x, x, a[0]);
+    a[1] = fmaf(y, y, a[1]);
+    a[2] = fmaf(z, z, a[2]);
+    a[3] = fmaf(q, q, a[3]);
+  } else {
+    float v[8];
+    unpack8(w, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k & 3] = fmaf(v[k], v[k], a[k & 3]);
+  }
+}
+// A vector's elements times coef.
+__device__ __forceinline__ uint4 scaled(uint4 w, int f32, float coef) {
+  if (coef == 1.0f) return w;
+  if (f32)
+    return make_uint4(__float_as_uint(__fmul_rn(__uint_as_float(w.x), coef)),
+                      __float_as_uint(__fmul_rn(__uint_as_float(w.y), coef)),
+                      __float_as_uint(__fmul_rn(__uint_as_float(w.z), coef)),
+                      __float_as_uint(__fmul_rn(__uint_as_float(w.w), coef)));
+  float v[8];
+  unpack8(w, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], coef);
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
 // Sum over the CTA's 512 threads, in a fixed order; thread 0 has the result.
 __device__ __forceinline__ float block_sum(float v) {
   __shared__ float red[kClipThreads / 32];
@@ -45,7 +77,7 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const ClipChunk *__restrict__ table,
+__global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const ClipChunk *__restrict__ table,
                                                                  int64_t chunks,
                                                                  float *__restrict__ partials) {
   pdl_wait_then_release();
@@ -56,22 +88,15 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const ClipChunk
     if (vec_ok(c)) {
       const uint4 *p = static_cast<const uint4 *>(c.src);
       const int per = c.f32 ? 4 : 8, nv = c.n / per;
-      for (int i = threadIdx.x; i < nv; i += kClipThreads) {
-        const uint4 w = p[i];
-        if (c.f32) {
-          const float x = __uint_as_float(w.x), y = __uint_as_float(w.y);
-          const float z = __uint_as_float(w.z), q = __uint_as_float(w.w);
-          a[0] = fmaf(x, x, a[0]);
-          a[1] = fmaf(y, y, a[1]);
-          a[2] = fmaf(z, z, a[2]);
-          a[3] = fmaf(q, q, a[3]);
-        } else {
-          float v[8];
-          unpack8(w, v);
+      int i = threadIdx.x;
+      for (; i + 3 * kClipThreads < nv; i += 4 * kClipThreads) {  // four loads in flight
+        uint4 w[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) a[k & 3] = fmaf(v[k], v[k], a[k & 3]);
-        }
+        for (int k = 0; k < 4; ++k) w[k] = p[i + k * kClipThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add_squares(w[k], c.f32, a);
       }
+      for (; i < nv; i += kClipThreads) add_squares(p[i], c.f32, a);
       done = nv * per;
     }
     for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {
@@ -102,7 +127,7 @@ __device__ __forceinline__ float norm_of(const float *partials, int n) {
   return norm;
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const ClipChunk *__restrict__ table,
+__global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const ClipChunk *__restrict__ table,
                                                                   int64_t chunks,
                                                                   const float *__restrict__ partials,
                                                                   int n_partials, float max_norm,
@@ -120,24 +145,15 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const ClipChun
       const uint4 *p = static_cast<const uint4 *>(c.src);
       uint4 *q = static_cast<uint4 *>(c.dst);
       const int per = c.f32 ? 4 : 8, nv = c.n / per;
-      for (int i = threadIdx.x; i < nv; i += kClipThreads) {
-        uint4 w = p[i];
-        if (coef == 1.0f) {
-        } else if (c.f32) {
-          w.x = __float_as_uint(__fmul_rn(__uint_as_float(w.x), coef));
-          w.y = __float_as_uint(__fmul_rn(__uint_as_float(w.y), coef));
-          w.z = __float_as_uint(__fmul_rn(__uint_as_float(w.z), coef));
-          w.w = __float_as_uint(__fmul_rn(__uint_as_float(w.w), coef));
-        } else {
-          float v[8];
-          unpack8(w, v);
+      int i = threadIdx.x;
+      for (; i + 3 * kClipThreads < nv; i += 4 * kClipThreads) {
+        uint4 w[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], coef);
-          w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                         pack_bf16x2(v[6], v[7]));
-        }
-        q[i] = w;
+        for (int k = 0; k < 4; ++k) w[k] = p[i + k * kClipThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[i + k * kClipThreads] = scaled(w[k], c.f32, coef);
       }
+      for (; i < nv; i += kClipThreads) q[i] = scaled(p[i], c.f32, coef);
       done = nv * per;
     }
     for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {

@@ -325,15 +325,21 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
           }
           if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) { ok = false; break; }
           ptx::tc_fence_after();
+          // 16 columns at a time, G then U; the next chunk's load is in flight
+          // while this one is promoted
+          uint32_t raw[2][16];
+          ptx::tmem_ld16(tl + ab * BN, raw[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {  // 16 columns at a time: G, then U
-            uint32_t raw[16];
-            ptx::tmem_ld16(tl + ab * BN + (c >> 2) * BF + 16 * (c & 3), raw);
-            ptx::tmem_ld_wait();
-            if (c == 7) release_acc(ab);
+          for (int c = 0; c < 8; ++c) {
+            ptx::tmem_ld_wait16(raw[c & 1]);
+            if (c < 7)
+              ptx::tmem_ld16(tl + ab * BN + ((c + 1) >> 2) * BF + 16 * ((c + 1) & 3), raw[(c + 1) & 1]);
+            else
+              release_acc(ab);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              acc[8 * c + j] = fma2(pk(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])),
+              acc[8 * c + j] = fma2(pk(__uint_as_float(raw[c & 1][2 * j]),
+                                       __uint_as_float(raw[c & 1][2 * j + 1])),
                                     c < 4 ? sg : su, acc[8 * c + j]);
           }
           ++nacc;
@@ -366,6 +372,227 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// ---------------------------------------------------------------- few tokens
+// Up to 64 tokens the weight is all the traffic that counts, so the operands
+// trade places: 128 weight rows are the M side of the MMAs (gate rows and up
+// rows as two accumulators) and NT = 16, 32 or 64 tokens the N side.  One CTA
+// streams 256 weight rows of one K range; a cluster of S CTAs shares a tile of
+// 128 outputs, splits K, and sums the S partials in rank order over
+// distributed shared memory (deterministic, one launch, no workspace).
+constexpr int kSmallThreads = 192;  // producer, MMA issuer, 4 epilogue warps
+constexpr int kSmallTokens = 64;
+constexpr int kSmallMaxStages = 6;
+constexpr int kSmallSmem = 112 * 1024;  // two CTAs per SM
+
+struct SmallCtl {
+  uint64_t full[kSmallMaxStages], empty[kSmallMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kSmallCtlBytes = (int)((sizeof(SmallCtl) + 127) / 128 * 128);
+
+struct SmallArgs {
+  int64_t N, F;
+  int kbs, kbs_cta, split, stages;
+  int ring_bytes;
+  const float *x_sinv, *w_sinv;
+  uint32_t idesc;
+  __nv_bfloat16 *H, *G, *U;  // G and U null: not kept
+};
+
+template <int SCALING, int ACT, int NT>
+__global__ void __launch_bounds__(kSmallThreads, 2)
+    gated_small_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmW, const SmallArgs a) {
+  constexpr bool kTensor = SCALING == FP8_SCALING_TENSOR;
+  constexpr int kStageBytes = 2 * BF * BK + NT * BK;
+  constexpr uint32_t kCols = 4 * NT;  // two buffers of G and U
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  SmallCtl *ctl = reinterpret_cast<SmallCtl *>(ring + a.ring_bytes);
+  float *xsc = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ctl) + kSmallCtlBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % a.split, f0 = (int)blockIdx.x / a.split * BF;
+  // K blocks rank, rank + split, ...: the cluster reads neighbouring 128-byte
+  // pieces of the same weight rows at the same time
+  const int nkb = (a.kbs - rank + a.split - 1) / a.split;
+  auto kx = [&](int i) { return (rank + a.split * i) * BK; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      ptx::mbar_init(&ctl->full[s], 1);
+      ptx::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ctl->acc_full[b], 1);
+      ptx::mbar_init(&ctl->acc_empty[b], 4);
+    }
+    ptx::mbar_init(&ctl->mma_done, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&ctl->tmem_base, kCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int *abort = &ctl->abort;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return pipe::wait_bar(bar, parity, abort, &g_gated_status);
+  };
+  float *red = reinterpret_cast<float *>(ring);  // [2][NT][128] partials, once the ring is idle
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int issued = 0;
+      for (; issued < nkb; ++issued) {
+        if (!wait(&ctl->empty[stage], phase ^ 1)) { ok = false; break; }
+        uint8_t *sw = ring + (size_t)stage * kStageBytes;
+        ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
+        ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(issued), f0);
+        ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(issued), (int)a.F + f0);
+        ptx::tma_load_2d(sw + 2 * BF * BK, &tmX, &ctl->full[stage], kx(issued), 0);
+        if (++stage == a.stages) { stage = 0; phase ^= 1; }
+      }
+      if (!ok)  // the last copies of each stage land before the CTA can exit
+        for (int i = max(0, issued - a.stages); i < issued; ++i)
+          pipe::drain_wait(&ctl->full[i % a.stages], (uint32_t)((i / a.stages) & 1), &g_gated_status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, nacc = 0;
+      for (int i = 0; i < nkb; ++i) {
+        const bool first = !kTensor || i == 0, last = !kTensor || i == nkb - 1;
+        if (first) {
+          if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) break;
+          ptx::tc_fence_after();
+        }
+        if (!wait(&ctl->full[stage], phase)) break;
+        ptx::tc_fence_after();
+        const uint32_t w_addr = ptx::smem_u32(ring + (size_t)stage * kStageBytes);
+        const uint64_t gdesc = ptx::smem_desc_sw128(w_addr);
+        const uint64_t udesc = ptx::smem_desc_sw128(w_addr + BF * BK);
+        const uint64_t xdesc = ptx::smem_desc_sw128(w_addr + 2 * BF * BK);
+        const uint32_t d = tmem + (nacc & 1) * 2 * NT;
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k) {
+          const uint32_t more = (!first || k > 0) ? 1u : 0u;
+          ptx::mma_f8f6f4(d, gdesc + 2 * k, xdesc + 2 * k, a.idesc, more);
+          ptx::mma_f8f6f4(d + NT, udesc + 2 * k, xdesc + 2 * k, a.idesc, more);
+        }
+        ptx::mma_commit(&ctl->empty[stage]);
+        if (last) {
+          ptx::mma_commit(&ctl->acc_full[nacc & 1]);
+          ++nacc;
+        }
+        if (++stage == a.stages) { stage = 0; phase ^= 1; }
+      }
+      ptx::mma_commit(&ctl->mma_done);
+      pipe::drain_wait(&ctl->mma_done, 0, &g_gated_status);
+    }
+  } else {
+    const int q = warp & 3, f = q * 32 + lane, et = (warp - 2) * 32 + lane;
+    float acc[2 * NT];  // G of this weight row for every token, then U
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) acc[n] = 0.0f;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    if constexpr (!kTensor) {
+      // token scales of this CTA's K blocks, [K block][token]; absent tokens: 0
+      for (int i = et; i < nkb * NT; i += 128) {
+        const int n = i / nkb, k = i % nkb;
+        xsc[k * NT + n] = n < a.N ? a.x_sinv[(int64_t)n * a.kbs + rank + a.split * k] : 0.0f;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    const int uses = kTensor ? 1 : nkb;  // split <= kbs: no rank is without a block
+    const float *wg = a.w_sinv + (int64_t)(f0 / BF) * a.kbs + rank;
+    const float *wu = wg + (a.F / BF) * a.kbs;
+    for (int i = 0; i < uses; ++i) {
+      const uint32_t ab = i & 1;
+      float gs = 1.0f, us = 1.0f;
+      if (!kTensor) { gs = wg[a.split * i]; us = wu[a.split * i]; }
+      if (!wait(&ctl->acc_full[ab], (i >> 1) & 1)) break;
+      ptx::tc_fence_after();
+      constexpr int kW = NT < 32 ? NT : 32;
+#pragma unroll
+      for (int c = 0; c < 2 * NT; c += kW) {
+        uint32_t raw[kW];
+        if constexpr (kW == 16) ptx::tmem_ld16(tl + ab * 2 * NT + c, raw);
+        else ptx::tmem_ld32(tl + ab * 2 * NT + c, raw);
+        ptx::tmem_ld_wait();
+        if (c + kW == 2 * NT) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
+        }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          if (kTensor)
+            acc[c + j] = __uint_as_float(raw[j]);
+          else
+            acc[c + j] = fmaf(__uint_as_float(raw[j]),
+                              __fmul_rn(xsc[i * NT + (c + j) % NT], c < NT ? gs : us), acc[c + j]);
+        }
+      }
+    }
+    // the ring is idle: every MMA that read it has completed
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) red[n * BF + f] = acc[n];
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  if (a.split > 1) ptx::cluster_sync();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
+  // token rank + split * i of the cluster's tokens, two columns per thread
+  const int pairs = BF / 2, sub = (int)threadIdx.x / pairs;  // 3 tokens at a time
+  const int f = 2 * ((int)threadIdx.x % pairs);
+  float s_tensor = 1.0f;
+  if (kTensor) s_tensor = __fmul_rn(a.x_sinv[0], a.w_sinv[0]);
+  for (int n = rank + a.split * sub; n < a.N; n += a.split * (kSmallThreads / pairs)) {
+    float2 g = make_float2(0.0f, 0.0f), u = g;
+    for (int r = 0; r < a.split; ++r) {
+      const uint32_t at = ptx::smem_u32(red + n * BF + f), au = at + NT * BF * 4;
+      const float2 x = a.split > 1 ? ptx::ld_shared_cluster_f2(ptx::mapa_shared(at, r))
+                                   : *reinterpret_cast<float2 *>(red + n * BF + f);
+      const float2 y = a.split > 1 ? ptx::ld_shared_cluster_f2(ptx::mapa_shared(au, r))
+                                   : *reinterpret_cast<float2 *>(red + (NT + n) * BF + f);
+      g.x += x.x;
+      g.y += x.y;
+      u.x += y.x;
+      u.y += y.y;
+    }
+    if (kTensor) {
+      g.x = __fmul_rn(g.x, s_tensor);
+      g.y = __fmul_rn(g.y, s_tensor);
+      u.x = __fmul_rn(u.x, s_tensor);
+      u.y = __fmul_rn(u.y, s_tensor);
+    }
+    if (f0 + f >= a.F) continue;
+    float a0, a1;
+    act2<ACT>(g.x, g.y, a0, a1);
+    const int64_t o = (int64_t)n * a.F + f0 + f;
+    *reinterpret_cast<uint32_t *>(a.H + o) = pack_bf16x2(__fmul_rn(a0, u.x), __fmul_rn(a1, u.y));
+    if (a.G) {
+      *reinterpret_cast<uint32_t *>(a.G + o) = pack_bf16x2(g.x, g.y);
+      *reinterpret_cast<uint32_t *>(a.U + o) = pack_bf16x2(u.x, u.y);
+    }
+  }
+  __syncwarp();
+  if (a.split > 1) ptx::cluster_sync();  // no CTA leaves while another reads its partials
 }
 
 // ---------------------------------------------------------------- backward
@@ -429,6 +656,7 @@ struct __align__(128) BSmem {
   uint32_t tile[2][128 * 32];  // FP8 bytes of dG and dU for the transposed layout
   float colred[16][2][128];    // per-warp column maxima
   float colsc[2][128];
+  float rowsc[2][128];         // row maxima, then row scales
   float red[16];
   float tscale;
   uint64_t full;
@@ -507,7 +735,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     __syncthreads();  // the buffers are read, and the last tile's transpose too
     prefetch(id + gridDim.x);
-    float rs[2][4];
+    // 0 * v is NaN exactly for an infinite or NaN v: selects the cast's fix-up
+    float nan_acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        nan_acc = fmaf(v[0][i][j], 0.0f, fmaf(v[1][i][j], 0.0f, nan_acc));
+    const bool special = isnan(nan_acc);
     if constexpr (BLOCK) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
@@ -522,53 +757,71 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
 #pragma unroll
           for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          float si;
-          scale_from_amax(m, kE5M2Max, rs[z][i], si);
-          const int64_t row = r0 + rr + 32 * i;
-          if (cg == 0 && row < p.N)
-            p.row_scale_inv[row * (2 * tiles_c) + z * tiles_c + tc] = si;
+          if (cg == 0) S.rowsc[z][rr + 32 * i] = m;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-        if (lane < 16)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) S.colred[warp][z][8 * cg + j] = cm[j];
+        if (lane < 16) {
+          float4 *dst = reinterpret_cast<float4 *>(&S.colred[warp][z][8 * cg]);
+          dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
+          dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
+        }
       }
       __syncthreads();
-      if (t < 256) {
-        const int z = t >> 7, c = t & 127;
-        float m = 0.0f;
+      {  // one scale per thread: rows of dG, rows of dU, columns of dG, columns of dU
+        const int z = (t >> 7) & 1, c = t & 127;
+        float m, s, si;
+        if (t < 256) {
+          m = S.rowsc[z][c];
+        } else {
+          m = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) m = fmaxf(m, S.colred[w][z][c]);
-        float s, si;
+          for (int w = 0; w < 16; ++w) m = fmaxf(m, S.colred[w][z][c]);
+        }
         scale_from_amax(m, kE5M2Max, s, si);
-        S.colsc[z][c] = s;
-        if (c < cols_here) p.col_scale_inv[(z * p.F + c0 + c) * tiles_r + tr] = si;
+        if (t < 256) {
+          S.rowsc[z][c] = s;
+          if (c < rows_here) p.row_scale_inv[(r0 + c) * (2 * tiles_c) + z * tiles_c + tc] = si;
+        } else {
+          S.colsc[z][c] = s;
+          if (c < cols_here) p.col_scale_inv[(z * p.F + c0 + c) * tiles_r + tr] = si;
+        }
       }
       __syncthreads();
     }
+    auto cast8 = [&](const float(&x)[8], const float(&s)[8]) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) upk(mul2(pk(x[j], x[j + 1]), pk(s[j], s[j + 1])), y[j], y[j + 1]);
+      uint2 q;
+      if (!special) {
+        q.x = cvt4_finite<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
+        q.y = cvt4_finite<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
+      } else {
+        q.x = cvt4<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
+        q.y = cvt4<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
+      }
+      return q;
+    };
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      float cs[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) cs[j] = BLOCK ? S.colsc[z][8 * cg + j] : ts;
+      float cs[8], rs[8];
+      if (BLOCK) {
+        const float4 *c4 = reinterpret_cast<const float4 *>(&S.colsc[z][8 * cg]);
+        const float4 x = c4[0], y = c4[1];
+        cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
+        cs[4] = y.x; cs[5] = y.y; cs[6] = y.z; cs[7] = y.w;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = rr + 32 * i;
-        const float s = BLOCK ? rs[z][i] : ts;
-        uint2 q;
-        q.x = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][0], s), __fmul_rn(v[z][i][1], s),
-                                    __fmul_rn(v[z][i][2], s), __fmul_rn(v[z][i][3], s));
-        q.y = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][4], s), __fmul_rn(v[z][i][5], s),
-                                    __fmul_rn(v[z][i][6], s), __fmul_rn(v[z][i][7], s));
+        const float s = BLOCK ? S.rowsc[z][r] : ts;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rs[j] = s;
+        uint2 q = cast8(v[z][i], rs);
         if (col_ok && r < rows_here)
           *reinterpret_cast<uint2 *>(p.row + (r0 + r) * F2 + z * p.F + c0 + 8 * cg) = q;
-        if (BLOCK) {
-          q.x = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][0], cs[0]), __fmul_rn(v[z][i][1], cs[1]),
-                                      __fmul_rn(v[z][i][2], cs[2]), __fmul_rn(v[z][i][3], cs[3]));
-          q.y = cvt4<FP8_FORMAT_E5M2>(__fmul_rn(v[z][i][4], cs[4]), __fmul_rn(v[z][i][5], cs[5]),
-                                      __fmul_rn(v[z][i][6], cs[6]), __fmul_rn(v[z][i][7], cs[7]));
-        }
+        if (BLOCK) q = cast8(v[z][i], cs);
         *reinterpret_cast<uint2 *>(&S.tile[z][r * 32 + ((2 * cg) ^ swz(r))]) = q;
       }
     }
@@ -632,6 +885,48 @@ cudaError_t launch_fwd_save(const CUtensorMap (&m)[5], const GatedArgs &g, bool 
   return save ? launch_fwd<SCALING, ACT, true>(m, g, st) : launch_fwd<SCALING, ACT, false>(m, g, st);
 }
 
+template <int SCALING, int ACT, int NT>
+cudaError_t launch_small(const uint8_t *xq, const uint8_t *wq, int64_t K, SmallArgs a,
+                         cudaStream_t st) {
+  CUtensorMap mx, mw;
+  if (!make_u8_map(&mx, xq, a.N, K, NT) || !make_u8_map(&mw, wq, 2 * a.F, K, BF))
+    return cudaErrorInvalidValue;
+  constexpr int kStageBytes = 2 * BF * BK + NT * BK;
+  const int scales = SCALING == FP8_SCALING_TENSOR ? 0 : a.kbs_cta * NT * 4;
+  const int fixed = 1024 + kSmallCtlBytes + scales;
+  a.stages = std::max(1, std::min({kSmallMaxStages, a.kbs_cta, (kSmallSmem - fixed) / kStageBytes}));
+  a.ring_bytes = std::max(a.stages * kStageBytes, 2 * NT * BF * 4);
+  a.idesc = ptx::idesc_f8f6f4(FP8_FORMAT_E4M3, FP8_FORMAT_E4M3, BM, NT);
+  auto kernel = gated_small_kernel<SCALING, ACT, NT>;
+  static bool done[64];
+  const cudaError_t e = opt_in_smem(kernel, kSmallSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.numAttrs = 1;
+  if (pdl_enabled()) {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attr;
+  cfg.gridDim = dim3((unsigned)((a.F + BF - 1) / BF * a.split));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = (size_t)(fixed + a.ring_bytes);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a);
+}
+template <int SCALING, int ACT>
+cudaError_t launch_small_nt(const uint8_t *xq, const uint8_t *wq, int64_t K, const SmallArgs &a,
+                            cudaStream_t st) {
+  if (a.N <= 16) return launch_small<SCALING, ACT, 16>(xq, wq, K, a, st);
+  if (a.N <= 32) return launch_small<SCALING, ACT, 32>(xq, wq, K, a, st);
+  return launch_small<SCALING, ACT, 64>(xq, wq, K, a, st);
+}
+
 template <bool BLOCK, int ACT>
 cudaError_t launch_cast(const CUtensorMap (&m)[3], const GatedBwd &p, cudaStream_t st) {
   static bool done[64];
@@ -651,6 +946,36 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
                              const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
                              int act, void *H, void *G, void *U, cudaStream_t st) {
   const bool save = G != nullptr;
+  const double bytes = (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F;
+  if (N <= kSmallTokens) {
+    SmallArgs a = {};
+    a.N = N;
+    a.F = F;
+    a.kbs = (int)((K + BK - 1) / BK);
+    // the smallest split of K that gives every SM a CTA
+    const int64_t tiles = (F + BF - 1) / BF;
+    a.split = 1;
+    while (a.split < 8 && a.split * 2 <= a.kbs && tiles * a.split < num_sms()) a.split *= 2;
+    a.kbs_cta = (a.kbs + a.split - 1) / a.split;
+    a.x_sinv = x_sinv;
+    a.w_sinv = w_sinv;
+    a.H = static_cast<__nv_bfloat16 *>(H);
+    a.G = static_cast<__nv_bfloat16 *>(G);
+    a.U = static_cast<__nv_bfloat16 *>(U);
+    // the token scales of a CTA's K range are kept in shared memory (K up to
+    // 8192 at any split, 65536 at the full one; wider ones take the other kernel)
+    if (a.kbs_cta <= 64 && tiles * a.split < (int64_t(1) << 31)) {
+      LaunchScope ls(block ? "gated_small_block" : "gated_small_tensor", st, bytes, 4.0 * N * K * F,
+                     N, F, K);
+      if (block)
+        return act == FP8_ACT_SILU
+                   ? launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_SILU>(xq, wq, K, a, st)
+                   : launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(xq, wq, K, a, st);
+      return act == FP8_ACT_SILU
+                 ? launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_SILU>(xq, wq, K, a, st)
+                 : launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_GELU>(xq, wq, K, a, st);
+    }
+  }
   CUtensorMap m[5];
   if (!make_u8_map(&m[0], xq, N, K, BM) || !make_u8_map(&m[1], wq, 2 * F, K, BF) ||
       !make_bf16_slab_map(&m[2], H, N, F))
@@ -673,7 +998,7 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
   // deep K: 16 token tiles share the weight tiles that L2 holds
   g.group_m = g.kbs >= 16 ? std::min(16, g.tiles_m) : 0;
   LaunchScope ls(block ? "gated_fwd_block" : "gated_fwd_tensor", st,
-                 (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F, 4.0 * N * K * F, N, F, K);
+                 bytes, 4.0 * N * K * F, N, F, K);
   if (block)
     return act == FP8_ACT_SILU ? launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_SILU>(m, g, save, st)
                                : launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(m, g, save, st);

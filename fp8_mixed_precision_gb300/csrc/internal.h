@@ -143,10 +143,10 @@ bool make_bf16_slab_map(CUtensorMap *m, void *base, int64_t rows, int64_t cols);
 constexpr int64_t kMaxNormCols = 16384;
 cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, int w_f32,
                                 int64_t rows, int64_t cols, float eps, void *r, float *rstd,
-                                void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
+                                float *rstd_lo, void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
                                 cudaStream_t st);
-cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const void *w, int w_f32,
-                                int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
+cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *rstd_lo,
+                                const void *w, int w_f32, int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
                                 float *col_scale_inv, cudaStream_t st);
 // partials: norm_bwd_ctas(rows, cols) x cols floats.
 int norm_bwd_ctas(int64_t rows, int64_t cols);

@@ -48,12 +48,52 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                     pack_bf16x2(v[6], v[7]));
 }
-// y = (r * rstd) * w, the one place where the forward pass forms it.
-__device__ __forceinline__ void norm8(uint4 r, float rstd, const float (&w)[8], float (&y)[8]) {
+// rstd is kept as a pair hi + lo (lo: what fp32 cannot hold of it), and
+// y = r * (hi + lo) * w is rounded once: t + e is r * rstd to about 2^-45, and
+// the last fma adds e * w to t * w exactly.  Both layouts then quantize the
+// correctly rounded fp32 y (all but about one in ten thousand), so their codes
+// are those of the exact norm and do not depend on the summation order.
+__device__ __forceinline__ void norm8(uint4 r, float hi, float lo, const float (&w)[8],
+                                      float (&y)[8]) {
+  using namespace gelu2;
   float v[8];
   unpack8(r, v);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(__fmul_rn(v[k], rstd), w[k]);
+  for (int k = 0; k < 8; k += 2) {
+    const uint64_t x = pk(v[k], v[k + 1]), ww = pk(w[k], w[k + 1]);
+    const uint64_t t = mul2(x, dup(hi));
+    const uint64_t e = fma2(x, dup(lo), fma2(x, dup(hi), mul2(t, dup(-1.0f))));
+    upk(fma2(t, ww, mul2(e, ww)), y[k], y[k + 1]);
+  }
+}
+// (a + b) as the rounded sum and its error.
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+  s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+}
+// 1 / sqrt((hi + lo) / C + eps) as a pair, from the hardware's approximate
+// reciprocal square root (relative error below 2^-22) and one Newton step with
+// its residual in full: what is left is below 2^-43.  inv_c: 1 / C as a pair.
+// A sum that is not finite gives the root's own value and lo = 0.
+__device__ __forceinline__ void rstd_pair(float hi, float lo, float C, float2 inv_c, float eps,
+                                          float &r, float &rlo) {
+  const float q = __fmul_rn(hi, inv_c.x);
+  const float qlo = fmaf(__fadd_rn(fmaf(-q, C, hi), lo), inv_c.x, 0.0f);
+  float m, mlo;
+  two_sum(q, eps, m, mlo);
+  mlo = __fadd_rn(mlo, qlo);
+  const float r0 = rsqrtf(m);
+  const float t = __fmul_rn(r0, r0), tlo = fmaf(r0, r0, -t);
+  const float e = fmaf(-mlo, t, fmaf(-m, tlo, fmaf(-m, t, 1.0f)));
+  // 1/sqrt(1 - e) = 1 + e/2 + 3/8 e^2 + ...
+  const float d = __fmul_rn(r0, __fmul_rn(e, fmaf(0.375f, e, 0.5f)));
+  r = __fadd_rn(r0, d);
+  rlo = __fadd_rn(__fsub_rn(r0, r), d);
+  if (!isfinite(rlo)) {
+    r = r0;
+    rlo = 0.0f;
+  }
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -61,13 +101,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Eight values -> eight E4M3 bytes; `special`: some value of the thread is
+// infinite or NaN, which selects the NaN fix-up.
+__device__ __forceinline__ uint2 cast8(const float (&v)[8], bool special) {
+  if (!special)
+    return make_uint2(cvt4_finite<FP8_FORMAT_E4M3>(v[0], v[1], v[2], v[3]),
+                      cvt4_finite<FP8_FORMAT_E4M3>(v[4], v[5], v[6], v[7]));
+  return make_uint2(cvt4<FP8_FORMAT_E4M3>(v[0], v[1], v[2], v[3]),
+                    cvt4<FP8_FORMAT_E4M3>(v[4], v[5], v[6], v[7]));
+}
+
+// v * s, two products per instruction
+__device__ __forceinline__ void scale8(const float (&v)[8], float s, float (&q)[8]) {
+  using namespace gelu2;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) upk(mul2(pk(v[k], v[k + 1]), dup(s)), q[k], q[k + 1]);
+}
+
 struct NormFwd {
   const uint4 *x, *res;  // bf16 [R, C]; res may be null
   NormW w;
   int64_t R, C;
   float eps;
+  float2 inv_c;  // 1 / C as a pair
   uint4 *r;      // bf16 [R, C]; written when res is given
-  float *rstd;   // [R] or null
+  float *rstd, *rstd_lo;  // [R] or null
   uint4 *y;      // bf16 [R, C] or null
   uint8_t *row;  // E4M3 [R, C] or null
   float *row_scale, *row_scale_inv;
@@ -88,83 +146,113 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
   const bool live = row < a.R;
   const int nv = (int)(a.C / 8);
   const int64_t base = row * nv;
-  uint4 rv[VPT];
-  float ss = 0.0f;
+  // vectors that hold columns of the row, whole warps at a time
+  const int vecs = min(VPT, (nv - wir * 32 + WPR * 32 - 1) / (WPR * 32));
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 rv[VPT], sv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = (j * WPR + wir) * 32 + lane;
-    rv[j] = make_uint4(0, 0, 0, 0);
-    if (live && v < nv) rv[j] = a.x[base + v];
+    const bool in = live && v < nv;
+    rv[j] = in ? __ldcs(a.x + base + v) : zero;
+    sv[j] = in && a.res ? __ldcs(a.res + base + v) : zero;
   }
-  if (a.res) {
-    uint4 sv[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = (j * WPR + wir) * 32 + lane;
-      sv[j] = make_uint4(0, 0, 0, 0);
-      if (live && v < nv) sv[j] = a.res[base + v];
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = (j * WPR + wir) * 32 + lane;
-      float p[8], q[8];
-      unpack8(rv[j], p);
-      unpack8(sv[j], q);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] += q[k];
-      rv[j] = pack8(p);
-      if (live && v < nv) a.r[base + v] = rv[j];
-    }
-  }
+  float ss = 0.0f, lo = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     float p[8];
     unpack8(rv[j], p);
+    if (a.res) {
+      float q[8];
+      unpack8(sv[j], q);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] += q[k];
+      rv[j] = pack8(p);
+      unpack8(rv[j], p);
+      const int v = (j * WPR + wir) * 32 + lane;
+      if (live && v < nv) a.r[base + v] = rv[j];
+    }
+    // bf16 squares have 16 bits, so a thread's few of them add up with next to
+    // no rounding; the last joins, whose roundings count, carry their errors along
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(p[k], p[k], ss);
   }
-  ss = warp_sum(ss);
-  if constexpr (WPR > 1) {
-    __shared__ float red[kWarps];
-    if (lane == 0) red[warp] = ss;
-    __syncthreads();
-    ss = 0.0f;
 #pragma unroll
-    for (int k = 0; k < WPR; ++k) ss += red[(warp / WPR) * WPR + k];
+  for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  {
+    float e;
+    two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, 8), ss, lo);
+    const float other_lo = __shfl_xor_sync(0xffffffffu, lo, 16);
+    two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, 16), ss, e);
+    lo = __fadd_rn(__fadd_rn(lo, other_lo), e);
+  }
+  if constexpr (WPR > 1) {
+    __shared__ float2 red[kWarps];
+    if (lane == 0) red[warp] = make_float2(ss, lo);
+    __syncthreads();
+    ss = lo = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) {
+      const float2 v = red[(warp / WPR) * WPR + k];
+      float e;
+      two_sum(ss, v.x, ss, e);
+      lo = __fadd_rn(__fadd_rn(lo, v.y), e);
+    }
   }
   if (!live) return;
-  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.C), a.eps));
-  if (a.rstd && wir == 0 && lane == 0) a.rstd[row] = rstd;
+  float rstd, rstd_lo;
+  rstd_pair(ss, lo, (float)a.C, a.inv_c, a.eps, rstd, rstd_lo);
+  if (wir == 0 && lane == 0) {
+    if (a.rstd) a.rstd[row] = rstd;
+    if (a.rstd_lo) a.rstd_lo[row] = rstd_lo;
+  }
   const int64_t nb = (a.C + 127) / 128;
+  float y[VPT][8], mx[VPT];
+  uint64_t nan_acc = 0;  // 0 * y is NaN exactly for an infinite or NaN y
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
+    if (j >= vecs) break;
     const int v = (j * WPR + wir) * 32 + lane;
     const bool in = v < nv;
-    if (__all_sync(0xffffffffu, !in)) break;
-    float w8[8] = {}, y[8];
+    float w8[8] = {};
     if (in) load_w8(a.w, (int64_t)v * 8, w8);
-    norm8(rv[j], rstd, w8, y);
-    if (a.y && in) a.y[base + v] = pack8(y);
-    if (a.row) {
-      float m = 0.0f;
+    norm8(rv[j], rstd, rstd_lo, w8, y[j]);
+    if (a.y && in) a.y[base + v] = pack8(y[j]);
+    mx[j] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = amax_acc(m, y[k]);
+    for (int k = 0; k < 8; ++k) mx[j] = amax_acc(mx[j], y[j][k]);
 #pragma unroll
-      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float s, si;
-      scale_from_amax(m, kE4M3Max, s, si);
-      if (in) {
-        uint2 q;
-        q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[0], s), __fmul_rn(y[1], s), __fmul_rn(y[2], s),
-                                    __fmul_rn(y[3], s));
-        q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[4], s), __fmul_rn(y[5], s), __fmul_rn(y[6], s),
-                                    __fmul_rn(y[7], s));
-        *reinterpret_cast<uint2 *>(a.row + row * a.C + (int64_t)v * 8) = q;
-        if ((lane & 15) == 0) {
-          a.row_scale[row * nb + v / 16] = s;
-          a.row_scale_inv[row * nb + v / 16] = si;
-        }
-      }
+    for (int k = 0; k < 8; k += 2)
+      nan_acc = gelu2::fma2(gelu2::pk(y[j][k], y[j][k + 1]), 0, nan_acc);
+  }
+  if (!a.row) return;
+  float n0, n1;
+  gelu2::upk(nan_acc, n0, n1);
+  const bool special = isnan(__fadd_rn(n0, n1));
+  // the block scales of the thread's vectors: lane j of each half warp divides
+  // for vector j, and the others take the result from it
+  float m = 0.0f, s, si;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if (j >= vecs) break;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+    if ((lane & 15) == j) m = mx[j];
+  }
+  scale_from_amax(m, kE4M3Max, s, si);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if (j >= vecs) break;
+    const int v = (j * WPR + wir) * 32 + lane;
+    const float sj = __shfl_sync(0xffffffffu, s, (lane & 16) + j);
+    if (v < nv) {
+      float q8[8];
+      scale8(y[j], sj, q8);
+      *reinterpret_cast<uint2 *>(a.row + row * a.C + (int64_t)v * 8) = cast8(q8, special);
+    }
+    if ((lane & 15) == j && v - j < nv) {  // v - j: the block's first vector
+      a.row_scale[row * nb + v / 16] = s;
+      a.row_scale_inv[row * nb + v / 16] = si;
     }
   }
 }
@@ -172,16 +260,18 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
 struct NormCols {
   NormW w;
   int64_t R, C, ldr;  // ldr: tokens per row of the transposed layout (R rounded up to 16)
-  const float *rstd;
+  const float *rstd, *rstd_lo;
   uint8_t *col;  // E4M3 [C, ldr]
   float *col_scale, *col_scale_inv;
 };
 
+constexpr int kColThreads = 256;
 struct __align__(128) CSmem {
   uint16_t in[2][128 * 128];
   uint32_t tile[128 * 32];
   float colred[8][128];
   float colsc[128];
+  float2 rs[128];
   uint64_t full[2];
 };
 
@@ -198,18 +288,21 @@ __device__ __forceinline__ void wait_tile(uint64_t *bar, uint32_t parity) {
     }
   }
 }
+// Word w of tile row r lives at word r*32 + (w ^ swz(r)): the transpose's lanes
+// (8 groups of 16 rows, 4 words) then fall on 32 different banks.
 __device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
 
 // Transposed copy: 128 tokens x 128 columns per iteration.  r comes back by
 // TMA, y is formed again from r, rstd and w, each column's maximum over its
 // 128 tokens gives its scale, and the bytes go through a swizzled tile so
-// that 16 tokens leave in one store.  Tokens past R are zeros.
-__global__ void __launch_bounds__(kNormThreads, 2)
+// that 16 tokens leave in one store.  Tokens past R are zeros.  Tiles run last
+// to first: the end of r is what L2 still holds after the row pass.
+__global__ void __launch_bounds__(kColThreads, 2)
     rmsnorm_cols_kernel(const __grid_constant__ CUtensorMap tmr, NormCols p) {
   extern __shared__ __align__(1024) uint8_t n_smem_raw[];
   CSmem &S = *reinterpret_cast<CSmem *>(n_smem_raw);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int cg = t & 15, rr = t >> 4;
+  const int cg = t & 15, rr = t >> 4;  // 8 columns, rows rr + 16 i
   const int64_t tiles_r = (p.R + 127) / 128, tiles_c = (p.C + 127) / 128;
   const int64_t ntiles = tiles_r * tiles_c;
   if (t == 0) {
@@ -222,7 +315,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   pdl_wait_then_release();
   auto prefetch = [&](int64_t id, int b) {
     if (t != 0 || id >= ntiles) return;
-    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    const int64_t tr = (ntiles - 1 - id) / tiles_c, tc = (ntiles - 1 - id) % tiles_c;
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive_expect_tx(&S.full[b], 128u * 128 * 2);
     ptx::tma_load_2d(S.in[b], &tmr, &S.full[b], (int)(tc * 128), (int)(tr * 128));
@@ -232,38 +325,47 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   prefetch(id + gridDim.x, 1);
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
     const int b = k & 1;
-    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    const int64_t tr = (ntiles - 1 - id) / tiles_c, tc = (ntiles - 1 - id) % tiles_c;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int rows_here = (int)(p.R - r0 < 128 ? p.R - r0 : 128);
     const int cols_here = (int)(p.C - c0 < 128 ? p.C - c0 : 128);
     float w8[8] = {};
     if (8 * cg < cols_here) load_w8(p.w, c0 + 8 * cg, w8);
-    float rs[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = rr + 16 * i;
-      rs[i] = r < rows_here ? p.rstd[r0 + r] : 0.0f;
+    if (t < 128) {
+      S.rs[t] = t < rows_here ? make_float2(p.rstd[r0 + t], p.rstd_lo[r0 + t]) : make_float2(0.0f, 0.0f);
     }
     wait_tile(&S.full[b], (k >> 1) & 1);
     __syncthreads();
-    uint4 xw[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      xw[i] = *reinterpret_cast<const uint4 *>(&S.in[b][(rr + 16 * i) * 128 + 8 * cg]);
-    float cm[8] = {};
+    float y[8][8];  // rows rr + 16 i; tokens past R: zeros
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float y[8];
-      norm8(xw[i], rs[i], w8, y);
-      if (rr + 16 * i < rows_here)
+      const int r = rr + 16 * i;
+      const float2 rs = S.rs[r];
+      norm8(*reinterpret_cast<const uint4 *>(&S.in[b][r * 128 + 8 * cg]), rs.x, rs.y, w8, y[i]);
+      if (r >= rows_here)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cm[j] = amax_acc(cm[j], y[j]);
+        for (int j = 0; j < 8; ++j) y[i][j] = 0.0f;
     }
+    float cm[8] = {};
+    uint64_t nan_acc = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        cm[j] = amax_acc(cm[j], y[i][j]);
+        cm[j + 1] = amax_acc(cm[j + 1], y[i][j + 1]);
+        nan_acc = gelu2::fma2(gelu2::pk(y[i][j], y[i][j + 1]), 0, nan_acc);
+      }
+    float n0, n1;
+    gelu2::upk(nan_acc, n0, n1);
+    const bool special = isnan(__fadd_rn(n0, n1));
 #pragma unroll
     for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-    if (lane < 16)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) S.colred[warp][8 * cg + j] = cm[j];
+    if (lane < 16) {
+      float4 *dst = reinterpret_cast<float4 *>(&S.colred[warp][8 * cg]);
+      dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
+      dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
+    }
     __syncthreads();
     prefetch(id + 2 * (int64_t)gridDim.x, b);  // every thread holds its elements
     if (t < 128) {
@@ -284,17 +386,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     for (int j = 0; j < 8; ++j) cs[j] = S.colsc[8 * cg + j];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      using namespace gelu2;
       const int r = rr + 16 * i;
-      float y[8];
-      norm8(xw[i], rs[i], w8, y);
-      uint2 q = make_uint2(0, 0);
-      if (r < rows_here) {
-        q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[0], cs[0]), __fmul_rn(y[1], cs[1]),
-                                    __fmul_rn(y[2], cs[2]), __fmul_rn(y[3], cs[3]));
-        q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(y[4], cs[4]), __fmul_rn(y[5], cs[5]),
-                                    __fmul_rn(y[6], cs[6]), __fmul_rn(y[7], cs[7]));
-      }
-      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = q;
+      float q8[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        upk(mul2(pk(y[i][j], y[i][j + 1]), pk(cs[j], cs[j + 1])), q8[j], q8[j + 1]);
+      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = cast8(q8, special);
     }
     __syncthreads();
     const int seg = t & 7, w = t >> 3;  // rows seg*16..+15, columns 4w..4w+3
@@ -337,7 +435,7 @@ struct NormBwd {
 // Backward: a group of WPR warps per row, rows in a grid-stride loop; each
 // thread keeps the dw sums of its own columns over all rows of its group.
 template <int VPT, int WPR>
-__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads, WPR > 8 ? 32 / WPR : WPR < 4 ? 2 : 4)
     rmsnorm_bwd_kernel(NormBwd a) {
   constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
   constexpr int kRows = kWarps / WPR;
@@ -432,24 +530,35 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
     }
 }
 
-// dw[c] = sum of the CTAs' partials in a fixed order: 32 columns x 8 parts of
-// the CTAs per block, the parts joined in order.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ partials, int n,
+// dw[c] = sum of the CTAs' partials in a fixed order: 16 columns (4 lanes of
+// four) x 128 parts of the CTAs per block, the parts joined in order.
+__global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float *__restrict__ partials, int n,
                                                          int64_t C, float *__restrict__ dw) {
   pdl_wait_then_release();
-  __shared__ float part[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < C)
-    for (int k = warp; k < n; k += 8) s += partials[(int64_t)k * C + c];
-  part[warp][lane] = s;
+  __shared__ float4 part[128][4];
+  const int quad = threadIdx.x & 3, k0 = threadIdx.x >> 2;
+  const int64_t c = (int64_t)blockIdx.x * 16 + quad * 4;  // C is a multiple of 16
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [](float4 &s, float4 v) {
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  };
+#pragma unroll 5
+  for (int k = k0; k < n; k += 128)
+    add(s, *reinterpret_cast<const float4 *>(partials + (int64_t)k * C + c));
+  part[k0][quad] = s;
   __syncthreads();
-  if (warp == 0 && c < C) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += part[k][lane];
-    dw[c] = s;
+  for (int d = 64; d; d >>= 1) {  // pairwise, in a fixed order
+    if (k0 < d) {
+      add(s, part[k0 + d][quad]);
+      part[k0][quad] = s;
+    }
+    __syncthreads();
   }
+  if (k0 == 0) *reinterpret_cast<float4 *>(dw + c) = s;
 }
 
 template <int VPT, int WPR>
@@ -484,16 +593,18 @@ int bwd_warps(int64_t C) {
 int norm_bwd_ctas(int64_t rows, int64_t cols) {
   const int wpr = bwd_warps(cols);
   const int64_t per_cta = wpr >= 8 ? 1 : 8 / wpr;
-  const int64_t most = wpr <= 8 ? 152 * 4 : wpr == 16 ? 152 * 2 : 152;
+  const int64_t most = 152 * (wpr < 4 ? 2 : wpr <= 8 ? 4 : wpr == 16 ? 2 : 1);  // one wave
   return (int)std::max<int64_t>(1, std::min<int64_t>((rows + per_cta - 1) / per_cta, most));
 }
 
 cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, int w_f32,
                                 int64_t rows, int64_t cols, float eps, void *r, float *rstd,
-                                void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
+                                float *rstd_lo, void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
                                 cudaStream_t st) {
+  const float inv = (float)(1.0 / (double)cols);
   NormFwd a{static_cast<const uint4 *>(x), static_cast<const uint4 *>(res), {w, w_f32}, rows, cols,
-            eps, static_cast<uint4 *>(r), rstd, static_cast<uint4 *>(y), row, row_scale,
+            eps, make_float2(inv, (float)(1.0 / (double)cols - (double)inv)),
+            static_cast<uint4 *>(r), rstd, rstd_lo, static_cast<uint4 *>(y), row, row_scale,
             row_scale_inv};
   const double n = (double)rows * cols;
   LaunchScope ls("rmsnorm_rows", st,
@@ -506,12 +617,12 @@ cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, i
   if (nv <= 128) return launch_rows<4, 1>(a, st);
   if (nv <= 256) return launch_rows<4, 2>(a, st);
   if (nv <= 512) return launch_rows<4, 4>(a, st);
-  if (nv <= 1024) return launch_rows<4, 8>(a, st);
-  return launch_rows<4, 16>(a, st);  // up to kMaxNormCols
+  if (nv <= 1024) return launch_rows<2, 16>(a, st);
+  return launch_rows<2, 32>(a, st);  // up to kMaxNormCols
 }
 
-cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const void *w, int w_f32,
-                                int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
+cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *rstd_lo,
+                                const void *w, int w_f32, int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
                                 float *col_scale_inv, cudaStream_t st) {
   CUtensorMap tm;
   if (!make_bf16_tile_map(&tm, r, rows, cols, 128, 128)) return cudaErrorInvalidValue;
@@ -524,13 +635,13 @@ cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const void *w,
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  NormCols p{{w, w_f32}, rows, cols, (rows + 15) / 16 * 16, rstd, col, col_scale, col_scale_inv};
+  NormCols p{{w, w_f32}, rows, cols, (rows + 15) / 16 * 16, rstd, rstd_lo, col, col_scale, col_scale_inv};
   const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
   const int64_t grid = std::min<int64_t>(tiles, (int64_t)num_sms() * 2);
   LaunchScope ls("rmsnorm_cols", st,
                  3.0 * rows * cols + 4.0 * rows + 8.0 * cols * ((rows + 127) / 128),
                  2.0 * rows * cols, rows, cols);
-  return launch_kernel(rmsnorm_cols_kernel, dim3((unsigned)grid), dim3(kNormThreads),
+  return launch_kernel(rmsnorm_cols_kernel, dim3((unsigned)grid), dim3(kColThreads),
                        sizeof(CSmem), st, tm, p);
 }
 
@@ -556,7 +667,7 @@ cudaError_t launch_rmsnorm_bwd(const void *dy, const void *dr, const void *r, co
     if (e != cudaSuccess) return e;
   }
   LaunchScope ls("rmsnorm_dw", st, 4.0 * grid * cols + 4.0 * cols, (double)grid * cols, grid, cols);
-  return launch_kernel(rmsnorm_dw_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st,
+  return launch_kernel(rmsnorm_dw_kernel, dim3((unsigned)(cols / 16)), dim3(512), 0, st,
                        (const float *)partials, grid, cols, dw);
 }
 

@@ -347,9 +347,9 @@ fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream
  * fp8_rmsnorm_fwd: the residual stream's addition, its root-mean-square norm
  * and the norm's FP8 output, for a bf16 [rows, cols] x:
  *   r = bf16(x + residual) (residual NULL: r = x), rstd = (mean(r^2) + eps)^-1/2,
- *   y = (r * rstd) * w in fp32; y is quantized as it is (E4M3, activation role
- *   of the block recipe, 1x128 blocks, scale rule as above) and/or rounded to
- *   bf16.  Squares and sums are fp32.
+ *   y = r * rstd * w; the fp32 y is quantized as it is (E4M3, activation role of
+ *   the block recipe, 1x128 blocks, scale rule as above) and/or rounded to bf16.
+ *   Sums and rstd are carried as pairs of fp32, so that y is rounded once.
  *   rows           any number of tokens; cols: a multiple of 16, at most 16384
  *   w              device bf16 or fp32 [cols], as w_dtype says
  *   eps            positive
@@ -357,6 +357,8 @@ fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream
  *                  May be x or residual itself (in place).
  *   rstd           device f32 [rows], or NULL; required with colwise_out and
  *                  for a backward pass
+ *   rstd_lo        device f32 [rows], or NULL; required with colwise_out: what
+ *                  fp32 cannot hold of rstd, for the pass that writes it
  *   y              device bf16 [rows, cols] or NULL
  *   rowwise_out    device u8 [rows, cols] or NULL, with row_scale,
  *                  row_scale_inv f32 [rows, ceil(cols/128)]
@@ -375,10 +377,10 @@ fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream
 typedef enum { FP8_DTYPE_BF16 = 0, FP8_DTYPE_F32 = 1 } fp8_dtype;
 
 fp8_status fp8_rmsnorm_fwd(const void *x, const void *residual, const void *w, fp8_dtype w_dtype,
-                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd, void *y,
-                           uint8_t *rowwise_out, uint8_t *colwise_out, float *row_scale,
-                           float *row_scale_inv, float *col_scale, float *col_scale_inv,
-                           fp8_stream_t stream);
+                           int64_t rows, int64_t cols, float eps, void *r_out, float *rstd,
+                           float *rstd_lo, void *y, uint8_t *rowwise_out, uint8_t *colwise_out,
+                           float *row_scale, float *row_scale_inv, float *col_scale,
+                           float *col_scale_inv, fp8_stream_t stream);
 fp8_status fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes);
 fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const float *rstd,
                            const void *w, fp8_dtype w_dtype, int64_t rows, int64_t cols, void *dx,

@@ -119,6 +119,11 @@ def test_tensorwise(fp, N, K, F, recipe, act):
     _check(fp, N, K, F, recipe, act)
 
 
+def test_few_tokens_over_a_very_deep_product(fp):
+    """More K blocks than the few-token kernel takes in one CTA."""
+    _check(fp, 3, 66048, 128, "block", "silu")
+
+
 @pytest.mark.parametrize("recipe", ["tensorwise", "block"])
 def test_several_waves(fp, recipe):
     """More output tiles than the GPU has SMs, so every ring and accumulator

@@ -18,7 +18,7 @@ def L():
 
 
 def _norm_args(**kw):
-    a = dict(x=A, res=A, w=A, dt=1, rows=5, cols=256, eps=1e-6, r=A, rstd=A, y=None, row=A, col=A, rs=A, rsi=A,
+    a = dict(x=A, res=A, w=A, dt=1, rows=5, cols=256, eps=1e-6, r=A, rstd=A, lo=A, y=None, row=A, col=A, rs=A, rsi=A,
              cs=A, csi=A, st=None)
     a.update(kw)
     return list(a.values())
@@ -27,7 +27,7 @@ def _norm_args(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), ARG), (dict(cols=250), SHAPE), (dict(cols=16400), UNSUPPORTED), (dict(dt=2), ARG),
     (dict(eps=0.0), ARG), (dict(eps=float("nan")), ARG), (dict(row=None, col=None), ARG), (dict(r=None), ARG),
-    (dict(res=None), ARG), (dict(rstd=None), ARG), (dict(rsi=None), ARG), (dict(csi=None), ARG), (dict(w=None), ARG),
+    (dict(res=None), ARG), (dict(rstd=None), ARG), (dict(lo=None), ARG), (dict(rsi=None), ARG), (dict(csi=None), ARG), (dict(w=None), ARG),
     (dict(x=ODD), ALIGN), (dict(w=ODD), ALIGN), (dict(row=ODD), ALIGN), (dict(rows=0), OK)])
 def test_norm_forward(L, kw, want):
     n = L.fp8_launch_count()
