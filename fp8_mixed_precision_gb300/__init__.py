@@ -23,7 +23,7 @@ __all__ = [
     "fp8_amax_partials", "fp8_linear_fwd_after_amax", "fp8_linear_bwd_after_amax",
     "ACTIVATION", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "rmsnorm_buffers", "rmsnorm_workspace",
     "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd", "GatedContext", "gated_context",
-    "gated_workspace", "fp8_gated_ctx_layout", "GradClip", "NormBuffers",
+    "gated_workspace", "gated_norm_columns", "fp8_gated_ctx_layout", "GradClip", "NormBuffers",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -667,6 +667,10 @@ class NormBuffers(dict):
         super().__setitem__(key, value)
         self.checked = None
 
+    def update(self, *args, **kw):
+        super().update(*args, **kw)
+        self.checked = None
+
     def check(self, R, C, wanted):
         """wanted: (r, rowwise, colwise, y) to be written for an [R, C] input."""
         nb, rb = -(-C // 128), -(-R // 128)
@@ -735,9 +739,10 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
     _check(lib().fp8_rmsnorm_fwd(
         x.data_ptr(), _ptr(residual), w.data_ptr(), _DTYPE[w.dtype], R, C, eps,
         _ptr(out["r"]) if residual is not None else None, out["rstd"].data_ptr(),
-        _ptr(out["rstd_lo"]) if colwise else None, _ptr(out["y"]) if bf16 else None, _ptr(out["row"]) if rowwise else None,
-        _ptr(out["col"]) if colwise else None, _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]),
-        _ptr(out["col_scale"]), _ptr(out["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
+        _ptr(out["rstd_lo"]) if colwise else None, _ptr(out["y"]) if bf16 else None,
+        _ptr(out["row"]) if rowwise else None, _ptr(out["col"]) if colwise else None,
+        _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]), _ptr(out["col_scale"]),
+        _ptr(out["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
     return out if residual is not None else dict(out, r=x)
 
 
@@ -801,6 +806,25 @@ def fp8_gated_ctx_layout(recipe: str, ctx: GatedContext):
     _check(lib().fp8_gated_ctx_layout(RECIPE[recipe], ctx.N, ctx.K, ctx.F, _ptr(ctx.ctx),
                                       *[ctypes.byref(q) for q in p]), "fp8_gated_ctx_layout")
     return tuple(p)
+
+
+def gated_norm_columns(recipe: str, ctx: GatedContext) -> dict:
+    """The transposed part of ctx as output buffers of fp8_rmsnorm_fwd (col,
+    col_scale, col_scale_inv; block recipe), so that a norm fills the context
+    that fp8_gated_fwd_quantized then uses."""
+    if recipe != "block":
+        raise ValueError("the norm's FP8 output is the block recipe's")
+    p = fp8_gated_ctx_layout(recipe, ctx)
+    base = ctx.ctx.data_ptr()
+    Np, rb = -(-ctx.N // 16) * 16, -(-ctx.N // 128)
+
+    def at(q, rows, cols, dtype, size):
+        off = q.value - base
+        return ctx.ctx[off:off + rows * cols * size].view(dtype).view(rows, cols)
+
+    return dict(col=at(p[0], ctx.K, Np, torch.uint8, 1),
+                col_scale=at(p[1], ctx.K, rb, torch.float32, 4),
+                col_scale_inv=at(p[2], ctx.K, rb, torch.float32, 4))
 
 
 def _gated_out(N, K, cache, h, recipe, y, ctx, train, device):

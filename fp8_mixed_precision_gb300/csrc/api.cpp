@@ -827,6 +827,19 @@ fp8_status gated_entry(fp8_weight_cache *cache, fp8_weight_handle h, int recipe,
   return FP8_OK;
 }
 
+// The forward kernel on quantized tokens.  own_input: the kernel before it on
+// the stream is this call's quantizer.
+fp8_status gated_fwd_on(const uint8_t *xq, const float *xsi, int64_t N,
+                        const fp8_weight_cache::Entry &e, int recipe, int act, void *H, void *ctx,
+                        bool own_input, fp8_stream_t stream) {
+  const int64_t F = e.O / 2;
+  const GatedCtx L = gated_ctx((fp8_recipe)recipe, N, e.K, F);
+  uint8_t *c = static_cast<uint8_t *>(ctx);
+  return from_cuda(launch_gated_fwd(xq, xsi, e.w_row, e.row_scale_inv, N, e.K, F,
+                                    recipe == FP8_RECIPE_BLOCK, act, H, c ? c + L.g : nullptr,
+                                    c ? c + L.u : nullptr, own_input, cs(stream)));
+}
+
 }  // namespace
 
 fp8_status fp8_gated_ctx_size(fp8_recipe recipe, int64_t N, int64_t K, int64_t F, size_t *bytes) {
@@ -873,12 +886,7 @@ fp8_status fp8_gated_fwd_quantized(const uint8_t *xq_row, const float *xq_row_sc
   if (N == 0) return FP8_OK;
   if (!xq_row || !xq_row_scale_inv || !H) return FP8_ERR_INVALID_ARG;
   if (!aligned16(xq_row) || !aligned16(H) || !aligned16(ctx)) return FP8_ERR_ALIGN;
-  const int64_t F = e->O / 2;
-  const GatedCtx L = gated_ctx(recipe, N, K, F);
-  uint8_t *c = static_cast<uint8_t *>(ctx);
-  return from_cuda(launch_gated_fwd(xq_row, xq_row_scale_inv, e->w_row, e->row_scale_inv, N, K, F,
-                                    recipe == FP8_RECIPE_BLOCK, act, H, c ? c + L.g : nullptr,
-                                    c ? c + L.u : nullptr, cs(stream)));
+  return gated_fwd_on(xq_row, xq_row_scale_inv, N, *e, recipe, act, H, ctx, false, stream);
 }
 
 fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *cache,
@@ -899,13 +907,17 @@ fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *
   float *cscale = nullptr, *cscale_inv = nullptr;
   void *g, *u;
   if (ctx) fp8_gated_ctx_layout(recipe, N, K, F, ctx, &col, &cscale, &cscale_inv, &g, &u);
-  st = from_cuda(launch_quantize(X, N, K, recipe == FP8_RECIPE_BLOCK ? 1 : 0, FP8_FORMAT_E4M3,
-                                 w + L.xq, col, reinterpret_cast<float *>(w + L.xs),
-                                 reinterpret_cast<float *>(w + L.xsi), cscale, cscale_inv,
-                                 reinterpret_cast<float *>(w + L.part), cs(stream)));
+  const bool block = recipe == FP8_RECIPE_BLOCK;
+  float *xsi = reinterpret_cast<float *>(w + L.xsi);
+  if (gated_quantizes_few(N, K, block))
+    st = from_cuda(launch_gated_quantize_few(X, N, K, block, w + L.xq, col, xsi, cscale_inv,
+                                             cs(stream)));
+  else
+    st = from_cuda(launch_quantize(X, N, K, block ? 1 : 0, FP8_FORMAT_E4M3, w + L.xq, col,
+                                   reinterpret_cast<float *>(w + L.xs), xsi, cscale, cscale_inv,
+                                   reinterpret_cast<float *>(w + L.part), cs(stream)));
   if (st != FP8_OK) return st;
-  return fp8_gated_fwd_quantized(w + L.xq, reinterpret_cast<float *>(w + L.xsi), N, K, cache, h,
-                                 recipe, act, H, ctx, stream);
+  return gated_fwd_on(w + L.xq, xsi, N, *e, recipe, act, H, ctx, true, stream);
 }
 
 fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
@@ -965,10 +977,11 @@ fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_g
     elements += (double)d.n;
     bytes += (double)d.n * (double)size;
   }
-  // Chunk: a power of two between 2048 and 32768 elements, so that small sets
-  // still spread over the GPU's CTAs and large ones have few chunks.
-  int64_t chunk = 2048;
-  while (chunk < 32768 && elements / (double)chunk > 4096.0) chunk *= 2;
+  // Chunk: two for each of the 2 x 152 CTAs that fill the GPU, within 2048 to
+  // 32768 elements, so that small sets still spread over the CTAs and large
+  // ones take many short turns.
+  const int64_t chunk = std::min<int64_t>(
+      32768, std::max<int64_t>(2048, ((int64_t)(elements / 608.0) + 2047) / 2048 * 2048));
   try {
     auto p = std::make_unique<fp8_grad_clip>();
     p->elements = elements;

@@ -77,30 +77,49 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-__global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const ClipChunk *__restrict__ table,
-                                                                 int64_t chunks,
-                                                                 float *__restrict__ partials) {
+// The first kAhead vectors per thread of a chunk, requested before they are
+// needed (a chunk off the 16-byte grid has none).
+constexpr int kAhead = 8;
+__device__ __forceinline__ int vectors_of(const ClipChunk &c) {
+  return vec_ok(c) ? c.n / (c.f32 ? 4 : 8) : 0;
+}
+__device__ __forceinline__ void request(const ClipChunk &c, int nv, uint4 (&w)[kAhead]) {
+  const uint4 *p = static_cast<const uint4 *>(c.src);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = threadIdx.x + k * kClipThreads;
+    w[k] = i < nv ? p[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+__global__ void __launch_bounds__(kClipThreads, 2) clip_norm_kernel(const ClipChunk *__restrict__ table,
+                                                                    int64_t chunks,
+                                                                    float *__restrict__ partials) {
   pdl_wait_then_release();
   float a[4] = {};
-  for (int64_t id = blockIdx.x; id < chunks; id += gridDim.x) {
-    const ClipChunk c = table[id];
-    int done = 0;
-    if (vec_ok(c)) {
-      const uint4 *p = static_cast<const uint4 *>(c.src);
-      const int per = c.f32 ? 4 : 8, nv = c.n / per;
-      int i = threadIdx.x;
-      for (; i + 3 * kClipThreads < nv; i += 4 * kClipThreads) {  // four loads in flight
-        uint4 w[4];
+  int64_t id = blockIdx.x;
+  ClipChunk c = {};
+  if (id < chunks) c = table[id];
+  while (id < chunks) {
+    const int nv = vectors_of(c);
+    uint4 w[kAhead];
+    request(c, nv, w);
+    const ClipChunk now = c;
+    id += gridDim.x;
+    if (id < chunks) c = table[id];  // arrives while this chunk is worked on
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = p[i + k * kClipThreads];
+    for (int k = 0; k < kAhead; ++k) add_squares(w[k], now.f32, a);
+    const uint4 *p = static_cast<const uint4 *>(now.src);
+    int i = threadIdx.x + kAhead * kClipThreads;
+    for (; i + (kAhead - 1) * kClipThreads < nv; i += kAhead * kClipThreads) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add_squares(w[k], c.f32, a);
-      }
-      for (; i < nv; i += kClipThreads) add_squares(p[i], c.f32, a);
-      done = nv * per;
+      for (int k = 0; k < kAhead; ++k) w[k] = p[i + k * kClipThreads];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) add_squares(w[k], now.f32, a);
     }
-    for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {
-      const float v = load1(c, i);
+    for (; i < nv; i += kClipThreads) add_squares(p[i], now.f32, a);
+    for (int e = nv * (now.f32 ? 4 : 8) + threadIdx.x; e < now.n; e += kClipThreads) {
+      const float v = load1(now, e);
       a[0] = fmaf(v, v, a[0]);
     }
   }
@@ -127,50 +146,60 @@ __device__ __forceinline__ float norm_of(const float *partials, int n) {
   return norm;
 }
 
-__global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const ClipChunk *__restrict__ table,
+__global__ void __launch_bounds__(kClipThreads, 2) clip_scale_kernel(const ClipChunk *__restrict__ table,
                                                                   int64_t chunks,
                                                                   const float *__restrict__ partials,
                                                                   int n_partials, float max_norm,
                                                                   float *__restrict__ norm_out) {
   pdl_wait_then_release();
+  // last chunk first: what the first pass read last may still be in L2; the
+  // first vectors are on their way while the norm is formed
+  int64_t id = blockIdx.x;
+  ClipChunk c = {};
+  uint4 w[kAhead];
+  if (id < chunks) c = table[chunks - 1 - id];
+  request(c, vectors_of(c), w);
   const float norm = norm_of(partials, n_partials);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float coef = isfinite(norm) ? fminf(1.0f, __fdiv_rn(max_norm, norm + 1e-6f)) : 1.0f;
-  // last chunk first: what the first pass read last may still be in L2
-  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const ClipChunk c = table[chunks - 1 - k];
-    if (c.dst == c.src && coef == 1.0f) continue;  // in place and nothing to change
-    int done = 0;
-    if (vec_ok(c)) {
-      const uint4 *p = static_cast<const uint4 *>(c.src);
-      uint4 *q = static_cast<uint4 *>(c.dst);
-      const int per = c.f32 ? 4 : 8, nv = c.n / per;
-      int i = threadIdx.x;
-      for (; i + 3 * kClipThreads < nv; i += 4 * kClipThreads) {
-        uint4 w[4];
+  while (id < chunks) {
+    const int nv = vectors_of(c);
+    const ClipChunk now = c;
+    id += gridDim.x;
+    if (id < chunks) c = table[chunks - 1 - id];
+    if (now.dst != now.src || coef != 1.0f) {  // in place, a factor of 1 changes nothing
+      const uint4 *p = static_cast<const uint4 *>(now.src);
+      uint4 *q = static_cast<uint4 *>(now.dst);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = p[i + k * kClipThreads];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q[i + k * kClipThreads] = scaled(w[k], c.f32, coef);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = threadIdx.x + k * kClipThreads;
+        if (i < nv) q[i] = scaled(w[k], now.f32, coef);
       }
-      for (; i < nv; i += kClipThreads) q[i] = scaled(p[i], c.f32, coef);
-      done = nv * per;
+      int i = threadIdx.x + kAhead * kClipThreads;
+      for (; i + (kAhead - 1) * kClipThreads < nv; i += kAhead * kClipThreads) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) w[k] = p[i + k * kClipThreads];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) q[i + k * kClipThreads] = scaled(w[k], now.f32, coef);
+      }
+      for (; i < nv; i += kClipThreads) q[i] = scaled(p[i], now.f32, coef);
+      for (int e = nv * (now.f32 ? 4 : 8) + threadIdx.x; e < now.n; e += kClipThreads) {
+        const float v = load1(now, e);
+        if (now.f32)
+          static_cast<float *>(now.dst)[e] = coef == 1.0f ? v : __fmul_rn(v, coef);
+        else
+          static_cast<__nv_bfloat16 *>(now.dst)[e] =
+              __float2bfloat16_rn(coef == 1.0f ? v : __fmul_rn(v, coef));
+      }
     }
-    for (int i = done + threadIdx.x; i < c.n; i += kClipThreads) {
-      const float v = load1(c, i);
-      if (c.f32)
-        static_cast<float *>(c.dst)[i] = coef == 1.0f ? v : __fmul_rn(v, coef);
-      else
-        static_cast<__nv_bfloat16 *>(c.dst)[i] =
-            __float2bfloat16_rn(coef == 1.0f ? v : __fmul_rn(v, coef));
-    }
+    if (id < chunks) request(c, vectors_of(c), w);
   }
 }
 
 }  // namespace
 
 int clip_ctas(int64_t chunks) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)num_sms() * 4));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)num_sms() * 2));
 }
 
 cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,

@@ -381,10 +381,11 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
 // streams 256 weight rows of one K range; a cluster of S CTAs shares a tile of
 // 128 outputs, splits K, and sums the S partials in rank order over
 // distributed shared memory (deterministic, one launch, no workspace).
-constexpr int kSmallThreads = 192;  // producer, MMA issuer, 4 epilogue warps
-constexpr int kSmallTokens = 64;
+constexpr int kSmallEpi = 8;  // epilogue warps: 4 for G, 4 for U
+constexpr int kSmallThreads = 32 * (2 + kSmallEpi);  // producer, MMA issuer, epilogue
+constexpr int kSmallTokens = 64;  // per CTA
 constexpr int kSmallMaxStages = 6;
-constexpr int kSmallSmem = 112 * 1024;  // two CTAs per SM
+constexpr int kSmallSmem = 200 * 1024;  // one CTA per SM, room for the quantizer's beside it
 
 struct SmallCtl {
   uint64_t full[kSmallMaxStages], empty[kSmallMaxStages];
@@ -402,10 +403,11 @@ struct SmallArgs {
   const float *x_sinv, *w_sinv;
   uint32_t idesc;
   __nv_bfloat16 *H, *G, *U;  // G and U null: not kept
+  int early;  // the weight may be read before the wait (see launch_gated_fwd)
 };
 
 template <int SCALING, int ACT, int NT>
-__global__ void __launch_bounds__(kSmallThreads, 2)
+__global__ void __launch_bounds__(kSmallThreads, 1)
     gated_small_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW, const SmallArgs a) {
   constexpr bool kTensor = SCALING == FP8_SCALING_TENSOR;
@@ -417,6 +419,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   float *xsc = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ctl) + kSmallCtlBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % a.split, f0 = (int)blockIdx.x / a.split * BF;
+  const int n0 = (int)blockIdx.y * NT;                      // first token
+  const int tokens = (int)min((int64_t)NT, a.N - n0);       // of this CTA
   // K blocks rank, rank + split, ...: the cluster reads neighbouring 128-byte
   // pieces of the same weight rows at the same time
   const int nkb = (a.kbs - rank + a.split - 1) / a.split;
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->acc_full[b], 1);
-      ptx::mbar_init(&ctl->acc_empty[b], 4);
+      ptx::mbar_init(&ctl->acc_empty[b], kSmallEpi);
     }
     ptx::mbar_init(&ctl->mma_done, 1);
     ctl->abort = 0;
@@ -439,6 +443,18 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     ptx::tmem_alloc(&ctl->tmem_base, kCols);
     ptx::tmem_relinquish();
   }
+  // The first stages' weight tiles: requested before the wait when the kernel
+  // before this one only makes the tokens (they are then on their way while
+  // it runs: a token at K 4096, F 14336 takes 21 us a pass instead of 24).
+  const int ahead = a.early ? min(a.stages, nkb) : 0;
+  auto load_weight = [&](int i, int stage) {
+    uint8_t *sw = ring + (size_t)stage * kStageBytes;
+    ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
+    ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(i), f0);
+    ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(i), (int)a.F + f0);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < ahead; ++i) load_weight(i, i);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -458,11 +474,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       int issued = 0;
       for (; issued < nkb; ++issued) {
         if (!wait(&ctl->empty[stage], phase ^ 1)) { ok = false; break; }
-        uint8_t *sw = ring + (size_t)stage * kStageBytes;
-        ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
-        ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(issued), f0);
-        ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(issued), (int)a.F + f0);
-        ptx::tma_load_2d(sw + 2 * BF * BK, &tmX, &ctl->full[stage], kx(issued), 0);
+        if (issued >= ahead) load_weight(issued, stage);
+        ptx::tma_load_2d(ring + (size_t)stage * kStageBytes + 2 * BF * BK, &tmX, &ctl->full[stage],
+                         kx(issued), n0);
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
       }
       if (!ok)  // the last copies of each stage land before the CTA can exit
@@ -504,52 +518,53 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
   } else {
     const int q = warp & 3, f = q * 32 + lane, et = (warp - 2) * 32 + lane;
-    float acc[2 * NT];  // G of this weight row for every token, then U
+    const int z = (warp - 2) >> 2;  // 0: G, 1: U
+    uint64_t acc[NT / 2];           // of this weight row for every token, in pairs
 #pragma unroll
-    for (int n = 0; n < 2 * NT; ++n) acc[n] = 0.0f;
-    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    for (int n = 0; n < NT / 2; ++n) acc[n] = 0;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(z * NT);
     if constexpr (!kTensor) {
       // token scales of this CTA's K blocks, [K block][token]; absent tokens: 0
-      for (int i = et; i < nkb * NT; i += 128) {
+      for (int i = et; i < nkb * NT; i += 32 * kSmallEpi) {
         const int n = i / nkb, k = i % nkb;
-        xsc[k * NT + n] = n < a.N ? a.x_sinv[(int64_t)n * a.kbs + rank + a.split * k] : 0.0f;
+        xsc[k * NT + n] =
+            n < tokens ? a.x_sinv[(int64_t)(n0 + n) * a.kbs + rank + a.split * k] : 0.0f;
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmallEpi) : "memory");
     }
     const int uses = kTensor ? 1 : nkb;  // split <= kbs: no rank is without a block
-    const float *wg = a.w_sinv + (int64_t)(f0 / BF) * a.kbs + rank;
-    const float *wu = wg + (a.F / BF) * a.kbs;
+    const float *wsc = a.w_sinv + (f0 / BF + z * (a.F / BF)) * a.kbs + rank;
     for (int i = 0; i < uses; ++i) {
       const uint32_t ab = i & 1;
-      float gs = 1.0f, us = 1.0f;
-      if (!kTensor) { gs = wg[a.split * i]; us = wu[a.split * i]; }
+      const uint64_t ws = kTensor ? 0 : dup(wsc[a.split * i]);
       if (!wait(&ctl->acc_full[ab], (i >> 1) & 1)) break;
       ptx::tc_fence_after();
-      constexpr int kW = NT < 32 ? NT : 32;
 #pragma unroll
-      for (int c = 0; c < 2 * NT; c += kW) {
-        uint32_t raw[kW];
-        if constexpr (kW == 16) ptx::tmem_ld16(tl + ab * 2 * NT + c, raw);
-        else ptx::tmem_ld32(tl + ab * 2 * NT + c, raw);
-        ptx::tmem_ld_wait();
-        if (c + kW == 2 * NT) {
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t raw[16];
+        ptx::tmem_ld16(tl + ab * 2 * NT + c, raw);
+        ptx::tmem_ld_wait16(raw);
+        if (c + 16 == NT) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
         }
 #pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          if (kTensor)
-            acc[c + j] = __uint_as_float(raw[j]);
-          else
-            acc[c + j] = fmaf(__uint_as_float(raw[j]),
-                              __fmul_rn(xsc[i * NT + (c + j) % NT], c < NT ? gs : us), acc[c + j]);
+        for (int j = 0; j < 16; j += 2) {
+          const uint64_t v = pk(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]));
+          uint64_t &o = acc[(c + j) / 2];
+          o = kTensor ? v : fma2(v, mul2(*reinterpret_cast<const uint64_t *>(xsc + i * NT + c + j), ws), o);
         }
       }
     }
     // the ring is idle: every MMA that read it has completed
 #pragma unroll
-    for (int n = 0; n < 2 * NT; ++n) red[n * BF + f] = acc[n];
+    for (int n = 0; n < NT; n += 2) {
+      float v0, v1;
+      upk(acc[n / 2], v0, v1);
+      red[(z * NT + n) * BF + f] = v0;
+      red[(z * NT + n + 1) * BF + f] = v1;
+    }
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -558,22 +573,34 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
   // token rank + split * i of the cluster's tokens, two columns per thread
-  const int pairs = BF / 2, sub = (int)threadIdx.x / pairs;  // 3 tokens at a time
+  const int pairs = BF / 2, sub = (int)threadIdx.x / pairs;  // 5 tokens at a time
   const int f = 2 * ((int)threadIdx.x % pairs);
   float s_tensor = 1.0f;
   if (kTensor) s_tensor = __fmul_rn(a.x_sinv[0], a.w_sinv[0]);
-  for (int n = rank + a.split * sub; n < a.N; n += a.split * (kSmallThreads / pairs)) {
-    float2 g = make_float2(0.0f, 0.0f), u = g;
-    for (int r = 0; r < a.split; ++r) {
-      const uint32_t at = ptx::smem_u32(red + n * BF + f), au = at + NT * BF * 4;
-      const float2 x = a.split > 1 ? ptx::ld_shared_cluster_f2(ptx::mapa_shared(at, r))
-                                   : *reinterpret_cast<float2 *>(red + n * BF + f);
-      const float2 y = a.split > 1 ? ptx::ld_shared_cluster_f2(ptx::mapa_shared(au, r))
-                                   : *reinterpret_cast<float2 *>(red + (NT + n) * BF + f);
-      g.x += x.x;
-      g.y += x.y;
-      u.x += y.x;
-      u.y += y.y;
+  for (int n = rank + a.split * sub; n < tokens; n += a.split * (kSmallThreads / pairs)) {
+    // every rank's partials are requested before the first is added
+    float2 x[8], y[8];
+    const uint32_t at = ptx::smem_u32(red + n * BF + f), au = at + NT * BF * 4;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      x[r] = y[r] = make_float2(0.0f, 0.0f);
+      if (r < a.split) {
+        if (a.split > 1) {
+          x[r] = ptx::ld_shared_cluster_f2(ptx::mapa_shared(at, r));
+          y[r] = ptx::ld_shared_cluster_f2(ptx::mapa_shared(au, r));
+        } else {
+          x[r] = *reinterpret_cast<float2 *>(red + n * BF + f);
+          y[r] = *reinterpret_cast<float2 *>(red + (NT + n) * BF + f);
+        }
+      }
+    }
+    float2 g = x[0], u = y[0];
+#pragma unroll
+    for (int r = 1; r < 8; ++r) {
+      g.x += x[r].x;
+      g.y += x[r].y;
+      u.x += y[r].x;
+      u.y += y[r].y;
     }
     if (kTensor) {
       g.x = __fmul_rn(g.x, s_tensor);
@@ -584,7 +611,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     if (f0 + f >= a.F) continue;
     float a0, a1;
     act2<ACT>(g.x, g.y, a0, a1);
-    const int64_t o = (int64_t)n * a.F + f0 + f;
+    const int64_t o = (int64_t)(n0 + n) * a.F + f0 + f;
     *reinterpret_cast<uint32_t *>(a.H + o) = pack_bf16x2(__fmul_rn(a0, u.x), __fmul_rn(a1, u.y));
     if (a.G) {
       *reinterpret_cast<uint32_t *>(a.G + o) = pack_bf16x2(g.x, g.y);
@@ -593,6 +620,124 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   }
   __syncwarp();
   if (a.split > 1) ptx::cluster_sync();  // no CTA leaves while another reads its partials
+}
+
+// Quantizer for few tokens: one CTA per 128 columns holds them for every token
+// in registers.  Tensor scaling needs the whole tensor's maximum first, which
+// every CTA takes for itself (at most kFewElements, from L2): one launch
+// instead of two.
+constexpr int kFewThreads = 256;
+constexpr int64_t kFewElements = 131072;
+constexpr int kFewRows = kSmallTokens / 16;  // tokens per thread
+
+template <bool BLOCK>
+__global__ void __launch_bounds__(kFewThreads)
+    gated_quant_few_kernel(const uint4 *__restrict__ x, int N, int64_t K, uint8_t *__restrict__ row,
+                           uint8_t *__restrict__ col, float *__restrict__ row_scale_inv,
+                           float *__restrict__ col_scale_inv) {
+  __shared__ float red[8];
+  __shared__ float colmx[16][128];
+  __shared__ float colsc[128];
+  __shared__ __align__(16) uint8_t tile[128][kSmallTokens + 16];
+  pdl_wait_then_release();
+  const int t = threadIdx.x, lane = t & 31, cg = t & 15, rr = t >> 4;
+  const int64_t c0 = (int64_t)blockIdx.x * 128, k8 = K / 8;
+  const int cols_here = (int)min((int64_t)128, K - c0);
+  const bool col_ok = 8 * cg < cols_here;
+  uint4 xw[kFewRows];  // tokens rr + 16 i, columns 8 cg ..
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i) {
+    const int n = rr + 16 * i;
+    xw[i] = n < N && col_ok ? x[n * k8 + c0 / 8 + cg] : make_uint4(0, 0, 0, 0);
+  }
+  auto value = [&](int i, int j) {
+    const uint32_t w[4] = {xw[i].x, xw[i].y, xw[i].z, xw[i].w};
+    return j & 1 ? bf16hi(w[j >> 1]) : bf16lo(w[j >> 1]);
+  };
+  float ts = 1.0f;
+  if (!BLOCK) {
+    float m = 0.0f;
+    for (int64_t i = t; i < N * k8; i += kFewThreads) {
+      const uint4 v = x[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = amax_acc(amax_acc(m, bf16lo(w[k])), bf16hi(w[k]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[t >> 5] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
+    float si;
+    scale_from_amax(m, kE4M3Max, ts, si);
+    if (blockIdx.x == 0 && t == 0) {
+      row_scale_inv[0] = si;
+      if (col) col_scale_inv[0] = si;
+    }
+  }
+  float cm[8] = {};
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i) {
+    const int n = rr + 16 * i;
+    float s = ts, m = 0.0f, v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = value(i, j);
+      m = amax_acc(m, v[j]);
+      cm[j] = amax_acc(cm[j], v[j]);
+    }
+    if (BLOCK) {
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float si;
+      scale_from_amax(m, kE4M3Max, s, si);
+      if (cg == 0 && n < N) row_scale_inv[(int64_t)n * gridDim.x + blockIdx.x] = si;
+    }
+    uint2 q;
+    q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(v[0], s), __fmul_rn(v[1], s), __fmul_rn(v[2], s),
+                                __fmul_rn(v[3], s));
+    q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(v[4], s), __fmul_rn(v[5], s), __fmul_rn(v[6], s),
+                                __fmul_rn(v[7], s));
+    if (n < N && col_ok) *reinterpret_cast<uint2 *>(row + n * K + c0 + 8 * cg) = q;
+    if (!BLOCK && col) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        tile[8 * cg + j][n] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+  }
+  if (!col) return;
+  if (BLOCK) {  // each column's own scale over the tokens (one 1x128 block)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) colmx[rr][8 * cg + j] = cm[j];
+    __syncthreads();
+    if (t < 128) {
+      float m = 0.0f, s, si;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) m = fmaxf(m, colmx[k][t]);
+      scale_from_amax(m, kE4M3Max, s, si);
+      colsc[t] = s;
+      if (t < cols_here) col_scale_inv[c0 + t] = si;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t q = cvt2<FP8_FORMAT_E4M3>(__fmul_rn(value(i, j), colsc[8 * cg + j]),
+                                                 __fmul_rn(value(i, j + 1), colsc[8 * cg + j + 1]));
+        tile[8 * cg + j][rr + 16 * i] = (uint8_t)q;
+        tile[8 * cg + j + 1][rr + 16 * i] = (uint8_t)(q >> 8);
+      }
+  }
+  __syncthreads();
+  const int Np = (N + 15) / 16 * 16;  // tokens past N: zeros
+  for (int i = t; i < cols_here * (Np / 16); i += kFewThreads) {
+    const int c = i / (Np / 16), seg = i % (Np / 16);
+    *reinterpret_cast<uint4 *>(col + (c0 + c) * Np + 16 * seg) =
+        *reinterpret_cast<const uint4 *>(&tile[c][16 * seg]);
+  }
 }
 
 // ---------------------------------------------------------------- backward
@@ -913,7 +1058,7 @@ cudaError_t launch_small(const uint8_t *xq, const uint8_t *wq, int64_t K, SmallA
     cfg.numAttrs = 2;
   }
   cfg.attrs = attr;
-  cfg.gridDim = dim3((unsigned)((a.F + BF - 1) / BF * a.split));
+  cfg.gridDim = dim3((unsigned)((a.F + BF - 1) / BF * a.split), (unsigned)((a.N + NT - 1) / NT));
   cfg.blockDim = dim3(kSmallThreads);
   cfg.dynamicSmemBytes = (size_t)(fixed + a.ring_bytes);
   cfg.stream = st;
@@ -944,24 +1089,33 @@ cudaError_t launch_cast(const CUtensorMap (&m)[3], const GatedBwd &p, cudaStream
 
 cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
                              const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
-                             int act, void *H, void *G, void *U, cudaStream_t st) {
+                             int act, void *H, void *G, void *U, bool own_input, cudaStream_t st) {
   const bool save = G != nullptr;
   const double bytes = (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F;
-  if (N <= kSmallTokens) {
+  const int64_t tiles = (F + BF - 1) / BF;
+  // Few tokens; or a deep product whose 128 x 128 tiles would fill less than
+  // half the SMs: chunks of 64 tokens and the split of K put more of them to
+  // work, the weight coming from L2 for all chunks but the first (us a pass,
+  // here / 128-token tiles: 100 tokens, K 4096, F 256: 11.5 / 19.4; 1000, 4096,
+  // 512: 19.6 / 21.4; below K = 3072 the tiles win, 256, 1024, 2048: 12.1 / 10.0)
+  if (N <= kSmallTokens || ((N + BM - 1) / BM * tiles * 2 <= num_sms() && K >= 24 * BK)) {
     SmallArgs a = {};
     a.N = N;
     a.F = F;
     a.kbs = (int)((K + BK - 1) / BK);
-    // the smallest split of K that gives every SM a CTA
-    const int64_t tiles = (F + BF - 1) / BF;
+    // the largest split of K that still gives every CTA an SM of its own (a
+    // deep ring each; two CTAs per SM with half of it: 10 tokens at K 4096,
+    // F 4096 take 11.7 us a pass, here 9.8)
+    const int64_t chunks = (N + kSmallTokens - 1) / kSmallTokens;
     a.split = 1;
-    while (a.split < 8 && a.split * 2 <= a.kbs && tiles * a.split < num_sms()) a.split *= 2;
+    while (a.split < 8 && a.split * 2 <= a.kbs && tiles * chunks * a.split * 2 <= num_sms()) a.split *= 2;
     a.kbs_cta = (a.kbs + a.split - 1) / a.split;
     a.x_sinv = x_sinv;
     a.w_sinv = w_sinv;
     a.H = static_cast<__nv_bfloat16 *>(H);
     a.G = static_cast<__nv_bfloat16 *>(G);
     a.U = static_cast<__nv_bfloat16 *>(U);
+    a.early = own_input;
     // the token scales of a CTA's K range are kept in shared memory (K up to
     // 8192 at any split, 65536 at the full one; wider ones take the other kernel)
     if (a.kbs_cta <= 64 && tiles * a.split < (int64_t(1) << 31)) {
@@ -1004,6 +1158,21 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
                                : launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(m, g, save, st);
   return act == FP8_ACT_SILU ? launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_SILU>(m, g, save, st)
                              : launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_GELU>(m, g, save, st);
+}
+
+bool gated_quantizes_few(int64_t N, int64_t K, bool block) {
+  return N <= kSmallTokens && (block || N * K <= kFewElements);
+}
+
+cudaError_t launch_gated_quantize_few(const void *x, int64_t N, int64_t K, bool block, uint8_t *row,
+                                      uint8_t *col, float *row_scale_inv, float *col_scale_inv,
+                                      cudaStream_t st) {
+  LaunchScope ls(block ? "gated_quant_few_block" : "gated_quant_few_tensor", st,
+                 (col ? 4.0 : 3.0) * N * K, 0.0, N, K);
+  auto kernel = block ? gated_quant_few_kernel<true> : gated_quant_few_kernel<false>;
+  return launch_kernel(kernel, dim3((unsigned)((K + 127) / 128)), dim3(kFewThreads), 0, st,
+                       static_cast<const uint4 *>(x), (int)N, K, row, col, row_scale_inv,
+                       col_scale_inv);
 }
 
 cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void *U, int64_t N,

@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "pipe.cuh"
 #include "ptx.cuh"
 
 namespace fp8lin {
@@ -51,8 +52,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // rstd is kept as a pair hi + lo (lo: what fp32 cannot hold of it), and
 // y = r * (hi + lo) * w is rounded once: t + e is r * rstd to about 2^-45, and
 // the last fma adds e * w to t * w exactly.  Both layouts then quantize the
-// correctly rounded fp32 y (all but about one in ten thousand), so their codes
-// are those of the exact norm and do not depend on the summation order.
+// correctly rounded fp32 y (all but about one in a hundred, which are the
+// other neighbour of a near tie), so their codes are those of the exact norm
+// but for a handful in 10^8 and do not depend on the summation order.
 __device__ __forceinline__ void norm8(uint4 r, float hi, float lo, const float (&w)[8],
                                       float (&y)[8]) {
   using namespace gelu2;
@@ -131,32 +133,18 @@ struct NormFwd {
   float *row_scale, *row_scale_inv;
 };
 
-// Rows: a group of WPR warps holds one row in registers (VPT vectors of 8
-// elements per thread), so x and the residual are read once and everything
-// that the row alone determines is written from there.
-template <int VPT, int WPR>
-__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
-    rmsnorm_rows_kernel(NormFwd a) {
-  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
-  constexpr int kRows = kWarps / WPR;  // rows per CTA
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wir = warp % WPR;
-  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
-  const bool live = row < a.R;
+// One row, held by WPR warps (VPT vectors of 8 elements per thread) as rv (x)
+// and sv (the residual): everything that the row alone determines is written
+// from these registers.  `sync` joins the row's warps; `red` is theirs.
+template <int VPT, int WPR, typename Sync>
+__device__ __forceinline__ void norm_row(const NormFwd &a, int64_t row, bool live, int wir,
+                                         uint4 (&rv)[VPT], const uint4 (&sv)[VPT], float2 *red,
+                                         Sync sync) {
+  const int lane = threadIdx.x & 31;
   const int nv = (int)(a.C / 8);
   const int64_t base = row * nv;
   // vectors that hold columns of the row, whole warps at a time
   const int vecs = min(VPT, (nv - wir * 32 + WPR * 32 - 1) / (WPR * 32));
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 rv[VPT], sv[VPT];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int v = (j * WPR + wir) * 32 + lane;
-    const bool in = live && v < nv;
-    rv[j] = in ? __ldcs(a.x + base + v) : zero;
-    sv[j] = in && a.res ? __ldcs(a.res + base + v) : zero;
-  }
   float ss = 0.0f, lo = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -172,31 +160,33 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
       const int v = (j * WPR + wir) * 32 + lane;
       if (live && v < nv) a.r[base + v] = rv[j];
     }
-    // bf16 squares have 16 bits, so a thread's few of them add up with next to
-    // no rounding; the last joins, whose roundings count, carry their errors along
+    // bf16 squares have 16 bits, so four of them add up with next to no
+    // rounding; every join of such sums carries its error along
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(p[k], p[k], ss);
+    for (int h = 0; h < 8; h += 4) {
+      float e;
+      const float q = fmaf(p[h + 3], p[h + 3],
+                           fmaf(p[h + 2], p[h + 2], fmaf(p[h + 1], p[h + 1], __fmul_rn(p[h], p[h]))));
+      two_sum(ss, q, ss, e);
+      lo = __fadd_rn(lo, e);
+    }
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  {
+  for (int o = 16; o; o >>= 1) {
     float e;
-    two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, 8), ss, lo);
-    const float other_lo = __shfl_xor_sync(0xffffffffu, lo, 16);
-    two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, 16), ss, e);
+    const float other_lo = __shfl_xor_sync(0xffffffffu, lo, o);
+    two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, o), ss, e);
     lo = __fadd_rn(__fadd_rn(lo, other_lo), e);
   }
   if constexpr (WPR > 1) {
-    __shared__ float2 red[kWarps];
-    if (lane == 0) red[warp] = make_float2(ss, lo);
-    __syncthreads();
+    if (lane == 0) red[wir] = make_float2(ss, lo);
+    sync();
     ss = lo = 0.0f;
 #pragma unroll
     for (int k = 0; k < WPR; ++k) {
-      const float2 v = red[(warp / WPR) * WPR + k];
       float e;
-      two_sum(ss, v.x, ss, e);
-      lo = __fadd_rn(__fadd_rn(lo, v.y), e);
+      two_sum(ss, red[k].x, ss, e);
+      lo = __fadd_rn(__fadd_rn(lo, red[k].y), e);
     }
   }
   if (!live) return;
@@ -255,6 +245,32 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
       a.row_scale_inv[row * nb + v / 16] = si;
     }
   }
+}
+
+// Each row's warps load it themselves; many small CTAs per SM hide the latency
+// of the row sum.  (131072 x 512: 81 us; fed by the ring of the backward pass,
+// with 18 warps per SM, 111 us.)
+template <int VPT, int WPR>
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
+    rmsnorm_rows_kernel(NormFwd a) {
+  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
+  constexpr int kRows = kWarps / WPR;  // rows per CTA
+  __shared__ float2 red[kWarps];
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wir = warp % WPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
+  const bool live = row < a.R;
+  const int nv = (int)(a.C / 8);
+  uint4 rv[VPT], sv[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = (j * WPR + wir) * 32 + lane;
+    const bool in = live && v < nv;
+    rv[j] = in ? a.x[row * nv + v] : make_uint4(0, 0, 0, 0);
+    sv[j] = in && a.res ? a.res[row * nv + v] : make_uint4(0, 0, 0, 0);
+  }
+  norm_row<VPT, WPR>(a, row, live, wir, rv, sv, red + warp / WPR * WPR, [] { __syncthreads(); });
 }
 
 struct NormCols {
@@ -432,97 +448,167 @@ struct NormBwd {
   float *partials;  // [gridDim.x, C] sums of this CTA's rows
 };
 
-// Backward: a group of WPR warps per row, rows in a grid-stride loop; each
-// thread keeps the dw sums of its own columns over all rows of its group.
+// One producer thread per CTA streams whole groups of rows (contiguous in
+// memory) of the three inputs into a shared-memory ring with bulk copies, so
+// the bytes in flight do not depend on how far the warps have come.
+constexpr int kRingStages = 8;
+struct RingCtl {
+  uint64_t full[kRingStages], empty[kRingStages];
+  int abort;
+};
+constexpr int kRingCtlBytes = (int)((sizeof(RingCtl) + 127) / 128 * 128);
+
+// Warps per CTA that work on rows, for WPR warps per row; the producer is one more.
+constexpr int ring_warps(int wpr) { return wpr > 8 ? wpr : 8; }
+
+// The producer's loop: stages of `group` rows (row_bytes each) of the tensors
+// in[0 .. NIN - 1] (null ones are skipped).
+template <int NIN>
+__device__ __forceinline__ void ring_produce(RingCtl *ctl, uint8_t *ring, int stages, int group,
+                                             int64_t R, int64_t row_bytes,
+                                             const void *const (&in)[NIN]) {
+  volatile int *abort = &ctl->abort;
+  int issued = 0;
+  bool ok = true;
+  for (int64_t row0 = (int64_t)blockIdx.x * group; row0 < R; row0 += (int64_t)gridDim.x * group) {
+    const int s = issued % stages;
+    if (!pipe::wait_bar(&ctl->empty[s], ((issued / stages) & 1) ^ 1, abort, &g_norm_status)) {
+      ok = false;
+      break;
+    }
+    const int64_t rows = R - row0 < group ? R - row0 : group;
+    const uint32_t bytes = (uint32_t)(rows * row_bytes);
+    uint32_t all = 0;
+#pragma unroll
+    for (int k = 0; k < NIN; ++k) all += in[k] ? bytes : 0;
+    ptx::mbar_arrive_expect_tx(&ctl->full[s], all);
+    uint8_t *dst = ring + (int64_t)s * NIN * group * row_bytes;
+#pragma unroll
+    for (int k = 0; k < NIN; ++k)
+      if (in[k])
+        ptx::bulk_load(dst + k * group * row_bytes,
+                       static_cast<const uint8_t *>(in[k]) + row0 * row_bytes, bytes, &ctl->full[s]);
+    ++issued;
+  }
+  if (!ok)  // the copies in flight land before the CTA can exit
+    for (int i = max(0, issued - stages); i < issued; ++i)
+      pipe::drain_wait(&ctl->full[i % stages], (uint32_t)((i / stages) & 1), &g_norm_status);
+}
+__device__ __forceinline__ void ring_init(RingCtl *ctl, int stages, int warps) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&ctl->full[s], 1);
+      ptx::mbar_init(&ctl->empty[s], warps);
+    }
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+}
+// Joins the WPR warps of group grp (whole CTA rows: barrier 1 + grp).
+template <int WPR>
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * WPR) : "memory");
+}
+
+// Backward: a group of WPR warps per row, fed by the ring; each thread keeps
+// the dw sums of its own columns over all rows of its group.  A row is read
+// from shared memory twice (for c, then for dx) instead of being held.
 template <int VPT, int WPR>
-__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads, WPR > 8 ? 32 / WPR : WPR < 4 ? 2 : 4)
-    rmsnorm_bwd_kernel(NormBwd a) {
-  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
-  constexpr int kRows = kWarps / WPR;
+__global__ void __launch_bounds__(32 * (ring_warps(WPR) + 1), WPR > 8 ? 1 : 3)
+    rmsnorm_bwd_kernel(NormBwd a, int stages) {
+  constexpr int kWarps = ring_warps(WPR), kGroup = kWarps / WPR;
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  RingCtl *ctl = reinterpret_cast<RingCtl *>(ring_smem);
+  uint8_t *ring = ring_smem + kRingCtlBytes;
   __shared__ float red[2][kWarps];
-  extern __shared__ float dwsum[];  // kRows > 1: [kRows - 1][C] sums of the other groups
+  ring_init(ctl, stages, kWarps);
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row_bytes = a.C * 2;
   const int wir = warp % WPR, grp = warp / WPR;
   const int nv = (int)(a.C / 8);
   float dw[VPT][8] = {};
-  const float inv_c = __fdiv_rn(1.0f, (float)a.C);
-  int buf = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.R;
-       row0 += (int64_t)gridDim.x * kRows) {
-    const int64_t row = row0 + grp;
-    const bool live = row < a.R;
-    const int64_t base = row * nv;
-    uint4 dyv[VPT], rv[VPT], drv[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = (j * WPR + wir) * 32 + lane;
-      const bool in = live && v < nv;
-      dyv[j] = rv[j] = drv[j] = make_uint4(0, 0, 0, 0);
-      if (in) dyv[j] = a.dy[base + v];
-      if (in) rv[j] = a.r[base + v];
-      if (in && a.dr) drv[j] = a.dr[base + v];
-    }
-    const float rstd = live ? a.rstd[row] : 0.0f;
-    float c = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = (j * WPR + wir) * 32 + lane;
-      float w8[8] = {}, d[8], r[8];
-      if (v < nv) load_w8(a.w, (int64_t)v * 8, w8);
-      unpack8(dyv[j], d);
-      unpack8(rv[j], r);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        c = fmaf(d[k] * w8[k], r[k], c);
-        dw[j][k] = fmaf(d[k] * r[k], rstd, dw[j][k]);
-      }
-    }
-    c = warp_sum(c);
-    if constexpr (WPR > 1) {
-      if (lane == 0) red[buf][warp] = c;
-      __syncthreads();
-      c = 0.0f;
-#pragma unroll
-      for (int k = 0; k < WPR; ++k) c += red[buf][grp * WPR + k];
-      buf ^= 1;  // the other half next time: one barrier per row
-    }
-    const float c3 = c * inv_c * rstd * rstd * rstd;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = (j * WPR + wir) * 32 + lane;
-      if (live && v < nv) {
-        float w8[8], d[8], r[8], e[8];
-        load_w8(a.w, (int64_t)v * 8, w8);
-        unpack8(dyv[j], d);
-        unpack8(rv[j], r);
-        unpack8(drv[j], e);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = fmaf(-r[k], c3, fmaf(d[k] * w8[k], rstd, e[k]));
-        a.dx[base + v] = pack8(e);
-      }
-    }
-  }
-  // this CTA's column sums: the groups in order
-  if constexpr (kRows > 1) {
-    if (grp > 0)
+  if (warp == kWarps) {
+    const void *const in[3] = {a.dy, a.r, a.dr};
+    if (lane == 0) ring_produce<3>(ctl, ring, stages, kGroup, a.R, row_bytes, in);
+  } else {
+    const float inv_c = __fdiv_rn(1.0f, (float)a.C);
+    int it = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * kGroup; row0 < a.R;
+         row0 += (int64_t)gridDim.x * kGroup, ++it) {
+      const int s = it % stages;
+      const int64_t row = row0 + grp;
+      const bool live = row < a.R;
+      const float rstd = live ? a.rstd[row] : 0.0f;
+      pipe::wait_bar(&ctl->full[s], (it / stages) & 1, &ctl->abort, &g_norm_status);
+      const uint4 *pd = reinterpret_cast<const uint4 *>(ring + (int64_t)s * 3 * kGroup * row_bytes +
+                                                        grp * row_bytes);
+      const uint4 *pr = pd + kGroup * nv, *pe = pr + kGroup * nv;
+      float c = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int v = (j * WPR + wir) * 32 + lane;
-        if (v < nv)
+        if (live && v < nv) {
+          float w8[8], d[8], r[8];
+          load_w8(a.w, (int64_t)v * 8, w8);
+          unpack8(pd[v], d);
+          unpack8(pr[v], r);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dwsum[(int64_t)(grp - 1) * a.C + v * 8 + k] = dw[j][k];
+          for (int k = 0; k < 8; ++k) {
+            const float dr = d[k] * r[k];
+            c = fmaf(dr, w8[k], c);
+            dw[j][k] = fmaf(dr, rstd, dw[j][k]);
+          }
+        }
       }
-    __syncthreads();
+      c = warp_sum(c);
+      if constexpr (WPR > 1) {
+        if (lane == 0) red[it & 1][warp] = c;
+        group_sync<WPR>(grp);
+        c = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WPR; ++k) c += red[it & 1][grp * WPR + k];
+      }
+      const float c3 = c * inv_c * rstd * rstd * rstd;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = (j * WPR + wir) * 32 + lane;
+        if (live && v < nv) {
+          float w8[8], d[8], r[8], e[8] = {};
+          load_w8(a.w, (int64_t)v * 8, w8);
+          unpack8(pd[v], d);
+          unpack8(pr[v], r);
+          if (a.dr) unpack8(pe[v], e);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = fmaf(-r[k], c3, fmaf(d[k] * w8[k], rstd, e[k]));
+          a.dx[row * nv + v] = pack8(e);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->empty[s]);
+    }
   }
+  // this CTA's column sums: the groups in order, through the idle ring
+  float *sums = reinterpret_cast<float *>(ring);  // [kGroup - 1][C]
+  __syncthreads();
+  if (kGroup > 1 && warp < kWarps && grp > 0)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = (j * WPR + wir) * 32 + lane;
+      if (v < nv)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums[(int64_t)(grp - 1) * a.C + v * 8 + k] = dw[j][k];
+    }
+  __syncthreads();
   if (grp == 0)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = (j * WPR + wir) * 32 + lane;
       if (v < nv) {
-        for (int g = 1; g < kRows; ++g)
+        for (int g = 1; g < kGroup; ++g)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dw[j][k] += dwsum[(int64_t)(g - 1) * a.C + v * 8 + k];
+          for (int k = 0; k < 8; ++k) dw[j][k] += sums[(int64_t)(g - 1) * a.C + v * 8 + k];
         float4 *dst = reinterpret_cast<float4 *>(a.partials + (int64_t)blockIdx.x * a.C + v * 8);
         dst[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
         dst[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
@@ -561,6 +647,33 @@ __global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float *__restrict
   if (k0 == 0) *reinterpret_cast<float4 *>(dw + c) = s;
 }
 
+// Warps per row at VPT vectors per thread: a power of two that covers C.
+int bwd_vpt(int64_t C) { return C > 8192 ? 4 : 2; }
+int row_warps(int64_t C, int vpt) {
+  int wpr = 1;
+  while ((int64_t)wpr * 256 * vpt < C) wpr *= 2;
+  return wpr;
+}
+
+template <typename Kernel>
+cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+// Shared memory of a ring kernel's CTA: three CTAs per SM, one with 16 warps a row.
+template <int WPR>
+constexpr int kRingSmem = WPR > 8 ? 208 * 1024 : 72 * 1024;
+// Stages that fit, for groups of `group` rows of `tensors` tensors.
+int ring_stages(int smem, int group, int64_t C, int tensors) {
+  return (int)std::min<int64_t>(kRingStages, (smem - kRingCtlBytes) / (group * C * 2 * tensors));
+}
+
 template <int VPT, int WPR>
 cudaError_t launch_rows(const NormFwd &a, cudaStream_t st) {
   constexpr int kThreads = WPR > 8 ? 32 * WPR : kNormThreads;
@@ -571,36 +684,29 @@ cudaError_t launch_rows(const NormFwd &a, cudaStream_t st) {
 
 template <int VPT, int WPR>
 cudaError_t launch_bwd(NormBwd a, int grid, cudaStream_t st) {
-  constexpr int kThreads = WPR > 8 ? 32 * WPR : kNormThreads;
-  constexpr int kRows = kThreads / 32 / WPR;
-  const size_t smem = (size_t)(kRows - 1) * a.C * 4;
-  return launch_kernel(rmsnorm_bwd_kernel<VPT, WPR>, dim3((unsigned)grid), dim3(kThreads), smem, st,
-                       a);
-}
-
-// Warps per row of the backward pass for C columns, at two vectors (16
-// elements) per thread: 32 warps hold kMaxNormCols columns.
-int bwd_warps(int64_t C) {
-  int wpr = 1;
-  while ((int64_t)wpr * 512 < C) wpr *= 2;
-  return wpr;
+  constexpr int kWarps = ring_warps(WPR);
+  static bool done[64];
+  const cudaError_t e = opt_in_smem(rmsnorm_bwd_kernel<VPT, WPR>, kRingSmem<WPR>, done);
+  if (e != cudaSuccess) return e;
+  const int stages = ring_stages(kRingSmem<WPR>, kWarps / WPR, a.C, 3);
+  return launch_kernel(rmsnorm_bwd_kernel<VPT, WPR>, dim3((unsigned)grid), dim3(32 * (kWarps + 1)),
+                       kRingSmem<WPR>, st, a, stages);
 }
 
 }  // namespace
 
-// CTAs of the backward pass: a function of the shape alone, so that the order
-// of the dw sums is too.
+// CTAs of the backward pass (one wave): a function of the shape alone, so that
+// the order of the dw sums is too.
 int norm_bwd_ctas(int64_t rows, int64_t cols) {
-  const int wpr = bwd_warps(cols);
-  const int64_t per_cta = wpr >= 8 ? 1 : 8 / wpr;
-  const int64_t most = 152 * (wpr < 4 ? 2 : wpr <= 8 ? 4 : wpr == 16 ? 2 : 1);  // one wave
-  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + per_cta - 1) / per_cta, most));
+  const int wpr = row_warps(cols, bwd_vpt(cols));
+  const int64_t group = ring_warps(wpr) / wpr, most = wpr > 8 ? 152 : 456;
+  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + group - 1) / group, most));
 }
 
 cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, int w_f32,
                                 int64_t rows, int64_t cols, float eps, void *r, float *rstd,
-                                float *rstd_lo, void *y, uint8_t *row, float *row_scale, float *row_scale_inv,
-                                cudaStream_t st) {
+                                float *rstd_lo, void *y, uint8_t *row, float *row_scale,
+                                float *row_scale_inv, cudaStream_t st) {
   const float inv = (float)(1.0 / (double)cols);
   NormFwd a{static_cast<const uint4 *>(x), static_cast<const uint4 *>(res), {w, w_f32}, rows, cols,
             eps, make_float2(inv, (float)(1.0 / (double)cols - (double)inv)),
@@ -611,14 +717,15 @@ cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, i
                  n * (2 + (res ? 4 : 0) + (y ? 2 : 0) + (row ? 1 : 0)) +
                      rows * 8.0 * ((cols + 127) / 128),
                  4 * n, rows, cols);
-  const int64_t nv = cols / 8;
-  if (nv <= 32) return launch_rows<1, 1>(a, st);
-  if (nv <= 64) return launch_rows<2, 1>(a, st);
-  if (nv <= 128) return launch_rows<4, 1>(a, st);
-  if (nv <= 256) return launch_rows<4, 2>(a, st);
-  if (nv <= 512) return launch_rows<4, 4>(a, st);
-  if (nv <= 1024) return launch_rows<2, 16>(a, st);
-  return launch_rows<2, 32>(a, st);  // up to kMaxNormCols
+  if (cols <= 256) return launch_rows<1, 1>(a, st);
+  if (cols <= 512) return launch_rows<2, 1>(a, st);
+  switch (row_warps(cols, 4)) {  // up to kMaxNormCols
+    case 1: return launch_rows<4, 1>(a, st);
+    case 2: return launch_rows<4, 2>(a, st);
+    case 4: return launch_rows<4, 4>(a, st);
+    case 8: return launch_rows<4, 8>(a, st);
+    default: return launch_rows<4, 16>(a, st);
+  }
 }
 
 cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *rstd_lo,
@@ -656,18 +763,19 @@ cudaError_t launch_rmsnorm_bwd(const void *dy, const void *dr, const void *r, co
     LaunchScope ls("rmsnorm_bwd", st, (dr ? 8.0 : 6.0) * rows * cols + 4.0 * rows,
                    8.0 * rows * cols, rows, cols);
     cudaError_t e;
-    switch (bwd_warps(cols)) {
-      case 1: e = launch_bwd<2, 1>(a, grid, st); break;
-      case 2: e = launch_bwd<2, 2>(a, grid, st); break;
-      case 4: e = launch_bwd<2, 4>(a, grid, st); break;
-      case 8: e = launch_bwd<2, 8>(a, grid, st); break;
-      case 16: e = launch_bwd<2, 16>(a, grid, st); break;
-      default: e = launch_bwd<2, 32>(a, grid, st); break;
-    }
+    const int wpr = row_warps(cols, bwd_vpt(cols));
+    if (bwd_vpt(cols) == 4) e = launch_bwd<4, 16>(a, grid, st);
+    else if (wpr == 1) e = launch_bwd<2, 1>(a, grid, st);
+    else if (wpr == 2) e = launch_bwd<2, 2>(a, grid, st);
+    else if (wpr == 4) e = launch_bwd<2, 4>(a, grid, st);
+    else if (wpr == 8) e = launch_bwd<2, 8>(a, grid, st);
+    else e = launch_bwd<2, 16>(a, grid, st);
     if (e != cudaSuccess) return e;
   }
   LaunchScope ls("rmsnorm_dw", st, 4.0 * grid * cols + 4.0 * cols, (double)grid * cols, grid, cols);
-  return launch_kernel(rmsnorm_dw_kernel, dim3((unsigned)(cols / 16)), dim3(512), 0, st,
+  // a plain launch: overlapped with the pass before it, a forward and backward
+  // at 16379 x 4096 took 237 us instead of 220
+  return launch_kernel_as(false, rmsnorm_dw_kernel, dim3((unsigned)(cols / 16)), dim3(512), 0, st,
                        (const float *)partials, grid, cols, dw);
 }
 

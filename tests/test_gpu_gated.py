@@ -261,3 +261,24 @@ def test_refusals(fp):
     cache.get(odd)
     with pytest.raises(fp.FP8Error):                       # F = 160: tiles would straddle Wg and Wu
         fp.fp8_gated_fwd(x, cache, odd, "block")
+
+
+@pytest.mark.parametrize("recipe", ["tensorwise", "block"])
+@pytest.mark.parametrize("N,K", [(16, 16), (16, 528), (32, 1040), (48, 2048), (64, 4096)])
+def test_few_token_quantizer_equals_the_quantizer(fp, recipe, N, K):
+    """The transposed FP8 input kept for the backward pass is that of
+    fp8_quantize bit for bit, special values included."""
+    F = 128
+    x, w, dh, cache, h = _case(fp, N, K, F, recipe, 9)
+    x[0, 0] = float("nan")
+    x[N - 1, K - 1] = -float("inf") if recipe == "block" else 0.0
+    x[3, :] = 0
+    x[:, 5] = 0
+    y, ctx = fp.fp8_gated_fwd(x, cache, h, recipe)
+    q = fp.fp8_quantize(x, recipe, "act")
+    p = fp.fp8_gated_ctx_layout(recipe, ctx)
+    off = p[0].value - ctx.ctx.data_ptr()
+    assert torch.equal(ctx.ctx[off:off + N * K].view(K, N), q["col"])
+    off = p[2].value - ctx.ctx.data_ptr()
+    si = q["col_scale_inv"]
+    assert torch.equal(ctx.ctx[off:off + 4 * si.numel()].view(torch.float32).view(si.shape), si)

@@ -60,7 +60,8 @@ def _check_scale(scale, inv, y, what):
 
 
 @pytest.mark.parametrize("R,C", [(1, 16), (1, 4096), (2, 128), (17, 144), (127, 272), (128, 256), (129, 512),
-                                 (300, 1040), (64, 2064), (33, 4112), (40, 8192), (5, 8208), (3, 16384)])
+                                 (300, 1040), (64, 2064), (33, 4112), (40, 8192), (5, 8208), (3, 16384),
+                                 (5003, 144), (9001, 512), (5111, 1040), (1301, 4096), (1217, 8192), (400, 16384)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_forward(fp, R, C, residual):
     t = _inputs(R, C, R * 7 + C)
@@ -127,7 +128,7 @@ def test_zero_and_nonfinite_rows(fp):
 
 
 @pytest.mark.parametrize("R,C", [(1, 16), (1, 4096), (9, 144), (129, 512), (1500, 528), (2500, 1024), (300, 2064),
-                                 (700, 4096), (50, 8192), (3, 16384)])
+                                 (700, 4096), (50, 8192), (3, 16384), (9001, 272), (1999, 4112), (700, 16384)])
 @pytest.mark.parametrize("stream_grad", [True, False])
 def test_backward(fp, R, C, stream_grad):
     t = _inputs(R, C, R + C)
