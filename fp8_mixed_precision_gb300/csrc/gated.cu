@@ -61,6 +61,21 @@ __device__ __forceinline__ void act2(float g0, float g1, float &a0, float &a1) {
     gelu_f2(g0, g1, a0, a1);
   }
 }
+// GELU and its derivative from one evaluation of the erfc fit (common.cuh):
+// Phi(g) is erfc(|g| / sqrt 2) / 2 or one minus it, GELU = g Phi and
+// GELU' = Phi + g phi.
+__device__ __forceinline__ void gelu_both2(float g0, float g1, float &a0, float &a1, float &d0,
+                                           float &d1) {
+  uint64_t tq, e64;
+  gelu2::parts(g0, g1, tq, e64);
+  const uint64_t e = mul2(e64, dup(5.42101086242752217e-20f));  // exp(-g^2 / 2)
+  float t0, t1;
+  upk(mul2(tq, e), t0, t1);
+  const uint64_t g = pk(g0, g1);
+  const uint64_t p = pk(g0 >= 0.0f ? __fsub_rn(1.0f, t0) : t0, g1 >= 0.0f ? __fsub_rn(1.0f, t1) : t1);
+  upk(mul2(g, p), a0, a1);
+  upk(fma2(mul2(g, dup(0.39894228040143268f)), e, p), d0, d1);
+}
 // act and act' of two values
 template <int ACT>
 __device__ __forceinline__ void act_grad2(float g0, float g1, float &a0, float &a1, float &d0,
@@ -72,8 +87,7 @@ __device__ __forceinline__ void act_grad2(float g0, float g1, float &a0, float &
     d0 = __fmul_rn(s0, fmaf(g0, 1.0f - s0, 1.0f));
     d1 = __fmul_rn(s1, fmaf(g1, 1.0f - s1, 1.0f));
   } else {
-    gelu_f2(g0, g1, a0, a1);
-    gelu_grad_f2(g0, g1, d0, d1);
+    gelu_both2(g0, g1, a0, a1, d0, d1);
   }
 }
 
