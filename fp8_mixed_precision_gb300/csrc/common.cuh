@@ -72,7 +72,8 @@ __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
   return cvt2<FMT>(a, b) | (cvt2<FMT>(c, d) << 16);
 }
 
-// As cvt2 without the NaN fix-up: only for values known not to be NaN.
+// As cvt2 without the NaN fix-up (sm_103a's conversion itself gives 0x7F for
+// every NaN, checked for both formats, signs and payloads).
 template <int FMT>
 __device__ __forceinline__ uint32_t cvt2_finite(float lo, float hi) {
   uint16_t r;

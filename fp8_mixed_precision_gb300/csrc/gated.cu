@@ -894,14 +894,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     __syncthreads();  // the buffers are read, and the last tile's transpose too
     prefetch(id + gridDim.x);
-    // 0 * v is NaN exactly for an infinite or NaN v: selects the cast's fix-up
-    float nan_acc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        nan_acc = fmaf(v[0][i][j], 0.0f, fmaf(v[1][i][j], 0.0f, nan_acc));
-    const bool special = isnan(nan_acc);
     if constexpr (BLOCK) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
@@ -953,13 +945,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) upk(mul2(pk(x[j], x[j + 1]), pk(s[j], s[j + 1])), y[j], y[j + 1]);
       uint2 q;
-      if (!special) {
-        q.x = cvt4_finite<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
-        q.y = cvt4_finite<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
-      } else {
-        q.x = cvt4<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
-        q.y = cvt4<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
-      }
+      q.x = cvt4_finite<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
+      q.y = cvt4_finite<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
       return q;
     };
 #pragma unroll

@@ -103,16 +103,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Eight values -> eight E4M3 bytes; `special`: some value of the thread is
-// infinite or NaN, which selects the NaN fix-up.
-__device__ __forceinline__ uint2 cast8(const float (&v)[8], bool special) {
-  if (!special)
-    return make_uint2(cvt4_finite<FP8_FORMAT_E4M3>(v[0], v[1], v[2], v[3]),
-                      cvt4_finite<FP8_FORMAT_E4M3>(v[4], v[5], v[6], v[7]));
-  return make_uint2(cvt4<FP8_FORMAT_E4M3>(v[0], v[1], v[2], v[3]),
-                    cvt4<FP8_FORMAT_E4M3>(v[4], v[5], v[6], v[7]));
+// Eight values -> eight E4M3 bytes (the hardware's conversion maps every NaN to
+// 0x7F, the library's NaN byte, and infinities to the largest magnitude).
+__device__ __forceinline__ uint2 cast8(const float (&v)[8]) {
+  return make_uint2(cvt4_finite<FP8_FORMAT_E4M3>(v[0], v[1], v[2], v[3]),
+                    cvt4_finite<FP8_FORMAT_E4M3>(v[4], v[5], v[6], v[7]));
 }
-
 // v * s, two products per instruction
 __device__ __forceinline__ void scale8(const float (&v)[8], float s, float (&q)[8]) {
   using namespace gelu2;
@@ -133,33 +129,55 @@ struct NormFwd {
   float *row_scale, *row_scale_inv;
 };
 
-// One row, held by WPR warps (VPT vectors of 8 elements per thread) as rv (x)
-// and sv (the residual): everything that the row alone determines is written
-// from these registers.  `sync` joins the row's warps; `red` is theirs.
-template <int VPT, int WPR, typename Sync>
-__device__ __forceinline__ void norm_row(const NormFwd &a, int64_t row, bool live, int wir,
-                                         uint4 (&rv)[VPT], const uint4 (&sv)[VPT], float2 *red,
-                                         Sync sync) {
-  const int lane = threadIdx.x & 31;
+// bf16(x + res): the exact sum rounded once.
+__device__ __forceinline__ uint4 add8(uint4 x, uint4 res) {
+  auto add = [](uint32_t a, uint32_t b) {
+    const __nv_bfloat162 s = __hadd2(*reinterpret_cast<__nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&s);
+  };
+  return make_uint4(add(x.x, res.x), add(x.y, res.y), add(x.z, res.z), add(x.w, res.w));
+}
+
+// Rows: a group of WPR warps, or of LANES = 16 lanes of one, holds one row in
+// registers (VPT vectors of 8 elements per thread), so x and the residual are
+// read once and everything that the row alone determines is written from
+// there; many small CTAs per SM hide the latency of the row sum.  Half a warp
+// takes the rows of up to 512 columns: what is done once per row (joining the
+// sum, the root, the scales' divisions) is then spread over twice the elements.
+template <int VPT, int WPR, int LANES = 32>
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
+    rmsnorm_rows_kernel(NormFwd a) {
+  static_assert(LANES == 32 || (LANES == 16 && WPR == 1), "half a warp per row");
+  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
+  constexpr int kRows = kWarps * 32 / (WPR * LANES);  // rows per CTA
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lir = lane % LANES;
+  const int wir = warp % WPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (WPR * LANES);
+  const bool live = row < a.R;
   const int nv = (int)(a.C / 8);
   const int64_t base = row * nv;
-  // vectors that hold columns of the row, whole warps at a time
-  const int vecs = min(VPT, (nv - wir * 32 + WPR * 32 - 1) / (WPR * 32));
+  // vectors that hold columns of the row, whole groups at a time
+  const int vecs = min(VPT, (nv - wir * LANES + WPR * LANES - 1) / (WPR * LANES));
+  auto vec = [&](int j) { return (j * WPR + wir) * LANES + lir; };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 rv[VPT], sv[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const bool in = live && vec(j) < nv;
+    rv[j] = in ? a.x[base + vec(j)] : zero;
+    sv[j] = in && a.res ? a.res[base + vec(j)] : zero;
+  }
   float ss = 0.0f, lo = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
+    if (a.res) {
+      rv[j] = add8(rv[j], sv[j]);
+      if (live && vec(j) < nv) a.r[base + vec(j)] = rv[j];
+    }
     float p[8];
     unpack8(rv[j], p);
-    if (a.res) {
-      float q[8];
-      unpack8(sv[j], q);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] += q[k];
-      rv[j] = pack8(p);
-      unpack8(rv[j], p);
-      const int v = (j * WPR + wir) * 32 + lane;
-      if (live && v < nv) a.r[base + v] = rv[j];
-    }
     // bf16 squares have 16 bits, so four of them add up with next to no
     // rounding; every join of such sums carries its error along
 #pragma unroll
@@ -172,53 +190,46 @@ __device__ __forceinline__ void norm_row(const NormFwd &a, int64_t row, bool liv
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = LANES / 2; o; o >>= 1) {
     float e;
     const float other_lo = __shfl_xor_sync(0xffffffffu, lo, o);
     two_sum(ss, __shfl_xor_sync(0xffffffffu, ss, o), ss, e);
     lo = __fadd_rn(__fadd_rn(lo, other_lo), e);
   }
   if constexpr (WPR > 1) {
-    if (lane == 0) red[wir] = make_float2(ss, lo);
-    sync();
+    __shared__ float2 red[kWarps];
+    if (lane == 0) red[warp] = make_float2(ss, lo);
+    __syncthreads();
     ss = lo = 0.0f;
 #pragma unroll
     for (int k = 0; k < WPR; ++k) {
+      const float2 v = red[warp / WPR * WPR + k];
       float e;
-      two_sum(ss, red[k].x, ss, e);
-      lo = __fadd_rn(__fadd_rn(lo, red[k].y), e);
+      two_sum(ss, v.x, ss, e);
+      lo = __fadd_rn(__fadd_rn(lo, v.y), e);
     }
   }
-  if (!live) return;
+  if (__all_sync(0xffffffffu, !live)) return;
   float rstd, rstd_lo;
   rstd_pair(ss, lo, (float)a.C, a.inv_c, a.eps, rstd, rstd_lo);
-  if (wir == 0 && lane == 0) {
+  if (live && wir == 0 && lir == 0) {
     if (a.rstd) a.rstd[row] = rstd;
     if (a.rstd_lo) a.rstd_lo[row] = rstd_lo;
   }
   const int64_t nb = (a.C + 127) / 128;
   float y[VPT][8], mx[VPT];
-  uint64_t nan_acc = 0;  // 0 * y is NaN exactly for an infinite or NaN y
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     if (j >= vecs) break;
-    const int v = (j * WPR + wir) * 32 + lane;
-    const bool in = v < nv;
     float w8[8] = {};
-    if (in) load_w8(a.w, (int64_t)v * 8, w8);
+    if (vec(j) < nv) load_w8(a.w, (int64_t)vec(j) * 8, w8);
     norm8(rv[j], rstd, rstd_lo, w8, y[j]);
-    if (a.y && in) a.y[base + v] = pack8(y[j]);
+    if (a.y && live && vec(j) < nv) a.y[base + vec(j)] = pack8(y[j]);
     mx[j] = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) mx[j] = amax_acc(mx[j], y[j][k]);
-#pragma unroll
-    for (int k = 0; k < 8; k += 2)
-      nan_acc = gelu2::fma2(gelu2::pk(y[j][k], y[j][k + 1]), 0, nan_acc);
   }
   if (!a.row) return;
-  float n0, n1;
-  gelu2::upk(nan_acc, n0, n1);
-  const bool special = isnan(__fadd_rn(n0, n1));
   // the block scales of the thread's vectors: lane j of each half warp divides
   // for vector j, and the others take the result from it
   float m = 0.0f, s, si;
@@ -233,44 +244,18 @@ __device__ __forceinline__ void norm_row(const NormFwd &a, int64_t row, bool liv
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     if (j >= vecs) break;
-    const int v = (j * WPR + wir) * 32 + lane;
+    const int v = vec(j);
     const float sj = __shfl_sync(0xffffffffu, s, (lane & 16) + j);
-    if (v < nv) {
+    if (live && v < nv) {
       float q8[8];
       scale8(y[j], sj, q8);
-      *reinterpret_cast<uint2 *>(a.row + row * a.C + (int64_t)v * 8) = cast8(q8, special);
+      *reinterpret_cast<uint2 *>(a.row + row * a.C + (int64_t)v * 8) = cast8(q8);
     }
-    if ((lane & 15) == j && v - j < nv) {  // v - j: the block's first vector
+    if (live && (lane & 15) == j && v - j < nv) {  // v - j: the block's first vector
       a.row_scale[row * nb + v / 16] = s;
       a.row_scale_inv[row * nb + v / 16] = si;
     }
   }
-}
-
-// Each row's warps load it themselves; many small CTAs per SM hide the latency
-// of the row sum.  (131072 x 512: 81 us; fed by the ring of the backward pass,
-// with 18 warps per SM, 111 us.)
-template <int VPT, int WPR>
-__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
-    rmsnorm_rows_kernel(NormFwd a) {
-  constexpr int kWarps = WPR > 8 ? WPR : kNormThreads / 32;
-  constexpr int kRows = kWarps / WPR;  // rows per CTA
-  __shared__ float2 red[kWarps];
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wir = warp % WPR;
-  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
-  const bool live = row < a.R;
-  const int nv = (int)(a.C / 8);
-  uint4 rv[VPT], sv[VPT];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int v = (j * WPR + wir) * 32 + lane;
-    const bool in = live && v < nv;
-    rv[j] = in ? a.x[row * nv + v] : make_uint4(0, 0, 0, 0);
-    sv[j] = in && a.res ? a.res[row * nv + v] : make_uint4(0, 0, 0, 0);
-  }
-  norm_row<VPT, WPR>(a, row, live, wir, rv, sv, red + warp / WPR * WPR, [] { __syncthreads(); });
 }
 
 struct NormCols {
@@ -363,18 +348,13 @@ __global__ void __launch_bounds__(kColThreads, 2)
         for (int j = 0; j < 8; ++j) y[i][j] = 0.0f;
     }
     float cm[8] = {};
-    uint64_t nan_acc = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         cm[j] = amax_acc(cm[j], y[i][j]);
         cm[j + 1] = amax_acc(cm[j + 1], y[i][j + 1]);
-        nan_acc = gelu2::fma2(gelu2::pk(y[i][j], y[i][j + 1]), 0, nan_acc);
       }
-    float n0, n1;
-    gelu2::upk(nan_acc, n0, n1);
-    const bool special = isnan(__fadd_rn(n0, n1));
 #pragma unroll
     for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
     if (lane < 16) {
@@ -408,7 +388,7 @@ __global__ void __launch_bounds__(kColThreads, 2)
 #pragma unroll
       for (int j = 0; j < 8; j += 2)
         upk(mul2(pk(y[i][j], y[i][j + 1]), pk(cs[j], cs[j + 1])), q8[j], q8[j + 1]);
-      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = cast8(q8, special);
+      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = cast8(q8);
     }
     __syncthreads();
     const int seg = t & 7, w = t >> 3;  // rows seg*16..+15, columns 4w..4w+3
@@ -674,12 +654,12 @@ int ring_stages(int smem, int group, int64_t C, int tensors) {
   return (int)std::min<int64_t>(kRingStages, (smem - kRingCtlBytes) / (group * C * 2 * tensors));
 }
 
-template <int VPT, int WPR>
+template <int VPT, int WPR, int LANES = 32>
 cudaError_t launch_rows(const NormFwd &a, cudaStream_t st) {
   constexpr int kThreads = WPR > 8 ? 32 * WPR : kNormThreads;
-  constexpr int kRows = kThreads / 32 / WPR;
-  return launch_kernel(rmsnorm_rows_kernel<VPT, WPR>, dim3((unsigned)((a.R + kRows - 1) / kRows)),
-                       dim3(kThreads), 0, st, a);
+  constexpr int kRows = kThreads / (WPR * LANES);
+  return launch_kernel(rmsnorm_rows_kernel<VPT, WPR, LANES>,
+                       dim3((unsigned)((a.R + kRows - 1) / kRows)), dim3(kThreads), 0, st, a);
 }
 
 template <int VPT, int WPR>
@@ -717,8 +697,8 @@ cudaError_t launch_rmsnorm_rows(const void *x, const void *res, const void *w, i
                  n * (2 + (res ? 4 : 0) + (y ? 2 : 0) + (row ? 1 : 0)) +
                      rows * 8.0 * ((cols + 127) / 128),
                  4 * n, rows, cols);
-  if (cols <= 256) return launch_rows<1, 1>(a, st);
-  if (cols <= 512) return launch_rows<2, 1>(a, st);
+  if (cols <= 256) return launch_rows<2, 1, 16>(a, st);
+  if (cols <= 512) return launch_rows<4, 1, 16>(a, st);
   switch (row_warps(cols, 4)) {  // up to kMaxNormCols
     case 1: return launch_rows<4, 1>(a, st);
     case 2: return launch_rows<4, 2>(a, st);
