@@ -266,12 +266,13 @@ struct NormCols {
   float *col_scale, *col_scale_inv;
 };
 
-constexpr int kColThreads = 256;
+// Tile of the transposing pass: 128 tokens x 64 columns per CTA of 4 warps.
+constexpr int kColThreads = 128, kColTile = 64;
 struct __align__(128) CSmem {
-  uint16_t in[2][128 * 128];
-  uint32_t tile[128 * 32];
-  float colred[8][128];
-  float colsc[128];
+  uint16_t in[2][128 * kColTile];
+  uint32_t tile[128 * kColTile / 4 + 32];  // FP8 bytes, 4 words of padding per 16 rows
+  float colred[4][kColTile];
+  float colsc[kColTile];
   float2 rs[128];
   uint64_t full[2];
 };
@@ -289,22 +290,26 @@ __device__ __forceinline__ void wait_tile(uint64_t *bar, uint32_t parity) {
     }
   }
 }
-// Word w of tile row r lives at word r*32 + (w ^ swz(r)): the transpose's lanes
-// (8 groups of 16 rows, 4 words) then fall on 32 different banks.
-__device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
+// Word w (4 columns) of tile row r.  The padding puts the transpose's lanes (8
+// groups of 16 rows, 4 words) on 32 different banks.
+__device__ __forceinline__ int tile_word(int r, int w) {
+  return r * (kColTile / 4) + (r >> 4) * 4 + w;
+}
 
-// Transposed copy: 128 tokens x 128 columns per iteration.  r comes back by
+// Transposed copy: 128 tokens x 64 columns per iteration.  r comes back by
 // TMA, y is formed again from r, rstd and w, each column's maximum over its
-// 128 tokens gives its scale, and the bytes go through a swizzled tile so
-// that 16 tokens leave in one store.  Tokens past R are zeros.  Tiles run last
-// to first: the end of r is what L2 still holds after the row pass.
-__global__ void __launch_bounds__(kColThreads, 2)
+// 128 tokens gives its scale, and the bytes go through a padded tile so that
+// 16 tokens leave in one store.  Tokens past R are zeros.  Tiles run last to
+// first: the end of r is what L2 still holds after the row pass.  What bounds
+// it is the instructions between a tile's barriers, so CTAs are small (4 warps,
+// four CTAs per SM).
+__global__ void __launch_bounds__(kColThreads, 4)
     rmsnorm_cols_kernel(const __grid_constant__ CUtensorMap tmr, NormCols p) {
   extern __shared__ __align__(1024) uint8_t n_smem_raw[];
   CSmem &S = *reinterpret_cast<CSmem *>(n_smem_raw);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int cg = t & 15, rr = t >> 4;  // 8 columns, rows rr + 16 i
-  const int64_t tiles_r = (p.R + 127) / 128, tiles_c = (p.C + 127) / 128;
+  const int cg = t & 7, rr = t >> 3;  // 8 columns, rows rr + 16 i
+  const int64_t tiles_r = (p.R + 127) / 128, tiles_c = (p.C + kColTile - 1) / kColTile;
   const int64_t ntiles = tiles_r * tiles_c;
   if (t == 0) {
     ptx::mbar_init(&S.full[0], 1);
@@ -318,8 +323,8 @@ __global__ void __launch_bounds__(kColThreads, 2)
     if (t != 0 || id >= ntiles) return;
     const int64_t tr = (ntiles - 1 - id) / tiles_c, tc = (ntiles - 1 - id) % tiles_c;
     ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive_expect_tx(&S.full[b], 128u * 128 * 2);
-    ptx::tma_load_2d(S.in[b], &tmr, &S.full[b], (int)(tc * 128), (int)(tr * 128));
+    ptx::mbar_arrive_expect_tx(&S.full[b], 128u * kColTile * 2);
+    ptx::tma_load_2d(S.in[b], &tmr, &S.full[b], (int)(tc * kColTile), (int)(tr * 128));
   };
   int64_t id = blockIdx.x;
   prefetch(id, 0);
@@ -327,14 +332,12 @@ __global__ void __launch_bounds__(kColThreads, 2)
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
     const int b = k & 1;
     const int64_t tr = (ntiles - 1 - id) / tiles_c, tc = (ntiles - 1 - id) % tiles_c;
-    const int64_t r0 = tr * 128, c0 = tc * 128;
+    const int64_t r0 = tr * 128, c0 = tc * kColTile;
     const int rows_here = (int)(p.R - r0 < 128 ? p.R - r0 : 128);
-    const int cols_here = (int)(p.C - c0 < 128 ? p.C - c0 : 128);
+    const int cols_here = (int)(p.C - c0 < kColTile ? p.C - c0 : kColTile);
     float w8[8] = {};
     if (8 * cg < cols_here) load_w8(p.w, c0 + 8 * cg, w8);
-    if (t < 128) {
-      S.rs[t] = t < rows_here ? make_float2(p.rstd[r0 + t], p.rstd_lo[r0 + t]) : make_float2(0.0f, 0.0f);
-    }
+    S.rs[t] = t < rows_here ? make_float2(p.rstd[r0 + t], p.rstd_lo[r0 + t]) : make_float2(0.0f, 0.0f);
     wait_tile(&S.full[b], (k >> 1) & 1);
     __syncthreads();
     float y[8][8];  // rows rr + 16 i; tokens past R: zeros
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kColThreads, 2)
     for (int i = 0; i < 8; ++i) {
       const int r = rr + 16 * i;
       const float2 rs = S.rs[r];
-      norm8(*reinterpret_cast<const uint4 *>(&S.in[b][r * 128 + 8 * cg]), rs.x, rs.y, w8, y[i]);
+      norm8(*reinterpret_cast<const uint4 *>(&S.in[b][r * kColTile + 8 * cg]), rs.x, rs.y, w8, y[i]);
       if (r >= rows_here)
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[i][j] = 0.0f;
@@ -351,23 +354,22 @@ __global__ void __launch_bounds__(kColThreads, 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        cm[j] = amax_acc(cm[j], y[i][j]);
-        cm[j + 1] = amax_acc(cm[j + 1], y[i][j + 1]);
-      }
+      for (int j = 0; j < 8; ++j) cm[j] = amax_acc(cm[j], y[i][j]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-    if (lane < 16) {
+    for (int j = 0; j < 8; ++j) {
+      cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 8));
+      cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+    }
+    if (lane < 8) {
       float4 *dst = reinterpret_cast<float4 *>(&S.colred[warp][8 * cg]);
       dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
       dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
     }
     __syncthreads();
     prefetch(id + 2 * (int64_t)gridDim.x, b);  // every thread holds its elements
-    if (t < 128) {
-      float m = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) m = fmaxf(m, S.colred[w][t]);
+    if (t < kColTile) {
+      const float m = fmaxf(fmaxf(S.colred[0][t], S.colred[1][t]),
+                            fmaxf(S.colred[2][t], S.colred[3][t]));
       float s, si;
       scale_from_amax(m, kE4M3Max, s, si);
       S.colsc[t] = s;
@@ -383,22 +385,18 @@ __global__ void __launch_bounds__(kColThreads, 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       using namespace gelu2;
-      const int r = rr + 16 * i;
       float q8[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 2)
         upk(mul2(pk(y[i][j], y[i][j + 1]), pk(cs[j], cs[j + 1])), q8[j], q8[j + 1]);
-      *reinterpret_cast<uint2 *>(&S.tile[r * 32 + ((2 * cg) ^ swz(r))]) = cast8(q8);
+      *reinterpret_cast<uint2 *>(&S.tile[tile_word(rr + 16 * i, 2 * cg)]) = cast8(q8);
     }
     __syncthreads();
     const int seg = t & 7, w = t >> 3;  // rows seg*16..+15, columns 4w..4w+3
     if (4 * w < cols_here && 16 * seg < rows_here) {
       uint32_t a[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = seg * 16 + i;
-        a[i] = S.tile[r * 32 + (w ^ swz(r))];
-      }
+      for (int i = 0; i < 16; ++i) a[i] = S.tile[tile_word(seg * 16 + i, w)];
       uint32_t o[4][4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -712,7 +710,7 @@ cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *r
                                 const void *w, int w_f32, int64_t rows, int64_t cols, uint8_t *col, float *col_scale,
                                 float *col_scale_inv, cudaStream_t st) {
   CUtensorMap tm;
-  if (!make_bf16_tile_map(&tm, r, rows, cols, 128, 128)) return cudaErrorInvalidValue;
+  if (!make_bf16_tile_map(&tm, r, rows, cols, 128, kColTile)) return cudaErrorInvalidValue;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -723,8 +721,8 @@ cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *r
     attr_set[dev] = true;
   }
   NormCols p{{w, w_f32}, rows, cols, (rows + 15) / 16 * 16, rstd, rstd_lo, col, col_scale, col_scale_inv};
-  const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
-  const int64_t grid = std::min<int64_t>(tiles, (int64_t)num_sms() * 2);
+  const int64_t tiles = ((rows + 127) / 128) * ((cols + kColTile - 1) / kColTile);
+  const int64_t grid = std::min<int64_t>(tiles, (int64_t)num_sms() * 4);
   LaunchScope ls("rmsnorm_cols", st,
                  3.0 * rows * cols + 4.0 * rows + 8.0 * cols * ((rows + 127) / 128),
                  2.0 * rows * cols, rows, cols);
