@@ -107,7 +107,9 @@ struct GCfg {
   static constexpr int kStageA = BM * BK, kStageB = BN * BK;
   static constexpr int kStageBytes = kStageA + kStageB;
   static constexpr int kSlabBytes = 32 * 128;  // 32 tokens x 64 bf16 columns
-  static constexpr int kSlabs = SAVE ? 2 : 1;  // per epilogue warp
+  // One slab buffer per warp, which leaves room for a fourth operand stage
+  // (131072 x 2048, K 512, keeping G and U: 302 us; two buffers, three stages 324)
+  static constexpr int kSlabs = 1;
   static constexpr int kOutBytes = kEpi * kSlabs * kSlabBytes;
   static constexpr int kRing = kSmemBudget - 1024 - kOutBytes - kCtlBytes;
   static constexpr int kStages = kRing / kStageBytes;
@@ -849,7 +851,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   pdl_wait_then_release();
   auto prefetch = [&](int64_t id) {
     if (t != 0 || id >= ntiles) return;
-    const int x = (int)(id % tiles_c) * 128, y = (int)(id / tiles_c) * 128;
+    const int64_t at = BLOCK ? id : ntiles - 1 - id;
+    const int x = (int)(at % tiles_c) * 128, y = (int)(at / tiles_c) * 128;
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive_expect_tx(&S.full, 3u * 128 * 128 * 2);
     ptx::tma_load_2d(S.in[0], &tmD, &S.full, x, y);
@@ -878,22 +881,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   volatile int no_abort = 0;
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
-    const int64_t tr = id / tiles_c, tc = id % tiles_c;
+    // tensor scaling: last tile first, where the maximum's pass ended
+    const int64_t at = BLOCK ? id : ntiles - 1 - id;
+    const int64_t tr = at / tiles_c, tc = at % tiles_c;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int rows_here = (int)(p.N - r0 < 128 ? p.N - r0 : 128);
     const int cols_here = (int)(p.F - c0 < 128 ? p.F - c0 : 128);
     const bool col_ok = 8 * cg < cols_here;
     pipe::wait_bar(&S.full, k & 1, &no_abort, &g_gated_status);  // on expiry: recorded, carry on
-    float v[2][4][8];  // [dG, dU][row][column]
+    uint4 in[3][4];  // dH, G, U of this thread's 4 rows
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int o = (rr + 32 * i) * 128 + 8 * cg;
-      dgu8<ACT>(*reinterpret_cast<const uint4 *>(&S.in[0][o]),
-                *reinterpret_cast<const uint4 *>(&S.in[1][o]),
-                *reinterpret_cast<const uint4 *>(&S.in[2][o]), v[0][i], v[1][i]);
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k3 = 0; k3 < 3; ++k3)
+        in[k3][i] = *reinterpret_cast<const uint4 *>(&S.in[k3][(rr + 32 * i) * 128 + 8 * cg]);
+    // dG and dU are formed after the next tile has been requested where memory
+    // is the bound (tensor scaling, 131072 x 2048: 404 us, before it 435), and
+    // before where the arithmetic is (block scaling, 16384 x 14336: 502 / 519)
+    float v[2][4][8];  // [dG, dU][row][column]
+    auto form = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dgu8<ACT>(in[0][i], in[1][i], in[2][i], v[0][i], v[1][i]);
+    };
+    if (BLOCK) form();
     __syncthreads();  // the buffers are read, and the last tile's transpose too
     prefetch(id + gridDim.x);
+    if (!BLOCK) form();
     if constexpr (BLOCK) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
