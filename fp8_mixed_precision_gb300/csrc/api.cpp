@@ -827,17 +827,16 @@ fp8_status gated_entry(fp8_weight_cache *cache, fp8_weight_handle h, int recipe,
   return FP8_OK;
 }
 
-// The forward kernel on quantized tokens.  own_input: the kernel before it on
-// the stream is this call's quantizer.
+// The forward kernel on quantized tokens.
 fp8_status gated_fwd_on(const uint8_t *xq, const float *xsi, int64_t N,
                         const fp8_weight_cache::Entry &e, int recipe, int act, void *H, void *ctx,
-                        bool own_input, fp8_stream_t stream) {
+                        fp8_stream_t stream) {
   const int64_t F = e.O / 2;
   const GatedCtx L = gated_ctx((fp8_recipe)recipe, N, e.K, F);
   uint8_t *c = static_cast<uint8_t *>(ctx);
   return from_cuda(launch_gated_fwd(xq, xsi, e.w_row, e.row_scale_inv, N, e.K, F,
                                     recipe == FP8_RECIPE_BLOCK, act, H, c ? c + L.g : nullptr,
-                                    c ? c + L.u : nullptr, own_input, cs(stream)));
+                                    c ? c + L.u : nullptr, cs(stream)));
 }
 
 }  // namespace
@@ -886,7 +885,7 @@ fp8_status fp8_gated_fwd_quantized(const uint8_t *xq_row, const float *xq_row_sc
   if (N == 0) return FP8_OK;
   if (!xq_row || !xq_row_scale_inv || !H) return FP8_ERR_INVALID_ARG;
   if (!aligned16(xq_row) || !aligned16(H) || !aligned16(ctx)) return FP8_ERR_ALIGN;
-  return gated_fwd_on(xq_row, xq_row_scale_inv, N, *e, recipe, act, H, ctx, false, stream);
+  return gated_fwd_on(xq_row, xq_row_scale_inv, N, *e, recipe, act, H, ctx, stream);
 }
 
 fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *cache,
@@ -917,7 +916,7 @@ fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *
                                    reinterpret_cast<float *>(w + L.xs), xsi, cscale, cscale_inv,
                                    reinterpret_cast<float *>(w + L.part), cs(stream)));
   if (st != FP8_OK) return st;
-  return gated_fwd_on(w + L.xq, xsi, N, *e, recipe, act, H, ctx, true, stream);
+  return gated_fwd_on(w + L.xq, xsi, N, *e, recipe, act, H, ctx, stream);
 }
 
 fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,

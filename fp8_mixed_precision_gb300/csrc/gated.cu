@@ -419,7 +419,6 @@ struct SmallArgs {
   const float *x_sinv, *w_sinv;
   uint32_t idesc;
   __nv_bfloat16 *H, *G, *U;  // G and U null: not kept
-  int early;  // the weight may be read before the wait (see launch_gated_fwd)
 };
 
 template <int SCALING, int ACT, int NT>
@@ -459,18 +458,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     ptx::tmem_alloc(&ctl->tmem_base, kCols);
     ptx::tmem_relinquish();
   }
-  // The first stages' weight tiles: requested before the wait when the kernel
-  // before this one only makes the tokens (they are then on their way while
-  // it runs: a token at K 4096, F 14336 takes 21 us a pass instead of 24).
-  const int ahead = a.early ? min(a.stages, nkb) : 0;
-  auto load_weight = [&](int i, int stage) {
-    uint8_t *sw = ring + (size_t)stage * kStageBytes;
-    ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
-    ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(i), f0);
-    ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(i), (int)a.F + f0);
-  };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < ahead; ++i) load_weight(i, i);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -490,9 +477,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       int issued = 0;
       for (; issued < nkb; ++issued) {
         if (!wait(&ctl->empty[stage], phase ^ 1)) { ok = false; break; }
-        if (issued >= ahead) load_weight(issued, stage);
-        ptx::tma_load_2d(ring + (size_t)stage * kStageBytes + 2 * BF * BK, &tmX, &ctl->full[stage],
-                         kx(issued), n0);
+        uint8_t *sw = ring + (size_t)stage * kStageBytes;
+        ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
+        ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(issued), f0);
+        ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(issued), (int)a.F + f0);
+        ptx::tma_load_2d(sw + 2 * BF * BK, &tmX, &ctl->full[stage], kx(issued), n0);
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
       }
       if (!ok)  // the last copies of each stage land before the CTA can exit
@@ -1103,7 +1092,7 @@ cudaError_t launch_cast(const CUtensorMap (&m)[3], const GatedBwd &p, cudaStream
 
 cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
                              const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
-                             int act, void *H, void *G, void *U, bool own_input, cudaStream_t st) {
+                             int act, void *H, void *G, void *U, cudaStream_t st) {
   const bool save = G != nullptr;
   const double bytes = (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F;
   const int64_t tiles = (F + BF - 1) / BF;
@@ -1129,7 +1118,6 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
     a.H = static_cast<__nv_bfloat16 *>(H);
     a.G = static_cast<__nv_bfloat16 *>(G);
     a.U = static_cast<__nv_bfloat16 *>(U);
-    a.early = own_input;
     // the token scales of a CTA's K range are kept in shared memory (K up to
     // 8192 at any split, 65536 at the full one; wider ones take the other kernel)
     if (a.kbs_cta <= 64 && tiles * a.split < (int64_t(1) << 31)) {
