@@ -651,6 +651,14 @@ def fp8_linear_bwd_after_amax(dy: torch.Tensor, dy_partials: torch.Tensor, ctx: 
     return dx, dw
 
 
+def _scratch(t: torch.Tensor, stream):
+    """A workspace made for one call: kept from reuse until the work on `stream`
+    (if not the current one) is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 # ---------------------------------------------------------------- RMS norm
 def _need(t, name, shape, dtype):
     if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
@@ -767,7 +775,7 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: to
     _need(dx, "dx", (R, C), torch.bfloat16)
     _need(dw, "dw", (C,), torch.float32)
     if ws is None:
-        ws = rmsnorm_workspace(R, C, dy.device)
+        ws = _scratch(rmsnorm_workspace(R, C, dy.device), stream)
     _check(lib().fp8_rmsnorm_bwd(_ptr(dy), _ptr(dr), _ptr(r), _ptr(rstd), _ptr(w), _DTYPE[w.dtype],
                                  R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
            "fp8_rmsnorm_bwd")
@@ -850,7 +858,7 @@ def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act:
     N, K = x.shape
     F, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, train, x.device)
     if ws is None:
-        ws = gated_workspace(recipe, N, K, F, x.device, train=False)
+        ws = _scratch(gated_workspace(recipe, N, K, F, x.device, train=False), stream)
     _check(lib().fp8_gated_fwd(_ptr(x), N, K, cache.handle, h, RECIPE[recipe], ACTIVATION[act],
                                _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws), ws.numel(),
                                _stream(stream)), "fp8_gated_fwd")
@@ -891,7 +899,7 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
         _need(dx, "dx", (N, K), torch.bfloat16)
     _need(dw, "dw", (2 * F, K), torch.bfloat16)
     if ws is None:
-        ws = gated_workspace(recipe, N, K, F, dev)
+        ws = _scratch(gated_workspace(recipe, N, K, F, dev), stream)
     _check(lib().fp8_gated_bwd(_ptr(dh), N, F, _ptr(ctx.ctx), cache.handle, h, RECIPE[recipe],
                                ACTIVATION[ctx.act], _ptr(dx) if need_dx else None, _ptr(dw),
                                _ptr(ws), ws.numel(), _stream(stream)), "fp8_gated_bwd")

@@ -123,3 +123,132 @@ def test_example_runs(fp, capsys):
     from fp8_mixed_precision_gb300 import gated_mlp
     gated_mlp.main()
     assert "one token" in capsys.readouterr().out
+
+
+PDL_CHILD = r"""
+import hashlib
+import torch
+import fp8_mixed_precision_gb300 as fp
+from fp8_mixed_precision_gb300 import synthetic as syn
+from fp8_mixed_precision_gb300.gated_mlp import FP8GatedMLPStack
+
+h = hashlib.sha256()
+for recipe in ("block", "tensorwise"):
+    m = FP8GatedMLPStack(512, 1024, 2, 1040, recipe, max_norm=0.1)
+    xs = [syn.bf16_normal((1040, 512), 1.0, 42 + i, device="cuda") for i in range(2)]
+    dys = [syn.bf16_normal((1040, 512), 1e-2, 44 + i, device="cuda") for i in range(2)]
+    norm, grads = m.step(xs, dys)
+    m.load()
+    for t in [norm, *grads, m.decode(xs[0][:1]), m.decode(xs[0][:77])]:
+        h.update(t.contiguous().view(torch.uint8).cpu().numpy().tobytes())
+assert fp.fp8_get_device_status() == 0
+print(h.hexdigest())
+"""
+
+
+def test_overlapped_and_plain_launches_give_the_same_bytes(tmp_path):
+    """The launch mode is read once per process: two children, every kernel of
+    the step and of decoding."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    script = tmp_path / "child.py"
+    script.write_text(PDL_CHILD)
+    out = []
+    for pdl in ("0", "1"):
+        env = dict(os.environ, FP8LIN_PDL=pdl, PYTHONPATH=root + os.pathsep + os.environ.get("PYTHONPATH", ""))
+        r = subprocess.run([sys.executable, str(script)], cwd=root, env=env, capture_output=True, text=True,
+                           timeout=600)
+        assert r.returncode == 0, r.stderr[-2000:]
+        out.append(r.stdout.strip().splitlines()[-1])
+    assert out[0] == out[1]
+
+
+@pytest.mark.parametrize("recipe", ["block", "tensorwise"])
+def test_a_step_replays_from_a_graph(fp, recipe):
+    """Norm, gated feed-forward, linear and clipping captured in a CUDA graph and
+    replayed on new inputs equal the same calls made one by one."""
+    n, d, F = 160, 256, 384
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((n, d), generator=g).to(torch.bfloat16).cuda()
+    dy = (torch.randn((n, F), generator=g) * 1e-2).to(torch.bfloat16).cuda()
+    w = (torch.randn((2 * F, d), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    wn = torch.ones(d, device="cuda")
+    cache = fp.WeightCache()
+    h = cache.register(w, recipe)
+    cache.begin_cycle()
+    cache.get(h)
+    ctx = fp.gated_context(recipe, n, d, F, "cuda")
+    ws = fp.gated_workspace(recipe, n, d, F, "cuda")
+    buf = fp.rmsnorm_buffers(n, d, "cuda", residual=False, rowwise=False, colwise=False, bf16=True)
+    nws = fp.rmsnorm_workspace(n, d, "cuda")
+    y, dx, dw = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((n, F), (n, d), (2 * F, d)))
+    dxn, dwn = torch.empty_like(dx), torch.empty(d, device="cuda")
+    acc = [torch.empty_like(dw), torch.empty_like(dwn)]
+    clip = fp.GradClip([dw, dwn], acc)
+
+    def step():
+        o = fp.fp8_rmsnorm_fwd(x, wn, rowwise=False, colwise=False, bf16=True, out=buf)
+        fp.fp8_gated_fwd(o["y"], cache, h, recipe, ws=ws, y=y, ctx=ctx)
+        fp.fp8_gated_bwd(dy, ctx, cache, h, recipe, ws=ws, dx=dx, dw=dw)
+        fp.fp8_rmsnorm_bwd(dx, x, o["rstd"], wn, dx=dxn, dw=dwn, ws=nws)
+        clip.clip(0.01)
+
+    step()  # loads every kernel
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.copy_(torch.randn((n, d), generator=g).to(torch.bfloat16))
+    step()
+    want = [t.clone() for t in (y, dxn, *acc)]
+    for t in (y, dxn, *acc):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, (y, dxn, *acc)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("recipe", ["block", "tensorwise"])
+def test_calls_on_another_stream_keep_their_scratch(fp, recipe):
+    """Workspaces made inside a call on another stream are not handed to the
+    current stream's allocations while that call still runs."""
+    n, d, F = 700, 512, 640
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn((n, d), generator=g).to(torch.bfloat16).cuda()
+    dy = (torch.randn((n, F), generator=g) * 1e-2).to(torch.bfloat16).cuda()
+    w = (torch.randn((2 * F, d), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    wn = torch.ones(d, device="cuda")
+    rstd = torch.ones(n, device="cuda")
+    cache = fp.WeightCache()
+    h = cache.register(w, recipe)
+    cache.begin_cycle()
+    cache.get(h)
+
+    def calls(stream):
+        y, ctx = fp.fp8_gated_fwd(x, cache, h, recipe, stream=stream)
+        junk(stream)
+        dx, dw = fp.fp8_gated_bwd(dy, ctx, cache, h, recipe, stream=stream)
+        junk(stream)
+        dxn, dwn = fp.fp8_rmsnorm_bwd(dx, x, rstd, wn, stream=stream)
+        junk(stream)
+        keep.append(ctx)
+        return y, dx, dw, dxn, dwn
+
+    def junk(stream):
+        if stream is not None:  # what the current stream allocates next is written at once
+            for rows in (n, 4 * n, 16 * n):
+                torch.full((rows, 2 * d), float("nan"), dtype=torch.bfloat16, device="cuda")
+            stream.wait_stream(torch.cuda.current_stream())  # the next call's outputs may lie there
+
+    keep = []
+    want = calls(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        got = calls(s)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
