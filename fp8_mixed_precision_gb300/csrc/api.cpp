@@ -794,7 +794,8 @@ GatedWs gated_ws(fp8_recipe recipe, int64_t N, int64_t K, int64_t F) {
   Carver b(nullptr);
   const int64_t Np = round16(N);
   L.row = at(b, (size_t)N * 2 * F);
-  L.col = at(b, (size_t)Np * 2 * F);
+  // (tensorwise, the wgrad reads the row layout itself: gated.cu)
+  L.col = at(b, recipe == FP8_RECIPE_BLOCK ? (size_t)Np * 2 * F : 0);
   L.rsi = at(b, (size_t)scale_elems(ar, FP8_ROLE_GRAD, N, 2 * F, 0) * 4);
   L.csi = at(b, (size_t)scale_elems(ar, FP8_ROLE_GRAD, N, 2 * F, 1) * 4);
   L.bpart = at(b, part);
@@ -951,9 +952,10 @@ fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
                                cs(stream)));
     if (st != FP8_OK) return st;
   }
-  return from_cuda(launch_gemm(w + L.col, FP8_FORMAT_E5M2, csi, c + C.x.xq_col, FP8_FORMAT_E4M3,
-                               reinterpret_cast<const float *>(c + C.x.scale_inv), 2 * F, K,
-                               round16(N), wgrad_scaling(recipe), dW, w + L.gemm, cs(stream)));
+  return from_cuda(launch_gemm(w + (block ? L.col : L.row), FP8_FORMAT_E5M2, csi, c + C.x.xq_col,
+                               FP8_FORMAT_E4M3, reinterpret_cast<const float *>(c + C.x.scale_inv),
+                               2 * F, K, round16(N), wgrad_scaling(recipe), dW, w + L.gemm,
+                               cs(stream), block ? 0 : N));
 }
 
 // ---------------------------------------------------------------- gradient clipping

@@ -748,9 +748,8 @@ struct GatedBwd {
   const uint4 *dh, *g, *u;  // bf16 [N, F]
   int64_t N, F, ldn;        // ldn: tokens per row of the transposed layout (N rounded up to 16)
   uint8_t *row;             // E5M2 [N, 2F]
-  uint8_t *col;             // E5M2 [2F, ldn]
-  float *row_scale_inv, *col_scale_inv;  // block scaling
-  float *scale_inv;                      // tensor scaling (1)
+  uint8_t *col;             // E5M2 [2F, ldn] (block scaling)
+  float *row_scale_inv, *col_scale_inv;  // block scaling; tensor scaling: row_scale_inv (1)
   const float *partials;                 // tensor scaling: maxima of the first pass
   int n_partials;
 };
@@ -798,6 +797,70 @@ __global__ void __launch_bounds__(kAmaxThreads)
   }
 }
 
+// Eight products, each with its own scale, as E5M2.
+__device__ __forceinline__ uint2 cast8(const float (&x)[8], const float (&s)[8]) {
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) upk(mul2(pk(x[j], x[j + 1]), pk(s[j], s[j + 1])), y[j], y[j + 1]);
+  uint2 q;
+  q.x = cvt4_finite<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
+  q.y = cvt4_finite<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
+  return q;
+}
+
+// Tensor scaling, second pass: dG and dU formed again and cast with the one
+// scale, rows only; the wgrad GEMM reads them M-major, so no transposed copy is
+// made: 8 bytes an output of the forward pass instead of 10, and no shared memory
+// between (131072 x 2048: 309 us, 6.9 TB/s; both layouts from 128 x 128 tiles took
+// 404).  Last element first, where the first pass ended.  Memory is the bound:
+// requesting the next elements before the present ones are formed, 512 threads
+// and streaming stores change nothing, five CTAs per SM are slower (378).
+constexpr int kCastThreads = 256;
+template <int ACT>
+__global__ void __launch_bounds__(kCastThreads)
+    gated_bwd_cast_rows_kernel(const GatedBwd p) {
+  __shared__ float red[kCastThreads / 32];
+  __shared__ float scale;
+  pdl_wait_then_release();
+  const int t = threadIdx.x;
+  const int64_t f8 = p.F / 8, n8 = p.N * f8, stride = (int64_t)gridDim.x * kCastThreads;
+  int64_t at = n8 - 1 - ((int64_t)blockIdx.x * kCastThreads + t);
+  uint4 dh, g, u;
+  if (at >= 0) dh = p.dh[at], g = p.g[at], u = p.u[at];
+  float m = 0.0f;
+  for (int k = t; k < p.n_partials; k += kCastThreads) m = fmaxf(m, p.partials[k]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((t & 31) == 0) red[t >> 5] = m;
+  __syncthreads();
+  if (t == 0) {
+    for (int k = 1; k < kCastThreads / 32; ++k) m = fmaxf(m, red[k]);
+    float s, si;
+    scale_from_amax(m, kE5M2Max, s, si);
+    scale = s;
+    if (blockIdx.x == 0) p.row_scale_inv[0] = si;
+  }
+  __syncthreads();
+  float s8[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s8[j] = scale;
+  // row and column of element `at`, moved along by whole strides
+  int64_t r = at >= 0 ? at / f8 : 0, c = at >= 0 ? at % f8 : 0;
+  const int64_t dr = stride / f8, dc = stride % f8;
+  while (at >= 0) {
+    float dg[8], du[8];
+    dgu8<ACT>(dh, g, u, dg, du);
+    uint8_t *out = p.row + r * 2 * p.F + 8 * c;
+    *reinterpret_cast<uint2 *>(out) = cast8(dg, s8);
+    *reinterpret_cast<uint2 *>(out + p.F) = cast8(du, s8);
+    r -= dr;
+    c -= dc;
+    if (c < 0) c += f8, --r;
+    at -= stride;
+    if (at >= 0) dh = p.dh[at], g = p.g[at], u = p.u[at];
+  }
+}
+
 constexpr int kBwdThreads = 512;
 struct __align__(128) BSmem {
   uint16_t in[3][128 * 128];   // dH, G, U tiles (TMA destinations)
@@ -805,17 +868,15 @@ struct __align__(128) BSmem {
   float colred[16][2][128];    // per-warp column maxima
   float colsc[2][128];
   float rowsc[2][128];         // row maxima, then row scales
-  float red[16];
-  float tscale;
   uint64_t full;
 };
 
 __device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
 
-// One 128-token x 128-column tile of dH, G, U per iteration: dG and dU are
-// formed once, in registers, and leave as E5M2 in both layouts, each with its
-// own 1x128 blocks (block scaling) or one scale (tensor scaling).
-template <bool BLOCK, int ACT>
+// Block scaling: one 128-token x 128-column tile of dH, G, U per iteration; dG
+// and dU are formed once, in registers, and leave as E5M2 in both layouts, each
+// with its own 1x128 blocks.  F is a multiple of 128.
+template <int ACT>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     gated_bwd_cast_kernel(const __grid_constant__ CUtensorMap tmD,
                           const __grid_constant__ CUtensorMap tmG,
@@ -824,7 +885,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   BSmem &S = *reinterpret_cast<BSmem *>(b_smem_raw);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int cg = t & 15, rr = t >> 4;  // 8 columns, rows rr + 32 i
-  const int64_t tiles_r = (p.N + 127) / 128, tiles_c = (p.F + 127) / 128;
+  const int64_t tiles_r = (p.N + 127) / 128, tiles_c = p.F / 128;
   const int64_t ntiles = tiles_r * tiles_c;
   const int64_t F2 = 2 * p.F;
   if (t == 0) {
@@ -838,8 +899,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   pdl_wait_then_release();
   auto prefetch = [&](int64_t id) {
     if (t != 0 || id >= ntiles) return;
-    const int64_t at = BLOCK ? id : ntiles - 1 - id;
-    const int x = (int)(at % tiles_c) * 128, y = (int)(at / tiles_c) * 128;
+    const int x = (int)(id % tiles_c) * 128, y = (int)(id / tiles_c) * 128;
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive_expect_tx(&S.full, 3u * 128 * 128 * 2);
     ptx::tma_load_2d(S.in[0], &tmD, &S.full, x, y);
@@ -848,33 +908,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   int64_t id = blockIdx.x;
   prefetch(id);
-  float ts = 1.0f;
-  if constexpr (!BLOCK) {
-    float m = 0.0f;
-    for (int k = t; k < p.n_partials; k += kBwdThreads) m = fmaxf(m, p.partials[k]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) S.red[warp] = m;
-    __syncthreads();
-    if (t == 0) {
-      for (int k = 1; k < 16; ++k) m = fmaxf(m, S.red[k]);
-      float s, si;
-      scale_from_amax(m, kE5M2Max, s, si);
-      S.tscale = s;
-      if (blockIdx.x == 0) p.scale_inv[0] = si;
-    }
-    __syncthreads();
-    ts = S.tscale;
-  }
   volatile int no_abort = 0;
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
-    // tensor scaling: last tile first, where the maximum's pass ended
-    const int64_t at = BLOCK ? id : ntiles - 1 - id;
-    const int64_t tr = at / tiles_c, tc = at % tiles_c;
+    const int64_t tr = id / tiles_c, tc = id % tiles_c;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int rows_here = (int)(p.N - r0 < 128 ? p.N - r0 : 128);
-    const int cols_here = (int)(p.F - c0 < 128 ? p.F - c0 : 128);
-    const bool col_ok = 8 * cg < cols_here;
     pipe::wait_bar(&S.full, k & 1, &no_abort, &g_gated_status);  // on expiry: recorded, carry on
     uint4 in[3][4];  // dH, G, U of this thread's 4 rows
 #pragma unroll
@@ -882,92 +920,74 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
       for (int k3 = 0; k3 < 3; ++k3)
         in[k3][i] = *reinterpret_cast<const uint4 *>(&S.in[k3][(rr + 32 * i) * 128 + 8 * cg]);
-    // dG and dU are formed after the next tile has been requested where memory
-    // is the bound (tensor scaling, 131072 x 2048: 404 us, before it 435), and
-    // before where the arithmetic is (block scaling, 16384 x 14336: 502 / 519)
+    // formed before the next tile is requested: the arithmetic is the bound
+    // (16384 x 14336: 502 us, after it 519)
     float v[2][4][8];  // [dG, dU][row][column]
-    auto form = [&] {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dgu8<ACT>(in[0][i], in[1][i], in[2][i], v[0][i], v[1][i]);
-    };
-    if (BLOCK) form();
+    for (int i = 0; i < 4; ++i) dgu8<ACT>(in[0][i], in[1][i], in[2][i], v[0][i], v[1][i]);
     __syncthreads();  // the buffers are read, and the last tile's transpose too
     prefetch(id + gridDim.x);
-    if (!BLOCK) form();
-    if constexpr (BLOCK) {
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        float cm[8] = {};
+    for (int z = 0; z < 2; ++z) {
+      float cm[8] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float m = 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        float m = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            m = amax_acc(m, v[z][i][j]);
-            cm[j] = amax_acc(cm[j], v[z][i][j]);
-          }
-#pragma unroll
-          for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (cg == 0) S.rowsc[z][rr + 32 * i] = m;
+        for (int j = 0; j < 8; ++j) {
+          m = amax_acc(m, v[z][i][j]);
+          cm[j] = amax_acc(cm[j], v[z][i][j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
-        if (lane < 16) {
-          float4 *dst = reinterpret_cast<float4 *>(&S.colred[warp][z][8 * cg]);
-          dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
-          dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
-        }
+        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (cg == 0) S.rowsc[z][rr + 32 * i] = m;
       }
-      __syncthreads();
-      {  // one scale per thread: rows of dG, rows of dU, columns of dG, columns of dU
-        const int z = (t >> 7) & 1, c = t & 127;
-        float m, s, si;
-        if (t < 256) {
-          m = S.rowsc[z][c];
-        } else {
-          m = 0.0f;
 #pragma unroll
-          for (int w = 0; w < 16; ++w) m = fmaxf(m, S.colred[w][z][c]);
-        }
-        scale_from_amax(m, kE5M2Max, s, si);
-        if (t < 256) {
-          S.rowsc[z][c] = s;
-          if (c < rows_here) p.row_scale_inv[(r0 + c) * (2 * tiles_c) + z * tiles_c + tc] = si;
-        } else {
-          S.colsc[z][c] = s;
-          if (c < cols_here) p.col_scale_inv[(z * p.F + c0 + c) * tiles_r + tr] = si;
-        }
+      for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+      if (lane < 16) {
+        float4 *dst = reinterpret_cast<float4 *>(&S.colred[warp][z][8 * cg]);
+        dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
+        dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
       }
-      __syncthreads();
     }
-    auto cast8 = [&](const float(&x)[8], const float(&s)[8]) {
-      float y[8];
+    __syncthreads();
+    {  // one scale per thread: rows of dG, rows of dU, columns of dG, columns of dU
+      const int z = (t >> 7) & 1, c = t & 127;
+      float m, s, si;
+      if (t < 256) {
+        m = S.rowsc[z][c];
+      } else {
+        m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) upk(mul2(pk(x[j], x[j + 1]), pk(s[j], s[j + 1])), y[j], y[j + 1]);
-      uint2 q;
-      q.x = cvt4_finite<FP8_FORMAT_E5M2>(y[0], y[1], y[2], y[3]);
-      q.y = cvt4_finite<FP8_FORMAT_E5M2>(y[4], y[5], y[6], y[7]);
-      return q;
-    };
+        for (int w = 0; w < 16; ++w) m = fmaxf(m, S.colred[w][z][c]);
+      }
+      scale_from_amax(m, kE5M2Max, s, si);
+      if (t < 256) {
+        S.rowsc[z][c] = s;
+        if (c < rows_here) p.row_scale_inv[(r0 + c) * (2 * tiles_c) + z * tiles_c + tc] = si;
+      } else {
+        S.colsc[z][c] = s;
+        p.col_scale_inv[(z * p.F + c0 + c) * tiles_r + tr] = si;
+      }
+    }
+    __syncthreads();
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       float cs[8], rs[8];
-      if (BLOCK) {
-        const float4 *c4 = reinterpret_cast<const float4 *>(&S.colsc[z][8 * cg]);
-        const float4 x = c4[0], y = c4[1];
-        cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
-        cs[4] = y.x; cs[5] = y.y; cs[6] = y.z; cs[7] = y.w;
-      }
+      const float4 *c4 = reinterpret_cast<const float4 *>(&S.colsc[z][8 * cg]);
+      const float4 x = c4[0], y = c4[1];
+      cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
+      cs[4] = y.x; cs[5] = y.y; cs[6] = y.z; cs[7] = y.w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = rr + 32 * i;
-        const float s = BLOCK ? S.rowsc[z][r] : ts;
+        const float s = S.rowsc[z][r];
 #pragma unroll
         for (int j = 0; j < 8; ++j) rs[j] = s;
         uint2 q = cast8(v[z][i], rs);
-        if (col_ok && r < rows_here)
+        if (r < rows_here)
           *reinterpret_cast<uint2 *>(p.row + (r0 + r) * F2 + z * p.F + c0 + 8 * cg) = q;
-        if (BLOCK) q = cast8(v[z][i], cs);
+        q = cast8(v[z][i], cs);
         *reinterpret_cast<uint2 *>(&S.tile[z][r * 32 + ((2 * cg) ^ swz(r))]) = q;
       }
     }
@@ -975,7 +995,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     {
       // tokens past N are zeros (the TMA load's fill, and dH = 0 gives 0 there)
       const int z = t >> 8, seg = t & 7, w = (t >> 3) & 31;
-      if (4 * w < cols_here && 16 * seg < rows_here) {
+      if (16 * seg < rows_here) {
         uint32_t a[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -1073,17 +1093,47 @@ cudaError_t launch_small_nt(const uint8_t *xq, const uint8_t *wq, int64_t K, con
   return launch_small<SCALING, ACT, 64>(xq, wq, K, a, st);
 }
 
-template <bool BLOCK, int ACT>
-cudaError_t launch_cast(const CUtensorMap (&m)[3], const GatedBwd &p, cudaStream_t st) {
+template <int ACT>
+cudaError_t launch_cast_block(const GatedBwd &p, cudaStream_t st) {
+  CUtensorMap m[3];
+  if (!make_bf16_tile_map(&m[0], p.dh, p.N, p.F, 128, 128) ||
+      !make_bf16_tile_map(&m[1], p.g, p.N, p.F, 128, 128) ||
+      !make_bf16_tile_map(&m[2], p.u, p.N, p.F, 128, 128))
+    return cudaErrorInvalidValue;
   static bool done[64];
-  const cudaError_t e = opt_in_smem(gated_bwd_cast_kernel<BLOCK, ACT>, sizeof(BSmem), done);
+  const cudaError_t e = opt_in_smem(gated_bwd_cast_kernel<ACT>, sizeof(BSmem), done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((p.N + 127) / 128) * ((p.F + 127) / 128);
+  const int64_t tiles = ((p.N + 127) / 128) * (p.F / 128);
   const int64_t grid = std::min<int64_t>(tiles, num_sms());
-  LaunchScope ls(BLOCK ? "gated_bwd_cast_block" : "gated_bwd_cast_tensor", st, 10.0 * p.N * p.F, 0.0,
-                 p.N, p.F);
-  return launch_kernel(gated_bwd_cast_kernel<BLOCK, ACT>, dim3((unsigned)grid), dim3(kBwdThreads),
+  LaunchScope ls("gated_bwd_cast_block", st, 10.0 * p.N * p.F, 0.0, p.N, p.F);
+  return launch_kernel(gated_bwd_cast_kernel<ACT>, dim3((unsigned)grid), dim3(kBwdThreads),
                        sizeof(BSmem), st, m[0], m[1], m[2], p);
+}
+
+// A grid of the kernel's resident CTAs, or as many as n8 vectors fill.
+template <typename Kernel>
+int64_t vector_grid(Kernel kernel, int threads, int64_t n8, int *bps) {
+  const int64_t resident = (int64_t)blocks_per_sm(kernel, threads, bps) * num_sms();
+  return std::max<int64_t>(1, std::min<int64_t>((n8 + threads - 1) / threads, resident));
+}
+
+template <int ACT>
+cudaError_t launch_cast_tensor(GatedBwd p, float *partials, cudaStream_t st) {
+  const int64_t n8 = p.N * p.F / 8;
+  static int amax_bps[64], cast_bps[64];
+  p.n_partials = (int)std::min<int64_t>(
+      vector_grid(gated_bwd_amax_kernel<ACT>, kAmaxThreads, n8, amax_bps), kMaxPartials);
+  {
+    LaunchScope ls("gated_bwd_amax", st, 6.0 * p.N * p.F, 0.0, p.N, p.F);
+    const cudaError_t e = launch_kernel(gated_bwd_amax_kernel<ACT>, dim3((unsigned)p.n_partials),
+                                        dim3(kAmaxThreads), 0, st, p.dh, p.g, p.u, n8, partials);
+    if (e != cudaSuccess) return e;
+  }
+  p.partials = partials;
+  const int64_t grid = vector_grid(gated_bwd_cast_rows_kernel<ACT>, kCastThreads, n8, cast_bps);
+  LaunchScope ls("gated_bwd_cast_tensor", st, 8.0 * p.N * p.F, 0.0, p.N, p.F);
+  return launch_kernel(gated_bwd_cast_rows_kernel<ACT>, dim3((unsigned)grid), dim3(kCastThreads), 0, st,
+                       p);
 }
 
 }  // namespace
@@ -1098,7 +1148,7 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
   // half the SMs: chunks of 64 tokens and the split of K put more of them to
   // work, the weight coming from L2 for all chunks but the first (us a pass,
   // here / 128-token tiles: 100 tokens, K 4096, F 256: 11.5 / 19.4; 1000, 4096,
-  // 512: 19.6 / 21.4; below K = 3072 the tiles win, 256, 1024, 2048: 12.1 / 10.0)
+  // 512: 19.6 / 21.4; in shallower ones the tiles win, 256, 1024, 2048: 12.1 / 10.0)
   if (N <= kSmallTokens || ((N + BM - 1) / BM * tiles * 2 <= num_sms() && K >= 24 * BK)) {
     SmallArgs a = {};
     a.N = N;
@@ -1179,32 +1229,14 @@ cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void 
                                       int64_t F, bool block, int act, uint8_t *row, uint8_t *col,
                                       float *row_scale_inv, float *col_scale_inv, float *partials,
                                       cudaStream_t st) {
-  CUtensorMap m[3];
-  if (!make_bf16_tile_map(&m[0], dH, N, F, 128, 128) || !make_bf16_tile_map(&m[1], G, N, F, 128, 128) ||
-      !make_bf16_tile_map(&m[2], U, N, F, 128, 128))
-    return cudaErrorInvalidValue;
-  GatedBwd p{static_cast<const uint4 *>(dH), static_cast<const uint4 *>(G),
-             static_cast<const uint4 *>(U), N, F, (N + 15) / 16 * 16, row, col, row_scale_inv,
-             col_scale_inv, row_scale_inv, partials, 0};
+  const GatedBwd p{static_cast<const uint4 *>(dH), static_cast<const uint4 *>(G),
+                   static_cast<const uint4 *>(U), N, F, (N + 15) / 16 * 16, row, col, row_scale_inv,
+                   col_scale_inv, nullptr, 0};
   if (block)
-    return act == FP8_ACT_SILU ? launch_cast<true, FP8_ACT_SILU>(m, p, st)
-                               : launch_cast<true, FP8_ACT_GELU>(m, p, st);
-  const int64_t n8 = N * F / 8;
-  static int bps[2][64];
-  const int i = act == FP8_ACT_SILU ? 0 : 1;
-  auto kernel = i == 0 ? gated_bwd_amax_kernel<FP8_ACT_SILU> : gated_bwd_amax_kernel<FP8_ACT_GELU>;
-  const int64_t resident = (int64_t)blocks_per_sm(kernel, kAmaxThreads, bps[i]) * num_sms();
-  p.n_partials = (int)std::max<int64_t>(
-      1, std::min<int64_t>({(n8 + kAmaxThreads - 1) / kAmaxThreads, resident, kMaxPartials}));
-  {
-    LaunchScope ls("gated_bwd_amax", st, 6.0 * N * F, 0.0, N, F);
-    const cudaError_t e =
-        launch_kernel(kernel, dim3((unsigned)p.n_partials), dim3(kAmaxThreads), 0, st, p.dh, p.g, p.u,
-                      n8, partials);
-    if (e != cudaSuccess) return e;
-  }
-  return act == FP8_ACT_SILU ? launch_cast<false, FP8_ACT_SILU>(m, p, st)
-                             : launch_cast<false, FP8_ACT_GELU>(m, p, st);
+    return act == FP8_ACT_SILU ? launch_cast_block<FP8_ACT_SILU>(p, st)
+                               : launch_cast_block<FP8_ACT_GELU>(p, st);
+  return act == FP8_ACT_SILU ? launch_cast_tensor<FP8_ACT_SILU>(p, partials, st)
+                             : launch_cast_tensor<FP8_ACT_GELU>(p, partials, st);
 }
 
 cudaError_t gated_read_status(unsigned *status) {

@@ -299,7 +299,10 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <int SCALING, bool SPLIT, int BN, int MH, bool PR>
+// AM: A is given M-contiguous, as [K, M] rows.  A stage then holds 128 rows of
+// K with 128 bytes along M each (one swizzle atom wide per M half), and the
+// MMA's instruction descriptor names A as M-major.
+template <int SCALING, bool SPLIT, int BN, int MH, bool PR, bool AM>
 __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const GemmArgs g) {
@@ -307,6 +310,9 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
   static_assert(MH == 1 || SCALING == FP8_SCALING_TENSOR, "M halves: tensor scaling only");
   static_assert(!PR || (SCALING == FP8_SCALING_TENSOR && BN == 256),
                 "CTA pairs: tensor scaling, 256-wide tiles");
+  static_assert(!AM || SCALING == FP8_SCALING_TENSOR, "M-contiguous A: tensor scaling only");
+  // start-address advance of A per 32-deep MMA: 32 bytes along K, or 32 rows
+  constexpr uint64_t kStepA = AM ? 32 * 128 / 16 : 2;
   // PR: a cluster of two CTAs computes a (2 * MH * 128) x BN tile with
   // cta_group::2 MMAs issued by rank 0 (the leader), one M = 256 MMA per M
   // half taking 128 rows from each CTA.  Each CTA loads its MH x 128 rows of A
@@ -460,7 +466,8 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
             const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&ctl->full[stage]), 0);
             if (leader) ptx::mbar_arrive_expect_tx(&ctl->full[stage], 2u * C::kStageBytes);
             for (int mh = 0; mh < MH; ++mh)  // rows past M (or wholly outside) read as zeros
-              ptx::tma_load_2d_pair(sa + mh * BM * BK, &tmA, fb, kb * BK, (tm * MH + mh) * BM);
+              ptx::tma_load_2d_pair(sa + mh * BM * BK, &tmA, fb, AM ? (tm * MH + mh) * BM : kb * BK,
+                                    AM ? kb * BK : (tm * MH + mh) * BM);
             ptx::tma_load_2d_pair(sa + C::kStageA, &tmB, fb, kb * BK,
                                   tn * BN + (int)rank * (BN / 2));
             last_phase[stage] = (int)phase;
@@ -474,8 +481,9 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
           ptx::mbar_arrive_expect_tx(&ctl->full[stage],
                                      (uint32_t)(C::kStageBytes - (MH - halves) * BM * BK));
           for (int mh = 0; mh < halves; ++mh)
-            ptx::tma_load_2d(sa + mh * BM * BK, &tmA, &ctl->full[stage], kb * BK,
-                             (int)(row0 + mh * BM));
+            ptx::tma_load_2d(sa + mh * BM * BK, &tmA, &ctl->full[stage],
+                             AM ? (int)(row0 + mh * BM) : kb * BK,
+                             AM ? kb * BK : (int)(row0 + mh * BM));
           ptx::tma_load_2d(sa + C::kStageA, &tmB, &ctl->full[stage], kb * BK, tn * BN);
           last_phase[stage] = (int)phase;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -518,10 +526,10 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
               const uint32_t d = tmem + ((nacc + mh) % NB) * BN;
               const uint64_t adesc = ptx::smem_desc_sw128(a_addr + mh * BM * BK);
               if (PR)
-                ptx::mma_f8f6f4_pair(d, adesc + 2 * k, bdesc + 2 * k, g.idesc,
+                ptx::mma_f8f6f4_pair(d, adesc + kStepA * k, bdesc + 2 * k, g.idesc,
                                      (!first || k > 0) ? 1u : 0u);
               else
-                ptx::mma_f8f6f4(d, adesc + 2 * k, bdesc + 2 * k, g.idesc,
+                ptx::mma_f8f6f4(d, adesc + kStepA * k, bdesc + 2 * k, g.idesc,
                                 (!first || k > 0) ? 1u : 0u);
             }
           if (PR)
@@ -1108,12 +1116,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int scaling) {
   return p;
 }
 
-template <int SCALING, bool SPLIT, int BN, int MH = 1, bool PR = false>
+template <int SCALING, bool SPLIT, int BN, int MH, bool PR, bool AM>
 cudaError_t launch_variant(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc,
                            const GemmArgs &g, cudaStream_t st) {
   using C = Cfg<SCALING, SPLIT, BN, MH, PR>;
   constexpr int kCl = PR ? 2 : 1;  // CTAs per cluster
-  auto kernel = fp8_gemm_kernel<SCALING, SPLIT, BN, MH, PR>;
+  auto kernel = fp8_gemm_kernel<SCALING, SPLIT, BN, MH, PR, AM>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1169,28 +1177,28 @@ cudaError_t launch_variant(const CUtensorMap &ta, const CUtensorMap &tb, const C
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, tc, g);
 }
 
-template <int SCALING>
+template <int SCALING, bool AM = false>
 cudaError_t launch_scaling(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc,
                            const GemmArgs &g, bool split, int bn, int mh, int pr,
                            cudaStream_t st) {
   if constexpr (SCALING == FP8_SCALING_TENSOR) {
     if (bn == 256 && mh == 2 && pr)
-      return split ? launch_variant<SCALING, true, 256, 2, true>(ta, tb, tc, g, st)
-                   : launch_variant<SCALING, false, 256, 2, true>(ta, tb, tc, g, st);
+      return split ? launch_variant<SCALING, true, 256, 2, true, AM>(ta, tb, tc, g, st)
+                   : launch_variant<SCALING, false, 256, 2, true, AM>(ta, tb, tc, g, st);
     if (bn == 256 && mh == 2)
-      return split ? launch_variant<SCALING, true, 256, 2>(ta, tb, tc, g, st)
-                   : launch_variant<SCALING, false, 256, 2>(ta, tb, tc, g, st);
+      return split ? launch_variant<SCALING, true, 256, 2, false, AM>(ta, tb, tc, g, st)
+                   : launch_variant<SCALING, false, 256, 2, false, AM>(ta, tb, tc, g, st);
   }
   if constexpr (SCALING == FP8_SCALING_1x128_1x128) {
     if (bn == kWideBN)
-      return split ? launch_variant<SCALING, true, kWideBN>(ta, tb, tc, g, st)
-                   : launch_variant<SCALING, false, kWideBN>(ta, tb, tc, g, st);
+      return split ? launch_variant<SCALING, true, kWideBN, 1, false, AM>(ta, tb, tc, g, st)
+                   : launch_variant<SCALING, false, kWideBN, 1, false, AM>(ta, tb, tc, g, st);
   } else if (bn == 256) {
-    return split ? launch_variant<SCALING, true, 256>(ta, tb, tc, g, st)
-                 : launch_variant<SCALING, false, 256>(ta, tb, tc, g, st);
+    return split ? launch_variant<SCALING, true, 256, 1, false, AM>(ta, tb, tc, g, st)
+                 : launch_variant<SCALING, false, 256, 1, false, AM>(ta, tb, tc, g, st);
   }
-  return split ? launch_variant<SCALING, true, 128>(ta, tb, tc, g, st)
-               : launch_variant<SCALING, false, 128>(ta, tb, tc, g, st);
+  return split ? launch_variant<SCALING, true, 128, 1, false, AM>(ta, tb, tc, g, st)
+               : launch_variant<SCALING, false, 128, 1, false, AM>(ta, tb, tc, g, st);
 }
 
 }  // namespace
@@ -1223,13 +1231,15 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int scaling) {
 
 cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const uint8_t *B,
                         int b_fmt, const float *b_sinv, int64_t M, int64_t N, int64_t K,
-                        int scaling, void *Cout, void *ws, cudaStream_t st) {
+                        int scaling, void *Cout, void *ws, cudaStream_t st, int64_t a_rows) {
   if (M == 0 || N == 0) return cudaSuccess;
   if (K == 0) return cudaMemsetAsync(Cout, 0, (size_t)M * N * 2, st);
   const Plan p = make_plan(M, N, K, scaling);
   CUtensorMap ta, tb, tc;
   // a CTA pair loads the B tile as two halves of bn / 2 rows
-  if (!make_map(&ta, A, M, K, BM) || !make_map(&tb, B, N, K, p.pr ? p.bn / 2 : p.bn))
+  // M-contiguous A: rows of K, those past a_rows read as zeros
+  if (!(a_rows ? make_map(&ta, A, a_rows, M, BK) : make_map(&ta, A, M, K, BM)) ||
+      !make_map(&tb, B, N, K, p.pr ? p.bn / 2 : p.bn))
     return cudaErrorInvalidValue;
   if (p.splits == 1 && !(scaling == FP8_SCALING_1x128_1x128 && p.bn == kWideBN)) {
     // the 128-wide 1x128 x 1x128 kernel's epilogue warps own 32 columns each
@@ -1254,7 +1264,8 @@ cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const 
   g.lds_a = p.kbs;
   g.lds_b = p.kbs;
   g.out = p.splits > 1 ? ws : Cout;
-  g.idesc = ptx::idesc_f8f6f4((uint32_t)a_fmt, (uint32_t)b_fmt, p.pr ? 2 * BM : BM, (uint32_t)p.bn);
+  g.idesc = ptx::idesc_f8f6f4((uint32_t)a_fmt, (uint32_t)b_fmt, p.pr ? 2 * BM : BM, (uint32_t)p.bn,
+                             a_rows != 0);
   g.vec4 = (p.kbs % 4 == 0) && (reinterpret_cast<uintptr_t>(a_sinv) % 16 == 0) &&
            (reinterpret_cast<uintptr_t>(b_sinv) % 16 == 0);
   // Wide 1x128 x 1x128 tiles stream both operands per 128-deep K block for
@@ -1272,7 +1283,9 @@ cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const 
   cudaError_t e;
   switch (scaling) {
     case FP8_SCALING_TENSOR:
-      e = launch_scaling<FP8_SCALING_TENSOR>(ta, tb, tc, g, split, p.bn, p.mh, p.pr, st);
+      e = a_rows
+              ? launch_scaling<FP8_SCALING_TENSOR, true>(ta, tb, tc, g, split, p.bn, p.mh, p.pr, st)
+              : launch_scaling<FP8_SCALING_TENSOR>(ta, tb, tc, g, split, p.bn, p.mh, p.pr, st);
       break;
     case FP8_SCALING_1x128_128x128:
       e = launch_scaling<FP8_SCALING_1x128_128x128>(ta, tb, tc, g, split, p.bn, p.mh, p.pr, st);

@@ -122,11 +122,12 @@ bool make_bf16_tile_map(CUtensorMap *m, const void *base, int64_t rows, int64_t 
 cudaError_t quant_read_status(unsigned *status);
 
 // FP8 GEMM (tcgen05).  scaling: fp8_scaling.  ws may be null when
-// gemm_workspace_bytes() is 0.
+// gemm_workspace_bytes() is 0.  a_rows != 0 (tensor scaling only): A is given
+// transposed, [a_rows, M] with M contiguous, and is zero from row a_rows to K.
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int scaling);
 cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const uint8_t *B,
                         int b_fmt, const float *b_sinv, int64_t M, int64_t N, int64_t K,
-                        int scaling, void *C, void *ws, cudaStream_t st);
+                        int scaling, void *C, void *ws, cudaStream_t st, int64_t a_rows = 0);
 // Launches the bounded-wait probe (a wait nobody satisfies; limit_ns <= 1 s).
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, cudaStream_t st);
 // Reads and clears the GEMM kernels' device status word (0 = ok).

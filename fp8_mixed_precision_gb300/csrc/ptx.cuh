@@ -360,7 +360,10 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
 // hold the fixed descriptor version 0b001; bits 61-63 the swizzle mode
 // (2 = 128-byte swizzle).  The tile base must be 1024-byte aligned (matrix
 // base offset 0); advancing along K inside the 128-byte row adds the byte
-// offset to the start address.
+// offset to the start address.  An M-major operand 128 bytes wide has the same
+// descriptor: its 8-row groups of 1024 bytes are stacked along K (stride byte
+// offset), and the leading byte offset, the step to the next 128 bytes along M,
+// is not used; advancing along K adds 128 bytes per row.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFF) >> 4);  // start address
@@ -371,12 +374,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   return d;
 }
 
-// Instruction descriptor for kind::f8f6f4, fp32 accumulator, both operands
-// K-major, dense: [4,6) D format (1 = f32), [7,10) A format, [10,13) B format
-// (0 = E4M3, 1 = E5M2), [17,23) N >> 3, [24,29) M >> 4.
+// Instruction descriptor for kind::f8f6f4, fp32 accumulator, dense: [4,6) D
+// format (1 = f32), [7,10) A format, [10,13) B format (0 = E4M3, 1 = E5M2),
+// [15] A is M-major (otherwise K-major, as B is), [17,23) N >> 3, [24,29) M >> 4.
 __host__ __device__ constexpr uint32_t idesc_f8f6f4(uint32_t a_fmt, uint32_t b_fmt, uint32_t M,
-                                                    uint32_t N) {
-  return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+                                                    uint32_t N, bool a_m_major = false) {
+  return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | ((uint32_t)a_m_major << 15) | ((N >> 3) << 17) |
+         ((M >> 4) << 24);
 }
 
 }  // namespace ptx

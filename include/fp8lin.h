@@ -402,8 +402,8 @@ fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const 
  *   from fp8_rmsnorm_fwd); with ctx the caller has already filled its transposed
  *   part (fp8_gated_ctx_layout says where).
  * fp8_gated_bwd: with G and U as the forward pass kept them (bf16),
- *   dG = (dH * U) * act'(G), dU = dH * act(G) in fp32, cast to E5M2 in both
- *   layouts as one [N, 2F] tensor; dX = dGU W (or NULL), dW = dGU^T X [2F, K],
+ *   dG = (dH * U) * act'(G), dU = dH * act(G) in fp32, cast to E5M2 as one
+ *   [N, 2F] tensor (block recipe: in both layouts, each with its own blocks); dX = dGU W (or NULL), dW = dGU^T X [2F, K],
  *   the forward's rounded W and X reused (bf16; dW zeros when N = 0).
  * act: silu(g) = g / (1 + e^-g), or GELU in its exact erf form.
  * Weight-cache and recipe rules as fp8_linear_fwd / bwd (delayed recipe: its

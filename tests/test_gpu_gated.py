@@ -282,3 +282,28 @@ def test_few_token_quantizer_equals_the_quantizer(fp, recipe, N, K):
     off = p[2].value - ctx.ctx.data_ptr()
     si = q["col_scale_inv"]
     assert torch.equal(ctx.ctx[off:off + 4 * si.numel()].view(torch.float32).view(si.shape), si)
+
+
+@pytest.mark.parametrize("N,K,F", [(1, 16, 16), (65, 128, 272), (5000, 128, 272), (555, 272, 128), (2003, 352, 176),
+                                   (2217, 800, 2624), (10556, 272, 2960), (8246, 816, 2736), (23795, 288, 2560)])
+def test_weight_gradient_from_the_row_layout(fp, N, K, F):
+    """Tensor scaling keeps dGU in rows only: the product that reads them
+    M-major equals, bit for bit, the GEMM on a transposed copy.  The sizes take
+    every tile shape of the GEMM, with and without a split of the tokens."""
+    x, w, dh, cache, h = _case(fp, N, K, F, "tensorwise", 11)
+    y, ctx = fp.fp8_gated_fwd(x, cache, h, "tensorwise")
+    ws = fp.gated_workspace("tensorwise", N, K, F, "cuda")
+    ws.fill_(0xFF)
+    dx, dw = fp.fp8_gated_bwd(dh, ctx, cache, h, "tensorwise", ws=ws)
+    Np = (N + 15) // 16 * 16
+    # the workspace begins with the rows, their scale_inv follows
+    rows = N * 2 * F
+    a = torch.zeros((2 * F, Np), dtype=torch.uint8, device="cuda")
+    a[:, :N] = ws[:rows].view(N, 2 * F).t()
+    sa = ws[-(-rows // 256) * 256:][:4].view(torch.float32)
+    p = fp.fp8_gated_ctx_layout("tensorwise", ctx)
+    off, sb = p[0].value - ctx.ctx.data_ptr(), p[2].value - ctx.ctx.data_ptr()
+    xt = ctx.ctx[off:off + K * Np].view(K, Np)
+    want = fp.fp8_gemm(a, "e5m2", sa, xt, "e4m3", ctx.ctx[sb:sb + 4].view(torch.float32), "tensor")
+    assert torch.equal(dw, want)
+    assert fp.fp8_get_device_status() == 0
