@@ -982,7 +982,8 @@ fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_g
   // 32768 elements, so that small sets still spread over the CTAs and large
   // ones take many short turns.
   const int64_t chunk = std::min<int64_t>(
-      32768, std::max<int64_t>(2048, ((int64_t)(elements / 608.0) + 2047) / 2048 * 2048));
+      32768, std::max<int64_t>(kClipChunkMin, ((int64_t)(elements / 608.0) + kClipChunkMin - 1) /
+                                                  kClipChunkMin * kClipChunkMin));
   try {
     auto p = std::make_unique<fp8_grad_clip>();
     p->elements = elements;

@@ -183,6 +183,8 @@ struct ClipChunk {
   int32_t n;    // elements
   int32_t f32;  // 1: fp32, 0: bf16
 };
+constexpr int kClipChunkMin = 2048;  // elements; sets of few chunks have chunks of this size
+constexpr int kClipFewChunks = 16;   // up to here one launch does it (clip_few_kernel)
 int clip_ctas(int64_t chunks);  // partial sums the first pass writes
 // write = false: the norm alone.
 cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,

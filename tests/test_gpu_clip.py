@@ -2,7 +2,7 @@
 
 Tolerances, with u = 2^-24: a thread adds at most 4096 squares in a row into
 four sums (a chain of 1100 at most here), then 5 shuffle steps, 16 warps and
-an fp64 sum; the root halves the relative error: norm within 600 u.  coef adds
+a sum of fp32 pairs; the root halves the relative error: norm within 600 u.  coef adds
 three roundings, a product one, and a bf16 result its own 2^-8 (8 significand bits).
 """
 import math
@@ -112,3 +112,31 @@ def test_refusals(fp):
     for bad in (0.0, -1.0, float("nan")):
         with pytest.raises(fp.FP8Error):
             c.clip(bad)
+
+
+@pytest.mark.parametrize("n", [100, 200_000])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 1e30])
+def test_nonfinite_norm_keeps_its_kind(fp, n, bad):
+    """One kernel for small sets, two for larger ones: an infinite sum (1e30
+    squared among them) gives an infinite norm, a NaN gives a NaN."""
+    grads = _grads([n, 33], [torch.float32])
+    grads[0][n // 2] = bad
+    norm, out = fp.GradClip(grads, [torch.empty_like(g) for g in grads]).clip(0.5)
+    assert math.isnan(float(norm)) if math.isnan(bad) else float(norm) == math.inf
+    for a, b in zip(out, grads):
+        assert torch.equal(a.nan_to_num(1.0), b.nan_to_num(1.0))
+
+
+@pytest.mark.parametrize("count", [1, 15, 16, 17, 40])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_sets_at_any_alignment(fp, count, dtype):
+    base = _grads([count * 2100], [dtype])[0]
+    src = [base[i * 2100 + i % 9:][:1 + (i * 293) % 2048] for i in range(count)]
+    buf = torch.zeros(count * 2100, dtype=dtype, device="cuda")
+    out = [buf[i * 2100 + i % 9:][:s.numel()] for i, s in enumerate(src)]
+    norm, got = fp.GradClip(src, out).clip(0.01)
+    _check(norm, got, src, 0.01)
+    keep = buf.clone()
+    for o in out:
+        o.zero_()
+    assert int(buf.count_nonzero()) == 0 and int(keep.count_nonzero()) > 0  # nothing written beside them
