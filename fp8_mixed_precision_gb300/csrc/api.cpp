@@ -909,6 +909,9 @@ fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *
   if (ctx) fp8_gated_ctx_layout(recipe, N, K, F, ctx, &col, &cscale, &cscale_inv, &g, &u);
   const bool block = recipe == FP8_RECIPE_BLOCK;
   float *xsi = reinterpret_cast<float *>(w + L.xsi);
+  if (!ctx && gated_takes_bf16(N, K, F, block))
+    return from_cuda(launch_gated_fwd(nullptr, nullptr, e->w_row, e->row_scale_inv, N, K, F, block,
+                                      act, H, nullptr, nullptr, cs(stream), X));
   if (gated_quantizes_few(N, K, block))
     st = from_cuda(launch_gated_quantize_few(X, N, K, block, w + L.xq, col, xsi, cscale_inv,
                                              cs(stream)));

@@ -395,18 +395,27 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
 // streams 256 weight rows of one K range; a cluster of S CTAs shares a tile of
 // 128 outputs, splits K, and sums the S partials in rank order over
 // distributed shared memory (deterministic, one launch, no workspace).
+//
+// Tokens that nothing else needs in FP8 (no backward pass follows) can be given
+// in bf16: the epilogue warps, idle until the first product, quantize the CTA's
+// K blocks into shared memory while the weight's first tiles arrive.  The codes
+// and scales are gated_quant_few_kernel's, whose launch is saved (1 token, K
+// 4096, F 14336: 23.9 -> 22.5 us; 37 tokens, K 512, F 2048: 8.7 -> 6.8).
 constexpr int kSmallEpi = 8;  // epilogue warps: 4 for G, 4 for U
 constexpr int kSmallThreads = 32 * (2 + kSmallEpi);  // producer, MMA issuer, epilogue
 constexpr int kSmallTokens = 64;  // per CTA
 constexpr int kSmallMaxStages = 6;
+constexpr int kSmallOwnX = 36 * 1024;  // most of it for tokens that the CTA quantizes itself
+constexpr int kSmallOwnItems = 64;     // and most of them, tokens x K blocks
 constexpr int kSmallSmem = 200 * 1024;  // one CTA per SM, room for the quantizer's beside it
 
 struct SmallCtl {
   uint64_t full[kSmallMaxStages], empty[kSmallMaxStages];
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t mma_done;
+  uint64_t mma_done, x_ready;
   uint32_t tmem_base;
   int abort;
+  float xmax[kSmallEpi], x_sinv;  // bf16 tokens, tensor scaling
 };
 constexpr int kSmallCtlBytes = (int)((sizeof(SmallCtl) + 127) / 128 * 128);
 
@@ -417,19 +426,45 @@ struct SmallArgs {
   const float *x_sinv, *w_sinv;
   uint32_t idesc;
   __nv_bfloat16 *H, *G, *U;  // G and U null: not kept
+  const uint4 *x;            // bf16 tokens [N, K], or null: FP8 tokens by tmX and x_sinv
+  int64_t K;
 };
+// Shared memory of a CTA's quantized tokens: rows of 128 bytes in groups of 8 per
+// K block.  The MMA reads NT rows; those past the tokens' last group are the next
+// block's (or the pad's), and only reach accumulator columns that nothing reads.
+__host__ __device__ constexpr int x_group_bytes(int tokens) { return (tokens + 7) / 8 * 1024; }
+__host__ __device__ constexpr int x_tile_bytes(int kbs_cta, int tokens, int nt) {
+  return kbs_cta * x_group_bytes(tokens) + nt * BK - x_group_bytes(tokens);
+}
+
+__device__ __forceinline__ float amax8(float m, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = amax_acc(amax_acc(m, bf16lo(w[k])), bf16hi(w[k]));
+  return m;
+}
+__device__ __forceinline__ uint2 cast_e4m3(uint4 v, float s) {
+  uint2 q;
+  q.x = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(bf16lo(v.x), s), __fmul_rn(bf16hi(v.x), s),
+                              __fmul_rn(bf16lo(v.y), s), __fmul_rn(bf16hi(v.y), s));
+  q.y = cvt4<FP8_FORMAT_E4M3>(__fmul_rn(bf16lo(v.z), s), __fmul_rn(bf16hi(v.z), s),
+                              __fmul_rn(bf16lo(v.w), s), __fmul_rn(bf16hi(v.w), s));
+  return q;
+}
 
 template <int SCALING, int ACT, int NT>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     gated_small_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW, const SmallArgs a) {
   constexpr bool kTensor = SCALING == FP8_SCALING_TENSOR;
-  constexpr int kStageBytes = 2 * BF * BK + NT * BK;
   constexpr uint32_t kCols = 4 * NT;  // two buffers of G and U
+  const bool own_x = a.x != nullptr;
+  const int stage_bytes = 2 * BF * BK + (own_x ? 0 : NT * BK);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   SmallCtl *ctl = reinterpret_cast<SmallCtl *>(ring + a.ring_bytes);
   float *xsc = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ctl) + kSmallCtlBytes);
+  uint8_t *xq = ring + (size_t)a.stages * stage_bytes;  // own_x (inside ring_bytes)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % a.split, f0 = (int)blockIdx.x / a.split * BF;
   const int n0 = (int)blockIdx.y * NT;                      // first token
@@ -449,6 +484,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       ptx::mbar_init(&ctl->acc_empty[b], kSmallEpi);
     }
     ptx::mbar_init(&ctl->mma_done, 1);
+    ptx::mbar_init(&ctl->x_ready, kSmallEpi);
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
@@ -475,11 +511,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       int issued = 0;
       for (; issued < nkb; ++issued) {
         if (!wait(&ctl->empty[stage], phase ^ 1)) { ok = false; break; }
-        uint8_t *sw = ring + (size_t)stage * kStageBytes;
-        ptx::mbar_arrive_expect_tx(&ctl->full[stage], kStageBytes);
+        uint8_t *sw = ring + (size_t)stage * stage_bytes;
+        ptx::mbar_arrive_expect_tx(&ctl->full[stage], (uint32_t)stage_bytes);
         ptx::tma_load_2d(sw, &tmW, &ctl->full[stage], kx(issued), f0);
         ptx::tma_load_2d(sw + BF * BK, &tmW, &ctl->full[stage], kx(issued), (int)a.F + f0);
-        ptx::tma_load_2d(sw + 2 * BF * BK, &tmX, &ctl->full[stage], kx(issued), n0);
+        if (!own_x) ptx::tma_load_2d(sw + 2 * BF * BK, &tmX, &ctl->full[stage], kx(issued), n0);
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
       }
       if (!ok)  // the last copies of each stage land before the CTA can exit
@@ -490,7 +526,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, nacc = 0;
-      for (int i = 0; i < nkb; ++i) {
+      const bool have_x = !own_x || wait(&ctl->x_ready, 0);
+      for (int i = 0; have_x && i < nkb; ++i) {
         const bool first = !kTensor || i == 0, last = !kTensor || i == nkb - 1;
         if (first) {
           if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) break;
@@ -498,10 +535,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         }
         if (!wait(&ctl->full[stage], phase)) break;
         ptx::tc_fence_after();
-        const uint32_t w_addr = ptx::smem_u32(ring + (size_t)stage * kStageBytes);
+        const uint32_t w_addr = ptx::smem_u32(ring + (size_t)stage * stage_bytes);
         const uint64_t gdesc = ptx::smem_desc_sw128(w_addr);
         const uint64_t udesc = ptx::smem_desc_sw128(w_addr + BF * BK);
-        const uint64_t xdesc = ptx::smem_desc_sw128(w_addr + 2 * BF * BK);
+        const uint64_t xdesc = ptx::smem_desc_sw128(
+            own_x ? ptx::smem_u32(xq) + i * x_group_bytes(tokens) : w_addr + 2 * BF * BK);
         const uint32_t d = tmem + (nacc & 1) * 2 * NT;
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k) {
@@ -526,7 +564,52 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
     for (int n = 0; n < NT / 2; ++n) acc[n] = 0;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(z * NT);
-    if constexpr (!kTensor) {
+    if (own_x) {
+      float ts = 1.0f;
+      const int64_t k8 = a.K / 8;
+      if constexpr (kTensor) {  // the whole tensor's maximum, from L2
+        float m = 0.0f;
+        for (int64_t i = et; i < a.N * k8; i += 32 * kSmallEpi) m = amax8(m, a.x[i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) ctl->xmax[warp - 2] = m;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmallEpi) : "memory");
+#pragma unroll
+        for (int k = 0; k < kSmallEpi; ++k) m = fmaxf(m, ctl->xmax[k]);
+        float si;
+        scale_from_amax(m, kE4M3Max, ts, si);
+        if (et == 0) ctl->x_sinv = si;
+      }
+      // 16 lanes to a token's 128 columns of a K block, all requested at once
+      constexpr int kPer = kSmallOwnItems / (2 * kSmallEpi);
+      const int hl = lane & 15, items = tokens * nkb;
+      uint4 xw[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int it = (et >> 4) + k * 2 * kSmallEpi, c = kx(it % nkb) + 8 * hl;
+        xw[k] = it < items && c < a.K ? a.x[(int64_t)(n0 + it / nkb) * k8 + c / 8]
+                                      : make_uint4(0, 0, 0, 0);  // past K: zeros
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int it = (et >> 4) + k * 2 * kSmallEpi, n = it / nkb, i = it % nkb;
+        float s = ts, si;
+        if constexpr (!kTensor) {
+          float m = amax8(0.0f, xw[k]);
+#pragma unroll
+          for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          scale_from_amax(m, kE4M3Max, s, si);
+        }
+        if (it >= items) continue;
+        if (!kTensor && hl == 0) xsc[i * NT + n] = si;
+        *reinterpret_cast<uint2 *>(xq + i * x_group_bytes(tokens) + n * 128 +
+                                   (((hl >> 1) ^ (n & 7)) * 16) + (hl & 1) * 8) = cast_e4m3(xw[k], s);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->x_ready);
+      if (!kTensor) asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmallEpi) : "memory");  // xsc
+    } else if constexpr (!kTensor) {
       // token scales of this CTA's K blocks, [K block][token]; absent tokens: 0
       for (int i = et; i < nkb * NT; i += 32 * kSmallEpi) {
         const int n = i / nkb, k = i % nkb;
@@ -579,7 +662,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int pairs = BF / 2, sub = (int)threadIdx.x / pairs;  // 5 tokens at a time
   const int f = 2 * ((int)threadIdx.x % pairs);
   float s_tensor = 1.0f;
-  if (kTensor) s_tensor = __fmul_rn(a.x_sinv[0], a.w_sinv[0]);
+  if (kTensor) s_tensor = __fmul_rn(own_x ? ctl->x_sinv : a.x_sinv[0], a.w_sinv[0]);
   for (int n = rank + a.split * sub; n < tokens; n += a.split * (kSmallThreads / pairs)) {
     // every rank's partials are requested before the first is added
     float2 x[8], y[8];
@@ -660,12 +743,7 @@ __global__ void __launch_bounds__(kFewThreads)
   float ts = 1.0f;
   if (!BLOCK) {
     float m = 0.0f;
-    for (int64_t i = t; i < N * k8; i += kFewThreads) {
-      const uint4 v = x[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m = amax_acc(amax_acc(m, bf16lo(w[k])), bf16hi(w[k]));
-    }
+    for (int64_t i = t; i < N * k8; i += kFewThreads) m = amax8(m, x[i]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) red[t >> 5] = m;
@@ -1055,13 +1133,18 @@ template <int SCALING, int ACT, int NT>
 cudaError_t launch_small(const uint8_t *xq, const uint8_t *wq, int64_t K, SmallArgs a,
                          cudaStream_t st) {
   CUtensorMap mx, mw;
-  if (!make_u8_map(&mx, xq, a.N, K, NT) || !make_u8_map(&mw, wq, 2 * a.F, K, BF))
+  if (!make_u8_map(&mw, wq, 2 * a.F, K, BF)) return cudaErrorInvalidValue;
+  if (a.x)
+    mx = mw;  // unused
+  else if (!make_u8_map(&mx, xq, a.N, K, NT))
     return cudaErrorInvalidValue;
-  constexpr int kStageBytes = 2 * BF * BK + NT * BK;
+  const int stage_bytes = 2 * BF * BK + (a.x ? 0 : NT * BK);
+  const int own = a.x ? x_tile_bytes(a.kbs_cta, (int)a.N, NT) : 0;
   const int scales = SCALING == FP8_SCALING_TENSOR ? 0 : a.kbs_cta * NT * 4;
   const int fixed = 1024 + kSmallCtlBytes + scales;
-  a.stages = std::max(1, std::min({kSmallMaxStages, a.kbs_cta, (kSmallSmem - fixed) / kStageBytes}));
-  a.ring_bytes = std::max(a.stages * kStageBytes, 2 * NT * BF * 4);
+  a.stages =
+      std::max(1, std::min({kSmallMaxStages, a.kbs_cta, (kSmallSmem - fixed - own) / stage_bytes}));
+  a.ring_bytes = std::max(a.stages * stage_bytes + own, 2 * NT * BF * 4);
   a.idesc = ptx::idesc_f8f6f4(FP8_FORMAT_E4M3, FP8_FORMAT_E4M3, BM, NT);
   auto kernel = gated_small_kernel<SCALING, ACT, NT>;
   static bool done[64];
@@ -1085,12 +1168,15 @@ cudaError_t launch_small(const uint8_t *xq, const uint8_t *wq, int64_t K, SmallA
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a);
 }
+int small_nt(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 template <int SCALING, int ACT>
 cudaError_t launch_small_nt(const uint8_t *xq, const uint8_t *wq, int64_t K, const SmallArgs &a,
                             cudaStream_t st) {
-  if (a.N <= 16) return launch_small<SCALING, ACT, 16>(xq, wq, K, a, st);
-  if (a.N <= 32) return launch_small<SCALING, ACT, 32>(xq, wq, K, a, st);
-  return launch_small<SCALING, ACT, 64>(xq, wq, K, a, st);
+  switch (small_nt(a.N)) {
+    case 16: return launch_small<SCALING, ACT, 16>(xq, wq, K, a, st);
+    case 32: return launch_small<SCALING, ACT, 32>(xq, wq, K, a, st);
+    default: return launch_small<SCALING, ACT, 64>(xq, wq, K, a, st);
+  }
 }
 
 template <int ACT>
@@ -1136,49 +1222,62 @@ cudaError_t launch_cast_tensor(GatedBwd p, float *partials, cudaStream_t st) {
                        p);
 }
 
+// Whether the few-token kernel takes a call, and its split of K.
+// Few tokens; or a deep product whose 128 x 128 tiles would fill less than
+// half the SMs: chunks of 64 tokens and the split of K put more of them to
+// work, the weight coming from L2 for all chunks but the first (us a pass,
+// here / 128-token tiles: 100 tokens, K 4096, F 256: 11.5 / 19.4; 1000, 4096,
+// 512: 19.6 / 21.4; in shallower ones the tiles win, 256, 1024, 2048: 12.1 / 10.0)
+bool small_plan(int64_t N, int64_t K, int64_t F, SmallArgs &a) {
+  const int64_t tiles = (F + BF - 1) / BF;
+  if (N > kSmallTokens && ((N + BM - 1) / BM * tiles * 2 > num_sms() || K < 24 * BK)) return false;
+  a.N = N;
+  a.F = F;
+  a.kbs = (int)((K + BK - 1) / BK);
+  // the largest split of K that still gives every CTA an SM of its own (a
+  // deep ring each; two CTAs per SM with half of it: 10 tokens at K 4096,
+  // F 4096 take 11.7 us a pass, here 9.8).  A cluster lies within one GPC, so not
+  // every SM can hold a CTA of one: of 152 SMs, clusters of 8 fill 120 and those
+  // of 4 144, and one cluster more runs after the others (1 token, K 4096: 15
+  // clusters of 8 6.3 us, 16 11.5, as clusters of 4 8.1; 36 of 4 9.3, 37 15.9, as
+  // pairs 12.1).  Fixed shares with room for a GPC with fewer SMs: a split that
+  // depended on the GPC would change results from one GPU to the next.
+  const int64_t ctas = tiles * ((N + kSmallTokens - 1) / kSmallTokens);
+  auto fits = [&](int split) {
+    const int sixteenths = split == 8 ? 12 : split == 4 ? 15 : 16;
+    return split <= a.kbs && ctas * split * 16 <= (int64_t)num_sms() * sixteenths;
+  };
+  a.split = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+  a.kbs_cta = (a.kbs + a.split - 1) / a.split;
+  // the token scales of a CTA's K range are kept in shared memory (K up to
+  // 8192 at any split, 65536 at the full one; wider ones take the other kernel)
+  return a.kbs_cta <= 64 && tiles * a.split < (int64_t(1) << 31);
+}
+
 }  // namespace
 
 cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
                              const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
-                             int act, void *H, void *G, void *U, cudaStream_t st) {
+                             int act, void *H, void *G, void *U, cudaStream_t st, const void *x) {
   const bool save = G != nullptr;
   const double bytes = (double)N * K + 2.0 * F * K + (save ? 6.0 : 2.0) * N * F;
-  const int64_t tiles = (F + BF - 1) / BF;
-  // Few tokens; or a deep product whose 128 x 128 tiles would fill less than
-  // half the SMs: chunks of 64 tokens and the split of K put more of them to
-  // work, the weight coming from L2 for all chunks but the first (us a pass,
-  // here / 128-token tiles: 100 tokens, K 4096, F 256: 11.5 / 19.4; 1000, 4096,
-  // 512: 19.6 / 21.4; in shallower ones the tiles win, 256, 1024, 2048: 12.1 / 10.0)
-  if (N <= kSmallTokens || ((N + BM - 1) / BM * tiles * 2 <= num_sms() && K >= 24 * BK)) {
-    SmallArgs a = {};
-    a.N = N;
-    a.F = F;
-    a.kbs = (int)((K + BK - 1) / BK);
-    // the largest split of K that still gives every CTA an SM of its own (a
-    // deep ring each; two CTAs per SM with half of it: 10 tokens at K 4096,
-    // F 4096 take 11.7 us a pass, here 9.8)
-    const int64_t chunks = (N + kSmallTokens - 1) / kSmallTokens;
-    a.split = 1;
-    while (a.split < 8 && a.split * 2 <= a.kbs && tiles * chunks * a.split * 2 <= num_sms()) a.split *= 2;
-    a.kbs_cta = (a.kbs + a.split - 1) / a.split;
+  SmallArgs a = {};
+  if (small_plan(N, K, F, a)) {
     a.x_sinv = x_sinv;
     a.w_sinv = w_sinv;
     a.H = static_cast<__nv_bfloat16 *>(H);
     a.G = static_cast<__nv_bfloat16 *>(G);
     a.U = static_cast<__nv_bfloat16 *>(U);
-    // the token scales of a CTA's K range are kept in shared memory (K up to
-    // 8192 at any split, 65536 at the full one; wider ones take the other kernel)
-    if (a.kbs_cta <= 64 && tiles * a.split < (int64_t(1) << 31)) {
-      LaunchScope ls(block ? "gated_small_block" : "gated_small_tensor", st, bytes, 4.0 * N * K * F,
-                     N, F, K);
-      if (block)
-        return act == FP8_ACT_SILU
-                   ? launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_SILU>(xq, wq, K, a, st)
-                   : launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(xq, wq, K, a, st);
+    a.x = static_cast<const uint4 *>(x);
+    a.K = K;
+    LaunchScope ls(block ? "gated_small_block" : "gated_small_tensor", st, bytes + (x ? N * K : 0),
+                   4.0 * N * K * F, N, F, K);
+    if (block)
       return act == FP8_ACT_SILU
-                 ? launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_SILU>(xq, wq, K, a, st)
-                 : launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_GELU>(xq, wq, K, a, st);
-    }
+                 ? launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_SILU>(xq, wq, K, a, st)
+                 : launch_small_nt<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(xq, wq, K, a, st);
+    return act == FP8_ACT_SILU ? launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_SILU>(xq, wq, K, a, st)
+                               : launch_small_nt<FP8_SCALING_TENSOR, FP8_ACT_GELU>(xq, wq, K, a, st);
   }
   CUtensorMap m[5];
   if (!make_u8_map(&m[0], xq, N, K, BM) || !make_u8_map(&m[1], wq, 2 * F, K, BF) ||
@@ -1208,6 +1307,17 @@ cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8
                                : launch_fwd_save<FP8_SCALING_1x128_128x128, FP8_ACT_GELU>(m, g, save, st);
   return act == FP8_ACT_SILU ? launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_SILU>(m, g, save, st)
                              : launch_fwd_save<FP8_SCALING_TENSOR, FP8_ACT_GELU>(m, g, save, st);
+}
+
+// Up to 64 pieces of 128 columns per CTA, which its threads request at once (us a
+// pass, here / through the quantizer: block, 1, 4096, 14336: 22.7 / 23.9; 37, 512,
+// 2048: 6.7 / 8.4; 64, 512, 2048: 7.8 / 8.3; more lose, 37, 1024, 4096: 8.8 / 8.6; 8,
+// 4096, 14336: 29.3 / 24.6), and while five stages of the weight still fit beside.
+bool gated_takes_bf16(int64_t N, int64_t K, int64_t F, bool block) {
+  SmallArgs a = {};
+  return gated_quantizes_few(N, K, block) && small_plan(N, K, F, a) &&
+         N * a.kbs_cta <= kSmallOwnItems &&
+         x_tile_bytes(a.kbs_cta, (int)N, small_nt(N)) <= kSmallOwnX;
 }
 
 bool gated_quantizes_few(int64_t N, int64_t K, bool block) {

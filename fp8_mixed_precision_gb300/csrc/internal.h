@@ -157,10 +157,13 @@ cudaError_t launch_rmsnorm_bwd(const void *dy, const void *dr, const void *r, co
 cudaError_t norm_read_status(unsigned *status);
 
 // Gated feed-forward (gated.cu).  Any number of tokens N; G and U null: no
-// backward pass follows.
+// backward pass follows.  x not null (where gated_takes_bf16): the tokens in
+// bf16, xq and x_sinv unused.
 cudaError_t launch_gated_fwd(const uint8_t *xq, const float *x_sinv, const uint8_t *wq,
                              const float *w_sinv, int64_t N, int64_t K, int64_t F, bool block,
-                             int act, void *H, void *G, void *U, cudaStream_t st);
+                             int act, void *H, void *G, void *U, cudaStream_t st,
+                             const void *x = nullptr);
+bool gated_takes_bf16(int64_t N, int64_t K, int64_t F, bool block);
 // Activation quantizer (E4M3) for few tokens in one launch, with the bytes and
 // scales of launch_quantize; col may be null.
 bool gated_quantizes_few(int64_t N, int64_t K, bool block);

@@ -307,3 +307,26 @@ def test_weight_gradient_from_the_row_layout(fp, N, K, F):
     want = fp.fp8_gemm(a, "e5m2", sa, xt, "e4m3", ctx.ctx[sb:sb + 4].view(torch.float32), "tensor")
     assert torch.equal(dw, want)
     assert fp.fp8_get_device_status() == 0
+
+
+@pytest.mark.parametrize("recipe", ["tensorwise", "block"])
+@pytest.mark.parametrize("N,K,F", [(1, 16, 128), (1, 4096, 14336), (2, 4096, 1024), (7, 144, 256), (8, 528, 256),
+                                   (9, 2064, 512), (16, 4096, 2048), (17, 1040, 128), (33, 512, 2048), (37, 512, 2048),
+                                   (40, 400, 640), (57, 1552, 128), (64, 128, 256), (64, 2032, 512)])
+def test_tokens_quantized_in_the_kernel(fp, recipe, N, K, F):
+    """Without a backward pass few tokens go into the kernel as bf16: the same
+    bits as through the quantizer, special values included."""
+    x, w, dh, cache, h = _case(fp, N, K, F, recipe, 12)
+    x[N // 2, K // 2] = 0.0
+    x[N - 1, :] = 0.0
+    if N > 2:
+        x[1, 3] = float("nan")
+    y, ctx = fp.fp8_gated_fwd(x, cache, h, recipe)
+    y2, _ = fp.fp8_gated_fwd(x, cache, h, recipe, train=False)
+    assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+    if N > 3 and recipe == "block":
+        x[2, K - 1] = float("inf")
+        y, ctx = fp.fp8_gated_fwd(x, cache, h, recipe)
+        y2, _ = fp.fp8_gated_fwd(x, cache, h, recipe, train=False)
+        assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+    assert fp.fp8_get_device_status() == 0
