@@ -964,13 +964,14 @@ fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
 // ---------------------------------------------------------------- gradient clipping
 struct fp8_grad_clip {
   std::vector<ClipChunk> table;
+  bool few = false;  // kClipFewChunks chunks of kClipFewElements at most
   double elements = 0.0, bytes = 0.0;
 };
 
 fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_grad_clip **out) {
   if (!out || count < 0 || (count > 0 && !descs)) return FP8_ERR_INVALID_ARG;
   *out = nullptr;
-  double elements = 0.0, bytes = 0.0;
+  double elements = 0.0, bytes = 0.0, small_chunks = 0.0;
   for (int64_t i = 0; i < count; ++i) {
     const fp8_grad_desc &d = descs[i];
     if (d.n < 0 || !valid_dtype(d.dtype) || (d.n > 0 && (!d.src || !d.dst)))
@@ -979,18 +980,23 @@ fp8_status fp8_grad_clip_create(const fp8_grad_desc *descs, int64_t count, fp8_g
     if ((reinterpret_cast<uintptr_t>(d.src) | reinterpret_cast<uintptr_t>(d.dst)) % size)
       return FP8_ERR_ALIGN;
     elements += (double)d.n;
+    small_chunks += (double)((d.n + kClipFewElements - 1) / kClipFewElements);
     bytes += (double)d.n * (double)size;
   }
-  // Chunk: two for each of the 2 x 152 CTAs that fill the GPU, within 2048 to
-  // 32768 elements, so that small sets still spread over the CTAs and large
-  // ones take many short turns.
-  const int64_t chunk = std::min<int64_t>(
-      32768, std::max<int64_t>(kClipChunkMin, ((int64_t)(elements / 608.0) + kClipChunkMin - 1) /
-                                                  kClipChunkMin * kClipChunkMin));
+  // Chunk: two for each of the 2 x 152 CTAs that fill the GPU, within 8192 to
+  // 32768 elements, so that large sets take many short turns and small ones,
+  // spread over the CTAs, no second turn that costs another round trip to memory
+  // (30 tensors of up to 33333: 7.3 us in chunks of 2048, 5.8 here).
+  const bool few = small_chunks <= kClipFewChunks;
+  const int64_t chunk =
+      few ? kClipFewElements
+          : std::min<int64_t>(
+                32768, std::max<int64_t>(8192, ((int64_t)(elements / 608.0) + 2047) / 2048 * 2048));
   try {
     auto p = std::make_unique<fp8_grad_clip>();
     p->elements = elements;
     p->bytes = bytes;
+    p->few = few;
     for (int64_t i = 0; i < count; ++i) {
       const fp8_grad_desc &d = descs[i];
       const int64_t size = d.dtype == FP8_DTYPE_F32 ? 4 : 2;
@@ -1040,7 +1046,7 @@ fp8_status clip_run(const fp8_grad_clip *plan, const void *table, bool write, fl
   fp8_grad_clip_workspace_size(plan, &need);
   if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
   return from_cuda(launch_clip(static_cast<const ClipChunk *>(table), (int64_t)plan->table.size(),
-                               plan->bytes, plan->elements, write, max_norm, norm,
+                               plan->few, plan->bytes, plan->elements, write, max_norm, norm,
                                static_cast<float *>(ws), cs(stream)));
 }
 }  // namespace

@@ -97,11 +97,12 @@ constexpr int kAhead = 8;
 __device__ __forceinline__ int vectors_of(const ClipChunk &c) {
   return vec_ok(c) ? c.n / (c.f32 ? 4 : 8) : 0;
 }
-__device__ __forceinline__ void request(const ClipChunk &c, int nv, uint4 (&w)[kAhead]) {
+__device__ __forceinline__ void request(const ClipChunk &c, int nv, uint4 (&w)[kAhead],
+                                        int from = 0) {
   const uint4 *p = static_cast<const uint4 *>(c.src);
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    const int i = threadIdx.x + k * kClipThreads;
+    const int i = from + threadIdx.x + k * kClipThreads;
     w[k] = i < nv ? p[i] : make_uint4(0, 0, 0, 0);
   }
 }
@@ -123,15 +124,11 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_norm_kernel(const ClipCh
     if (id < chunks) c = table[id];  // arrives while this chunk is worked on
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) add_squares(w[k], now.f32, a);
-    const uint4 *p = static_cast<const uint4 *>(now.src);
-    int i = threadIdx.x + kAhead * kClipThreads;
-    for (; i + (kAhead - 1) * kClipThreads < nv; i += kAhead * kClipThreads) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) w[k] = p[i + k * kClipThreads];
+    for (int from = kAhead * kClipThreads; from < nv; from += kAhead * kClipThreads) {
+      request(now, nv, w, from);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) add_squares(w[k], now.f32, a);
     }
-    for (; i < nv; i += kClipThreads) add_squares(p[i], now.f32, a);
     for (int e = nv * (now.f32 ? 4 : 8) + threadIdx.x; e < now.n; e += kClipThreads) {
       const float v = load1(now, e);
       a[0] = fmaf(v, v, a[0]);
@@ -194,21 +191,15 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_scale_kernel(const ClipC
     id += gridDim.x;
     if (id < chunks) c = table[chunks - 1 - id];
     if (now.dst != now.src || coef != 1.0f) {  // in place, a factor of 1 changes nothing
-      const uint4 *p = static_cast<const uint4 *>(now.src);
       uint4 *q = static_cast<uint4 *>(now.dst);
+      for (int from = 0; from < nv; from += kAhead * kClipThreads) {
+        if (from) request(now, nv, w, from);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = threadIdx.x + k * kClipThreads;
-        if (i < nv) q[i] = scaled(w[k], now.f32, coef);
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = from + threadIdx.x + k * kClipThreads;
+          if (i < nv) q[i] = scaled(w[k], now.f32, coef);
+        }
       }
-      int i = threadIdx.x + kAhead * kClipThreads;
-      for (; i + (kAhead - 1) * kClipThreads < nv; i += kAhead * kClipThreads) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) w[k] = p[i + k * kClipThreads];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) q[i + k * kClipThreads] = scaled(w[k], now.f32, coef);
-      }
-      for (; i < nv; i += kClipThreads) q[i] = scaled(p[i], now.f32, coef);
       for (int e = nv * (now.f32 ? 4 : 8) + threadIdx.x; e < now.n; e += kClipThreads)
         store1(now, e, coef);
     }
@@ -216,14 +207,14 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_scale_kernel(const ClipC
   }
 }
 
-// Few chunks (kClipFewChunks of kClipChunkMin elements): one CTA does both
+// Few chunks (kClipFewChunks of kClipFewElements at most): one CTA does both
 // passes in one launch, 64 threads to a chunk, the gradients staying in registers
 // in between.  Bound by the launch and the round trips to memory: 9 vectors of
 // 515 floats take 3.6 us a call (2.7 in a graph), as the two kernels 5.2 (4.0); 16
 // full chunks 4.6 (4.4) against 5.2 (4.0).  A cluster of eight CTAs joined over
 // distributed shared memory: 5.5.
 constexpr int kFewThreads = 1024, kFewGroup = kFewThreads / kClipFewChunks;
-static_assert(kClipChunkMin / 4 == kAhead * kFewGroup, "a chunk's vectors fit its threads' registers");
+static_assert(kClipFewElements / 4 == kAhead * kFewGroup, "a chunk's vectors fit its threads' registers");
 static_assert(kFewThreads == 32 * 32, "one lane per warp's sum");
 
 __global__ void __launch_bounds__(kFewThreads) clip_few_kernel(const ClipChunk *__restrict__ table,
@@ -274,9 +265,9 @@ int clip_ctas(int64_t chunks) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)num_sms() * 2));
 }
 
-cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,
+cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, bool few, double in_bytes, double elements,
                         bool write, float max_norm, float *norm, float *partials, cudaStream_t st) {
-  if (chunks <= kClipFewChunks) {
+  if (few) {
     LaunchScope ls("clip_few", st, (write ? 2.0 : 1.0) * in_bytes, 3.0 * elements, (int64_t)elements);
     return launch_kernel(clip_few_kernel, dim3(1), dim3(kFewThreads), 0, st, table, (int)chunks,
                          (int)write, max_norm, norm);

@@ -186,11 +186,12 @@ struct ClipChunk {
   int32_t n;    // elements
   int32_t f32;  // 1: fp32, 0: bf16
 };
-constexpr int kClipChunkMin = 2048;  // elements; sets of few chunks have chunks of this size
-constexpr int kClipFewChunks = 16;   // up to here one launch does it (clip_few_kernel)
+// Sets of at most 16 chunks of 2048 elements take one launch (few: the table is
+// cut so).
+constexpr int kClipFewChunks = 16, kClipFewElements = 2048;
 int clip_ctas(int64_t chunks);  // partial sums the first pass writes
 // write = false: the norm alone.
-cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, double in_bytes, double elements,
+cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, bool few, double in_bytes, double elements,
                         bool write, float max_norm, float *norm, float *partials, cudaStream_t st);
 
 cudaError_t launch_gelu_fwd(const void *H, void *A, int64_t n, cudaStream_t st);
