@@ -9,6 +9,7 @@ compiled library is missing, importing works but the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass, field
 
@@ -786,18 +787,37 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: to
 @dataclass
 class GatedContext:
     """What a gated forward pass keeps for its backward pass: the device buffer,
-    its shape, and the activation (set by the forward pass)."""
+    its shape, and the activation and recipe (set by the forward pass; the
+    recipes place and size what the buffer holds differently)."""
     ctx: torch.Tensor
     N: int
     K: int
     F: int
     act: str = "silu"
+    recipe: str | None = None
+
+    def check(self, recipe: str, N: int, K: int, F: int):
+        """Refuses a buffer that a call of this recipe and shape cannot use."""
+        if (self.N, self.K, self.F) != (N, K, F):
+            raise ValueError("ctx was made for another shape")
+        if self.recipe is not None and (self.recipe == "block") != (recipe == "block"):
+            raise ValueError(f"ctx was made for the {self.recipe} recipe")
+        t = self.ctx
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("ctx must hold a contiguous CUDA tensor")
+        if t.numel() * t.element_size() < _gated_ctx_bytes(recipe, N, K, F):
+            raise ValueError("ctx is smaller than the recipe's context")
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_ctx_bytes(recipe, N, K, F):
+    b = _c_sz()
+    _check(lib().fp8_gated_ctx_size(RECIPE[recipe], N, K, F, ctypes.byref(b)), "fp8_gated_ctx_size")
+    return b.value
 
 
 def gated_context(recipe: str, N: int, K: int, F: int, device) -> GatedContext:
-    b = _c_sz()
-    _check(lib().fp8_gated_ctx_size(RECIPE[recipe], N, K, F, ctypes.byref(b)), "fp8_gated_ctx_size")
-    return GatedContext(_empty_bytes(b.value, device), N, K, F)
+    return GatedContext(_empty_bytes(_gated_ctx_bytes(recipe, N, K, F), device), N, K, F, recipe=recipe)
 
 
 def gated_workspace(recipe: str, N: int, K: int, F: int, device, train: bool = True) -> torch.Tensor:
@@ -810,6 +830,7 @@ def gated_workspace(recipe: str, N: int, K: int, F: int, device, train: bool = T
 def fp8_gated_ctx_layout(recipe: str, ctx: GatedContext):
     """Device pointers inside ctx: (transposed FP8 input, its scale, its
     scale_inv, G, U)."""
+    ctx.check(recipe, ctx.N, ctx.K, ctx.F)
     p = [_c_p() for _ in range(5)]
     _check(lib().fp8_gated_ctx_layout(RECIPE[recipe], ctx.N, ctx.K, ctx.F, _ptr(ctx.ctx),
                                       *[ctypes.byref(q) for q in p]), "fp8_gated_ctx_layout")
@@ -844,8 +865,8 @@ def _gated_out(N, K, cache, h, recipe, y, ctx, train, device):
     _need(y, "y", (N, F), torch.bfloat16)
     if train and ctx is None:
         ctx = gated_context(recipe, N, K, F, device)
-    if train and (ctx.N, ctx.K, ctx.F) != (N, K, F):
-        raise ValueError("ctx was made for another shape")
+    if train:
+        ctx.check(recipe, N, K, F)
     return F, y, ctx if train else None
 
 
@@ -863,7 +884,7 @@ def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act:
                                _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws), ws.numel(),
                                _stream(stream)), "fp8_gated_fwd")
     if train:
-        ctx.act = act
+        ctx.act, ctx.recipe = act, recipe
     return y, ctx
 
 
@@ -881,7 +902,7 @@ def fp8_gated_fwd_quantized(row: torch.Tensor, row_scale_inv: torch.Tensor, cach
                                          None if ctx is None else _ptr(ctx.ctx), _stream(stream)),
            "fp8_gated_fwd_quantized")
     if ctx is not None:
-        ctx.act = act
+        ctx.act, ctx.recipe = act, recipe
     return y, ctx
 
 
@@ -891,6 +912,11 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
     """Returns (dX or None, dW [2F, K]) of the forward pass that made ctx."""
     _need(dh, "dh", (ctx.N, ctx.F), torch.bfloat16)
     N, K, F, dev = ctx.N, ctx.K, ctx.F, dh.device
+    ctx.check(recipe, N, K, F)
+    if not 0 <= h < len(cache.entries):
+        raise ValueError("no such weight handle")
+    if cache.entries[h].w.shape != (2 * F, K):
+        raise ValueError("ctx was made with a weight of another shape")
     if need_dx and dx is None:
         dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
     if dw is None:
