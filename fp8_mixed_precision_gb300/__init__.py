@@ -891,11 +891,18 @@ def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act:
 def fp8_gated_fwd_quantized(row: torch.Tensor, row_scale_inv: torch.Tensor, cache: WeightCache,
                             h: int, recipe: str, act: str = "silu", y: torch.Tensor | None = None,
                             ctx: GatedContext | None = None, stream=None):
-    """fp8_gated_fwd on an input given as E4M3 bytes [N, K] and scale_inv; with
-    ctx its transposed part (fp8_gated_ctx_layout) is already filled."""
+    """fp8_gated_fwd on an input given as E4M3 bytes [N, K] and scale_inv
+    ([N, ceil(K / 128)] under the block recipe, else one); with ctx its
+    transposed part (fp8_gated_ctx_layout) is already filled."""
     if not (row.is_cuda and row.dtype == torch.uint8 and row.is_contiguous()):
         raise ValueError("row must be a contiguous uint8 CUDA tensor")
     N, K = row.shape
+    nb = -(-K // 128)
+    t = row_scale_inv
+    if not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()):
+        raise ValueError("row_scale_inv must be a contiguous float32 CUDA tensor")
+    if not (t.shape in ((N, nb), (N * nb,)) if recipe == "block" else t.numel() == 1):
+        raise ValueError(f"row_scale_inv must hold {f'{N} x {nb} values' if recipe == 'block' else 'one value'}")
     _, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, ctx is not None, row.device)
     _check(lib().fp8_gated_fwd_quantized(_ptr(row), _ptr(row_scale_inv), N, K, cache.handle, h,
                                          RECIPE[recipe], ACTIVATION[act], _ptr(y),

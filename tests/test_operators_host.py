@@ -3,7 +3,7 @@ and allocate, on the host: nothing reaches a GPU (hostcalls.py)."""
 import pytest
 import torch
 
-from hostcalls import Host, bf16
+from hostcalls import Host, bf16, dev, f32
 
 
 @pytest.fixture(scope="module")
@@ -84,3 +84,34 @@ def test_backward_with_a_weight_of_another_shape(fp, host):
     assert not host.calls
     fp.fp8_gated_bwd(bf16(40, 256), ctx, cache, h, "tensorwise")
     assert len(host.calls) == 1
+
+
+# ---------------------------------------------------------------- quantized input
+@pytest.mark.parametrize("bad", [
+    dict(shape=(40, 1)), dict(shape=(39, 2)), dict(shape=(2, 40)), dict(shape=(79,)), dict(shape=(81,)),
+    dict(dtype=torch.float64), dict(dtype=torch.bfloat16), dict(strided=True), dict(on_host=True)])
+def test_scales_of_a_quantized_input(fp, host, bad):
+    """The block kernel reads one float per token and 128 columns."""
+    cache, h = _weight(fp, "block")
+    row = dev(torch.zeros((40, 256), dtype=torch.uint8))
+    s = torch.zeros(bad.get("shape", (40, 2)), dtype=bad.get("dtype", torch.float32))
+    if bad.get("strided"):
+        s = torch.zeros((40, 4))[:, ::2]
+    with pytest.raises(ValueError):
+        fp.fp8_gated_fwd_quantized(row, s if bad.get("on_host") else dev(s), cache, h, "block")
+    assert not host.calls
+
+
+@pytest.mark.parametrize("recipe,shape", [("block", (40, 2)), ("block", (80,)), ("tensorwise", (1,)),
+                                          ("tensorwise", (1, 1)), ("tensorwise", ()), ("delayed", (1,))])
+def test_scales_that_fit(fp, host, recipe, shape):
+    cache, h = _weight(fp, recipe)
+    fp.fp8_gated_fwd_quantized(dev(torch.zeros((40, 256), dtype=torch.uint8)), f32(*shape), cache, h, recipe)
+    assert len(host.calls) == 1
+
+
+def test_one_scale_for_the_tensorwise_recipe(fp, host):
+    cache, h = _weight(fp, "tensorwise")
+    with pytest.raises(ValueError):
+        fp.fp8_gated_fwd_quantized(dev(torch.zeros((40, 256), dtype=torch.uint8)), f32(0), cache, h, "tensorwise")
+    assert not host.calls
