@@ -8,6 +8,7 @@ compiled library is missing, importing works but the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -652,12 +653,16 @@ def fp8_linear_bwd_after_amax(dy: torch.Tensor, dy_partials: torch.Tensor, ctx: 
     return dx, dw
 
 
-def _scratch(t: torch.Tensor, stream):
-    """A workspace made for one call: kept from reuse until the work on `stream`
-    (if not the current one) is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _on(stream):
+    """The calls below make their tensors under the stream that their kernels run
+    on, as `with torch.cuda.stream(stream)` would: the memory is then free of
+    earlier work in that stream's order and goes back to it in that order.
+    What a call returns belongs to that stream; what it is given has to be
+    ready there, and kept until the work is done."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+_CURRENT = contextlib.nullcontext()
 
 
 # ---------------------------------------------------------------- RMS norm
@@ -739,7 +744,8 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
     if residual is not None:
         _need(residual, "residual", (R, C), torch.bfloat16)
     if out is None:
-        out = rmsnorm_buffers(R, C, x.device, residual is not None, rowwise, colwise, bf16)
+        with _on(stream):
+            out = rmsnorm_buffers(R, C, x.device, residual is not None, rowwise, colwise, bf16)
     if not isinstance(out, NormBuffers):
         out = NormBuffers(out)
     wanted = (residual is not None, rowwise, colwise, bf16)
@@ -769,14 +775,15 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: to
     _need(w, "w", (C,), w.dtype)
     if dr is not None:
         _need(dr, "dr", (R, C), torch.bfloat16)
-    if dx is None:
-        dx = torch.empty_like(dy)
-    if dw is None:
-        dw = torch.empty(C, dtype=torch.float32, device=dy.device)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty_like(dy)
+        if dw is None:
+            dw = torch.empty(C, dtype=torch.float32, device=dy.device)
+        if ws is None:
+            ws = rmsnorm_workspace(R, C, dy.device)
     _need(dx, "dx", (R, C), torch.bfloat16)
     _need(dw, "dw", (C,), torch.float32)
-    if ws is None:
-        ws = _scratch(rmsnorm_workspace(R, C, dy.device), stream)
     _check(lib().fp8_rmsnorm_bwd(_ptr(dy), _ptr(dr), _ptr(r), _ptr(rstd), _ptr(w), _DTYPE[w.dtype],
                                  R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
            "fp8_rmsnorm_bwd")
@@ -856,15 +863,16 @@ def gated_norm_columns(recipe: str, ctx: GatedContext) -> dict:
                 col_scale_inv=at(p[2], ctx.K, rb, torch.float32, 4))
 
 
-def _gated_out(N, K, cache, h, recipe, y, ctx, train, device):
+def _gated_out(N, K, cache, h, recipe, y, ctx, train, device, stream):
     if not 0 <= h < len(cache.entries):
         raise ValueError("no such weight handle")
     F = cache.entries[h].w.shape[0] // 2
-    if y is None:
-        y = torch.empty((N, F), dtype=torch.bfloat16, device=device)
+    with _on(stream):
+        if y is None:
+            y = torch.empty((N, F), dtype=torch.bfloat16, device=device)
+        if train and ctx is None:
+            ctx = gated_context(recipe, N, K, F, device)
     _need(y, "y", (N, F), torch.bfloat16)
-    if train and ctx is None:
-        ctx = gated_context(recipe, N, K, F, device)
     if train:
         ctx.check(recipe, N, K, F)
     return F, y, ctx if train else None
@@ -877,9 +885,10 @@ def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act:
     (H, GatedContext), the context None with train=False."""
     _need_bf16_cuda(x, "x")
     N, K = x.shape
-    F, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, train, x.device)
+    F, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, train, x.device, stream)
     if ws is None:
-        ws = _scratch(gated_workspace(recipe, N, K, F, x.device, train=False), stream)
+        with _on(stream):
+            ws = gated_workspace(recipe, N, K, F, x.device, train=False)
     _check(lib().fp8_gated_fwd(_ptr(x), N, K, cache.handle, h, RECIPE[recipe], ACTIVATION[act],
                                _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws), ws.numel(),
                                _stream(stream)), "fp8_gated_fwd")
@@ -903,7 +912,7 @@ def fp8_gated_fwd_quantized(row: torch.Tensor, row_scale_inv: torch.Tensor, cach
         raise ValueError("row_scale_inv must be a contiguous float32 CUDA tensor")
     if not (t.shape in ((N, nb), (N * nb,)) if recipe == "block" else t.numel() == 1):
         raise ValueError(f"row_scale_inv must hold {f'{N} x {nb} values' if recipe == 'block' else 'one value'}")
-    _, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, ctx is not None, row.device)
+    _, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, ctx is not None, row.device, stream)
     _check(lib().fp8_gated_fwd_quantized(_ptr(row), _ptr(row_scale_inv), N, K, cache.handle, h,
                                          RECIPE[recipe], ACTIVATION[act], _ptr(y),
                                          None if ctx is None else _ptr(ctx.ctx), _stream(stream)),
@@ -924,15 +933,16 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
         raise ValueError("no such weight handle")
     if cache.entries[h].w.shape != (2 * F, K):
         raise ValueError("ctx was made with a weight of another shape")
-    if need_dx and dx is None:
-        dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    if dw is None:
-        dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=dev)
+    with _on(stream):
+        if need_dx and dx is None:
+            dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        if dw is None:
+            dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = gated_workspace(recipe, N, K, F, dev)
     if need_dx:
         _need(dx, "dx", (N, K), torch.bfloat16)
     _need(dw, "dw", (2 * F, K), torch.bfloat16)
-    if ws is None:
-        ws = _scratch(gated_workspace(recipe, N, K, F, dev), stream)
     _check(lib().fp8_gated_bwd(_ptr(dh), N, F, _ptr(ctx.ctx), cache.handle, h, RECIPE[recipe],
                                ACTIVATION[ctx.act], _ptr(dx) if need_dx else None, _ptr(dw),
                                _ptr(ws), ws.numel(), _stream(stream)), "fp8_gated_bwd")

@@ -3,7 +3,7 @@ and allocate, on the host: nothing reaches a GPU (hostcalls.py)."""
 import pytest
 import torch
 
-from hostcalls import Host, bf16, dev, f32
+from hostcalls import FakeStream, Host, bf16, dev, f32
 
 
 @pytest.fixture(scope="module")
@@ -115,3 +115,47 @@ def test_one_scale_for_the_tensorwise_recipe(fp, host):
     with pytest.raises(ValueError):
         fp.fp8_gated_fwd_quantized(dev(torch.zeros((40, 256), dtype=torch.uint8)), f32(0), cache, h, "tensorwise")
     assert not host.calls
+
+
+# ---------------------------------------------------------------- streams
+def test_tensors_of_a_call_come_from_its_stream(fp, host):
+    """What a call on another stream allocates (outputs, context, workspace) has
+    to come from that stream's pool: a block just freed on the current stream may
+    still be written by work queued there, and one freed right after the call
+    may be handed to the current stream while the call's kernels use it."""
+    s = FakeStream(77)
+    cache, h = _weight(fp, "block")
+    x, w, dh = bf16(40, 256), f32(256), bf16(40, 256)
+
+    def only(stream, count):
+        made, host.made[:] = list(host.made), []
+        assert len(made) == count and all(at == stream for _, at in made)
+
+    host.made.clear()
+    for stream, at in ((s, 77), (None, 0)):
+        o = fp.fp8_rmsnorm_fwd(x, w, residual=x, bf16=True, stream=stream)
+        only(at, 10)
+        fp.fp8_rmsnorm_bwd(dh, x, o["rstd"], w, stream=stream)
+        only(at, 3)
+        fp.fp8_gated_fwd(x, cache, h, "block", train=False, stream=stream)
+        only(at, 2)
+        _, ctx = fp.fp8_gated_fwd(x, cache, h, "block", stream=stream)
+        only(at, 3)
+        fp.fp8_gated_bwd(dh, ctx, cache, h, "block", stream=stream)
+        only(at, 3)
+        fp.fp8_gated_fwd_quantized(o["row"], o["row_scale_inv"], cache, h, "block", stream=stream)
+        only(at, 1)
+    assert host.on == []
+
+
+def test_buffers_given_are_not_made_again(fp, host):
+    cache, h = _weight(fp, "block")
+    x, dh = bf16(40, 256), bf16(40, 256)
+    y, ctx = bf16(40, 256), fp.gated_context("block", 40, 256, 256, "cuda")
+    ws = fp.gated_workspace("block", 40, 256, 256, "cuda")
+    dx, dw = bf16(40, 256), bf16(512, 256)
+    host.made.clear()
+    s = FakeStream(77)
+    assert fp.fp8_gated_fwd(x, cache, h, "block", ws=ws, y=y, ctx=ctx, stream=s) == (y, ctx)
+    fp.fp8_gated_bwd(dh, ctx, cache, h, "block", ws=ws, dx=dx, dw=dw, stream=s)
+    assert host.made == [] and [a[-1] for _, a in host.calls] == [77, 77]
