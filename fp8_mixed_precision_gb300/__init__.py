@@ -953,7 +953,9 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
 class GradClip:
     """Global norm and clipping of a fixed set of gradient tensors (bf16 or
     float32, contiguous, any sizes).  out: tensors of the same types and sizes
-    that take the clipped gradients; by default the gradients themselves."""
+    that take the clipped gradients; by default the gradients themselves.  Calls
+    of one plan share its workspace, so they have to follow one another (on one
+    stream, or with a wait between streams)."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -978,25 +980,38 @@ class GradClip:
         _check(lib().fp8_grad_clip_table_write(h, _ptr(host), host.numel()),
                "fp8_grad_clip_table_write")
         dev = self.grads[0].device if n else torch.device("cuda")
-        self._table = host.to(dev)
         _check(lib().fp8_grad_clip_workspace_size(h, ctypes.byref(b)),
                "fp8_grad_clip_workspace_size")
         self._ws = _empty_bytes(b.value, dev)
         self._norm = torch.empty(1, dtype=torch.float32, device=dev)
+        # the upload returns once it is done, and all that this stream had queued
+        # before it: from here on any stream may use the table and what is above
+        self._table = host.to(dev)
+        self._streams = {_stream()}
+
+    def _on_stream(self, stream):
+        """The cudaStream_t of a call; the plan's memory outlives the work there."""
+        raw = _stream(stream)
+        if raw not in self._streams:
+            s = torch.cuda.current_stream() if stream is None else stream
+            for t in (self._table, self._ws, self._norm):
+                t.record_stream(s)
+            self._streams.add(raw)
+        return raw
 
     def clip(self, max_norm: float, stream=None):
         """Scales the gradients to a global norm of at most max_norm; returns
         (norm, out), the norm as a float32 device tensor of the unclipped
         gradients.  A norm that is not finite leaves them as they are."""
         _check(lib().fp8_grad_clip_run(self._h, _ptr(self._table), max_norm, _ptr(self._norm),
-                                       _ptr(self._ws), self._ws.numel(), _stream(stream)),
+                                       _ptr(self._ws), self._ws.numel(), self._on_stream(stream)),
                "fp8_grad_clip_run")
         return self._norm, self.out
 
     def norm(self, stream=None) -> torch.Tensor:
         """The global norm alone (float32 device tensor, reused by later calls)."""
         _check(lib().fp8_grad_norm(self._h, _ptr(self._table), _ptr(self._norm), _ptr(self._ws),
-                                   self._ws.numel(), _stream(stream)), "fp8_grad_norm")
+                                   self._ws.numel(), self._on_stream(stream)), "fp8_grad_norm")
         return self._norm
 
     def __del__(self):

@@ -159,3 +159,29 @@ def test_buffers_given_are_not_made_again(fp, host):
     assert fp.fp8_gated_fwd(x, cache, h, "block", ws=ws, y=y, ctx=ctx, stream=s) == (y, ctx)
     fp.fp8_gated_bwd(dh, ctx, cache, h, "block", ws=ws, dx=dx, dw=dw, stream=s)
     assert host.made == [] and [a[-1] for _, a in host.calls] == [77, 77]
+
+
+# ---------------------------------------------------------------- clipping
+def test_plan_of_a_clipping_run_on_other_streams(fp, host):
+    """The plan's own memory is recorded on every stream that a call uses: a plan
+    dropped while a call is pending must not give its pointer table away."""
+    c = fp.GradClip([f32(100)])
+    table, ws = c._table, c._ws
+    c.clip(1.0)
+    assert not table.recorded and not ws.recorded  # made on this stream
+    c.clip(1.0, stream=FakeStream(5))
+    c.norm(stream=FakeStream(6))
+    host.current = 9                                # the caller's current stream has changed
+    c.clip(1.0)
+    c.clip(1.0, stream=FakeStream(5))
+    assert table.recorded == ws.recorded == [5, 6, 9]
+    assert [a[-1] for _, a in host.calls] == [0, 5, 6, 9, 5]
+
+
+def test_plan_memory_is_ready_for_every_stream(fp, host):
+    """The table's upload returns when it is done, and all earlier work of its
+    stream with it; the workspace made before it is then free of such work too."""
+    host.made.clear()
+    c = fp.GradClip([f32(100)])
+    order = [t.data_ptr() for t, _ in host.made]
+    assert order.index(c._ws.data_ptr()) < order.index(c._table.data_ptr())
