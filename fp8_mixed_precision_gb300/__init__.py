@@ -673,17 +673,41 @@ def _need(t, name, shape, dtype):
 
 class NormBuffers(dict):
     """Output buffers of fp8_rmsnorm_fwd.  Their shapes are checked on the first
-    call that writes them and again after an entry has been replaced."""
+    call that writes them and again after any change of the entries."""
 
     checked = None
 
     def __setitem__(self, key, value):
-        super().__setitem__(key, value)
         self.checked = None
+        super().__setitem__(key, value)
+
+    def __delitem__(self, key):
+        self.checked = None
+        super().__delitem__(key)
 
     def update(self, *args, **kw):
-        super().update(*args, **kw)
         self.checked = None
+        super().update(*args, **kw)
+
+    def __ior__(self, other):
+        self.update(other)
+        return self
+
+    def setdefault(self, key, default=None):
+        self.checked = None
+        return super().setdefault(key, default)
+
+    def pop(self, *args):
+        self.checked = None
+        return super().pop(*args)
+
+    def popitem(self):
+        self.checked = None
+        return super().popitem()
+
+    def clear(self):
+        self.checked = None
+        super().clear()
 
     def check(self, R, C, wanted):
         """wanted: (r, rowwise, colwise, y) to be written for an [R, C] input."""

@@ -185,3 +185,33 @@ def test_plan_memory_is_ready_for_every_stream(fp, host):
     c = fp.GradClip([f32(100)])
     order = [t.data_ptr() for t, _ in host.made]
     assert order.index(c._ws.data_ptr()) < order.index(c._table.data_ptr())
+
+
+# ---------------------------------------------------------------- norm buffers
+
+@pytest.mark.parametrize("change", [
+    lambda b, t: b.__setitem__("row", t), lambda b, t: b.update(row=t), lambda b, t: b.update({"row": t}),
+    lambda b, t: b.__ior__({"row": t}), lambda b, t: (b.pop("row"), b.setdefault("row", t)),
+    lambda b, t: (b.__delitem__("row"), b.setdefault("row", t)),
+    lambda b, t: (lambda rest: (b.clear(), rest.update(row=t), [b.setdefault(k, v) for k, v in rest.items()]))(dict(b))])
+def test_every_change_of_the_buffers_is_checked(fp, host, change):
+    x, w = bf16(40, 256), f32(256)
+    buf = fp.rmsnorm_buffers(40, 256, "cuda")
+    fp.fp8_rmsnorm_fwd(x, w, residual=x, out=buf)
+    assert len(host.calls) == 1 and buf.checked is not None
+    change(buf, torch.empty((4, 128), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        fp.fp8_rmsnorm_fwd(x, w, residual=x, out=buf)
+    assert len(host.calls) == 1
+
+
+@pytest.mark.parametrize("gone", [lambda b: b.pop("col"), lambda b: b.__delitem__("col"), lambda b: b.clear(),
+                                  lambda b: [b.popitem() for _ in range(3)]])
+def test_buffers_taken_out(fp, host, gone):
+    x, w = bf16(40, 256), f32(256)
+    buf = fp.rmsnorm_buffers(40, 256, "cuda")
+    fp.fp8_rmsnorm_fwd(x, w, residual=x, out=buf)
+    gone(buf)
+    with pytest.raises(ValueError):
+        fp.fp8_rmsnorm_fwd(x, w, residual=x, out=buf)
+    assert len(host.calls) == 1
