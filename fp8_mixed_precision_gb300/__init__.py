@@ -676,9 +676,12 @@ class NormBuffers(dict):
     call that writes them and again after any change of the entries."""
 
     checked = None
+    r_is_input = False  # the result of a call without a residual: r is its x, no buffer
 
     def __setitem__(self, key, value):
         self.checked = None
+        if key == "r":
+            self.r_is_input = False
         super().__setitem__(key, value)
 
     def __delitem__(self, key):
@@ -686,8 +689,8 @@ class NormBuffers(dict):
         super().__delitem__(key)
 
     def update(self, *args, **kw):
-        self.checked = None
-        super().update(*args, **kw)
+        for key, value in dict(*args, **kw).items():
+            self[key] = value
 
     def __ior__(self, other):
         self.update(other)
@@ -720,7 +723,7 @@ class NormBuffers(dict):
                 ("row_scale_inv", row, (R, nb), f32), ("col", col, (C, -(-R // 16) * 16), u8),
                 ("col_scale", col, (C, rb), f32), ("col_scale_inv", col, (C, rb), f32)):
             if want:
-                if self.get(key) is None:
+                if self.get(key) is None or (key == "r" and self.r_is_input):
                     raise ValueError(f"out has no buffer for {key}")
                 _need(self[key], key, shape, dtype)
         self.checked = (R, C, wanted)
@@ -782,7 +785,11 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
         _ptr(out["row"]) if rowwise else None, _ptr(out["col"]) if colwise else None,
         _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]), _ptr(out["col_scale"]),
         _ptr(out["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
-    return out if residual is not None else dict(out, r=x)
+    if residual is not None:
+        return out
+    result = NormBuffers(out, r=x)
+    result.r_is_input = True
+    return result
 
 
 def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: torch.Tensor,

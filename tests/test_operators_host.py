@@ -215,3 +215,24 @@ def test_buffers_taken_out(fp, host, gone):
     with pytest.raises(ValueError):
         fp.fp8_rmsnorm_fwd(x, w, residual=x, out=buf)
     assert len(host.calls) == 1
+
+
+def test_result_without_a_residual_holds_no_buffer_for_the_stream(fp, host):
+    """There r is the caller's x: given back as `out` of a call with a residual it
+    must not be written over."""
+    x, w = bf16(40, 256), f32(256)
+    o = fp.fp8_rmsnorm_fwd(x, w)
+    assert o["r"] is x
+    with pytest.raises(ValueError):
+        fp.fp8_rmsnorm_fwd(bf16(40, 256), w, residual=bf16(40, 256), out=o)
+    assert len(host.calls) == 1
+    p = fp.fp8_rmsnorm_fwd(bf16(40, 256), w, out=o)  # without one nothing is written there
+    q = fp.fp8_rmsnorm_fwd(bf16(40, 256), w, out=p)
+    with pytest.raises(ValueError):
+        fp.fp8_rmsnorm_fwd(bf16(40, 256), w, residual=bf16(40, 256), out=q)
+    r = bf16(40, 256)
+    o["r"] = r                                       # now it does
+    assert fp.fp8_rmsnorm_fwd(x, w, residual=x, out=o)["r"] is r
+    assert host.launches("fp8_rmsnorm_fwd")[-1][7] == r.data_ptr()
+    p.update(r=r)
+    assert fp.fp8_rmsnorm_fwd(x, w, residual=x, out=p)["r"] is r
