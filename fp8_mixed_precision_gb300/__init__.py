@@ -783,8 +783,8 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
         _ptr(out["r"]) if residual is not None else None, out["rstd"].data_ptr(),
         _ptr(out["rstd_lo"]) if colwise else None, _ptr(out["y"]) if bf16 else None,
         _ptr(out["row"]) if rowwise else None, _ptr(out["col"]) if colwise else None,
-        _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]), _ptr(out["col_scale"]),
-        _ptr(out["col_scale_inv"]), _stream(stream)), "fp8_rmsnorm_fwd")
+        _ptr(out.get("row_scale")), _ptr(out.get("row_scale_inv")), _ptr(out.get("col_scale")),
+        _ptr(out.get("col_scale_inv")), _stream(stream)), "fp8_rmsnorm_fwd")
     if residual is not None:
         return out
     result = NormBuffers(out, r=x)

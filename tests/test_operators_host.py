@@ -236,3 +236,13 @@ def test_result_without_a_residual_holds_no_buffer_for_the_stream(fp, host):
     assert host.launches("fp8_rmsnorm_fwd")[-1][7] == r.data_ptr()
     p.update(r=r)
     assert fp.fp8_rmsnorm_fwd(x, w, residual=x, out=p)["r"] is r
+
+
+def test_buffers_of_the_outputs_asked_for_are_enough(fp, host):
+    x, w = bf16(40, 256), f32(256)
+    o = fp.fp8_rmsnorm_fwd(x, w, rowwise=False, colwise=False, bf16=True, out=dict(rstd=f32(40), y=bf16(40, 256)))
+    assert o["r"] is x and o["y"].shape == (40, 256)
+    row = dict(rstd=f32(40), row=dev(torch.zeros((40, 256), dtype=torch.uint8)), row_scale=f32(40, 2),
+               row_scale_inv=f32(40, 2), r=bf16(40, 256))
+    fp.fp8_rmsnorm_fwd(x, w, residual=x, colwise=False, out=row)
+    assert len(host.calls) == 2
