@@ -1014,36 +1014,44 @@ class GradClip:
         _check(lib().fp8_grad_clip_workspace_size(h, ctypes.byref(b)),
                "fp8_grad_clip_workspace_size")
         self._ws = _empty_bytes(b.value, dev)
-        self._norm = torch.empty(1, dtype=torch.float32, device=dev)
         # the upload returns once it is done, and all that this stream had queued
-        # before it: from here on any stream may use the table and what is above
+        # before it: from here on any stream may use the table and the workspace
         self._table = host.to(dev)
         self._streams = {_stream()}
+        self._device = dev
 
     def _on_stream(self, stream):
         """The cudaStream_t of a call; the plan's memory outlives the work there."""
         raw = _stream(stream)
         if raw not in self._streams:
             s = torch.cuda.current_stream() if stream is None else stream
-            for t in (self._table, self._ws, self._norm):
+            for t in (self._table, self._ws):
                 t.record_stream(s)
             self._streams.add(raw)
         return raw
 
+    def _new_norm(self, stream):
+        if stream is None:
+            return torch.empty(1, dtype=torch.float32, device=self._device)
+        with _on(stream):
+            return torch.empty(1, dtype=torch.float32, device=self._device)
+
     def clip(self, max_norm: float, stream=None):
         """Scales the gradients to a global norm of at most max_norm; returns
-        (norm, out), the norm as a float32 device tensor of the unclipped
+        (norm, out), the norm as a new float32 device tensor of the unclipped
         gradients.  A norm that is not finite leaves them as they are."""
-        _check(lib().fp8_grad_clip_run(self._h, _ptr(self._table), max_norm, _ptr(self._norm),
-                                       _ptr(self._ws), self._ws.numel(), self._on_stream(stream)),
+        norm = self._new_norm(stream)
+        _check(lib().fp8_grad_clip_run(self._h, self._table.data_ptr(), max_norm, norm.data_ptr(),
+                                       self._ws.data_ptr(), self._ws.numel(), self._on_stream(stream)),
                "fp8_grad_clip_run")
-        return self._norm, self.out
+        return norm, self.out
 
     def norm(self, stream=None) -> torch.Tensor:
-        """The global norm alone (float32 device tensor, reused by later calls)."""
-        _check(lib().fp8_grad_norm(self._h, _ptr(self._table), _ptr(self._norm), _ptr(self._ws),
+        """The global norm alone (a new float32 device tensor)."""
+        norm = self._new_norm(stream)
+        _check(lib().fp8_grad_norm(self._h, self._table.data_ptr(), norm.data_ptr(), self._ws.data_ptr(),
                                    self._ws.numel(), self._on_stream(stream)), "fp8_grad_norm")
-        return self._norm
+        return norm
 
     def __del__(self):
         if getattr(self, "_h", None) is not None and _lib is not None:

@@ -246,3 +246,17 @@ def test_buffers_of_the_outputs_asked_for_are_enough(fp, host):
                row_scale_inv=f32(40, 2), r=bf16(40, 256))
     fp.fp8_rmsnorm_fwd(x, w, residual=x, colwise=False, out=row)
     assert len(host.calls) == 2
+
+
+def test_every_call_returns_a_norm_of_its_own(fp, host):
+    """A caller that collects the norms of several steps reads them later."""
+    c = fp.GradClip([f32(100)])
+    host.made.clear()
+    a, _ = c.clip(1.0)
+    b = c.norm()
+    d, _ = c.clip(1.0, stream=FakeStream(5))
+    assert len({t.data_ptr() for t in (a, b, d)}) == 3
+    assert [(t.data_ptr(), at) for t, at in host.made] == [(a.data_ptr(), 0), (b.data_ptr(), 0), (d.data_ptr(), 5)]
+    assert all(t.shape == (1,) and t.dtype == torch.float32 for t in (a, b, d))
+    assert [args[3] for args in host.launches("fp8_grad_clip_run")] == [a.data_ptr(), d.data_ptr()]
+    assert [args[2] for args in host.launches("fp8_grad_norm")] == [b.data_ptr()]
