@@ -80,9 +80,12 @@ class FP8GatedMLPStack:
 
     def microbatch(self, x: torch.Tensor, dy: torch.Tensor, use_cache: bool = True):
         """Forward and backward of one microbatch: x [N, d] enters the stream, dy
-        is the gradient of the output.  Returns (output, dx); weight gradients
-        accumulate."""
+        is the gradient of the output.  Returns (output, dx), new tensors; weight
+        gradients accumulate."""
         b, r, c, block = self._buffers(), self.recipe, self.cache, self.recipe == "block"
+        b["final"]["y"] = torch.empty((self.N, self.d), dtype=torch.bfloat16, device=self.dev)
+        # the stream's gradient: two buffers in turn, the last one returned
+        grad = [torch.empty_like(b["final"]["y"])] + [b["g"][l % 2] for l in range(self.L)]
         stream, branch = None, x
         for l, t in enumerate(b["layers"]):
             c.get(self.hgu[l], self.version, use_cache)
@@ -100,7 +103,7 @@ class FP8GatedMLPStack:
             stream, branch = o["r"], t["Y"]
         f = fp.fp8_rmsnorm_fwd(branch, self.wn[self.L], residual=stream, rowwise=False,
                                colwise=False, bf16=True, out=b["final"])
-        g, _ = fp.fp8_rmsnorm_bwd(dy, f["r"], f["rstd"], self.wn[self.L], dx=b["g"][self.L % 2],
+        g, _ = fp.fp8_rmsnorm_bwd(dy, f["r"], f["rstd"], self.wn[self.L], dx=grad[self.L],
                                   dw=b["dwn"], ws=b["ws"])
         self.dwn[self.L].add_(b["dwn"])
         for l in reversed(range(self.L)):
@@ -112,13 +115,14 @@ class FP8GatedMLPStack:
                              dw=b["dwgu"])
             fp.fp8_grad_accumulate(self.dwgu[l], b["dwgu"])
             g, _ = fp.fp8_rmsnorm_bwd(b["dXn"], t["r"], t["rstd"], self.wn[l], dr=g,
-                                      dx=b["g"][l % 2], dw=b["dwn"], ws=b["ws"])
+                                      dx=grad[l], dw=b["dwn"], ws=b["ws"])
             self.dwn[l].add_(b["dwn"])
         return f["y"], g
 
     def step(self, xs, dys, use_cache: bool = True):
         """One gradient-accumulation cycle, then clipping.  Returns (global norm
-        before clipping as a device tensor, the clipped gradients)."""
+        before clipping as a new device tensor, the clipped gradients, which are
+        the accumulators that the next step clears)."""
         self.cache.begin_cycle()
         self.version += 1
         for g in self.grads:
