@@ -666,9 +666,17 @@ _CURRENT = contextlib.nullcontext()
 
 
 # ---------------------------------------------------------------- RMS norm
-def _need(t, name, shape, dtype):
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+def _need(t, name, shape, dtype, dev):
+    """dev: index of the CUDA device of the call's input."""
+    if not (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+
+
+def _bytes(t, name, dev):
+    """The size of a workspace."""
+    if not (t.get_device() == dev and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
+    return t.numel() * t.element_size()
 
 
 class NormBuffers(dict):
@@ -712,8 +720,8 @@ class NormBuffers(dict):
         self.checked = None
         super().clear()
 
-    def check(self, R, C, wanted):
-        """wanted: (r, rowwise, colwise, y) to be written for an [R, C] input."""
+    def check(self, R, C, wanted, dev):
+        """wanted: (r, rowwise, colwise, y) to be written for an [R, C] input on cuda:dev."""
         nb, rb = -(-C // 128), -(-R // 128)
         r, row, col, y = wanted
         bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
@@ -725,8 +733,8 @@ class NormBuffers(dict):
             if want:
                 if self.get(key) is None or (key == "r" and self.r_is_input):
                     raise ValueError(f"out has no buffer for {key}")
-                _need(self[key], key, shape, dtype)
-        self.checked = (R, C, wanted)
+                _need(self[key], key, shape, dtype, dev)
+        self.checked = (R, C, wanted, dev)
 
 
 def rmsnorm_buffers(R: int, C: int, device, residual: bool = True, rowwise: bool = True,
@@ -765,19 +773,20 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | N
     blocks, y the norm in bf16.  out: buffers of rmsnorm_buffers to write."""
     _need_bf16_cuda(x, "x")
     R, C = x.shape
+    dev = x.get_device()
     if w.dtype not in _DTYPE:
         raise ValueError("w must be bf16 or float32")
-    _need(w, "w", (C,), w.dtype)
+    _need(w, "w", (C,), w.dtype, dev)
     if residual is not None:
-        _need(residual, "residual", (R, C), torch.bfloat16)
+        _need(residual, "residual", (R, C), torch.bfloat16, dev)
     if out is None:
         with _on(stream):
             out = rmsnorm_buffers(R, C, x.device, residual is not None, rowwise, colwise, bf16)
     if not isinstance(out, NormBuffers):
         out = NormBuffers(out)
     wanted = (residual is not None, rowwise, colwise, bf16)
-    if out.checked != (R, C, wanted):
-        out.check(R, C, wanted)
+    if out.checked != (R, C, wanted, dev):
+        out.check(R, C, wanted, dev)
     _check(lib().fp8_rmsnorm_fwd(
         x.data_ptr(), _ptr(residual), w.data_ptr(), _DTYPE[w.dtype], R, C, eps,
         _ptr(out["r"]) if residual is not None else None, out["rstd"].data_ptr(),
@@ -799,13 +808,14 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: to
     float32; dr is the gradient that the stream r has from elsewhere."""
     _need_bf16_cuda(dy, "dy")
     R, C = dy.shape
-    _need(r, "r", (R, C), torch.bfloat16)
-    _need(rstd, "rstd", (R,), torch.float32)
+    dev = dy.get_device()
+    _need(r, "r", (R, C), torch.bfloat16, dev)
+    _need(rstd, "rstd", (R,), torch.float32, dev)
     if w.dtype not in _DTYPE:
         raise ValueError("w must be bf16 or float32")
-    _need(w, "w", (C,), w.dtype)
+    _need(w, "w", (C,), w.dtype, dev)
     if dr is not None:
-        _need(dr, "dr", (R, C), torch.bfloat16)
+        _need(dr, "dr", (R, C), torch.bfloat16, dev)
     with _on(stream):
         if dx is None:
             dx = torch.empty_like(dy)
@@ -813,10 +823,10 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor, w: to
             dw = torch.empty(C, dtype=torch.float32, device=dy.device)
         if ws is None:
             ws = rmsnorm_workspace(R, C, dy.device)
-    _need(dx, "dx", (R, C), torch.bfloat16)
-    _need(dw, "dw", (C,), torch.float32)
+    _need(dx, "dx", (R, C), torch.bfloat16, dev)
+    _need(dw, "dw", (C,), torch.float32, dev)
     _check(lib().fp8_rmsnorm_bwd(_ptr(dy), _ptr(dr), _ptr(r), _ptr(rstd), _ptr(w), _DTYPE[w.dtype],
-                                 R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream)),
+                                 R, C, _ptr(dx), _ptr(dw), _ptr(ws), _bytes(ws, "ws", dev), _stream(stream)),
            "fp8_rmsnorm_bwd")
     return dx, dw
 
@@ -834,16 +844,13 @@ class GatedContext:
     act: str = "silu"
     recipe: str | None = None
 
-    def check(self, recipe: str, N: int, K: int, F: int):
+    def check(self, recipe: str, N: int, K: int, F: int, dev: int):
         """Refuses a buffer that a call of this recipe and shape cannot use."""
         if (self.N, self.K, self.F) != (N, K, F):
             raise ValueError("ctx was made for another shape")
         if self.recipe is not None and (self.recipe == "block") != (recipe == "block"):
             raise ValueError(f"ctx was made for the {self.recipe} recipe")
-        t = self.ctx
-        if not (t.is_cuda and t.is_contiguous()):
-            raise ValueError("ctx must hold a contiguous CUDA tensor")
-        if t.numel() * t.element_size() < _gated_ctx_bytes(recipe, N, K, F):
+        if _bytes(self.ctx, "ctx", dev) < _gated_ctx_bytes(recipe, N, K, F):
             raise ValueError("ctx is smaller than the recipe's context")
 
 
@@ -868,7 +875,7 @@ def gated_workspace(recipe: str, N: int, K: int, F: int, device, train: bool = T
 def fp8_gated_ctx_layout(recipe: str, ctx: GatedContext):
     """Device pointers inside ctx: (transposed FP8 input, its scale, its
     scale_inv, G, U)."""
-    ctx.check(recipe, ctx.N, ctx.K, ctx.F)
+    ctx.check(recipe, ctx.N, ctx.K, ctx.F, ctx.ctx.get_device())
     p = [_c_p() for _ in range(5)]
     _check(lib().fp8_gated_ctx_layout(RECIPE[recipe], ctx.N, ctx.K, ctx.F, _ptr(ctx.ctx),
                                       *[ctypes.byref(q) for q in p]), "fp8_gated_ctx_layout")
@@ -894,19 +901,25 @@ def gated_norm_columns(recipe: str, ctx: GatedContext) -> dict:
                 col_scale_inv=at(p[2], ctx.K, rb, torch.float32, 4))
 
 
-def _gated_out(N, K, cache, h, recipe, y, ctx, train, device, stream):
+def _gated_out(x, cache, h, recipe, y, ctx, train, stream):
+    """(N, K, F, y, ctx) of a forward call on x [N, K], in bf16 or FP8."""
+    N, K = x.shape
     if not 0 <= h < len(cache.entries):
         raise ValueError("no such weight handle")
-    F = cache.entries[h].w.shape[0] // 2
+    w = cache.entries[h].w
+    dev = w.get_device()
+    if x.get_device() != dev:
+        raise ValueError(f"the input must be on cuda:{dev}, as the weight")
+    F = w.shape[0] // 2
     with _on(stream):
         if y is None:
-            y = torch.empty((N, F), dtype=torch.bfloat16, device=device)
+            y = torch.empty((N, F), dtype=torch.bfloat16, device=x.device)
         if train and ctx is None:
-            ctx = gated_context(recipe, N, K, F, device)
-    _need(y, "y", (N, F), torch.bfloat16)
+            ctx = gated_context(recipe, N, K, F, x.device)
+    _need(y, "y", (N, F), torch.bfloat16, dev)
     if train:
-        ctx.check(recipe, N, K, F)
-    return F, y, ctx if train else None
+        ctx.check(recipe, N, K, F, dev)
+    return N, K, F, y, ctx if train else None
 
 
 def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act: str = "silu",
@@ -915,14 +928,13 @@ def fp8_gated_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str, act:
     """H = act(X Wg^T) * (X Wu^T) for the weight [Wg; Wu] of handle h; returns
     (H, GatedContext), the context None with train=False."""
     _need_bf16_cuda(x, "x")
-    N, K = x.shape
-    F, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, train, x.device, stream)
+    N, K, F, y, ctx = _gated_out(x, cache, h, recipe, y, ctx, train, stream)
     if ws is None:
         with _on(stream):
             ws = gated_workspace(recipe, N, K, F, x.device, train=False)
     _check(lib().fp8_gated_fwd(_ptr(x), N, K, cache.handle, h, RECIPE[recipe], ACTIVATION[act],
-                               _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws), ws.numel(),
-                               _stream(stream)), "fp8_gated_fwd")
+                               _ptr(y), _ptr(ctx.ctx) if train else None, _ptr(ws),
+                               _bytes(ws, "ws", x.get_device()), _stream(stream)), "fp8_gated_fwd")
     if train:
         ctx.act, ctx.recipe = act, recipe
     return y, ctx
@@ -939,11 +951,11 @@ def fp8_gated_fwd_quantized(row: torch.Tensor, row_scale_inv: torch.Tensor, cach
     N, K = row.shape
     nb = -(-K // 128)
     t = row_scale_inv
-    if not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()):
-        raise ValueError("row_scale_inv must be a contiguous float32 CUDA tensor")
+    if not (t.get_device() == row.get_device() and t.dtype == torch.float32 and t.is_contiguous()):
+        raise ValueError("row_scale_inv must be a contiguous float32 tensor on the device of row")
     if not (t.shape in ((N, nb), (N * nb,)) if recipe == "block" else t.numel() == 1):
         raise ValueError(f"row_scale_inv must hold {f'{N} x {nb} values' if recipe == 'block' else 'one value'}")
-    _, y, ctx = _gated_out(N, K, cache, h, recipe, y, ctx, ctx is not None, row.device, stream)
+    _, _, _, y, ctx = _gated_out(row, cache, h, recipe, y, ctx, ctx is not None, stream)
     _check(lib().fp8_gated_fwd_quantized(_ptr(row), _ptr(row_scale_inv), N, K, cache.handle, h,
                                          RECIPE[recipe], ACTIVATION[act], _ptr(y),
                                          None if ctx is None else _ptr(ctx.ctx), _stream(stream)),
@@ -957,26 +969,27 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
                   need_dx: bool = True, ws: torch.Tensor | None = None,
                   dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
     """Returns (dX or None, dW [2F, K]) of the forward pass that made ctx."""
-    _need(dh, "dh", (ctx.N, ctx.F), torch.bfloat16)
-    N, K, F, dev = ctx.N, ctx.K, ctx.F, dh.device
-    ctx.check(recipe, N, K, F)
     if not 0 <= h < len(cache.entries):
         raise ValueError("no such weight handle")
-    if cache.entries[h].w.shape != (2 * F, K):
+    w = cache.entries[h].w
+    N, K, F, dev = ctx.N, ctx.K, ctx.F, w.get_device()
+    _need(dh, "dh", (N, F), torch.bfloat16, dev)
+    ctx.check(recipe, N, K, F, dev)
+    if w.shape != (2 * F, K):
         raise ValueError("ctx was made with a weight of another shape")
     with _on(stream):
         if need_dx and dx is None:
-            dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+            dx = torch.empty((N, K), dtype=torch.bfloat16, device=w.device)
         if dw is None:
-            dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=dev)
+            dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=w.device)
         if ws is None:
-            ws = gated_workspace(recipe, N, K, F, dev)
+            ws = gated_workspace(recipe, N, K, F, w.device)
     if need_dx:
-        _need(dx, "dx", (N, K), torch.bfloat16)
-    _need(dw, "dw", (2 * F, K), torch.bfloat16)
+        _need(dx, "dx", (N, K), torch.bfloat16, dev)
+    _need(dw, "dw", (2 * F, K), torch.bfloat16, dev)
     _check(lib().fp8_gated_bwd(_ptr(dh), N, F, _ptr(ctx.ctx), cache.handle, h, RECIPE[recipe],
                                ACTIVATION[ctx.act], _ptr(dx) if need_dx else None, _ptr(dw),
-                               _ptr(ws), ws.numel(), _stream(stream)), "fp8_gated_bwd")
+                               _ptr(ws), _bytes(ws, "ws", dev), _stream(stream)), "fp8_gated_bwd")
     return (dx if need_dx else None), dw
 
 
@@ -994,10 +1007,11 @@ class GradClip:
         if len(self.out) != len(self.grads):
             raise ValueError("out must have one tensor per gradient")
         for g, o in zip(self.grads, self.out):
-            if g.dtype not in _DTYPE:
-                raise ValueError("gradients must be bf16 or float32")
-            _need(g, "gradient", g.shape, g.dtype)
-            _need(o, "out", g.shape, g.dtype)
+            if g.dtype not in _DTYPE or not g.is_cuda:
+                raise ValueError("gradients must be bf16 or float32 CUDA tensors")
+            dev = self.grads[0].get_device()
+            _need(g, "gradient", g.shape, g.dtype, dev)
+            _need(o, "out", g.shape, g.dtype, dev)
         n = len(self.grads)
         descs = (_GradDesc * max(n, 1))(*[_GradDesc(g.data_ptr(), o.data_ptr(), g.numel(),
                                                     _DTYPE[g.dtype])

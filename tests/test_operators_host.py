@@ -260,3 +260,57 @@ def test_every_call_returns_a_norm_of_its_own(fp, host):
     assert all(t.shape == (1,) and t.dtype == torch.float32 for t in (a, b, d))
     assert [args[3] for args in host.launches("fp8_grad_clip_run")] == [a.data_ptr(), d.data_ptr()]
     assert [args[2] for args in host.launches("fp8_grad_norm")] == [b.data_ptr()]
+
+
+# ---------------------------------------------------------------- devices and workspaces
+def test_workspaces_on_the_host_are_refused(fp, host):
+    cache, h = _weight(fp, "block")
+    x, dh, w = bf16(40, 256), bf16(40, 256), f32(256)
+    _, ctx = fp.fp8_gated_fwd(x, cache, h, "block")
+    n = len(host.calls)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8)
+    for call in (lambda: fp.fp8_gated_fwd(x, cache, h, "block", ws=ws),
+                 lambda: fp.fp8_gated_bwd(dh, ctx, cache, h, "block", ws=ws),
+                 lambda: fp.fp8_rmsnorm_bwd(x, x, f32(40), w, ws=ws)):
+        with pytest.raises(ValueError):
+            call()
+        ws2 = dev(torch.zeros((1 << 12, 1 << 12), dtype=torch.uint8))[:, ::2]
+        ws, ws2 = ws2, ws
+        with pytest.raises(ValueError):
+            call()
+        ws = ws2
+    assert len(host.calls) == n
+
+
+def test_workspaces_count_bytes(fp, host):
+    """A float32 workspace of as many bytes serves."""
+    cache, h = _weight(fp, "block")
+    x = bf16(40, 256)
+    need = fp.gated_workspace("block", 40, 256, 256, "cuda", train=False).numel()
+    fp.fp8_gated_fwd(x, cache, h, "block", train=False, ws=f32(need // 4))
+    assert host.calls[-1][1][-2] == need
+
+
+def test_tensors_of_another_device_are_refused(fp, host):
+    cache, h = _weight(fp, "block")
+    x, dh, w, rstd = bf16(40, 256), bf16(40, 256), f32(256), f32(40)
+    _, ctx = fp.fp8_gated_fwd(x, cache, h, "block")
+    n = len(host.calls)
+
+    def away(t):
+        return dev(t.clone(), 1)
+
+    u8 = dev(torch.zeros((40, 256), dtype=torch.uint8))
+    for call in (lambda: fp.fp8_rmsnorm_fwd(x, away(w)), lambda: fp.fp8_rmsnorm_fwd(x, w, residual=away(x)),
+                 lambda: fp.fp8_rmsnorm_fwd(away(x), w, out=fp.rmsnorm_buffers(40, 256, "cuda", residual=False)),
+                 lambda: fp.fp8_rmsnorm_bwd(x, away(x), rstd, w), lambda: fp.fp8_rmsnorm_bwd(x, x, away(rstd), w),
+                 lambda: fp.fp8_rmsnorm_bwd(x, x, rstd, w, ws=away(u8)),
+                 lambda: fp.fp8_gated_fwd(away(x), cache, h, "block", y=bf16(40, 256)),
+                 lambda: fp.fp8_gated_fwd(x, cache, h, "block", ws=away(u8)),
+                 lambda: fp.fp8_gated_fwd_quantized(u8, away(f32(40, 2)), cache, h, "block"),
+                 lambda: fp.fp8_gated_bwd(away(dh), ctx, cache, h, "block", dx=bf16(40, 256), dw=bf16(512, 256)),
+                 lambda: fp.fp8_gated_bwd(dh, ctx, cache, h, "block", dx=away(x)),
+                 lambda: fp.GradClip([f32(8), away(f32(8))]), lambda: fp.GradClip([f32(8)], [away(f32(8))])):
+        with pytest.raises(ValueError):
+            call()
+    assert len(host.calls) == n
