@@ -86,6 +86,7 @@ class Host:
             host.on.pop()
 
         monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: FakeStream(host.at()))
 
     def at(self):
