@@ -1035,44 +1035,39 @@ class GradClip:
         self._device = dev
         self._norms, self._norms_on = [], None  # norms not yet handed out
 
-    def _on_stream(self, stream):
-        """The cudaStream_t of a call; the plan's memory outlives the work there."""
+    def _begin(self, stream):
+        """(cudaStream_t, norm) of a call.  The plan's memory outlives the work there.
+        The norm is one of 64 allocated together on the current stream (nine
+        vectors, a call with an allocation 9.4 us, here 6.9); that of a captured
+        call comes from the graph's pool, which lives as long as its replays."""
         raw = _stream(stream)
         if raw not in self._streams:
             s = torch.cuda.current_stream() if stream is None else stream
             for t in (self._table, self._ws):
                 t.record_stream(s)
             self._streams.add(raw)
-        return raw
-
-    def _new_norm(self, stream):
-        """A norm of its own for a call: one of 64 allocated together on the current
-        stream (nine vectors, a call with an allocation 9.4 us, here 6.3).  A
-        captured call's comes from the graph's pool, which lives as long as replays."""
         if stream is None and not torch._C._cuda_isCurrentStreamCapturing():
-            raw = _stream()
             if not self._norms or raw != self._norms_on:
                 block = torch.empty(64, dtype=torch.float32, device=self._device)
                 self._norms, self._norms_on = list(block.split(1)), raw
-            return self._norms.pop()
+            return raw, self._norms.pop()
         with _on(stream):
-            return torch.empty(1, dtype=torch.float32, device=self._device)
+            return raw, torch.empty(1, dtype=torch.float32, device=self._device)
 
     def clip(self, max_norm: float, stream=None):
         """Scales the gradients to a global norm of at most max_norm; returns
         (norm, out), the norm as a new float32 device tensor of the unclipped
         gradients.  A norm that is not finite leaves them as they are."""
-        norm = self._new_norm(stream)
+        raw, norm = self._begin(stream)
         _check(lib().fp8_grad_clip_run(self._h, self._table.data_ptr(), max_norm, norm.data_ptr(),
-                                       self._ws.data_ptr(), self._ws.numel(), self._on_stream(stream)),
-               "fp8_grad_clip_run")
+                                       self._ws.data_ptr(), self._ws.numel(), raw), "fp8_grad_clip_run")
         return norm, self.out
 
     def norm(self, stream=None) -> torch.Tensor:
         """The global norm alone (a new float32 device tensor)."""
-        norm = self._new_norm(stream)
+        raw, norm = self._begin(stream)
         _check(lib().fp8_grad_norm(self._h, self._table.data_ptr(), norm.data_ptr(), self._ws.data_ptr(),
-                                   self._ws.numel(), self._on_stream(stream)), "fp8_grad_norm")
+                                   self._ws.numel(), raw), "fp8_grad_norm")
         return norm
 
     def __del__(self):
