@@ -997,9 +997,15 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
 class GradClip:
     """Global norm and clipping of a fixed set of gradient tensors (bf16 or
     float32, contiguous, any sizes).  out: tensors of the same types and sizes
-    that take the clipped gradients; by default the gradients themselves.  Calls
-    of one plan share its workspace, so they have to follow one another (on one
-    stream, or with a wait between streams)."""
+    that take the clipped gradients; by default the gradients themselves.
+
+    The plan is for the memory that the tensors have when it is made, and keeps
+    that memory: right for gradients that stay where they are (accumulators,
+    flat buffers).  Gradients allocated anew, or moved by `g.data = ...`, need a
+    new plan (a table of 24 bytes per 8192 to 32768 elements, made on the host
+    and uploaded with a synchronisation).  Calls of one plan share its workspace,
+    so they have to follow one another (on one stream, or with a wait between
+    streams)."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -1012,6 +1018,7 @@ class GradClip:
             dev = self.grads[0].get_device()
             _need(g, "gradient", g.shape, g.dtype, dev)
             _need(o, "out", g.shape, g.dtype, dev)
+        self._memory = [t.detach() for t in self.grads + self.out]
         n = len(self.grads)
         descs = (_GradDesc * max(n, 1))(*[_GradDesc(g.data_ptr(), o.data_ptr(), g.numel(),
                                                     _DTYPE[g.dtype])
