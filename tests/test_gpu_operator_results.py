@@ -47,3 +47,17 @@ def test_norms_of_one_plan(fp):
     after = c.norm()
     assert float(before) == float(during) > 0.11
     assert abs(float(after) - 0.1) < 1e-3  # bf16 gradients: 2^-8 each, in part
+
+
+def test_a_plan_keeps_the_memory_it_points_to(fp):
+    """Its table holds addresses: memory that a gradient is moved away from must
+    not become another tensor's."""
+    g, o = torch.zeros(3_000_017, device="cuda"), torch.zeros(3_000_017, device="cuda")
+    at = {g.data_ptr(), o.data_ptr()}
+    plan = fp.GradClip([g], [o])
+    g.data, o.data = torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")
+    new = [torch.empty(3_000_017, device="cuda") for _ in range(4)]
+    assert at.isdisjoint(t.data_ptr() for t in new)
+    del plan, new
+    new = [torch.empty(3_000_017, device="cuda") for _ in range(4)]
+    assert at <= {t.data_ptr() for t in new}
