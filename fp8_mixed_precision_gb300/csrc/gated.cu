@@ -44,13 +44,15 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemBudget = 227 * 1024;
 constexpr int kMaxStages = 8;
 
-// silu and its derivative, from the hardware's base-2 exponential and
-// reciprocal (each within 2 ulp of fp32).
+// sigma(g) = 1 / (1 + e^-g), from the hardware's base-2 exponential and
+// reciprocal (each within 2 ulp of fp32).  The reciprocal is taken of a quarter
+// of the sum: it flushes results below 2^-126, and sigma falls below that at
+// g = -87.3 while g sigma(g) is a normal number as far as e^-g is finite (-88.7).
 __device__ __forceinline__ float sigmoid_f(float g) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(e, 1.0f)));
-  return s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(e, 0.25f, 0.25f)));
+  return __fmul_rn(s, 0.25f);
 }
 template <int ACT>
 __device__ __forceinline__ void act2(float g0, float g1, float &a0, float &a1) {
