@@ -59,5 +59,5 @@ def test_a_plan_keeps_the_memory_it_points_to(fp):
     new = [torch.empty(3_000_017, device="cuda") for _ in range(4)]
     assert at.isdisjoint(t.data_ptr() for t in new)
     del plan, new
-    new = [torch.empty(3_000_017, device="cuda") for _ in range(4)]
+    new = [torch.empty(3_000_017, device="cuda") for _ in range(6)]
     assert at <= {t.data_ptr() for t in new}
