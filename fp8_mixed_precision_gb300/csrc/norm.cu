@@ -51,10 +51,12 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 // rstd is kept as a pair hi + lo (lo: what fp32 cannot hold of it), and
 // y = r * (hi + lo) * w is rounded once: t + e is r * rstd to about 2^-45, and
-// the last fma adds e * w to t * w exactly.  Both layouts then quantize the
-// correctly rounded fp32 y (all but about one in a hundred, which are the
-// other neighbour of a near tie), so their codes are those of the exact norm
-// but for a handful in 10^8 and do not depend on the summation order.
+// the last fma adds e * w to t * w exactly.  With rstd within 2^-43 (the sum of
+// squares keeps its errors) both layouts quantize the correctly rounded fp32 y,
+// all but about one in 2^18, so their scales and codes are those of the exact
+// norm (none of 3 x 10^8 codes differs) and do not depend on the summation
+// order.  Squares summed in fp32 four at a time left rstd at 2^-24: one scale
+// in 15 and one code in 10^7 differed, in the same time.
 __device__ __forceinline__ void norm8(uint4 r, float hi, float lo, const float (&w)[8],
                                       float (&y)[8]) {
   using namespace gelu2;
@@ -129,6 +131,12 @@ struct NormFwd {
   float *row_scale, *row_scale_inv;
 };
 
+// Larger magnitude of each half of two bf16 pairs.
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 v = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&m),
+                                   __habs2(*reinterpret_cast<__nv_bfloat162 *>(&w)));
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 // bf16(x + res): the exact sum rounded once.
 __device__ __forceinline__ uint4 add8(uint4 x, uint4 res) {
   auto add = [](uint32_t a, uint32_t b) {
@@ -169,25 +177,43 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : kNormThreads)
     rv[j] = in ? a.x[base + vec(j)] : zero;
     sv[j] = in && a.res ? a.res[base + vec(j)] : zero;
   }
-  float ss = 0.0f, lo = 0.0f;
+  uint32_t most = 0;  // largest magnitude, bf16 pair
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     if (a.res) {
       rv[j] = add8(rv[j], sv[j]);
       if (live && vec(j) < nv) a.r[base + vec(j)] = rv[j];
     }
-    float p[8];
-    unpack8(rv[j], p);
-    // bf16 squares have 16 bits, so four of them add up with next to no
-    // rounding; every join of such sums carries its error along
+    most = absmax2(absmax2(absmax2(absmax2(most, rv[j].x), rv[j].y), rv[j].z), rv[j].w);
+  }
+  // Sums of the even and the odd columns, and their errors.  They start from the
+  // largest square of the thread, so that each addition has the larger operand
+  // in front: the part of a square that the sum takes up, and so the rest, is then
+  // exact (the fma forms the 16 bits of the square without rounding).
+  using namespace gelu2;
+  const float top = fmaxf(bf16lo(most), bf16hi(most));
+  const float start = top < 1e17f ? __fmul_rn(top, top) : 0.0f;  // not finite: as it comes
+  uint64_t s2 = dup(start), l2 = 0;
 #pragma unroll
-    for (int h = 0; h < 8; h += 4) {
-      float e;
-      const float q = fmaf(p[h + 3], p[h + 3],
-                           fmaf(p[h + 2], p[h + 2], fmaf(p[h + 1], p[h + 1], __fmul_rn(p[h], p[h]))));
-      two_sum(ss, q, ss, e);
-      lo = __fadd_rn(lo, e);
+  for (int j = 0; j < VPT; ++j) {
+    const uint32_t w4[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint64_t x = pk(bf16lo(w4[h]), bf16hi(w4[h]));
+      const uint64_t t = fma2(x, x, s2);
+      l2 = fma2(fma2(x, x, fma2(t, dup(-1.0f), s2)), dup(1.0f), l2);
+      s2 = t;
     }
+  }
+  float ss, lo;
+  {
+    float even, odd, le, lod, e0, e1, e2;
+    upk(s2, even, odd);
+    upk(l2, le, lod);
+    two_sum(even, -start, even, e0);
+    two_sum(odd, -start, odd, e1);
+    two_sum(even, odd, ss, e2);
+    lo = __fadd_rn(__fadd_rn(__fadd_rn(le, e0), __fadd_rn(lod, e1)), e2);
   }
 #pragma unroll
   for (int o = LANES / 2; o; o >>= 1) {
