@@ -9,8 +9,9 @@
 // cover tensors of any number and size.  Bound by memory: the first pass reads
 // every gradient once, the second reads it again (from L2 where it still is)
 // and writes it once; a set of few chunks takes one kernel that does both.  Sums
-// are fp32 per thread and CTA and pairs of fp32 over the CTAs, in an order that
-// depends on the table and the GPU alone.
+// are fp32 within a thread's part of a chunk, pairs of fp32 over its chunks, fp32
+// within a CTA and pairs over the CTAs, in an order that depends on the table and
+// the GPU alone.
 #include <algorithm>
 
 #include "common.cuh"
@@ -78,6 +79,19 @@ __device__ __forceinline__ float clip_coef(float norm, float max_norm) {
   return isfinite(norm) ? fminf(1.0f, __fdiv_rn(max_norm, norm + 1e-6f)) : 1.0f;
 }
 
+// A sum as an unevaluated pair of fp32 (about 48 bits): this GPU's fp64 rate is
+// so low that forming the norm in it took 1.2 us longer.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const float s = __fadd_rn(a.hi, b.hi);
+  const float z = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, z)), __fsub_rn(b.hi, z));
+  // an infinite sum stays one (its error term would be a NaN)
+  return {s, isfinite(s) ? __fadd_rn(e, __fadd_rn(a.lo, b.lo)) : 0.0f};
+}
+
 // Sum over the CTA's 512 threads, in a fixed order; thread 0 has the result.
 __device__ __forceinline__ float block_sum(float v) {
   __shared__ float red[kClipThreads / 32];
@@ -111,12 +125,13 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_norm_kernel(const ClipCh
                                                                     int64_t chunks,
                                                                     float *__restrict__ partials) {
   pdl_wait_then_release();
-  float a[4] = {};
+  Pair sum = {0.0f, 0.0f};
   int64_t id = blockIdx.x;
   ClipChunk c = {};
   if (id < chunks) c = table[id];
   while (id < chunks) {
     const int nv = vectors_of(c);
+    float a[4] = {};
     uint4 w[kAhead];
     request(c, nv, w);
     const ClipChunk now = c;
@@ -133,22 +148,12 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_norm_kernel(const ClipCh
       const float v = load1(now, e);
       a[0] = fmaf(v, v, a[0]);
     }
+    // closed here, so that no chain is longer than a chunk's, however large the set
+    // (2^31 equal values, one chain: the norm 430 units of roundoff off)
+    sum = add(sum, Pair{(a[0] + a[1]) + (a[2] + a[3]), 0.0f});
   }
-  const float s = block_sum((a[0] + a[1]) + (a[2] + a[3]));
+  const float s = block_sum(__fadd_rn(sum.hi, sum.lo));
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
-}
-
-// A sum as an unevaluated pair of fp32 (about 48 bits): this GPU's fp64 rate is
-// so low that forming the norm in it took 1.2 us longer.
-struct Pair {
-  float hi, lo;
-};
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-  const float s = __fadd_rn(a.hi, b.hi);
-  const float z = __fsub_rn(s, a.hi);
-  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, z)), __fsub_rn(b.hi, z));
-  // an infinite sum stays one (its error term would be a NaN)
-  return {s, isfinite(s) ? __fadd_rn(e, __fadd_rn(a.lo, b.lo)) : 0.0f};
 }
 
 // Every warp forms the norm from the partials, in the same order.
