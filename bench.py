@@ -683,7 +683,7 @@ def run_ours(args):
             "baseline_note": "vs_baseline divides by the RTX 4090 fused-layout FP8 figures of "
                              "the reconstruction's table (context only)",
         }
-        print(json.dumps(line), flush=True)
+        report(line, args.details)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
@@ -1198,6 +1198,42 @@ def _link_GBps(dev, nbytes=1 << 30):
     return best
 
 
+def _short(v):
+    """v with floats at six significant digits."""
+    if isinstance(v, float):
+        return float(f"{v:.6g}")
+    if isinstance(v, dict):
+        return {k: _short(x) for k, x in v.items()}
+    return [_short(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+
+def headline(line):
+    """The result line without its long parts: per-instantiation rooflines, input
+    hashes and step groups are left out, and a workload keeps its own figures
+    without those of its kernels and samples."""
+    out = {k: v for k, v in line.items() if k not in ("input_sha256", "workloads")}
+    out["roofline"] = {k: v for k, v in line["roofline"].items() if k != "per_instantiation"}
+    out["step_ms_groups"] = {k: v for k, v in line["step_ms_groups"].items() if k != "groups"}
+    if line.get("workloads") is not None:
+        out["workloads"] = {name: {k: v for k, v in w.items() if isinstance(v, (int, float))}
+                            for name, w in line["workloads"].items()}
+        out["workloads"] = {name: w for name, w in out["workloads"].items() if w}
+    return dict(_short(out), value=line["value"], ms_per_step=line["ms_per_step"])
+
+
+def report(line, details=None):
+    """One line on standard output; everything measured goes to the file
+    `details`, or to standard error (a line of 50 KB is cut where output is
+    kept in part, and its headline lost)."""
+    whole = json.dumps(line)
+    if details:
+        with open(details, "w") as f:
+            f.write(whole + "\n")
+    else:
+        print(whole, file=sys.stderr, flush=True)
+    print(json.dumps(headline(line)), flush=True)
+
+
 def run_e2e(fp, layers, cache, ws, ctx, N, dev, world, args, stream):
     """Same step through the C ABI's host-buffer entry point
     (fp8_linear_step_host): every input is copied from pinned host memory and
@@ -1270,6 +1306,8 @@ def main(argv=None):
                          "serial: every kernel on one stream")
     ap.add_argument("--no-mlp", action="store_true",
                     help="skip the MLP-level workloads reported beside the main line")
+    ap.add_argument("--details", default=None,
+                    help="file for everything measured (default: standard error)")
     ap.add_argument("--oracle-timing", default=None, help=argparse.SUPPRESS)
     args = ap.parse_args(argv)
     if args.oracle_timing is not None:     # internal: one CPU-oracle timing run (subprocess)
