@@ -949,6 +949,7 @@ struct __align__(128) BSmem {
   float colsc[2][128];
   float rowsc[2][128];         // row maxima, then row scales
   uint64_t full;
+  int abort;
 };
 
 __device__ __forceinline__ int swz(int r) { return ((r >> 4) & 7) << 2; }
@@ -970,6 +971,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int64_t F2 = 2 * p.F;
   if (t == 0) {
     ptx::mbar_init(&S.full, 1);
+    S.abort = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tmD);
     ptx::tma_prefetch_desc(&tmG);
@@ -988,12 +990,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   int64_t id = blockIdx.x;
   prefetch(id);
-  volatile int no_abort = 0;
+  volatile int *abort = &S.abort;
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
     const int64_t tr = id / tiles_c, tc = id % tiles_c;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     const int rows_here = (int)(p.N - r0 < 128 ? p.N - r0 : 128);
-    pipe::wait_bar(&S.full, k & 1, &no_abort, &g_gated_status);  // on expiry: recorded, carry on
+    pipe::wait_bar(&S.full, k & 1, abort, &g_gated_status);
     uint4 in[3][4];  // dH, G, U of this thread's 4 rows
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -1006,6 +1008,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dgu8<ACT>(in[0][i], in[1][i], in[2][i], v[0][i], v[1][i]);
     __syncthreads();  // the buffers are read, and the last tile's transpose too
+    if (*abort) {     // given up (every thread sees it): what was asked for lands before the CTA leaves
+      if (t == 0) pipe::drain_wait(&S.full, k & 1, &g_gated_status);
+      return;
+    }
     prefetch(id + gridDim.x);
 #pragma unroll
     for (int z = 0; z < 2; ++z) {

@@ -21,7 +21,6 @@ namespace fp8lin {
 namespace {
 
 __device__ unsigned g_norm_status;
-constexpr uint64_t kNWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kNormThreads = 256;
 
 // Norm weight: bf16 or fp32, eight consecutive values.
@@ -301,21 +300,9 @@ struct __align__(128) CSmem {
   float colsc[kColTile];
   float2 rs[128];
   uint64_t full[2];
+  int abort;
 };
 
-// Bounded wait for a tile; on expiry the status word records FP8_ERR_TIMEOUT
-// and the caller carries on (its results are then invalid).
-__device__ __forceinline__ void wait_tile(uint64_t *bar, uint32_t parity) {
-  if (ptx::mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = ptx::globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (ptx::mbar_try_wait(bar, parity)) return;
-    if ((it & 63) == 0 && ptx::globaltimer() - t0 > kNWaitLimitNs) {
-      atomicCAS(&g_norm_status, 0u, (unsigned)FP8_ERR_TIMEOUT);
-      return;
-    }
-  }
-}
 // Word w (4 columns) of tile row r.  The padding puts the transpose's lanes (8
 // groups of 16 rows, 4 words) on 32 different banks.
 __device__ __forceinline__ int tile_word(int r, int w) {
@@ -340,6 +327,7 @@ __global__ void __launch_bounds__(kColThreads, 4)
   if (t == 0) {
     ptx::mbar_init(&S.full[0], 1);
     ptx::mbar_init(&S.full[1], 1);
+    S.abort = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tmr);
   }
@@ -353,6 +341,7 @@ __global__ void __launch_bounds__(kColThreads, 4)
     ptx::tma_load_2d(S.in[b], &tmr, &S.full[b], (int)(tc * kColTile), (int)(tr * 128));
   };
   int64_t id = blockIdx.x;
+  volatile int *abort = &S.abort;
   prefetch(id, 0);
   prefetch(id + gridDim.x, 1);
   for (int k = 0; id < ntiles; ++k, id += gridDim.x) {
@@ -364,8 +353,9 @@ __global__ void __launch_bounds__(kColThreads, 4)
     float w8[8] = {};
     if (8 * cg < cols_here) load_w8(p.w, c0 + 8 * cg, w8);
     S.rs[t] = t < rows_here ? make_float2(p.rstd[r0 + t], p.rstd_lo[r0 + t]) : make_float2(0.0f, 0.0f);
-    wait_tile(&S.full[b], (k >> 1) & 1);
+    pipe::wait_bar(&S.full[b], (k >> 1) & 1, abort, &g_norm_status);
     __syncthreads();
+    const bool gave_up = *abort;  // the same for every thread
     float y[8][8];  // rows rr + 16 i; tokens past R: zeros
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -392,6 +382,14 @@ __global__ void __launch_bounds__(kColThreads, 4)
       dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
     }
     __syncthreads();
+    if (gave_up) {  // what was asked for lands before the CTA leaves
+      if (t == 0) {
+        pipe::drain_wait(&S.full[b], (k >> 1) & 1, &g_norm_status);
+        if (id + gridDim.x < ntiles)
+          pipe::drain_wait(&S.full[b ^ 1], ((k + 1) >> 1) & 1, &g_norm_status);
+      }
+      return;
+    }
     prefetch(id + 2 * (int64_t)gridDim.x, b);  // every thread holds its elements
     if (t < kColTile) {
       const float m = fmaxf(fmaxf(S.colred[0][t], S.colred[1][t]),
@@ -473,13 +471,9 @@ __device__ __forceinline__ void ring_produce(RingCtl *ctl, uint8_t *ring, int st
                                              const void *const (&in)[NIN]) {
   volatile int *abort = &ctl->abort;
   int issued = 0;
-  bool ok = true;
   for (int64_t row0 = (int64_t)blockIdx.x * group; row0 < R; row0 += (int64_t)gridDim.x * group) {
     const int s = issued % stages;
-    if (!pipe::wait_bar(&ctl->empty[s], ((issued / stages) & 1) ^ 1, abort, &g_norm_status)) {
-      ok = false;
-      break;
-    }
+    if (!pipe::wait_bar(&ctl->empty[s], ((issued / stages) & 1) ^ 1, abort, &g_norm_status)) break;
     const int64_t rows = R - row0 < group ? R - row0 : group;
     const uint32_t bytes = (uint32_t)(rows * row_bytes);
     uint32_t all = 0;
@@ -494,9 +488,9 @@ __device__ __forceinline__ void ring_produce(RingCtl *ctl, uint8_t *ring, int st
                        static_cast<const uint8_t *>(in[k]) + row0 * row_bytes, bytes, &ctl->full[s]);
     ++issued;
   }
-  if (!ok)  // the copies in flight land before the CTA can exit
-    for (int i = max(0, issued - stages); i < issued; ++i)
-      pipe::drain_wait(&ctl->full[i % stages], (uint32_t)((i / stages) & 1), &g_norm_status);
+  // the last copies land before the CTA can exit, also if the warps gave up on one
+  for (int i = max(0, issued - stages); i < issued; ++i)
+    pipe::drain_wait(&ctl->full[i % stages], (uint32_t)((i / stages) & 1), &g_norm_status);
 }
 __device__ __forceinline__ void ring_init(RingCtl *ctl, int stages, int warps) {
   if (threadIdx.x == 0) {
