@@ -913,7 +913,7 @@ fp8_status fp8_gated_fwd(const void *X, int64_t N, int64_t K, fp8_weight_cache *
     return from_cuda(launch_gated_fwd(nullptr, nullptr, e->w_row, e->row_scale_inv, N, K, F, block,
                                       act, H, nullptr, nullptr, cs(stream), X));
   if (gated_quantizes_few(N, K, block))
-    st = from_cuda(launch_gated_quantize_few(X, N, K, block, w + L.xq, col, xsi, cscale_inv,
+    st = from_cuda(launch_gated_quantize_few(X, N, K, block, w + L.xq, col, xsi, cscale, cscale_inv,
                                              cs(stream)));
   else
     st = from_cuda(launch_quantize(X, N, K, block ? 1 : 0, FP8_FORMAT_E4M3, w + L.xq, col,

@@ -722,7 +722,7 @@ template <bool BLOCK>
 __global__ void __launch_bounds__(kFewThreads)
     gated_quant_few_kernel(const uint4 *__restrict__ x, int N, int64_t K, uint8_t *__restrict__ row,
                            uint8_t *__restrict__ col, float *__restrict__ row_scale_inv,
-                           float *__restrict__ col_scale_inv) {
+                           float *__restrict__ col_scale, float *__restrict__ col_scale_inv) {
   __shared__ float red[8];
   __shared__ float colmx[16][128];
   __shared__ float colsc[128];
@@ -757,7 +757,10 @@ __global__ void __launch_bounds__(kFewThreads)
     scale_from_amax(m, kE4M3Max, ts, si);
     if (blockIdx.x == 0 && t == 0) {
       row_scale_inv[0] = si;
-      if (col) col_scale_inv[0] = si;
+      if (col) {
+        col_scale[0] = ts;
+        col_scale_inv[0] = si;
+      }
     }
   }
   float cm[8] = {};
@@ -801,7 +804,10 @@ __global__ void __launch_bounds__(kFewThreads)
       for (int k = 0; k < 16; ++k) m = fmaxf(m, colmx[k][t]);
       scale_from_amax(m, kE4M3Max, s, si);
       colsc[t] = s;
-      if (t < cols_here) col_scale_inv[c0 + t] = si;
+      if (t < cols_here) {
+        col_scale[c0 + t] = s;
+        col_scale_inv[c0 + t] = si;
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -1333,14 +1339,14 @@ bool gated_quantizes_few(int64_t N, int64_t K, bool block) {
 }
 
 cudaError_t launch_gated_quantize_few(const void *x, int64_t N, int64_t K, bool block, uint8_t *row,
-                                      uint8_t *col, float *row_scale_inv, float *col_scale_inv,
-                                      cudaStream_t st) {
+                                      uint8_t *col, float *row_scale_inv, float *col_scale,
+                                      float *col_scale_inv, cudaStream_t st) {
   LaunchScope ls(block ? "gated_quant_few_block" : "gated_quant_few_tensor", st,
                  (col ? 4.0 : 3.0) * N * K, 0.0, N, K);
   auto kernel = block ? gated_quant_few_kernel<true> : gated_quant_few_kernel<false>;
   return launch_kernel(kernel, dim3((unsigned)((K + 127) / 128)), dim3(kFewThreads), 0, st,
                        static_cast<const uint4 *>(x), (int)N, K, row, col, row_scale_inv,
-                       col_scale_inv);
+                       col_scale, col_scale_inv);
 }
 
 cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void *U, int64_t N,

@@ -168,8 +168,8 @@ bool gated_takes_bf16(int64_t N, int64_t K, int64_t F, bool block);
 // scales of launch_quantize; col may be null.
 bool gated_quantizes_few(int64_t N, int64_t K, bool block);
 cudaError_t launch_gated_quantize_few(const void *x, int64_t N, int64_t K, bool block, uint8_t *row,
-                                      uint8_t *col, float *row_scale_inv, float *col_scale_inv,
-                                      cudaStream_t st);
+                                      uint8_t *col, float *row_scale_inv, float *col_scale,
+                                      float *col_scale_inv, cudaStream_t st);
 // dG and dU, E5M2, as one [N, 2F] tensor and its transpose [2F, N rounded up
 // to 16].  Tensor scaling: row_scale_inv takes the one scale, partials
 // kMaxPartials floats.
