@@ -102,7 +102,6 @@ struct GatedCtl {
 };
 constexpr int kCtlBytes = (int)((sizeof(GatedCtl) + 127) / 128 * 128);
 
-template <bool SAVE>
 struct GCfg {
   static constexpr int kEpi = 8;
   static constexpr int kThreads = 32 * (2 + kEpi);
@@ -111,8 +110,7 @@ struct GCfg {
   static constexpr int kSlabBytes = 32 * 128;  // 32 tokens x 64 bf16 columns
   // One slab buffer per warp, which leaves room for a fourth operand stage
   // (131072 x 2048, K 512, keeping G and U: 302 us; two buffers, three stages 324)
-  static constexpr int kSlabs = 1;
-  static constexpr int kOutBytes = kEpi * kSlabs * kSlabBytes;
+  static constexpr int kOutBytes = kEpi * kSlabBytes;
   static constexpr int kRing = kSmemBudget - 1024 - kOutBytes - kCtlBytes;
   static constexpr int kStages = kRing / kStageBytes;
   static constexpr size_t kSmemBytes =
@@ -155,11 +153,11 @@ __device__ __forceinline__ void stage64(uint8_t *slab, int row, const uint32_t (
 }
 
 template <int SCALING, int ACT, bool SAVE>
-__global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
+__global__ void __launch_bounds__(GCfg::kThreads, 1)
     gated_fwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmG,
                      const __grid_constant__ CUtensorMap tmU, const GatedArgs g) {
-  using C = GCfg<SAVE>;
+  using C = GCfg;
   constexpr bool kTensor = SCALING == FP8_SCALING_TENSOR;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -213,7 +211,9 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
           uint8_t *sa = smem + (size_t)stage * C::kStageBytes;
           ptx::mbar_arrive_expect_tx(&ctl->full[stage], C::kStageBytes);
           ptx::tma_load_2d(sa, &tmX, &ctl->full[stage], kb * BK, tm * BM);
-          // gate rows, then the up rows of the same columns (past the weight: zeros)
+          // gate rows, then the up rows of the same columns.  Of a ragged last tile the
+          // gate part reads on into Wu and the up part past the weight (zeros): columns
+          // that are not stored
           ptx::tma_load_2d(sa + C::kStageA, &tmW, &ctl->full[stage], kb * BK, tf * BF);
           ptx::tma_load_2d(sa + C::kStageA + BF * BK, &tmW, &ctl->full[stage], kb * BK,
                            (int)g.F + tf * BF);
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
   } else {
     const int ew = warp - 2, q = warp & 3, h = ew >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 64);
-    uint32_t nacc = 0, nout = 0;
-    uint8_t *slabs = out_stage + (size_t)ew * C::kSlabs * C::kSlabBytes;
+    uint32_t nacc = 0;
+    uint8_t *slab = out_stage + (size_t)ew * C::kSlabBytes;
     float s_tensor = 0.0f;
     if (kTensor) s_tensor = __fmul_rn(g.x_sinv[0], g.w_sinv[0]);
     auto release_acc = [&](uint32_t ab) {
@@ -273,8 +273,7 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
     };
     auto emit = [&](const CUtensorMap *map, const uint32_t (&w)[32], int col0, int row0) {
-      uint8_t *slab = slabs + (nout % C::kSlabs) * C::kSlabBytes;
-      if (lane == 0) ptx::bulk_wait_read<C::kSlabs - 1>();
+      if (lane == 0) ptx::bulk_wait_read<0>();
       __syncwarp();
       stage64(slab, lane, w);
       ptx::fence_proxy_async_smem();
@@ -283,7 +282,6 @@ __global__ void __launch_bounds__(GCfg<SAVE>::kThreads, 1)
         ptx::tma_store_2d(map, slab, col0, row0);
         ptx::bulk_commit();
       }
-      ++nout;
     };
     for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {
       int tm, tf;
@@ -1129,7 +1127,7 @@ cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
 
 template <int SCALING, int ACT, bool SAVE>
 cudaError_t launch_fwd(const CUtensorMap (&m)[5], const GatedArgs &g, cudaStream_t st) {
-  using C = GCfg<SAVE>;
+  using C = GCfg;
   static bool done[64];
   const cudaError_t e = opt_in_smem(gated_fwd_kernel<SCALING, ACT, SAVE>, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;

@@ -170,9 +170,9 @@ bool gated_quantizes_few(int64_t N, int64_t K, bool block);
 cudaError_t launch_gated_quantize_few(const void *x, int64_t N, int64_t K, bool block, uint8_t *row,
                                       uint8_t *col, float *row_scale_inv, float *col_scale,
                                       float *col_scale_inv, cudaStream_t st);
-// dG and dU, E5M2, as one [N, 2F] tensor and its transpose [2F, N rounded up
-// to 16].  Tensor scaling: row_scale_inv takes the one scale, partials
-// kMaxPartials floats.
+// dG and dU, E5M2, as one [N, 2F] tensor; block scaling: its transpose [2F, N
+// rounded up to 16] too.  Tensor scaling: no transpose (col and col_scale_inv
+// unused), row_scale_inv takes the one scale, partials kMaxPartials floats.
 cudaError_t launch_gated_bwd_quantize(const void *dH, const void *G, const void *U, int64_t N,
                                       int64_t F, bool block, int act, uint8_t *row, uint8_t *col,
                                       float *row_scale_inv, float *col_scale_inv, float *partials,

@@ -13,18 +13,13 @@ namespace pipe {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr uint64_t kDrainLimitNs = 100000000ull;  // 0.1 s
 
-// Wait for phase `parity` of `bar`; false on abort or timeout.  CLUSTER: the
-// barrier's arrivals may come from another CTA of the cluster.
-template <bool CLUSTER = false>
+// Wait for phase `parity` of `bar`; false on abort or timeout.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          unsigned *status) {
-  auto probe = [&]() {
-    return CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-  };
-  if (probe()) return true;
+  if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t it = 1;; ++it) {
-    if (probe()) return true;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     if ((it & 63) == 0) {
       if (*abort) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
