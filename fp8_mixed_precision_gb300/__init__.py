@@ -994,6 +994,19 @@ def fp8_gated_bwd(dh: torch.Tensor, ctx: GatedContext, cache: WeightCache, h: in
 
 
 # ---------------------------------------------------------------- gradient clipping
+def _disjoint(src, dst):
+    """Each dst is its own src or apart from it, and apart from all others."""
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i, w)
+             for w, ts in enumerate((src, dst)) for i, t in enumerate(ts) if t.numel()]
+    far = ([], [])  # the two furthest ends so far of sources and of outputs (one may be the tensor's own)
+    for lo, hi, i, w in sorted(spans):
+        for w2 in (0, 1):
+            for hi2, lo2, i2 in far[w2]:
+                if lo < hi2 and (w or w2) and not (w != w2 and i == i2 and (lo, hi) == (lo2, hi2)):
+                    raise ValueError("clipped tensors must not overlap (out may be the gradients themselves)")
+        far[w][:] = sorted(far[w] + [(hi, lo, i)])[-2:]
+
+
 class GradClip:
     """Global norm and clipping of a fixed set of gradient tensors (bf16 or
     float32, contiguous, any sizes).  out: tensors of the same types and sizes
@@ -1018,6 +1031,7 @@ class GradClip:
             dev = self.grads[0].get_device()
             _need(g, "gradient", g.shape, g.dtype, dev)
             _need(o, "out", g.shape, g.dtype, dev)
+        _disjoint(self.grads, self.out)
         self._memory = [t.detach() for t in self.grads + self.out]
         n = len(self.grads)
         descs = (_GradDesc * max(n, 1))(*[_GradDesc(g.data_ptr(), o.data_ptr(), g.numel(),

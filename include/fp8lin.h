@@ -438,8 +438,9 @@ fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
  * sizes).  Its table goes into caller-owned device memory: write it into host
  * memory of fp8_grad_clip_table_size bytes, copy that to the device (8-byte
  * aligned) and pass it to every call.
- *   src, dst   device tensors of n elements, dst = src clips in place; any
- *              alignment of the element type (16-byte aligned ones are faster)
+ *   src, dst   device tensors of n elements, dst = src clips in place; a dst
+ *              overlaps no other tensor of the set.  Any alignment of the
+ *              element type (16-byte aligned ones are faster)
  *   max_norm   positive; infinity leaves every gradient as it is
  *   norm       device f32 [1]
  *   workspace  fp8_grad_clip_workspace_size bytes

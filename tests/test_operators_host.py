@@ -330,3 +330,19 @@ def test_norms_share_one_allocation_of_their_stream(fp, host, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True, raising=False)
     a, b = c.norm(), c.norm()
     assert len(host.made) == 6 and a.data_ptr() == host.made[-2][0].data_ptr() != b.data_ptr()
+
+
+def test_clipped_tensors_that_overlap_are_refused(fp, host):
+    """The same memory scaled by two chunks at once: neither order nor factor
+    would be certain.  Reading one tensor twice is fine."""
+    g, o = f32(4096), f32(4096)
+    a = dev(torch.zeros(8192))
+    for grads, out in (([g, g], None), ([g, g[100:200]], None), ([g, f32(4096)], [o, o]), ([a[:4096]], [a[1:4097]]),
+                       ([a[:4096], a[4096:]], [a[4096:], a[:4096]]), ([g, o], [f32(4096), g]),
+                       ([a[:100], a[50:150]], [f32(100), a[50:150]])):
+        with pytest.raises(ValueError):
+            fp.GradClip(grads, out)
+    fp.GradClip([g, g], [f32(4096), o])
+    fp.GradClip([a[:4096], a[4096:], a[5:5]])
+    fp.GradClip([a[:4096]], [a[4096:]])
+    fp.GradClip([g, f32(0), f32(0)])
