@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kClipThreads, 2) clip_scale_kernel(const ClipC
 // Few chunks (kClipFewChunks of kClipFewElements at most): one CTA does both
 // passes in one launch, 64 threads to a chunk, the gradients staying in registers
 // in between.  Bound by the launch and the round trips to memory: 9 vectors of
-// 515 floats take 3.6 us a call (2.7 in a graph), as the two kernels 5.2 (4.0); 16
-// full chunks 4.6 (4.4) against 5.2 (4.0).  A cluster of eight CTAs joined over
+// 515 floats take 3.6 us a library call (2.7 in a graph), as the two kernels 5.2
+// (4.0); 16 full chunks 4.6 (4.4) against 5.2 (4.0).  A cluster of eight CTAs joined over
 // distributed shared memory: 5.5.
 constexpr int kFewThreads = 1024, kFewGroup = kFewThreads / kClipFewChunks;
 static_assert(kClipFewElements / 4 == kAhead * kFewGroup, "a chunk's vectors fit its threads' registers");

@@ -349,7 +349,8 @@ fp8_status fp8_grad_accumulate(float *acc, const void *dW, int64_t n, fp8_stream
  *   r = bf16(x + residual) (residual NULL: r = x), rstd = (mean(r^2) + eps)^-1/2,
  *   y = r * rstd * w; the fp32 y is quantized as it is (E4M3, activation role of
  *   the block recipe, 1x128 blocks, scale rule as above) and/or rounded to bf16.
- *   Sums and rstd are carried as pairs of fp32, so that y is rounded once.
+ *   Sums and rstd are carried as pairs of fp32 (rstd within 2^-43), so that y is
+ *   rounded once.
  *   rows           any number of tokens; cols: a multiple of 16, at most 16384
  *   w              device bf16 or fp32 [cols], as w_dtype says
  *   eps            positive
@@ -395,7 +396,7 @@ fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const 
  *       multiple of 128 (the weight's 128x128 tiles must not straddle Wg and Wu)
  *   ctx device buffer of fp8_gated_ctx_size bytes for the backward pass (the
  *       transposed FP8 X and its scales, and both projections as bf16), or NULL
- *       when none follows
+ *       when none follows; of the same recipe and shape in every call that takes it
  *   ws  device scratch of fp8_gated_workspace_size bytes (train = 0: enough for
  *       the forward pass alone)
  * fp8_gated_fwd_quantized: X given as its rowwise bytes and scale_inv (e.g.
@@ -403,7 +404,8 @@ fp8_status fp8_rmsnorm_bwd(const void *dy, const void *dr, const void *r, const 
  *   part (fp8_gated_ctx_layout says where).
  * fp8_gated_bwd: with G and U as the forward pass kept them (bf16),
  *   dG = (dH * U) * act'(G), dU = dH * act(G) in fp32, cast to E5M2 as one
- *   [N, 2F] tensor (block recipe: in both layouts, each with its own blocks); dX = dGU W (or NULL), dW = dGU^T X [2F, K],
+ *   [N, 2F] tensor (block recipe: in both layouts, each with its own blocks);
+ *   dX = dGU W (or NULL), dW = dGU^T X [2F, K],
  *   the forward's rounded W and X reused (bf16; dW zeros when N = 0).
  * act: silu(g) = g / (1 + e^-g), or GELU in its exact erf form.
  * Weight-cache and recipe rules as fp8_linear_fwd / bwd (delayed recipe: its
@@ -434,6 +436,7 @@ fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
  *   norm = sqrt(sum of g^2 over all tensors), coef = min(1, max_norm / (norm + 1e-6)),
  *   dst = g * coef.  A norm that is not finite (an inf or NaN gradient, or squares
  *   past the fp32 range) leaves coef at 1, so the caller reads `norm` and decides.
+ *   Squares below the fp32 range (of gradients under about 1e-22) are lost.
  * A plan is a host object made once for a set of tensors (their addresses and
  * sizes).  Its table goes into caller-owned device memory: write it into host
  * memory of fp8_grad_clip_table_size bytes, copy that to the device (8-byte
@@ -443,7 +446,7 @@ fp8_status fp8_gated_bwd(const void *dH, int64_t N, int64_t F, const void *ctx,
  *              element type (16-byte aligned ones are faster)
  *   max_norm   positive; infinity leaves every gradient as it is
  *   norm       device f32 [1]
- *   workspace  fp8_grad_clip_workspace_size bytes
+ *   workspace  fp8_grad_clip_workspace_size bytes, of one call at a time
  * fp8_grad_norm: the norm alone; nothing else is written.
  * Deterministic for a plan on a GPU.
  * Errors: INVALID_ARG, ALIGN, WORKSPACE, CUDA. */
