@@ -1,9 +1,9 @@
 """Python binding of the GB300 FP8 linear-layer library (libfp8lin.so).
 
 Argument marshalling only: every function below allocates its outputs with
-torch on the current CUDA device, passes raw device pointers and the current
-stream to the C ABI declared in include/fp8lin.h, and raises FP8Error on a
-non-OK status.  Names follow the C ABI.  There is no fallback: if the
+torch on the current CUDA device and the call's stream (`stream`, by default
+the current one), passes raw device pointers and that stream to the C ABI
+declared in include/fp8lin.h, and raises FP8Error on a non-OK status.  Names follow the C ABI.  There is no fallback: if the
 compiled library is missing, importing works but the first call raises.
 """
 from __future__ import annotations
@@ -203,6 +203,18 @@ def _stream(stream=None):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Calls make their tensors under the stream that their kernels run on, as
+    `with torch.cuda.stream(stream)` would: the memory is then free of earlier
+    work in that stream's order and goes back to it in that order.
+    What a call returns belongs to that stream; what it is given has to be
+    ready there, and kept until the work is done."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
 def _need_bf16_cuda(t, name):
     if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
@@ -241,18 +253,18 @@ def fp8_quantize(x: torch.Tensor, recipe: str, role: str, rowwise: bool = True,
                col_scale_inv=None)
     rs = fp8_scale_shape(recipe, role, R, C, False)
     cs = fp8_scale_shape(recipe, role, R, C, True)
-    if rowwise or recipe == "tensorwise":
-        out["row_scale"] = torch.empty(rs, dtype=torch.float32, device=dev)
-        out["row_scale_inv"] = torch.empty(rs, dtype=torch.float32, device=dev)
-    if colwise:
-        out["col_scale"] = torch.empty(cs, dtype=torch.float32, device=dev)
-        out["col_scale_inv"] = torch.empty(cs, dtype=torch.float32, device=dev)
-    if rowwise:
-        out["row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-    if colwise:
-        out["col"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
-    wsb = _quant_ws_bytes(recipe, R, C)
-    ws = _empty_bytes(wsb, dev)
+    with _on(stream):
+        if rowwise or recipe == "tensorwise":
+            out["row_scale"] = torch.empty(rs, dtype=torch.float32, device=dev)
+            out["row_scale_inv"] = torch.empty(rs, dtype=torch.float32, device=dev)
+        if colwise:
+            out["col_scale"] = torch.empty(cs, dtype=torch.float32, device=dev)
+            out["col_scale_inv"] = torch.empty(cs, dtype=torch.float32, device=dev)
+        if rowwise:
+            out["row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        if colwise:
+            out["col"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
+        ws = _empty_bytes(_quant_ws_bytes(recipe, R, C), dev)
     _check(lib().fp8_quantize(_ptr(x), R, C, RECIPE[recipe], ROLE[role], _ptr(out["row"]),
                               _ptr(out["col"]), _ptr(out["row_scale"]), _ptr(out["row_scale_inv"]),
                               _ptr(out["col_scale"]), _ptr(out["col_scale_inv"]), _ptr(ws),
@@ -269,11 +281,12 @@ def fp8_quantize_delayed(x: torch.Tensor, role: str, history: torch.Tensor, step
         raise ValueError("history must be a float32 CUDA tensor")
     R, C = x.shape
     dev = x.device
-    out = dict(row=torch.empty((R, C), dtype=torch.uint8, device=dev) if rowwise else None,
-               col=torch.empty((C, R), dtype=torch.uint8, device=dev) if colwise else None,
-               scale=torch.empty(1, dtype=torch.float32, device=dev),
-               scale_inv=torch.empty(1, dtype=torch.float32, device=dev))
-    ws = _empty_bytes(_quant_ws_bytes("tensorwise", R, C), dev)
+    with _on(stream):
+        out = dict(row=torch.empty((R, C), dtype=torch.uint8, device=dev) if rowwise else None,
+                   col=torch.empty((C, R), dtype=torch.uint8, device=dev) if colwise else None,
+                   scale=torch.empty(1, dtype=torch.float32, device=dev),
+                   scale_inv=torch.empty(1, dtype=torch.float32, device=dev))
+        ws = _empty_bytes(_quant_ws_bytes("tensorwise", R, C), dev)
     _check(lib().fp8_quantize_delayed(_ptr(x), R, C, ROLE[role], _ptr(out["row"]), _ptr(out["col"]),
                                       _ptr(out["scale"]), _ptr(out["scale_inv"]), _ptr(history),
                                       history.numel(), int(step), _ptr(ws), ws.numel(),
@@ -290,11 +303,12 @@ def fp8_gemm(a: torch.Tensor, a_fmt: str, a_scale_inv: torch.Tensor, b: torch.Te
     if K2 != K:
         raise ValueError("inner dimensions differ")
     dev = a.device
-    C = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     wsb = _c_sz()
     _check(lib().fp8_gemm_workspace_size(M, N, K, SCALING[scaling], ctypes.byref(wsb)),
            "fp8_gemm_workspace_size")
-    ws = _empty_bytes(wsb.value, dev)
+    with _on(stream):
+        C = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        ws = _empty_bytes(wsb.value, dev)
     _check(lib().fp8_gemm(_ptr(a), FORMAT[a_fmt], _ptr(a_scale_inv), _ptr(b), FORMAT[b_fmt],
                           _ptr(b_scale_inv), M, N, K, SCALING[scaling], _ptr(C), _ptr(ws),
                           wsb.value, _stream(stream)), "fp8_gemm")
@@ -411,12 +425,13 @@ def fp8_linear_fwd(x: torch.Tensor, cache: WeightCache, h: int, recipe: str,
     N, K = x.shape
     O = cache.entries[h].w.shape[0]
     dev = x.device
-    if y is None:
-        y = torch.empty((N, O), dtype=torch.bfloat16, device=dev)
-    if ctx is None:
-        ctx = LinearContext(_empty_bytes(_ctx_bytes(recipe, N, K), dev), N, K)
-    if ws is None:
-        ws = linear_workspace(recipe, N, K, O, dev)
+    with _on(stream):
+        if y is None:
+            y = torch.empty((N, O), dtype=torch.bfloat16, device=dev)
+        if ctx is None:
+            ctx = LinearContext(_empty_bytes(_ctx_bytes(recipe, N, K), dev), N, K)
+        if ws is None:
+            ws = linear_workspace(recipe, N, K, O, dev)
     _check(lib().fp8_linear_fwd(_ptr(x), N, K, cache.handle, h, RECIPE[recipe], _ptr(y),
                                 _ptr(ctx.ctx), _ptr(ws), ws.numel(), _stream(stream)),
            "fp8_linear_fwd")
@@ -431,12 +446,13 @@ def fp8_linear_bwd(dy: torch.Tensor, ctx: LinearContext, cache: WeightCache, h: 
     N, O = dy.shape
     K = ctx.K
     dev = dy.device
-    if need_dx and dx is None:
-        dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    if dw is None:
-        dw = torch.empty((O, K), dtype=torch.bfloat16, device=dev)
-    if ws is None:
-        ws = linear_workspace(recipe, N, K, O, dev)
+    with _on(stream):
+        if need_dx and dx is None:
+            dx = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        if dw is None:
+            dw = torch.empty((O, K), dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = linear_workspace(recipe, N, K, O, dev)
     _check(lib().fp8_linear_bwd(_ptr(dy), N, O, _ptr(ctx.ctx), cache.handle, h, RECIPE[recipe],
                                 _ptr(dx) if need_dx else None, _ptr(dw), _ptr(ws), ws.numel(),
                                 _stream(stream)), "fp8_linear_bwd")
@@ -445,7 +461,8 @@ def fp8_linear_bwd(dy: torch.Tensor, ctx: LinearContext, cache: WeightCache, h: 
 
 def fp8_gelu_fwd(h: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _need_bf16_cuda(h, "h")
-    a = out if out is not None else torch.empty_like(h)
+    with _on(stream):
+        a = out if out is not None else torch.empty_like(h)
     _check(lib().fp8_gelu_fwd(_ptr(h), _ptr(a), h.numel(), _stream(stream)), "fp8_gelu_fwd")
     return a
 
@@ -454,7 +471,8 @@ def fp8_gelu_bwd(da: torch.Tensor, h: torch.Tensor, out: torch.Tensor | None = N
                  stream=None) -> torch.Tensor:
     _need_bf16_cuda(da, "da")
     _need_bf16_cuda(h, "h")
-    dh = out if out is not None else torch.empty_like(h)
+    with _on(stream):
+        dh = out if out is not None else torch.empty_like(h)
     _check(lib().fp8_gelu_bwd(_ptr(da), _ptr(h), _ptr(dh), h.numel(), _stream(stream)),
            "fp8_gelu_bwd")
     return dh
@@ -651,18 +669,6 @@ def fp8_linear_bwd_after_amax(dy: torch.Tensor, dy_partials: torch.Tensor, ctx: 
                                            _ptr(ws), ws.numel(), _stream(stream)),
            "fp8_linear_bwd_after_amax")
     return dx, dw
-
-
-def _on(stream):
-    """The calls below make their tensors under the stream that their kernels run
-    on, as `with torch.cuda.stream(stream)` would: the memory is then free of
-    earlier work in that stream's order and goes back to it in that order.
-    What a call returns belongs to that stream; what it is given has to be
-    ready there, and kept until the work is done."""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
-
-
-_CURRENT = contextlib.nullcontext()
 
 
 # ---------------------------------------------------------------- RMS norm

@@ -9,7 +9,7 @@ import torch
 # functions that enqueue work: recorded with their arguments, answered with 0
 LAUNCHING = ("fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd",
              "fp8_grad_clip_run", "fp8_grad_norm", "fp8_weight_cache_get", "fp8_linear_fwd", "fp8_linear_bwd",
-             "fp8_grad_accumulate")
+             "fp8_grad_accumulate", "fp8_quantize", "fp8_quantize_delayed", "fp8_gemm", "fp8_gelu_fwd", "fp8_gelu_bwd")
 
 
 class Dev(torch.Tensor):

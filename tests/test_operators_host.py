@@ -346,3 +346,33 @@ def test_clipped_tensors_that_overlap_are_refused(fp, host):
     fp.GradClip([a[:4096], a[4096:], a[5:5]])
     fp.GradClip([a[:4096]], [a[4096:]])
     fp.GradClip([g, f32(0), f32(0)])
+
+
+# ---------------------------------------------------------------- the linear's calls
+def test_tensors_of_the_linear_calls_come_from_their_stream(fp, host):
+    s = FakeStream(77)
+    cache, h = _weight(fp, "block")
+    x, dy = bf16(48, 256), bf16(48, 512)
+    u8 = dev(torch.zeros((48, 256), dtype=torch.uint8))
+
+    def only(at, count):
+        made, host.made[:] = list(host.made), []
+        assert len(made) == count and all(a == at for _, a in made)
+
+    host.made.clear()
+    for stream, at in ((s, 77), (None, 0)):
+        for recipe, count in (("block", 7), ("tensorwise", 7)):
+            fp.fp8_quantize(x, recipe, "act", stream=stream)
+            only(at, count)
+        fp.fp8_quantize_delayed(x, "act", f32(16), 0, stream=stream)
+        only(at, 5)
+        fp.fp8_gemm(u8, "e4m3", f32(1), u8, "e4m3", f32(1), "tensor", stream=stream)
+        only(at, 2)
+        _, ctx = fp.fp8_linear_fwd(x, cache, h, "block", stream=stream)
+        only(at, 3)
+        fp.fp8_linear_bwd(dy, ctx, cache, h, "block", stream=stream)
+        only(at, 3)
+        a = fp.fp8_gelu_fwd(x, stream=stream)
+        only(at, 1)
+        fp.fp8_gelu_bwd(a, x, stream=stream)
+        only(at, 1)
