@@ -682,7 +682,7 @@ def _bytes(t, name, dev):
     """The size of a workspace."""
     if not (t.get_device() == dev and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 class NormBuffers(dict):
@@ -917,11 +917,12 @@ def _gated_out(x, cache, h, recipe, y, ctx, train, stream):
     if x.get_device() != dev:
         raise ValueError(f"the input must be on cuda:{dev}, as the weight")
     F = w.shape[0] // 2
-    with _on(stream):
-        if y is None:
-            y = torch.empty((N, F), dtype=torch.bfloat16, device=x.device)
-        if train and ctx is None:
-            ctx = gated_context(recipe, N, K, F, x.device)
+    if y is None or (train and ctx is None):
+        with _on(stream):
+            if y is None:
+                y = torch.empty((N, F), dtype=torch.bfloat16, device=x.device)
+            if train and ctx is None:
+                ctx = gated_context(recipe, N, K, F, x.device)
     _need(y, "y", (N, F), torch.bfloat16, dev)
     if train:
         ctx.check(recipe, N, K, F, dev)
