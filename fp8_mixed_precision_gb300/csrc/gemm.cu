@@ -730,7 +730,8 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
         for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
         const int64_t mrow = m < g.M ? m : g.M - 1;  // clamp for the scale read only
         const float *arow = g.a_sinv + mrow * g.lds_a;
-        const float *bt = g.b_sinv + (colbase / 128) * g.lds_b;  // 128x128: this warp's column block
+        // 128x128: this warp's column block (a warp wholly past N reads the last one)
+        const float *bt = g.b_sinv + (min(colbase, g.N - 1) / 128) * g.lds_b;
         // Scales of K blocks kb .. kb+kPre-1 in a register ring (slot 0 = current):
         // the loads are issued kPre blocks before their use, hiding their latency.
         bool ok = true;
