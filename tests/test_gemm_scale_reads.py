@@ -11,9 +11,10 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 def _index():
     """The row of b_sinv that a warp whose columns start at colbase reads."""
     src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "gemm.cu")).read())
-    m = re.findall(r"const float \*bt = g\.b_sinv \+ \((.*?)\) \* g\.lds_b;", src)
+    m = re.findall(r"const uint32_t btile = \(uint32_t\)(.*?) / 128u;\s*"
+                   r"const float \*bt = g\.b_sinv \+ \(int64_t\)btile \* g\.lds_b;", src)
     assert len(m) == 1, m
-    return eval("lambda colbase, N: " + m[0].replace("g.N", "N").replace("/", "//"))
+    return eval(f"lambda colbase, N: {m[0].replace('g.N', 'N')} // 128")
 
 
 def test_rows_of_the_column_blocks_scales():
