@@ -26,6 +26,9 @@ __all__ = [
     "ACTIVATION", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "rmsnorm_buffers", "rmsnorm_workspace",
     "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd", "GatedContext", "gated_context",
     "gated_workspace", "gated_norm_columns", "fp8_gated_ctx_layout", "GradClip", "NormBuffers",
+    "SCORE", "fp8_route_fwd", "fp8_route_bwd", "ExpertOrder", "expert_rows", "fp8_expert_order",
+    "fp8_expert_gather", "fp8_expert_combine", "fp8_expert_combine_bwd", "W4Weight", "fp8_w4_quantize",
+    "fp8_w4_linear", "fp8_w4_gated", "fp8_w4_experts", "w4_experts_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +40,7 @@ FORMAT = {"e4m3": 0, "e5m2": 1}
 SCALING = {"tensor": 0, "1x128_128x128": 1, "1x128_1x128": 2}
 
 ACTIVATION = {"silu": 0, "gelu": 1}
+SCORE = {"softmax": 0, "sigmoid": 1}
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 _c_i64 = ctypes.c_int64
@@ -147,6 +151,35 @@ _SIGS.update({
     "fp8_grad_clip_workspace_size": (_c_int, [_c_p, ctypes.POINTER(_c_sz)]),
     "fp8_grad_clip_run": (_c_int, [_c_p, _c_p, ctypes.c_float, _c_p, _c_p, _c_sz, _c_p]),
     "fp8_grad_norm": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+})
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("codes", _c_p), ("scale", _c_p), ("zero", _c_p), ("E", _c_i64), ("rows", _c_i64),
+                ("K", _c_i64), ("group", _c_int)]
+
+
+_SIGS.update({
+    "fp8_route_fwd": (_c_int, [_c_p, _c_int, _c_p, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int,
+                               _c_int, _c_int, ctypes.c_float, _c_p, _c_p, _c_p]),
+    "fp8_route_bwd": (_c_int, [_c_p, _c_p, _c_int, _c_p, _c_p, _c_i64, _c_i64, _c_int, _c_int,
+                               _c_int, ctypes.c_float, _c_p, _c_p]),
+    "fp8_expert_rows": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+    "fp8_expert_order_workspace_size": (_c_int, [_c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fp8_expert_order": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz,
+                                  _c_p]),
+    "fp8_expert_gather": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                   _c_p, _c_p]),
+    "fp8_expert_combine": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "fp8_expert_combine_bwd": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_int, _c_i64, _c_i64] +
+                               [_c_p] * 7),
+    "fp8_w4_quantize": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "fp8_w4_linear": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_p, _c_p]),
+    "fp8_w4_gated": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_int, _c_p, _c_p]),
+    "fp8_w4_experts_workspace_size": (_c_int, [_c_i64, _c_int, _c_i64, _c_i64, _c_i64,
+                                               ctypes.POINTER(_c_sz)]),
+    "fp8_w4_experts": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_p, ctypes.POINTER(_W4),
+                                ctypes.POINTER(_W4), _c_int, _c_p, _c_p, _c_sz, _c_p]),
 })
 
 
@@ -1102,3 +1135,325 @@ class GradClip:
         if getattr(self, "_h", None) is not None and _lib is not None:
             _lib.fp8_grad_clip_destroy(self._h)
             self._h = None
+
+
+# ---------------------------------------------------------------- routing to experts
+def _here(t, name, stream):
+    """Index of t's device, which has to be the one that the call's stream is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if torch.cuda.is_initialized():
+        on = torch._C._cuda_getDevice() if stream is None else stream.device_index
+        if on != dev:
+            raise ValueError(f"{name} is on cuda:{dev}, the call's stream on cuda:{on}")
+    return dev
+
+
+def _route_input(logits, k, stream):
+    if logits.dtype not in _DTYPE or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous bf16 or float32 tensor [T, E]")
+    return (*logits.shape, _here(logits, "logits", stream))
+
+
+def fp8_route_fwd(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                  groups: int = 1, groups_kept: int | None = None, group_top: int = 1,
+                  renormalize: bool = True, scale: float = 1.0,
+                  out: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None):
+    """The k experts of each token and their weights, from logits [T, E] in bf16
+    or float32; returns (weights float32 [T, k], experts int32 [T, k]).  bias:
+    float32 [E], added to the scores for the choice alone; groups: only experts
+    of the groups_kept best of that many groups (by the sum of a group's
+    group_top best scores) are chosen.  Experts with a logit of -inf are never
+    chosen: slots left over have expert -1 and weight 0.  out: tensors to write."""
+    T, E, dev = _route_input(logits, k, stream)
+    if bias is not None:
+        _need(bias, "bias", (E,), torch.float32, dev)
+    if out is None:
+        with _on(stream):
+            w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+            e = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    else:
+        w, e = out
+        _need(w, "weights", (T, k), torch.float32, dev)
+        _need(e, "experts", (T, k), torch.int32, dev)
+    _check(lib().fp8_route_fwd(logits.data_ptr(), _DTYPE[logits.dtype], _ptr(bias), T, E, k, SCORE[score], groups,
+                               groups if groups_kept is None else groups_kept, group_top, renormalize, scale,
+                               w.data_ptr(), e.data_ptr(), _stream(stream)), "fp8_route_fwd")
+    return w, e
+
+
+def fp8_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor,
+                  score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits [T, E], in their type, from that of the weights;
+    logits, weights, experts, score, renormalize and scale of fp8_route_fwd."""
+    k = experts.shape[-1]
+    T, E, dev = _route_input(logits, k, stream)
+    _need(experts, "experts", (T, k), torch.int32, dev)
+    _need(weights, "weights", (T, k), torch.float32, dev)
+    _need(dweights, "dweights", (T, k), torch.float32, dev)
+    if out is None:
+        with _on(stream):
+            out = torch.empty_like(logits)
+    _need(out, "out", (T, E), logits.dtype, dev)
+    _check(lib().fp8_route_bwd(dweights.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype], weights.data_ptr(),
+                               experts.data_ptr(), T, E, k, SCORE[score], renormalize, scale, out.data_ptr(),
+                               _stream(stream)), "fp8_route_bwd")
+    return out
+
+
+# ---------------------------------------------------------------- rows in the experts' order
+@dataclass
+class ExpertOrder:
+    """The T k slots (t k + j: choice j of token t) sorted by expert.  counts [E]
+    and offsets [E + 1]: rows of each expert, where they begin (multiples of
+    align), and the rows in use; position [T, k]: a slot's row, -1 without an
+    expert; order [rows]: a row's slot, -1 in the gap behind an expert's rows,
+    undefined past offsets[E].  rows: the rows that any choice can need."""
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    position: torch.Tensor
+    order: torch.Tensor
+    T: int
+    k: int
+    E: int
+    align: int
+    rows: int
+
+
+def expert_rows(T: int, k: int, n_experts: int, align: int = 1) -> int:
+    """Rows of a buffer in the experts' order that any choice fits."""
+    return int(lib().fp8_expert_rows(T * k, n_experts, align))
+
+
+def fp8_expert_order(experts: torch.Tensor, n_experts: int, align: int = 1, out: ExpertOrder | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> ExpertOrder:
+    """The order of the choices experts int32 [T, k] (values outside 0 ..
+    n_experts - 1: no expert).  align = 16 gives every expert a row count that
+    the FP8 linear takes.  out: an order of the same shape to write again."""
+    if experts.dtype != torch.int32 or experts.dim() != 2 or not experts.is_contiguous():
+        raise ValueError("experts must be a contiguous int32 tensor [T, k]")
+    dev = _here(experts, "experts", stream)
+    T, k = experts.shape
+    E, slots = n_experts, T * k
+    b = _c_sz()
+    _check(lib().fp8_expert_order_workspace_size(slots, E, ctypes.byref(b)), "fp8_expert_order_workspace_size")
+    need = b.value
+    if out is None:
+        rows = expert_rows(T, k, E, align)
+        with _on(stream):
+            # one allocation (a call for few tokens is bound by the host)
+            m = torch.empty(2 * E + 1 + slots + rows, dtype=torch.int32, device=experts.device)
+        counts, offsets, position, order = m.split((E, E + 1, slots, rows))
+        out = ExpertOrder(counts, offsets, position.view(T, k), order, T, k, E, align, rows)
+    elif (out.T, out.k, out.E, out.align) != (T, k, E, align):
+        raise ValueError("out is an order of another shape")
+    else:
+        for t, name, shape in ((out.counts, "counts", (E,)), (out.offsets, "offsets", (E + 1,)),
+                               (out.position, "position", (T, k)), (out.order, "order", (out.rows,))):
+            _need(t, name, shape, torch.int32, dev)
+        if out.rows != expert_rows(T, k, E, align):
+            raise ValueError("out is an order of another shape")
+    if ws is None and need:
+        with _on(stream):
+            ws = _empty_bytes(need, experts.device)
+    _check(lib().fp8_expert_order(experts.data_ptr(), slots, E, align, out.counts.data_ptr(), out.offsets.data_ptr(),
+                                  out.position.data_ptr(), out.order.data_ptr(), _ptr(ws),
+                                  0 if ws is None else _bytes(ws, "ws", dev), _stream(stream)), "fp8_expert_order")
+    return out
+
+
+def _order_on(order: ExpertOrder, dev: int):
+    if order.position.get_device() != dev:
+        raise ValueError(f"order must be on cuda:{dev}")
+
+
+def fp8_expert_gather(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Token rows x [T, C] in the experts' order: [order.rows, C], zeros in the
+    gaps between experts, rows past order.offsets[E] as they were."""
+    _need_bf16_cuda(x, "x")
+    dev = _here(x, "x", stream)
+    _order_on(order, dev)
+    T, C = x.shape
+    if T != order.T:
+        raise ValueError(f"x must have {order.T} rows")
+    if out is None:
+        with _on(stream):
+            out = torch.empty((order.rows, C), dtype=torch.bfloat16, device=x.device)
+    _need(out, "out", (order.rows, C), torch.bfloat16, dev)
+    _check(lib().fp8_expert_gather(x.data_ptr(), T, C, order.k, order.E, order.align, order.counts.data_ptr(),
+                                   order.offsets.data_ptr(), order.position.data_ptr(), out.data_ptr(),
+                                   _stream(stream)), "fp8_expert_gather")
+    return out
+
+
+def fp8_expert_combine(z: torch.Tensor, order: ExpertOrder, weights: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] z[row of (t, j)], [T, C]; without weights the
+    plain sum, which is the backward pass of fp8_expert_gather."""
+    _need_bf16_cuda(z, "z")
+    dev = _here(z, "z", stream)
+    _order_on(order, dev)
+    T, k, C = order.T, order.k, z.shape[1]
+    if z.shape[0] != order.rows:
+        raise ValueError(f"z must have {order.rows} rows")
+    if weights is not None:
+        _need(weights, "weights", (T, k), torch.float32, dev)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, C), dtype=torch.bfloat16, device=z.device)
+    _need(out, "out", (T, C), torch.bfloat16, dev)
+    _check(lib().fp8_expert_combine(z.data_ptr(), T, C, k, order.position.data_ptr(), _ptr(weights), out.data_ptr(),
+                                    _stream(stream)), "fp8_expert_combine")
+    return out
+
+
+def fp8_expert_combine_bwd(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder, weights: torch.Tensor,
+                           dz: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
+    """Returns (dz [order.rows, C], dweights float32 [T, k]); dz is zero in the
+    gaps between experts and as it was past order.offsets[E]."""
+    _need_bf16_cuda(dy, "dy")
+    dev = _here(dy, "dy", stream)
+    _order_on(order, dev)
+    T, k, C = order.T, order.k, dy.shape[1]
+    _need(dy, "dy", (T, C), torch.bfloat16, dev)
+    _need(z, "z", (order.rows, C), torch.bfloat16, dev)
+    _need(weights, "weights", (T, k), torch.float32, dev)
+    with _on(stream):
+        if dz is None:
+            dz = torch.empty_like(z)
+        if dweights is None:
+            dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    _need(dz, "dz", (order.rows, C), torch.bfloat16, dev)
+    _need(dweights, "dweights", (T, k), torch.float32, dev)
+    _check(lib().fp8_expert_combine_bwd(dy.data_ptr(), z.data_ptr(), T, C, k, order.E, order.align,
+                                        order.counts.data_ptr(), order.offsets.data_ptr(), order.position.data_ptr(),
+                                        weights.data_ptr(), dz.data_ptr(), dweights.data_ptr(), _stream(stream)),
+           "fp8_expert_combine_bwd")
+    return dz, dweights
+
+
+# ---------------------------------------------------------------- 4-bit weights
+class W4Weight:
+    """A 4-bit weight [N, K], or a stack [E, N, K]: codes uint8 [..., K / 2] (the
+    even k in the low four bits), scale bf16 and zero uint8 [..., ceil(K / group)]
+    (zero None: 8), W = scale * (code - zero) in groups of 32, 64 or 128 along K."""
+
+    __slots__ = ("codes", "scale", "zero", "group", "E", "N", "K", "stack", "device", "_c")
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None,
+                 group: int = 128):
+        if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_cuda or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous uint8 CUDA tensor [N, K / 2] or [E, N, K / 2]")
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        dev = codes.get_device()
+        self.stack = codes.dim() == 3
+        self.E = codes.shape[0] if self.stack else 1
+        self.N, self.K = codes.shape[-2], 2 * codes.shape[-1]
+        if self.N % 16 or self.K % 32:
+            raise ValueError("a 4-bit weight has rows in multiples of 16 and K in multiples of 32")
+        shape = (*codes.shape[:-1], -(-self.K // group))
+        _need(scale, "scale", shape, torch.bfloat16, dev)
+        if zero is not None:
+            _need(zero, "zero", shape, torch.uint8, dev)
+        self.codes, self.scale, self.zero, self.group, self.device = codes, scale, zero, group, codes.device
+        self._c = _W4(codes.data_ptr(), scale.data_ptr(), _ptr(zero), self.E, self.N, self.K, group)
+
+
+def fp8_w4_quantize(w: torch.Tensor, group: int = 128, zero: bool = False, stream=None) -> W4Weight:
+    """4-bit codes, scales (and zero points) of a bf16 weight [N, K] or stack
+    [E, N, K], rounded to the nearest."""
+    _need_bf16_cuda(w, "w")
+    _here(w, "w", stream)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    K = w.shape[-1]
+    if K % 32 or w.shape[-2] % 16 or group not in (32, 64, 128):
+        raise ValueError("a 4-bit weight has rows in multiples of 16, K in multiples of 32 and groups of 32, 64 or 128")
+    shape = (*w.shape[:-1], -(-K // group))
+    with _on(stream):
+        codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
+        scale = torch.empty(shape, dtype=torch.bfloat16, device=w.device)
+        z = torch.empty(shape, dtype=torch.uint8, device=w.device) if zero else None
+    _check(lib().fp8_w4_quantize(w.data_ptr(), w.shape[:-1].numel(), K, group, codes.data_ptr(), scale.data_ptr(),
+                                 _ptr(z), _stream(stream)), "fp8_w4_quantize")
+    return W4Weight(codes, scale, z, group)
+
+
+def _w4_input(x, w, stream):
+    _need_bf16_cuda(x, "x")
+    dev = _here(x, "x", stream)
+    if x.dim() != 2 or x.shape[1] != w.K:
+        raise ValueError(f"x must be [T, {w.K}]")
+    if w.device != x.device:
+        raise ValueError("the weight must be on the device of x")
+    return x.shape[0], dev
+
+
+def fp8_w4_linear(x: torch.Tensor, w: W4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [T, N] = x W^T for bf16 x [T, K], written for few tokens."""
+    T, dev = _w4_input(x, w, stream)
+    if w.stack:
+        raise ValueError("w is a stack of weights")
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, w.N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, "out", (T, w.N), torch.bfloat16, dev)
+    _check(lib().fp8_w4_linear(x.data_ptr(), T, w._c, out.data_ptr(), _stream(stream)), "fp8_w4_linear")
+    return out
+
+
+def fp8_w4_gated(x: torch.Tensor, w: W4Weight, act: str = "silu", out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """h [T, F] = act(x Wg^T) * (x Wu^T) for the weight [Wg; Wu] of 2F rows."""
+    T, dev = _w4_input(x, w, stream)
+    if w.stack or w.N % 32:
+        raise ValueError("w must be one weight with an even number of 16-row blocks")
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, w.N // 2), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, "out", (T, w.N // 2), torch.bfloat16, dev)
+    _check(lib().fp8_w4_gated(x.data_ptr(), T, w._c, ACTIVATION[act], out.data_ptr(), _stream(stream)), "fp8_w4_gated")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _w4_experts_bytes(T, k, E, F, N):
+    b = _c_sz()
+    _check(lib().fp8_w4_experts_workspace_size(T, k, E, F, N, ctypes.byref(b)), "fp8_w4_experts_workspace_size")
+    return b.value
+
+
+def w4_experts_workspace(T: int, k: int, gate_up: W4Weight, down: W4Weight) -> torch.Tensor:
+    return _empty_bytes(_w4_experts_bytes(T, k, gate_up.E, down.K, down.N), gate_up.device)
+
+
+def fp8_w4_experts(x: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor, gate_up: W4Weight, down: W4Weight,
+                   act: str = "silu", ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """y [T, N] = sum_j weights[t, j] (act(x Wg_e^T) * (x Wu_e^T)) Wd_e^T with e =
+    experts[t, j]: the gated MLP of each token's experts, gate_up a stack [E, 2F,
+    K], down one [E, N, F].  weights and experts [T, k] as of fp8_route_fwd.  ws:
+    a w4_experts_workspace, of one call at a time."""
+    T, dev = _w4_input(x, gate_up, stream)
+    k = experts.shape[-1]
+    _need(experts, "experts", (T, k), torch.int32, dev)
+    _need(weights, "weights", (T, k), torch.float32, dev)
+    if gate_up.N != 2 * down.K or gate_up.E != down.E or down.device != x.device:
+        raise ValueError("gate_up [E, 2F, K] and down [E, N, F] do not belong together")
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty((T, down.N), dtype=torch.bfloat16, device=x.device)
+            if ws is None:
+                ws = w4_experts_workspace(T, k, gate_up, down)
+    _need(out, "out", (T, down.N), torch.bfloat16, dev)
+    _check(lib().fp8_w4_experts(x.data_ptr(), T, k, weights.data_ptr(), experts.data_ptr(), gate_up._c, down._c,
+                                ACTIVATION[act], out.data_ptr(), ws.data_ptr(), _bytes(ws, "ws", dev),
+                                _stream(stream)), "fp8_w4_experts")
+    return out

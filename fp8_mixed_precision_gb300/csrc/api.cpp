@@ -1062,6 +1062,296 @@ fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *no
   return clip_run(plan, table, false, 1.0f, norm, workspace, workspace_bytes, stream);
 }
 
+// ---------------------------------------------------------------- routing, rows, 4-bit weights
+namespace {
+constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (int64_t(1) << 25);
+bool element_aligned(const void *p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_DTYPE_F32 ? 3 : 1)) == 0;
+}
+bool vectors_ok(const void *p, int dtype, int64_t E) {
+  return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_DTYPE_F32 ? 15 : 7)) == 0;
+}
+fp8_status check_route(int64_t T, int64_t E, int k, int dtype, int score, float scale) {
+  if (T < 0 || E < 1 || k < 1 || k > E || !valid_dtype(dtype)) return FP8_ERR_INVALID_ARG;
+  if (score != FP8_SCORE_SOFTMAX && score != FP8_SCORE_SIGMOID) return FP8_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale > 3.4e38f) return FP8_ERR_INVALID_ARG;
+  if (E > kMaxExperts || k > kMaxChoices) return FP8_ERR_UNSUPPORTED;
+  if (T > kMaxSlots / k) return FP8_ERR_SHAPE;
+  return FP8_OK;
+}
+fp8_status check_rows(int64_t T, int64_t C, int k, int64_t E, int64_t align) {
+  if (T < 0 || C < 0 || k < 1 || E < 1 || align < 1) return FP8_ERR_INVALID_ARG;
+  if (C % 16 || C > (1 << 20) || T > kMaxSlots / k || align > 1024) return FP8_ERR_SHAPE;
+  if (E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
+  return FP8_OK;
+}
+bool valid_w4(const fp8_w4_weight *w) {
+  return w && w->E >= 1 && w->rows >= 0 && w->K >= 0 && (w->group == 32 || w->group == 64 || w->group == 128);
+}
+fp8_status check_w4(const fp8_w4_weight *w) {
+  if (!valid_w4(w)) return FP8_ERR_INVALID_ARG;
+  if (w->rows % 16 || w->K % 32 || w->rows > (1 << 30) || w->K > (1 << 30)) return FP8_ERR_SHAPE;
+  if (w->E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
+  if (!w->rows || !w->K) return FP8_OK;
+  if (!w->codes || !w->scale) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(w->codes) || (reinterpret_cast<uintptr_t>(w->scale) & 1)) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
+  W4Args a = {};
+  a.codes = w.codes;
+  a.scale = static_cast<const uint16_t *>(w.scale);
+  a.zero = w.zero;
+  a.x = x;
+  a.out = out;
+  a.T = (int)T;
+  a.E = (int)w.E;
+  a.k = 1;
+  a.N = a.rows = (int)w.rows;
+  a.K = (int)w.K;
+  a.group = w.group;
+  return a;
+}
+// One weight for T tokens.
+fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated, int act, void *out,
+                    fp8_stream_t stream) {
+  const fp8_status st = check_w4(w);
+  if (st != FP8_OK) return st;
+  if (w->E != 1 || T < 0 || (act != FP8_ACT_SILU && act != FP8_ACT_GELU)) return FP8_ERR_INVALID_ARG;
+  if ((gated && w->rows % 32) || T > (1 << 30)) return FP8_ERR_SHAPE;
+  if (T == 0 || w->rows == 0) return FP8_OK;
+  if (!out) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(out)) return FP8_ERR_ALIGN;
+  if (w->K == 0)
+    return from_cuda(cudaMemsetAsync(out, 0, (size_t)T * w->rows * (gated ? 1 : 2), cs(stream)));
+  if (!x) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(x)) return FP8_ERR_ALIGN;
+  W4Args a = w4_args(x, T, *w, out);
+  if (gated) {
+    a.gated = 1;
+    a.act = act;
+    a.N = a.rows / 2;
+  }
+  return from_cuda(launch_w4_product(a, 1, (int)std::min<int64_t>(T, 1024), cs(stream)));
+}
+struct W4Workspace {
+  int *counts, *offsets, *position, *order, *hist;
+  void *h;
+  float *z;
+  size_t bytes;
+};
+W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t F, int64_t N) {
+  Carver c(base);
+  const int64_t slots = T * k;
+  const int chunks = order_chunks(slots);
+  W4Workspace w;
+  w.counts = c.take<int>(4 * E);
+  w.offsets = c.take<int>(4 * (E + 1));
+  w.position = c.take<int>(4 * slots);
+  w.order = c.take<int>(4 * slots);
+  w.hist = c.take<int>(chunks > 1 ? 4 * E * chunks : 0);
+  w.h = c.take<void>(2 * slots * F);
+  w.z = c.take<float>(4 * slots * N);
+  w.bytes = c.off;
+  return w;
+}
+}  // namespace
+
+fp8_status fp8_route_fwd(const void *logits, fp8_dtype dtype, const float *bias, int64_t T, int64_t E, int k,
+                         fp8_score score, int groups, int groups_kept, int group_top, int renormalize, float scale,
+                         float *weights, int32_t *experts, fp8_stream_t stream) {
+  const fp8_status st = check_route(T, E, k, dtype, score, scale);
+  if (st != FP8_OK) return st;
+  if (groups < 1 || groups_kept < 1 || groups_kept > groups || E % groups || (group_top != 1 && group_top != 2))
+    return FP8_ERR_INVALID_ARG;
+  if (k > E / groups * groups_kept) return FP8_ERR_INVALID_ARG;
+  if (groups > kMaxChoices) return FP8_ERR_UNSUPPORTED;
+  if (T == 0) return FP8_OK;
+  if (!logits || !weights || !experts) return FP8_ERR_INVALID_ARG;
+  if (!element_aligned(logits, dtype)) return FP8_ERR_ALIGN;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.T = T;
+  a.E = (int)E;
+  a.k = k;
+  a.groups = groups;
+  a.kept = groups_kept;
+  a.top = group_top;
+  a.f32 = dtype == FP8_DTYPE_F32;
+  a.sigmoid = score == FP8_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.vec = vectors_ok(logits, dtype, E);
+  a.scale = scale;
+  return from_cuda(launch_route_fwd(a, weights, experts, cs(stream)));
+}
+
+fp8_status fp8_route_bwd(const float *dweights, const void *logits, fp8_dtype dtype, const float *weights,
+                         const int32_t *experts, int64_t T, int64_t E, int k, fp8_score score, int renormalize,
+                         float scale, void *dlogits, fp8_stream_t stream) {
+  const fp8_status st = check_route(T, E, k, dtype, score, scale);
+  if (st != FP8_OK) return st;
+  if (T == 0) return FP8_OK;
+  if (!dweights || !logits || !weights || !experts || !dlogits) return FP8_ERR_INVALID_ARG;
+  if (!element_aligned(logits, dtype) || !element_aligned(dlogits, dtype)) return FP8_ERR_ALIGN;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.T = T;
+  a.E = (int)E;
+  a.k = k;
+  a.groups = a.kept = a.top = 1;
+  a.f32 = dtype == FP8_DTYPE_F32;
+  a.sigmoid = score == FP8_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.vec = vectors_ok(logits, dtype, E) && vectors_ok(dlogits, dtype, E);
+  a.scale = scale;
+  return from_cuda(launch_route_bwd(a, dweights, weights, experts, dlogits, cs(stream)));
+}
+
+int64_t fp8_expert_rows(int64_t slots, int64_t E, int64_t align) {
+  if (slots <= 0 || E < 1 || align < 1) return 0;
+  return cdiv(slots + (align - 1) * std::min(E, slots), align) * align;
+}
+
+fp8_status fp8_expert_order_workspace_size(int64_t slots, int64_t E, size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_rows(slots, 0, 1, E, 1);
+  if (st != FP8_OK) return st;
+  const int chunks = order_chunks(slots);
+  *bytes = chunks > 1 ? (size_t)chunks * E * 4 : 0;
+  return FP8_OK;
+}
+
+fp8_status fp8_expert_order(const int32_t *experts, int64_t slots, int64_t E, int64_t align, int32_t *counts,
+                            int32_t *offsets, int32_t *position, int32_t *order, void *ws, size_t ws_bytes,
+                            fp8_stream_t stream) {
+  size_t need = 0;
+  fp8_status st = check_rows(slots, 0, 1, E, align);
+  if (st == FP8_OK) st = fp8_expert_order_workspace_size(slots, E, &need);
+  if (st != FP8_OK) return st;
+  if (!counts || !offsets) return FP8_ERR_INVALID_ARG;
+  if (slots == 0) {
+    const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)E * 4, cs(stream));
+    return from_cuda(e != cudaSuccess ? e : cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, cs(stream)));
+  }
+  if (!experts || !position || !order) return FP8_ERR_INVALID_ARG;
+  if (need && (!ws || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  return from_cuda(launch_expert_order(experts, slots, (int)E, (int)align, counts, offsets, position, order,
+                                       static_cast<int *>(ws), cs(stream)));
+}
+
+fp8_status fp8_expert_gather(const void *x, int64_t T, int64_t C, int k, int64_t E, int64_t align,
+                             const int32_t *counts, const int32_t *offsets, const int32_t *position, void *xs,
+                             fp8_stream_t stream) {
+  const fp8_status st = check_rows(T, C, k, E, align);
+  if (st != FP8_OK) return st;
+  if (T == 0 || C == 0) return FP8_OK;
+  if (!x || !counts || !offsets || !position || !xs) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(xs)) return FP8_ERR_ALIGN;
+  if (T * (C / 8) > (int64_t(1) << 38)) return FP8_ERR_SHAPE;
+  return from_cuda(launch_rows_gather(x, T, C, k, (int)E, (int)align, counts, offsets, position, xs, cs(stream)));
+}
+
+fp8_status fp8_expert_combine(const void *z, int64_t T, int64_t C, int k, const int32_t *position,
+                              const float *weights, void *y, fp8_stream_t stream) {
+  const fp8_status st = check_rows(T, C, k, 1, 1);
+  if (st != FP8_OK) return st;
+  if (T == 0 || C == 0) return FP8_OK;
+  if (!z || !position || !y) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(z) || !aligned16(y)) return FP8_ERR_ALIGN;
+  if (T * (C / 8) > (int64_t(1) << 38)) return FP8_ERR_SHAPE;
+  return from_cuda(launch_rows_combine(z, position, weights, T, C, k, y, cs(stream)));
+}
+
+fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int64_t C, int k, int64_t E, int64_t align,
+                                  const int32_t *counts, const int32_t *offsets, const int32_t *position,
+                                  const float *weights, void *dz, float *dweights, fp8_stream_t stream) {
+  const fp8_status st = check_rows(T, C, k, E, align);
+  if (st != FP8_OK) return st;
+  if (T == 0) return FP8_OK;
+  if (!dweights) return FP8_ERR_INVALID_ARG;
+  if (C == 0) return from_cuda(cudaMemsetAsync(dweights, 0, (size_t)T * k * 4, cs(stream)));
+  if (!dy || !z || !counts || !offsets || !position || !weights || !dz) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(z) || !aligned16(dz)) return FP8_ERR_ALIGN;
+  return from_cuda(launch_rows_combine_bwd(dy, z, position, weights, T, C, k, (int)E, (int)align, counts, offsets, dz,
+                                           dweights, cs(stream)));
+}
+
+fp8_status fp8_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes, void *scale,
+                           uint8_t *zero, fp8_stream_t stream) {
+  if (rows < 0 || K < 0 || (group != 32 && group != 64 && group != 128)) return FP8_ERR_INVALID_ARG;
+  if (rows % 16 || K % 32 || K > (1 << 30) || (K && rows > (int64_t(1) << 33) / cdiv(K, group))) return FP8_ERR_SHAPE;
+  if (rows == 0 || K == 0) return FP8_OK;
+  if (!w || !codes || !scale) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scale) & 1)) return FP8_ERR_ALIGN;
+  return from_cuda(launch_w4_quantize(w, rows, K, group, codes, scale, zero, cs(stream)));
+}
+
+fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y, fp8_stream_t stream) {
+  return w4_dense(x, T, w, false, FP8_ACT_SILU, y, stream);
+}
+
+fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h, fp8_stream_t stream) {
+  return w4_dense(x, T, w, true, act, h, stream);
+}
+
+fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t F, int64_t N, size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  fp8_status st = check_rows(T, 0, k, E, 1);
+  if (st != FP8_OK) return st;
+  if (F < 0 || N < 0 || F % 32 || N % 16 || F > (1 << 29) || N > (1 << 30)) return FP8_ERR_SHAPE;
+  *bytes = w4_workspace(nullptr, T, k, E, F, N).bytes;
+  return FP8_OK;
+}
+
+fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights, const int32_t *experts,
+                          const fp8_w4_weight *gate_up, const fp8_w4_weight *down, fp8_act act, void *y, void *ws,
+                          size_t ws_bytes, fp8_stream_t stream) {
+  fp8_status st = check_w4(gate_up);
+  if (st == FP8_OK) st = check_w4(down);
+  if (st != FP8_OK) return st;
+  if (T < 0 || k < 1 || (act != FP8_ACT_SILU && act != FP8_ACT_GELU)) return FP8_ERR_INVALID_ARG;
+  const int64_t E = gate_up->E, F = down->K, N = down->rows;
+  if (down->E != E || gate_up->rows != 2 * F) return FP8_ERR_SHAPE;
+  size_t need = 0;
+  st = fp8_w4_experts_workspace_size(T, k, E, F, N, &need);
+  if (st != FP8_OK) return st;
+  if (T == 0 || N == 0) return FP8_OK;
+  if (!F || !gate_up->K) return FP8_ERR_SHAPE;
+  if (!x || !weights || !experts || !y) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return FP8_ERR_ALIGN;
+  if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
+  const W4Workspace w = w4_workspace(ws, T, k, E, F, N);
+  const int64_t slots = T * k;
+  // one token: its slots stand in their own order
+  const bool sorted = T > 1;
+  if (sorted) {
+    st = from_cuda(launch_expert_order(experts, slots, (int)E, 1, w.counts, w.offsets, w.position, w.order, w.hist,
+                                       cs(stream)));
+    if (st != FP8_OK) return st;
+  }
+  W4Args a = w4_args(x, T, *gate_up, w.h), b = w4_args(w.h, T, *down, w.z);
+  a.gated = a.tokens = 1;
+  a.act = act;
+  a.N = (int)F;
+  b.out_f32 = 1;
+  const int lists = (int)std::min(E, slots);
+  for (W4Args *p : {&a, &b}) {
+    p->experts = experts;
+    p->k = k;
+    if (sorted) {
+      p->order = w.order;
+      p->offsets = w.offsets;
+      p->counts = w.counts;
+      p->by_row = slots < E;
+    }
+    st = from_cuda(launch_w4_product(*p, sorted ? lists : k, (int)std::min<int64_t>(cdiv(slots, E), 1024), cs(stream)));
+    if (st != FP8_OK) return st;
+  }
+  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, y,
+                                  cs(stream)));
+}
+
 fp8_status fp8_profile_begin(void) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   for (auto &r : g_prof) {

@@ -194,6 +194,61 @@ int clip_ctas(int64_t chunks);  // partial sums the first pass writes
 cudaError_t launch_clip(const ClipChunk *table, int64_t chunks, bool few, double in_bytes, double elements,
                         bool write, float max_norm, float *norm, float *partials, cudaStream_t st);
 
+// Routing (route.cu): logits [T, E] bf16 or fp32, bias fp32 [E] or null; E <= kMaxExperts,
+// k and groups <= 32.  per, per_magic and groups_pow2 are filled in by the launch.
+constexpr int kMaxExperts = 1024, kMaxChoices = 32;
+struct RouteArgs {
+  const void *logits;
+  const float *bias;
+  int64_t T;
+  int E, k, groups, kept, top;
+  int f32, sigmoid, renorm, vec;
+  float scale;
+  int per;             // experts of a group
+  unsigned per_magic;  // e * per_magic >> 20 = e / per
+  int groups_pow2;
+};
+cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStream_t st);
+cudaError_t launch_route_bwd(RouteArgs a, const float *dweights, const float *weights, const int *experts,
+                             void *dlogits, cudaStream_t st);
+
+// Rows in the experts' order (rows.cu).  hist: E x order_chunks(slots) ints,
+// unused for one chunk.
+int order_chunks(int64_t slots);
+cudaError_t launch_expert_order(const int *experts, int64_t slots, int E, int align, int *counts, int *offsets,
+                                int *position, int *order, int *hist, cudaStream_t st);
+cudaError_t launch_rows_gather(const void *x, int64_t T, int64_t C, int k, int E, int align, const int *counts,
+                               const int *offsets, const int *position, void *xs, cudaStream_t st);
+cudaError_t launch_rows_combine(const void *z, const int *position, const float *weights, int64_t T, int64_t C, int k,
+                                void *y, cudaStream_t st);
+cudaError_t launch_rows_combine_bwd(const void *dy, const void *z, const int *position, const float *weights, int64_t T,
+                                    int64_t C, int k, int E, int align, const int *counts, const int *offsets, void *dz,
+                                    float *dweights, cudaStream_t st);
+
+// 4-bit weights (w4.cu).  One weight: experts null, T tokens.  A stack: `experts`
+// the slots' experts [T k], order/offsets/counts their rows in the experts'
+// order (null for one token, whose slots are the rows); tokens: x has a row per
+// token, else per row of that order.  groups, warps_k are filled in by the launch.
+struct W4Args {
+  const uint8_t *codes;   // [E, rows, K / 2]
+  const uint16_t *scale;  // bf16 [E, rows, ceil(K / group)]
+  const uint8_t *zero;    // the same shape, or null: 8
+  const void *x;
+  void *out;              // gated: bf16 [., N]; else bf16 or fp32
+  const int *experts, *order, *offsets, *counts;
+  int T, E, k, by_row, tokens;
+  int N, rows, K, group;  // N outputs; rows = 2 N when gated
+  int gated, act, out_f32;
+  int groups, warps_k;
+};
+// lists: rows of the grid, one per expert (or per row, by_row); likely: tokens
+// that an expert may be expected to have.
+cudaError_t launch_w4_product(W4Args a, int lists, int likely, cudaStream_t st);
+cudaError_t launch_w4_join(const float *z, const int *experts, const int *position, const float *weights, int64_t T,
+                           int64_t N, int k, int E, void *y, cudaStream_t st);
+cudaError_t launch_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes, void *scale,
+                               uint8_t *zero, cudaStream_t st);
+
 cudaError_t launch_gelu_fwd(const void *H, void *A, int64_t n, cudaStream_t st);
 cudaError_t launch_gelu_bwd(const void *dA, const void *H, void *dH, int64_t n, cudaStream_t st);
 cudaError_t launch_grad_accumulate(float *acc, const void *dW, int64_t n, cudaStream_t st);

@@ -1,0 +1,498 @@
+// Routing of tokens to experts.
+//
+//   s = softmax(l) or sigmoid(l) over a token's E logits
+//   c = s + bias                                    (selection only)
+//   group score = sum of the group's best 1 or 2 c; the best groups stay
+//   experts = the k largest c left, descending, ties to the lowest index
+//   w_j = scale s_j / (sum of the chosen s), or scale s_j
+//
+// An expert with logit or bias -inf is never chosen; slots left over get expert
+// -1 and weight 0.  Renormalised weights are the softmax of log s over the
+// chosen ones, which no underflow of s can make 0 / 0.
+//
+// The choice is that of the exact scores.  Where c is monotone in the logits
+// (no bias, and at most one score to a group) the logits are compared
+// themselves.  Elsewhere c is formed in fp32; a row in which two scores that
+// decide something are closer than fp32's error is chosen anew in fp64.
+//
+// LANES threads hold one token's logits in registers, four consecutive ones
+// each, CHUNKS times.
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fp8lin {
+namespace {
+
+constexpr int kRouteThreads = 128;
+constexpr unsigned kFull = 0xffffffffu;
+
+// Order-preserving map of fp32 onto unsigned; 0 stands for "not a candidate"
+// (below every number's image but that of a NaN with the sign set).
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 ties with +0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+template <int LANES>
+__device__ __forceinline__ float sum_over(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float max_over(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+// Largest key of the token's lanes and the lowest index that has it.
+template <int LANES>
+__device__ __forceinline__ void best_over(uint32_t &key, int &at) {
+  if constexpr (LANES == 32) {
+    const uint32_t m = __reduce_max_sync(kFull, key);
+    at = (int)__reduce_min_sync(kFull, key == m ? (unsigned)at : 0xffffffffu);
+    key = m;
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+      const uint32_t k2 = __shfl_xor_sync(kFull, key, o);
+      const int a2 = __shfl_xor_sync(kFull, at, o);
+      if (k2 > key || (k2 == key && a2 < at)) key = k2, at = a2;
+    }
+  }
+}
+
+__device__ __forceinline__ float load_logit(const void *l, int f32, int64_t i) {
+  return f32 ? static_cast<const float *>(l)[i] : bf16lo(static_cast<const uint16_t *>(l)[i]);
+}
+
+// The four logits from e on of a row (those from E on: -inf).  vec: rows begin
+// on the vector's boundary, E a multiple of 4.
+__device__ __forceinline__ void load4(const void *l, int f32, bool vec, int64_t row, int e, int E,
+                                      float (&v)[4]) {
+  const int64_t i = row * E + e;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = -INFINITY;
+  if (vec) {
+    if (e >= E) return;
+    if (f32) {
+      const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(l) + i);
+      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(l) + i);
+      v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (e + q < E) v[q] = load_logit(l, f32, i + q);
+}
+
+// Two largest values seen.
+struct Two {
+  double a, b;
+};
+__device__ __forceinline__ void push(Two &t, double v) {
+  if (v > t.a) {
+    t.b = t.a;
+    t.a = v;
+  } else if (v > t.b) {
+    t.b = v;
+  }
+}
+
+// The choice in fp64 for one row, by the LANES lanes of its token (`mask`);
+// c: E doubles of shared memory.  Lane j of the token returns expert j.
+template <int LANES>
+__device__ __noinline__ int choose64(unsigned mask, const RouteArgs &a, int64_t t, double *c) {
+  const int lane = threadIdx.x & (LANES - 1);
+  double m = -INFINITY;
+  for (int e = lane; e < a.E; e += LANES) m = fmax(m, (double)load_logit(a.logits, a.f32, t * a.E + e));
+  for (int o = LANES / 2; o; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
+  double z = 0.0;
+  if (!a.sigmoid) {
+    for (int e = lane; e < a.E; e += LANES) z += exp((double)load_logit(a.logits, a.f32, t * a.E + e) - m);
+    for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(mask, z, o);
+  }
+  for (int e = lane; e < a.E; e += LANES) {
+    const double l = load_logit(a.logits, a.f32, t * a.E + e);
+    double v = -INFINITY;
+    if (l > -INFINITY) {
+      v = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / z;
+      if (a.bias) v += (double)a.bias[e];
+    }
+    c[e] = v;
+  }
+  __syncwarp(mask);
+  const int per = a.E / a.groups;
+  if (a.groups > 1) {
+    // bit g: group g is kept
+    unsigned kept = 0;
+    for (int n = 0; n < a.kept; ++n) {
+      double best = -INFINITY;
+      int at = -1;
+      for (int g = lane; g < a.groups; g += LANES) {
+        if (kept >> g & 1u) continue;
+        Two two = {-INFINITY, -INFINITY};
+        for (int e = g * per; e < (g + 1) * per; ++e) push(two, c[e]);
+        const double s = a.top == 2 && two.b > -INFINITY ? two.a + two.b : two.a;
+        if (s > best) best = s, at = g;
+      }
+      for (int o = LANES / 2; o; o >>= 1) {
+        const double b2 = __shfl_xor_sync(mask, best, o);
+        const int a2 = __shfl_xor_sync(mask, at, o);
+        if (a2 >= 0 && (at < 0 || b2 > best || (b2 == best && a2 < at))) best = b2, at = a2;
+      }
+      if (at < 0) break;
+      kept |= 1u << at;
+    }
+    for (int e = lane; e < a.E; e += LANES)
+      if (!(kept >> (e / per) & 1u)) c[e] = -INFINITY;
+    __syncwarp(mask);
+  }
+  int mine = -1;
+  for (int j = 0; j < a.k; ++j) {
+    double best = -INFINITY;
+    int at = -1;
+    for (int e = lane; e < a.E; e += LANES)
+      if (c[e] > best) best = c[e], at = e;
+    for (int o = LANES / 2; o; o >>= 1) {
+      const double b2 = __shfl_xor_sync(mask, best, o);
+      const int a2 = __shfl_xor_sync(mask, at, o);
+      if (a2 >= 0 && (at < 0 || b2 > best || (b2 == best && a2 < at))) best = b2, at = a2;
+    }
+    if (j == lane) mine = at;
+    if (at >= 0 && at % LANES == lane) c[at] = -INFINITY;
+    __syncwarp(mask);
+  }
+  return mine;
+}
+
+// sigmoid(l), its smallest values included
+__device__ __forceinline__ float sigmoid(float l) {
+  const float t = expf(-fabsf(l));
+  return __fdiv_rn(l >= 0.0f ? 1.0f : t, 1.0f + t);
+}
+// log(sigmoid(l))
+__device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
+
+// GENERAL: scores are formed (a bias, or two to a group); else logits alone choose.
+template <int LANES, int CHUNKS, bool GENERAL>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a, float *__restrict__ weights,
+                                                              int *__restrict__ experts) {
+  constexpr int kTokens = kRouteThreads / LANES;
+  // a row of c: fp32 for the groups' scores, fp64 for the choice made anew
+  __shared__ double rows[kTokens][GENERAL ? 4 * LANES * CHUNKS : 2 * LANES * CHUNKS];
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & (LANES - 1), slot = threadIdx.x / LANES;
+  const int64_t row = (int64_t)blockIdx.x * kTokens + slot;
+  const int64_t t = row < a.T ? row : a.T - 1;  // spare lanes repeat the last token and write nothing
+  const unsigned mask = LANES == 32 ? kFull : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+
+  float l[CHUNKS][4];
+  bool bad = false;
+  float m = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    load4(a.logits, a.f32, a.vec, t, 4 * LANES * c + 4 * lane, a.E, l[c]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      m = fmaxf(m, l[c][q]);
+      bad |= isnan(l[c][q]) || (!a.sigmoid && l[c][q] == INFINITY);
+    }
+  }
+  m = max_over<LANES>(m);
+  float z = 1.0f;
+  if (!a.sigmoid && (GENERAL || !a.renorm)) {
+    z = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z += l[c][q] > -INFINITY ? expf(l[c][q] - m) : 0.0f;
+    z = sum_over<LANES>(z);
+  }
+  uint32_t key[CHUNKS][4];
+  float *line = reinterpret_cast<float *>(rows[slot]);
+  float tol = 0.0f;
+  {
+    float smax = 0.0f, cmax = 0.0f;
+    const float rz = GENERAL ? __fdiv_rn(1.0f, z) : 1.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int e = 4 * LANES * c + 4 * lane + q;
+        const float x = l[c][q];
+        float v = x, g = x;  // what chooses experts, and groups
+        if (GENERAL) {
+          const float s = a.sigmoid ? sigmoid(x) : expf(x - m) * rz;
+          const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
+          const float score = s + b;
+          if (x > -INFINITY) {
+            bad |= isnan(score);
+            smax = fmaxf(smax, s);
+            if (fabsf(score) < INFINITY) cmax = fmaxf(cmax, fabsf(score));
+          }
+          if (a.bias) v = score;
+          g = a.top == 2 ? score : v;
+        }
+        const bool some = x > -INFINITY && v > -INFINITY;
+        key[c][q] = some ? key_of(v) : 0u;
+        if (a.groups > 1) line[e] = some ? g : -INFINITY;
+      }
+    // twice the fp32 error of a score: the sum's and the exponential's part of
+    // s (under 32 units of roundoff), and the addition's
+    if (GENERAL) tol = 0x1p-18f * max_over<LANES>(smax) + 0x1p-22f * max_over<LANES>(cmax);
+  }
+  bool again = false;
+  if (a.groups > 1) {
+    __syncwarp();
+    // a group's scores are shared out over `share` lanes
+    const int share = LANES / a.groups_pow2, g = lane / share;
+    float two0 = -INFINITY, two1 = -INFINITY;
+    if (g < a.groups)
+      for (int i = lane % share; i < a.per; i += share) {
+        const float v = line[g * a.per + i];
+        if (v > two0) {
+          two1 = two0;
+          two0 = v;
+        } else {
+          two1 = fmaxf(two1, v);
+        }
+      }
+    for (int o = share / 2; o; o >>= 1) {
+      const float b0 = __shfl_xor_sync(kFull, two0, o), b1 = __shfl_xor_sync(kFull, two1, o);
+      two1 = fmaxf(fminf(two0, b0), fmaxf(two1, b1));
+      two0 = fmaxf(two0, b0);
+    }
+    const float score = a.top == 2 && two1 > -INFINITY ? two0 + two1 : two0;
+    uint32_t gkey = g < a.groups && lane % share == 0 && two0 > -INFINITY ? key_of(score) : 0u;
+    unsigned kept = 0;
+    float last = 0.0f;
+    for (int n = 0; n < a.kept; ++n) {
+      uint32_t k1 = gkey;
+      int at = g;
+      best_over<LANES>(k1, at);
+      if (k1 == 0) continue;
+      kept |= 1u << at;
+      last = of_key(k1);
+      if (at == g) gkey = 0u;
+    }
+    if (GENERAL) again = kept && gkey && !(of_key(gkey) <= last - 2.0f * tol);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int e = 4 * LANES * c + 4 * lane + q;
+        if (!(kept >> ((unsigned)e * a.per_magic >> 20 & 31u) & 1u)) key[c][q] = 0u;
+      }
+  }
+  int mine = -1;        // the expert in slot `lane`
+  uint32_t mine_key = 0u, last_key = 0u;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0u;
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (key[c][q] > best) best = key[c][q], at = 4 * LANES * c + 4 * lane + q;
+    best_over<LANES>(best, at);
+    if (best) {
+      if (lane == j) mine = at, mine_key = best;
+      last_key = best;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (at == 4 * LANES * c + 4 * lane + q) key[c][q] = 0u;
+    }
+  }
+  float x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+  if (GENERAL && a.bias) {
+    // neighbours in the order closer than the error, equal logits and biases apart
+    const float b = mine >= 0 ? a.bias[mine] : 0.0f;
+    const float x2 = __shfl_down_sync(kFull, x, 1, LANES), b2 = __shfl_down_sync(kFull, b, 1, LANES);
+    const uint32_t k2 = __shfl_down_sync(kFull, mine_key, 1, LANES);
+    if (lane + 1 < a.k && k2 && !(of_key(k2) <= of_key(mine_key) - tol)) again |= x != x2 || b != b2;
+    // those left that come as close to the last one chosen
+    const float xl = __shfl_sync(kFull, x, a.k - 1, LANES), bl = __shfl_sync(kFull, b, a.k - 1, LANES);
+    const float edge = of_key(last_key) - tol;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (key[c][q] && !(of_key(key[c][q]) <= edge)) {
+          const int e = 4 * LANES * c + 4 * lane + q;
+          again |= load_logit(a.logits, a.f32, t * a.E + e) != xl || a.bias[e] != bl;
+        }
+  }
+  bad = __any_sync(kFull, bad) && (__ballot_sync(kFull, bad) & mask);
+  if (GENERAL) {
+    again = (__ballot_sync(kFull, again) & mask) && !bad;
+    if (again) {
+      mine = choose64<LANES>(mask, a, t, rows[slot]);
+      x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+    }
+    __syncwarp();
+  }
+  const bool some = mine >= 0;
+  float w = 0.0f;
+  if (a.renorm) {
+    const float g = some ? (a.sigmoid ? log_sigmoid(x) : x) : -INFINITY;
+    const float top = max_over<LANES>(g);
+    const float u = some ? expf(g - top) : 0.0f;
+    const float total = sum_over<LANES>(u);
+    if (some) w = __fdiv_rn(u, total) * a.scale;
+  } else if (some) {
+    w = (a.sigmoid ? sigmoid(x) : __fdiv_rn(expf(x - m), z)) * a.scale;
+  }
+  if (row < a.T && lane < a.k) {
+    weights[t * a.k + lane] = bad ? __int_as_float(0x7fc00000) : w;
+    experts[t * a.k + lane] = bad ? -1 : mine;
+  }
+}
+
+// dL/dlog s_j = w_j g_j, or w_j (g_j - sum_i g_i w_i / scale) with renormalised
+// weights; softmax: dl_e = that of e - s_e times their sum (0 when
+// renormalised); sigmoid: times 1 - s_e.
+template <int LANES, int CHUNKS>
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArgs a, const float *__restrict__ dweights,
+                                                                  const float *__restrict__ weights,
+                                                                  const int *__restrict__ experts,
+                                                                  void *__restrict__ dlogits) {
+  constexpr int kTokens = kRouteThreads / LANES;
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t row = (int64_t)blockIdx.x * kTokens + threadIdx.x / LANES;
+  const int64_t t = row < a.T ? row : a.T - 1;
+  int e = -1;
+  float w = 0.0f, g = 0.0f;
+  if (lane < a.k) {
+    e = experts[t * a.k + lane];
+    w = weights[t * a.k + lane];
+    g = dweights[t * a.k + lane];
+  }
+  const bool some = e >= 0 && e < a.E;
+  float d = some ? w * g : 0.0f;
+  if (a.renorm) {
+    const float total = sum_over<LANES>(d);
+    if (some) d = w * (g - __fdiv_rn(total, a.scale));
+  }
+  if (a.sigmoid && some) d *= sigmoid(-load_logit(a.logits, a.f32, t * a.E + e));
+  float v[CHUNKS][4];
+  if (!a.sigmoid && !a.renorm) {
+    float m = -INFINITY, z = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      load4(a.logits, a.f32, a.vec, t, 4 * LANES * c + 4 * lane, a.E, v[c]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = fmaxf(m, v[c][q]);
+    }
+    m = max_over<LANES>(m);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[c][q] = v[c][q] > -INFINITY ? expf(v[c][q] - m) : 0.0f;
+        z += v[c][q];
+      }
+    z = sum_over<LANES>(z);
+    const float total = sum_over<LANES>(d);
+    const float f = z > 0.0f ? -__fdiv_rn(total, z) : 0.0f;  // a row without a candidate: zeros
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[c][q] *= f;
+  } else {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[c][q] = 0.0f;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    const int ej = __shfl_sync(kFull, some ? e : -1, j, LANES);
+    const float dj = __shfl_sync(kFull, d, j, LANES);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (ej == 4 * LANES * c + 4 * lane + q) v[c][q] += dj;
+  }
+  if (row >= a.T) return;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int e0 = 4 * LANES * c + 4 * lane;
+    const int64_t i = t * a.E + e0;
+    if (a.vec) {
+      if (e0 >= a.E) continue;
+      if (a.f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(dlogits) + i) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+      else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dlogits) + i) =
+            make_uint2(pack_bf16x2(v[c][0], v[c][1]), pack_bf16x2(v[c][2], v[c][3]));
+      continue;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (e0 + q < a.E) {
+        if (a.f32)
+          static_cast<float *>(dlogits)[i + q] = v[c][q];
+        else
+          static_cast<__nv_bfloat16 *>(dlogits)[i + q] = __float2bfloat16_rn(v[c][q]);
+      }
+  }
+}
+
+// Calls f with the LANES and CHUNKS that hold E experts, k choices and the groups.
+template <typename F>
+cudaError_t with_shape(const RouteArgs &a, F f) {
+  const int lanes = std::max(std::max((a.E + 3) / 4, a.k), a.groups);
+  using std::integral_constant;
+  if (lanes <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+  if (lanes <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+  if (lanes <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+  if (lanes <= 64) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
+  if (lanes <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
+  return f(integral_constant<int, 32>(), integral_constant<int, 8>());
+}
+
+}  // namespace
+
+cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStream_t st) {
+  a.per = a.E / a.groups;
+  a.per_magic = (1u << 20) / (unsigned)a.per + 1u;
+  for (a.groups_pow2 = 1; a.groups_pow2 < a.groups;) a.groups_pow2 *= 2;
+  LaunchScope ls("route_fwd", st, (double)a.T * (a.E * (a.f32 ? 4.0 : 2.0) + 8.0 * a.k), 4.0 * a.T * a.E, a.T, a.E,
+                 a.k);
+  return with_shape(a, [&](auto lanes, auto chunks) {
+    constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
+    const dim3 grid((unsigned)((a.T + kRouteThreads / L - 1) / (kRouteThreads / L)));
+    if (a.bias || (a.groups > 1 && a.top == 2))
+      return launch_kernel(route_kernel<L, C, true>, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
+    return launch_kernel(route_kernel<L, C, false>, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
+  });
+}
+
+cudaError_t launch_route_bwd(RouteArgs a, const float *dweights, const float *weights, const int *experts,
+                             void *dlogits, cudaStream_t st) {
+  LaunchScope ls("route_bwd", st, (double)a.T * (a.E * (a.f32 ? 4.0 : 2.0) + 12.0 * a.k), 2.0 * a.T * a.E, a.T, a.E,
+                 a.k);
+  return with_shape(a, [&](auto lanes, auto chunks) {
+    constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
+    const dim3 grid((unsigned)((a.T + kRouteThreads / L - 1) / (kRouteThreads / L)));
+    return launch_kernel(route_bwd_kernel<L, C>, grid, dim3(kRouteThreads), 0, st, a, dweights, weights, experts,
+                         dlogits);
+  });
+}
+
+}  // namespace fp8lin

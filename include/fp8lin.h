@@ -468,6 +468,119 @@ fp8_status fp8_grad_clip_run(const fp8_grad_clip *plan, const void *table, float
 fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *norm, void *workspace,
                          size_t workspace_bytes, fp8_stream_t stream);
 
+/* ------------------------------------------------------------------ routing to experts
+ * Scores of T tokens for E experts, the choice of k of them, and their weights:
+ *   s = softmax(l) or sigmoid(l) over a token's logits l
+ *   c = s + bias                                   (for the choice alone)
+ *   groups > 1: E / groups neighbouring experts to a group, whose score is the
+ *       sum of its group_top (1 or 2) largest c; the groups_kept best groups stay
+ *   experts = the k largest c left, in descending order
+ *   w_j = scale * s_j / sum of the chosen s (renormalize), else scale * s_j
+ * Ties go to the lowest index, of groups and of experts; the order is that of the
+ * exact scores (decided in fp64 where fp32 could err).  An expert whose logit or
+ * bias is -inf is never chosen; slots left over get expert -1 and weight 0, so a
+ * row of -inf (a padding token) has no expert.  A row with a NaN score (a NaN
+ * logit or bias, or +inf under softmax) gets experts -1 and weights NaN.
+ *   logits   device bf16 or f32 [T, E], any alignment of the type
+ *   bias     device f32 [E] or NULL
+ *   weights, experts   device f32 and int32 [T, k]
+ *   E <= 1024; k, groups <= 32; k <= E; groups divides E; scale > 0
+ * fp8_route_bwd: dlogits (the type of logits) from the weights' gradient, with
+ *   logits, weights and experts of the forward pass and its score, renormalize
+ *   and scale.  The bias has no gradient; a slot without an expert passes none.
+ * Errors: INVALID_ARG, UNSUPPORTED (E, k or groups past their limits), CUDA. */
+typedef enum { FP8_SCORE_SOFTMAX = 0, FP8_SCORE_SIGMOID = 1 } fp8_score;
+
+fp8_status fp8_route_fwd(const void *logits, fp8_dtype dtype, const float *bias, int64_t T, int64_t E,
+                         int k, fp8_score score, int groups, int groups_kept, int group_top,
+                         int renormalize, float scale, float *weights, int32_t *experts,
+                         fp8_stream_t stream);
+fp8_status fp8_route_bwd(const float *dweights, const void *logits, fp8_dtype dtype,
+                         const float *weights, const int32_t *experts, int64_t T, int64_t E, int k,
+                         fp8_score score, int renormalize, float scale, void *dlogits,
+                         fp8_stream_t stream);
+
+/* ------------------------------------------------------------------ rows in the experts' order
+ * fp8_expert_order sorts the `slots` = T k choices (slot t k + j: choice j of
+ * token t) by expert, stably:
+ *   experts   device int32 [slots]; values outside 0 .. E - 1: no expert
+ *   align     each expert's first row is a multiple of it (1: no gaps; 16: row
+ *             counts as the FP8 linear takes them)
+ *   counts    device int32 [E]: rows of each expert
+ *   offsets   device int32 [E + 1]: each expert's first row, and the rows in use
+ *   position  device int32 [slots]: a slot's row, -1 without an expert
+ *   order     device int32 [fp8_expert_rows]: a row's slot, -1 in the gap behind
+ *             an expert's rows; past offsets[E] left as it was
+ *   ws        fp8_expert_order_workspace_size bytes
+ * fp8_expert_rows: rows that any choice can need.
+ * Moving bf16 rows of C values (a multiple of 16) between tokens and that order:
+ *   fp8_expert_gather       xs[position[t, j]] = x[t]; rows in gaps become zeros
+ *   fp8_expert_combine      y[t] = sum_j weights[t, j] z[position[t, j]] (fp32
+ *                           sums in the order of j; weights NULL: 1).  Without
+ *                           weights it is fp8_expert_gather's backward pass.  A
+ *                           slot without a row counts as its weight times zero
+ *   fp8_expert_combine_bwd  dz[position[t, j]] = weights[t, j] dy[t]; rows in
+ *                           gaps become zeros; dweights[t, j] = <dy[t], z[position[t, j]]>,
+ *                           0 without a row
+ *   Rows past offsets[E] of xs and dz are left as they were.  C <= 2^20.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (E > 1024), WORKSPACE, CUDA. */
+int64_t fp8_expert_rows(int64_t slots, int64_t E, int64_t align);
+fp8_status fp8_expert_order_workspace_size(int64_t slots, int64_t E, size_t *bytes);
+fp8_status fp8_expert_order(const int32_t *experts, int64_t slots, int64_t E, int64_t align,
+                            int32_t *counts, int32_t *offsets, int32_t *position, int32_t *order,
+                            void *ws, size_t ws_bytes, fp8_stream_t stream);
+fp8_status fp8_expert_gather(const void *x, int64_t T, int64_t C, int k, int64_t E, int64_t align,
+                             const int32_t *counts, const int32_t *offsets, const int32_t *position,
+                             void *xs, fp8_stream_t stream);
+fp8_status fp8_expert_combine(const void *z, int64_t T, int64_t C, int k, const int32_t *position,
+                              const float *weights, void *y, fp8_stream_t stream);
+fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int64_t C, int k, int64_t E,
+                                  int64_t align, const int32_t *counts, const int32_t *offsets,
+                                  const int32_t *position, const float *weights, void *dz,
+                                  float *dweights, fp8_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit weights
+ * A weight W [rows, K], or a stack of E of them, with 4-bit codes in groups of
+ * `group` (32, 64 or 128) neighbours along K, the last group of a row perhaps short:
+ *   W[n, k] = scale[n, k / group] * (code[n, k] - zero[n, k / group])
+ *   codes  device u8 [E, rows, K / 2]: the even k in the low four bits
+ *   scale  device bf16 [E, rows, ceil(K / group)]
+ *   zero   device u8, of the same shape, 0 .. 15; NULL: 8
+ *   rows a multiple of 16, K of 32
+ * Products are exact within a group and summed in fp32, for any number of tokens T;
+ * written for few (decoding), where the weights' bytes are all that counts.
+ * fp8_w4_quantize: codes, scales (and zero points, unless NULL) of bf16 weights
+ *   [rows, K] by rounding to the nearest: scale = bf16(max |w| / 7) and zero 8, or
+ *   scale = bf16((max - min) / 15) with max >= 0 >= min and zero = round(-min / scale);
+ *   1 where that is 0.  Finite weights.
+ * fp8_w4_linear: y [T, rows] = x W^T in bf16.
+ * fp8_w4_gated:  h [T, F] = act(x Wg^T) * (x Wu^T) in bf16, W = [Wg; Wu] with 2F rows.
+ * fp8_w4_experts: the gated MLP of each token's experts,
+ *   y[t] = sum_j weights[t, j] h_tj Wd_e^T, h_tj = bf16(act(x_t Wg_e^T) * (x_t Wu_e^T)), e = experts[t, j],
+ *   gate_up a stack of E weights [2F, K], down one of E weights [N, F]; weights f32
+ *   and experts int32 [T, k] (values outside 0 .. E - 1: no expert, which counts as
+ *   the weight times zero); ws fp8_w4_experts_workspace_size bytes, of one call at a time.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (E > 1024), WORKSPACE, CUDA. */
+typedef struct {
+  const uint8_t *codes;
+  const void *scale;
+  const uint8_t *zero;
+  int64_t E, rows, K;
+  int group;
+} fp8_w4_weight;
+fp8_status fp8_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes,
+                           void *scale, uint8_t *zero, fp8_stream_t stream);
+fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y,
+                         fp8_stream_t stream);
+fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h,
+                        fp8_stream_t stream);
+fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t F, int64_t N,
+                                         size_t *bytes);
+fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
+                          const int32_t *experts, const fp8_w4_weight *gate_up,
+                          const fp8_w4_weight *down, fp8_act act, void *y, void *ws, size_t ws_bytes,
+                          fp8_stream_t stream);
+
 /* ------------------------------------------------------------------ host-buffer steps
  * One forward + backward of an isolated FP8 linear (fp8_linear_fwd then
  * fp8_linear_bwd, same recipe rules) whose inputs and results live in HOST
