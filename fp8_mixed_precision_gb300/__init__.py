@@ -28,7 +28,7 @@ __all__ = [
     "gated_workspace", "gated_norm_columns", "fp8_gated_ctx_layout", "GradClip", "NormBuffers",
     "SCORE", "fp8_route_fwd", "fp8_route_bwd", "ExpertOrder", "expert_rows", "fp8_expert_order",
     "fp8_expert_gather", "fp8_expert_combine", "fp8_expert_combine_bwd", "W4Weight", "fp8_w4_quantize",
-    "fp8_w4_linear", "fp8_w4_gated", "fp8_w4_experts", "w4_experts_workspace",
+    "fp8_w4_linear", "fp8_w4_gated", "fp8_w4_experts", "w4_workspace", "w4_experts_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -174,9 +174,10 @@ _SIGS.update({
     "fp8_expert_combine_bwd": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_int, _c_i64, _c_i64] +
                                [_c_p] * 7),
     "fp8_w4_quantize": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]),
-    "fp8_w4_linear": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_p, _c_p]),
-    "fp8_w4_gated": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_int, _c_p, _c_p]),
-    "fp8_w4_experts_workspace_size": (_c_int, [_c_i64, _c_int, _c_i64, _c_i64, _c_i64,
+    "fp8_w4_workspace_size": (_c_int, [ctypes.POINTER(_W4), _c_i64, _c_int, ctypes.POINTER(_c_sz)]),
+    "fp8_w4_linear": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_p, _c_p, _c_sz, _c_p]),
+    "fp8_w4_gated": (_c_int, [_c_p, _c_i64, ctypes.POINTER(_W4), _c_int, _c_p, _c_p, _c_sz, _c_p]),
+    "fp8_w4_experts_workspace_size": (_c_int, [_c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64,
                                                ctypes.POINTER(_c_sz)]),
     "fp8_w4_experts": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_p, ctypes.POINTER(_W4),
                                 ctypes.POINTER(_W4), _c_int, _c_p, _c_p, _c_sz, _c_p]),
@@ -1393,7 +1394,33 @@ def _w4_input(x, w, stream):
     return x.shape[0], dev
 
 
-def fp8_w4_linear(x: torch.Tensor, w: W4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+@functools.lru_cache(maxsize=1024)
+def _w4_bytes(N, K, group, T, gated):
+    b = _c_sz()
+    any_address = 16  # the size depends on the shape alone
+    _check(lib().fp8_w4_workspace_size(_W4(any_address, any_address, None, 1, N, K, group), T, gated, ctypes.byref(b)),
+           "fp8_w4_workspace_size")
+    return b.value
+
+
+def w4_workspace(w: W4Weight, T: int, gated: bool = False) -> torch.Tensor:
+    """Workspace of fp8_w4_linear or fp8_w4_gated for callers that keep it."""
+    return _empty_bytes(_w4_bytes(w.N, w.K, w.group, T, gated), w.device)
+
+
+def _w4_ws(w, T, gated, ws, dev, stream):
+    """(tensor, pointer, bytes) of a call's workspace."""
+    if ws is None:
+        need = _w4_bytes(w.N, w.K, w.group, T, gated)
+        if not need:
+            return None, None, 0
+        with _on(stream):
+            ws = _empty_bytes(need, w.device)
+    return ws, ws.data_ptr(), _bytes(ws, "ws", dev)
+
+
+def fp8_w4_linear(x: torch.Tensor, w: W4Weight, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
     """y [T, N] = x W^T for bf16 x [T, K], written for few tokens."""
     T, dev = _w4_input(x, w, stream)
     if w.stack:
@@ -1403,12 +1430,13 @@ def fp8_w4_linear(x: torch.Tensor, w: W4Weight, out: torch.Tensor | None = None,
             out = torch.empty((T, w.N), dtype=torch.bfloat16, device=x.device)
     else:
         _need(out, "out", (T, w.N), torch.bfloat16, dev)
-    _check(lib().fp8_w4_linear(x.data_ptr(), T, w._c, out.data_ptr(), _stream(stream)), "fp8_w4_linear")
+    ws, at, size = _w4_ws(w, T, False, ws, dev, stream)
+    _check(lib().fp8_w4_linear(x.data_ptr(), T, w._c, out.data_ptr(), at, size, _stream(stream)), "fp8_w4_linear")
     return out
 
 
 def fp8_w4_gated(x: torch.Tensor, w: W4Weight, act: str = "silu", out: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """h [T, F] = act(x Wg^T) * (x Wu^T) for the weight [Wg; Wu] of 2F rows."""
     T, dev = _w4_input(x, w, stream)
     if w.stack or w.N % 32:
@@ -1418,19 +1446,21 @@ def fp8_w4_gated(x: torch.Tensor, w: W4Weight, act: str = "silu", out: torch.Ten
             out = torch.empty((T, w.N // 2), dtype=torch.bfloat16, device=x.device)
     else:
         _need(out, "out", (T, w.N // 2), torch.bfloat16, dev)
-    _check(lib().fp8_w4_gated(x.data_ptr(), T, w._c, ACTIVATION[act], out.data_ptr(), _stream(stream)), "fp8_w4_gated")
+    ws, at, size = _w4_ws(w, T, True, ws, dev, stream)
+    _check(lib().fp8_w4_gated(x.data_ptr(), T, w._c, ACTIVATION[act], out.data_ptr(), at, size, _stream(stream)),
+           "fp8_w4_gated")
     return out
 
 
 @functools.lru_cache(maxsize=256)
-def _w4_experts_bytes(T, k, E, F, N):
+def _w4_experts_bytes(T, k, E, K, F, N):
     b = _c_sz()
-    _check(lib().fp8_w4_experts_workspace_size(T, k, E, F, N, ctypes.byref(b)), "fp8_w4_experts_workspace_size")
+    _check(lib().fp8_w4_experts_workspace_size(T, k, E, K, F, N, ctypes.byref(b)), "fp8_w4_experts_workspace_size")
     return b.value
 
 
 def w4_experts_workspace(T: int, k: int, gate_up: W4Weight, down: W4Weight) -> torch.Tensor:
-    return _empty_bytes(_w4_experts_bytes(T, k, gate_up.E, down.K, down.N), gate_up.device)
+    return _empty_bytes(_w4_experts_bytes(T, k, gate_up.E, gate_up.K, down.K, down.N), gate_up.device)
 
 
 def fp8_w4_experts(x: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor, gate_up: W4Weight, down: W4Weight,

@@ -1065,6 +1065,7 @@ fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *no
 // ---------------------------------------------------------------- routing, rows, 4-bit weights
 namespace {
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (int64_t(1) << 25);
+constexpr int64_t kMaxW4Tokens = 1 << 18;  // the grid's third dimension, at least eight tokens a block
 bool element_aligned(const void *p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_DTYPE_F32 ? 3 : 1)) == 0;
 }
@@ -1090,11 +1091,11 @@ bool valid_w4(const fp8_w4_weight *w) {
 }
 fp8_status check_w4(const fp8_w4_weight *w) {
   if (!valid_w4(w)) return FP8_ERR_INVALID_ARG;
-  if (w->rows % 16 || w->K % 32 || w->rows > (1 << 30) || w->K > (1 << 30)) return FP8_ERR_SHAPE;
+  if (w->rows % 16 || w->K % 32 || w->rows > (1 << 26) || w->K > (1 << 26)) return FP8_ERR_SHAPE;
   if (w->E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
   if (!w->rows || !w->K) return FP8_OK;
   if (!w->codes || !w->scale) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(w->codes) || (reinterpret_cast<uintptr_t>(w->scale) & 1)) return FP8_ERR_ALIGN;
+  if (!aligned16(w->codes) || !aligned16(w->scale) || !aligned16(w->zero)) return FP8_ERR_ALIGN;
   return FP8_OK;
 }
 W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
@@ -1104,7 +1105,7 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
   a.zero = w.zero;
   a.x = x;
   a.out = out;
-  a.T = (int)T;
+  a.T = a.P = (int)T;
   a.E = (int)w.E;
   a.k = 1;
   a.N = a.rows = (int)w.rows;
@@ -1112,13 +1113,24 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
   a.group = w.group;
   return a;
 }
+// Blocks of tokens of one weight's product, which run side by side.
+int w4_token_blocks(int64_t T, const W4Plan &p) { return (int)cdiv(T, 8 * p.nt); }
+W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
+  const int tokens = (int)std::min<int64_t>(T, 1024);
+  W4Plan p = w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, 1, false);
+  const int blocks = w4_token_blocks(T, p);
+  return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, false);
+}
+size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
+  return p.parts > 1 ? (size_t)p.parts * T * w.rows * 4 : 0;
+}
 // One weight for T tokens.
-fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated, int act, void *out,
-                    fp8_stream_t stream) {
+fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated, int act, void *out, void *ws,
+                    size_t ws_bytes, fp8_stream_t stream) {
   const fp8_status st = check_w4(w);
   if (st != FP8_OK) return st;
   if (w->E != 1 || T < 0 || (act != FP8_ACT_SILU && act != FP8_ACT_GELU)) return FP8_ERR_INVALID_ARG;
-  if ((gated && w->rows % 32) || T > (1 << 30)) return FP8_ERR_SHAPE;
+  if ((gated && w->rows % 32) || T > kMaxW4Tokens) return FP8_ERR_SHAPE;
   if (T == 0 || w->rows == 0) return FP8_OK;
   if (!out) return FP8_ERR_INVALID_ARG;
   if (!aligned16(out)) return FP8_ERR_ALIGN;
@@ -1132,26 +1144,41 @@ fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated
     a.act = act;
     a.N = a.rows / 2;
   }
-  return from_cuda(launch_w4_product(a, 1, (int)std::min<int64_t>(T, 1024), cs(stream)));
+  const W4Plan p = w4_dense_plan(*w, T, gated);
+  const size_t need = w4_dense_bytes(*w, T, p);
+  if (need) {
+    if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if (!aligned16(ws)) return FP8_ERR_ALIGN;
+    a.part = ws;
+  }
+  return from_cuda(launch_w4_product(a, p, w4_token_blocks(T, p), cs(stream)));
 }
 struct W4Workspace {
+  W4Plan up, down;
   int *counts, *offsets, *position, *order, *hist;
+  float *up_part;
   void *h;
   float *z;
   size_t bytes;
 };
-W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t F, int64_t N) {
+W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int64_t F, int64_t N) {
   Carver c(base);
   const int64_t slots = T * k;
   const int chunks = order_chunks(slots);
+  // twice the mean, so that few experts have more tokens than a block takes at once
+  const int likely = T == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024);
+  const int lists = (int)std::min(E, slots);
   W4Workspace w;
+  w.up = w4_plan((int)F, (int)K, true, likely, lists, false);
+  w.down = w4_plan((int)N, (int)F, false, likely, lists, true);
   w.counts = c.take<int>(4 * E);
   w.offsets = c.take<int>(4 * (E + 1));
   w.position = c.take<int>(4 * slots);
   w.order = c.take<int>(4 * slots);
   w.hist = c.take<int>(chunks > 1 ? 4 * E * chunks : 0);
+  w.up_part = c.take<float>(w.up.parts > 1 ? 8 * slots * F * w.up.parts : 0);
   w.h = c.take<void>(2 * slots * F);
-  w.z = c.take<float>(4 * slots * N);
+  w.z = c.take<float>(4 * slots * N * w.down.parts);
   w.bytes = c.off;
   return w;
 }
@@ -1283,24 +1310,38 @@ fp8_status fp8_w4_quantize(const void *w, int64_t rows, int64_t K, int group, ui
   if (rows % 16 || K % 32 || K > (1 << 30) || (K && rows > (int64_t(1) << 33) / cdiv(K, group))) return FP8_ERR_SHAPE;
   if (rows == 0 || K == 0) return FP8_OK;
   if (!w || !codes || !scale) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(w) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scale) & 1)) return FP8_ERR_ALIGN;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scale) || !aligned16(zero)) return FP8_ERR_ALIGN;
   return from_cuda(launch_w4_quantize(w, rows, K, group, codes, scale, zero, cs(stream)));
 }
 
-fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y, fp8_stream_t stream) {
-  return w4_dense(x, T, w, false, FP8_ACT_SILU, y, stream);
-}
-
-fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h, fp8_stream_t stream) {
-  return w4_dense(x, T, w, true, act, h, stream);
-}
-
-fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t F, int64_t N, size_t *bytes) {
+fp8_status fp8_w4_workspace_size(const fp8_w4_weight *w, int64_t T, int gated, size_t *bytes) {
   if (!bytes) return FP8_ERR_INVALID_ARG;
-  fp8_status st = check_rows(T, 0, k, E, 1);
+  const fp8_status st = check_w4(w);
   if (st != FP8_OK) return st;
-  if (F < 0 || N < 0 || F % 32 || N % 16 || F > (1 << 29) || N > (1 << 30)) return FP8_ERR_SHAPE;
-  *bytes = w4_workspace(nullptr, T, k, E, F, N).bytes;
+  if (T < 0) return FP8_ERR_INVALID_ARG;
+  if ((gated && w->rows % 32) || T > kMaxW4Tokens) return FP8_ERR_SHAPE;
+  *bytes = T && w->rows && w->K ? w4_dense_bytes(*w, T, w4_dense_plan(*w, T, gated != 0)) : 0;
+  return FP8_OK;
+}
+
+fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y, void *ws, size_t ws_bytes,
+                         fp8_stream_t stream) {
+  return w4_dense(x, T, w, false, FP8_ACT_SILU, y, ws, ws_bytes, stream);
+}
+
+fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h, void *ws,
+                        size_t ws_bytes, fp8_stream_t stream) {
+  return w4_dense(x, T, w, true, act, h, ws, ws_bytes, stream);
+}
+
+fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t K, int64_t F, int64_t N, size_t *bytes) {
+  if (!bytes) return FP8_ERR_INVALID_ARG;
+  const fp8_status st = check_rows(T, 0, k, E, 1);
+  if (st != FP8_OK) return st;
+  if (K < 0 || F < 0 || N < 0) return FP8_ERR_INVALID_ARG;
+  if (K % 32 || F % 32 || N % 16 || K > (1 << 26) || F > (1 << 25) || N > (1 << 26) || T * k > kMaxW4Tokens * 64)
+    return FP8_ERR_SHAPE;
+  *bytes = T && K && F && N ? w4_workspace(nullptr, T, k, E, K, F, N).bytes : 0;
   return FP8_OK;
 }
 
@@ -1311,17 +1352,17 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   if (st == FP8_OK) st = check_w4(down);
   if (st != FP8_OK) return st;
   if (T < 0 || k < 1 || (act != FP8_ACT_SILU && act != FP8_ACT_GELU)) return FP8_ERR_INVALID_ARG;
-  const int64_t E = gate_up->E, F = down->K, N = down->rows;
+  const int64_t E = gate_up->E, K = gate_up->K, F = down->K, N = down->rows;
   if (down->E != E || gate_up->rows != 2 * F) return FP8_ERR_SHAPE;
   size_t need = 0;
-  st = fp8_w4_experts_workspace_size(T, k, E, F, N, &need);
+  st = fp8_w4_experts_workspace_size(T, k, E, K, F, N, &need);
   if (st != FP8_OK) return st;
   if (T == 0 || N == 0) return FP8_OK;
-  if (!F || !gate_up->K) return FP8_ERR_SHAPE;
+  if (!F || !K) return FP8_ERR_SHAPE;
   if (!x || !weights || !experts || !y) return FP8_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return FP8_ERR_ALIGN;
   if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
-  const W4Workspace w = w4_workspace(ws, T, k, E, F, N);
+  const W4Workspace w = w4_workspace(ws, T, k, E, K, F, N);
   const int64_t slots = T * k;
   // one token: its slots stand in their own order
   const bool sorted = T > 1;
@@ -1334,22 +1375,25 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   a.gated = a.tokens = 1;
   a.act = act;
   a.N = (int)F;
+  a.part = w.up_part;
   b.out_f32 = 1;
-  const int lists = (int)std::min(E, slots);
+  b.part = w.z;
+  const int lists = (int)(sorted ? std::min(E, slots) : slots);
   for (W4Args *p : {&a, &b}) {
     p->experts = experts;
     p->k = k;
+    p->P = (int)slots;
     if (sorted) {
       p->order = w.order;
       p->offsets = w.offsets;
       p->counts = w.counts;
       p->by_row = slots < E;
     }
-    st = from_cuda(launch_w4_product(*p, sorted ? lists : k, (int)std::min<int64_t>(cdiv(slots, E), 1024), cs(stream)));
+    st = from_cuda(launch_w4_product(*p, p == &a ? w.up : w.down, lists, cs(stream)));
     if (st != FP8_OK) return st;
   }
-  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, y,
-                                  cs(stream)));
+  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, w.down.parts,
+                                  y, cs(stream)));
 }
 
 fp8_status fp8_profile_begin(void) {

@@ -228,24 +228,32 @@ cudaError_t launch_rows_combine_bwd(const void *dy, const void *z, const int *po
 // 4-bit weights (w4.cu).  One weight: experts null, T tokens.  A stack: `experts`
 // the slots' experts [T k], order/offsets/counts their rows in the experts'
 // order (null for one token, whose slots are the rows); tokens: x has a row per
-// token, else per row of that order.  groups, warps_k are filled in by the launch.
+// token, else per row of that order.
 struct W4Args {
   const uint8_t *codes;   // [E, rows, K / 2]
   const uint16_t *scale;  // bf16 [E, rows, ceil(K / group)]
   const uint8_t *zero;    // the same shape, or null: 8
   const void *x;
-  void *out;              // gated: bf16 [., N]; else bf16 or fp32
+  void *out;              // gated: bf16 [P, N]; else bf16, or (out_f32) fp32 [parts, P, N]
+  void *part;             // fp32 [parts, P, rows], with more than one part
   const int *experts, *order, *offsets, *counts;
-  int T, E, k, by_row, tokens;
-  int N, rows, K, group;  // N outputs; rows = 2 N when gated
+  int T, P, E, k, by_row, tokens;  // P: output rows (T, or the slots)
+  int N, rows, K, group;           // N outputs; rows = 2 N when gated
   int gated, act, out_f32;
-  int groups, warps_k;
+  int groups;  // filled in by the launch
 };
-// lists: rows of the grid, one per expert (or per row, by_row); likely: tokens
-// that an expert may be expected to have.
-cudaError_t launch_w4_product(W4Args a, int lists, int likely, cudaStream_t st);
+// How a product is cut: n-tiles of 8 tokens, parts of K, warps (256 of K each)
+// and blocks to a part.  tokens: as many as a list may be expected to have;
+// lists: weights that are read at once; joined: the caller sums the parts.
+struct W4Plan {
+  int nt, parts, warps, blocks;
+};
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, bool joined);
+// lists: the grid's lists, one per expert (or per row, by_row); one weight: blocks
+// of 8 nt tokens.  Sums the parts unless out_f32.
+cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st);
 cudaError_t launch_w4_join(const float *z, const int *experts, const int *position, const float *weights, int64_t T,
-                           int64_t N, int k, int E, void *y, cudaStream_t st);
+                           int64_t N, int k, int E, int parts, void *y, cudaStream_t st);
 cudaError_t launch_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes, void *scale,
                                uint8_t *zero, cudaStream_t st);
 

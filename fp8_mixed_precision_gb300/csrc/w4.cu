@@ -5,14 +5,26 @@
 //
 // for one weight, or for a stack of experts each with its own tokens.
 //
-// Bound by the weights' bytes: each is read once, by asynchronous copies into a
-// ring that every warp has for itself.  A warp holds tiles of 16 weight rows
-// against 8 NT tokens on mma.m16n8k16: code - zero is an integer of at most 15
-// in magnitude, exact in bf16, so the products within a group are exact and
-// their sum (fp32) is scaled once per group; no weight is ever rounded.  The
-// codes of a 32-bit word are k .. k + 7; one and + or turns nibbles i and i + 4
-// into the bf16 pair (128 + code), one packed subtraction takes 128 + zero off,
-// and the tokens' values are paired to match (x_i, x_{i+4}).
+// Bound by the weights' bytes, if the instructions per byte stay few.  They do with
+// fp16 operands on mma.m16n8k16: a 16-bit half with a code in its lowest four or
+// next four bits is the fp16 number code 2^-24 or code 2^-20 (subnormal), so a word
+// of eight codes becomes four operand registers by four masks and one shift, and
+// nothing is ever rounded on the weights' side.  (As bf16 operands, by or-ing codes
+// into mantissas and subtracting 128 + zero, it took 15 instructions for these 5 and
+// 21.5 us for one token through [28672, 4096]; as E4M3 bytes the instruction is
+// emulated on this GPU, 25.9 us.)
+//
+// The tokens' values are scaled by a power of two, to [2^14, 2^15) for the largest
+// of a warp's 256, and become fp16 too: exact for every bf16 value down to 2^-27 of
+// that largest one, and below within 2^-36 of it, far less than the rounding of the
+// fp32 sums.  Products are exact, sums fp32; zero points enter as zero times the
+// group's sum of x; the scale is applied once per group.
+//
+// A block takes a range of K (256 to a warp) and walks over the weight's rows, 16
+// at a time, its tokens' values in registers throughout and the codes on their way
+// through a ring of asynchronous copies that every warp has for itself.  Two tiles
+// of rows (gated: one of the gate, one of the up projection) end in an exchange of
+// the warps' sums.  K beyond one block's range is summed by a second kernel.
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,40 +34,71 @@
 namespace fp8lin {
 namespace {
 
-constexpr int kW4Warps = 8, kW4Threads = 32 * kW4Warps;
-constexpr int kStages = 3;
-constexpr int kChunk = 256;              // codes of a row in a stage: 128 bytes
+constexpr int kChunk = 256;              // codes of a row in a tile: 128 bytes
 constexpr int kTileBytes = 16 * kChunk / 2;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kColStride = 20;           // floats from one token's partial sums to the next's
+constexpr int kTokenStride = 36;         // floats from one token's sums to the next's: no bank conflicts
+// Warps of an SM: registers allow 16 with up to 8 tokens to a block, 8 with more.
+constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 8; }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// D = A B (the first product of a group), and D += A B, on fp16 operands.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Codes i and i + 4 of a word, as bf16, less zz = (128 + zero, 128 + zero).
-__device__ __forceinline__ uint32_t codes_at(uint32_t w, int i, uint32_t zz) {
-  const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&zz));
-  return *reinterpret_cast<const uint32_t *>(&d);
+// What a tile of a warp's ring holds: the codes, and of each row the aligned words
+// that hold its scales and zero points, wherever those begin.
+template <int GROUP>
+struct Tile {
+  static constexpr int kGroups = kChunk / GROUP;  // of a row in a tile
+  static constexpr int kScaleWords = kGroups / 2 + 1, kZeroWords = (kGroups + 3 + 3) / 4;
+  static constexpr int kScale = kTileBytes, kZero = kScale + 16 * kScaleWords * 4;
+  static constexpr int kBytes = kZero + 16 * kZeroWords * 4;
+  static constexpr int kStages = GROUP == 32 ? 4 : 5;
+};
+// A zero point as a number.
+__device__ __forceinline__ float number_of(uint8_t z) { return __uint_as_float(0x4b000000u | z) - 8388608.0f; }
+
+// A lane's N neighbouring words of a row.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
 }
-__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
-// The tokens of block row y: expert, first row in the experts' order and count.
+// The tokens of list y: expert, first row in the experts' order and count.
 struct Tokens {
   int e, first, count;
 };
 __device__ __forceinline__ Tokens tokens_of(const W4Args &a, int y) {
-  if (!a.experts) return {0, 0, a.T};
   const auto valid = [&](int e) { return e >= 0 && e < a.E; };
   if (!a.order) {  // one token: its slots are the rows
     const int e = a.experts[y];
@@ -70,201 +113,267 @@ __device__ __forceinline__ Tokens tokens_of(const W4Args &a, int y) {
   return {e, a.offsets[e], a.counts[e]};
 }
 
-// TILES: tiles of 16 weight rows to a warp (gated: one of the gate, one of the
-// up projection).  GROUP: weights to a scale.
-template <int TILES, int NT, int GROUP>
-__global__ void __launch_bounds__(kW4Threads) w4_kernel(const W4Args a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kStage = TILES * kTileBytes;
-  constexpr int kGroups = kChunk / GROUP;      // groups of a row in a chunk
-  constexpr int kHeld = kGroups / 2;           // of a tile's 2 kGroups scales, those that a lane loads
-  constexpr int kSteps = GROUP / 32;           // 32-deep steps to a group
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int kw = a.warps_k, wk = warp % kw, wr = warp / kw;
-  uint8_t *ring = smem + warp * kStages * kStage;
-  pdl_wait_then_release();
-  const Tokens tk = tokens_of(a, blockIdx.y);
-  if (tk.count == 0) return;
-  const int tile = blockIdx.x * (kW4Warps / kw) + wr;  // of 16 TILES output rows (gated: 16)
-  const int rows_out = a.gated ? 16 : 16 * TILES;
-  const int n0 = tile * rows_out;
-  const int64_t row_bytes = a.K / 2;
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  const bool live = n0 < a.N;
-  // first weight row of each tile within the stack
-  int64_t first[TILES];
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) {
-    int r = a.gated ? i * a.N + n0 : n0 + 16 * i;
-    if (r > a.rows - 16) r = a.rows - 16;  // a second tile past the last row: not stored
-    first[i] = (int64_t)tk.e * a.rows + (live ? r : 0);
+__device__ __forceinline__ float gate_times(float gate, float up, int act) {
+  float h;
+  if (act == FP8_ACT_SILU) {
+    const float t = expf(-fabsf(gate));  // no overflow on either side
+    h = gate * __fdiv_rn(gate >= 0.0f ? 1.0f : t, 1.0f + t);
+  } else {
+    float unused;
+    gelu_f2(gate, gate, h, unused);
   }
+  return h * up;
+}
 
-  const auto request = [&](int c, int stage) {
-    if (live && c < chunks) {
+// NT: n-tiles, of 8 tokens each.  GROUP: weights to a scale.
+template <int NT, int GROUP>
+__global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using R = Tile<GROUP>;
+  constexpr int kTokens = 8 * NT;
+  constexpr int kGroups = R::kGroups, kStages = R::kStages;
+  constexpr int kSteps = GROUP / 32;  // 32-deep steps to a group
+  // A lane takes kSteps neighbouring words of a row's group, lane q those from
+  // q kSteps on.  The 16-byte pieces of a row stand at piece ^ f(row), so that
+  // these loads touch every bank once.
+  constexpr int kRows = 8 / kSteps;
+  const int kw = blockDim.x / 32, wk = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  uint8_t *ring = smem + wk * kStages * R::kBytes;
+  float *part = reinterpret_cast<float *>(smem + kw * kStages * R::kBytes);  // [2][kw][kTokens][kTokenStride]
+  float *sums = part + 2 * kw * kTokens * kTokenStride + wk * kTokens * kGroups;  // [kGroups][kTokens]
+  pdl_wait_then_release();
+  const bool list = a.experts != nullptr;
+  const Tokens tk = list ? tokens_of(a, blockIdx.z) : Tokens{0, 0, a.T};
+  const int chunk = blockIdx.y * kw + wk, k0 = chunk * kChunk;
+  const int row_bytes = a.K / 2;
+  const int items = (a.N + (a.gated ? 15 : 31)) / (a.gated ? 16 : 32);
+  const int tiles = 2 * ((items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
+  // first weight row of tile n of this block (two tiles to an item)
+  const auto row_of = [&](int n) {
+    const int item = blockIdx.x + (n >> 1) * gridDim.x;
+    const int r = a.gated ? (n & 1) * a.N + item * 16 : item * 32 + (n & 1) * 16;
+    return r <= a.rows - 16 ? r : 0;  // past the last row: read, not stored
+  };
+  // the piece of 16 bytes that this lane copies of every fourth row, and where
+  // it goes in rows lane / 8 + 8 .. and lane / 8 + 4 + 8 ..
+  const bool in = k0 + 32 * (lane & 7) < a.K;
+  const uint8_t *codes = a.codes + ((int64_t)tk.e * a.rows + (lane >> 3)) * row_bytes + (in ? k0 / 2 + 16 * (lane & 7) : 0);
+  const uint32_t bytes = in ? 16u : 0u;
+  uint8_t *to = ring + (lane >> 3) * 128;
+  const int piece0 = ((lane & 7) ^ ((lane >> 3) % kRows * kSteps)) << 4;
+  const int piece1 = ((lane & 7) ^ (((lane >> 3) + 4) % kRows * kSteps)) << 4;
+  // Scales and zero points: this lane copies the words lane, lane + 32, .. of the
+  // 16 rows' words, each as far as its row and chunk need it (so nothing behind the
+  // arrays is touched).  Weight rows come in sixteens: what is aligned stays so.
+  const int group0 = chunk * kGroups, need = min(kGroups, a.groups - group0);  // perhaps none
+  constexpr int kScaleOps = (16 * R::kScaleWords + 31) / 32, kZeroOps = (16 * R::kZeroWords + 31) / 32;
+  const uint8_t *scale[kScaleOps], *zero[kZeroOps];
+  uint32_t scale_bytes[kScaleOps], zero_bytes[kZeroOps];
+  const auto word = [&](const uint8_t *base, int size, int id, int words, const uint8_t *&src, uint32_t &count) {
+    const int64_t at = (((int64_t)tk.e * a.rows + id / words) * a.groups + group0) * size;
+    const int lead = (int)(at & 3), left = lead + need * size - 4 * (id % words);  // bytes from this word on
+    count = need > 0 && left > 0 ? (uint32_t)min(left, 4) : 0u;
+    src = base + (count ? at - lead + 4 * (id % words) : 0);
+  };
 #pragma unroll
-      for (int i = 0; i < TILES; ++i)
+  for (int m = 0; m < kScaleOps; ++m)
+    word(reinterpret_cast<const uint8_t *>(a.scale), 2, lane + 32 * m, R::kScaleWords, scale[m], scale_bytes[m]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = (lane >> 3) + 4 * j, p = lane & 7;
-          const bool in = c * kChunk + p * 32 < a.K;
-          const uint8_t *src = a.codes + (first[i] + r) * row_bytes + (in ? c * (kChunk / 2) + p * 16 : 0);
-          ptx::cp_async16_zfill(ring + stage * kStage + i * kTileBytes + r * 128 + ((p ^ (r & 7)) << 4), src,
-                                in ? 16u : 0u);
-        }
+  for (int m = 0; m < kZeroOps; ++m) word(a.zero, 1, lane + 32 * m, R::kZeroWords, zero[m], zero_bytes[m]);
+  const auto request = [&](int n, int stage) {
+    if (n < tiles) {
+      const int row = row_of(n);
+      const uint8_t *from = codes + (int64_t)row * row_bytes;
+      uint8_t *dst = to + stage * R::kBytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ptx::cp_async16_zfill(dst + 512 * j + (j & 1 ? piece1 : piece0), from + 4 * j * row_bytes, bytes);
+      const int64_t groups = (int64_t)row * a.groups;
+      uint8_t *at = ring + stage * R::kBytes + 4 * lane;
+#pragma unroll
+      for (int m = 0; m < kScaleOps; ++m)
+        if (lane + 32 * m < 16 * R::kScaleWords)
+          ptx::cp_async4(at + R::kScale + 128 * m, scale[m] + 2 * groups, scale_bytes[m]);
+      if (a.zero) {
+#pragma unroll
+        for (int m = 0; m < kZeroOps; ++m)
+          if (lane + 32 * m < 16 * R::kZeroWords)
+            ptx::cp_async4(at + R::kZero + 128 * m, zero[m] + groups, zero_bytes[m]);
+      }
     }
     ptx::cp_async_commit();
   };
-  // Of the scales of rows g and g + 8 (half h, group s of the chunk: number
-  // h kGroups + s), lane q of a row's four holds those of number q modulo 4:
-  // the scale in the upper, 128 + zero (bf16) in the lower 16 bits.
-  const auto scales = [&](int c, uint32_t (&sz)[TILES][kHeld]) {
+  // where this lane's rows g and g + 8 have their first scale and zero point in a tile
+  const int lead2 = (g & a.groups & 1) * 2, lead1 = (g * a.groups + group0) & 3;
+  const int scale_lo = R::kScale + g * R::kScaleWords * 4 + lead2, scale_hi = scale_lo + 8 * R::kScaleWords * 4;
+  const int zero_lo = R::kZero + g * R::kZeroWords * 4 + lead1, zero_hi = zero_lo + 8 * R::kZeroWords * 4;
+
+  for (int tb = list ? 0 : blockIdx.z * kTokens; tb < tk.count; tb += list ? kTokens : gridDim.z * kTokens) {
 #pragma unroll
-    for (int i = 0; i < TILES; ++i)
+    for (int s = 0; s < kStages - 1; ++s) request(s, s);
+    // Column g of n-tile j is token 8 j + g; lane (g, q) has the values that its
+    // words' codes meet, those of the codes at bit 4 of a half divided by 16.
+    uint32_t b[NT][8][4];
+    float unscale[NT][2];  // of tokens 8 j + 2 q, + 1
 #pragma unroll
-      for (int m = 0; m < kHeld; ++m) {
-        const int id = q + 4 * m, h = id / kGroups, s = id % kGroups;
-        const int at = min(c * kGroups + s, a.groups - 1);
-        sz[i][m] = 0u;
-        if (live && c < chunks) {
-          const int64_t o = (first[i] + g + 8 * h) * a.groups + at;
-          sz[i][m] = (uint32_t)a.scale[o] << 16 | 0x4300u | (a.zero ? a.zero[o] & 15u : 8u);
+    for (int j = 0; j < NT; ++j) {
+      const int n = tb + 8 * j + g, p = tk.first + n;
+      const bool some = n < tk.count;
+      const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
+      const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.K + k0 + 8 * kSteps * q;
+      uint4 v[8];
+      uint32_t top = 0u;  // largest |x| as bits, both halves
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int k = s / kSteps * GROUP + s % kSteps * 8;
+        v[s] = make_uint4(0, 0, 0, 0);
+        if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu),
+                                     __vmaxu2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu)));
+      }
+      top = max(top >> 16, top & 0xffffu);
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      // 2^(14 - exponent), at most 2^126; an infinity or a NaN makes the token's product NaN
+      const int up = min(14 + 127 - (int)(top >> 7), 126);
+      const bool bad = top >= 0x7f80u;
+      const float f = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
+      const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 - up) << 23);
+      unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
+      unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
+      float sum = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float x0 = bf16lo(v[s].x) * f, x1 = bf16hi(v[s].x) * f, x2 = bf16lo(v[s].y) * f, x3 = bf16hi(v[s].y) * f;
+        const float x4 = bf16lo(v[s].z) * f, x5 = bf16hi(v[s].z) * f, x6 = bf16lo(v[s].w) * f, x7 = bf16hi(v[s].w) * f;
+        b[j][s][0] = f16x2(x0, x4);
+        b[j][s][1] = f16x2(x1 * 0.0625f, x5 * 0.0625f);
+        b[j][s][2] = f16x2(x2, x6);
+        b[j][s][3] = f16x2(x3 * 0.0625f, x7 * 0.0625f);
+        sum += ((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7));
+        if (s % kSteps == kSteps - 1) {  // the group's sum, in units of the products (2^-24)
+          sum += __shfl_xor_sync(kFull, sum, 1);
+          sum += __shfl_xor_sync(kFull, sum, 2);
+          if (q == 0) sums[s / kSteps * kTokens + 8 * j + g] = sum * 0x1p-24f;
+          sum = 0.0f;
         }
       }
-  };
-
-  for (int tb = 0; tb < tk.count; tb += 8 * NT) {
-    const uint16_t *xp[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int p = tk.first + tb + 8 * n + g;
-      xp[n] = nullptr;
-      if (tb + 8 * n + g < tk.count) {
-        const int64_t row = a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
-        xp[n] = static_cast<const uint16_t *>(a.x) + row * a.K + 8 * q;
-      }
     }
-    float tot[TILES][NT][4] = {};
-    uint32_t sz[TILES][kHeld];
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) request(wk + s * kw, s);
-    scales(wk, sz);
-    int stage = 0;
-    for (int c = wk; c < chunks; c += kw) {
+    __syncwarp();
+
+    int stage = 0, buf = 0;
+    for (int n = 0; n < tiles; ++n) {
       cp_async_wait_group<kStages - 2>();
       __syncwarp();
-      request(c + (kStages - 1) * kw, stage == 0 ? kStages - 1 : stage - 1);
-      uint32_t next[TILES][kHeld];
-      scales(c + kw, next);
-      const uint8_t *base = ring + stage * kStage;
-      if (live) {
+      request(n + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t *held = ring + stage * R::kBytes, *base = held + g * 128 + 4 * kSteps * q;
+      float tot[NT][4] = {};
 #pragma unroll
-        for (int s = 0; s < kGroups; ++s) {
-          uint32_t lo[TILES], hi[TILES];  // rows g, g + 8: scale and zero of this group
+      for (int s = 0; s < kGroups; ++s) {
+        uint32_t w[2][kSteps];  // codes of rows g and g + 8
 #pragma unroll
-          for (int i = 0; i < TILES; ++i) {
-            lo[i] = __shfl_sync(kFull, sz[i][s / 4], s % 4, 4);
-            hi[i] = __shfl_sync(kFull, sz[i][(kGroups + s) / 4], (kGroups + s) % 4, 4);
-          }
-          float acc[TILES][NT][4] = {};
+        for (int h = 0; h < 2; ++h) load_words<kSteps>(base + 8 * 128 * h + ((s ^ g % kRows) * kSteps << 4), w[h]);
+        float acc[NT][4];
 #pragma unroll
-          for (int st = 0; st < kSteps; ++st) {
-            const int step = s * kSteps + st;
-            uint32_t b[NT][4];
+        for (int st = 0; st < kSteps; ++st) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              const int kk = c * kChunk + 32 * step;
-              if (xp[n] && kk < a.K) v = *reinterpret_cast<const uint4 *>(xp[n] + kk);
-              b[n][0] = __byte_perm(v.x, v.z, 0x5410);
-              b[n][1] = __byte_perm(v.x, v.z, 0x7632);
-              b[n][2] = __byte_perm(v.y, v.w, 0x5410);
-              b[n][3] = __byte_perm(v.y, v.w, 0x7632);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w0 = h ? w[0][st] >> 8 : w[0][st], w1 = h ? w[1][st] >> 8 : w[1][st];
+            const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-              const uint8_t *p = base + i * kTileBytes + g * 128 + ((step ^ g) << 4) + 4 * q;
-              const uint32_t w0 = lds32(p), w1 = lds32(p + 8 * 128);
-              const uint32_t z0 = __byte_perm(lo[i], 0, 0x1010), z1 = __byte_perm(hi[i], 0, 0x1010);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a0 = codes_at(w0, 2 * h, z0), a1 = codes_at(w1, 2 * h, z1);
-                const uint32_t a2 = codes_at(w0, 2 * h + 1, z0), a3 = codes_at(w1, 2 * h + 1, z1);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(acc[i][n], a0, a1, a2, a3, b[n][2 * h], b[n][2 * h + 1]);
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < TILES; ++i) {
-            const float s0 = bf16hi(lo[i]), s1 = bf16hi(hi[i]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              tot[i][n][0] = fmaf(acc[i][n][0], s0, tot[i][n][0]);
-              tot[i][n][1] = fmaf(acc[i][n][1], s0, tot[i][n][1]);
-              tot[i][n][2] = fmaf(acc[i][n][2], s1, tot[i][n][2]);
-              tot[i][n][3] = fmaf(acc[i][n][3], s1, tot[i][n][3]);
+            for (int j = 0; j < NT; ++j) {
+              const uint32_t *bb = b[j][s * kSteps + st] + 2 * h;
+              if (st == 0 && h == 0)
+                mma_first(acc[j], a0, a1, a2, a3, bb[0], bb[1]);
+              else
+                mma_add(acc[j], a0, a1, a2, a3, bb[0], bb[1]);
             }
           }
         }
+        const float sl = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_lo + 2 * s));
+        const float sh = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_hi + 2 * s));
+        float zl = -8.0f, zh = -8.0f;
+        if (a.zero) zl = -number_of(held[zero_lo + s]), zh = -number_of(held[zero_hi + s]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float2 x = *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
+          tot[j][0] = fmaf(sl, fmaf(zl, x.x, acc[j][0]), tot[j][0]);
+          tot[j][1] = fmaf(sl, fmaf(zl, x.y, acc[j][1]), tot[j][1]);
+          tot[j][2] = fmaf(sh, fmaf(zh, x.x, acc[j][2]), tot[j][2]);
+          tot[j][3] = fmaf(sh, fmaf(zh, x.y, acc[j][3]), tot[j][3]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < TILES; ++i)
-#pragma unroll
-        for (int m = 0; m < kHeld; ++m) sz[i][m] = next[i][m];
       stage = stage == kStages - 1 ? 0 : stage + 1;
+      float *mine = part + (buf * kw + wk) * kTokens * kTokenStride + 16 * (n & 1) + g;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mine[(8 * j + 2 * q + (i & 1)) * kTokenStride + (i >> 1) * 8] = tot[j][i] * 0x1p24f * unscale[j][i & 1];
+      if (!(n & 1)) continue;
+      // Two buffers in turn: a warp writes one again only behind the barrier that
+      // follows its last readers.
+      __syncthreads();
+      const float *from = part + buf * kw * kTokens * kTokenStride + lane;
+      buf ^= 1;
+      const int item = blockIdx.x + (n >> 1) * gridDim.x, count = min(kTokens, tk.count - tb);
+      const int out = a.gated ? item * 16 + (lane & 15) : item * 32 + lane;
+      // a lane per row; the warps take the tokens in turn, the next ones each time
+      for (int t = (wk + (n >> 1)) % kw; t < count; t += kw) {
+        float v = 0.0f;
+        for (int w = 0; w < kw; ++w) v += from[(w * kTokens + t) * kTokenStride];
+        const int64_t p = tk.first + tb + t;
+        if (gridDim.y > 1) {  // one part of K
+          if (a.gated || out < a.N)
+            static_cast<float *>(a.part)[(blockIdx.y * (int64_t)a.P + p) * a.rows + (lane & 16 && a.gated ? a.N : 0) +
+                                         out] = v;
+        } else if (a.gated) {
+          const float up = __shfl_down_sync(kFull, v, 16);
+          if (lane < 16) static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(gate_times(v, up, a.act));
+        } else if (out < a.N) {
+          if (a.out_f32)
+            static_cast<float *>(a.out)[p * a.N + out] = v;
+          else
+            static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(v);
+        }
+      }
     }
     cp_async_wait_group<0>();
-    __syncwarp();
-    // partial sums over K, [tile][token][row], in the warp's own ring
-    float *mine = reinterpret_cast<float *>(ring);
-#pragma unroll
-    for (int i = 0; i < TILES; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          mine[(i * 8 * NT + 8 * n + 2 * q + (v & 1)) * kColStride + g + (v >> 1) * 8] = tot[i][n][v];
-    __syncthreads();
-    const int per = a.gated ? 16 : 16 * TILES;  // output rows of a tile
-    for (int id = threadIdx.x; id < kW4Warps / kw * per * 8 * NT; id += kW4Threads) {
-      const int r = id % per, n = id / per % (8 * NT), w0 = id / (per * 8 * NT) * kw;
-      const int out = (blockIdx.x * (kW4Warps / kw) + id / (per * 8 * NT)) * per + r;
-      if (tb + n >= tk.count || out >= a.N) continue;
-      const float *from = reinterpret_cast<const float *>(smem + w0 * kStages * kStage);
-      constexpr int kWarpFloats = kStages * kStage / 4;
-      const auto sum = [&](int i) {
-        float s = 0.0f;
-        for (int w = 0; w < kw; ++w) s += from[w * kWarpFloats + (i * 8 * NT + n) * kColStride + (r & 15)];
-        return s;
-      };
-      const int64_t o = (int64_t)(tk.first + tb + n) * a.N + out;
-      if (a.gated) {
-        const float gate = sum(0), up = sum(TILES - 1);
-        float h;
-        if (a.act == FP8_ACT_SILU) {
-          const float t = expf(-fabsf(gate));  // no overflow on either side
-          h = gate * __fdiv_rn(gate >= 0.0f ? 1.0f : t, 1.0f + t);
-        } else {
-          float unused;
-          gelu_f2(gate, gate, h, unused);
-        }
-        static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(h * up);
-      } else if (a.out_f32) {
-        static_cast<float *>(a.out)[o] = sum(r >> 4);
-      } else {
-        static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum(r >> 4));
-      }
-    }
     __syncthreads();
   }
 }
 
-// y[t] = sum_j w[t, j] z[row of slot t k + j], z fp32.
+// Sums the parts of K: four outputs a thread.
+__global__ void __launch_bounds__(256) w4_finish_kernel(const float *__restrict__ part, int64_t total, int64_t plane,
+                                                        int parts, int vecs, int N, int gated, int act,
+                                                        void *__restrict__ out) {
+  pdl_wait_then_release();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int64_t p = i / vecs;
+  const int c = (int)(i - p * vecs) * 4;
+  const auto sum = [&](int64_t at) {
+    float4 s = *reinterpret_cast<const float4 *>(part + at);
+    for (int k = 1; k < parts; ++k) {
+      const float4 v = *reinterpret_cast<const float4 *>(part + k * plane + at);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    return s;
+  };
+  float4 v = sum(p * (gated ? 2 : 1) * N + c);
+  if (gated) {
+    const float4 u = sum(p * 2 * N + N + c);
+    v = make_float4(gate_times(v.x, u.x, act), gate_times(v.y, u.y, act), gate_times(v.z, u.z, act),
+                    gate_times(v.w, u.w, act));
+  }
+  reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// y[t] = sum_j w[t, j] z[row of slot t k + j], z fp32 in `parts` planes.
 __global__ void __launch_bounds__(256) w4_join_kernel(const float *__restrict__ z, const int *__restrict__ experts,
                                                       const int *__restrict__ position,
                                                       const float *__restrict__ weights, int64_t total, int vecs, int k,
-                                                      int E, void *__restrict__ y) {
+                                                      int E, int parts, int64_t plane, void *__restrict__ y) {
   pdl_wait_then_release();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
@@ -276,7 +385,13 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const float *__restrict__ 
     const int e = experts[slot];
     const float w = weights[slot];
     float4 v = make_float4(0, 0, 0, 0);
-    if (e >= 0 && e < E) v = reinterpret_cast<const float4 *>(z)[(position ? position[slot] : slot) * vecs + c];
+    if (e >= 0 && e < E) {
+      const float *from = z + ((position ? position[slot] : slot) * vecs + c) * 4;
+      for (int m = 0; m < parts; ++m) {
+        const float4 u = *reinterpret_cast<const float4 *>(from + m * plane);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+    }
     s.x = fmaf(w, v.x, s.x);
     s.y = fmaf(w, v.y, s.y);
     s.z = fmaf(w, v.z, s.z);
@@ -332,51 +447,81 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
   }
 }
 
-template <int TILES, int NT, int GROUP>
-cudaError_t launch_w4(const W4Args &a, dim3 grid, cudaStream_t st) {
-  constexpr size_t smem = (size_t)kW4Warps * kStages * TILES * kTileBytes;
-  static_assert(TILES * 8 * NT * kColStride * 4 <= kStages * TILES * kTileBytes, "partial sums fit a warp's ring");
+template <int NT, int GROUP>
+cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  const auto bytes = [](int warps) {
+    return (size_t)warps * (Tile<GROUP>::kStages * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 + 8 * NT * (kChunk / GROUP) * 4);
+  };
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(w4_kernel<TILES, NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)bytes(w4_warps(NT)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  return launch_kernel(w4_kernel<TILES, NT, GROUP>, grid, dim3(kW4Threads), smem, st, a);
+  return launch_kernel(w4_kernel<NT, GROUP>, dim3((unsigned)p.blocks, (unsigned)p.parts, (unsigned)lists),
+                       dim3(32 * p.warps), bytes(p.warps), st, a);
 }
-template <int TILES, int NT>
-cudaError_t by_group(const W4Args &a, dim3 grid, cudaStream_t st) {
-  if (a.group == 32) return launch_w4<TILES, NT, 32>(a, grid, st);
-  if (a.group == 64) return launch_w4<TILES, NT, 64>(a, grid, st);
-  return launch_w4<TILES, NT, 128>(a, grid, st);
+template <int NT>
+cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  if (a.group == 32) return launch_w4<NT, 32>(a, p, lists, st);
+  if (a.group == 64) return launch_w4<NT, 64>(a, p, lists, st);
+  return launch_w4<NT, 128>(a, p, lists, st);
 }
 
 }  // namespace
 
-cudaError_t launch_w4_product(W4Args a, int lists, int likely, cudaStream_t st) {
-  a.groups = (a.K + a.group - 1) / a.group;
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  for (a.warps_k = kW4Warps; a.warps_k > chunks; a.warps_k /= 2) {
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, bool joined) {
+  W4Plan best = {};
+  best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
+  const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;
+  const int most = w4_warps(best.nt);
+  double least = 0.0;
+  for (int64_t parts = (chunks + most - 1) / most; parts <= std::max<int64_t>(16, (chunks + most - 1) / most); ++parts) {
+    if (parts > chunks) break;
+    const int64_t warps = (chunks + parts - 1) / parts, slots = sms * (most / warps);
+    const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / (parts * lists)));
+    const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * lists + sms - 1) / sms;
+    // in times of an SM's share of memory bandwidth for 4 KB (a warp's two tiles),
+    // about 0.1 us; an exchange costs about 2 of them, the sum over the parts 15
+    const double cost = (double)rounds * (double)(warps * together + 2) + (parts > 1 && !joined ? 15.0 : 0.0);
+    if (best.warps == 0 || cost < least) {
+      least = cost;
+      best.warps = (int)warps;
+      best.parts = (int)((chunks + warps - 1) / warps);
+      best.blocks = (int)blocks;
+    }
   }
-  const int tiles = a.gated ? (a.N + 15) / 16 : (a.N + 31) / 32;
-  const dim3 grid((unsigned)((tiles + kW4Warps / a.warps_k - 1) / (kW4Warps / a.warps_k)), (unsigned)lists);
-  const double weights = (double)a.rows * a.K * (a.experts ? std::min(a.E, lists) : 1);
-  LaunchScope ls(a.gated ? "w4_gated" : "w4_linear", st, weights * (0.5 + (a.zero ? 3.0 : 2.0) / a.group),
-                 2.0 * a.rows * a.K * a.T, a.T, a.N, a.K);
-  if (likely <= 8) return by_group<2, 1>(a, grid, st);
-  if (likely <= 16) return by_group<2, 2>(a, grid, st);
-  return by_group<2, 4>(a, grid, st);
+  return best;
+}
+
+cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st) {
+  a.groups = (a.K + a.group - 1) / a.group;
+  {
+    const double weights = (double)a.rows * a.K * (a.experts ? std::min(a.E, lists) : 1);
+    LaunchScope ls(a.gated ? "w4_gated" : "w4_linear", st, weights * (0.5 + (a.zero ? 3.0 : 2.0) / a.group),
+                   2.0 * a.rows * a.K * a.P, a.P, a.N, a.K);
+    const cudaError_t e = p.nt == 1   ? by_group<1>(a, p, lists, st)
+                          : p.nt == 2 ? by_group<2>(a, p, lists, st)
+                                      : by_group<4>(a, p, lists, st);
+    if (e != cudaSuccess || p.parts == 1 || a.out_f32) return e;
+  }
+  const int vecs = a.N / 4;
+  const int64_t total = (int64_t)a.P * vecs;
+  LaunchScope ls("w4_finish", st, 4.0 * p.parts * a.P * a.rows + 2.0 * a.P * a.N, (double)p.parts * a.P * a.rows, a.P,
+                 a.N, p.parts);
+  return launch_kernel(w4_finish_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st,
+                       (const float *)a.part, total, (int64_t)a.P * a.rows, p.parts, vecs, a.N, a.gated, a.act, a.out);
 }
 
 cudaError_t launch_w4_join(const float *z, const int *experts, const int *position, const float *weights, int64_t T,
-                           int64_t N, int k, int E, void *y, cudaStream_t st) {
+                           int64_t N, int k, int E, int parts, void *y, cudaStream_t st) {
   const int vecs = (int)(N / 4);
-  LaunchScope ls("w4_join", st, 4.0 * T * N * k + 2.0 * T * N, 2.0 * T * N * k, T, N, k);
+  LaunchScope ls("w4_join", st, 4.0 * T * N * k * parts + 2.0 * T * N, 2.0 * T * N * k, T, N, k);
   return launch_kernel(w4_join_kernel, dim3((unsigned)((T * vecs + 255) / 256)), dim3(256), 0, st, z, experts, position,
-                       weights, T * vecs, vecs, k, E, y);
+                       weights, T * vecs, vecs, k, E, parts, T * k * N, y);
 }
 
 cudaError_t launch_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes, void *scale,

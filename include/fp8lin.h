@@ -547,8 +547,12 @@ fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int6
  *   scale  device bf16 [E, rows, ceil(K / group)]
  *   zero   device u8, of the same shape, 0 .. 15; NULL: 8
  *   rows a multiple of 16, K of 32
- * Products are exact within a group and summed in fp32, for any number of tokens T;
- * written for few (decoding), where the weights' bytes are all that counts.
+ * Products are exact but for values of x under 2^-13 of the largest of their 256
+ * neighbours (k to k + 255, k a multiple of 256), which are taken within 2^-22 of
+ * that one; sums are fp32.  A token with an infinity or a NaN gets NaN.  Any number
+ * of tokens T up to 2^18; written for few (decoding), where the weights' bytes are
+ * all that counts.  ws: fp8_w4_workspace_size bytes (0 for many shapes; then NULL
+ * will do), of one call at a time.
  * fp8_w4_quantize: codes, scales (and zero points, unless NULL) of bf16 weights
  *   [rows, K] by rounding to the nearest: scale = bf16(max |w| / 7) and zero 8, or
  *   scale = bf16((max - min) / 15) with max >= 0 >= min and zero = round(-min / scale);
@@ -570,11 +574,12 @@ typedef struct {
 } fp8_w4_weight;
 fp8_status fp8_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes,
                            void *scale, uint8_t *zero, fp8_stream_t stream);
-fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y,
-                         fp8_stream_t stream);
-fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h,
-                        fp8_stream_t stream);
-fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t F, int64_t N,
+fp8_status fp8_w4_workspace_size(const fp8_w4_weight *w, int64_t T, int gated, size_t *bytes);
+fp8_status fp8_w4_linear(const void *x, int64_t T, const fp8_w4_weight *w, void *y, void *ws,
+                         size_t ws_bytes, fp8_stream_t stream);
+fp8_status fp8_w4_gated(const void *x, int64_t T, const fp8_w4_weight *w, fp8_act act, void *h, void *ws,
+                        size_t ws_bytes, fp8_stream_t stream);
+fp8_status fp8_w4_experts_workspace_size(int64_t T, int k, int64_t E, int64_t K, int64_t F, int64_t N,
                                          size_t *bytes);
 fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
                           const int32_t *experts, const fp8_w4_weight *gate_up,
