@@ -41,15 +41,7 @@ constexpr int kTokenStride = 36;         // floats from one token's sums to the 
 // Warps of an SM: registers allow 16 with up to 8 tokens to a block, 8 with more.
 constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 8; }
 
-// D = A B (the first product of a group), and D += A B, on fp16 operands.
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
+// D += A B on fp16 operands.
 __device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -145,72 +137,84 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   const bool list = a.experts != nullptr;
   const Tokens tk = list ? tokens_of(a, blockIdx.z) : Tokens{0, 0, a.T};
   const int chunk = blockIdx.y * kw + wk, k0 = chunk * kChunk;
-  const int row_bytes = a.K / 2;
-  const int items = (a.N + (a.gated ? 15 : 31)) / (a.gated ? 16 : 32);
-  const int tiles = 2 * ((items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
-  // first weight row of tile n of this block (two tiles to an item)
-  const auto row_of = [&](int n) {
-    const int item = blockIdx.x + (n >> 1) * gridDim.x;
-    const int r = a.gated ? (n & 1) * a.N + item * 16 : item * 32 + (n & 1) * 16;
-    return r <= a.rows - 16 ? r : 0;  // past the last row: read, not stored
-  };
-  // the piece of 16 bytes that this lane copies of every fourth row, and where
-  // it goes in rows lane / 8 + 8 .. and lane / 8 + 4 + 8 ..
-  const bool in = k0 + 32 * (lane & 7) < a.K;
-  const uint8_t *codes = a.codes + ((int64_t)tk.e * a.rows + (lane >> 3)) * row_bytes + (in ? k0 / 2 + 16 * (lane & 7) : 0);
-  const uint32_t bytes = in ? 16u : 0u;
-  uint8_t *to = ring + (lane >> 3) * 128;
-  const int piece0 = ((lane & 7) ^ ((lane >> 3) % kRows * kSteps)) << 4;
-  const int piece1 = ((lane & 7) ^ (((lane >> 3) + 4) % kRows * kSteps)) << 4;
-  // Scales and zero points: this lane copies the words lane, lane + 32, .. of the
-  // 16 rows' words, each as far as its row and chunk need it (so nothing behind the
-  // arrays is touched).  Weight rows come in sixteens: what is aligned stays so.
-  const int group0 = chunk * kGroups, need = min(kGroups, a.groups - group0);  // perhaps none
+  const int row_bytes = a.K / 2, group0 = chunk * kGroups;
+  const int per = a.gated ? 16 : 32, items = (a.N + per - 1) / per, step = per * (int)gridDim.x;
+  // A block's items: output rows from blockIdx.x per on, `step` rows apart, each of
+  // two tiles of 16 weight rows, `second` rows apart.
+  const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int second = a.gated ? a.N : 16;
+  const int64_t row0 = (int64_t)tk.e * a.rows + blockIdx.x * per;
+
+  // Codes: of each tile this lane copies pieces (lane & 3) and 4 + (lane & 3) of
+  // rows lane / 4 and 8 + lane / 4.
+  const int f = g % kRows * kSteps;
+  const int to0 = g * 128 + ((q ^ (f & 3)) << 4) + (f >> 2) * 64, to1 = to0 ^ 64;
+  const uint32_t in0 = k0 + 32 * q < a.K ? 16u : 0u, in1 = k0 + 128 + 32 * q < a.K ? 16u : 0u;
+  const uint8_t *codes = a.codes + (row0 + g) * row_bytes + (in0 ? k0 / 2 + 16 * q : 0);
+  const int next1 = in1 ? 64 : 0;
+  // Scales and zero points: the words lane, lane + 32, .. of the 16 rows' words,
+  // each as far as its row and chunk need it (so nothing behind the arrays is
+  // touched).  Weight rows come in sixteens: what is aligned stays so.
+  const int need = min(kGroups, a.groups - group0);  // perhaps none
   constexpr int kScaleOps = (16 * R::kScaleWords + 31) / 32, kZeroOps = (16 * R::kZeroWords + 31) / 32;
-  const uint8_t *scale[kScaleOps], *zero[kZeroOps];
+  int scale_at[kScaleOps], zero_at[kZeroOps];  // bytes from the item's first row's first group
   uint32_t scale_bytes[kScaleOps], zero_bytes[kZeroOps];
-  const auto word = [&](const uint8_t *base, int size, int id, int words, const uint8_t *&src, uint32_t &count) {
-    const int64_t at = (((int64_t)tk.e * a.rows + id / words) * a.groups + group0) * size;
-    const int lead = (int)(at & 3), left = lead + need * size - 4 * (id % words);  // bytes from this word on
+  const auto word = [&](int size, int id, int words, int &at, uint32_t &count) {
+    const int from = (id / words * a.groups + group0) * size;
+    const int lead = from & 3, left = lead + need * size - 4 * (id % words);  // bytes from this word on
     count = need > 0 && left > 0 ? (uint32_t)min(left, 4) : 0u;
-    src = base + (count ? at - lead + 4 * (id % words) : 0);
+    at = count ? from - lead + 4 * (id % words) : 0;
   };
 #pragma unroll
-  for (int m = 0; m < kScaleOps; ++m)
-    word(reinterpret_cast<const uint8_t *>(a.scale), 2, lane + 32 * m, R::kScaleWords, scale[m], scale_bytes[m]);
+  for (int m = 0; m < kScaleOps; ++m) word(2, lane + 32 * m, R::kScaleWords, scale_at[m], scale_bytes[m]);
 #pragma unroll
-  for (int m = 0; m < kZeroOps; ++m) word(a.zero, 1, lane + 32 * m, R::kZeroWords, zero[m], zero_bytes[m]);
-  const auto request = [&](int n, int stage) {
-    if (n < tiles) {
-      const int row = row_of(n);
-      const uint8_t *from = codes + (int64_t)row * row_bytes;
-      uint8_t *dst = to + stage * R::kBytes;
+  for (int m = 0; m < kZeroOps; ++m) word(1, lane + 32 * m, R::kZeroWords, zero_at[m], zero_bytes[m]);
+  // one tile: codes at `from`, its first row's scales from group `groups` of the stack on
+  const auto request = [&](const uint8_t *from, int64_t groups, uint8_t *stage) {
+    ptx::cp_async16_zfill(stage + to0, from, in0);
+    ptx::cp_async16_zfill(stage + to1, from + next1, in1);
+    from += 8 * row_bytes;
+    ptx::cp_async16_zfill(stage + to0 + 1024, from, in0);
+    ptx::cp_async16_zfill(stage + to1 + 1024, from + next1, in1);
+    const uint8_t *sc = reinterpret_cast<const uint8_t *>(a.scale + groups);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        ptx::cp_async16_zfill(dst + 512 * j + (j & 1 ? piece1 : piece0), from + 4 * j * row_bytes, bytes);
-      const int64_t groups = (int64_t)row * a.groups;
-      uint8_t *at = ring + stage * R::kBytes + 4 * lane;
+    for (int m = 0; m < kScaleOps; ++m)
+      if (16 * R::kScaleWords % 32 == 0 || lane + 32 * m < 16 * R::kScaleWords)
+        ptx::cp_async4(stage + R::kScale + 128 * m + 4 * lane, sc + scale_at[m], scale_bytes[m]);
+    if (a.zero) {
 #pragma unroll
-      for (int m = 0; m < kScaleOps; ++m)
-        if (lane + 32 * m < 16 * R::kScaleWords)
-          ptx::cp_async4(at + R::kScale + 128 * m, scale[m] + 2 * groups, scale_bytes[m]);
-      if (a.zero) {
-#pragma unroll
-        for (int m = 0; m < kZeroOps; ++m)
-          if (lane + 32 * m < 16 * R::kZeroWords)
-            ptx::cp_async4(at + R::kZero + 128 * m, zero[m] + groups, zero_bytes[m]);
-      }
+      for (int m = 0; m < kZeroOps; ++m)
+        if (16 * R::kZeroWords % 32 == 0 || lane + 32 * m < 16 * R::kZeroWords)
+          ptx::cp_async4(stage + R::kZero + 128 * m + 4 * lane, a.zero + groups + zero_at[m], zero_bytes[m]);
     }
-    ptx::cp_async_commit();
   };
   // where this lane's rows g and g + 8 have their first scale and zero point in a tile
   const int lead2 = (g & a.groups & 1) * 2, lead1 = (g * a.groups + group0) & 3;
-  const int scale_lo = R::kScale + g * R::kScaleWords * 4 + lead2, scale_hi = scale_lo + 8 * R::kScaleWords * 4;
+  const int scale_lo = R::kScale + g * R::kScaleWords * 4, scale_hi = scale_lo + 8 * R::kScaleWords * 4;
   const int zero_lo = R::kZero + g * R::kZeroWords * 4 + lead1, zero_hi = zero_lo + 8 * R::kZeroWords * 4;
 
   for (int tb = list ? 0 : blockIdx.z * kTokens; tb < tk.count; tb += list ? kTokens : gridDim.z * kTokens) {
+    // the item whose tiles are requested next; a second tile past the last row: the
+    // first one's rows again, read and not stored
+    const uint8_t *from = codes;
+    int64_t groups = row0 * a.groups;
+    int ahead = 0, into = 0;
+    const auto request_next = [&](int i) {
+      if (ahead < mine) {
+        const int more = i && (a.gated || blockIdx.x * per + ahead * step + 16 < a.N) ? second : 0;
+        request(from + (int64_t)more * row_bytes, groups + (int64_t)more * a.groups, ring + into * R::kBytes);
+        if (i) {
+          ++ahead;
+          from += (int64_t)step * row_bytes;
+          groups += (int64_t)step * a.groups;
+        }
+      }
+      ptx::cp_async_commit();
+      into = into == kStages - 1 ? 0 : into + 1;
+    };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) request(s, s);
+    for (int s = 0; s < kStages - 1; ++s) request_next(s & 1);
+
     // Column g of n-tile j is token 8 j + g; lane (g, q) has the values that its
     // words' codes meet, those of the codes at bit 4 of a half divided by 16.
     uint32_t b[NT][8][4];
@@ -237,91 +241,100 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       // 2^(14 - exponent), at most 2^126; an infinity or a NaN makes the token's product NaN
       const int up = min(14 + 127 - (int)(top >> 7), 126);
       const bool bad = top >= 0x7f80u;
-      const float f = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
+      const float by = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
       const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 - up) << 23);
       unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
       unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
       float sum = 0.0f;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const float x0 = bf16lo(v[s].x) * f, x1 = bf16hi(v[s].x) * f, x2 = bf16lo(v[s].y) * f, x3 = bf16hi(v[s].y) * f;
-        const float x4 = bf16lo(v[s].z) * f, x5 = bf16hi(v[s].z) * f, x6 = bf16lo(v[s].w) * f, x7 = bf16hi(v[s].w) * f;
+        const float x0 = bf16lo(v[s].x) * by, x1 = bf16hi(v[s].x) * by, x2 = bf16lo(v[s].y) * by;
+        const float x3 = bf16hi(v[s].y) * by, x4 = bf16lo(v[s].z) * by, x5 = bf16hi(v[s].z) * by;
+        const float x6 = bf16lo(v[s].w) * by, x7 = bf16hi(v[s].w) * by;
         b[j][s][0] = f16x2(x0, x4);
         b[j][s][1] = f16x2(x1 * 0.0625f, x5 * 0.0625f);
         b[j][s][2] = f16x2(x2, x6);
         b[j][s][3] = f16x2(x3 * 0.0625f, x7 * 0.0625f);
         sum += ((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7));
-        if (s % kSteps == kSteps - 1) {  // the group's sum, in units of the products (2^-24)
+        if (s % kSteps == kSteps - 1) {
+          // the group's sum in units of the products, as it enters them: times -8
+          // with no zero points
           sum += __shfl_xor_sync(kFull, sum, 1);
           sum += __shfl_xor_sync(kFull, sum, 2);
-          if (q == 0) sums[s / kSteps * kTokens + 8 * j + g] = sum * 0x1p-24f;
+          if (q == 0) sums[s / kSteps * kTokens + 8 * j + g] = sum * (a.zero ? -0x1p-24f : -0x1p-21f);
           sum = 0.0f;
         }
       }
     }
     __syncwarp();
 
-    int stage = 0, buf = 0;
-    for (int n = 0; n < tiles; ++n) {
-      cp_async_wait_group<kStages - 2>();
-      __syncwarp();
-      request(n + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-      const uint8_t *held = ring + stage * R::kBytes, *base = held + g * 128 + 4 * kSteps * q;
-      float tot[NT][4] = {};
+    int stage = 0;
+    for (int it = 0; it < mine; ++it) {
+      // two buffers in turn: a warp writes one again only behind the barrier that
+      // follows its last readers
+      float *buffer = part + (it & 1) * kw * kTokens * kTokenStride;
 #pragma unroll
-      for (int s = 0; s < kGroups; ++s) {
-        uint32_t w[2][kSteps];  // codes of rows g and g + 8
+      for (int i = 0; i < 2; ++i) {
+        cp_async_wait_group<kStages - 2>();
+        __syncwarp();
+        request_next((kStages - 1 + i) & 1);
+        const uint8_t *held = ring + stage * R::kBytes, *base = held + g * 128 + 4 * kSteps * q;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        float tot[NT][4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) load_words<kSteps>(base + 8 * 128 * h + ((s ^ g % kRows) * kSteps << 4), w[h]);
-        float acc[NT][4];
+        for (int s = 0; s < kGroups; ++s) {
+          uint32_t w[2][kSteps];  // codes of rows g and g + 8
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
+          for (int h = 0; h < 2; ++h) load_words<kSteps>(base + 8 * 128 * h + ((s ^ g % kRows) * kSteps << 4), w[h]);
+          const float sl = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_lo + lead2 + 2 * s));
+          const float sh = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_hi + lead2 + 2 * s));
+          float acc[NT][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = h ? w[0][st] >> 8 : w[0][st], w1 = h ? w[1][st] >> 8 : w[1][st];
-            const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
+          for (int j = 0; j < NT; ++j) {
+            const float2 x = *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
+            acc[j][0] = acc[j][2] = x.x;
+            acc[j][1] = acc[j][3] = x.y;
+          }
+          if (a.zero) {
+            const float zl = number_of(held[zero_lo + s]), zh = number_of(held[zero_hi + s]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const uint32_t *bb = b[j][s * kSteps + st] + 2 * h;
-              if (st == 0 && h == 0)
-                mma_first(acc[j], a0, a1, a2, a3, bb[0], bb[1]);
-              else
-                mma_add(acc[j], a0, a1, a2, a3, bb[0], bb[1]);
+            for (int j = 0; j < NT; ++j) acc[j][0] *= zl, acc[j][1] *= zl, acc[j][2] *= zh, acc[j][3] *= zh;
+          }
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w0 = h ? w[0][st] >> 8 : w[0][st], w1 = h ? w[1][st] >> 8 : w[1][st];
+              const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+                mma_add(acc[j], a0, a1, a2, a3, b[j][s * kSteps + st][2 * h], b[j][s * kSteps + st][2 * h + 1]);
             }
           }
-        }
-        const float sl = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_lo + 2 * s));
-        const float sh = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_hi + 2 * s));
-        float zl = -8.0f, zh = -8.0f;
-        if (a.zero) zl = -number_of(held[zero_lo + s]), zh = -number_of(held[zero_hi + s]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float2 x = *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
-          tot[j][0] = fmaf(sl, fmaf(zl, x.x, acc[j][0]), tot[j][0]);
-          tot[j][1] = fmaf(sl, fmaf(zl, x.y, acc[j][1]), tot[j][1]);
-          tot[j][2] = fmaf(sh, fmaf(zh, x.x, acc[j][2]), tot[j][2]);
-          tot[j][3] = fmaf(sh, fmaf(zh, x.y, acc[j][3]), tot[j][3]);
+          for (int j = 0; j < NT; ++j) {
+            tot[j][0] = fmaf(sl, acc[j][0], tot[j][0]);
+            tot[j][1] = fmaf(sl, acc[j][1], tot[j][1]);
+            tot[j][2] = fmaf(sh, acc[j][2], tot[j][2]);
+            tot[j][3] = fmaf(sh, acc[j][3], tot[j][3]);
+          }
         }
+        float *to = buffer + wk * kTokens * kTokenStride + 16 * i + g;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            to[(8 * j + 2 * q + (v & 1)) * kTokenStride + (v >> 1) * 8] = tot[j][v] * unscale[j][v & 1];
       }
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      float *mine = part + (buf * kw + wk) * kTokens * kTokenStride + 16 * (n & 1) + g;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mine[(8 * j + 2 * q + (i & 1)) * kTokenStride + (i >> 1) * 8] = tot[j][i] * 0x1p24f * unscale[j][i & 1];
-      if (!(n & 1)) continue;
-      // Two buffers in turn: a warp writes one again only behind the barrier that
-      // follows its last readers.
       __syncthreads();
-      const float *from = part + buf * kw * kTokens * kTokenStride + lane;
-      buf ^= 1;
-      const int item = blockIdx.x + (n >> 1) * gridDim.x, count = min(kTokens, tk.count - tb);
-      const int out = a.gated ? item * 16 + (lane & 15) : item * 32 + lane;
+      const int count = min(kTokens, tk.count - tb), item = blockIdx.x * per + it * step;
+      const int out = item + (a.gated ? lane & 15 : lane);
       // a lane per row; the warps take the tokens in turn, the next ones each time
-      for (int t = (wk + (n >> 1)) % kw; t < count; t += kw) {
+      int t = wk + it % kw;
+      for (t = t >= kw ? t - kw : t; t < count; t += kw) {
         float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += from[(w * kTokens + t) * kTokenStride];
+        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + t) * kTokenStride + lane];
+        v *= 0x1p24f;
         const int64_t p = tk.first + tb + t;
         if (gridDim.y > 1) {  // one part of K
           if (a.gated || out < a.N)
