@@ -1117,9 +1117,9 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
 int w4_token_blocks(int64_t T, const W4Plan &p) { return (int)cdiv(T, 8 * p.nt); }
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   const int tokens = (int)std::min<int64_t>(T, 1024);
-  W4Plan p = w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, 1, false);
+  W4Plan p = w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, 1, T, false);
   const int blocks = w4_token_blocks(T, p);
-  return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, false);
+  return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
   return p.parts > 1 ? (size_t)p.parts * T * w.rows * 4 : 0;
@@ -1169,8 +1169,8 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   const int likely = T == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024);
   const int lists = (int)std::min(E, slots);
   W4Workspace w;
-  w.up = w4_plan((int)F, (int)K, true, likely, lists, false);
-  w.down = w4_plan((int)N, (int)F, false, likely, lists, true);
+  w.up = w4_plan((int)F, (int)K, true, likely, lists, slots, false);
+  w.down = w4_plan((int)N, (int)F, false, likely, lists, slots, true);
   w.counts = c.take<int>(4 * E);
   w.offsets = c.take<int>(4 * (E + 1));
   w.position = c.take<int>(4 * slots);

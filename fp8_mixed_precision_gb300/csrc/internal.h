@@ -244,11 +244,11 @@ struct W4Args {
 };
 // How a product is cut: n-tiles of 8 tokens, parts of K, warps (256 of K each)
 // and blocks to a part.  tokens: as many as a list may be expected to have;
-// lists: weights that are read at once; joined: the caller sums the parts.
+// lists: weights that are read at once; P: output rows; joined: the caller sums the parts.
 struct W4Plan {
   int nt, parts, warps, blocks;
 };
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, bool joined);
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined);
 // lists: the grid's lists, one per expert (or per row, by_row); one weight: blocks
 // of 8 nt tokens.  Sums the parts unless out_f32.
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st);

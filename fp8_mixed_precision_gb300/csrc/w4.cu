@@ -38,8 +38,8 @@ constexpr int kChunk = 256;              // codes of a row in a tile: 128 bytes
 constexpr int kTileBytes = 16 * kChunk / 2;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTokenStride = 36;         // floats from one token's sums to the next's: no bank conflicts
-// Warps of an SM: registers allow 16 with up to 8 tokens to a block, 8 with more.
-constexpr int w4_warps(int nt) { return nt == 1 ? 16 : 8; }
+// Warps of an SM: registers allow 16 with up to 16 tokens to a block, 8 with more.
+constexpr int w4_warps(int nt) { return nt <= 2 ? 16 : 8; }
 
 // D += A B on fp16 operands.
 __device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -58,8 +58,9 @@ struct Tile {
   static constexpr int kScaleWords = kGroups / 2 + 1, kZeroWords = (kGroups + 3 + 3) / 4;
   static constexpr int kScale = kTileBytes, kZero = kScale + 16 * kScaleWords * 4;
   static constexpr int kBytes = kZero + 16 * kZeroWords * 4;
-  static constexpr int kStages = GROUP == 32 ? 4 : 5;
 };
+// Tiles of a warp's ring: what shared memory holds with w4_warps warps to an SM.
+constexpr int w4_stages(int nt, int group) { return nt == 2 ? 3 : nt == 1 && group == 32 ? 4 : 5; }
 // A zero point as a number.
 __device__ __forceinline__ float number_of(uint8_t z) { return __uint_as_float(0x4b000000u | z) - 8388608.0f; }
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   using R = Tile<GROUP>;
   constexpr int kTokens = 8 * NT;
-  constexpr int kGroups = R::kGroups, kStages = R::kStages;
+  constexpr int kGroups = R::kGroups, kStages = w4_stages(NT, GROUP);
   constexpr int kSteps = GROUP / 32;  // 32-deep steps to a group
   // A lane takes kSteps neighbouring words of a row's group, lane q those from
   // q kSteps on.  The 16-byte pieces of a row stand at piece ^ f(row), so that
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
 template <int NT, int GROUP>
 cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
   const auto bytes = [](int warps) {
-    return (size_t)warps * (Tile<GROUP>::kStages * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 + 8 * NT * (kChunk / GROUP) * 4);
+    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 + 8 * NT * (kChunk / GROUP) * 4);
   };
   static bool set[64] = {};
   int dev = 0;
@@ -486,7 +487,7 @@ cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t s
 
 }  // namespace
 
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, bool joined) {
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined) {
   W4Plan best = {};
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
   const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;
@@ -498,8 +499,11 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, bool joined) {
     const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / (parts * lists)));
     const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * lists + sms - 1) / sms;
     // in times of an SM's share of memory bandwidth for 4 KB (a warp's two tiles),
-    // about 0.1 us; an exchange costs about 2 of them, the sum over the parts 15
-    const double cost = (double)rounds * (double)(warps * together + 2) + (parts > 1 && !joined ? 15.0 : 0.0);
+    // about 0.1 us; an exchange costs about 2 of them, the sum over the parts 15 and
+    // their bytes, written and read
+    const double bytes = 8.0 * (double)P * N * (gated ? 2 : 1) * (double)(parts > 1 || joined ? parts : 0);
+    const double cost = (double)rounds * (double)(warps * together + 2) + (parts > 1 && !joined ? 15.0 : 0.0) +
+                        bytes / (4096.0 * (double)sms);
     if (best.warps == 0 || cost < least) {
       least = cost;
       best.warps = (int)warps;
