@@ -25,6 +25,8 @@
 // through a ring of asynchronous copies that every warp has for itself.  Two tiles
 // of rows (gated: one of the gate, one of the up projection) end in an exchange of
 // the warps' sums.  K beyond one block's range is summed by a second kernel.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -85,6 +87,13 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Two fp16 values divided by 16.
+__device__ __forceinline__ uint32_t sixteenth(uint32_t v) {
+  const uint32_t by = 0x2c002c00u;
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&by));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The tokens of list y: expert, first row in the experts' order and count.
@@ -213,29 +222,36 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       ptx::cp_async_commit();
       into = into == kStages - 1 ? 0 : into + 1;
     };
+    uint4 v[8];  // the values of one n-tile's tokens
+    const auto load_tokens = [&](int tb, int j) {
+      const int n = tb + 8 * j + g, p = tk.first + n;
+      const bool some = n < tk.count;
+      const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
+      const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.K + k0 + 8 * kSteps * q;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int k = s / kSteps * GROUP + s % kSteps * 8;
+        v[s] = make_uint4(0, 0, 0, 0);
+        if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
+      }
+    };
+    load_tokens(tb, 0);
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) request_next(s & 1);
 
     // Column g of n-tile j is token 8 j + g; lane (g, q) has the values that its
     // words' codes meet, those of the codes at bit 4 of a half divided by 16.
     uint32_t b[NT][8][4];
-    float unscale[NT][2];  // of tokens 8 j + 2 q, + 1
+    float unscale[NT][2];                        // of tokens 8 j + 2 q, + 1
+    float held_sums[kGroups][2];   // their groups' sums, with one n-tile
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int n = tb + 8 * j + g, p = tk.first + n;
-      const bool some = n < tk.count;
-      const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
-      const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.K + k0 + 8 * kSteps * q;
-      uint4 v[8];
+      if (j > 0) load_tokens(tb, j);
       uint32_t top = 0u;  // largest |x| as bits, both halves
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int k = s / kSteps * GROUP + s % kSteps * 8;
-        v[s] = make_uint4(0, 0, 0, 0);
-        if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
+      for (int s = 0; s < 8; ++s)
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu),
                                      __vmaxu2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu)));
-      }
       top = max(top >> 16, top & 0xffffu);
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -246,34 +262,44 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 - up) << 23);
       unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
       unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
-      float sum = 0.0f;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const float x0 = bf16lo(v[s].x) * by, x1 = bf16hi(v[s].x) * by, x2 = bf16lo(v[s].y) * by;
-        const float x3 = bf16hi(v[s].y) * by, x4 = bf16lo(v[s].z) * by, x5 = bf16hi(v[s].z) * by;
-        const float x6 = bf16lo(v[s].w) * by, x7 = bf16hi(v[s].w) * by;
-        b[j][s][0] = f16x2(x0, x4);
-        b[j][s][1] = f16x2(x1 * 0.0625f, x5 * 0.0625f);
-        b[j][s][2] = f16x2(x2, x6);
-        b[j][s][3] = f16x2(x3 * 0.0625f, x7 * 0.0625f);
-        sum += ((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7));
-        if (s % kSteps == kSteps - 1) {
-          // the group's sum in units of the products, as it enters them: times -8
-          // with no zero points
-          sum += __shfl_xor_sync(kFull, sum, 1);
-          sum += __shfl_xor_sync(kFull, sum, 2);
-          if (q == 0) sums[s / kSteps * kTokens + 8 * j + g] = sum * (a.zero ? -0x1p-24f : -0x1p-21f);
-          sum = 0.0f;
+        b[j][s][0] = f16x2(bf16lo(v[s].x) * by, bf16lo(v[s].z) * by);
+        b[j][s][1] = sixteenth(f16x2(bf16hi(v[s].x) * by, bf16hi(v[s].z) * by));
+        b[j][s][2] = f16x2(bf16lo(v[s].y) * by, bf16lo(v[s].w) * by);
+        b[j][s][3] = sixteenth(f16x2(bf16hi(v[s].y) * by, bf16hi(v[s].w) * by));
+      }
+      // the groups' sums as they enter the products (times -8 with no zero points):
+      // products with codes of one
+#pragma unroll
+      for (int s = 0; s < kGroups; ++s) {
+        float acc[4] = {};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          const uint32_t *x = b[j][s * kSteps + st];
+          mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[0], x[1]);
+          mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[2], x[3]);
         }
+        acc[0] *= a.zero ? -1.0f : -8.0f;
+        acc[1] *= a.zero ? -1.0f : -8.0f;
+        // (the products' first eight rows are alike)
+        if (NT == 1)
+          held_sums[s][0] = acc[0], held_sums[s][1] = acc[1];
+        else if (g == 0)
+          *reinterpret_cast<float2 *>(sums + s * kTokens + 8 * j + 2 * q) = make_float2(acc[0], acc[1]);
       }
     }
     __syncwarp();
 
-    int stage = 0;
+    // The warps' sums meet for as many items at once as fit the buffer (all of them,
+    // mostly, with one token: a barrier for each item took 3.4 us of 19.4).  Two
+    // buffers in turn: a warp writes one again only behind the barrier that follows
+    // its last readers.
+    const int count = min(kTokens, tk.count - tb);
+    const int slots = count <= 1 ? 1 : 1 << (32 - __clz(count - 1)), batch = kTokens / slots;
+    int stage = 0, at = 0;
+    float *buffer = part;
     for (int it = 0; it < mine; ++it) {
-      // two buffers in turn: a warp writes one again only behind the barrier that
-      // follows its last readers
-      float *buffer = part + (it & 1) * kw * kTokens * kTokenStride;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         cp_async_wait_group<kStages - 2>();
@@ -292,7 +318,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
           float acc[NT][4];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const float2 x = *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
+            const float2 x = NT == 1 ? make_float2(held_sums[s][0], held_sums[s][1])
+                                     : *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
             acc[j][0] = acc[j][2] = x.x;
             acc[j][1] = acc[j][3] = x.y;
           }
@@ -320,21 +347,26 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
             tot[j][3] = fmaf(sh, acc[j][3], tot[j][3]);
           }
         }
-        float *to = buffer + wk * kTokens * kTokenStride + 16 * i + g;
+        float *to = buffer + (wk * kTokens + at * slots + 2 * q) * kTokenStride + 16 * i + g;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            to[(8 * j + 2 * q + (v & 1)) * kTokenStride + (v >> 1) * 8] = tot[j][v] * unscale[j][v & 1];
+          for (int v = 0; v < 2; ++v)
+            if (8 * j + 2 * q + v < slots) {
+              to[(8 * j + v) * kTokenStride] = tot[j][v] * unscale[j][v];
+              to[(8 * j + v) * kTokenStride + 8] = tot[j][2 + v] * unscale[j][v];
+            }
       }
+      if (++at < batch && it + 1 < mine) continue;
       __syncthreads();
-      const int count = min(kTokens, tk.count - tb), item = blockIdx.x * per + it * step;
-      const int out = item + (a.gated ? lane & 15 : lane);
-      // a lane per row; the warps take the tokens in turn, the next ones each time
-      int t = wk + it % kw;
-      for (t = t >= kw ? t - kw : t; t < count; t += kw) {
+      // a lane per row; the warps take the items' tokens in turn, the next ones each time
+      int id = wk + it % kw;
+      for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
+        const int t = id & (slots - 1), back = at - 1 - id / slots;  // items before the last one
+        if (t >= count) continue;
+        const int item = blockIdx.x * per + (it - back) * step, out = item + (a.gated ? lane & 15 : lane);
         float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + t) * kTokenStride + lane];
+        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + id) * kTokenStride + lane];
         v *= 0x1p24f;
         const int64_t p = tk.first + tb + t;
         if (gridDim.y > 1) {  // one part of K
@@ -351,6 +383,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
             static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(v);
         }
       }
+      at = 0;
+      buffer = part + (buffer == part) * kw * kTokens * kTokenStride;
     }
     cp_async_wait_group<0>();
     __syncthreads();
