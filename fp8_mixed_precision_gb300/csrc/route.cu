@@ -12,11 +12,15 @@
 //
 // The choice is that of the exact scores.  Where c is monotone in the logits
 // (no bias, and at most one score to a group) the logits are compared
-// themselves.  Elsewhere c is formed in fp32; a row in which two scores that
-// decide something are closer than fp32's error is chosen anew in fp64.
+// themselves.  Elsewhere c is formed in fp32; where two scores that decide
+// something are closer than fp32's error, fp64 decides: between the experts in
+// question, or, where groups are, for the whole row.
 //
 // LANES threads hold one token's logits in registers, four consecutive ones
-// each, CHUNKS times.
+// each, CHUNKS times.  Bound by instructions (a row of 128 logits is 256 bytes, its
+// eight rounds of finding the largest some 150 instructions of a warp): bf16
+// logits that choose by themselves are packed with their index into one word, sorted
+// within each lane, and each round is one warp-wide maximum.
 #include <math.h>
 
 #include <algorithm>
@@ -49,9 +53,25 @@ __device__ __forceinline__ float sum_over(float v) {
 }
 template <int LANES>
 __device__ __forceinline__ float max_over(float v) {
+  if constexpr (LANES == 32) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
 #pragma unroll
-  for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+    for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t max_over(uint32_t v) {
+  if constexpr (LANES == 32) {
+    return __reduce_max_sync(kFull, v);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
 }
 // Largest key of the token's lanes and the lowest index that has it.
 template <int LANES>
@@ -177,6 +197,43 @@ __device__ __noinline__ int choose64(unsigned mask, const RouteArgs &a, int64_t 
   return mine;
 }
 
+// Order-preserving map of fp64 onto unsigned (-0 and +0 alike).
+__device__ __forceinline__ unsigned long long key_of(double v) {
+  const unsigned long long b = __double_as_longlong(v + 0.0);
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+// As choose64, between n <= LANES experts alone: lane i's candidate `e`.  The others
+// are known to be below the k best of these.
+template <int LANES>
+__device__ __noinline__ int choose64_of(unsigned mask, const RouteArgs &a, int64_t t, int e, int n, int *list) {
+  const int lane = threadIdx.x & (LANES - 1);
+  double z = 1.0, m = 0.0;
+  if (!a.sigmoid) {
+    m = -INFINITY;
+    for (int i = lane; i < a.E; i += LANES) m = fmax(m, (double)load_logit(a.logits, a.f32, t * a.E + i));
+    for (int o = LANES / 2; o; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
+    z = 0.0;
+    for (int i = lane; i < a.E; i += LANES) z += exp((double)load_logit(a.logits, a.f32, t * a.E + i) - m);
+    for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(mask, z, o);
+  }
+  unsigned long long key = 0ull;
+  if (lane < n) {
+    const double l = load_logit(a.logits, a.f32, t * a.E + e);
+    key = key_of((a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / z) + (double)a.bias[e]);
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long k2 = __shfl_sync(mask, key, i, LANES);
+    const int e2 = __shfl_sync(mask, e, i, LANES);
+    rank += k2 > key || (k2 == key && e2 < e);
+  }
+  __syncwarp(mask);
+  if (lane < n && rank < a.k) list[rank] = e;
+  __syncwarp(mask);
+  return lane < min(n, a.k) ? list[lane] : -1;
+}
+
 // sigmoid(l), its smallest values included
 __device__ __forceinline__ float sigmoid(float l) {
   const float t = expf(-fabsf(l));
@@ -185,174 +242,283 @@ __device__ __forceinline__ float sigmoid(float l) {
 // log(sigmoid(l))
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
 
-// GENERAL: scores are formed (a bias, or two to a group); else logits alone choose.
-template <int LANES, int CHUNKS, bool GENERAL>
+enum RouteMode {
+  kPacked,   // bf16 logits choose by themselves
+  kLogits,   // logits choose by themselves
+  kGeneral,  // scores are formed: a bias, or two to a group
+};
+
+// Sorts N packed keys, largest first (a network of exchanges of neighbours in the
+// bitonic order; N = 4 or 8).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
+  const auto exchange = [&](int i, int j) {
+    const uint32_t hi = max(k[i], k[j]), lo = min(k[i], k[j]);
+    k[i] = hi;
+    k[j] = lo;
+  };
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    exchange(i, i + 1), exchange(i + 2, i + 3);
+    exchange(i, i + 2), exchange(i + 1, i + 3);
+    exchange(i + 1, i + 2);
+  }
+  if (N == 8) {  // two sorted fours
+#pragma unroll
+    for (int i = 0; i < 4; ++i) exchange(i, 7 - i);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      exchange(i, i + 2), exchange(i + 1, i + 3);
+      exchange(i, i + 1), exchange(i + 2, i + 3);
+    }
+  }
+}
+
+template <int LANES, int CHUNKS, RouteMode MODE>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a, float *__restrict__ weights,
                                                               int *__restrict__ experts) {
+  constexpr bool GENERAL = MODE == kGeneral;
   constexpr int kTokens = kRouteThreads / LANES;
   // a row of c: fp32 for the groups' scores, fp64 for the choice made anew
-  __shared__ double rows[kTokens][GENERAL ? 4 * LANES * CHUNKS : 2 * LANES * CHUNKS];
+  __shared__ double rows[MODE == kPacked ? 1 : kTokens][GENERAL ? 4 * LANES * CHUNKS : 2 * LANES * CHUNKS];
   pdl_wait_then_release();
-  const int lane = threadIdx.x & (LANES - 1), slot = threadIdx.x / LANES;
-  const int64_t row = (int64_t)blockIdx.x * kTokens + slot;
+  const int lane = threadIdx.x & (LANES - 1), slot = MODE == kPacked ? 0 : threadIdx.x / LANES;
+  const int64_t row = (int64_t)blockIdx.x * kTokens + threadIdx.x / LANES;
   const int64_t t = row < a.T ? row : a.T - 1;  // spare lanes repeat the last token and write nothing
   const unsigned mask = LANES == 32 ? kFull : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
 
   float l[CHUNKS][4];
   bool bad = false;
-  float m = -INFINITY;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     load4(a.logits, a.f32, a.vec, t, 4 * LANES * c + 4 * lane, a.E, l[c]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      m = fmaxf(m, l[c][q]);
-      bad |= isnan(l[c][q]) || (!a.sigmoid && l[c][q] == INFINITY);
-    }
+    for (int q = 0; q < 4; ++q) bad |= !(l[c][q] < INFINITY) && (!a.sigmoid || isnan(l[c][q]));
   }
-  m = max_over<LANES>(m);
-  float z = 1.0f;
-  if (!a.sigmoid && (GENERAL || !a.renorm)) {
+  int mine = -1;  // the expert in slot `lane`
+  float x = 0.0f;  // its logit
+  float m = -INFINITY, z = 1.0f;
+  const auto maximum = [&] {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = fmaxf(m, l[c][q]);
+    m = max_over<LANES>(m);
+  };
+  const auto total = [&] {
     z = 0.0f;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
       for (int q = 0; q < 4; ++q) z += l[c][q] > -INFINITY ? expf(l[c][q] - m) : 0.0f;
     z = sum_over<LANES>(z);
-  }
-  uint32_t key[CHUNKS][4];
-  float *line = reinterpret_cast<float *>(rows[slot]);
-  float tol = 0.0f;
-  {
-    float smax = 0.0f, cmax = 0.0f;
-    const float rz = GENERAL ? __fdiv_rn(1.0f, z) : 1.0f;
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int e = 4 * LANES * c + 4 * lane + q;
-        const float x = l[c][q];
-        float v = x, g = x;  // what chooses experts, and groups
-        if (GENERAL) {
-          const float s = a.sigmoid ? sigmoid(x) : expf(x - m) * rz;
-          const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
-          const float score = s + b;
-          if (x > -INFINITY) {
-            bad |= isnan(score);
-            smax = fmaxf(smax, s);
-            if (fabsf(score) < INFINITY) cmax = fmaxf(cmax, fabsf(score));
-          }
-          if (a.bias) v = score;
-          g = a.top == 2 ? score : v;
-        }
-        const bool some = x > -INFINITY && v > -INFINITY;
-        key[c][q] = some ? key_of(v) : 0u;
-        if (a.groups > 1) line[e] = some ? g : -INFINITY;
-      }
-    // twice the fp32 error of a score: the sum's and the exponential's part of
-    // s (under 32 units of roundoff), and the addition's
-    if (GENERAL) tol = 0x1p-18f * max_over<LANES>(smax) + 0x1p-22f * max_over<LANES>(cmax);
-  }
-  bool again = false;
-  if (a.groups > 1) {
-    __syncwarp();
-    // a group's scores are shared out over `share` lanes
-    const int share = LANES / a.groups_pow2, g = lane / share;
-    float two0 = -INFINITY, two1 = -INFINITY;
-    if (g < a.groups)
-      for (int i = lane % share; i < a.per; i += share) {
-        const float v = line[g * a.per + i];
-        if (v > two0) {
-          two1 = two0;
-          two0 = v;
-        } else {
-          two1 = fmaxf(two1, v);
-        }
-      }
-    for (int o = share / 2; o; o >>= 1) {
-      const float b0 = __shfl_xor_sync(kFull, two0, o), b1 = __shfl_xor_sync(kFull, two1, o);
-      two1 = fmaxf(fminf(two0, b0), fmaxf(two1, b1));
-      two0 = fmaxf(two0, b0);
-    }
-    const float score = a.top == 2 && two1 > -INFINITY ? two0 + two1 : two0;
-    uint32_t gkey = g < a.groups && lane % share == 0 && two0 > -INFINITY ? key_of(score) : 0u;
-    unsigned kept = 0;
-    float last = 0.0f;
-    for (int n = 0; n < a.kept; ++n) {
-      uint32_t k1 = gkey;
-      int at = g;
-      best_over<LANES>(k1, at);
-      if (k1 == 0) continue;
-      kept |= 1u << at;
-      last = of_key(k1);
-      if (at == g) gkey = 0u;
-    }
-    if (GENERAL) again = kept && gkey && !(of_key(gkey) <= last - 2.0f * tol);
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int e = 4 * LANES * c + 4 * lane + q;
-        if (!(kept >> ((unsigned)e * a.per_magic >> 20 & 31u) & 1u)) key[c][q] = 0u;
-      }
-  }
-  int mine = -1;        // the expert in slot `lane`
-  uint32_t mine_key = 0u, last_key = 0u;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0u;
-    int at = 0x7fffffff;
+  };
+
+  if constexpr (MODE == kPacked) {
+    uint32_t key[4 * CHUNKS];  // the ordered bf16, and below it the index from the end
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (key[c][q] > best) best = key[c][q], at = 4 * LANES * c + 4 * lane + q;
-    best_over<LANES>(best, at);
-    if (best) {
-      if (lane == j) mine = at, mine_key = best;
-      last_key = best;
+        key[4 * c + q] = l[c][q] > -INFINITY
+                             ? (key_of(l[c][q]) & 0xffff0000u) | (uint32_t)(0xffff - (4 * LANES * c + 4 * lane + q))
+                             : 0u;
+    sort_down(key);
+    uint32_t got = 0u;
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t best = max_over<LANES>(key[0]);
+      if (lane == j) got = best;
+      if (key[0] == best) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * CHUNKS; ++i) key[i] = key[i + 1];
+        key[4 * CHUNKS - 1] = 0u;
+      }
+    }
+    if (got) {
+      mine = 0xffff - (int)(got & 0xffffu);
+      x = of_key(got & 0x80000000u ? got & 0xffff0000u : got | 0xffffu);
+    }
+    if (!a.sigmoid && !a.renorm) {
+      m = __shfl_sync(kFull, got ? x : -INFINITY, 0, LANES);
+      total();
+    }
+  } else {
+    if (!a.sigmoid && (GENERAL || !a.renorm)) {
+      maximum();
+      total();
+    }
+    uint32_t key[CHUNKS][4];
+    float *line = reinterpret_cast<float *>(rows[slot]);
+    float tol = 0.0f;
+    {
+      float smax = 0.0f, cmax = 0.0f;
+      const float rz = GENERAL ? __fdiv_rn(1.0f, z) : 1.0f;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 4 * LANES * c + 4 * lane + q;
+          const float y = l[c][q];
+          float v = y, g = y;  // what chooses experts, and groups
+          if (GENERAL) {
+            const float s = a.sigmoid ? sigmoid(y) : expf(y - m) * rz;
+            const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
+            const float score = s + b;
+            if (y > -INFINITY) {
+              bad |= isnan(score);
+              smax = fmaxf(smax, s);
+              if (fabsf(score) < INFINITY) cmax = fmaxf(cmax, fabsf(score));
+            }
+            if (a.bias) v = score;
+            g = a.top == 2 ? score : v;
+          }
+          const bool some = y > -INFINITY && v > -INFINITY;
+          key[c][q] = some ? key_of(v) : 0u;
+          if (a.groups > 1) line[e] = some ? g : -INFINITY;
+        }
+      // twice the fp32 error of a score, in units of roundoff: of s, 6 (sigmoid:
+      // exponential, sum, quotient) or 8 and half the terms of a lane's and the lanes'
+      // sum; of the addition, 1
+      if (GENERAL)
+        tol = (a.sigmoid ? 12.0f : 16.0f + 4 * CHUNKS + 6) * 0x1p-24f * max_over<LANES>(smax) +
+              0x1p-23f * max_over<LANES>(cmax);
+    }
+    bool again = false;  // groups in question
+    if (a.groups > 1) {
+      __syncwarp();
+      // a group's scores are shared out over `share` lanes
+      const int share = LANES / a.groups_pow2, g = lane / share;
+      float two0 = -INFINITY, two1 = -INFINITY;
+      if (g < a.groups)
+        for (int i = lane % share; i < a.per; i += share) {
+          const float v = line[g * a.per + i];
+          two1 = fmaxf(two1, fminf(two0, v));
+          two0 = fmaxf(two0, v);
+        }
+      for (int o = share / 2; o; o >>= 1) {
+        const float b0 = __shfl_xor_sync(kFull, two0, o), b1 = __shfl_xor_sync(kFull, two1, o);
+        two1 = fmaxf(fminf(two0, b0), fmaxf(two1, b1));
+        two0 = fmaxf(two0, b0);
+      }
+      const float score = a.top == 2 && two1 > -INFINITY ? two0 + two1 : two0;
+      uint32_t gkey = g < a.groups && lane % share == 0 && two0 > -INFINITY ? key_of(score) : 0u;
+      unsigned kept = 0;
+      float last = 0.0f;
+      for (int n = 0; n < a.kept; ++n) {
+        uint32_t k1 = gkey;
+        int at = g;
+        best_over<LANES>(k1, at);
+        if (k1 == 0) continue;
+        kept |= 1u << at;
+        last = of_key(k1);
+        if (at == g) gkey = 0u;
+      }
+      // (a sum of two rounds once more)
+      if (GENERAL) again = kept && gkey && !(of_key(gkey) <= last - 2.0f * tol - 0x1p-22f * fabsf(last));
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 4 * LANES * c + 4 * lane + q;
+          if (!(kept >> ((unsigned)e * a.per_magic >> 20 & 31u) & 1u)) key[c][q] = 0u;
+        }
+    }
+    uint32_t mine_key = 0u, last_key = 0u;
+    // each lane's best; the lane that had the best of all looks for its next one
+    uint32_t own = 0u;
+    int own_at = 0x7fffffff;
+    const auto own_best = [&] {
+      own = 0u;
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (at == 4 * LANES * c + 4 * lane + q) key[c][q] = 0u;
-    }
-  }
-  float x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
-  if (GENERAL && a.bias) {
-    // neighbours in the order closer than the error, equal logits and biases apart
-    const float b = mine >= 0 ? a.bias[mine] : 0.0f;
-    const float x2 = __shfl_down_sync(kFull, x, 1, LANES), b2 = __shfl_down_sync(kFull, b, 1, LANES);
-    const uint32_t k2 = __shfl_down_sync(kFull, mine_key, 1, LANES);
-    if (lane + 1 < a.k && k2 && !(of_key(k2) <= of_key(mine_key) - tol)) again |= x != x2 || b != b2;
-    // those left that come as close to the last one chosen
-    const float xl = __shfl_sync(kFull, x, a.k - 1, LANES), bl = __shfl_sync(kFull, b, a.k - 1, LANES);
-    const float edge = of_key(last_key) - tol;
+          if (key[c][q] > own) own = key[c][q], own_at = 4 * LANES * c + 4 * lane + q;
+    };
+    own_best();
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t best = own;
+      int at = own_at;
+      best_over<LANES>(best, at);
+      if (best) {
+        if (lane == j) mine = at, mine_key = best;
+        last_key = best;
+        if (own == best && own_at == at) {
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
+          for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (key[c][q] && !(of_key(key[c][q]) <= edge)) {
-          const int e = 4 * LANES * c + 4 * lane + q;
-          again |= load_logit(a.logits, a.f32, t * a.E + e) != xl || a.bias[e] != bl;
+            for (int q = 0; q < 4; ++q)
+              if (at == 4 * LANES * c + 4 * lane + q) key[c][q] = 0u;
+          own_best();
         }
-  }
-  bad = __any_sync(kFull, bad) && (__ballot_sync(kFull, bad) & mask);
-  if (GENERAL) {
-    again = (__ballot_sync(kFull, again) & mask) && !bad;
-    if (again) {
-      mine = choose64<LANES>(mask, a, t, rows[slot]);
-      x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+      }
     }
-    __syncwarp();
+    x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+    bool close = false;  // experts in question
+    float edge = 0.0f;
+    if (GENERAL && a.bias) {
+      // neighbours in the order closer than the error, equal logits and biases apart
+      const float b = mine >= 0 ? a.bias[mine] : 0.0f;
+      const float x2 = __shfl_down_sync(kFull, x, 1, LANES), b2 = __shfl_down_sync(kFull, b, 1, LANES);
+      const uint32_t k2 = __shfl_down_sync(kFull, mine_key, 1, LANES);
+      if (lane + 1 < a.k && k2 && !(of_key(k2) <= of_key(mine_key) - tol)) close = x != x2 || b != b2;
+      // those left that come as close to the last one chosen
+      const float xl = __shfl_sync(kFull, x, a.k - 1, LANES), bl = __shfl_sync(kFull, b, a.k - 1, LANES);
+      edge = of_key(last_key) - tol;
+      // (an exact tie is no question: equal logits and biases, told by the index)
+      const auto other_near = [&] {
+        bool other = false;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int e = 4 * LANES * c + 4 * lane + q;
+            if (key[c][q] && !(of_key(key[c][q]) <= edge))
+              other |= load_logit(a.logits, a.f32, t * a.E + e) != xl || a.bias[e] != bl;
+          }
+        return other;
+      };
+      if (own && !(of_key(own) <= edge)) close |= other_near();
+    }
+    bad = __any_sync(kFull, bad) && (__ballot_sync(kFull, bad) & mask);
+    if (GENERAL) {
+      again = (__ballot_sync(kFull, again) & mask) && !bad;
+      close = (__ballot_sync(kFull, close) & mask) && !bad && !again;
+      if (close) {
+        int *list = reinterpret_cast<int *>(rows[slot]);
+        __syncwarp(mask);
+        int n = __popc(__ballot_sync(mask, mine >= 0) & mask);
+        if (mine >= 0) list[lane] = mine;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bool near = key[c][q] && !(of_key(key[c][q]) <= edge);
+            const unsigned who = __ballot_sync(mask, near) & mask;
+            const int at = n + __popc(who & ((1u << (threadIdx.x & 31)) - 1u));
+            if (near && at < LANES) list[at] = 4 * LANES * c + 4 * lane + q;
+            n += __popc(who);
+          }
+        __syncwarp(mask);
+        if (n <= LANES)
+          mine = choose64_of<LANES>(mask, a, t, lane < n ? list[lane] : 0, n, list);
+        else
+          again = true;
+      }
+      if (again) mine = choose64<LANES>(mask, a, t, rows[slot]);
+      if (again || close) x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+      __syncwarp();
+    }
   }
+  if (!GENERAL) bad = __any_sync(kFull, bad) && (__ballot_sync(kFull, bad) & mask);
   const bool some = mine >= 0;
   float w = 0.0f;
   if (a.renorm) {
     const float g = some ? (a.sigmoid ? log_sigmoid(x) : x) : -INFINITY;
     const float top = max_over<LANES>(g);
     const float u = some ? expf(g - top) : 0.0f;
-    const float total = sum_over<LANES>(u);
-    if (some) w = __fdiv_rn(u, total) * a.scale;
+    const float all = sum_over<LANES>(u);
+    if (some) w = __fdiv_rn(u, all) * a.scale;
   } else if (some) {
     w = (a.sigmoid ? sigmoid(x) : __fdiv_rn(expf(x - m), z)) * a.scale;
   }
@@ -419,14 +585,35 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[c][q] = 0.0f;
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int ej = __shfl_sync(kFull, some ? e : -1, j, LANES);
-    const float dj = __shfl_sync(kFull, d, j, LANES);
+  // The chosen experts' part meets the row in shared memory (k rounds of comparing
+  // every lane's indices took 45.7 us for 131072 x 128 with k = 8).  An expert
+  // named twice in a row, which the forward pass does not do, takes those rounds.
+  __shared__ float4 rows[kTokens][LANES * CHUNKS];
+  float4 *line = rows[threadIdx.x / LANES];
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
+  for (int c = 0; c < CHUNKS; ++c) line[LANES * c + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __syncwarp();
+  if (some) reinterpret_cast<int *>(line)[e] = lane;
+  __syncwarp();
+  const bool twice = some && reinterpret_cast<int *>(line)[e] != lane;  // another lane wrote there too
+  if (__any_sync(kFull, twice)) {
+    for (int j = 0; j < a.k; ++j) {
+      const int ej = __shfl_sync(kFull, some ? e : -1, j, LANES);
+      const float dj = __shfl_sync(kFull, d, j, LANES);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (ej == 4 * LANES * c + 4 * lane + q) v[c][q] += dj;
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (ej == 4 * LANES * c + 4 * lane + q) v[c][q] += dj;
+    }
+  } else {
+    if (some) reinterpret_cast<float *>(line)[e] = d;
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const float4 w4 = line[LANES * c + lane];
+      v[c][0] += w4.x, v[c][1] += w4.y, v[c][2] += w4.z, v[c][3] += w4.w;
+    }
   }
   if (row >= a.T) return;
 #pragma unroll
@@ -477,9 +664,13 @@ cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStre
   return with_shape(a, [&](auto lanes, auto chunks) {
     constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
     const dim3 grid((unsigned)((a.T + kRouteThreads / L - 1) / (kRouteThreads / L)));
-    if (a.bias || (a.groups > 1 && a.top == 2))
-      return launch_kernel(route_kernel<L, C, true>, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
-    return launch_kernel(route_kernel<L, C, false>, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
+    const auto go = [&](auto kernel) {
+      return launch_kernel(kernel, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
+    };
+    if (a.bias || (a.groups > 1 && a.top == 2)) return go(route_kernel<L, C, kGeneral>);
+    if constexpr (C <= 2)  // more keys than a lane can keep in order
+      if (!a.f32 && a.groups == 1) return go(route_kernel<L, C, kPacked>);
+    return go(route_kernel<L, C, kLogits>);
   });
 }
 

@@ -169,6 +169,18 @@ __device__ __forceinline__ void add8(uint4 v, float w, float (&a)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&a)[8]) {
   return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
 }
+// Piece i of rows of `vecs` pieces: (row, piece).  A 64-bit division takes some 100
+// instructions.
+__device__ __forceinline__ int64_t row_of(int64_t i, int vecs, int &c) {
+  if (i >> 32) {
+    const int64_t t = i / vecs;
+    c = (int)(i - t * vecs);
+    return t;
+  }
+  const uint32_t t = (uint32_t)i / (uint32_t)vecs;
+  c = (int)((uint32_t)i - t * (uint32_t)vecs);
+  return t;
+}
 // The rows behind an expert's last, up to the next one's first: zeros, so that
 // products over whole aligned groups of rows take nothing from them.
 __device__ __forceinline__ void zero_gap(void *rows, int vecs, int e, const int *counts, const int *offsets) {
@@ -189,8 +201,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_gather_kernel(const void *__
   const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
   if (i >= total) return;
   const uint4 v = load16(x, i);
-  const int64_t t = i / vecs;
-  const int c = (int)(i - t * vecs);
+  int c;
+  const int64_t t = row_of(i, vecs, c);
   for (int j = 0; j < k; ++j) {
     const int p = position[t * k + j];
     if (p >= 0) static_cast<uint4 *>(xs)[(int64_t)p * vecs + c] = v;
@@ -198,34 +210,50 @@ __global__ void __launch_bounds__(kRowThreads) rows_gather_kernel(const void *__
 }
 
 // weights null: the sum of the rows.  A slot without an expert counts as its
-// weight times zero, so that a weight that is NaN shows.
+// weight times zero, so that a weight that is NaN shows.  ITEMS 16-byte pieces to a
+// thread, kRowThreads apart, so that their places and then their rows are on the way
+// at once (131072 x 2 x 512: one piece 100 us, the copy rate's 59).
+template <int ITEMS>
 __global__ void __launch_bounds__(kRowThreads) rows_combine_kernel(const void *__restrict__ z,
                                                                    const int *__restrict__ position,
                                                                    const float *__restrict__ weights, int64_t total,
                                                                    int vecs, int k, void *__restrict__ y) {
+  constexpr int kAtOnce = 4 / ITEMS;  // slots
   pdl_wait_then_release();
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= total) return;
-  const int64_t t = i / vecs;
-  const int c = (int)(i - t * vecs);
-  float a[8] = {};
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    uint4 v[4];
-    float w[4];
+  const int64_t i0 = (int64_t)blockIdx.x * (ITEMS * kRowThreads) + threadIdx.x;
+  int64_t slot[ITEMS];
+  int c[ITEMS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = make_uint4(0, 0, 0, 0);
-      w[j] = 0.0f;
-      if (j0 + j < k) {
-        const int p = position[t * k + j0 + j];
-        w[j] = weights ? weights[t * k + j0 + j] : 1.0f;
-        if (p >= 0) v[j] = load16(z, (int64_t)p * vecs + c);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) add8(v[j], w[j], a);
+  for (int n = 0; n < ITEMS; ++n) {
+    const int64_t i = min(i0 + n * kRowThreads, total - 1);
+    slot[n] = row_of(i, vecs, c[n]) * k;
   }
-  static_cast<uint4 *>(y)[i] = pack8(a);
+  float a[ITEMS][8] = {};
+  for (int j0 = 0; j0 < k; j0 += kAtOnce) {
+    int p[ITEMS][kAtOnce];
+    float w[ITEMS][kAtOnce];
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n)
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const bool in = j0 + j < k;
+        p[n][j] = in ? position[slot[n] + j0 + j] : -1;
+        w[n][j] = !in ? 0.0f : weights ? weights[slot[n] + j0 + j] : 1.0f;
+      }
+    uint4 v[ITEMS][kAtOnce];
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n)
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        v[n][j] = p[n][j] >= 0 ? load16(z, (int64_t)p[n][j] * vecs + c[n]) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n)
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) add8(v[n][j], w[n][j], a[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < ITEMS; ++n)
+    if (i0 + n * kRowThreads < total) static_cast<uint4 *>(y)[i0 + n * kRowThreads] = pack8(a[n]);
 }
 
 // dz[row] = w dy[t] and dweights[slot] = <dy[t], z[row]>: TPT threads per token,
@@ -333,8 +361,12 @@ cudaError_t launch_rows_combine(const void *z, const int *position, const float 
                                 void *y, cudaStream_t st) {
   const int vecs = (int)(C / 8);
   LaunchScope ls("rows_combine", st, 2.0 * T * C * (1 + k), 2.0 * T * C * k, T, C, k);
-  return launch_kernel(rows_combine_kernel, dim3((unsigned)((T * vecs + kRowThreads - 1) / kRowThreads)),
-                       dim3(kRowThreads), 0, st, z, position, weights, T * vecs, vecs, k, y);
+  const auto go = [&](auto kernel, int items) {
+    return launch_kernel(kernel, dim3((unsigned)((T * vecs + items * kRowThreads - 1) / (items * kRowThreads))),
+                         dim3(kRowThreads), 0, st, z, position, weights, T * vecs, vecs, k, y);
+  };
+  // few rows: one piece a thread, on as many SMs as there are
+  return T * vecs >= (int64_t)num_sms() * 8 * kRowThreads ? go(rows_combine_kernel<2>, 2) : go(rows_combine_kernel<1>, 1);
 }
 
 cudaError_t launch_rows_combine_bwd(const void *dy, const void *z, const int *position, const float *weights, int64_t T,
