@@ -1197,7 +1197,8 @@ def fp8_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, weights: torch.T
     if out is None:
         with _on(stream):
             out = torch.empty_like(logits)
-    _need(out, "out", (T, E), logits.dtype, dev)
+    else:
+        _need(out, "out", (T, E), logits.dtype, dev)
     _check(lib().fp8_route_bwd(dweights.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype], weights.data_ptr(),
                                experts.data_ptr(), T, E, k, SCORE[score], renormalize, scale, out.data_ptr(),
                                _stream(stream)), "fp8_route_bwd")
@@ -1205,27 +1206,49 @@ def fp8_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, weights: torch.T
 
 
 # ---------------------------------------------------------------- rows in the experts' order
-@dataclass
 class ExpertOrder:
     """The T k slots (t k + j: choice j of token t) sorted by expert.  counts [E]
     and offsets [E + 1]: rows of each expert, where they begin (multiples of
     align), and the rows in use; position [T, k]: a slot's row, -1 without an
     expert; order [rows]: a row's slot, -1 in the gap behind an expert's rows,
-    undefined past offsets[E].  rows: the rows that any choice can need."""
-    counts: torch.Tensor
-    offsets: torch.Tensor
-    position: torch.Tensor
-    order: torch.Tensor
-    T: int
-    k: int
-    E: int
-    align: int
-    rows: int
+    undefined past offsets[E].  rows: the rows that any choice can need.  The
+    tensors are views of one int32 buffer, made when asked for."""
+
+    __slots__ = ("T", "k", "E", "align", "rows", "buffer", "device", "_at", "_views")
+
+    def __init__(self, T: int, k: int, E: int, align: int, device):
+        self.T, self.k, self.E, self.align = T, k, E, align
+        self.rows = expert_rows(T, k, E, align)
+        self.buffer = torch.empty(2 * E + 1 + T * k + self.rows, dtype=torch.int32, device=device)
+        self.device = self.buffer.get_device()
+        at = self.buffer.data_ptr()
+        # addresses of counts, offsets, position and order
+        self._at = (at, at + 4 * E, at + 4 * (2 * E + 1), at + 4 * (2 * E + 1 + T * k))
+        self._views = None
+
+    def _view(self, i):
+        if self._views is None:
+            c, o, p, r = self.buffer.split((self.E, self.E + 1, self.T * self.k, self.rows))
+            self._views = (c, o, p.view(self.T, self.k), r)
+        return self._views[i]
+
+    counts = property(lambda self: self._view(0))
+    offsets = property(lambda self: self._view(1))
+    position = property(lambda self: self._view(2))
+    order = property(lambda self: self._view(3))
 
 
+@functools.lru_cache(maxsize=1024)
 def expert_rows(T: int, k: int, n_experts: int, align: int = 1) -> int:
     """Rows of a buffer in the experts' order that any choice fits."""
     return int(lib().fp8_expert_rows(T * k, n_experts, align))
+
+
+@functools.lru_cache(maxsize=1024)
+def _order_bytes(slots, E):
+    b = _c_sz()
+    _check(lib().fp8_expert_order_workspace_size(slots, E, ctypes.byref(b)), "fp8_expert_order_workspace_size")
+    return b.value
 
 
 def fp8_expert_order(experts: torch.Tensor, n_experts: int, align: int = 1, out: ExpertOrder | None = None,
@@ -1238,35 +1261,22 @@ def fp8_expert_order(experts: torch.Tensor, n_experts: int, align: int = 1, out:
     dev = _here(experts, "experts", stream)
     T, k = experts.shape
     E, slots = n_experts, T * k
-    b = _c_sz()
-    _check(lib().fp8_expert_order_workspace_size(slots, E, ctypes.byref(b)), "fp8_expert_order_workspace_size")
-    need = b.value
+    need = _order_bytes(slots, E)
     if out is None:
-        rows = expert_rows(T, k, E, align)
         with _on(stream):
-            # one allocation (a call for few tokens is bound by the host)
-            m = torch.empty(2 * E + 1 + slots + rows, dtype=torch.int32, device=experts.device)
-        counts, offsets, position, order = m.split((E, E + 1, slots, rows))
-        out = ExpertOrder(counts, offsets, position.view(T, k), order, T, k, E, align, rows)
-    elif (out.T, out.k, out.E, out.align) != (T, k, E, align):
-        raise ValueError("out is an order of another shape")
-    else:
-        for t, name, shape in ((out.counts, "counts", (E,)), (out.offsets, "offsets", (E + 1,)),
-                               (out.position, "position", (T, k)), (out.order, "order", (out.rows,))):
-            _need(t, name, shape, torch.int32, dev)
-        if out.rows != expert_rows(T, k, E, align):
-            raise ValueError("out is an order of another shape")
+            out = ExpertOrder(T, k, E, align, experts.device)
+    elif (out.T, out.k, out.E, out.align, out.device) != (T, k, E, align, dev):
+        raise ValueError("out is an order of another shape or device")
     if ws is None and need:
         with _on(stream):
             ws = _empty_bytes(need, experts.device)
-    _check(lib().fp8_expert_order(experts.data_ptr(), slots, E, align, out.counts.data_ptr(), out.offsets.data_ptr(),
-                                  out.position.data_ptr(), out.order.data_ptr(), _ptr(ws),
+    _check(lib().fp8_expert_order(experts.data_ptr(), slots, E, align, *out._at, _ptr(ws),
                                   0 if ws is None else _bytes(ws, "ws", dev), _stream(stream)), "fp8_expert_order")
     return out
 
 
 def _order_on(order: ExpertOrder, dev: int):
-    if order.position.get_device() != dev:
+    if order.device != dev:
         raise ValueError(f"order must be on cuda:{dev}")
 
 
@@ -1283,10 +1293,11 @@ def fp8_expert_gather(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | N
     if out is None:
         with _on(stream):
             out = torch.empty((order.rows, C), dtype=torch.bfloat16, device=x.device)
-    _need(out, "out", (order.rows, C), torch.bfloat16, dev)
-    _check(lib().fp8_expert_gather(x.data_ptr(), T, C, order.k, order.E, order.align, order.counts.data_ptr(),
-                                   order.offsets.data_ptr(), order.position.data_ptr(), out.data_ptr(),
-                                   _stream(stream)), "fp8_expert_gather")
+    else:
+        _need(out, "out", (order.rows, C), torch.bfloat16, dev)
+    counts, offsets, position, _ = order._at
+    _check(lib().fp8_expert_gather(x.data_ptr(), T, C, order.k, order.E, order.align, counts, offsets, position,
+                                   out.data_ptr(), _stream(stream)), "fp8_expert_gather")
     return out
 
 
@@ -1297,16 +1308,18 @@ def fp8_expert_combine(z: torch.Tensor, order: ExpertOrder, weights: torch.Tenso
     _need_bf16_cuda(z, "z")
     dev = _here(z, "z", stream)
     _order_on(order, dev)
-    T, k, C = order.T, order.k, z.shape[1]
-    if z.shape[0] != order.rows:
+    T, k = order.T, order.k
+    rows, C = z.shape
+    if rows != order.rows:
         raise ValueError(f"z must have {order.rows} rows")
     if weights is not None:
         _need(weights, "weights", (T, k), torch.float32, dev)
     if out is None:
         with _on(stream):
             out = torch.empty((T, C), dtype=torch.bfloat16, device=z.device)
-    _need(out, "out", (T, C), torch.bfloat16, dev)
-    _check(lib().fp8_expert_combine(z.data_ptr(), T, C, k, order.position.data_ptr(), _ptr(weights), out.data_ptr(),
+    else:
+        _need(out, "out", (T, C), torch.bfloat16, dev)
+    _check(lib().fp8_expert_combine(z.data_ptr(), T, C, k, order._at[2], _ptr(weights), out.data_ptr(),
                                     _stream(stream)), "fp8_expert_combine")
     return out
 
@@ -1322,17 +1335,18 @@ def fp8_expert_combine_bwd(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder
     _need(dy, "dy", (T, C), torch.bfloat16, dev)
     _need(z, "z", (order.rows, C), torch.bfloat16, dev)
     _need(weights, "weights", (T, k), torch.float32, dev)
-    with _on(stream):
-        if dz is None:
-            dz = torch.empty_like(z)
-        if dweights is None:
-            dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    if dz is None or dweights is None:
+        with _on(stream):
+            if dz is None:
+                dz = torch.empty_like(z)
+            if dweights is None:
+                dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     _need(dz, "dz", (order.rows, C), torch.bfloat16, dev)
     _need(dweights, "dweights", (T, k), torch.float32, dev)
-    _check(lib().fp8_expert_combine_bwd(dy.data_ptr(), z.data_ptr(), T, C, k, order.E, order.align,
-                                        order.counts.data_ptr(), order.offsets.data_ptr(), order.position.data_ptr(),
-                                        weights.data_ptr(), dz.data_ptr(), dweights.data_ptr(), _stream(stream)),
-           "fp8_expert_combine_bwd")
+    counts, offsets, position, _ = order._at
+    _check(lib().fp8_expert_combine_bwd(dy.data_ptr(), z.data_ptr(), T, C, k, order.E, order.align, counts, offsets,
+                                        position, weights.data_ptr(), dz.data_ptr(), dweights.data_ptr(),
+                                        _stream(stream)), "fp8_expert_combine_bwd")
     return dz, dweights
 
 

@@ -1122,7 +1122,7 @@ W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
-  return p.parts > 1 ? (size_t)p.parts * T * w.rows * 4 : 0;
+  return p.planes > 1 ? (size_t)p.planes * T * w.rows * 4 : 0;
 }
 // One weight for T tokens.
 fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated, int act, void *out, void *ws,
@@ -1176,9 +1176,9 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   w.position = c.take<int>(4 * slots);
   w.order = c.take<int>(4 * slots);
   w.hist = c.take<int>(chunks > 1 ? 4 * E * chunks : 0);
-  w.up_part = c.take<float>(w.up.parts > 1 ? 8 * slots * F * w.up.parts : 0);
+  w.up_part = c.take<float>(w.up.planes > 1 ? 8 * slots * F * w.up.planes : 0);
   w.h = c.take<void>(2 * slots * F);
-  w.z = c.take<float>(4 * slots * N * w.down.parts);
+  w.z = c.take<float>(4 * slots * N * w.down.planes);
   w.bytes = c.off;
   return w;
 }
@@ -1392,7 +1392,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
     st = from_cuda(launch_w4_product(*p, p == &a ? w.up : w.down, lists, cs(stream)));
     if (st != FP8_OK) return st;
   }
-  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, w.down.parts,
+  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, w.down.planes,
                                   y, cs(stream)));
 }
 

@@ -234,26 +234,28 @@ struct W4Args {
   const uint16_t *scale;  // bf16 [E, rows, ceil(K / group)]
   const uint8_t *zero;    // the same shape, or null: 8
   const void *x;
-  void *out;              // gated: bf16 [P, N]; else bf16, or (out_f32) fp32 [parts, P, N]
-  void *part;             // fp32 [parts, P, rows], with more than one part
+  void *out;              // gated: bf16 [P, N]; else bf16, or (out_f32) fp32 [planes, P, N]
+  void *part;             // fp32 [planes, P, rows], with more than one
   const int *experts, *order, *offsets, *counts;
   int T, P, E, k, by_row, tokens;  // P: output rows (T, or the slots)
   int N, rows, K, group;           // N outputs; rows = 2 N when gated
   int gated, act, out_f32;
-  int groups;  // filled in by the launch
+  int groups, cluster;  // filled in by the launch
 };
 // How a product is cut: n-tiles of 8 tokens, parts of K, warps (256 of K each)
-// and blocks to a part.  tokens: as many as a list may be expected to have;
-// lists: weights that are read at once; P: output rows; joined: the caller sums the parts.
+// and blocks to a part; planes: partial sums that are left for a second kernel (1:
+// none, the parts are added within the launch).  tokens: as many as a list may be
+// expected to have; lists: weights that are read at once; P: output rows;
+// joined: the caller adds the planes.
 struct W4Plan {
-  int nt, parts, warps, blocks;
+  int nt, parts, warps, blocks, planes;
 };
 W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined);
 // lists: the grid's lists, one per expert (or per row, by_row); one weight: blocks
-// of 8 nt tokens.  Sums the parts unless out_f32.
+// of 8 nt tokens.  Sums the planes unless out_f32.
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st);
 cudaError_t launch_w4_join(const float *z, const int *experts, const int *position, const float *weights, int64_t T,
-                           int64_t N, int k, int E, int parts, void *y, cudaStream_t st);
+                           int64_t N, int k, int E, int planes, void *y, cudaStream_t st);
 cudaError_t launch_w4_quantize(const void *w, int64_t rows, int64_t K, int group, uint8_t *codes, void *scale,
                                uint8_t *zero, cudaStream_t st);
 

@@ -24,7 +24,8 @@
 // at a time, its tokens' values in registers throughout and the codes on their way
 // through a ring of asynchronous copies that every warp has for itself.  Two tiles
 // of rows (gated: one of the gate, one of the up projection) end in an exchange of
-// the warps' sums.  K beyond one block's range is summed by a second kernel.
+// the warps' sums.  More ranges of K are the blocks of a cluster, which adds their
+// sums over distributed shared memory, or are summed by a second kernel (w4_plan).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -39,6 +40,7 @@ namespace {
 constexpr int kChunk = 256;              // codes of a row in a tile: 128 bytes
 constexpr int kTileBytes = 16 * kChunk / 2;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kW4Cluster = 8;             // parts of K that a cluster sums
 constexpr int kTokenStride = 36;         // floats from one token's sums to the next's: no bank conflicts
 // Warps of an SM: registers allow 16 with up to 16 tokens to a block, 8 with more.
 constexpr int w4_warps(int nt) { return nt <= 2 ? 16 : 8; }
@@ -143,6 +145,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   uint8_t *ring = smem + wk * kStages * R::kBytes;
   float *part = reinterpret_cast<float *>(smem + kw * kStages * R::kBytes);  // [2][kw][kTokens][kTokenStride]
   float *sums = part + 2 * kw * kTokens * kTokenStride + wk * kTokens * kGroups;  // [kGroups][kTokens]
+  float *joint = sums + (kw - wk) * kTokens * kGroups;  // [2][kTokens][32]: this block's sums for its cluster
+  const bool cluster = a.cluster != 0;                  // its blocks are the parts of K
   pdl_wait_then_release();
   const bool list = a.experts != nullptr;
   const Tokens tk = list ? tokens_of(a, blockIdx.z) : Tokens{0, 0, a.T};
@@ -359,17 +363,12 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       }
       if (++at < batch && it + 1 < mine) continue;
       __syncthreads();
-      // a lane per row; the warps take the items' tokens in turn, the next ones each time
-      int id = wk + it % kw;
-      for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
-        const int t = id & (slots - 1), back = at - 1 - id / slots;  // items before the last one
-        if (t >= count) continue;
-        const int item = blockIdx.x * per + (it - back) * step, out = item + (a.gated ? lane & 15 : lane);
-        float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + id) * kTokenStride + lane];
-        v *= 0x1p24f;
+      // a lane per row: `id` is one token of one item
+      const auto leave = [&](int id, float v) {
+        const int t = id & (slots - 1), item = it + 1 - at + id / slots;
+        const int out = blockIdx.x * per + item * step + (a.gated ? lane & 15 : lane);
         const int64_t p = tk.first + tb + t;
-        if (gridDim.y > 1) {  // one part of K
+        if (gridDim.y > 1 && !cluster) {  // one part of K
           if (a.gated || out < a.N)
             static_cast<float *>(a.part)[(blockIdx.y * (int64_t)a.P + p) * a.rows + (lane & 16 && a.gated ? a.N : 0) +
                                          out] = v;
@@ -382,12 +381,43 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
           else
             static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(v);
         }
+      };
+      // the warps take them in turn, the next ones each time
+      float *result = joint + (buffer == part ? 0 : kTokens * 32) + lane;
+      int id = wk + it % kw;
+      for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
+        if ((id & (slots - 1)) >= count) continue;
+        float v = 0.0f;
+        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + id) * kTokenStride + lane];
+        v *= 0x1p24f;
+        if (cluster)
+          result[id * 32] = v;
+        else
+          leave(id, v);
+      }
+      if (cluster) {
+        // the parts' sums, one block's share each; what is read here is written again
+        // behind the next barrier at the earliest
+        __syncwarp();
+        ptx::cluster_sync();
+        const int rank = blockIdx.y, parts = gridDim.y;
+        for (id = rank + parts * wk; id < at * slots; id += parts * kw) {
+          if ((id & (slots - 1)) >= count) continue;
+          const uint32_t at0 = ptx::smem_u32(result + id * 32);
+          float v = 0.0f;
+          for (int m = 0; m < parts; ++m) v += ptx::ld_shared_cluster_f(ptx::mapa_shared(at0, m));
+          leave(id, v);
+        }
+        __syncwarp();
       }
       at = 0;
       buffer = part + (buffer == part) * kw * kTokens * kTokenStride;
     }
     cp_async_wait_group<0>();
-    __syncthreads();
+    if (cluster)
+      ptx::cluster_sync();  // no block leaves, or writes again, what another still reads
+    else
+      __syncthreads();
   }
 }
 
@@ -498,7 +528,9 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
 template <int NT, int GROUP>
 cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
   const auto bytes = [](int warps) {
-    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 + 8 * NT * (kChunk / GROUP) * 4);
+    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 +
+                            8 * NT * (kChunk / GROUP) * 4) +
+           2 * 8 * NT * 32 * 4;
   };
   static bool set[64] = {};
   int dev = 0;
@@ -509,8 +541,25 @@ cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  return launch_kernel(w4_kernel<NT, GROUP>, dim3((unsigned)p.blocks, (unsigned)p.parts, (unsigned)lists),
-                       dim3(32 * p.warps), bytes(p.warps), st, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)p.parts, (unsigned)lists);
+  cfg.blockDim = dim3(32 * p.warps);
+  cfg.dynamicSmemBytes = bytes(p.warps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (a.cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = (unsigned)p.parts;
+    cfg.numAttrs = 1;
+  }
+  if (pdl_enabled()) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, w4_kernel<NT, GROUP>, a);
 }
 template <int NT>
 cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
@@ -526,18 +575,25 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool 
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
   const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;
   const int most = w4_warps(best.nt);
+  const int64_t fewest = (chunks + most - 1) / most;
+  // A cluster's exchange is worth its barriers where it saves a second kernel and the
+  // sums are few (4096 x 14336, 7 tokens: 11.2 us against 11.6 and 7 us less of the
+  // host; 2 x 57344 x 4096, 32 tokens: 209 us against 161).
+  const bool cluster = best.nt == 1 && !joined && fewest <= kW4Cluster;
+  const int64_t limit = cluster ? kW4Cluster : std::max<int64_t>(16, fewest);
   double least = 0.0;
-  for (int64_t parts = (chunks + most - 1) / most; parts <= std::max<int64_t>(16, (chunks + most - 1) / most); ++parts) {
-    if (parts > chunks) break;
-    const int64_t warps = (chunks + parts - 1) / parts, slots = sms * (most / warps);
-    const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / (parts * lists)));
+  for (int64_t parts = fewest; parts <= limit && parts <= chunks; ++parts) {
+    const int64_t warps = (chunks + parts - 1) / parts, resident = most / warps;
+    // a cluster's blocks stay within a processor cluster, of an eighth of the SMs
+    const int64_t slots = cluster ? 8 * (sms / 8 * resident / parts) : sms * resident / parts;
+    const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / lists));
     const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * lists + sms - 1) / sms;
     // in times of an SM's share of memory bandwidth for 4 KB (a warp's two tiles),
-    // about 0.1 us; an exchange costs about 2 of them, the sum over the parts 15 and
-    // their bytes, written and read
-    const double bytes = 8.0 * (double)P * N * (gated ? 2 : 1) * (double)(parts > 1 || joined ? parts : 0);
-    const double cost = (double)rounds * (double)(warps * together + 2) + (parts > 1 && !joined ? 15.0 : 0.0) +
-                        bytes / (4096.0 * (double)sms);
+    // about 0.1 us; an exchange costs about 2 of them, one through a cluster 6, the
+    // second kernel 15, and the sums' bytes, written and read
+    const double bytes = 8.0 * (double)P * N * (gated ? 2 : 1) * (double)parts;
+    const double cost = (double)rounds * (double)(warps * together + (parts > 1 && cluster ? 6 : 2)) +
+                        (cluster || (parts == 1 && !joined) ? 0.0 : (joined ? 0.0 : 15.0) + bytes / (4096.0 * (double)sms));
     if (best.warps == 0 || cost < least) {
       least = cost;
       best.warps = (int)warps;
@@ -545,11 +601,13 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool 
       best.blocks = (int)blocks;
     }
   }
+  best.planes = cluster ? 1 : best.parts;
   return best;
 }
 
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st) {
   a.groups = (a.K + a.group - 1) / a.group;
+  a.cluster = p.parts > 1 && p.planes == 1;
   {
     const double weights = (double)a.rows * a.K * (a.experts ? std::min(a.E, lists) : 1);
     LaunchScope ls(a.gated ? "w4_gated" : "w4_linear", st, weights * (0.5 + (a.zero ? 3.0 : 2.0) / a.group),
@@ -557,7 +615,7 @@ cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t
     const cudaError_t e = p.nt == 1   ? by_group<1>(a, p, lists, st)
                           : p.nt == 2 ? by_group<2>(a, p, lists, st)
                                       : by_group<4>(a, p, lists, st);
-    if (e != cudaSuccess || p.parts == 1 || a.out_f32) return e;
+    if (e != cudaSuccess || p.planes == 1 || a.out_f32) return e;
   }
   const int vecs = a.N / 4;
   const int64_t total = (int64_t)a.P * vecs;

@@ -56,7 +56,7 @@ def gated(x, v, act):
     return a * u, ea * (u.abs() + eb[:, F:]) + a.abs() * eb[:, F:] + (a * u).abs() * 4 * U
 
 
-SHAPES = [(16, 32), (32, 64), (48, 96), (64, 512), (272, 288), (512, 2048), (2048, 512), (80, 4128), (16, 14336)]
+SHAPES = [(16, 32), (32, 64), (48, 96), (64, 512), (272, 288), (512, 2048), (2048, 512), (80, 4128), (16, 14336), (4096, 4608), (32, 40960)]
 
 
 @pytest.mark.parametrize("N,K", SHAPES)
@@ -75,7 +75,7 @@ def test_linear(fp, N, K, group, zero):
         assert bool((out[T] == 7.0).all())
 
 
-@pytest.mark.parametrize("F,K", [(16, 32), (48, 512), (2048, 512), (144, 4096)])
+@pytest.mark.parametrize("F,K", [(16, 32), (48, 512), (2048, 512), (144, 4096), (512, 8224), (16, 36864)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_gated(fp, F, K, group, act):
@@ -111,7 +111,8 @@ def test_nonfinite_stays_in_its_row(fp):
 
 @pytest.mark.parametrize("T,E,k,K,F,N", [(1, 1, 1, 32, 32, 16), (1, 8, 2, 512, 256, 512), (1, 3, 4, 96, 64, 48),
                                          (5, 4, 2, 512, 96, 512), (37, 32, 4, 256, 128, 256), (3, 64, 2, 128, 64, 128),
-                                         (70, 2, 1, 544, 160, 64), (64, 5, 3, 512, 2048, 512), (700, 4, 3, 64, 32, 32)])
+                                         (70, 2, 1, 544, 160, 64), (64, 5, 3, 512, 2048, 512), (700, 4, 3, 64, 32, 32),
+                                         (1, 2, 2, 64, 36864, 32), (9, 2, 2, 36864, 32, 32), (40, 3, 2, 4096, 4096, 64)])
 @pytest.mark.parametrize("group,zero,act", [(32, True, "silu"), (64, False, "gelu"), (128, True, "silu")])
 @pytest.mark.parametrize("kind", ["random", "holes"])
 def test_experts(fp, T, E, k, K, F, N, group, zero, act, kind):
