@@ -1228,7 +1228,7 @@ class ExpertOrder:
 
     def _view(self, i):
         if self._views is None:
-            c, o, p, r = self.buffer.split((self.E, self.E + 1, self.T * self.k, self.rows))
+            c, o, p, r = torch.unsafe_split_with_sizes(self.buffer, (self.E, self.E + 1, self.T * self.k, self.rows))
             self._views = (c, o, p.view(self.T, self.k), r)
         return self._views[i]
 

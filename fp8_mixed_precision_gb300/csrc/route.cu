@@ -117,90 +117,106 @@ __device__ __forceinline__ void load4(const void *l, int f32, bool vec, int64_t 
     if (e + q < E) v[q] = load_logit(l, f32, i + q);
 }
 
-// Two largest values seen.
-struct Two {
-  double a, b;
-};
-__device__ __forceinline__ void push(Two &t, double v) {
-  if (v > t.a) {
-    t.b = t.a;
-    t.a = v;
-  } else if (v > t.b) {
-    t.b = v;
-  }
-}
-
-// The choice in fp64 for one row, by the LANES lanes of its token (`mask`);
-// c: E doubles of shared memory.  Lane j of the token returns expert j.
-template <int LANES>
-__device__ __noinline__ int choose64(unsigned mask, const RouteArgs &a, int64_t t, double *c) {
-  const int lane = threadIdx.x & (LANES - 1);
-  double m = -INFINITY;
-  for (int e = lane; e < a.E; e += LANES) m = fmax(m, (double)load_logit(a.logits, a.f32, t * a.E + e));
-  for (int o = LANES / 2; o; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
-  double z = 0.0;
-  if (!a.sigmoid) {
-    for (int e = lane; e < a.E; e += LANES) z += exp((double)load_logit(a.logits, a.f32, t * a.E + e) - m);
-    for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(mask, z, o);
-  }
-  for (int e = lane; e < a.E; e += LANES) {
-    const double l = load_logit(a.logits, a.f32, t * a.E + e);
-    double v = -INFINITY;
-    if (l > -INFINITY) {
-      v = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / z;
-      if (a.bias) v += (double)a.bias[e];
-    }
-    c[e] = v;
-  }
-  __syncwarp(mask);
-  const int per = a.E / a.groups;
-  if (a.groups > 1) {
-    // bit g: group g is kept
-    unsigned kept = 0;
-    for (int n = 0; n < a.kept; ++n) {
-      double best = -INFINITY;
-      int at = -1;
-      for (int g = lane; g < a.groups; g += LANES) {
-        if (kept >> g & 1u) continue;
-        Two two = {-INFINITY, -INFINITY};
-        for (int e = g * per; e < (g + 1) * per; ++e) push(two, c[e]);
-        const double s = a.top == 2 && two.b > -INFINITY ? two.a + two.b : two.a;
-        if (s > best) best = s, at = g;
-      }
-      for (int o = LANES / 2; o; o >>= 1) {
-        const double b2 = __shfl_xor_sync(mask, best, o);
-        const int a2 = __shfl_xor_sync(mask, at, o);
-        if (a2 >= 0 && (at < 0 || b2 > best || (b2 == best && a2 < at))) best = b2, at = a2;
-      }
-      if (at < 0) break;
-      kept |= 1u << at;
-    }
-    for (int e = lane; e < a.E; e += LANES)
-      if (!(kept >> (e / per) & 1u)) c[e] = -INFINITY;
-    __syncwarp(mask);
-  }
-  int mine = -1;
-  for (int j = 0; j < a.k; ++j) {
-    double best = -INFINITY;
-    int at = -1;
-    for (int e = lane; e < a.E; e += LANES)
-      if (c[e] > best) best = c[e], at = e;
-    for (int o = LANES / 2; o; o >>= 1) {
-      const double b2 = __shfl_xor_sync(mask, best, o);
-      const int a2 = __shfl_xor_sync(mask, at, o);
-      if (a2 >= 0 && (at < 0 || b2 > best || (b2 == best && a2 < at))) best = b2, at = a2;
-    }
-    if (j == lane) mine = at;
-    if (at >= 0 && at % LANES == lane) c[at] = -INFINITY;
-    __syncwarp(mask);
-  }
-  return mine;
-}
-
-// Order-preserving map of fp64 onto unsigned (-0 and +0 alike).
+// Order-preserving map of fp64 onto unsigned (-0 and +0 alike), and back.
 __device__ __forceinline__ unsigned long long key_of(double v) {
   const unsigned long long b = __double_as_longlong(v + 0.0);
   return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double of_key(unsigned long long k) {
+  return __longlong_as_double(k >> 63 ? k & ~(1ull << 63) : ~k);
+}
+
+// A row's maximum and sum of exponentials in fp64 (softmax; sigmoid: 0 and 1), by the
+// LANES lanes of its token (`mask`).
+template <int LANES>
+__device__ __forceinline__ void softmax64(unsigned mask, const RouteArgs &a, int64_t t, double &m, double &z) {
+  const int lane = threadIdx.x & (LANES - 1);
+  m = 0.0;
+  z = 1.0;
+  if (a.sigmoid) return;
+  float top = -INFINITY;
+  for (int e = lane; e < a.E; e += LANES) top = fmaxf(top, load_logit(a.logits, a.f32, t * a.E + e));
+  for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+  m = top;
+  z = 0.0;
+  for (int e = lane; e < a.E; e += LANES) z += exp((double)load_logit(a.logits, a.f32, t * a.E + e) - m);
+  for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(mask, z, o);
+}
+// The key of expert e's score, 0 where it is no candidate.
+__device__ __forceinline__ unsigned long long score64(const RouteArgs &a, int64_t t, int e, double m, double z) {
+  const double l = load_logit(a.logits, a.f32, t * a.E + e);
+  if (!(l > -INFINITY)) return 0ull;
+  const double c = (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / z) + (a.bias ? (double)a.bias[e] : 0.0);
+  return c > -INFINITY ? key_of(c) : 0ull;
+}
+
+// The kept groups of one row (bit g), decided in fp64; c: E keys of shared memory.
+template <int LANES>
+__device__ __noinline__ unsigned groups64(unsigned mask, const RouteArgs &a, int64_t t, unsigned long long *c) {
+  const int lane = threadIdx.x & (LANES - 1);
+  double m, z;
+  softmax64<LANES>(mask, a, t, m, z);
+  __syncwarp(mask);
+  for (int e = lane; e < a.E; e += LANES) c[e] = score64(a, t, e, m, z);
+  __syncwarp(mask);
+  const int share = LANES / a.groups_pow2, g = lane / share;
+  unsigned long long two0 = 0ull, two1 = 0ull;
+  if (g < a.groups)
+    for (int i = lane % share; i < a.per; i += share) {
+      const unsigned long long v = c[g * a.per + i];
+      two1 = max(two1, min(two0, v));
+      two0 = max(two0, v);
+    }
+  for (int o = share / 2; o; o >>= 1) {
+    const unsigned long long b0 = __shfl_xor_sync(mask, two0, o), b1 = __shfl_xor_sync(mask, two1, o);
+    two1 = max(min(two0, b0), max(two1, b1));
+    two0 = max(two0, b0);
+  }
+  unsigned long long score = 0ull;
+  if (g < a.groups && lane % share == 0 && two0)
+    score = a.top == 2 && two1 ? key_of(of_key(two0) + of_key(two1)) : two0;
+  unsigned kept = 0u;
+  for (int n = 0; n < a.kept; ++n) {
+    unsigned long long best = score;
+    int at = g;
+    for (int o = LANES / 2; o; o >>= 1) {
+      const unsigned long long b2 = __shfl_xor_sync(mask, best, o);
+      const int a2 = __shfl_xor_sync(mask, at, o);
+      if (b2 > best || (b2 == best && a2 < at)) best = b2, at = a2;
+    }
+    if (best == 0ull) break;
+    kept |= 1u << at;
+    if (at == g) score = 0ull;
+  }
+  return kept;
+}
+
+// The choice among the kept groups' experts in fp64; lane j of the token returns
+// expert j.  c: E keys of shared memory.
+template <int LANES>
+__device__ __noinline__ int choose64(unsigned mask, const RouteArgs &a, int64_t t, unsigned kept, unsigned long long *c) {
+  const int lane = threadIdx.x & (LANES - 1);
+  double m, z;
+  softmax64<LANES>(mask, a, t, m, z);
+  __syncwarp(mask);
+  for (int e = lane; e < a.E; e += LANES)
+    c[e] = a.groups == 1 || kept >> (e / a.per) & 1u ? score64(a, t, e, m, z) : 0ull;
+  int mine = -1;
+  for (int j = 0; j < a.k; ++j) {
+    unsigned long long best = 0ull;
+    int at = 0x7fffffff;
+    for (int e = lane; e < a.E; e += LANES)
+      if (c[e] > best) best = c[e], at = e;
+    for (int o = LANES / 2; o; o >>= 1) {
+      const unsigned long long b2 = __shfl_xor_sync(mask, best, o);
+      const int a2 = __shfl_xor_sync(mask, at, o);
+      if (b2 > best || (b2 == best && a2 < at)) best = b2, at = a2;
+    }
+    if (best == 0ull) break;
+    if (j == lane) mine = at;
+    if (at % LANES == lane) c[at] = 0ull;  // read by this lane alone
+  }
+  return mine;
 }
 
 // As choose64, between n <= LANES experts alone: lane i's candidate `e`.  The others
@@ -208,20 +224,9 @@ __device__ __forceinline__ unsigned long long key_of(double v) {
 template <int LANES>
 __device__ __noinline__ int choose64_of(unsigned mask, const RouteArgs &a, int64_t t, int e, int n, int *list) {
   const int lane = threadIdx.x & (LANES - 1);
-  double z = 1.0, m = 0.0;
-  if (!a.sigmoid) {
-    m = -INFINITY;
-    for (int i = lane; i < a.E; i += LANES) m = fmax(m, (double)load_logit(a.logits, a.f32, t * a.E + i));
-    for (int o = LANES / 2; o; o >>= 1) m = fmax(m, __shfl_xor_sync(mask, m, o));
-    z = 0.0;
-    for (int i = lane; i < a.E; i += LANES) z += exp((double)load_logit(a.logits, a.f32, t * a.E + i) - m);
-    for (int o = LANES / 2; o; o >>= 1) z += __shfl_xor_sync(mask, z, o);
-  }
-  unsigned long long key = 0ull;
-  if (lane < n) {
-    const double l = load_logit(a.logits, a.f32, t * a.E + e);
-    key = key_of((a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / z) + (double)a.bias[e]);
-  }
+  double m, z;
+  softmax64<LANES>(mask, a, t, m, z);
+  const unsigned long long key = lane < n ? score64(a, t, e, m, z) : 0ull;
   int rank = 0;
   for (int i = 0; i < n; ++i) {
     const unsigned long long k2 = __shfl_sync(mask, key, i, LANES);
@@ -243,13 +248,14 @@ __device__ __forceinline__ float sigmoid(float l) {
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
 
 enum RouteMode {
-  kPacked,   // bf16 logits choose by themselves
-  kLogits,   // logits choose by themselves
-  kGeneral,  // scores are formed: a bias, or two to a group
+  kPacked,  // bf16 logits choose by themselves
+  kLogits,  // logits choose by themselves
+  kSums,    // logits choose experts, sums of two scores groups
+  kBiased,  // scores with a bias choose
 };
 
-// Sorts N packed keys, largest first (a network of exchanges of neighbours in the
-// bitonic order; N = 4 or 8).
+// Sorts N keys, largest first: runs of `half` in order are merged, the second one
+// taken backwards.
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
   const auto exchange = [&](int i, int j) {
@@ -258,18 +264,17 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
     k[j] = lo;
   };
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    exchange(i, i + 1), exchange(i + 2, i + 3);
-    exchange(i, i + 2), exchange(i + 1, i + 3);
-    exchange(i + 1, i + 2);
-  }
-  if (N == 8) {  // two sorted fours
+  for (int half = 1; half < N; half *= 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) exchange(i, 7 - i);
+    for (int i = 0; i < N; i += 2 * half) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      exchange(i, i + 2), exchange(i + 1, i + 3);
-      exchange(i, i + 1), exchange(i + 2, i + 3);
+      for (int j = 0; j < half; ++j) exchange(i + j, i + 2 * half - 1 - j);
+    }
+#pragma unroll
+    for (int d = half / 2; d; d /= 2) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(i & d)) exchange(i, i + d);
     }
   }
 }
@@ -277,7 +282,8 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
 template <int LANES, int CHUNKS, RouteMode MODE>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a, float *__restrict__ weights,
                                                               int *__restrict__ experts) {
-  constexpr bool GENERAL = MODE == kGeneral;
+  constexpr bool GENERAL = MODE == kSums || MODE == kBiased;  // scores are formed
+  constexpr int kOwn = 4 * CHUNKS;                            // logits of a lane
   constexpr int kTokens = kRouteThreads / LANES;
   // a row of c: fp32 for the groups' scores, fp64 for the choice made anew
   __shared__ double rows[MODE == kPacked ? 1 : kTokens][GENERAL ? 4 * LANES * CHUNKS : 2 * LANES * CHUNKS];
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
     }
     uint32_t key[CHUNKS][4];
     float *line = reinterpret_cast<float *>(rows[slot]);
-    float tol = 0.0f;
+    float tol = 0.0f, top_score = 0.0f;
     {
       float smax = 0.0f, cmax = 0.0f;
       const float rz = GENERAL ? __fdiv_rn(1.0f, z) : 1.0f;
@@ -361,29 +367,32 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
           const float y = l[c][q];
           float v = y, g = y;  // what chooses experts, and groups
           if (GENERAL) {
-            const float s = a.sigmoid ? sigmoid(y) : expf(y - m) * rz;
-            const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
+            // (2 ulp off at most: the choice allows for it)
+            const float s = a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-y)) : expf(y - m) * rz;
+            const float b = MODE == kBiased && e < a.E ? a.bias[e] : 0.0f;
             const float score = s + b;
             if (y > -INFINITY) {
               bad |= isnan(score);
               smax = fmaxf(smax, s);
               if (fabsf(score) < INFINITY) cmax = fmaxf(cmax, fabsf(score));
             }
-            if (a.bias) v = score;
+            if (MODE == kBiased) v = score;
             g = a.top == 2 ? score : v;
           }
           const bool some = y > -INFINITY && v > -INFINITY;
           key[c][q] = some ? key_of(v) : 0u;
           if (a.groups > 1) line[e] = some ? g : -INFINITY;
         }
-      // twice the fp32 error of a score, in units of roundoff: of s, 6 (sigmoid:
+      // twice the fp32 error of a score, in units of roundoff: of s, 8 (sigmoid:
       // exponential, sum, quotient) or 8 and half the terms of a lane's and the lanes'
       // sum; of the addition, 1
-      if (GENERAL)
-        tol = (a.sigmoid ? 12.0f : 16.0f + 4 * CHUNKS + 6) * 0x1p-24f * max_over<LANES>(smax) +
-              0x1p-23f * max_over<LANES>(cmax);
+      if (GENERAL) {
+        tol = (a.sigmoid ? 16.0f : 16.0f + kOwn + 6) * 0x1p-24f * max_over<LANES>(smax) +
+              0x1p-23f * (cmax = max_over<LANES>(cmax));
+        top_score = cmax;
+      }
     }
-    bool again = false;  // groups in question
+    unsigned kept = 0u;  // groups
     if (a.groups > 1) {
       __syncwarp();
       // a group's scores are shared out over `share` lanes
@@ -402,7 +411,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
       }
       const float score = a.top == 2 && two1 > -INFINITY ? two0 + two1 : two0;
       uint32_t gkey = g < a.groups && lane % share == 0 && two0 > -INFINITY ? key_of(score) : 0u;
-      unsigned kept = 0;
       float last = 0.0f;
       for (int n = 0; n < a.kept; ++n) {
         uint32_t k1 = gkey;
@@ -413,8 +421,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
         last = of_key(k1);
         if (at == g) gkey = 0u;
       }
-      // (a sum of two rounds once more)
-      if (GENERAL) again = kept && gkey && !(of_key(gkey) <= last - 2.0f * tol - 0x1p-22f * fabsf(last));
+      if (GENERAL) {  // (a sum of two rounds once more)
+        const bool close = kept && gkey && !(of_key(gkey) <= last - 2.0f * tol - 0x1p-22f * fabsf(last));
+        if (__ballot_sync(kFull, close) & mask)
+          kept = groups64<LANES>(mask, a, t, reinterpret_cast<unsigned long long *>(rows[slot]));
+        __syncwarp();
+      }
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
@@ -423,90 +435,113 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
           if (!(kept >> ((unsigned)e * a.per_magic >> 20 & 31u) & 1u)) key[c][q] = 0u;
         }
     }
+    tol += kOwn * 0x1p-22f * top_score;  // what a lane's numbers take of the keys
     uint32_t mine_key = 0u, last_key = 0u;
-    // each lane's best; the lane that had the best of all looks for its next one
-    uint32_t own = 0u;
-    int own_at = 0x7fffffff;
-    const auto own_best = [&] {
-      own = 0u;
+    uint32_t kept_keys[kOwn];  // kBiased: a lane's keys in order, their lowest bits the number within the lane
+    if constexpr (MODE == kBiased) {
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c)
+      for (int i = 0; i < kOwn; ++i)
+        kept_keys[i] = key[i / 4][i % 4] ? (key[i / 4][i % 4] & ~(uint32_t)(kOwn - 1)) | (uint32_t)(kOwn - 1 - i) : 0u;
+      sort_down(kept_keys);
+      for (int j = 0; j < a.k; ++j) {
+        const int i = kOwn - 1 - (int)(kept_keys[0] & (kOwn - 1));
+        int at = 4 * LANES * (i / 4) + 4 * lane + i % 4;
+        // equal but for the numbers within the lanes: one of those below says so
+        uint32_t best = kept_keys[0] | (kOwn - 1);
+        const int own_at = at;
+        best_over<LANES>(best, at);
+        if (kept_keys[0] && own_at == at) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (key[c][q] > own) own = key[c][q], own_at = 4 * LANES * c + 4 * lane + q;
-    };
-    own_best();
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t best = own;
-      int at = own_at;
-      best_over<LANES>(best, at);
-      if (best) {
-        if (lane == j) mine = at, mine_key = best;
-        last_key = best;
-        if (own == best && own_at == at) {
+          for (int n = 0; n + 1 < kOwn; ++n) kept_keys[n] = kept_keys[n + 1];
+          kept_keys[kOwn - 1] = 0u;
+        }
+        if (best > (uint32_t)(kOwn - 1)) {
+          if (lane == j) mine = at, mine_key = best;
+          last_key = best;
+        }
+      }
+    } else {
+      // each lane's best; the lane that had the best of all looks for its next one
+      uint32_t own = 0u;
+      int own_at = 0x7fffffff;
+      const auto own_best = [&] {
+        own = 0u;
 #pragma unroll
-          for (int c = 0; c < CHUNKS; ++c)
+        for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (at == 4 * LANES * c + 4 * lane + q) key[c][q] = 0u;
-          own_best();
+          for (int q = 0; q < 4; ++q)
+            if (key[c][q] > own) own = key[c][q], own_at = 4 * LANES * c + 4 * lane + q;
+      };
+      own_best();
+      for (int j = 0; j < a.k; ++j) {
+        uint32_t best = own;
+        int at = own_at;
+        best_over<LANES>(best, at);
+        if (best) {
+          if (lane == j) mine = at;
+          if (own == best && own_at == at) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (at == 4 * LANES * c + 4 * lane + q) key[c][q] = 0u;
+            own_best();
+          }
         }
       }
     }
     x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
     bool close = false;  // experts in question
     float edge = 0.0f;
-    if (GENERAL && a.bias) {
-      // neighbours in the order closer than the error, equal logits and biases apart
+    const auto index_of = [&](uint32_t k) {  // of a key of this lane
+      const int i = kOwn - 1 - (int)(k & (kOwn - 1));
+      return 4 * LANES * (i / 4) + 4 * lane + i % 4;
+    };
+    const auto near = [&](uint32_t k) { return k && !(of_key(k | (kOwn - 1)) <= edge); };
+    if constexpr (MODE == kBiased) {
+      // neighbours in the order closer than the error, and those left that come as
+      // close to the last one chosen (an exact tie is no question: equal logits and
+      // biases, told by the index)
       const float b = mine >= 0 ? a.bias[mine] : 0.0f;
       const float x2 = __shfl_down_sync(kFull, x, 1, LANES), b2 = __shfl_down_sync(kFull, b, 1, LANES);
       const uint32_t k2 = __shfl_down_sync(kFull, mine_key, 1, LANES);
       if (lane + 1 < a.k && k2 && !(of_key(k2) <= of_key(mine_key) - tol)) close = x != x2 || b != b2;
-      // those left that come as close to the last one chosen
       const float xl = __shfl_sync(kFull, x, a.k - 1, LANES), bl = __shfl_sync(kFull, b, a.k - 1, LANES);
       edge = of_key(last_key) - tol;
-      // (an exact tie is no question: equal logits and biases, told by the index)
-      const auto other_near = [&] {
-        bool other = false;
+      if (near(kept_keys[0])) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int e = 4 * LANES * c + 4 * lane + q;
-            if (key[c][q] && !(of_key(key[c][q]) <= edge))
-              other |= load_logit(a.logits, a.f32, t * a.E + e) != xl || a.bias[e] != bl;
+        for (int i = 0; i < kOwn; ++i)
+          if (near(kept_keys[i])) {
+            const int e = index_of(kept_keys[i]);
+            close |= load_logit(a.logits, a.f32, t * a.E + e) != xl || a.bias[e] != bl;
           }
-        return other;
-      };
-      if (own && !(of_key(own) <= edge)) close |= other_near();
+      }
     }
     bad = __any_sync(kFull, bad) && (__ballot_sync(kFull, bad) & mask);
     if (GENERAL) {
-      again = (__ballot_sync(kFull, again) & mask) && !bad;
-      close = (__ballot_sync(kFull, close) & mask) && !bad && !again;
-      if (close) {
-        int *list = reinterpret_cast<int *>(rows[slot]);
-        __syncwarp(mask);
-        int n = __popc(__ballot_sync(mask, mine >= 0) & mask);
-        if (mine >= 0) list[lane] = mine;
+      close = (__ballot_sync(kFull, close) & mask) && !bad;
+      if constexpr (MODE == kBiased) {
+        if (close) {
+          int *list = reinterpret_cast<int *>(rows[slot]);
+          __syncwarp(mask);
+          int n = __popc(__ballot_sync(mask, mine >= 0) & mask);
+          if (mine >= 0) list[lane] = mine;
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bool near = key[c][q] && !(of_key(key[c][q]) <= edge);
-            const unsigned who = __ballot_sync(mask, near) & mask;
+          for (int i = 0; i < kOwn; ++i) {
+            const bool one = near(kept_keys[i]);
+            const unsigned who = __ballot_sync(mask, one) & mask;
             const int at = n + __popc(who & ((1u << (threadIdx.x & 31)) - 1u));
-            if (near && at < LANES) list[at] = 4 * LANES * c + 4 * lane + q;
+            if (one && at < LANES) list[at] = index_of(kept_keys[i]);
             n += __popc(who);
           }
-        __syncwarp(mask);
-        if (n <= LANES)
-          mine = choose64_of<LANES>(mask, a, t, lane < n ? list[lane] : 0, n, list);
-        else
-          again = true;
+          __syncwarp(mask);
+          if (n <= LANES)
+            mine = choose64_of<LANES>(mask, a, t, lane < n ? list[lane] : 0, n, list);
+          else
+            mine = choose64<LANES>(mask, a, t, kept, reinterpret_cast<unsigned long long *>(rows[slot]));
+          x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
+        }
       }
-      if (again) mine = choose64<LANES>(mask, a, t, rows[slot]);
-      if (again || close) x = mine >= 0 ? load_logit(a.logits, a.f32, t * a.E + mine) : 0.0f;
       __syncwarp();
     }
   }
@@ -667,7 +702,8 @@ cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStre
     const auto go = [&](auto kernel) {
       return launch_kernel(kernel, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
     };
-    if (a.bias || (a.groups > 1 && a.top == 2)) return go(route_kernel<L, C, kGeneral>);
+    if (a.bias) return go(route_kernel<L, C, kBiased>);
+    if (a.groups > 1 && a.top == 2) return go(route_kernel<L, C, kSums>);
     if constexpr (C <= 2)  // more keys than a lane can keep in order
       if (!a.f32 && a.groups == 1) return go(route_kernel<L, C, kPacked>);
     return go(route_kernel<L, C, kLogits>);
