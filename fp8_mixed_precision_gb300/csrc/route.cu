@@ -316,7 +316,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) z += l[c][q] > -INFINITY ? expf(l[c][q] - m) : 0.0f;
+      for (int q = 0; q < 4; ++q) {
+        // within 2 + 1.2 (m - l) ulp: of a term that is e^-(m - l) of the largest one
+        const float p = GENERAL ? expf(l[c][q] - m) : __expf(l[c][q] - m);
+        z += l[c][q] > -INFINITY ? p : 0.0f;
+      }
     z = sum_over<LANES>(z);
   };
 
@@ -331,6 +335,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
                              : 0u;
     sort_down(key);
     uint32_t got = 0u;
+#pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
       const uint32_t best = max_over<LANES>(key[0]);
       if (lane == j) got = best;
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        v[c][q] = v[c][q] > -INFINITY ? expf(v[c][q] - m) : 0.0f;
+        v[c][q] = v[c][q] > -INFINITY ? __expf(v[c][q] - m) : 0.0f;
         z += v[c][q];
       }
     z = sum_over<LANES>(z);
@@ -675,16 +680,28 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
   }
 }
 
-// Calls f with the LANES and CHUNKS that hold E experts, k choices and the groups.
-template <typename F>
+// Calls f with LANES and CHUNKS that hold E experts, k choices and the groups.  With
+// many tokens as few lanes to a token as `chunks` allows: what is done once per lane,
+// and the rounds across lanes, then serve several tokens (131072 x 128 with k = 8,
+// forward + backward: 32 lanes 78 us, 8 lanes 45).  With few, all 32: the shortest way
+// to one token's result.
+template <int MOST, typename F>
 cudaError_t with_shape(const RouteArgs &a, F f) {
-  const int lanes = std::max(std::max((a.E + 3) / 4, a.k), a.groups);
   using std::integral_constant;
-  if (lanes <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
-  if (lanes <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
-  if (lanes <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
-  if (lanes <= 64) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
-  if (lanes <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
+  const int lanes = std::max(a.k, a.groups);
+  const auto chunks = [&](int l) { return (a.E + 4 * l - 1) / (4 * l); };
+  if (a.T >= (int64_t)num_sms() * 32) {
+    if (lanes <= 8 && chunks(8) <= 1) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (lanes <= 8 && chunks(8) <= 2) return f(integral_constant<int, 8>(), integral_constant<int, 2>());
+    if constexpr (MOST >= 4)
+      if (lanes <= 8 && chunks(8) <= 4) return f(integral_constant<int, 8>(), integral_constant<int, 4>());
+    if (lanes <= 16 && chunks(16) <= 2) return f(integral_constant<int, 16>(), integral_constant<int, 2>());
+    if constexpr (MOST >= 4)
+      if (lanes <= 16 && chunks(16) <= 4) return f(integral_constant<int, 16>(), integral_constant<int, 4>());
+  }
+  if (chunks(32) <= 1) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+  if (chunks(32) <= 2) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
+  if (chunks(32) <= 4) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
   return f(integral_constant<int, 32>(), integral_constant<int, 8>());
 }
 
@@ -696,17 +713,20 @@ cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStre
   for (a.groups_pow2 = 1; a.groups_pow2 < a.groups;) a.groups_pow2 *= 2;
   LaunchScope ls("route_fwd", st, (double)a.T * (a.E * (a.f32 ? 4.0 : 2.0) + 8.0 * a.k), 4.0 * a.T * a.E, a.T, a.E,
                  a.k);
-  return with_shape(a, [&](auto lanes, auto chunks) {
-    constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
-    const dim3 grid((unsigned)((a.T + kRouteThreads / L - 1) / (kRouteThreads / L)));
-    const auto go = [&](auto kernel) {
-      return launch_kernel(kernel, grid, dim3(kRouteThreads), 0, st, a, weights, experts);
-    };
-    if (a.bias) return go(route_kernel<L, C, kBiased>);
-    if (a.groups > 1 && a.top == 2) return go(route_kernel<L, C, kSums>);
-    if constexpr (C <= 2)  // more keys than a lane can keep in order
-      if (!a.f32 && a.groups == 1) return go(route_kernel<L, C, kPacked>);
-    return go(route_kernel<L, C, kLogits>);
+  const auto go = [&](auto kernel, int l) {
+    return launch_kernel(kernel, dim3((unsigned)((a.T + kRouteThreads / l - 1) / (kRouteThreads / l))),
+                         dim3(kRouteThreads), 0, st, a, weights, experts);
+  };
+  // (with a bias 16 logits to a lane take more of the keys than they save: 16379 x 256
+  // 40 us against 33)
+  if (a.bias)
+    return with_shape<2>(a, [&](auto l, auto c) { return go(route_kernel<l(), c(), kBiased>, l()); });
+  if (a.groups > 1 && a.top == 2)
+    return with_shape<4>(a, [&](auto l, auto c) { return go(route_kernel<l(), c(), kSums>, l()); });
+  return with_shape<4>(a, [&](auto l, auto c) {
+    if constexpr (c() <= 4)  // (more than 16 keys are more than a lane can keep in order)
+      if (!a.f32 && a.groups == 1) return go(route_kernel<l(), c(), kPacked>, l());
+    return go(route_kernel<l(), c(), kLogits>, l());
   });
 }
 
@@ -714,7 +734,7 @@ cudaError_t launch_route_bwd(RouteArgs a, const float *dweights, const float *we
                              void *dlogits, cudaStream_t st) {
   LaunchScope ls("route_bwd", st, (double)a.T * (a.E * (a.f32 ? 4.0 : 2.0) + 12.0 * a.k), 2.0 * a.T * a.E, a.T, a.E,
                  a.k);
-  return with_shape(a, [&](auto lanes, auto chunks) {
+  return with_shape<4>(a, [&](auto lanes, auto chunks) {
     constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
     const dim3 grid((unsigned)((a.T + kRouteThreads / L - 1) / (kRouteThreads / L)));
     return launch_kernel(route_bwd_kernel<L, C>, grid, dim3(kRouteThreads), 0, st, a, dweights, weights, experts,

@@ -288,3 +288,82 @@ def test_many_tokens(fp):
     assert float((w.double() - torch.softmax(v[:, :k].double(), 1)).abs().max()) < 64 * U
     w2, e2 = fp.fp8_route_fwd(l, k)
     assert torch.equal(w, w2) and torch.equal(e, e2)
+
+
+def reference(l, k, score, bias, groups, kept, top, renorm, scale):
+    """weights and experts of many tokens, in fp64 on the GPU (no ties but of equal logits and biases)."""
+    l = l.double()
+    masked = l == -INF
+    p = torch.sigmoid(l) if score == "sigmoid" else torch.nan_to_num(torch.softmax(l, 1))
+    c = torch.where(masked, -INF, p if bias is None else p + bias.double())
+    T, E = l.shape
+    if groups > 1:
+        g = c.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :top]
+        v = torch.where(g == -INF, 0.0, g).sum(2)
+        v = torch.where(g[:, :, 0] == -INF, -INF, v)
+        keep = v.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        out = torch.ones((T, groups), dtype=torch.bool, device=l.device).scatter_(1, keep, False)
+        c = torch.where(out.repeat_interleave(E // groups, 1), -INF, c)
+    v, e = c.sort(dim=1, descending=True, stable=True)
+    v, e = v[:, :k], e[:, :k]
+    e = torch.where(v == -INF, -1, e)
+    w = torch.where(e < 0, 0.0, p.gather(1, e.clamp(min=0)))
+    if renorm:
+        w = w / torch.where(w.sum(1, keepdim=True) > 0, w.sum(1, keepdim=True), 1.0)
+    return w * scale, e.int()
+
+
+MANY = [  # E, k, score, bias, groups, kept, top, renorm
+    (32, 8, "softmax", False, 1, 1, 1, False), (31, 3, "sigmoid", False, 1, 1, 1, True),
+    (64, 8, "softmax", True, 1, 1, 1, True), (60, 7, "softmax", False, 4, 2, 2, True),
+    (128, 8, "softmax", False, 1, 1, 1, False), (125, 6, "sigmoid", True, 5, 3, 2, True),
+    (128, 12, "softmax", False, 8, 3, 1, True), (200, 9, "softmax", False, 1, 1, 1, False),
+    (256, 16, "sigmoid", False, 8, 4, 2, False), (256, 6, "sigmoid", True, 8, 3, 2, True),
+    (256, 17, "softmax", False, 1, 1, 1, True), (512, 8, "softmax", True, 16, 4, 1, False),
+    (130, 24, "sigmoid", True, 1, 1, 1, True), (1000, 10, "softmax", False, 1, 1, 1, True)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k,score,bias,groups,kept,top,renorm", MANY)
+def test_many_tokens_every_way(fp, dtype, E, k, score, bias, groups, kept, top, renorm):
+    """Enough tokens for few lanes to each one, forward and backward, the last block part full."""
+    T = 6001
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    l = torch.randn((T, E), generator=g, device="cuda").to(dtype)
+    l[5] = -INF
+    l[T - 1, k // 2:] = -INF
+    b = 0.1 * torch.randn(E, generator=g, device="cuda") if bias else None
+    kw = dict(score=score, renormalize=renorm, scale=1.5)
+    w, e = fp.fp8_route_fwd(l, k, bias=b, groups=groups, groups_kept=kept, group_top=top, **kw)
+    ww, ee = reference(l, k, score, b, groups, kept, top, renorm, 1.5)
+    assert torch.equal(e, ee)
+    assert bool(((w.double() - ww).abs() <= ww * (E / 8 + 140) * U + 1e-37).all())
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    d = fp.fp8_route_bwd(dw, l, w, e, **kw)
+    # the same tokens few at a time take 32 lanes each: other orders of the same sums
+    few = torch.cat([fp.fp8_route_bwd(dw[i:i + 1000], l[i:i + 1000], w[i:i + 1000], e[i:i + 1000], **kw)
+                     for i in range(0, T, 1000)])
+    p = (torch.sigmoid(l.double()) if score == "sigmoid" else torch.nan_to_num(torch.softmax(l.double(), 1)))
+    gr = dw.double().abs() * w.double().abs()
+    size = torch.zeros_like(p).scatter_add_(1, ee.clamp(min=0).long(), gr + w.double() * gr.sum(1, keepdim=True))
+    size = size + p * gr.sum(1, keepdim=True)
+    out = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    assert bool(((d.double() - few.double()).abs() <= 2 * (size * (E / 4 + 120) * U + d.double().abs() * out) + 1e-37).all())
+    assert bool((d[5] == 0).all())
+
+
+def test_backward_of_one_expert_named_twice(fp):
+    """Rows that the forward pass does not make: both slots count."""
+    for T in (3, 6000):
+        l = torch.randn((T, 16), device="cuda")
+        e = torch.zeros((T, 4), dtype=torch.int32, device="cuda")
+        e[:, 2] = 5
+        e[:, 3] = -1
+        w = torch.rand((T, 4), device="cuda")
+        dw = torch.randn((T, 4), device="cuda")
+        d = fp.fp8_route_bwd(dw, l, w, e, score="sigmoid", renormalize=False)
+        a = (dw * w).double() * torch.sigmoid(-l.double().gather(1, e.clamp(min=0).long()))
+        want = torch.zeros((T, 16), dtype=torch.float64, device="cuda")
+        want[:, 0] = a[:, 0] + a[:, 1]
+        want[:, 5] = a[:, 2]
+        assert bool(((d.double() - want).abs() <= 16 * U * (a.abs().sum(1, keepdim=True))).all())
