@@ -25,7 +25,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE]
 
 CU_SOURCES = ["quantize.cu", "gemm.cu", "glue.cu", "noalloc.cu", "norm.cu",
-              "gated.cu", "clip.cu", "route.cu", "rows.cu", "w4.cu"]
+              "gated.cu", "clip.cu", "route.cu", "rows.cu", "w4.cu",
+              "w4_wide.cu"]
 CXX_SOURCES = ["api.cpp"]
 
 

@@ -1114,7 +1114,7 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
   return a;
 }
 // Blocks of tokens of one weight's product, which run side by side.
-int w4_token_blocks(int64_t T, const W4Plan &p) { return (int)cdiv(T, 8 * p.nt); }
+int w4_token_blocks(int64_t T, const W4Plan &p) { return p.wide ? 1 : (int)cdiv(T, 8 * p.nt); }
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   const int tokens = (int)std::min<int64_t>(T, 1024);
   W4Plan p = w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, 1, T, false);
@@ -1122,7 +1122,7 @@ W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
-  return p.planes > 1 ? (size_t)p.planes * T * w.rows * 4 : 0;
+  return p.planes > 1 || p.wide ? (size_t)p.planes * T * w.rows * 4 : 0;
 }
 // One weight for T tokens.
 fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated, int act, void *out, void *ws,
@@ -1157,6 +1157,7 @@ struct W4Workspace {
   W4Plan up, down;
   int *counts, *offsets, *position, *order, *hist;
   float *up_part;
+  void *xs;  // token rows in the experts' order, for the kernel that reads tiles of them
   void *h;
   float *z;
   size_t bytes;
@@ -1176,7 +1177,8 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   w.position = c.take<int>(4 * slots);
   w.order = c.take<int>(4 * slots);
   w.hist = c.take<int>(chunks > 1 ? 4 * E * chunks : 0);
-  w.up_part = c.take<float>(w.up.planes > 1 ? 8 * slots * F * w.up.planes : 0);
+  w.up_part = c.take<float>(w.up.planes > 1 || w.up.wide ? 8 * slots * F * w.up.planes : 0);
+  w.xs = c.take<void>(w.up.wide ? 2 * slots * K : 0);
   w.h = c.take<void>(2 * slots * F);
   w.z = c.take<float>(4 * slots * N * w.down.planes);
   w.bytes = c.off;
@@ -1378,6 +1380,12 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   a.part = w.up_part;
   b.out_f32 = 1;
   b.part = w.z;
+  if (w.up.wide) {
+    st = from_cuda(launch_rows_gather(x, T, K, k, (int)E, 1, w.counts, w.offsets, w.position, w.xs, cs(stream)));
+    if (st != FP8_OK) return st;
+    a.x = w.xs;
+    a.tokens = 0;
+  }
   const int lists = (int)(sorted ? std::min(E, slots) : slots);
   for (W4Args *p : {&a, &b}) {
     p->experts = experts;
@@ -1604,12 +1612,13 @@ fp8_status fp8_debug_wait_timeout(uint64_t limit_ns, fp8_stream_t stream) {
 }
 
 fp8_status fp8_get_device_status(fp8_stream_t stream) {
-  unsigned s = 0, q = 0, n = 0, g = 0;
+  unsigned s = 0, q = 0, n = 0, g = 0, w = 0;
   if (gemm_read_status(&s, cs(stream)) != cudaSuccess) return FP8_ERR_CUDA;
   if (quant_read_status(&q) != cudaSuccess) return FP8_ERR_CUDA;
   if (norm_read_status(&n) != cudaSuccess) return FP8_ERR_CUDA;
   if (gated_read_status(&g) != cudaSuccess) return FP8_ERR_CUDA;
-  return (fp8_status)(s ? s : q ? q : n ? n : g);
+  if (w4_wide_read_status(&w) != cudaSuccess) return FP8_ERR_CUDA;
+  return (fp8_status)(s ? s : q ? q : n ? n : g ? g : w);
 }
 
 }  // extern "C"

@@ -249,8 +249,13 @@ struct W4Args {
 // joined: the caller adds the planes.
 struct W4Plan {
   int nt, parts, warps, blocks, planes;
+  bool wide;  // w4_wide.cu; its planes are always added after
 };
 W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined);
+// The same for w4_wide.cu, and its launch: sums over the parts into a.part, x [P, K].
+W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P);
+cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st);
+cudaError_t w4_wide_read_status(unsigned *status);
 // lists: the grid's lists, one per expert (or per row, by_row); one weight: blocks
 // of 8 nt tokens.  Sums the planes unless out_f32.
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st);

@@ -33,6 +33,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "w4.cuh"
 
 namespace fp8lin {
 namespace {
@@ -96,25 +97,6 @@ __device__ __forceinline__ uint32_t sixteenth(uint32_t v) {
   const uint32_t by = 0x2c002c00u;
   const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&by));
   return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// The tokens of list y: expert, first row in the experts' order and count.
-struct Tokens {
-  int e, first, count;
-};
-__device__ __forceinline__ Tokens tokens_of(const W4Args &a, int y) {
-  const auto valid = [&](int e) { return e >= 0 && e < a.E; };
-  if (!a.order) {  // one token: its slots are the rows
-    const int e = a.experts[y];
-    return valid(e) ? Tokens{e, y, 1} : Tokens{0, 0, 0};
-  }
-  int e = y;
-  if (a.by_row) {  // fewer rows than experts: the first row of an expert stands for it
-    if (y >= a.offsets[a.E]) return {0, 0, 0};
-    e = a.experts[a.order[y]];
-    if (a.offsets[e] != y) return {0, 0, 0};
-  }
-  return {e, a.offsets[e], a.counts[e]};
 }
 
 __device__ __forceinline__ float gate_times(float gate, float up, int act) {
@@ -571,6 +553,7 @@ cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t s
 }  // namespace
 
 W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined) {
+  if (tokens > 16 && K >= 128) return w4_wide_plan(N, K, gated, tokens, lists, P);
   W4Plan best = {};
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
   const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;
@@ -607,15 +590,16 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool 
 
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st) {
   a.groups = (a.K + a.group - 1) / a.group;
-  a.cluster = p.parts > 1 && p.planes == 1;
+  a.cluster = !p.wide && p.parts > 1 && p.planes == 1;
   {
     const double weights = (double)a.rows * a.K * (a.experts ? std::min(a.E, lists) : 1);
     LaunchScope ls(a.gated ? "w4_gated" : "w4_linear", st, weights * (0.5 + (a.zero ? 3.0 : 2.0) / a.group),
                    2.0 * a.rows * a.K * a.P, a.P, a.N, a.K);
-    const cudaError_t e = p.nt == 1   ? by_group<1>(a, p, lists, st)
+    const cudaError_t e = p.wide      ? launch_w4_wide(a, p, lists, st)
+                          : p.nt == 1 ? by_group<1>(a, p, lists, st)
                           : p.nt == 2 ? by_group<2>(a, p, lists, st)
                                       : by_group<4>(a, p, lists, st);
-    if (e != cudaSuccess || p.planes == 1 || a.out_f32) return e;
+    if (e != cudaSuccess || (p.planes == 1 && !p.wide) || a.out_f32) return e;
   }
   const int vecs = a.N / 4;
   const int64_t total = (int64_t)a.P * vecs;

@@ -1,0 +1,417 @@
+// Products with 4-bit weights for more than 16 tokens, on tcgen05: 128 weight rows
+// are the M side of the MMAs, 32 or 64 tokens the N side.
+//
+// The codes become bf16 integers code - zero (exact) on their way into shared memory,
+// in the swizzled layout that the MMAs read; the tokens arrive there by TMA as they
+// are.  Products are exact, sums within a group are the tensor core's in TMEM (two
+// accumulators in turn), and the epilogue adds each group's sum times its scale to
+// fp32 sums in registers, a lane per weight row.  Sums over a part of K go to memory
+// and are added by the kernel that follows.
+//
+// A code costs two instructions of the half-rate integer pipe (a byte taken out, and
+// one and-or behind a multiplication that moves its second code up 16 bits) and two
+// of the other: about as long as its half byte takes to arrive, so that with 64 tokens
+// the work is bound by those, not by the MMAs.  On mma.m16n8k16, which also moves every
+// product through the register file, 64 tokens through [28672, 4096] took 88 us.
+//
+// Warps: 0 requests the tokens' tiles, 1 issues the MMAs, 2-5 are the epilogue, 6-13
+// turn 16 rows each into operands.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "pipe.cuh"
+#include "ptx.cuh"
+#include "w4.cuh"
+
+namespace fp8lin {
+namespace {
+
+constexpr int kDepth = 128;              // codes of a row in a stage
+constexpr int kStages = 3;               // operand stages
+constexpr int kRing = 6;                 // tiles of codes that a warp has requested
+constexpr int kWorkers = 8, kThreads = 32 * (6 + kWorkers);
+constexpr int kOperandA = 128 * kDepth * 2;
+constexpr int kCodes = 16 * kDepth / 2;  // of one warp and stage
+constexpr int kZeros = 16 * 8;           // its zero points' words
+__device__ unsigned g_w4_wide_status;
+
+struct Control {
+  uint64_t a_full[kStages], b_full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int TN>
+constexpr int smem_bytes() {
+  return 1024 + kStages * (kOperandA + TN * kDepth * 2) + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T on bf16 operands, issued by one thread.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor for kind::f16: fp32 accumulator, bf16 A and B, both K-major.
+constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Byte j of w, two codes, as bf16 numbers less their zero point: zz = (128 + zero) twice.
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, int j, uint32_t zz) {
+  const uint32_t v = (__byte_perm(w, 0u, 0x4440 + j) * 0x1001u & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&zz));
+  return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// One unit of work: 128 weight rows (gated: 64 of the gate, 64 of the up projection)
+// by one part of K.
+struct Unit {
+  int tile, part, kb0, kbs;
+};
+__device__ __forceinline__ Unit unit_of(int u, int parts, int kbs, int per) {
+  const int tile = u / parts, part = u - tile * parts;
+  return {tile, part, part * per, min(per, kbs - part * per)};
+}
+
+template <int TN, int GROUP>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_wide_kernel(const __grid_constant__ CUtensorMap tmX, const W4Args a, const int parts, const int per_part) {
+  constexpr int kGroups = kDepth / GROUP;  // groups of a row in a stage
+  constexpr int kOperandB = TN * kDepth * 2;
+  constexpr int kSteps = GROUP / 16;  // MMAs to a group
+  constexpr int kZeroWords = (kGroups + 6) / 4;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *opA = smem, *opB = smem + kStages * kOperandA;
+  uint8_t *rings = opB + kStages * kOperandB;
+  Control *ctl = reinterpret_cast<Control *>(rings + kWorkers * kRing * (kCodes + kZeros));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&ctl->a_full[s], kWorkers);
+      ptx::mbar_init(&ctl->b_full[s], 1);
+      ptx::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ctl->acc_full[b], 1);
+      ptx::mbar_init(&ctl->acc_empty[b], 4);
+    }
+    ptx::mbar_init(&ctl->mma_done, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&ctl->tmem_base, 2 * TN);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  pdl_wait_then_release();
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int *abort = &ctl->abort;
+  const auto wait = [&](uint64_t *bar, uint32_t parity) { return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status); };
+  const Tokens tk = a.experts ? tokens_of(a, blockIdx.y) : Tokens{0, 0, a.T};
+  const int per = a.gated ? 64 : 128, tiles = (a.N + per - 1) / per, units = tiles * parts;
+  const int kbs = (a.K + kDepth - 1) / kDepth;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_phase[kStages];
+      for (int s = 0; s < kStages; ++s) last_phase[s] = -1;
+      bool ok = true;
+      for (int tb = 0; ok && tb < tk.count; tb += TN)
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+          const Unit un = unit_of(u, parts, kbs, per_part);
+          for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
+            if (!wait(&ctl->empty[stage], phase ^ 1)) {
+              ok = false;
+              break;
+            }
+            // (rows past the list's are read too, and not stored)
+            ptx::mbar_arrive_expect_tx(&ctl->b_full[stage], kOperandB);
+            uint8_t *b = opB + stage * kOperandB;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int r = 0; r < TN; r += 32)
+                ptx::tma_load_2d(b + half * (TN * 128) + r * 128, &tmX, &ctl->b_full[stage], kb * kDepth + 64 * half,
+                                 tk.first + tb + r);
+            last_phase[stage] = (int)phase;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+        }
+      if (!ok)  // let every issued copy land before the CTA can exit
+        for (int s = 0; s < kStages; ++s)
+          if (last_phase[s] >= 0) pipe::drain_wait(&ctl->b_full[s], (uint32_t)last_phase[s], &g_w4_wide_status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(128, TN);
+      int stage = 0;
+      uint32_t phase = 0, nacc = 0;
+      bool ok = true;
+      for (int tb = 0; ok && tb < tk.count; tb += TN)
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+          const Unit un = unit_of(u, parts, kbs, per_part);
+          for (int kb = 0; ok && kb < un.kbs; ++kb) {
+            if (!wait(&ctl->b_full[stage], phase) || !wait(&ctl->a_full[stage], phase)) {
+              ok = false;
+              break;
+            }
+            const uint64_t ad = ptx::smem_desc_sw128(ptx::smem_u32(opA + stage * kOperandA));
+            const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage * kOperandB));
+            for (int g = 0; g < kGroups; ++g) {
+              if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                const int step = g * kSteps + k;  // 16 deep: 32 bytes of a panel of 64
+                mma_bf16(tmem + (nacc & 1) * TN, ad + (step / 4) * (128 * 128 >> 4) + 2 * (step % 4),
+                         bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4), idesc, k > 0);
+              }
+              ptx::mma_commit(&ctl->acc_full[nacc & 1]);
+              ++nacc;
+            }
+            if (!ok) break;
+            ptx::mma_commit(&ctl->empty[stage]);
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+        }
+      ptx::mma_commit(&ctl->mma_done);
+      pipe::drain_wait(&ctl->mma_done, 0, &g_w4_wide_status);
+    }
+  } else if (warp < 6) {
+    // lane `row` of the tile: TMEM lanes are a warp's own quarter
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint32_t nacc = 0;
+    bool ok = true;
+    for (int tb = 0; ok && tb < tk.count; tb += TN)
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        __syncwarp();
+        const Unit un = unit_of(u, parts, kbs, per_part);
+        const int out = un.tile * per + (a.gated ? row & 63 : row);
+        const int wrow = (a.gated && row >= 64 ? a.N : 0) + min(out, a.N - 1);
+        const uint16_t *scale = a.scale + ((int64_t)tk.e * a.rows + wrow) * a.groups;
+        float tot[TN] = {};
+        float next = bf16lo(scale[un.kb0 * kGroups]);
+        for (int kb = un.kb0; ok && kb < un.kb0 + un.kbs; ++kb)
+#pragma unroll 1
+          for (int g = kb * kGroups; g < (kb + 1) * kGroups; ++g) {
+            const float s = next;
+            // (groups past the last one are products with zeros)
+            next = bf16lo(scale[min(g + 1, a.groups - 1)]);
+            const uint32_t ab = nacc & 1;
+            if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < TN; i += 32) {
+              uint32_t r[32];
+              ptx::tmem_ld32(tl + ab * TN + i, r);
+              ptx::tmem_ld_wait();
+              if (i + 32 == TN) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) tot[i + j] = fmaf(__uint_as_float(r[j]), s, tot[i + j]);
+            }
+            ++nacc;
+          }
+        if (!ok || out >= a.N) continue;
+        // a part's sums: token by token, 32 rows at a time
+        float *to = static_cast<float *>(a.part) + ((int64_t)un.part * a.P + tk.first + tb) * a.rows + wrow;
+        const int count = min(TN, tk.count - tb);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          if (i < count) to[(int64_t)i * a.rows] = tot[i];
+      }
+  } else {
+    const int wkr = warp - 6;  // rows 16 wkr .. of the tile
+    uint8_t *ring = rings + wkr * kRing * (kCodes + kZeros);
+    const int row_bytes = a.K / 2;
+    // copies: piece `lane & 3` (32 codes) of rows lane / 4 and lane / 4 + 8; a row's
+    // pieces stand at piece ^ (row / 2 & 3), so that eight rows' same piece touch all banks
+    const int crow = lane >> 2, cp = lane & 3;
+    const int cto = crow * 64 + ((cp ^ (crow >> 1 & 3)) << 4);
+    // work: piece lane / 8 of rows lane % 8 and + 8
+    const int row = lane & 7, p = lane >> 3;
+    const int from = row * 64 + ((p ^ (row >> 1 & 3)) << 4);
+    const int zgroup = p * 32 / GROUP;  // the piece's group in a stage
+    // the request that runs kRing - 1 stages ahead
+    int ru = blockIdx.x, rkb = 0, rtb = 0, into = 0;
+    const auto first_row = [&](int u) {
+      const Unit un = unit_of(u, parts, kbs, per_part);
+      const int r = a.gated ? (wkr >> 2) * a.N + un.tile * 64 + (wkr & 3) * 16 : un.tile * 128 + wkr * 16;
+      const int last = a.gated ? ((wkr >> 2) + 1) * a.N - 16 : a.N - 16;
+      return min(r, last);  // past the last row: read, not stored
+    };
+    const auto request = [&] {
+      if (rtb < tk.count && ru < units) {
+        const Unit un = unit_of(ru, parts, kbs, per_part);
+        const int64_t r0 = (int64_t)tk.e * a.rows + first_row(ru);
+        const int k0 = (un.kb0 + rkb) * kDepth;
+        const bool in = k0 + 32 * cp < a.K;
+        const uint8_t *src = a.codes + (r0 + crow) * row_bytes + (in ? k0 / 2 + 16 * cp : 0);
+        uint8_t *dst = ring + into * (kCodes + kZeros);
+        ptx::cp_async16_zfill(dst + cto, src, in ? 16u : 0u);
+        ptx::cp_async16_zfill(dst + cto + 512, src + 8 * row_bytes, in ? 16u : 0u);
+        if (a.zero && lane < 16 * kZeroWords) {
+          // the aligned words that hold each row's zero points of this stage
+          const int g0 = (un.kb0 + rkb) * kGroups, zr = lane / kZeroWords, i = lane % kZeroWords;
+          const int64_t at = (r0 + zr) * a.groups + g0;
+          const int lead = (int)(at & 3), left = lead + min(kGroups, a.groups - g0) - 4 * i;
+          ptx::cp_async4(dst + kCodes + 4 * lane, a.zero + (left > 0 ? at - lead + 4 * i : 0),
+                         left > 0 ? (uint32_t)min(left, 4) : 0u);
+        }
+        if (++rkb == un.kbs) {
+          rkb = 0;
+          ru += gridDim.x;
+          if (ru >= units) ru = blockIdx.x, rtb += TN;
+        }
+      }
+      ptx::cp_async_commit();
+      into = into == kRing - 1 ? 0 : into + 1;
+    };
+    for (int i = 0; i < kRing - 1; ++i) request();
+    int stage = 0, held = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tb = 0; ok && tb < tk.count; tb += TN)
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit un = unit_of(u, parts, kbs, per_part);
+        const int64_t r0 = (int64_t)tk.e * a.rows + first_row(u);
+        for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
+          cp_async_wait_group<kRing - 2>();
+          __syncwarp();
+          const uint8_t *src = ring + held * (kCodes + kZeros);
+          uint4 w[2];
+          uint32_t zz[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            w[h] = *reinterpret_cast<const uint4 *>(src + from + 512 * h);
+            uint32_t z = 8u;
+            if (a.zero) {
+              const int zr = row + 8 * h;
+              z = src[kCodes + zr * kZeroWords * 4 + (int)(((r0 + zr) * a.groups + kb * kGroups) & 3) + zgroup] & 15u;
+            }
+            zz[h] = (0x4300u | z) * 0x10001u;
+          }
+          __syncwarp();
+          request();  // into the tile before this one, which every lane has read
+          held = held == kRing - 1 ? 0 : held + 1;
+          if (!wait(&ctl->empty[stage], phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t *panel = opA + stage * kOperandA + (p >> 1) * (128 * 128) + (wkr * 16 + row) * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t ww[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4 *>(panel + h * 8 * 128 + ((((p & 1) * 4 + i) ^ row) << 4)) =
+                  make_uint4(two_codes(ww[i], 0, zz[h]), two_codes(ww[i], 1, zz[h]), two_codes(ww[i], 2, zz[h]),
+                             two_codes(ww[i], 3, zz[h]));
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl->a_full[stage]);
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+      }
+    cp_async_wait_group<0>();
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 2 * TN);
+  }
+}
+
+template <int TN, int GROUP>
+cudaError_t launch_wide(const W4Args &a, const CUtensorMap &tm, const W4Plan &p, int lists, cudaStream_t st) {
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(w4_wide_kernel<TN, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               smem_bytes<TN>());
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  const int kbs = (a.K + kDepth - 1) / kDepth;
+  return launch_kernel(w4_wide_kernel<TN, GROUP>, dim3((unsigned)p.blocks, (unsigned)lists), dim3(kThreads),
+                       (size_t)smem_bytes<TN>(), st, tm, a, p.parts, (kbs + p.parts - 1) / p.parts);
+}
+template <int TN>
+cudaError_t by_group(const W4Args &a, const CUtensorMap &tm, const W4Plan &p, int lists, cudaStream_t st) {
+  if (a.group == 32) return launch_wide<TN, 32>(a, tm, p, lists, st);
+  if (a.group == 64) return launch_wide<TN, 64>(a, tm, p, lists, st);
+  return launch_wide<TN, 128>(a, tm, p, lists, st);
+}
+
+}  // namespace
+
+W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P) {
+  W4Plan best = {};
+  best.nt = tokens <= 32 ? 4 : 8;
+  best.wide = true;
+  const int64_t sms = num_sms(), per = gated ? 64 : 128, tiles = (N + per - 1) / per, kbs = (K + kDepth - 1) / kDepth;
+  double least = 0.0;
+  for (int64_t parts = 1; parts <= 8 && parts <= kbs; ++parts) {
+    const int64_t each = (kbs + parts - 1) / parts, units = tiles * ((kbs + each - 1) / each);
+    const int64_t blocks = std::max<int64_t>(1, std::min(units, sms / lists));
+    const int64_t rounds = (units + blocks - 1) / blocks, waves = (blocks * lists + sms - 1) / sms;
+    // in times of an SM's share of memory bandwidth for a stage of 8 KB, 0.2 us: a unit's
+    // beginning and end cost about 4; the sums' bytes are written and read
+    const double cost = (double)(waves * rounds * (each + 4)) +
+                        8.0 * (double)P * N * (gated ? 2 : 1) * (double)parts / (8192.0 * (double)sms);
+    if (best.blocks == 0 || cost < least) {
+      least = cost;
+      best.parts = (int)((kbs + each - 1) / each);
+      best.blocks = (int)blocks;
+    }
+  }
+  best.planes = best.parts;
+  return best;
+}
+
+cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  CUtensorMap tm;
+  if (!make_bf16_slab_map(&tm, const_cast<void *>(a.x), a.P, a.K)) return cudaErrorInvalidValue;
+  return p.nt == 4 ? by_group<32>(a, tm, p, lists, st) : by_group<64>(a, tm, p, lists, st);
+}
+
+cudaError_t w4_wide_read_status(unsigned *status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_w4_wide_status, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_w4_wide_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace fp8lin
