@@ -28,7 +28,8 @@ namespace fp8lin {
 namespace {
 
 constexpr int kDepth = 128;              // codes of a row in a stage
-constexpr int kStages = 3;               // operand stages
+constexpr int kStages = 2;               // stages of the weights' operand
+constexpr int kStagesB = 5;              // and of the tokens', which come from L2
 constexpr int kRing = 6;                 // tiles of codes that a warp has requested
 constexpr int kWorkers = 8, kThreads = 32 * (6 + kWorkers);
 constexpr int kOperandA = 128 * kDepth * 2;
@@ -37,7 +38,7 @@ constexpr int kZeros = 16 * 8;           // its zero points' words
 __device__ unsigned g_w4_wide_status;
 
 struct Control {
-  uint64_t a_full[kStages], b_full[kStages], empty[kStages];
+  uint64_t a_full[kStages], a_empty[kStages], b_full[kStagesB], b_empty[kStagesB];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -46,7 +47,7 @@ struct Control {
 
 template <int TN>
 constexpr int smem_bytes() {
-  return 1024 + kStages * (kOperandA + TN * kDepth * 2) + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
+  return 1024 + kStages * kOperandA + kStagesB * TN * kDepth * 2 + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T on bf16 operands, issued by one thread.
@@ -66,9 +67,12 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Byte j of w, two codes, as bf16 numbers less their zero point: zz = (128 + zero) twice.
-__device__ __forceinline__ uint32_t two_codes(uint32_t w, int j, uint32_t zz) {
-  const uint32_t v = (__byte_perm(w, 0u, 0x4440 + j) * 0x1001u & 0x000f000fu) | 0x43004300u;
+// Byte j of w, two codes, as bf16 numbers less their zero point: zz = (128 + zero)
+// twice.  mask 0x000f000f and bias 0x43004300 come in registers: as constants they took
+// an instruction each.
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, int j, uint32_t zz, uint32_t mask, uint32_t bias) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(__byte_perm(w, 0u, 0x4440 + j) * 0x1001u), "r"(mask), "r"(bias));
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
                                    *reinterpret_cast<const __nv_bfloat162 *>(&zz));
   return *reinterpret_cast<const uint32_t *>(&d);
@@ -94,14 +98,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *opA = smem, *opB = smem + kStages * kOperandA;
-  uint8_t *rings = opB + kStages * kOperandB;
+  uint8_t *rings = opB + kStagesB * kOperandB;
   Control *ctl = reinterpret_cast<Control *>(rings + kWorkers * kRing * (kCodes + kZeros));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ctl->a_full[s], kWorkers);
+      ptx::mbar_init(&ctl->a_empty[s], 1);
+    }
+    for (int s = 0; s < kStagesB; ++s) {
       ptx::mbar_init(&ctl->b_full[s], 1);
-      ptx::mbar_init(&ctl->empty[s], 1);
+      ptx::mbar_init(&ctl->b_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->acc_full[b], 1);
@@ -131,14 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int last_phase[kStages];
-      for (int s = 0; s < kStages; ++s) last_phase[s] = -1;
+      int last_phase[kStagesB];
+      for (int s = 0; s < kStagesB; ++s) last_phase[s] = -1;
       bool ok = true;
       for (int tb = 0; ok && tb < tk.count; tb += TN)
         for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
           const Unit un = unit_of(u, parts, kbs, per_part);
           for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
-            if (!wait(&ctl->empty[stage], phase ^ 1)) {
+            if (!wait(&ctl->b_empty[stage], phase ^ 1)) {
               ok = false;
               break;
             }
@@ -152,29 +159,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tma_load_2d(b + half * (TN * 128) + r * 128, &tmX, &ctl->b_full[stage], kb * kDepth + 64 * half,
                                  tk.first + tb + r);
             last_phase[stage] = (int)phase;
-            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (++stage == kStagesB) stage = 0, phase ^= 1;
           }
         }
       if (!ok)  // let every issued copy land before the CTA can exit
-        for (int s = 0; s < kStages; ++s)
+        for (int s = 0; s < kStagesB; ++s)
           if (last_phase[s] >= 0) pipe::drain_wait(&ctl->b_full[s], (uint32_t)last_phase[s], &g_w4_wide_status);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16(128, TN);
-      int stage = 0;
-      uint32_t phase = 0, nacc = 0;
+      int stage = 0, stage_b = 0;
+      uint32_t phase = 0, phase_b = 0, nacc = 0;
       bool ok = true;
       for (int tb = 0; ok && tb < tk.count; tb += TN)
         for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
           const Unit un = unit_of(u, parts, kbs, per_part);
           for (int kb = 0; ok && kb < un.kbs; ++kb) {
-            if (!wait(&ctl->b_full[stage], phase) || !wait(&ctl->a_full[stage], phase)) {
+            if (!wait(&ctl->b_full[stage_b], phase_b) || !wait(&ctl->a_full[stage], phase)) {
               ok = false;
               break;
             }
             const uint64_t ad = ptx::smem_desc_sw128(ptx::smem_u32(opA + stage * kOperandA));
-            const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage * kOperandB));
+            const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage_b * kOperandB));
             for (int g = 0; g < kGroups; ++g) {
               if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) {
                 ok = false;
@@ -191,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++nacc;
             }
             if (!ok) break;
-            ptx::mma_commit(&ctl->empty[stage]);
+            ptx::mma_commit(&ctl->a_empty[stage]);
+            ptx::mma_commit(&ctl->b_empty[stage_b]);
             if (++stage == kStages) stage = 0, phase ^= 1;
+            if (++stage_b == kStagesB) stage_b = 0, phase_b ^= 1;
           }
         }
       ptx::mma_commit(&ctl->mma_done);
@@ -202,17 +211,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lane `row` of the tile: TMEM lanes are a warp's own quarter
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const auto row_of = [&](const Unit &un) {  // this lane's weight row of a unit
+      return (a.gated && row >= 64 ? a.N : 0) + min(un.tile * per + (a.gated ? row & 63 : row), a.N - 1);
+    };
+    const auto first_scale = [&](const Unit &un) {
+      return bf16lo(a.scale[((int64_t)tk.e * a.rows + row_of(un)) * a.groups + un.kb0 * kGroups]);
+    };
     uint32_t nacc = 0;
     bool ok = true;
+    float ahead = 0.0f;  // the next unit's first scale, a round trip to memory before its use
+    if (tk.count > 0 && (int)blockIdx.x < units) ahead = first_scale(unit_of(blockIdx.x, parts, kbs, per_part));
     for (int tb = 0; ok && tb < tk.count; tb += TN)
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         __syncwarp();
         const Unit un = unit_of(u, parts, kbs, per_part);
-        const int out = un.tile * per + (a.gated ? row & 63 : row);
-        const int wrow = (a.gated && row >= 64 ? a.N : 0) + min(out, a.N - 1);
+        const int out = un.tile * per + (a.gated ? row & 63 : row), wrow = row_of(un);
         const uint16_t *scale = a.scale + ((int64_t)tk.e * a.rows + wrow) * a.groups;
         float tot[TN] = {};
-        float next = bf16lo(scale[un.kb0 * kGroups]);
+        float next = ahead;
+        ahead = first_scale(unit_of(u + gridDim.x < units ? u + gridDim.x : blockIdx.x, parts, kbs, per_part));
         for (int kb = un.kb0; ok && kb < un.kb0 + un.kbs; ++kb)
 #pragma unroll 1
           for (int g = kb * kGroups; g < (kb + 1) * kGroups; ++g) {
@@ -260,49 +277,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = lane & 7, p = lane >> 3;
     const int from = row * 64 + ((p ^ (row >> 1 & 3)) << 4);
     const int zgroup = p * 32 / GROUP;  // the piece's group in a stage
-    // the request that runs kRing - 1 stages ahead
-    int ru = blockIdx.x, rkb = 0, rtb = 0, into = 0;
-    const auto first_row = [&](int u) {
-      const Unit un = unit_of(u, parts, kbs, per_part);
-      const int r = a.gated ? (wkr >> 2) * a.N + un.tile * 64 + (wkr & 3) * 16 : un.tile * 128 + wkr * 16;
+    // the request that runs kRing - 1 stages ahead: its unit, and where that continues
+    int ru = blockIdx.x, rkb = 0, rkbs = 0, rtb = 0, into = 0;
+    int64_t rfirst = 0;         // the unit's first row of this warp, within the stack
+    const uint8_t *rsrc = nullptr;  // this lane's next piece
+    const auto first_row = [&](int tile) {
+      const int r = a.gated ? (wkr >> 2) * a.N + tile * 64 + (wkr & 3) * 16 : tile * 128 + wkr * 16;
       const int last = a.gated ? ((wkr >> 2) + 1) * a.N - 16 : a.N - 16;
-      return min(r, last);  // past the last row: read, not stored
+      return (int64_t)tk.e * a.rows + min(r, last);  // past the last row: read, not stored
     };
+    const auto begin = [&] {
+      const Unit un = unit_of(ru, parts, kbs, per_part);
+      rkb = un.kb0;
+      rkbs = un.kbs;
+      rfirst = first_row(un.tile);
+      rsrc = a.codes + (rfirst + crow) * row_bytes + rkb * (kDepth / 2) + 16 * cp;
+    };
+    if (ru < units) begin();
     const auto request = [&] {
       if (rtb < tk.count && ru < units) {
-        const Unit un = unit_of(ru, parts, kbs, per_part);
-        const int64_t r0 = (int64_t)tk.e * a.rows + first_row(ru);
-        const int k0 = (un.kb0 + rkb) * kDepth;
-        const bool in = k0 + 32 * cp < a.K;
-        const uint8_t *src = a.codes + (r0 + crow) * row_bytes + (in ? k0 / 2 + 16 * cp : 0);
         uint8_t *dst = ring + into * (kCodes + kZeros);
-        ptx::cp_async16_zfill(dst + cto, src, in ? 16u : 0u);
-        ptx::cp_async16_zfill(dst + cto + 512, src + 8 * row_bytes, in ? 16u : 0u);
+        // (a piece past the row's end: zeros, from an address within it)
+        if (rkb < a.K / kDepth) {
+          ptx::cp_async16(dst + cto, rsrc);
+          ptx::cp_async16(dst + cto + 512, rsrc + 8 * row_bytes);
+        } else {
+          const bool in = rkb * kDepth + 32 * cp < a.K;
+          ptx::cp_async16_zfill(dst + cto, in ? rsrc : a.codes, in ? 16u : 0u);
+          ptx::cp_async16_zfill(dst + cto + 512, in ? rsrc + 8 * row_bytes : a.codes, in ? 16u : 0u);
+        }
         if (a.zero && lane < 16 * kZeroWords) {
           // the aligned words that hold each row's zero points of this stage
-          const int g0 = (un.kb0 + rkb) * kGroups, zr = lane / kZeroWords, i = lane % kZeroWords;
-          const int64_t at = (r0 + zr) * a.groups + g0;
+          const int g0 = rkb * kGroups, zr = lane / kZeroWords, i = lane % kZeroWords;
+          const int64_t at = (rfirst + zr) * a.groups + g0;
           const int lead = (int)(at & 3), left = lead + min(kGroups, a.groups - g0) - 4 * i;
           ptx::cp_async4(dst + kCodes + 4 * lane, a.zero + (left > 0 ? at - lead + 4 * i : 0),
                          left > 0 ? (uint32_t)min(left, 4) : 0u);
         }
-        if (++rkb == un.kbs) {
-          rkb = 0;
+        ++rkb;
+        rsrc += kDepth / 2;
+        if (--rkbs == 0) {
           ru += gridDim.x;
           if (ru >= units) ru = blockIdx.x, rtb += TN;
+          begin();
         }
       }
       ptx::cp_async_commit();
       into = into == kRing - 1 ? 0 : into + 1;
     };
     for (int i = 0; i < kRing - 1; ++i) request();
+    uint32_t mask, bias;
+    asm volatile("mov.b32 %0, 0x000f000f;\n mov.b32 %1, 0x43004300;" : "=r"(mask), "=r"(bias));
     int stage = 0, held = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tb = 0; ok && tb < tk.count; tb += TN)
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit un = unit_of(u, parts, kbs, per_part);
-        const int64_t r0 = (int64_t)tk.e * a.rows + first_row(u);
+        const int64_t r0 = first_row(un.tile);
         for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
           cp_async_wait_group<kRing - 2>();
           __syncwarp();
@@ -322,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           request();  // into the tile before this one, which every lane has read
           held = held == kRing - 1 ? 0 : held + 1;
-          if (!wait(&ctl->empty[stage], phase ^ 1)) {
+          if (!wait(&ctl->a_empty[stage], phase ^ 1)) {
             ok = false;
             break;
           }
@@ -333,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4 *>(panel + h * 8 * 128 + ((((p & 1) * 4 + i) ^ row) << 4)) =
-                  make_uint4(two_codes(ww[i], 0, zz[h]), two_codes(ww[i], 1, zz[h]), two_codes(ww[i], 2, zz[h]),
-                             two_codes(ww[i], 3, zz[h]));
+                  make_uint4(two_codes(ww[i], 0, zz[h], mask, bias), two_codes(ww[i], 1, zz[h], mask, bias),
+                             two_codes(ww[i], 2, zz[h], mask, bias), two_codes(ww[i], 3, zz[h], mask, bias));
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
