@@ -1116,10 +1116,11 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
 // Blocks of tokens of one weight's product, which run side by side.
 int w4_token_blocks(int64_t T, const W4Plan &p) { return p.wide ? 1 : (int)cdiv(T, 8 * p.nt); }
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
-  const int tokens = (int)std::min<int64_t>(T, 1024);
-  W4Plan p = w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, 1, T, false);
+  const int tokens = (int)std::min<int64_t>(T, 1024), N = (int)(gated ? w.rows / 2 : w.rows), K = (int)w.K;
+  if (w4_is_wide(w.rows * w.K, K, tokens)) return w4_wide_plan(N, K, gated, tokens, 1, T);
+  const W4Plan p = w4_plan(N, K, gated, tokens, 1, T, false);
   const int blocks = w4_token_blocks(T, p);
-  return blocks == 1 ? p : w4_plan((int)(gated ? w.rows / 2 : w.rows), (int)w.K, gated, tokens, blocks, T, false);
+  return blocks == 1 ? p : w4_plan(N, K, gated, tokens, blocks, T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
   return p.planes > 1 || p.wide ? (size_t)p.planes * T * w.rows * 4 : 0;
@@ -1170,8 +1171,10 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   const int likely = T == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024);
   const int lists = (int)std::min(E, slots);
   W4Workspace w;
-  w.up = w4_plan((int)F, (int)K, true, likely, lists, slots, false);
-  w.down = w4_plan((int)N, (int)F, false, likely, lists, slots, true);
+  w.up = w4_is_wide(2 * F * K * lists, (int)K, likely) ? w4_wide_plan((int)F, (int)K, true, likely, lists, slots)
+                                                       : w4_plan((int)F, (int)K, true, likely, lists, slots, false);
+  w.down = w4_is_wide(N * F * lists, (int)F, likely) ? w4_wide_plan((int)N, (int)F, false, likely, lists, slots)
+                                                     : w4_plan((int)N, (int)F, false, likely, lists, slots, true);
   w.counts = c.take<int>(4 * E);
   w.offsets = c.take<int>(4 * (E + 1));
   w.position = c.take<int>(4 * slots);

@@ -552,8 +552,12 @@ cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t s
 
 }  // namespace
 
+// tcgen05 from 17 tokens on, where it saves more than its second launch and workspace
+// cost the host (6 us): 64 tokens through [28672, 4096] 88 us here and 44 there, 37
+// tokens through [2048, 512] 16.5 us a call here and 22.9 there.
+bool w4_is_wide(int64_t weights, int K, int tokens) { return tokens > 16 && K >= kChunk && weights >= 1 << 23; }
+
 W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined) {
-  if (tokens > 16 && K >= 128) return w4_wide_plan(N, K, gated, tokens, lists, P);
   W4Plan best = {};
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
   const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;

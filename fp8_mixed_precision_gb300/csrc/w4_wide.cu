@@ -1,21 +1,19 @@
 // Products with 4-bit weights for more than 16 tokens, on tcgen05: 128 weight rows
 // are the M side of the MMAs, 32 or 64 tokens the N side.
 //
-// The codes become bf16 integers code - zero (exact) on their way into shared memory,
-// in the swizzled layout that the MMAs read; the tokens arrive there by TMA as they
-// are.  Products are exact, sums within a group are the tensor core's in TMEM (two
-// accumulators in turn), and the epilogue adds each group's sum times its scale to
-// fp32 sums in registers, a lane per weight row.  Sums over a part of K go to memory
-// and are added by the kernel that follows.
+// The codes become bf16 integers code - zero (exact) on their way into TMEM, from where
+// the MMAs take the weights' side: a lane per weight row.  (Through shared memory their
+// four bytes a code, written and read, were the bound: 45 us.)  The tokens arrive in
+// shared memory by TMA as they are.  Products are exact, sums within a group are the
+// tensor core's in TMEM (two accumulators in turn), and the epilogue adds each group's
+// sum times its scale to fp32 sums in registers, again a lane per weight row.  Sums over
+// a part of K go to memory and are added by the kernel that follows.
 //
-// A code costs two instructions of the half-rate integer pipe (a byte taken out, and
-// one and-or behind a multiplication that moves its second code up 16 bits) and two
-// of the other: about as long as its half byte takes to arrive, so that with 64 tokens
-// the work is bound by those, not by the MMAs.  On mma.m16n8k16, which also moves every
-// product through the register file, 64 tokens through [28672, 4096] took 88 us.
+// On mma.m16n8k16, which moves every product's operands through the register file, 64
+// tokens through [28672, 4096] took 88 us.
 //
 // Warps: 0 requests the tokens' tiles, 1 issues the MMAs, 2-5 are the epilogue, 6-13
-// turn 16 rows each into operands.
+// turn codes into operands: 32 rows (the TMEM lanes of the warp) by half a stage each.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,13 +26,14 @@ namespace fp8lin {
 namespace {
 
 constexpr int kDepth = 128;              // codes of a row in a stage
-constexpr int kStages = 2;               // stages of the weights' operand
-constexpr int kStagesB = 5;              // and of the tokens', which come from L2
-constexpr int kRing = 6;                 // tiles of codes that a warp has requested
+constexpr int kStages = 4;               // stages of the weights' operand
+constexpr int kStagesB = 6;              // and of the tokens', which come from L2
+constexpr int kRing = 8;                 // tiles of codes that a warp has requested
 constexpr int kWorkers = 8, kThreads = 32 * (6 + kWorkers);
-constexpr int kOperandA = 128 * kDepth * 2;
-constexpr int kCodes = 16 * kDepth / 2;  // of one warp and stage
-constexpr int kZeros = 16 * 8;           // its zero points' words
+constexpr int kColsA = kDepth / 2;       // TMEM columns of an operand stage
+constexpr int kTmemCols = 512;           // the operand stages, then two accumulators
+constexpr int kCodes = 32 * kDepth / 4;  // of one warp and stage: 32 rows of 32 bytes
+constexpr int kZeros = 32 * 8;           // its zero points' words
 __device__ unsigned g_w4_wide_status;
 
 struct Control {
@@ -47,18 +46,31 @@ struct Control {
 
 template <int TN>
 constexpr int smem_bytes() {
-  return 1024 + kStages * kOperandA + kStagesB * TN * kDepth * 2 + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
+  return 1024 + kStagesB * TN * kDepth * 2 + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
 }
 
-// D[tmem] (+)= A[smem] B[smem]^T on bf16 operands, issued by one thread.
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A[tmem] B[smem]^T on bf16 operands, issued by one thread.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 32 lanes x 32 consecutive 32-bit columns, lane i of the warp to lane (base lane + i).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Instruction descriptor for kind::f16: fp32 accumulator, bf16 A and B, both K-major.
 constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
@@ -94,10 +106,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kGroups = kDepth / GROUP;  // groups of a row in a stage
   constexpr int kOperandB = TN * kDepth * 2;
   constexpr int kSteps = GROUP / 16;  // MMAs to a group
-  constexpr int kZeroWords = (kGroups + 6) / 4;
+  constexpr int kHalfGroups = kGroups > 1 ? kGroups / 2 : 1;  // of a row in half a stage
+  constexpr int kZeroWords = (kHalfGroups + 6) / 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *opA = smem, *opB = smem + kStages * kOperandA;
+  uint8_t *opB = smem;
   uint8_t *rings = opB + kStagesB * kOperandB;
   Control *ctl = reinterpret_cast<Control *>(rings + kWorkers * kRing * (kCodes + kZeros));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -120,14 +133,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&ctl->tmem_base, 2 * TN);
+    ptx::tmem_alloc(&ctl->tmem_base, kTmemCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   pdl_wait_then_release();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = ctl->tmem_base, acc0 = tmem + kStages * kColsA;
   volatile int *abort = &ctl->abort;
   const auto wait = [&](uint64_t *bar, uint32_t parity) { return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status); };
   const Tokens tk = a.experts ? tokens_of(a, blockIdx.y) : Tokens{0, 0, a.T};
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            const uint64_t ad = ptx::smem_desc_sw128(ptx::smem_u32(opA + stage * kOperandA));
+            const uint32_t ta = tmem + stage * kColsA;
             const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage_b * kOperandB));
             for (int g = 0; g < kGroups; ++g) {
               if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) {
@@ -191,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < kSteps; ++k) {
                 const int step = g * kSteps + k;  // 16 deep: 32 bytes of a panel of 64
-                mma_bf16(tmem + (nacc & 1) * TN, ad + (step / 4) * (128 * 128 >> 4) + 2 * (step % 4),
-                         bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4), idesc, k > 0);
+                mma_bf16(acc0 + (nacc & 1) * TN, ta + 8 * step, bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4),
+                         idesc, k > 0);
               }
               ptx::mma_commit(&ctl->acc_full[nacc & 1]);
               ++nacc;
@@ -210,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 6) {
     // lane `row` of the tile: TMEM lanes are a warp's own quarter
     const int quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tl = acc0 + ((uint32_t)(quarter * 32) << 16);
     const auto row_of = [&](const Unit &un) {  // this lane's weight row of a unit
       return (a.gated && row >= 64 ? a.N : 0) + min(un.tile * per + (a.gated ? row & 63 : row), a.N - 1);
     };
@@ -266,56 +279,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i < count) to[(int64_t)i * a.rows] = tot[i];
       }
   } else {
-    const int wkr = warp - 6;  // rows 16 wkr .. of the tile
-    uint8_t *ring = rings + wkr * kRing * (kCodes + kZeros);
+    const int quarter = warp & 3, half = (warp - 6) >> 2;  // rows 32 quarter .. of the tile, codes 64 half ..
+    uint8_t *ring = rings + (warp - 6) * kRing * (kCodes + kZeros);
     const int row_bytes = a.K / 2;
-    // copies: piece `lane & 3` (32 codes) of rows lane / 4 and lane / 4 + 8; a row's
-    // pieces stand at piece ^ (row / 2 & 3), so that eight rows' same piece touch all banks
-    const int crow = lane >> 2, cp = lane & 3;
-    const int cto = crow * 64 + ((cp ^ (crow >> 1 & 3)) << 4);
-    // work: piece lane / 8 of rows lane % 8 and + 8
-    const int row = lane & 7, p = lane >> 3;
-    const int from = row * 64 + ((p ^ (row >> 1 & 3)) << 4);
-    const int zgroup = p * 32 / GROUP;  // the piece's group in a stage
+    // copies: piece `lane & 1` (32 codes) of rows lane / 2 and lane / 2 + 16.  Four rows'
+    // 128 bytes hold their pieces at piece 2 (row & 3) + which, moved by row / 4, so that
+    // eight rows' same piece touch all banks
+    const auto place = [](int row, int which) {
+      return (row >> 2) * 128 + ((((row & 3) * 2 + which) ^ (row >> 2 & 1)) << 4);
+    };
+    const int crow = lane >> 1, cp = lane & 1;
+    const int cto = place(crow, cp);  // (16 rows on: 512 bytes)
+    const int from0 = place(lane, 0), from1 = place(lane, 1);
+    // the first row of a unit's sixteen rows `j` of this warp, within the stack
+    const auto first_row = [&](int tile, int j) {
+      const int r = (a.gated ? tile * 64 + (quarter & 1) * 32 : tile * 128 + quarter * 32) + 16 * j;
+      return (int64_t)tk.e * a.rows + (a.gated ? (quarter >> 1) * a.N : 0) + min(r, a.N - 16);  // past the last: not stored
+    };
     // the request that runs kRing - 1 stages ahead: its unit, and where that continues
     int ru = blockIdx.x, rkb = 0, rkbs = 0, rtb = 0, into = 0;
-    int64_t rfirst = 0;         // the unit's first row of this warp, within the stack
-    const uint8_t *rsrc = nullptr;  // this lane's next piece
-    const auto first_row = [&](int tile) {
-      const int r = a.gated ? (wkr >> 2) * a.N + tile * 64 + (wkr & 3) * 16 : tile * 128 + wkr * 16;
-      const int last = a.gated ? ((wkr >> 2) + 1) * a.N - 16 : a.N - 16;
-      return (int64_t)tk.e * a.rows + min(r, last);  // past the last row: read, not stored
-    };
+    const uint8_t *rsrc0 = nullptr, *rsrc1 = nullptr;  // this lane's next pieces
+    int64_t rzero = 0;                                 // this lane's row's zero points
     const auto begin = [&] {
       const Unit un = unit_of(ru, parts, kbs, per_part);
       rkb = un.kb0;
       rkbs = un.kbs;
-      rfirst = first_row(un.tile);
-      rsrc = a.codes + (rfirst + crow) * row_bytes + rkb * (kDepth / 2) + 16 * cp;
+      const int64_t r0 = first_row(un.tile, 0), r1 = first_row(un.tile, 1);
+      const int at = rkb * (kDepth / 2) + 32 * half + 16 * cp;
+      rsrc0 = a.codes + (r0 + crow) * row_bytes + at;
+      rsrc1 = a.codes + (r1 + crow) * row_bytes + at;
+      rzero = ((lane < 16 ? r0 : r1) + (lane & 15)) * a.groups;
     };
     if (ru < units) begin();
+    const auto group_of = [&](int kb) { return kb * kGroups + (kGroups > 1 ? half * kHalfGroups : 0); };
     const auto request = [&] {
       if (rtb < tk.count && ru < units) {
         uint8_t *dst = ring + into * (kCodes + kZeros);
-        // (a piece past the row's end: zeros, from an address within it)
         if (rkb < a.K / kDepth) {
-          ptx::cp_async16(dst + cto, rsrc);
-          ptx::cp_async16(dst + cto + 512, rsrc + 8 * row_bytes);
+          ptx::cp_async16(dst + cto, rsrc0);
+          ptx::cp_async16(dst + cto + 512, rsrc1);
         } else {
-          const bool in = rkb * kDepth + 32 * cp < a.K;
-          ptx::cp_async16_zfill(dst + cto, in ? rsrc : a.codes, in ? 16u : 0u);
-          ptx::cp_async16_zfill(dst + cto + 512, in ? rsrc + 8 * row_bytes : a.codes, in ? 16u : 0u);
+          const bool in = rkb * kDepth + 64 * half + 32 * cp < a.K;
+          ptx::cp_async16_zfill(dst + cto, in ? rsrc0 : a.codes, in ? 16u : 0u);
+          ptx::cp_async16_zfill(dst + cto + 512, in ? rsrc1 : a.codes, in ? 16u : 0u);
         }
-        if (a.zero && lane < 16 * kZeroWords) {
-          // the aligned words that hold each row's zero points of this stage
-          const int g0 = rkb * kGroups, zr = lane / kZeroWords, i = lane % kZeroWords;
-          const int64_t at = (rfirst + zr) * a.groups + g0;
-          const int lead = (int)(at & 3), left = lead + min(kGroups, a.groups - g0) - 4 * i;
-          ptx::cp_async4(dst + kCodes + 4 * lane, a.zero + (left > 0 ? at - lead + 4 * i : 0),
-                         left > 0 ? (uint32_t)min(left, 4) : 0u);
+        if (a.zero) {
+          // the aligned words that hold this lane's row's zero points of this half stage
+          const int64_t at = rzero + group_of(rkb);
+          const int lead = (int)(at & 3);
+#pragma unroll
+          for (int i = 0; i < kZeroWords; ++i) {
+            const int left = group_of(rkb) < a.groups ? lead + min(kHalfGroups, a.groups - group_of(rkb)) - 4 * i : 0;
+            ptx::cp_async4(dst + kCodes + 8 * lane + 4 * i, a.zero + (left > 0 ? at - lead + 4 * i : 0),
+                           left > 0 ? (uint32_t)min(left, 4) : 0u);
+          }
         }
         ++rkb;
-        rsrc += kDepth / 2;
+        rsrc0 += kDepth / 2;
+        rsrc1 += kDepth / 2;
         if (--rkbs == 0) {
           ru += gridDim.x;
           if (ru >= units) ru = blockIdx.x, rtb += TN;
@@ -328,47 +349,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kRing - 1; ++i) request();
     uint32_t mask, bias;
     asm volatile("mov.b32 %0, 0x000f000f;\n mov.b32 %1, 0x43004300;" : "=r"(mask), "=r"(bias));
+    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kColsA / 2);
     int stage = 0, held = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tb = 0; ok && tb < tk.count; tb += TN)
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit un = unit_of(u, parts, kbs, per_part);
-        const int64_t r0 = first_row(un.tile);
+        const int64_t zero = (first_row(un.tile, lane >> 4) + (lane & 15)) * a.groups;
         for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
           cp_async_wait_group<kRing - 2>();
           __syncwarp();
           const uint8_t *src = ring + held * (kCodes + kZeros);
-          uint4 w[2];
-          uint32_t zz[2];
+          const uint4 w[2] = {*reinterpret_cast<const uint4 *>(src + from0), *reinterpret_cast<const uint4 *>(src + from1)};
+          uint32_t zz[2];  // of each piece's group
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            w[h] = *reinterpret_cast<const uint4 *>(src + from + 512 * h);
+          for (int i = 0; i < 2; ++i) {
             uint32_t z = 8u;
-            if (a.zero) {
-              const int zr = row + 8 * h;
-              z = src[kCodes + zr * kZeroWords * 4 + (int)(((r0 + zr) * a.groups + kb * kGroups) & 3) + zgroup] & 15u;
-            }
-            zz[h] = (0x4300u | z) * 0x10001u;
+            if (a.zero) z = src[kCodes + 8 * lane + (int)((zero + group_of(kb)) & 3) + (GROUP == 32 ? i : 0)] & 15u;
+            zz[i] = (0x4300u | z) * 0x10001u;
           }
           __syncwarp();
           request();  // into the tile before this one, which every lane has read
           held = held == kRing - 1 ? 0 : held + 1;
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = w[i >> 2];
+            const uint32_t word = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[4 * i + j] = two_codes(word, j, zz[i >> 2], mask, bias);
+          }
           if (!wait(&ctl->a_empty[stage], phase ^ 1)) {
             ok = false;
             break;
           }
-          uint8_t *panel = opA + stage * kOperandA + (p >> 1) * (128 * 128) + (wkr * 16 + row) * 128;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t ww[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4 *>(panel + h * 8 * 128 + ((((p & 1) * 4 + i) ^ row) << 4)) =
-                  make_uint4(two_codes(ww[i], 0, zz[h], mask, bias), two_codes(ww[i], 1, zz[h], mask, bias),
-                             two_codes(ww[i], 2, zz[h], mask, bias), two_codes(ww[i], 3, zz[h], mask, bias));
-          }
-          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          ptx::tc_fence_after();
+          tmem_st32(ta + stage * kColsA, r);
+          tmem_st_wait();
+          ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl->a_full[stage]);
           if (++stage == kStages) stage = 0, phase ^= 1;
@@ -381,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 2 * TN);
+    ptx::tmem_dealloc(tmem, kTmemCols);
   }
 }
 

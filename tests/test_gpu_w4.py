@@ -225,3 +225,77 @@ def test_weights_past_32_bits(fp):
     e = torch.full((1, 1), E - 1, dtype=torch.int32, device="cuda")
     y = fp.fp8_w4_experts(x, torch.ones((1, 1), device="cuda"), e, gu, dn)
     assert bool((y == 64.0 * F).all())
+
+
+WIDE = [  # N, K: weights enough for the kernel of many tokens, ragged tiles and chunks of each group size
+    (2064, 4128), (8192, 1056), (4112, 2080), (32768, 256)]
+
+
+@pytest.mark.parametrize("N,K", WIDE)
+@pytest.mark.parametrize("group,zero", [(32, True), (64, False), (64, True), (128, False), (128, True)])
+def test_many_tokens(fp, N, K, group, zero):
+    w, v = weight(fp, (N, K), group, zero, N)
+    v = v.cuda()
+    for T in (17, 32, 33, 64, 65, 200):
+        g = torch.Generator().manual_seed(T)
+        x = torch.randn((T, K), generator=g).bfloat16().cuda()
+        out = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = fp.fp8_w4_linear(x, w, out=out[:T])
+        want, bound = product(x.double(), v)
+        off = (y.double() - want).abs()
+        assert bool((off <= bound + want.abs() * UB + 1e-38).all()), (T, float((off - want.abs() * UB).max()))
+        assert bool((out[T] == 7.0).all())
+        if N % 32 == 0:
+            h = fp.fp8_w4_gated(x, w, "gelu" if zero else "silu").double()
+            want, bound = gated(x.double(), v, "gelu" if zero else "silu")
+            assert bool(((h - want).abs() <= (bound + want.abs() * UB) * 1.01 + 1e-38).all())
+    assert fp.fp8_get_device_status() == 0
+
+
+@pytest.mark.parametrize("group,zero", [(32, True), (128, False)])
+def test_many_tokens_an_expert(fp, group, zero):
+    """Lists longer and shorter than a tile of tokens, an expert without a token, NaN in one token."""
+    E, K, F, N, T, k = 5, 1056, 1024, 1040, 150, 2
+    gu, vgu = weight(fp, (E, 2 * F, K), group, zero, 1)
+    dn, vdn = weight(fp, (E, N, F), group, zero, 2)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((T, K), generator=g).bfloat16()
+    e = torch.randint(0, E - 1, (T, k), generator=g, dtype=torch.int32)
+    e[:100] = torch.tensor([0, 2], dtype=torch.int32)
+    e[torch.rand((T, k), generator=g) < 0.1] = -1
+    w = torch.rand((T, k), generator=g)
+    ws = fp.w4_experts_workspace(T, k, gu, dn).fill_(0xff)  # NaN wherever it is read as numbers
+    y = fp.fp8_w4_experts(x.cuda(), w.cuda(), e.cuda(), gu, dn, ws=ws).cpu()
+    want, bound = torch.zeros((T, N), dtype=torch.float64), torch.zeros((T, N), dtype=torch.float64)
+    for i in range(E):
+        t, j = (e == i).nonzero(as_tuple=True)
+        if t.numel() == 0:
+            continue
+        h, eh = gated(x.double()[t], vgu[i], "silu")
+        eh = eh * 1.01 + h.abs() * UB * 1.01
+        z, ez = product(h, vdn[i])
+        ez = ez * (1 + UB) + eh @ vdn[i].abs().t()
+        ww = w.double()[t, j][:, None]
+        want.index_add_(0, t, ww * z)
+        bound.index_add_(0, t, ww * (ez + z.abs() * (k + 2) * U))
+    assert bool(((y.double() - want).abs() <= bound + want.abs() * UB + 1e-38).all())
+    x2 = x.clone()
+    x2[7, 3] = math.nan
+    y2 = fp.fp8_w4_experts(x2.cuda(), w.cuda(), e.cuda(), gu, dn).cpu()
+    keep = torch.arange(T) != 7
+    assert torch.equal(y2[keep], y[keep]) and (bool(y2[7].isnan().all()) or bool((e[7] < 0).all()))
+    assert fp.fp8_get_device_status() == 0
+
+
+def test_many_tokens_in_a_graph(fp):
+    w, _ = weight(fp, (4096, 2112), 64, True, 5)
+    x = torch.randn((40, 2112), device="cuda").bfloat16()
+    ws = fp.w4_workspace(w, 40)
+    y = fp.fp8_w4_linear(x, w, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fp.fp8_w4_linear(x, w, out=y, ws=ws)
+    for _ in range(5):
+        x.normal_()
+        g.replay()
+        assert torch.equal(y, fp.fp8_w4_linear(x, w))
