@@ -65,7 +65,9 @@ struct Tile {
   static constexpr int kBytes = kZero + 16 * kZeroWords * 4;
 };
 // Tiles of a warp's ring: what shared memory holds with w4_warps warps to an SM.
-constexpr int w4_stages(int nt, int group) { return nt == 2 ? 3 : nt == 1 && group == 32 ? 4 : 5; }
+constexpr int w4_stages(int nt, int group) { return nt == 2 || (nt == 1 && group == 32) ? 3 : nt == 1 ? 4 : 5; }
+// Sums of one token and item that the warps leave before they meet.
+constexpr int w4_slots(int nt) { return nt == 1 ? 16 : 8 * nt; }
 // A zero point as a number.
 __device__ __forceinline__ float number_of(uint8_t z) { return __uint_as_float(0x4b000000u | z) - 8388608.0f; }
 
@@ -116,7 +118,7 @@ template <int NT, int GROUP>
 __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   using R = Tile<GROUP>;
-  constexpr int kTokens = 8 * NT;
+  constexpr int kTokens = 8 * NT, kSlots = w4_slots(NT);
   constexpr int kGroups = R::kGroups, kStages = w4_stages(NT, GROUP);
   constexpr int kSteps = GROUP / 32;  // 32-deep steps to a group
   // A lane takes kSteps neighbouring words of a row's group, lane q those from
@@ -125,9 +127,9 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   constexpr int kRows = 8 / kSteps;
   const int kw = blockDim.x / 32, wk = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   uint8_t *ring = smem + wk * kStages * R::kBytes;
-  float *part = reinterpret_cast<float *>(smem + kw * kStages * R::kBytes);  // [2][kw][kTokens][kTokenStride]
-  float *sums = part + 2 * kw * kTokens * kTokenStride + wk * kTokens * kGroups;  // [kGroups][kTokens]
-  float *joint = sums + (kw - wk) * kTokens * kGroups;  // [2][kTokens][32]: this block's sums for its cluster
+  float *part = reinterpret_cast<float *>(smem + kw * kStages * R::kBytes);  // [2][kw][kSlots][kTokenStride]
+  float *sums = part + 2 * kw * kSlots * kTokenStride + wk * kTokens * kGroups;  // [kGroups][kTokens]
+  float *joint = sums + (kw - wk) * kTokens * kGroups;  // [2][kSlots][32]: this block's sums for its cluster
   const bool cluster = a.cluster != 0;                  // its blocks are the parts of K
   pdl_wait_then_release();
   const bool list = a.experts != nullptr;
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
     // buffers in turn: a warp writes one again only behind the barrier that follows
     // its last readers.
     const int count = min(kTokens, tk.count - tb);
-    const int slots = count <= 1 ? 1 : 1 << (32 - __clz(count - 1)), batch = kTokens / slots;
+    const int slots = count <= 1 ? 1 : 1 << (32 - __clz(count - 1)), batch = kSlots / slots;
     int stage = 0, at = 0;
     float *buffer = part;
     for (int it = 0; it < mine; ++it) {
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
             tot[j][3] = fmaf(sh, acc[j][3], tot[j][3]);
           }
         }
-        float *to = buffer + (wk * kTokens + at * slots + 2 * q) * kTokenStride + 16 * i + g;
+        float *to = buffer + (wk * kSlots + at * slots + 2 * q) * kTokenStride + 16 * i + g;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -365,12 +367,12 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
         }
       };
       // the warps take them in turn, the next ones each time
-      float *result = joint + (buffer == part ? 0 : kTokens * 32) + lane;
+      float *result = joint + (buffer == part ? 0 : kSlots * 32) + lane;
       int id = wk + it % kw;
       for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
         if ((id & (slots - 1)) >= count) continue;
         float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += buffer[(w * kTokens + id) * kTokenStride + lane];
+        for (int w = 0; w < kw; ++w) v += buffer[(w * kSlots + id) * kTokenStride + lane];
         v *= 0x1p24f;
         if (cluster)
           result[id * 32] = v;
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
         __syncwarp();
       }
       at = 0;
-      buffer = part + (buffer == part) * kw * kTokens * kTokenStride;
+      buffer = part + (buffer == part) * kw * kSlots * kTokenStride;
     }
     cp_async_wait_group<0>();
     if (cluster)
@@ -510,9 +512,9 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
 template <int NT, int GROUP>
 cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
   const auto bytes = [](int warps) {
-    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * 8 * NT * kTokenStride * 4 +
+    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * w4_slots(NT) * kTokenStride * 4 +
                             8 * NT * (kChunk / GROUP) * 4) +
-           2 * 8 * NT * 32 * 4;
+           2 * w4_slots(NT) * 32 * 4;
   };
   static bool set[64] = {};
   int dev = 0;
