@@ -210,50 +210,37 @@ __global__ void __launch_bounds__(kRowThreads) rows_gather_kernel(const void *__
 }
 
 // weights null: the sum of the rows.  A slot without an expert counts as its
-// weight times zero, so that a weight that is NaN shows.  ITEMS 16-byte pieces to a
-// thread, kRowThreads apart, so that their places and then their rows are on the way
-// at once (131072 x 2 x 512: one piece 100 us, the copy rate's 59).
-template <int ITEMS>
+// weight times zero, so that a weight that is NaN shows.  One 16-byte piece to a
+// thread, the rows of four slots on the way at once: 131072 x 2 x 512 takes 69 us (59 at
+// the copy rate), 131072 x 8 x 512 174 (178); two pieces to a thread 81 and 227.
 __global__ void __launch_bounds__(kRowThreads) rows_combine_kernel(const void *__restrict__ z,
                                                                    const int *__restrict__ position,
                                                                    const float *__restrict__ weights, int64_t total,
                                                                    int vecs, int k, void *__restrict__ y) {
-  constexpr int kAtOnce = 4 / ITEMS;  // slots
+  constexpr int kAtOnce = 4;
   pdl_wait_then_release();
-  const int64_t i0 = (int64_t)blockIdx.x * (ITEMS * kRowThreads) + threadIdx.x;
-  int64_t slot[ITEMS];
-  int c[ITEMS];
-#pragma unroll
-  for (int n = 0; n < ITEMS; ++n) {
-    const int64_t i = min(i0 + n * kRowThreads, total - 1);
-    slot[n] = row_of(i, vecs, c[n]) * k;
-  }
-  float a[ITEMS][8] = {};
+  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= total) return;
+  int c;
+  const int64_t slot = row_of(i, vecs, c) * k;
+  float a[8] = {};
   for (int j0 = 0; j0 < k; j0 += kAtOnce) {
-    int p[ITEMS][kAtOnce];
-    float w[ITEMS][kAtOnce];
+    int p[kAtOnce];
+    float w[kAtOnce];
 #pragma unroll
-    for (int n = 0; n < ITEMS; ++n)
+    for (int j = 0; j < kAtOnce; ++j) {
+      const bool in = j0 + j < k;
+      p[j] = in ? position[slot + j0 + j] : -1;
+      w[j] = !in ? 0.0f : weights ? weights[slot + j0 + j] : 1.0f;
+    }
+    uint4 v[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const bool in = j0 + j < k;
-        p[n][j] = in ? position[slot[n] + j0 + j] : -1;
-        w[n][j] = !in ? 0.0f : weights ? weights[slot[n] + j0 + j] : 1.0f;
-      }
-    uint4 v[ITEMS][kAtOnce];
+    for (int j = 0; j < kAtOnce; ++j)
+      v[j] = p[j] >= 0 ? load16(z, (int64_t)p[j] * vecs + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int n = 0; n < ITEMS; ++n)
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        v[n][j] = p[n][j] >= 0 ? load16(z, (int64_t)p[n][j] * vecs + c[n]) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int n = 0; n < ITEMS; ++n)
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) add8(v[n][j], w[n][j], a[n]);
+    for (int j = 0; j < kAtOnce; ++j) add8(v[j], w[j], a);
   }
-#pragma unroll
-  for (int n = 0; n < ITEMS; ++n)
-    if (i0 + n * kRowThreads < total) static_cast<uint4 *>(y)[i0 + n * kRowThreads] = pack8(a[n]);
+  static_cast<uint4 *>(y)[i] = pack8(a);
 }
 
 // dz[row] = w dy[t] and dweights[slot] = <dy[t], z[row]>: TPT threads per token,
@@ -361,12 +348,8 @@ cudaError_t launch_rows_combine(const void *z, const int *position, const float 
                                 void *y, cudaStream_t st) {
   const int vecs = (int)(C / 8);
   LaunchScope ls("rows_combine", st, 2.0 * T * C * (1 + k), 2.0 * T * C * k, T, C, k);
-  const auto go = [&](auto kernel, int items) {
-    return launch_kernel(kernel, dim3((unsigned)((T * vecs + items * kRowThreads - 1) / (items * kRowThreads))),
-                         dim3(kRowThreads), 0, st, z, position, weights, T * vecs, vecs, k, y);
-  };
-  // few rows: one piece a thread, on as many SMs as there are
-  return T * vecs >= (int64_t)num_sms() * 8 * kRowThreads ? go(rows_combine_kernel<2>, 2) : go(rows_combine_kernel<1>, 1);
+  return launch_kernel(rows_combine_kernel, dim3((unsigned)((T * vecs + kRowThreads - 1) / kRowThreads)),
+                       dim3(kRowThreads), 0, st, z, position, weights, T * vecs, vecs, k, y);
 }
 
 cudaError_t launch_rows_combine_bwd(const void *dy, const void *z, const int *position, const float *weights, int64_t T,
