@@ -5,7 +5,7 @@
 // the MMAs take the weights' side: a lane per weight row.  (Through shared memory their
 // four bytes a code, written and read, were the bound: 45 us.)  The tokens arrive in
 // shared memory by TMA as they are.  Products are exact, sums within a group are the
-// tensor core's in TMEM (two accumulators in turn), and the epilogue adds each group's
+// tensor core's in TMEM (four accumulators in turn), and the epilogue adds each group's
 // sum times its scale to fp32 sums in registers, again a lane per weight row.  Sums over
 // a part of K go to memory and are added by the kernel that follows.
 //
@@ -31,14 +31,15 @@ constexpr int kStagesB = 6;              // and of the tokens', which come from 
 constexpr int kRing = 8;                 // tiles of codes that a warp has requested
 constexpr int kWorkers = 8, kThreads = 32 * (6 + kWorkers);
 constexpr int kColsA = kDepth / 2;       // TMEM columns of an operand stage
-constexpr int kTmemCols = 512;           // the operand stages, then two accumulators
+constexpr int kAcc = 4;                  // accumulators (a power of two)
+constexpr int kTmemCols = 512;           // the operand stages, then the accumulators
 constexpr int kCodes = 32 * kDepth / 4;  // of one warp and stage: 32 rows of 32 bytes
 constexpr int kZeros = 32 * 8;           // its zero points' words
 __device__ unsigned g_w4_wide_status;
 
 struct Control {
   uint64_t a_full[kStages], a_empty[kStages], b_full[kStagesB], b_empty[kStagesB];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kAcc], acc_empty[kAcc];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl->b_full[s], 1);
       ptx::mbar_init(&ctl->b_empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAcc; ++b) {
       ptx::mbar_init(&ctl->acc_full[b], 1);
       ptx::mbar_init(&ctl->acc_empty[b], 4);
     }
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ta = tmem + stage * kColsA;
             const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage_b * kOperandB));
             for (int g = 0; g < kGroups; ++g) {
-              if (!wait(&ctl->acc_empty[nacc & 1], ((nacc >> 1) & 1) ^ 1)) {
+              if (!wait(&ctl->acc_empty[nacc % kAcc], (nacc / kAcc & 1) ^ 1)) {
                 ok = false;
                 break;
               }
@@ -204,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < kSteps; ++k) {
                 const int step = g * kSteps + k;  // 16 deep: 32 bytes of a panel of 64
-                mma_bf16(acc0 + (nacc & 1) * TN, ta + 8 * step, bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4),
+                mma_bf16(acc0 + nacc % kAcc * TN, ta + 8 * step, bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4),
                          idesc, k > 0);
               }
-              ptx::mma_commit(&ctl->acc_full[nacc & 1]);
+              ptx::mma_commit(&ctl->acc_full[nacc % kAcc]);
               ++nacc;
             }
             if (!ok) break;
@@ -249,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float s = next;
             // (groups past the last one are products with zeros)
             next = bf16lo(scale[min(g + 1, a.groups - 1)]);
-            const uint32_t ab = nacc & 1;
-            if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) {
+            const uint32_t ab = nacc % kAcc;
+            if (!wait(&ctl->acc_full[ab], nacc / kAcc & 1)) {
               ok = false;
               break;
             }
