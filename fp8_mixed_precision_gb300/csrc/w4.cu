@@ -16,7 +16,7 @@
 //
 // The tokens' values are scaled by a power of two, to [2^14, 2^15) for the largest
 // of a warp's 256, and become fp16 too: exact for every bf16 value down to 2^-27 of
-// that largest one, and below within 2^-36 of it, far less than the rounding of the
+// that largest one, and below within 2^-34 of it, far less than the rounding of the
 // fp32 sums.  Products are exact, sums fp32; zero points enter as zero times the
 // group's sum of x; the scale is applied once per group.
 //
@@ -247,7 +247,9 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       const int up = min(14 + 127 - (int)(top >> 7), 126);
       const bool bad = top >= 0x7f80u;
       const float by = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
-      const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 - up) << 23);
+      // (half of the codes' 2^24 comes back here, half behind the warps' sum: neither
+      // overflows nor loses bits before the product itself does)
+      const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + 12 - up) << 23);
       unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
       unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
 #pragma unroll
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
         if ((id & (slots - 1)) >= count) continue;
         float v = 0.0f;
         for (int w = 0; w < kw; ++w) v += buffer[(w * kSlots + id) * kTokenStride + lane];
-        v *= 0x1p24f;
+        v *= 0x1p12f;
         if (cluster)
           result[id * 32] = v;
         else

@@ -14,6 +14,10 @@
  *   gated MLP   - RMS norm with the residual's addition and an FP8 output, the
  *                 gated feed-forward on FP8 operands, and global gradient
  *                 norm clipping, each with its backward pass where it has one;
+ *   experts     - routing of tokens to gated MLPs, rows in the experts' order, and
+ *                 their weighted sums, with the backward passes;
+ *   4-bit       - linear, gated MLP and experts' MLPs with 4-bit weights, for
+ *                 decoding;
  *   FP8 GEMMs   - fprop, dgrad and wgrad on tcgen05 tensor cores with fp32
  *                 accumulation and BF16 output (use_fast_accum=False in the
  *                 reconstruction's implementation paragraph).
@@ -30,6 +34,7 @@
  *     dimension need not be a multiple of 128: the last 128-block of a row,
  *     column or tile is then shorter ("ragged tail") and its amax covers the
  *     elements present.  A zero dimension makes the call a no-op (FP8_OK).
+ *     Routing takes any number of tokens and experts; 4-bit weights say theirs.
  *     The norm and the gated feed-forward take any number of tokens; their
  *     transposed FP8 layouts have rows of the token count rounded up to a
  *     multiple of 16, filled up with zero bytes.
@@ -547,12 +552,13 @@ fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int6
  *   scale  device bf16 [E, rows, ceil(K / group)]
  *   zero   device u8, of the same shape, 0 .. 15; NULL: 8
  *   rows a multiple of 16, K of 32
- * Products are exact but for values of x under 2^-13 of the largest of their 256
- * neighbours (k to k + 255, k a multiple of 256), which are taken within 2^-22 of
- * that one; sums are fp32.  A token with an infinity or a NaN gets NaN.  Any number
- * of tokens T up to 2^18; written for few (decoding), where the weights' bytes are
- * all that counts.  ws: fp8_w4_workspace_size bytes (0 for many shapes; then NULL
- * will do), of one call at a time.
+ * Products are exact but for values of x under 2^-27 of the largest of their 256
+ * neighbours (k to k + 255, k a multiple of 256), which may be taken within 2^-34 of
+ * that one; sums are fp32.  The products of a token with an infinity or a NaN are not
+ * finite (which of the two depends on the shape); other tokens' are as without it.
+ * Any number of tokens T up to 2^18; written for few (decoding), where the weights'
+ * bytes are all that counts, and meant up to some hundred.  ws: fp8_w4_workspace_size
+ * bytes (0 for many shapes; then NULL will do), of one call at a time.
  * fp8_w4_quantize: codes, scales (and zero points, unless NULL) of bf16 weights
  *   [rows, K] by rounding to the nearest: scale = bf16(max |w| / 7) and zero 8, or
  *   scale = bf16((max - min) / 15) with max >= 0 >= min and zero = round(-min / scale);

@@ -299,3 +299,19 @@ def test_many_tokens_in_a_graph(fp):
         x.normal_()
         g.replay()
         assert torch.equal(y, fp.fp8_w4_linear(x, w))
+
+
+@pytest.mark.parametrize("power", [-120, -100, 100, 115])
+@pytest.mark.parametrize("group,zero", [(32, True), (128, False)])
+def test_small_and_large_values(fp, power, group, zero):
+    """Tokens near either end of bf16: besides the usual bound, a sum of a warp's 256
+    terms is rounded at fp32's last denormal step 2^-149 at worst, 2^12 times smaller
+    than the product, and the result at bf16's, 2^-133."""
+    for N, K in ((64, 512), (16384, 512), (64, 8192)):
+        w, v = weight(fp, (N, K), group, zero, N + K)
+        for T in (1, 9, 40):
+            x = (torch.randn((T, K), generator=torch.Generator().manual_seed(T)) * 2.0 ** power).bfloat16()
+            y = fp.fp8_w4_linear(x.cuda(), w).cpu().double()
+            want, bound = product(x.double(), v)
+            bound = bound + K / 256 * 2.0 ** -136 + 2.0 ** -134 + K * 2.0 ** -149
+            assert bool(((y - want).abs() <= bound + want.abs() * UB).all()), (N, K, T)
