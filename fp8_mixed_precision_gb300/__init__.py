@@ -1331,7 +1331,7 @@ def fp8_expert_combine_bwd(dy: torch.Tensor, z: torch.Tensor, order: ExpertOrder
     _need_bf16_cuda(dy, "dy")
     dev = _here(dy, "dy", stream)
     _order_on(order, dev)
-    T, k, C = order.T, order.k, dy.shape[1]
+    T, k, C = order.T, order.k, dy.shape[-1]
     _need(dy, "dy", (T, C), torch.bfloat16, dev)
     _need(z, "z", (order.rows, C), torch.bfloat16, dev)
     _need(weights, "weights", (T, k), torch.float32, dev)

@@ -4,6 +4,7 @@
 // backward.  Host code only; every arithmetic step runs in the kernels.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <map>
@@ -1069,6 +1070,10 @@ constexpr int64_t kMaxW4Tokens = 1 << 18;  // the grid's third dimension, at lea
 bool element_aligned(const void *p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_DTYPE_F32 ? 3 : 1)) == 0;
 }
+// Pointers to 4-byte values: any alignment of the type.
+bool words_aligned(std::initializer_list<const void *> all) {
+  return std::all_of(all.begin(), all.end(), [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; });
+}
 bool vectors_ok(const void *p, int dtype, int64_t E) {
   return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_DTYPE_F32 ? 15 : 7)) == 0;
 }
@@ -1200,7 +1205,7 @@ fp8_status fp8_route_fwd(const void *logits, fp8_dtype dtype, const float *bias,
   if (groups > kMaxChoices) return FP8_ERR_UNSUPPORTED;
   if (T == 0) return FP8_OK;
   if (!logits || !weights || !experts) return FP8_ERR_INVALID_ARG;
-  if (!element_aligned(logits, dtype)) return FP8_ERR_ALIGN;
+  if (!element_aligned(logits, dtype) || !words_aligned({bias, weights, experts})) return FP8_ERR_ALIGN;
   RouteArgs a = {};
   a.logits = logits;
   a.bias = bias;
@@ -1226,6 +1231,7 @@ fp8_status fp8_route_bwd(const float *dweights, const void *logits, fp8_dtype dt
   if (T == 0) return FP8_OK;
   if (!dweights || !logits || !weights || !experts || !dlogits) return FP8_ERR_INVALID_ARG;
   if (!element_aligned(logits, dtype) || !element_aligned(dlogits, dtype)) return FP8_ERR_ALIGN;
+  if (!words_aligned({dweights, weights, experts})) return FP8_ERR_ALIGN;
   RouteArgs a = {};
   a.logits = logits;
   a.T = T;
@@ -1262,6 +1268,7 @@ fp8_status fp8_expert_order(const int32_t *experts, int64_t slots, int64_t E, in
   if (st == FP8_OK) st = fp8_expert_order_workspace_size(slots, E, &need);
   if (st != FP8_OK) return st;
   if (!counts || !offsets) return FP8_ERR_INVALID_ARG;
+  if (!words_aligned({experts, counts, offsets, position, order, ws})) return FP8_ERR_ALIGN;
   if (slots == 0) {
     const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)E * 4, cs(stream));
     return from_cuda(e != cudaSuccess ? e : cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, cs(stream)));
@@ -1279,7 +1286,7 @@ fp8_status fp8_expert_gather(const void *x, int64_t T, int64_t C, int k, int64_t
   if (st != FP8_OK) return st;
   if (T == 0 || C == 0) return FP8_OK;
   if (!x || !counts || !offsets || !position || !xs) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(xs)) return FP8_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(xs) || !words_aligned({counts, offsets, position})) return FP8_ERR_ALIGN;
   if (T * (C / 8) > (int64_t(1) << 38)) return FP8_ERR_SHAPE;
   return from_cuda(launch_rows_gather(x, T, C, k, (int)E, (int)align, counts, offsets, position, xs, cs(stream)));
 }
@@ -1290,7 +1297,7 @@ fp8_status fp8_expert_combine(const void *z, int64_t T, int64_t C, int k, const 
   if (st != FP8_OK) return st;
   if (T == 0 || C == 0) return FP8_OK;
   if (!z || !position || !y) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(z) || !aligned16(y)) return FP8_ERR_ALIGN;
+  if (!aligned16(z) || !aligned16(y) || !words_aligned({position, weights})) return FP8_ERR_ALIGN;
   if (T * (C / 8) > (int64_t(1) << 38)) return FP8_ERR_SHAPE;
   return from_cuda(launch_rows_combine(z, position, weights, T, C, k, y, cs(stream)));
 }
@@ -1302,6 +1309,7 @@ fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int6
   if (st != FP8_OK) return st;
   if (T == 0) return FP8_OK;
   if (!dweights) return FP8_ERR_INVALID_ARG;
+  if (!words_aligned({counts, offsets, position, weights, dweights})) return FP8_ERR_ALIGN;
   if (C == 0) return from_cuda(cudaMemsetAsync(dweights, 0, (size_t)T * k * 4, cs(stream)));
   if (!dy || !z || !counts || !offsets || !position || !weights || !dz) return FP8_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(z) || !aligned16(dz)) return FP8_ERR_ALIGN;
@@ -1365,7 +1373,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   if (T == 0 || N == 0) return FP8_OK;
   if (!F || !K) return FP8_ERR_SHAPE;
   if (!x || !weights || !experts || !y) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return FP8_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws) || !words_aligned({weights, experts})) return FP8_ERR_ALIGN;
   if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
   const W4Workspace w = w4_workspace(ws, T, k, E, K, F, N);
   const int64_t slots = T * k;

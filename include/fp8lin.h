@@ -488,12 +488,13 @@ fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *no
  * logit or bias, or +inf under softmax) gets experts -1 and weights NaN.
  *   logits   device bf16 or f32 [T, E], any alignment of the type
  *   bias     device f32 [E] or NULL
- *   weights, experts   device f32 and int32 [T, k]
+ *   weights, experts   device f32 and int32 [T, k], any alignment of the type
  *   E <= 1024; k, groups <= 32; k <= E; groups divides E; scale > 0
  * fp8_route_bwd: dlogits (the type of logits) from the weights' gradient, with
  *   logits, weights and experts of the forward pass and its score, renormalize
  *   and scale.  The bias has no gradient; a slot without an expert passes none.
- * Errors: INVALID_ARG, UNSUPPORTED (E, k or groups past their limits), CUDA. */
+ * Errors: INVALID_ARG, SHAPE (T k of 2^31 or so), ALIGN, UNSUPPORTED (E, k or groups past
+ * their limits), CUDA. */
 typedef enum { FP8_SCORE_SOFTMAX = 0, FP8_SCORE_SIGMOID = 1 } fp8_score;
 
 fp8_status fp8_route_fwd(const void *logits, fp8_dtype dtype, const float *bias, int64_t T, int64_t E,
@@ -517,6 +518,7 @@ fp8_status fp8_route_bwd(const float *dweights, const void *logits, fp8_dtype dt
  *   order     device int32 [fp8_expert_rows]: a row's slot, -1 in the gap behind
  *             an expert's rows; past offsets[E] left as it was
  *   ws        fp8_expert_order_workspace_size bytes
+ *   (these arrays, and weights: any alignment of the type)
  * fp8_expert_rows: rows that any choice can need.
  * Moving bf16 rows of C values (a multiple of 16) between tokens and that order:
  *   fp8_expert_gather       xs[position[t, j]] = x[t]; rows in gaps become zeros

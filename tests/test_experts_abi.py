@@ -179,3 +179,36 @@ def test_experts(fp, L):
     assert call(dn=_weight(fp, E=4, rows=96, K=96)) == SHAPE          # another F
     assert call(T=0, x=None, ws=None) == OK
     assert L.fp8_launch_count() == n
+
+
+def test_alignment_of_small_arrays(fp, L):
+    """Float and int arrays need their type's alignment, no more (4 is fine)."""
+    n = L.fp8_launch_count()
+    for name in ("w", "e", "bias"):
+        assert L.fp8_route_fwd(*{**ROUTE, name: ODD2}.values()) == ALIGN
+    for i in (0, 3, 4):
+        a = [A, A, 1, A, A, 5, 64, 8, 0, 1, 1.0, A, None]
+        a[i] = ODD2
+        assert L.fp8_route_bwd(*a) == ALIGN
+    for i in (0, 4, 5, 6, 7, 8):
+        a = [A, 64, 8, 16, A, A, A, A, A, 1 << 30, None]
+        a[i] = ODD2
+        assert L.fp8_expert_order(*a) == ALIGN
+    for i in (6, 7, 8):
+        a = [A, 5, 64, 2, 8, 16, A, A, A, A, None]
+        a[i] = ODD2
+        assert L.fp8_expert_gather(*a) == ALIGN
+    for i in (4, 5):
+        a = [A, 5, 64, 2, A, A, A, None]
+        a[i] = ODD2
+        assert L.fp8_expert_combine(*a) == ALIGN
+    for i in (7, 8, 9, 10, 12):
+        a = [A, A, 5, 64, 2, 8, 16, A, A, A, A, A, A, None]
+        a[i] = ODD2
+        assert L.fp8_expert_combine_bwd(*a) == ALIGN
+    gu, dn = _weight(fp, E=4, rows=128, K=256), _weight(fp, E=4, rows=96, K=64)
+    for i in (3, 4):
+        a = [A, 3, 2, A, A, gu, dn, 0, A, A, 1 << 30, None]
+        a[i] = ODD2
+        assert L.fp8_w4_experts(*a) == ALIGN
+    assert L.fp8_launch_count() == n
