@@ -113,8 +113,8 @@ __device__ __forceinline__ float gate_times(float gate, float up, int act) {
   return h * up;
 }
 
-// NT: n-tiles, of 8 tokens each.  GROUP: weights to a scale.
-template <int NT, int GROUP>
+// NT: n-tiles, of 8 tokens each.  GROUP: weights to a scale.  ZERO: zero points.
+template <int NT, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   using R = Tile<GROUP>;
@@ -143,13 +143,13 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   const int second = a.gated ? a.N : 16;
   const int64_t row0 = (int64_t)tk.e * a.rows + blockIdx.x * per;
 
-  // Codes: of each tile this lane copies pieces (lane & 3) and 4 + (lane & 3) of
-  // rows lane / 4 and 8 + lane / 4.
-  const int f = g % kRows * kSteps;
-  const int to0 = g * 128 + ((q ^ (f & 3)) << 4) + (f >> 2) * 64, to1 = to0 ^ 64;
-  const uint32_t in0 = k0 + 32 * q < a.K ? 16u : 0u, in1 = k0 + 128 + 32 * q < a.K ? 16u : 0u;
-  const uint8_t *codes = a.codes + (row0 + g) * row_bytes + (in0 ? k0 / 2 + 16 * q : 0);
-  const int next1 = in1 ? 64 : 0;
+  // Codes: of each tile this lane copies piece (lane & 7) of rows lane / 8 + 0, 4, 8, 12,
+  // a row's 128 bytes by eight lanes (so that writes touch every bank once, too).
+  const int crow = lane >> 3, cpiece = lane & 7;
+  const int to0 = crow * 128 + ((cpiece ^ crow % kRows * kSteps) << 4);
+  const int to1 = (crow + 4) * 128 + ((cpiece ^ (crow + 4) % kRows * kSteps) << 4);
+  const uint32_t in = k0 + 32 * cpiece < a.K ? 16u : 0u;
+  const uint8_t *codes = a.codes + (row0 + crow) * row_bytes + (in ? k0 / 2 + 16 * cpiece : 0);
   // Scales and zero points: the words lane, lane + 32, .. of the 16 rows' words,
   // each as far as its row and chunk need it (so nothing behind the arrays is
   // touched).  Weight rows come in sixteens: what is aligned stays so.
@@ -169,17 +169,16 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   for (int m = 0; m < kZeroOps; ++m) word(1, lane + 32 * m, R::kZeroWords, zero_at[m], zero_bytes[m]);
   // one tile: codes at `from`, its first row's scales from group `groups` of the stack on
   const auto request = [&](const uint8_t *from, int64_t groups, uint8_t *stage) {
-    ptx::cp_async16_zfill(stage + to0, from, in0);
-    ptx::cp_async16_zfill(stage + to1, from + next1, in1);
-    from += 8 * row_bytes;
-    ptx::cp_async16_zfill(stage + to0 + 1024, from, in0);
-    ptx::cp_async16_zfill(stage + to1 + 1024, from + next1, in1);
+    ptx::cp_async16_zfill(stage + to0, from, in);
+    ptx::cp_async16_zfill(stage + to1, from + 4 * row_bytes, in);
+    ptx::cp_async16_zfill(stage + to0 + 1024, from + 8 * row_bytes, in);
+    ptx::cp_async16_zfill(stage + to1 + 1024, from + 12 * row_bytes, in);
     const uint8_t *sc = reinterpret_cast<const uint8_t *>(a.scale + groups);
 #pragma unroll
     for (int m = 0; m < kScaleOps; ++m)
       if (16 * R::kScaleWords % 32 == 0 || lane + 32 * m < 16 * R::kScaleWords)
         ptx::cp_async4(stage + R::kScale + 128 * m + 4 * lane, sc + scale_at[m], scale_bytes[m]);
-    if (a.zero) {
+    if (ZERO) {
 #pragma unroll
       for (int m = 0; m < kZeroOps; ++m)
         if (16 * R::kZeroWords % 32 == 0 || lane + 32 * m < 16 * R::kZeroWords)
@@ -270,8 +269,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
           mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[0], x[1]);
           mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[2], x[3]);
         }
-        acc[0] *= a.zero ? -1.0f : -8.0f;
-        acc[1] *= a.zero ? -1.0f : -8.0f;
+        acc[0] *= ZERO ? -1.0f : -8.0f;
+        acc[1] *= ZERO ? -1.0f : -8.0f;
         // (the products' first eight rows are alike)
         if (NT == 1)
           held_sums[s][0] = acc[0], held_sums[s][1] = acc[1];
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
             acc[j][0] = acc[j][2] = x.x;
             acc[j][1] = acc[j][3] = x.y;
           }
-          if (a.zero) {
+          if (ZERO) {
             const float zl = number_of(held[zero_lo + s]), zh = number_of(held[zero_hi + s]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[j][0] *= zl, acc[j][1] *= zl, acc[j][2] *= zh, acc[j][3] *= zh;
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
   }
 }
 
-template <int NT, int GROUP>
+template <int NT, int GROUP, bool ZERO>
 cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
   const auto bytes = [](int warps) {
     return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * w4_slots(NT) * kTokenStride * 4 +
@@ -522,7 +521,7 @@ cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, GROUP, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)bytes(w4_warps(NT)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
@@ -545,13 +544,17 @@ cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t 
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   }
-  return cudaLaunchKernelEx(&cfg, w4_kernel<NT, GROUP>, a);
+  return cudaLaunchKernelEx(&cfg, w4_kernel<NT, GROUP, ZERO>, a);
+}
+template <int NT, bool ZERO>
+cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  if (a.group == 32) return launch_w4<NT, 32, ZERO>(a, p, lists, st);
+  if (a.group == 64) return launch_w4<NT, 64, ZERO>(a, p, lists, st);
+  return launch_w4<NT, 128, ZERO>(a, p, lists, st);
 }
 template <int NT>
-cudaError_t by_group(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
-  if (a.group == 32) return launch_w4<NT, 32>(a, p, lists, st);
-  if (a.group == 64) return launch_w4<NT, 64>(a, p, lists, st);
-  return launch_w4<NT, 128>(a, p, lists, st);
+cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  return a.zero ? by_group<NT, true>(a, p, lists, st) : by_group<NT, false>(a, p, lists, st);
 }
 
 }  // namespace
@@ -604,9 +607,9 @@ cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t
     LaunchScope ls(a.gated ? "w4_gated" : "w4_linear", st, weights * (0.5 + (a.zero ? 3.0 : 2.0) / a.group),
                    2.0 * a.rows * a.K * a.P, a.P, a.N, a.K);
     const cudaError_t e = p.wide      ? launch_w4_wide(a, p, lists, st)
-                          : p.nt == 1 ? by_group<1>(a, p, lists, st)
-                          : p.nt == 2 ? by_group<2>(a, p, lists, st)
-                                      : by_group<4>(a, p, lists, st);
+                          : p.nt == 1 ? by_zero<1>(a, p, lists, st)
+                          : p.nt == 2 ? by_zero<2>(a, p, lists, st)
+                                      : by_zero<4>(a, p, lists, st);
     if (e != cudaSuccess || (p.planes == 1 && !p.wide) || a.out_f32) return e;
   }
   const int vecs = a.N / 4;
