@@ -1123,9 +1123,9 @@ int w4_token_blocks(int64_t T, const W4Plan &p) { return p.wide ? 1 : (int)cdiv(
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   const int tokens = (int)std::min<int64_t>(T, 1024), N = (int)(gated ? w.rows / 2 : w.rows), K = (int)w.K;
   if (w4_is_wide(w.rows * w.K, K, tokens)) return w4_wide_plan(N, K, gated, tokens, 1, T);
-  const W4Plan p = w4_plan(N, K, gated, tokens, 1, T, false);
+  const W4Plan p = w4_plan(N, K, gated, tokens, 1, 1, T, false);
   const int blocks = w4_token_blocks(T, p);
-  return blocks == 1 ? p : w4_plan(N, K, gated, tokens, blocks, T, false);
+  return blocks == 1 ? p : w4_plan(N, K, gated, tokens, 1, blocks, T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
   return p.planes > 1 || p.wide ? (size_t)p.planes * T * w.rows * 4 : 0;
@@ -1162,6 +1162,8 @@ fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated
 struct W4Workspace {
   W4Plan up, down;
   int *counts, *offsets, *position, *order, *hist;
+  W4List *lists;
+  int most, tile;  // of them
   float *up_part;
   void *xs;  // token rows in the experts' order, for the kernel that reads tiles of them
   void *h;
@@ -1176,15 +1178,21 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   const int likely = T == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024);
   const int lists = (int)std::min(E, slots);
   W4Workspace w;
-  w.up = w4_is_wide(2 * F * K * lists, (int)K, likely) ? w4_wide_plan((int)F, (int)K, true, likely, lists, slots)
-                                                       : w4_plan((int)F, (int)K, true, likely, lists, slots, false);
-  w.down = w4_is_wide(N * F * lists, (int)F, likely) ? w4_wide_plan((int)N, (int)F, false, likely, lists, slots)
-                                                     : w4_plan((int)N, (int)F, false, likely, lists, slots, true);
+  const auto plan = [&](int64_t rows, int64_t in, bool gated) {
+    return w4_is_wide(rows * (gated ? 2 : 1) * in * lists, (int)in, likely)
+               ? w4_wide_plan((int)rows, (int)in, gated, likely, lists, slots)
+               : w4_plan((int)rows, (int)in, gated, likely, T > 1 ? lists : 1, T > 1 ? 1 : lists, slots, !gated);
+  };
+  w.up = plan(F, K, true);
+  w.down = plan(N, F, false);
   w.counts = c.take<int>(4 * E);
   w.offsets = c.take<int>(4 * (E + 1));
   w.position = c.take<int>(4 * slots);
   w.order = c.take<int>(4 * slots);
   w.hist = c.take<int>(chunks > 1 ? 4 * E * chunks : 0);
+  w.most = lists;
+  w.tile = 8 * (w.up.wide ? w.down.nt : w.up.nt);  // (of the kernel that takes lists)
+  w.lists = c.take<W4List>(sizeof(W4List) * (lists + 1));
   w.up_part = c.take<float>(w.up.planes > 1 || w.up.wide ? 8 * slots * F * w.up.planes : 0);
   w.xs = c.take<void>(w.up.wide ? 2 * slots * K : 0);
   w.h = c.take<void>(2 * slots * F);
@@ -1381,7 +1389,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   const bool sorted = T > 1;
   if (sorted) {
     st = from_cuda(launch_expert_order(experts, slots, (int)E, 1, w.counts, w.offsets, w.position, w.order, w.hist,
-                                       cs(stream)));
+                                       cs(stream), w.lists, w.most, w.tile));
     if (st != FP8_OK) return st;
   }
   W4Args a = w4_args(x, T, *gate_up, w.h), b = w4_args(w.h, T, *down, w.z);
@@ -1406,7 +1414,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
       p->order = w.order;
       p->offsets = w.offsets;
       p->counts = w.counts;
-      p->by_row = slots < E;
+      p->lists = w.lists;
     }
     st = from_cuda(launch_w4_product(*p, p == &a ? w.up : w.down, lists, cs(stream)));
     if (st != FP8_OK) return st;

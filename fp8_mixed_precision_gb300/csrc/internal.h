@@ -212,11 +212,18 @@ cudaError_t launch_route_fwd(RouteArgs a, float *weights, int *experts, cudaStre
 cudaError_t launch_route_bwd(RouteArgs a, const float *dweights, const float *weights, const int *experts,
                              void *dlogits, cudaStream_t st);
 
+// An expert with tokens: its rows in the experts' order, and the work (of one item of
+// the weight's rows, in the units of list_work) of all experts before it.  Behind the
+// last one an entry that has `from` alone, up to the count of lists that there might be.
+struct W4List {
+  int e, first, count, from;
+};
 // Rows in the experts' order (rows.cu).  hist: E x order_chunks(slots) ints,
-// unused for one chunk.
+// unused for one chunk.  lists: [most + 1], for products of `tile` tokens at a time.
 int order_chunks(int64_t slots);
 cudaError_t launch_expert_order(const int *experts, int64_t slots, int E, int align, int *counts, int *offsets,
-                                int *position, int *order, int *hist, cudaStream_t st);
+                                int *position, int *order, int *hist, cudaStream_t st, W4List *lists = nullptr,
+                                int most = 0, int tile = 0);
 cudaError_t launch_rows_gather(const void *x, int64_t T, int64_t C, int k, int E, int align, const int *counts,
                                const int *offsets, const int *position, void *xs, cudaStream_t st);
 cudaError_t launch_rows_combine(const void *z, const int *position, const float *weights, int64_t T, int64_t C, int k,
@@ -237,29 +244,31 @@ struct W4Args {
   void *out;              // gated: bf16 [P, N]; else bf16, or (out_f32) fp32 [planes, P, N]
   void *part;             // fp32 [planes, P, rows], with more than one
   const int *experts, *order, *offsets, *counts;
-  int T, P, E, k, by_row, tokens;  // P: output rows (T, or the slots)
-  int N, rows, K, group;           // N outputs; rows = 2 N when gated
+  const W4List *lists;     // with order: [min(E, P) + 1]
+  int T, P, E, k, tokens;  // P: output rows (T, or the slots)
+  int N, rows, K, group;   // N outputs; rows = 2 N when gated
   int gated, act, out_f32;
   int groups, cluster;  // filled in by the launch
+  unsigned per_block;   // 2^32 / blocks
 };
 // How a product is cut: n-tiles of 8 tokens, parts of K, warps (256 of K each)
 // and blocks to a part; planes: partial sums that are left for a second kernel (1:
 // none, the parts are added within the launch).  tokens: as many as a list may be
-// expected to have; lists: weights that are read at once; P: output rows;
-// joined: the caller adds the planes.
+// expected to have; lists: weights; side: blocks of tokens that read the weight side by
+// side; P: output rows; joined: the caller adds the planes.
 struct W4Plan {
   int nt, parts, warps, blocks, planes;
   bool wide;  // w4_wide.cu; its planes are always added after
 };
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined);
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int side, int64_t P, bool joined);
 // Whether w4_wide.cu takes a product of so many weights (of all lists).
 bool w4_is_wide(int64_t weights, int K, int tokens);
 // The same for w4_wide.cu, and its launch: sums over the parts into a.part, x [P, K].
 W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P);
 cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st);
 cudaError_t w4_wide_read_status(unsigned *status);
-// lists: the grid's lists, one per expert (or per row, by_row); one weight: blocks
-// of 8 nt tokens.  Sums the planes unless out_f32.
+// lists: as many experts as may have a token; one weight: blocks of 8 nt tokens.  Sums
+// the planes unless out_f32.
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st);
 cudaError_t launch_w4_join(const float *z, const int *experts, const int *position, const float *weights, int64_t T,
                            int64_t N, int k, int E, int planes, void *y, cudaStream_t st);

@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "w4.cuh"
 
 namespace fp8lin {
 namespace {
@@ -76,11 +77,13 @@ __global__ void __launch_bounds__(kOrderThreads) order_place_kernel(const int *_
                                                                     int align, const int *__restrict__ hist,
                                                                     int *__restrict__ counts, int *__restrict__ offsets,
                                                                     int *__restrict__ position,
-                                                                    int *__restrict__ order) {
+                                                                    int *__restrict__ order, W4List *__restrict__ lists,
+                                                                    int most, int tile) {
   extern __shared__ int smem[];
   int *mine = smem;                    // [kOrderWarps][E]: rows before this warp's next slot of e
   int *start = smem + kOrderWarps * E;  // [E + 1]
   __shared__ int part[kOrderWarps];
+  __shared__ int64_t part64[kOrderWarps];
   pdl_wait_then_release();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kOrderWarps * E; i += kOrderThreads) mine[i] = 0;
@@ -108,8 +111,10 @@ __global__ void __launch_bounds__(kOrderThreads) order_place_kernel(const int *_
     start[x] = hist ? counts[x] : before;
   }
   __syncthreads();
-  // exclusive sums of the aligned counts, 256 experts at a time
+  // exclusive sums of the aligned counts, 256 experts at a time (and for the products of
+  // the experts' tokens those of the lists and their work)
   int total = 0;
+  int64_t listed = 0;  // lists << 32 | work
   for (int b = 0; b < E; b += kOrderThreads) {
     const int x = b + threadIdx.x;
     const int v = x < E ? (start[x] + align - 1) / align * align : 0;
@@ -132,6 +137,23 @@ __global__ void __launch_bounds__(kOrderThreads) order_place_kernel(const int *_
     }
     for (int w = 0; w < kOrderWarps; ++w) total += part[w];
     __syncthreads();
+    if (lists && blockIdx.x == 0) {
+      const int n = x < E ? start[x] : 0;
+      const int64_t own = n ? (int64_t(1) << 32) + list_work(n, tile) : 0;
+      int64_t sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int64_t u = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += u;
+      }
+      if (lane == 31) part64[warp] = sum;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) sum += part64[w];
+      const int64_t at = listed + sum - own;
+      if (n) lists[at >> 32] = W4List{x, first, n, (int)at};
+      for (int w = 0; w < kOrderWarps; ++w) listed += part64[w];
+      __syncthreads();
+    }
     if (x < E) {
       const int base = first + (hist ? hist[(int64_t)x * gridDim.x + blockIdx.x] : 0);
 #pragma unroll
@@ -139,6 +161,9 @@ __global__ void __launch_bounds__(kOrderThreads) order_place_kernel(const int *_
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
+  if (lists && blockIdx.x == 0)
+    for (int l = (int)(listed >> 32) + threadIdx.x; l <= most; l += kOrderThreads)
+      lists[l] = W4List{0, 0, 0, (int)listed};
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kBatches; ++i) {
@@ -315,7 +340,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_combine_bwd_kernel(
 int order_chunks(int64_t slots) { return (int)((slots + kOrderChunk - 1) / kOrderChunk); }
 
 cudaError_t launch_expert_order(const int *experts, int64_t slots, int E, int align, int *counts, int *offsets,
-                                int *position, int *order, int *hist, cudaStream_t st) {
+                                int *position, int *order, int *hist, cudaStream_t st, W4List *lists, int most,
+                                int tile) {
   const int chunks = order_chunks(slots);
   const size_t smem = (size_t)(kOrderWarps * E + E + 1) * 4;
   if (chunks > 1) {
@@ -332,7 +358,8 @@ cudaError_t launch_expert_order(const int *experts, int64_t slots, int E, int al
   }
   LaunchScope ls("order_place", st, 12.0 * slots, 0.0, slots, E);
   return launch_kernel(order_place_kernel, dim3((unsigned)chunks), dim3(kOrderThreads), smem, st, experts, slots, E,
-                       align, chunks > 1 ? (const int *)hist : (const int *)nullptr, counts, offsets, position, order);
+                       align, chunks > 1 ? (const int *)hist : (const int *)nullptr, counts, offsets, position, order, lists, most,
+                       tile);
 }
 
 cudaError_t launch_rows_gather(const void *x, int64_t T, int64_t C, int k, int E, int align, const int *counts,

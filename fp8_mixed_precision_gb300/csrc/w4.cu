@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -113,6 +114,31 @@ __device__ __forceinline__ float gate_times(float gate, float up, int act) {
   return h * up;
 }
 
+// The lists' items, one list's after the other's, are cut into pieces of as much work, one
+// for a block, which begins within a list and may go on into the next ones.  (A list's
+// items cut by themselves, as many pieces of each: 64 tokens through 32 experts 173 us for
+// XXX.)  What a block takes of list `list`: items item0 .. item0 + mine - 1, perhaps none.
+struct Piece {
+  int e, first, count, item0, mine, list, last;  // last: nothing follows
+};
+// Not negative; a 64-bit division takes some 100 instructions.
+__device__ __forceinline__ int64_t divided(int64_t a, int b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+// All lists' work before a block's.
+__device__ __forceinline__ int64_t work_before(const W4Args &a, int64_t work, unsigned block) {
+  if (block == gridDim.x) return work;
+  return (int64_t)__umul64hi((uint64_t)work, (uint64_t)(block * a.per_block) << 32);
+}
+__device__ __forceinline__ Piece piece_of(const W4List &at, int next, int items, int l, int64_t from, int64_t to) {
+  const int64_t before = at.from * (int64_t)items, after = next * (int64_t)items;
+  if (before >= to || before == after) return {0, 0, 0, 0, 0, l, 1};  // (the same: behind the last list)
+  const int weight = next - at.from;
+  const int item0 = before >= from ? 0 : (int)divided(from - before + weight - 1, weight);
+  const int end = after <= to ? items : (int)divided(to - before + weight - 1, weight);
+  return {at.e, at.first, at.count, item0, end - item0, l, after >= to};
+}
+
 // NT: n-tiles, of 8 tokens each.  GROUP: weights to a scale.  ZERO: zero points.
 template <int NT, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
@@ -132,16 +158,10 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   float *joint = sums + (kw - wk) * kTokens * kGroups;  // [2][kSlots][32]: this block's sums for its cluster
   const bool cluster = a.cluster != 0;                  // its blocks are the parts of K
   pdl_wait_then_release();
-  const bool list = a.experts != nullptr;
-  const Tokens tk = list ? tokens_of(a, blockIdx.z) : Tokens{0, 0, a.T};
   const int chunk = blockIdx.y * kw + wk, k0 = chunk * kChunk;
   const int row_bytes = a.K / 2, group0 = chunk * kGroups;
-  const int per = a.gated ? 16 : 32, items = (a.N + per - 1) / per, step = per * (int)gridDim.x;
-  // A block's items: output rows from blockIdx.x per on, `step` rows apart, each of
-  // two tiles of 16 weight rows, `second` rows apart.
-  const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int second = a.gated ? a.N : 16;
-  const int64_t row0 = (int64_t)tk.e * a.rows + blockIdx.x * per;
+  // Items: `per` output rows, two tiles of 16 weight rows, `second` rows apart.
+  const int per = a.gated ? 16 : 32, items = (a.N + per - 1) / per, second = a.gated ? a.N : 16;
 
   // Codes: of each tile this lane copies piece (lane & 7) of rows lane / 8 + 0, 4, 8, 12,
   // a row's 128 bytes by eight lanes (so that writes touch every bank once, too).
@@ -149,7 +169,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   const int to0 = crow * 128 + ((cpiece ^ crow % kRows * kSteps) << 4);
   const int to1 = (crow + 4) * 128 + ((cpiece ^ (crow + 4) % kRows * kSteps) << 4);
   const uint32_t in = k0 + 32 * cpiece < a.K ? 16u : 0u;
-  const uint8_t *codes = a.codes + (row0 + crow) * row_bytes + (in ? k0 / 2 + 16 * cpiece : 0);
+  const int64_t code_at = (int64_t)crow * row_bytes + (in ? k0 / 2 + 16 * cpiece : 0);
   // Scales and zero points: the words lane, lane + 32, .. of the 16 rows' words,
   // each as far as its row and chunk need it (so nothing behind the arrays is
   // touched).  Weight rows come in sixteens: what is aligned stays so.
@@ -190,219 +210,273 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
   const int scale_lo = R::kScale + g * R::kScaleWords * 4, scale_hi = scale_lo + 8 * R::kScaleWords * 4;
   const int zero_lo = R::kZero + g * R::kZeroWords * 4 + lead1, zero_hi = zero_lo + 8 * R::kZeroWords * 4;
 
-  for (int tb = list ? 0 : blockIdx.z * kTokens; tb < tk.count; tb += list ? kTokens : gridDim.z * kTokens) {
-    // the item whose tiles are requested next; a second tile past the last row: the
-    // first one's rows again, read and not stored
-    const uint8_t *from = codes;
-    int64_t groups = row0 * a.groups;
-    int ahead = 0, into = 0;
-    const auto request_next = [&](int i) {
-      if (ahead < mine) {
-        const int more = i && (a.gated || blockIdx.x * per + ahead * step + 16 < a.N) ? second : 0;
-        request(from + (int64_t)more * row_bytes, groups + (int64_t)more * a.groups, ring + into * R::kBytes);
-        if (i) {
-          ++ahead;
-          from += (int64_t)step * row_bytes;
-          groups += (int64_t)step * a.groups;
-        }
-      }
-      ptx::cp_async_commit();
-      into = into == kStages - 1 ? 0 : into + 1;
-    };
-    uint4 v[8];  // the values of one n-tile's tokens
-    const auto load_tokens = [&](int tb, int j) {
-      const int n = tb + 8 * j + g, p = tk.first + n;
-      const bool some = n < tk.count;
-      const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
-      const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.K + k0 + 8 * kSteps * q;
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int k = s / kSteps * GROUP + s % kSteps * 8;
-        v[s] = make_uint4(0, 0, 0, 0);
-        if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
-      }
-    };
-    load_tokens(tb, 0);
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) request_next(s & 1);
-
-    // Column g of n-tile j is token 8 j + g; lane (g, q) has the values that its
-    // words' codes meet, those of the codes at bit 4 of a half divided by 16.
-    uint32_t b[NT][8][4];
-    float unscale[NT][2];                        // of tokens 8 j + 2 q, + 1
-    float held_sums[kGroups][2];   // their groups' sums, with one n-tile
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j > 0) load_tokens(tb, j);
-      uint32_t top = 0u;  // largest |x| as bits, both halves
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu),
-                                     __vmaxu2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu)));
-      top = max(top >> 16, top & 0xffffu);
-      top = max(top, __shfl_xor_sync(kFull, top, 1));
-      top = max(top, __shfl_xor_sync(kFull, top, 2));
-      // 2^(14 - exponent), at most 2^126; an infinity or a NaN makes the token's product NaN
-      const int up = min(14 + 127 - (int)(top >> 7), 126);
-      const bool bad = top >= 0x7f80u;
-      const float by = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
-      // (half of the codes' 2^24 comes back here, half behind the warps' sum: neither
-      // overflows nor loses bits before the product itself does)
-      const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + 12 - up) << 23);
-      unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
-      unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        b[j][s][0] = f16x2(bf16lo(v[s].x) * by, bf16lo(v[s].z) * by);
-        b[j][s][1] = sixteenth(f16x2(bf16hi(v[s].x) * by, bf16hi(v[s].z) * by));
-        b[j][s][2] = f16x2(bf16lo(v[s].y) * by, bf16lo(v[s].w) * by);
-        b[j][s][3] = sixteenth(f16x2(bf16hi(v[s].y) * by, bf16hi(v[s].w) * by));
-      }
-      // the groups' sums as they enter the products (times -8 with no zero points):
-      // products with codes of one
-#pragma unroll
-      for (int s = 0; s < kGroups; ++s) {
-        float acc[4] = {};
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-          const uint32_t *x = b[j][s * kSteps + st];
-          mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[0], x[1]);
-          mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[2], x[3]);
-        }
-        acc[0] *= ZERO ? -1.0f : -8.0f;
-        acc[1] *= ZERO ? -1.0f : -8.0f;
-        // (the products' first eight rows are alike)
-        if (NT == 1)
-          held_sums[s][0] = acc[0], held_sums[s][1] = acc[1];
-        else if (g == 0)
-          *reinterpret_cast<float2 *>(sums + s * kTokens + 8 * j + 2 * q) = make_float2(acc[0], acc[1]);
-      }
+  // One list (one weight, or the expert of one slot of one token): a block takes items
+  // blockIdx.x, blockIdx.x + gridDim.x, ..  Lists of tokens, long, short or empty: pieces.
+  __shared__ Piece tk;  // (registers are scarce)
+  if (a.order) {
+    const int most = min(a.E, a.P);
+    // (a thread's first entry and the sum come in one round trip to memory)
+    int i = threadIdx.x;
+    W4List at = a.lists[min(i, most - 1)];
+    int next = a.lists[min(i, most - 1) + 1].from;
+    const int64_t work = a.lists[most].from * (int64_t)items;
+    const int64_t from = work_before(a, work, blockIdx.x), to = work_before(a, work, blockIdx.x + 1);
+    if (from >= to) return;
+    for (;;) {
+      if (i < most && at.from * (int64_t)items <= from && from < next * (int64_t)items)
+        tk = piece_of(at, next, items, i, from, to);
+      if ((i += blockDim.x) >= most) break;
+      at = a.lists[i];
+      next = a.lists[i + 1].from;
     }
-    __syncwarp();
-
-    // The warps' sums meet for as many items at once as fit the buffer (all of them,
-    // mostly, with one token: a barrier for each item took 3.4 us of 19.4).  Two
-    // buffers in turn: a warp writes one again only behind the barrier that follows
-    // its last readers.
-    const int count = min(kTokens, tk.count - tb);
-    const int slots = count <= 1 ? 1 : 1 << (32 - __clz(count - 1)), batch = kSlots / slots;
-    int stage = 0, at = 0;
-    float *buffer = part;
-    for (int it = 0; it < mine; ++it) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        cp_async_wait_group<kStages - 2>();
-        __syncwarp();
-        request_next((kStages - 1 + i) & 1);
-        const uint8_t *held = ring + stage * R::kBytes, *base = held + g * 128 + 4 * kSteps * q;
-        stage = stage == kStages - 1 ? 0 : stage + 1;
-        float tot[NT][4] = {};
-#pragma unroll
-        for (int s = 0; s < kGroups; ++s) {
-          uint32_t w[2][kSteps];  // codes of rows g and g + 8
-#pragma unroll
-          for (int h = 0; h < 2; ++h) load_words<kSteps>(base + 8 * 128 * h + ((s ^ g % kRows) * kSteps << 4), w[h]);
-          const float sl = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_lo + lead2 + 2 * s));
-          const float sh = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_hi + lead2 + 2 * s));
-          float acc[NT][4];
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const float2 x = NT == 1 ? make_float2(held_sums[s][0], held_sums[s][1])
-                                     : *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
-            acc[j][0] = acc[j][2] = x.x;
-            acc[j][1] = acc[j][3] = x.y;
-          }
-          if (ZERO) {
-            const float zl = number_of(held[zero_lo + s]), zh = number_of(held[zero_hi + s]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j][0] *= zl, acc[j][1] *= zl, acc[j][2] *= zh, acc[j][3] *= zh;
-          }
-#pragma unroll
-          for (int st = 0; st < kSteps; ++st) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w0 = h ? w[0][st] >> 8 : w[0][st], w1 = h ? w[1][st] >> 8 : w[1][st];
-              const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-                mma_add(acc[j], a0, a1, a2, a3, b[j][s * kSteps + st][2 * h], b[j][s * kSteps + st][2 * h + 1]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            tot[j][0] = fmaf(sl, acc[j][0], tot[j][0]);
-            tot[j][1] = fmaf(sl, acc[j][1], tot[j][1]);
-            tot[j][2] = fmaf(sh, acc[j][2], tot[j][2]);
-            tot[j][3] = fmaf(sh, acc[j][3], tot[j][3]);
+  } else if (threadIdx.x == 0) {
+    const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int e = a.experts ? a.experts[blockIdx.z] : 0;  // of one token: its slots are the rows
+    tk = {e, a.experts ? (int)blockIdx.z : 0, a.T, (int)blockIdx.x, e >= 0 && e < a.E ? mine : 0, 0, 1};
+  }
+  __syncthreads();
+  const int step = a.order ? per : per * (int)gridDim.x;
+  for (;;) {
+    const int mine = tk.mine, out0 = tk.item0 * per;
+    const int64_t row0 = (int64_t)tk.e * a.rows + out0;
+    const int side = a.experts ? 1 : gridDim.z, at0 = a.experts ? 0 : blockIdx.z * kTokens;
+    for (int tb = at0; mine > 0 && tb < tk.count; tb += side * kTokens) {
+      // the item whose tiles are requested next; a second tile past the last row: the
+      // first one's rows again, read and not stored
+      const uint8_t *from = a.codes + row0 * row_bytes + code_at;
+      int64_t groups = row0 * a.groups;
+      int ahead = 0, into = 0;
+      const auto request_next = [&](int i) {
+        if (ahead < mine) {
+          const int more = i && (a.gated || out0 + ahead * step + 16 < a.N) ? second : 0;
+          request(from + (int64_t)more * row_bytes, groups + (int64_t)more * a.groups, ring + into * R::kBytes);
+          if (i) {
+            ++ahead;
+            from += (int64_t)step * row_bytes;
+            groups += (int64_t)step * a.groups;
           }
         }
-        float *to = buffer + (wk * kSlots + at * slots + 2 * q) * kTokenStride + 16 * i + g;
+        ptx::cp_async_commit();
+        into = into == kStages - 1 ? 0 : into + 1;
+      };
+      uint4 v[8];  // the values of one n-tile's tokens
+      const auto load_tokens = [&](int tb, int j) {
+        const int n = tb + 8 * j + g, p = tk.first + n;
+        const bool some = n < tk.count;
+        const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
+        const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.K + k0 + 8 * kSteps * q;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-            if (8 * j + 2 * q + v < slots) {
-              to[(8 * j + v) * kTokenStride] = tot[j][v] * unscale[j][v];
-              to[(8 * j + v) * kTokenStride + 8] = tot[j][2 + v] * unscale[j][v];
-            }
-      }
-      if (++at < batch && it + 1 < mine) continue;
-      __syncthreads();
-      // a lane per row: `id` is one token of one item
-      const auto leave = [&](int id, float v) {
-        const int t = id & (slots - 1), item = it + 1 - at + id / slots;
-        const int out = blockIdx.x * per + item * step + (a.gated ? lane & 15 : lane);
-        const int64_t p = tk.first + tb + t;
-        if (gridDim.y > 1 && !cluster) {  // one part of K
-          if (a.gated || out < a.N)
-            static_cast<float *>(a.part)[(blockIdx.y * (int64_t)a.P + p) * a.rows + (lane & 16 && a.gated ? a.N : 0) +
-                                         out] = v;
-        } else if (a.gated) {
-          const float up = __shfl_down_sync(kFull, v, 16);
-          if (lane < 16) static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(gate_times(v, up, a.act));
-        } else if (out < a.N) {
-          if (a.out_f32)
-            static_cast<float *>(a.out)[p * a.N + out] = v;
-          else
-            static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(v);
+        for (int s = 0; s < 8; ++s) {
+          const int k = s / kSteps * GROUP + s % kSteps * 8;
+          v[s] = make_uint4(0, 0, 0, 0);
+          if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
         }
       };
-      // the warps take them in turn, the next ones each time
-      float *result = joint + (buffer == part ? 0 : kSlots * 32) + lane;
-      int id = wk + it % kw;
-      for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
-        if ((id & (slots - 1)) >= count) continue;
-        float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += buffer[(w * kSlots + id) * kTokenStride + lane];
-        v *= 0x1p12f;
-        if (cluster)
-          result[id * 32] = v;
-        else
-          leave(id, v);
-      }
-      if (cluster) {
-        // the parts' sums, one block's share each; what is read here is written again
-        // behind the next barrier at the earliest
-        __syncwarp();
-        ptx::cluster_sync();
-        const int rank = blockIdx.y, parts = gridDim.y;
-        for (id = rank + parts * wk; id < at * slots; id += parts * kw) {
-          if ((id & (slots - 1)) >= count) continue;
-          const uint32_t at0 = ptx::smem_u32(result + id * 32);
-          float v = 0.0f;
-          for (int m = 0; m < parts; ++m) v += ptx::ld_shared_cluster_f(ptx::mapa_shared(at0, m));
-          leave(id, v);
+      load_tokens(tb, 0);
+#pragma unroll
+      for (int s = 0; s < kStages - 1; ++s) request_next(s & 1);
+
+      // Column g of n-tile j is token 8 j + g; lane (g, q) has the values that its
+      // words' codes meet, those of the codes at bit 4 of a half divided by 16.
+      uint32_t b[NT][8][4];
+      float unscale[NT][2];                        // of tokens 8 j + 2 q, + 1
+      float held_sums[kGroups][2];   // their groups' sums, with one n-tile
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j > 0) load_tokens(tb, j);
+        uint32_t top = 0u;  // largest |x| as bits, both halves
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu),
+                                       __vmaxu2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu)));
+        top = max(top >> 16, top & 0xffffu);
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        top = max(top, __shfl_xor_sync(kFull, top, 2));
+        // 2^(14 - exponent), at most 2^126; an infinity or a NaN makes the token's product NaN
+        const int up = min(14 + 127 - (int)(top >> 7), 126);
+        const bool bad = top >= 0x7f80u;
+        const float by = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + up) << 23);
+        // (half of the codes' 2^24 comes back here, half behind the warps' sum: neither
+        // overflows nor loses bits before the product itself does)
+        const float back = __uint_as_float(bad ? 0x7fc00000u : (uint32_t)(127 + 12 - up) << 23);
+        unscale[j][0] = __shfl_sync(kFull, back, 8 * q);
+        unscale[j][1] = __shfl_sync(kFull, back, 8 * q + 4);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          b[j][s][0] = f16x2(bf16lo(v[s].x) * by, bf16lo(v[s].z) * by);
+          b[j][s][1] = sixteenth(f16x2(bf16hi(v[s].x) * by, bf16hi(v[s].z) * by));
+          b[j][s][2] = f16x2(bf16lo(v[s].y) * by, bf16lo(v[s].w) * by);
+          b[j][s][3] = sixteenth(f16x2(bf16hi(v[s].y) * by, bf16hi(v[s].w) * by));
         }
-        __syncwarp();
+        // the groups' sums as they enter the products (times -8 with no zero points):
+        // products with codes of one
+#pragma unroll
+        for (int s = 0; s < kGroups; ++s) {
+          float acc[4] = {};
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+            const uint32_t *x = b[j][s * kSteps + st];
+            mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[0], x[1]);
+            mma_add(acc, 0x00010001u, 0u, 0x00100010u, 0u, x[2], x[3]);
+          }
+          acc[0] *= ZERO ? -1.0f : -8.0f;
+          acc[1] *= ZERO ? -1.0f : -8.0f;
+          // (the products' first eight rows are alike)
+          if (NT == 1)
+            held_sums[s][0] = acc[0], held_sums[s][1] = acc[1];
+          else if (g == 0)
+            *reinterpret_cast<float2 *>(sums + s * kTokens + 8 * j + 2 * q) = make_float2(acc[0], acc[1]);
+        }
       }
-      at = 0;
-      buffer = part + (buffer == part) * kw * kSlots * kTokenStride;
+      __syncwarp();
+
+      // The warps' sums meet for as many items at once as fit the buffer (all of them,
+      // mostly, with one token: a barrier for each item took 3.4 us of 19.4).  Two
+      // buffers in turn: a warp writes one again only behind the barrier that follows
+      // its last readers.
+      const int count = min(kTokens, tk.count - tb);
+      const int slots = count <= 1 ? 1 : 1 << (32 - __clz(count - 1)), batch = kSlots / slots;
+      int stage = 0, at = 0;
+      float *buffer = part;
+      // J: n-tiles that have a token
+      const auto walk = [&](auto j_tiles) {
+        constexpr int J = decltype(j_tiles)::value;
+        for (int it = 0; it < mine; ++it) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            cp_async_wait_group<kStages - 2>();
+            __syncwarp();
+            request_next((kStages - 1 + i) & 1);
+            const uint8_t *held = ring + stage * R::kBytes, *base = held + g * 128 + 4 * kSteps * q;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            float tot[J][4] = {};
+#pragma unroll
+            for (int s = 0; s < kGroups; ++s) {
+              uint32_t w[2][kSteps];  // codes of rows g and g + 8
+#pragma unroll
+              for (int h = 0; h < 2; ++h) load_words<kSteps>(base + 8 * 128 * h + ((s ^ g % kRows) * kSteps << 4), w[h]);
+              const float sl = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_lo + lead2 + 2 * s));
+              const float sh = bf16lo(*reinterpret_cast<const uint16_t *>(held + scale_hi + lead2 + 2 * s));
+              float acc[J][4];
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                const float2 x = NT == 1 ? make_float2(held_sums[s][0], held_sums[s][1])
+                                         : *reinterpret_cast<const float2 *>(sums + s * kTokens + 8 * j + 2 * q);
+                acc[j][0] = acc[j][2] = x.x;
+                acc[j][1] = acc[j][3] = x.y;
+              }
+              if (ZERO) {
+                const float zl = number_of(held[zero_lo + s]), zh = number_of(held[zero_hi + s]);
+#pragma unroll
+                for (int j = 0; j < J; ++j) acc[j][0] *= zl, acc[j][1] *= zl, acc[j][2] *= zh, acc[j][3] *= zh;
+              }
+#pragma unroll
+              for (int st = 0; st < kSteps; ++st) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t w0 = h ? w[0][st] >> 8 : w[0][st], w1 = h ? w[1][st] >> 8 : w[1][st];
+                  const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
+#pragma unroll
+                  for (int j = 0; j < J; ++j)
+                    mma_add(acc[j], a0, a1, a2, a3, b[j][s * kSteps + st][2 * h], b[j][s * kSteps + st][2 * h + 1]);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                tot[j][0] = fmaf(sl, acc[j][0], tot[j][0]);
+                tot[j][1] = fmaf(sl, acc[j][1], tot[j][1]);
+                tot[j][2] = fmaf(sh, acc[j][2], tot[j][2]);
+                tot[j][3] = fmaf(sh, acc[j][3], tot[j][3]);
+              }
+            }
+            float *to = buffer + (wk * kSlots + at * slots + 2 * q) * kTokenStride + 16 * i + g;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                if (8 * j + 2 * q + v < slots) {
+                  to[(8 * j + v) * kTokenStride] = tot[j][v] * unscale[j][v];
+                  to[(8 * j + v) * kTokenStride + 8] = tot[j][2 + v] * unscale[j][v];
+                }
+          }
+          if (++at < batch && it + 1 < mine) continue;
+          __syncthreads();
+          // a lane per row: `id` is one token of one item
+          const auto leave = [&](int id, float v) {
+            const int t = id & (slots - 1), item = it + 1 - at + id / slots;
+            const int out = out0 + item * step + (a.gated ? lane & 15 : lane);
+            const int64_t p = tk.first + tb + t;
+            if (gridDim.y > 1 && !cluster) {  // one part of K
+              if (a.gated || out < a.N)
+                static_cast<float *>(a.part)[(blockIdx.y * (int64_t)a.P + p) * a.rows + (lane & 16 && a.gated ? a.N : 0) +
+                                             out] = v;
+            } else if (a.gated) {
+              const float up = __shfl_down_sync(kFull, v, 16);
+              if (lane < 16) static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(gate_times(v, up, a.act));
+            } else if (out < a.N) {
+              if (a.out_f32)
+                static_cast<float *>(a.out)[p * a.N + out] = v;
+              else
+                static_cast<__nv_bfloat16 *>(a.out)[p * a.N + out] = __float2bfloat16_rn(v);
+            }
+          };
+          // the warps take them in turn, the next ones each time
+          float *result = joint + (buffer == part ? 0 : kSlots * 32) + lane;
+          int id = wk + it % kw;
+          for (id = id >= kw ? id - kw : id; id < at * slots; id += kw) {
+            if ((id & (slots - 1)) >= count) continue;
+            float v = 0.0f;
+            for (int w = 0; w < kw; ++w) v += buffer[(w * kSlots + id) * kTokenStride + lane];
+            v *= 0x1p12f;
+            if (cluster)
+              result[id * 32] = v;
+            else
+              leave(id, v);
+          }
+          if (cluster) {
+            // the parts' sums, one block's share each; what is read here is written again
+            // behind the next barrier at the earliest
+            __syncwarp();
+            ptx::cluster_sync();
+            const int rank = blockIdx.y, parts = gridDim.y;
+            for (id = rank + parts * wk; id < at * slots; id += parts * kw) {
+              if ((id & (slots - 1)) >= count) continue;
+              const uint32_t at0 = ptx::smem_u32(result + id * 32);
+              float v = 0.0f;
+              for (int m = 0; m < parts; ++m) v += ptx::ld_shared_cluster_f(ptx::mapa_shared(at0, m));
+              leave(id, v);
+            }
+            __syncwarp();
+          }
+          at = 0;
+          buffer = part + (buffer == part) * kw * kSlots * kTokenStride;
+        }
+      };
+      if constexpr (NT > 1) {
+        if (count <= 8)
+          walk(std::integral_constant<int, 1>());
+        else if (NT > 2 && count <= 16)
+          walk(std::integral_constant<int, 2>());
+        else
+          walk(std::integral_constant<int, NT>());
+      } else {
+        walk(std::integral_constant<int, 1>());
+      }
+      cp_async_wait_group<0>();
+      if (cluster)
+        ptx::cluster_sync();  // no block leaves, or writes again, what another still reads
+      else
+        __syncthreads();
     }
-    cp_async_wait_group<0>();
-    if (cluster)
-      ptx::cluster_sync();  // no block leaves, or writes again, what another still reads
-    else
-      __syncthreads();
+    if (tk.last) break;
+    const int l = tk.list + 1;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const int64_t work = a.lists[min(a.E, a.P)].from * (int64_t)items;
+      tk = piece_of(a.lists[l], a.lists[l + 1].from, items, l, work_before(a, work, blockIdx.x),
+                    work_before(a, work, blockIdx.x + 1));
+    }
+    __syncthreads();
   }
 }
 
@@ -527,7 +601,7 @@ cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t 
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)p.parts, (unsigned)lists);
+  cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)p.parts, a.order ? 1u : (unsigned)lists);
   cfg.blockDim = dim3(32 * p.warps);
   cfg.dynamicSmemBytes = bytes(p.warps);
   cfg.stream = st;
@@ -564,10 +638,12 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 // tokens through [2048, 512] 16.5 us a call here and 22.9 there.
 bool w4_is_wide(int64_t weights, int K, int tokens) { return tokens > 16 && K >= kChunk && weights >= 1 << 23; }
 
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool joined) {
+W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int side, int64_t P, bool joined) {
   W4Plan best = {};
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
-  const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32, items = (N + per - 1) / per;
+  const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32;
+  // (a list's items follow those of the list before it)
+  const int64_t items = (N + per - 1) / per * lists;
   const int most = w4_warps(best.nt);
   const int64_t fewest = (chunks + most - 1) / most;
   // A cluster's exchange is worth its barriers where it saves a second kernel and the
@@ -580,8 +656,8 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool 
     const int64_t warps = (chunks + parts - 1) / parts, resident = most / warps;
     // a cluster's blocks stay within a processor cluster, of an eighth of the SMs
     const int64_t slots = cluster ? 8 * (sms / 8 * resident / parts) : sms * resident / parts;
-    const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / lists));
-    const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * lists + sms - 1) / sms;
+    const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / side));
+    const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * side + sms - 1) / sms;
     // in times of an SM's share of memory bandwidth for 4 KB (a warp's two tiles),
     // about 0.1 us; an exchange costs about 2 of them, one through a cluster 6, the
     // second kernel 15, and the sums' bytes, written and read
@@ -601,6 +677,7 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int64_t P, bool 
 
 cudaError_t launch_w4_product(W4Args a, const W4Plan &p, int lists, cudaStream_t st) {
   a.groups = (a.K + a.group - 1) / a.group;
+  a.per_block = (unsigned)((1ull << 32) / (unsigned)p.blocks - (p.blocks == 1));
   a.cluster = !p.wide && p.parts > 1 && p.planes == 1;
   {
     const double weights = (double)a.rows * a.K * (a.experts ? std::min(a.E, lists) : 1);

@@ -6,23 +6,16 @@
 
 namespace fp8lin {
 
-// The tokens of list y: expert, first row in the experts' order and count.
+// The tokens of an expert: first row in the experts' order and count.
 struct Tokens {
   int e, first, count;
 };
-__device__ __forceinline__ Tokens tokens_of(const W4Args &a, int y) {
-  const auto valid = [&](int e) { return e >= 0 && e < a.E; };
-  if (!a.order) {  // one token: its slots are the rows
-    const int e = a.experts[y];
-    return valid(e) ? Tokens{e, y, 1} : Tokens{0, 0, 0};
-  }
-  int e = y;
-  if (a.by_row) {  // fewer rows than experts: the first row of an expert stands for it
-    if (y >= a.offsets[a.E]) return {0, 0, 0};
-    e = a.experts[a.order[y]];
-    if (a.offsets[e] != y) return {0, 0, 0};
-  }
-  return {e, a.offsets[e], a.counts[e]};
+// A list's work for one item of the weight's rows, as kernels of `tile` tokens (8, 16 or
+// 32) at a time take them: what a block does for the codes is worth as much as for eight
+// tokens' products.
+__host__ __device__ __forceinline__ int list_work(int count, int tile) {
+  const int rest = (count % tile + 7) / 8;
+  return count / tile * (1 + tile / 8) + (rest == 0 ? 0 : rest == 3 ? 5 : 1 + rest);
 }
 
 }  // namespace fp8lin

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base, acc0 = tmem + kStages * kColsA;
   volatile int *abort = &ctl->abort;
   const auto wait = [&](uint64_t *bar, uint32_t parity) { return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status); };
-  const Tokens tk = a.experts ? tokens_of(a, blockIdx.y) : Tokens{0, 0, a.T};
+  const Tokens tk = a.experts ? Tokens{(int)blockIdx.y, a.offsets[blockIdx.y], a.counts[blockIdx.y]} : Tokens{0, 0, a.T};
   const int per = a.gated ? 64 : 128, tiles = (a.N + per - 1) / per, units = tiles * parts;
   const int kbs = (a.K + kDepth - 1) / kDepth;
 
