@@ -222,8 +222,8 @@ struct W4List {
 // unused for one chunk.  lists: [most + 1], for products of `tile` tokens at a time.
 int order_chunks(int64_t slots);
 cudaError_t launch_expert_order(const int *experts, int64_t slots, int E, int align, int *counts, int *offsets,
-                                int *position, int *order, int *hist, cudaStream_t st, W4List *lists = nullptr,
-                                int most = 0, int tile = 0);
+                                int *position, int *order, int *hist, cudaStream_t st,
+                                W4List *lists = nullptr, int most = 0, int tile = 0);
 cudaError_t launch_rows_gather(const void *x, int64_t T, int64_t C, int k, int E, int align, const int *counts,
                                const int *offsets, const int *position, void *xs, cudaStream_t st);
 cudaError_t launch_rows_combine(const void *z, const int *position, const float *weights, int64_t T, int64_t C, int k,
