@@ -315,3 +315,52 @@ def test_small_and_large_values(fp, power, group, zero):
             want, bound = product(x.double(), v)
             bound = bound + K / 256 * 2.0 ** -136 + 2.0 ** -134 + K * 2.0 ** -149
             assert bool(((y - want).abs() <= bound + want.abs() * UB).all()), (N, K, T)
+
+
+def experts_product(x, e, w, vgu, vdn, act):
+    """fp8_w4_experts in 64 bits and its bound before the last rounding."""
+    k = e.shape[1]
+    want = torch.zeros((x.shape[0], vdn.shape[1]), dtype=torch.float64)
+    bound = torch.zeros_like(want)
+    for i in range(vgu.shape[0]):
+        t, j = (e == i).nonzero(as_tuple=True)
+        if t.numel():
+            h, eh = gated(x.double()[t], vgu[i], act)
+            eh = eh * 1.01 + h.abs() * UB * 1.01
+            z, ez = product(h, vdn[i])
+            ez = ez * (1 + UB) + eh @ vdn[i].abs().t()
+            ww = w.double()[t, j][:, None]
+            want.index_add_(0, t, ww * z)
+            bound.index_add_(0, t, ww.abs() * (ez + z.abs() * (k + 2) * U))
+    return want, bound
+
+
+@pytest.mark.parametrize("T,E,k,K,F,N", [(40, 24, 2, 96, 32, 16), (9, 70, 3, 320, 96, 48), (130, 12, 2, 544, 256, 160),
+                                         (50, 6, 3, 2048, 512, 256), (2, 1024, 4, 64, 32, 32)])
+@pytest.mark.parametrize("kind", ["one", "last", "none", "steps", "twice"])
+def test_experts_of_uneven_lists(fp, T, E, k, K, F, N, kind):
+    """Lists far longer than others, empty ones between them, fewer items than blocks, the same
+    expert twice in a token, and the workspace of another choice used again."""
+    gu, vgu = weight(fp, (E, 2 * F, K), 64, True, E)
+    dn, vdn = weight(fp, (E, N, F), 64, True, F)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, K), generator=g).bfloat16()
+    w = torch.rand((T, k), generator=g)
+    e = torch.full((T, k), -1, dtype=torch.int32)
+    if kind == "one":
+        e[:, 0] = E // 2
+    elif kind == "last":
+        e[:, k - 1] = E - 1
+        e[0, 0] = 0
+    elif kind == "steps":  # expert i has about twice the tokens of expert i + 2
+        at = torch.rand((T, k), generator=g).log2().mul(-2).int()
+        e = torch.where(at * 2 < E, at * 2, torch.tensor(-1, dtype=torch.int32)).contiguous()
+    elif kind == "twice":
+        e[:] = torch.randint(0, E, (T, 1), generator=g, dtype=torch.int32)
+    ws = fp.w4_experts_workspace(T, k, gu, dn).fill_(0xff)
+    every = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    for choice in (e, every, e):
+        y = fp.fp8_w4_experts(x.cuda(), w.cuda(), choice.cuda(), gu, dn, "gelu", ws=ws).cpu()
+        want, bound = experts_product(x, choice, w, vgu, vdn, "gelu")
+        assert bool(((y.double() - want).abs() <= bound + want.abs() * UB + 1e-38).all())
+
