@@ -260,7 +260,7 @@ struct W4Plan {
   int nt, parts, warps, blocks, planes;
   bool wide;  // w4_wide.cu; its planes are always added after
 };
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int side, int64_t P, bool joined);
+W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined);
 // Whether w4_wide.cu takes a product of so many weights (of all lists).
 bool w4_is_wide(int64_t weights, int K, int tokens);
 // The same for w4_wide.cu, and its launch: sums over the parts into a.part, x [P, K].

@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -598,26 +599,66 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
   }
 }
 
+// Dynamic shared memory of a block.
+template <int NT, int GROUP>
+constexpr size_t w4_bytes(int warps) {
+  return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * w4_slots(NT) * kTokenStride * 4 +
+                          8 * NT * (kChunk / GROUP) * 4) +
+         2 * w4_slots(NT) * 32 * 4;
+}
 template <int NT, int GROUP, bool ZERO>
-cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
-  const auto bytes = [](int warps) {
-    return (size_t)warps * (w4_stages(NT, GROUP) * Tile<GROUP>::kBytes + 2 * w4_slots(NT) * kTokenStride * 4 +
-                            8 * NT * (kChunk / GROUP) * 4) +
-           2 * w4_slots(NT) * 32 * 4;
-  };
+cudaError_t allow_bytes() {
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, GROUP, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)bytes(w4_warps(NT)));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) set[dev] = true;
-  }
+  if (dev >= 0 && dev < 64 && set[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, GROUP, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)w4_bytes<NT, GROUP>(w4_warps(NT)));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = true;
+  return e;
+}
+// Clusters of `parts` blocks that the GPU holds at once.  (Its processor clusters are not
+// of one size: an eighth of the SMs to each gave 40 clusters of 7 blocks for the 38 that
+// fit, and a second wave: 7 tokens through [16384, 14336] took 76 us for XXX.)
+template <int GROUP>
+int clusters_of(int warps, int parts) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, (unsigned)parts, 1);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = w4_bytes<1, GROUP>(warps);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.y = (unsigned)parts;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (allow_bytes<1, GROUP, false>() == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&n, w4_kernel<1, GROUP, false>, &cfg) == cudaSuccess && n > 0)
+    return n;
+  cudaGetLastError();  // no GPU: the plan is not launched
+  return std::max(1, num_sms() * (w4_warps(1) / warps) / parts);
+}
+int64_t max_clusters(int group, int warps, int parts) {
+  static std::atomic<int> known[64][3][w4_warps(1) + 1][kW4Cluster + 1];  // 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  std::atomic<int> &n = known[dev][group / 64][warps][parts];
+  if (n.load(std::memory_order_relaxed) == 0)
+    n.store(group == 32   ? clusters_of<32>(warps, parts)
+            : group == 64 ? clusters_of<64>(warps, parts)
+                          : clusters_of<128>(warps, parts),
+            std::memory_order_relaxed);
+  return n.load(std::memory_order_relaxed);
+}
+template <int NT, int GROUP, bool ZERO>
+cudaError_t launch_w4(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
+  const cudaError_t e = allow_bytes<NT, GROUP, ZERO>();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)p.parts, a.order ? 1u : (unsigned)lists);
   cfg.blockDim = dim3(32 * p.warps);
-  cfg.dynamicSmemBytes = bytes(p.warps);
+  cfg.dynamicSmemBytes = w4_bytes<NT, GROUP>(p.warps);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
@@ -652,7 +693,7 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 // tokens through [2048, 512] 16.5 us a call here and 22.9 there.
 bool w4_is_wide(int64_t weights, int K, int tokens) { return tokens > 16 && K >= kChunk && weights >= 1 << 23; }
 
-W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int side, int64_t P, bool joined) {
+W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined) {
   W4Plan best = {};
   best.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
   const int64_t sms = num_sms(), chunks = (K + kChunk - 1) / kChunk, per = gated ? 16 : 32;
@@ -668,8 +709,8 @@ W4Plan w4_plan(int N, int K, bool gated, int tokens, int lists, int side, int64_
   double least = 0.0;
   for (int64_t parts = fewest; parts <= limit && parts <= chunks; ++parts) {
     const int64_t warps = (chunks + parts - 1) / parts, resident = most / warps;
-    // a cluster's blocks stay within a processor cluster, of an eighth of the SMs
-    const int64_t slots = cluster ? 8 * (sms / 8 * resident / parts) : sms * resident / parts;
+    const int64_t slots =
+        cluster && parts > 1 ? max_clusters(group, (int)warps, (int)parts) : sms * resident / parts;
     const int64_t blocks = std::max<int64_t>(1, std::min(items, slots / side));
     const int64_t rounds = (items + blocks - 1) / blocks, together = (blocks * parts * side + sms - 1) / sms;
     // in times of an SM's share of memory bandwidth for 4 KB (a warp's two tiles),
