@@ -619,7 +619,8 @@ cudaError_t allow_bytes() {
 }
 // Clusters of `parts` blocks that the GPU holds at once.  (Its processor clusters are not
 // of one size: an eighth of the SMs to each gave 40 clusters of 7 blocks for the 38 that
-// fit, and a second wave: 7 tokens through [16384, 14336] took 76 us for XXX.)
+// fit, and a second wave: 7 tokens through [16384, 14336] took 76 us
+// for 41.)
 template <int GROUP>
 int clusters_of(int warps, int parts) {
   cudaLaunchConfig_t cfg = {};
