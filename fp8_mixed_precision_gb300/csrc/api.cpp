@@ -1122,7 +1122,7 @@ W4Args w4_args(const void *x, int64_t T, const fp8_w4_weight &w, void *out) {
 int w4_token_blocks(int64_t T, const W4Plan &p) { return p.wide ? 1 : (int)cdiv(T, 8 * p.nt); }
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   const int tokens = (int)std::min<int64_t>(T, 1024), N = (int)(gated ? w.rows / 2 : w.rows), K = (int)w.K;
-  if (w4_is_wide(w.rows * w.K, K, tokens)) return w4_wide_plan(N, K, gated, tokens, 1, T);
+  if (w4_is_wide(w.rows * w.K, K, tokens, 1)) return w4_wide_plan(N, K, gated, tokens, 1, T);
   const W4Plan p = w4_plan(N, K, w.group, gated, tokens, 1, 1, T, false);
   const int blocks = w4_token_blocks(T, p);
   return blocks == 1 ? p : w4_plan(N, K, w.group, gated, tokens, 1, blocks, T, false);
@@ -1179,7 +1179,7 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   const int lists = (int)std::min(E, slots);
   W4Workspace w;
   const auto plan = [&](int64_t rows, int64_t in, bool gated) {
-    return w4_is_wide(rows * (gated ? 2 : 1) * in * lists, (int)in, likely)
+    return w4_is_wide(rows * (gated ? 2 : 1) * in * lists, (int)in, slots / E, lists)
                ? w4_wide_plan((int)rows, (int)in, gated, likely, lists, slots)
                : w4_plan((int)rows, (int)in, 128, gated, likely, T > 1 ? lists : 1, T > 1 ? 1 : lists, slots, !gated);
   };

@@ -261,8 +261,9 @@ struct W4Plan {
   bool wide;  // w4_wide.cu; its planes are always added after
 };
 W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined);
-// Whether w4_wide.cu takes a product of so many weights (of all lists).
-bool w4_is_wide(int64_t weights, int K, int tokens);
+// Whether w4_wide.cu takes a product of so many weights (of all lists) and tokens (of a
+// list in the mean).
+bool w4_is_wide(int64_t weights, int K, int64_t tokens, int lists);
 // The same for w4_wide.cu, and its launch: sums over the parts into a.part, x [P, K].
 W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P);
 cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st);

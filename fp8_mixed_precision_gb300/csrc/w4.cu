@@ -26,6 +26,10 @@
 // of rows (gated: one of the gate, one of the up projection) end in an exchange of
 // the warps' sums.  More ranges of K are the blocks of a cluster, which adds their
 // sums over distributed shared memory, or are summed by a second kernel (w4_plan).
+// [28672, 4096], groups of 128 without zero points, 62 MB or 8.9 us at the copy rate:
+// 13.1 us for one token (ramp and tail; 42 for four times the rows, 5.9 TB/s), 21.3 for
+// 16, where instructions bound it.  64 tokens through 32 experts [2 2048, 4096] and
+// [4096, 2048], groups of 64 with zero points, 440 MB or 65 us: 137.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -690,9 +694,14 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 }  // namespace
 
 // tcgen05 from 17 tokens on, where it saves more than its second launch and workspace
-// cost the host (6 us): 64 tokens through [28672, 4096] 88 us here and 44 there, 37
-// tokens through [2048, 512] 16.5 us a call here and 22.9 there.
-bool w4_is_wide(int64_t weights, int K, int tokens) { return tokens > 16 && K >= kChunk && weights >= 1 << 23; }
+// cost the host (6 us): 32 tokens through [28672, 4096] 44.4 us here and 39.6 there, 64
+// tokens 79 and 42, 37 tokens through [2048, 512] 16.1 us a call here and 22.9 there.
+// Lists of uneven lengths from 24 tokens on in the mean (32 experts, [2 2048, 4096] and
+// [4096, 2048]: mean 16 250 and 330, 24 339 and 361, 32 398 and 367; 8 experts of
+// [28672, 4096]: 360 and 425, 451 and 437, 520 and 441).
+bool w4_is_wide(int64_t weights, int K, int64_t tokens, int lists) {
+  return tokens >= (lists > 1 ? 24 : 17) && K >= kChunk && weights >= 1 << 23;
+}
 
 W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined) {
   W4Plan best = {};
