@@ -14,6 +14,7 @@
 // rows of 512 to 2 of 16 experts are gathered in 59 us (6.9 TB/s), 16379 of 4096 to 4 of
 // 64 in 101 (6.7); their order takes 9 and 10.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -271,24 +272,24 @@ __global__ void __launch_bounds__(kRowThreads) rows_combine_kernel(const void *_
 }
 
 // dz[row] = w dy[t] and dweights[slot] = <dy[t], z[row]>: TPT threads per token,
-// four choices at a time, so that dy is read once for up to four.  131072 x 2 x 512 takes
-// 114 us (5.9 TB/s), 16379 x 4 x 4096 175 (6.9).
-template <int TPT>
+// AT choices at a time, so that dy is read once for as many.  131072 x 2 x 512 takes
+// 101 us (6.6 TB/s), 16379 x 4 x 4096 175 (6.9).
+template <int TPT, int AT>
 __global__ void __launch_bounds__(kRowThreads) rows_combine_bwd_kernel(
     const void *__restrict__ dy, const void *__restrict__ z, const int *__restrict__ position,
     const float *__restrict__ weights, int64_t T, int vecs, int k, unsigned blocks, const int *__restrict__ counts,
     const int *__restrict__ offsets, void *__restrict__ dz, float *__restrict__ dweights) {
   constexpr int kTokens = kRowThreads / TPT, kWarps = TPT / 32;
-  __shared__ float red[kTokens][kWarps][4];
+  __shared__ float red[kTokens][kWarps][AT];
   pdl_wait_then_release();
   if (blockIdx.x >= blocks) return zero_gap(dz, vecs, blockIdx.x - blocks, counts, offsets);
   const int slot = threadIdx.x / TPT, at = threadIdx.x % TPT;
   const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    int p[4];
-    float w[4], dot[4] = {};
+  for (int j0 = 0; j0 < k; j0 += AT) {
+    int p[AT];
+    float w[AT], dot[AT] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < AT; ++j) {
       const bool in = t < T && j0 + j < k;
       p[j] = in ? position[t * k + j0 + j] : -1;
       w[j] = in ? weights[t * k + j0 + j] : 0.0f;
@@ -296,13 +297,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_combine_bwd_kernel(
     if (t < T)
       for (int c = at; c < vecs; c += TPT) {
         const uint4 d = load16(dy, t * vecs + c);
-        uint4 v[4];
+        uint4 v[AT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = p[j] >= 0 ? load16(z, (int64_t)p[j] * vecs + c) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < AT; ++j) v[j] = p[j] >= 0 ? load16(z, (int64_t)p[j] * vecs + c) : make_uint4(0, 0, 0, 0);
         const float f[8] = {bf16lo(d.x), bf16hi(d.x), bf16lo(d.y), bf16hi(d.y),
                             bf16lo(d.z), bf16hi(d.z), bf16lo(d.w), bf16hi(d.w)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < AT; ++j) {
           if (p[j] < 0) continue;
           float s = dot[j];
           s = fmaf(f[0], bf16lo(v[j].x), s); s = fmaf(f[1], bf16hi(v[j].x), s);
@@ -317,24 +318,25 @@ __global__ void __launch_bounds__(kRowThreads) rows_combine_bwd_kernel(
         }
       }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < AT; ++j)
 #pragma unroll
       for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(kFull, dot[j], o);
     if (kWarps > 1) {
       if ((at & 31) == 0)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) red[slot][at / 32][j] = dot[j];
+        for (int j = 0; j < AT; ++j) red[slot][at / 32][j] = dot[j];
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < AT; ++j) {
         dot[j] = 0.0f;
 #pragma unroll
         for (int w2 = 0; w2 < kWarps; ++w2) dot[j] += red[slot][w2][j];
       }
       __syncthreads();
     }
-    if (t < T && at < 4 && j0 + at < k)
-      dweights[t * k + j0 + at] = at == 0 ? dot[0] : at == 1 ? dot[1] : at == 2 ? dot[2] : dot[3];
+#pragma unroll
+    for (int j = 0; j < AT; ++j)
+      if (t < T && at == j && j0 + j < k) dweights[t * k + j0 + j] = dot[j];
   }
 }
 
@@ -392,7 +394,16 @@ cudaError_t launch_rows_combine_bwd(const void *dy, const void *z, const int *po
     return launch_kernel(kernel, dim3(blocks + (align > 1 ? E : 0)), dim3(kRowThreads), 0, st, dy, z, position, weights,
                          T, vecs, k, blocks, counts, offsets, dz, dweights);
   };
-  return vecs > 128 ? go(rows_combine_bwd_kernel<256>, 256) : go(rows_combine_bwd_kernel<32>, 32);
+  // One or two choices: room in registers for more tokens at once (131072 x 2 x 512 114 us
+  // with four, 101 with two).  Threads to a token: a warp walks 16-byte pieces best where
+  // tokens are many (32768 x 2 x 2048 115 us with 256, 101 with 128, 100 with 32), a block
+  // where rows are long or few (16379 x 4 x 4096 175 and 182, 37 x 4 x 4096 3.2 and 9.8).
+  const auto by_row = [&](auto at) {
+    constexpr int AT = decltype(at)::value;
+    if (vecs > 256) return go(rows_combine_bwd_kernel<256, AT>, 256);
+    return vecs > 128 ? go(rows_combine_bwd_kernel<128, AT>, 128) : go(rows_combine_bwd_kernel<32, AT>, 32);
+  };
+  return k <= 2 ? by_row(std::integral_constant<int, 2>()) : by_row(std::integral_constant<int, 4>());
 }
 
 }  // namespace fp8lin
