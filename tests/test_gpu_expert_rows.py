@@ -178,3 +178,9 @@ def test_rows_past_32_bits(fp):
     assert torch.equal(dz, xs) and torch.equal(dw[:, 0], dw[:, 1])
     want = x[-1].double().square().sum()
     assert abs(float(dw[-1, 1]) - float(want)) <= float(want) * (C / 32 + 40) * U
+
+
+@pytest.mark.parametrize("T,k,E,C", [(19, 2, 6, 2048), (33, 1, 4, 1552), (21, 2, 5, 4112), (40, 1, 3, 8192), (50, 3, 7, 1936)])
+@pytest.mark.parametrize("kind", ["random", "holes"])
+def test_moves_of_other_row_lengths(fp, T, k, E, C, kind):
+    test_moves(fp, T, k, E, C, 16, kind)
