@@ -1123,9 +1123,8 @@ int w4_token_blocks(int64_t T, const W4Plan &p) { return p.wide ? 1 : (int)cdiv(
 W4Plan w4_dense_plan(const fp8_w4_weight &w, int64_t T, bool gated) {
   const int tokens = (int)std::min<int64_t>(T, 1024), N = (int)(gated ? w.rows / 2 : w.rows), K = (int)w.K;
   if (w4_is_wide(w.rows * w.K, K, tokens, 1)) return w4_wide_plan(N, K, gated, tokens, 1, T);
-  const W4Plan p = w4_plan(N, K, w.group, gated, tokens, 1, 1, T, false);
-  const int blocks = w4_token_blocks(T, p);
-  return blocks == 1 ? p : w4_plan(N, K, w.group, gated, tokens, 1, blocks, T, false);
+  const int each = w4_block_tokens(N, K, gated, T);
+  return w4_plan(N, K, w.group, gated, std::min(tokens, each), 1, (int)cdiv(T, each), T, false);
 }
 size_t w4_dense_bytes(const fp8_w4_weight &w, int64_t T, const W4Plan &p) {
   return p.planes > 1 || p.wide ? (size_t)p.planes * T * w.rows * 4 : 0;

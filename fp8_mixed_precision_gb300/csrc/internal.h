@@ -260,6 +260,8 @@ struct W4Plan {
   int nt, parts, warps, blocks, planes;
   bool wide;  // w4_wide.cu; its planes are always added after
 };
+// Tokens of one weight that a block takes: 8, 16 or 32.
+int w4_block_tokens(int N, int K, bool gated, int64_t T);
 W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined);
 // Whether w4_wide.cu takes a product of so many weights (of all lists) and tokens (of a
 // list in the mean).

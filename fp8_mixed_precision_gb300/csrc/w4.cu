@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
         ptx::cp_async_commit();
         into = into == kStages - 1 ? 0 : into + 1;
       };
-      uint4 v[8];  // the values of one n-tile's tokens
-      const auto load_tokens = [&](int tb, int j) {
+      uint4 two[NT > 1 ? 2 : 1][8];  // the values of one n-tile's tokens, the next one's on their way
+      const auto load_tokens = [&](int tb, int j, uint4(&v)[8]) {
         const int n = tb + 8 * j + g, p = tk.first + n;
         const bool some = n < tk.count;
         const int64_t row = !some ? 0 : a.tokens ? (a.order ? a.order[p] : p) / a.k : p;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
           if (some && k0 + k + 8 * kSteps * q < a.K) v[s] = *reinterpret_cast<const uint4 *>(x + k);
         }
       };
-      load_tokens(tb, 0);
+      load_tokens(tb, 0, two[0]);
 #pragma unroll
       for (int s = 0; s < kStages - 1; ++s) request_next(s & 1);
 
@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(32 * w4_warps(NT)) w4_kernel(const W4Args a) {
       float held_sums[kGroups][2];   // their groups' sums, with one n-tile
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        if (j > 0) load_tokens(tb, j);
+        if (j + 1 < NT) load_tokens(tb, j + 1, two[(j + 1) & 1]);
+        const uint4(&v)[8] = two[j & 1];
         uint32_t top = 0u;  // largest |x| as bits, both halves
 #pragma unroll
         for (int s = 0; s < 8; ++s)
@@ -695,12 +696,25 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 
 // tcgen05 from 17 tokens on, where it saves more than its second launch and workspace
 // cost the host (6 us): 32 tokens through [28672, 4096] 44.4 us here and 39.6 there, 64
-// tokens 79 and 42, 37 tokens through [2048, 512] 16.1 us a call here and 22.9 there.
+// tokens 79 and 42, 37 tokens through [2048, 512] 4.8 and 7.0.
 // Lists of uneven lengths from 24 tokens on in the mean (32 experts, [2 2048, 4096] and
 // [4096, 2048]: mean 16 250 and 330, 24 339 and 361, 32 398 and 367; 8 experts of
 // [28672, 4096]: 360 and 425, 451 and 437, 520 and 441).
 bool w4_is_wide(int64_t weights, int K, int64_t tokens, int lists) {
   return tokens >= (lists > 1 ? 24 : 17) && K >= kChunk && weights >= 1 << 23;
+}
+
+// As few as let all blocks run within two waves (a warp to 256 of K, 16 to an SM): a
+// block with more has longer work, one with fewer reads the codes, which come from L2
+// then, once more (37 tokens through [2048, 512] 4.8 us with 8 to a block, 6.5 with 16,
+// 9.1 with 32; 12 through [4096, 4096] 6.7 with 8, 7.8 with 16; 16 through [28672, 4096]
+// 23.6 with 8, 21.9 with 16).
+int w4_block_tokens(int N, int K, bool gated, int64_t T) {
+  const int64_t per = gated ? 16 : 32, work = (N + per - 1) / per * ((K + kChunk - 1) / kChunk);
+  const int64_t two_waves = 2 * (int64_t)num_sms() * w4_warps(1);
+  int tokens = 8;
+  while (tokens < 32 && tokens < T && work * ((T + tokens - 1) / tokens) > two_waves) tokens *= 2;
+  return tokens;
 }
 
 W4Plan w4_plan(int N, int K, int group, bool gated, int tokens, int lists, int side, int64_t P, bool joined) {

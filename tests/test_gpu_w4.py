@@ -364,3 +364,20 @@ def test_experts_of_uneven_lists(fp, T, E, k, K, F, N, kind):
         want, bound = experts_product(x, choice, w, vgu, vdn, "gelu")
         assert bool(((y.double() - want).abs() <= bound + want.abs() * UB + 1e-38).all())
 
+
+
+@pytest.mark.parametrize("N,K,T", [(2048, 512, 37), (512, 512, 700), (4096, 4096, 12), (1024, 1024, 90), (2080, 2048, 30),
+                                   (48, 9216, 100)])
+@pytest.mark.parametrize("group,zero", [(32, False), (64, True), (128, True)])
+def test_blocks_of_few_tokens(fp, N, K, T, group, zero):
+    """Small weights with more tokens than a block takes: blocks of tokens side by side, the last one short."""
+    w, v = weight(fp, (N, K), group, zero, N + T)
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(T)).bfloat16()
+    out = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = fp.fp8_w4_linear(x.cuda(), w, out=out[:T]).cpu().double()
+    want, bound = product(x.double(), v)
+    assert bool(((y - want).abs() <= bound + want.abs() * UB + 1e-38).all()) and bool((out[T] == 7.0).all())
+    if N % 32 == 0:
+        h = fp.fp8_w4_gated(x.cuda(), w, "silu").cpu().double()
+        want, bound = gated(x.double(), v, "silu")
+        assert bool(((h - want).abs() <= (bound + want.abs() * UB) * 1.01 + 1e-38).all())
