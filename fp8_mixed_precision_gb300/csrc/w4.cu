@@ -27,7 +27,7 @@
 // the warps' sums.  More ranges of K are the blocks of a cluster, which adds their
 // sums over distributed shared memory, or are summed by a second kernel (w4_plan).
 // [28672, 4096], groups of 128 without zero points, 62 MB or 8.9 us at the copy rate:
-// 13.1 us for one token (ramp and tail; 39.8 for four times the rows, 6.1 TB/s), 21.3 for
+// 13.1 us for one token (ramp and tail; 39.8 for four times the rows, 6.1 TB/s), 21.8 for
 // 16, where instructions bound it.  64 tokens through 32 experts [2 2048, 4096] and
 // [4096, 2048], groups of 64 with zero points, 440 MB or 65 us: 137.
 #include <cuda_fp16.h>
