@@ -1159,6 +1159,7 @@ fp8_status w4_dense(const void *x, int64_t T, const fp8_w4_weight *w, bool gated
   return from_cuda(launch_w4_product(a, p, w4_token_blocks(T, p), cs(stream)));
 }
 struct W4Workspace {
+  bool sorted;  // the slots' order is made
   W4Plan up, down;
   int *counts, *offsets, *position, *order, *hist;
   W4List *lists;
@@ -1173,14 +1174,17 @@ W4Workspace w4_workspace(void *base, int64_t T, int k, int64_t E, int64_t K, int
   Carver c(base);
   const int64_t slots = T * k;
   const int chunks = order_chunks(slots);
-  // twice the mean, so that few experts have more tokens than a block takes at once
-  const int likely = T == 1 ? 1 : (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024);
-  const int lists = (int)std::min(E, slots);
   W4Workspace w;
+  // One token's slots stand in their own order, an expert each; of more slots than experts
+  // some experts have several (w4_is_wide, whose kernel takes the order, asks for more still).
+  w.sorted = T > 1 || k > E;
+  // twice the mean, so that few experts have more tokens than a block takes at once
+  const int likely = w.sorted ? (int)std::min<int64_t>(std::max<int64_t>(2 * slots / E, 1), 1024) : 1;
+  const int lists = (int)std::min(E, slots);
   const auto plan = [&](int64_t rows, int64_t in, bool gated) {
     return w4_is_wide(rows * (gated ? 2 : 1) * in * lists, (int)in, slots / E, lists)
                ? w4_wide_plan((int)rows, (int)in, gated, likely, lists, slots)
-               : w4_plan((int)rows, (int)in, 128, gated, likely, T > 1 ? lists : 1, T > 1 ? 1 : lists, slots, !gated);
+               : w4_plan((int)rows, (int)in, 128, gated, likely, w.sorted ? lists : 1, w.sorted ? 1 : lists, slots, !gated);
   };
   w.up = plan(F, K, true);
   w.down = plan(N, F, false);
@@ -1384,9 +1388,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
   if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
   const W4Workspace w = w4_workspace(ws, T, k, E, K, F, N);
   const int64_t slots = T * k;
-  // one token: its slots stand in their own order
-  const bool sorted = T > 1;
-  if (sorted) {
+  if (w.sorted) {
     st = from_cuda(launch_expert_order(experts, slots, (int)E, 1, w.counts, w.offsets, w.position, w.order, w.hist,
                                        cs(stream), w.lists, w.most, w.tile));
     if (st != FP8_OK) return st;
@@ -1404,12 +1406,12 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
     a.x = w.xs;
     a.tokens = 0;
   }
-  const int lists = (int)(sorted ? std::min(E, slots) : slots);
+  const int lists = (int)std::min(E, slots);
   for (W4Args *p : {&a, &b}) {
     p->experts = experts;
     p->k = k;
     p->P = (int)slots;
-    if (sorted) {
+    if (w.sorted) {
       p->order = w.order;
       p->offsets = w.offsets;
       p->counts = w.counts;
@@ -1418,7 +1420,7 @@ fp8_status fp8_w4_experts(const void *x, int64_t T, int k, const float *weights,
     st = from_cuda(launch_w4_product(*p, p == &a ? w.up : w.down, lists, cs(stream)));
     if (st != FP8_OK) return st;
   }
-  return from_cuda(launch_w4_join(w.z, experts, sorted ? w.position : nullptr, weights, T, N, k, (int)E, w.down.planes,
+  return from_cuda(launch_w4_join(w.z, experts, w.sorted ? w.position : nullptr, weights, T, N, k, (int)E, w.down.planes,
                                   y, cs(stream)));
 }
 

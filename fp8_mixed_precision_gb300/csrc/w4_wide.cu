@@ -458,6 +458,7 @@ W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P) 
 
 cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st) {
   CUtensorMap tm;
+  if (a.experts && !a.order) return cudaErrorInvalidValue;  // the kernel takes rows in the experts' order
   if (!make_bf16_slab_map(&tm, const_cast<void *>(a.x), a.P, a.K)) return cudaErrorInvalidValue;
   return p.nt == 4 ? by_group<32>(a, tm, p, lists, st) : by_group<64>(a, tm, p, lists, st);
 }
