@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
         }
       // twice the fp32 error of a score, in units of roundoff: of s, 8 (sigmoid:
       // exponential, sum, quotient) or 8 and half the terms of a lane's and the lanes'
-      // sum; of the addition, 1
+      // sum; of the addition, 1.  Scores below the smallest normal number, 2^-126, may have
+      // become 0 (a row whose sigmoids all underflow, with a bias of zeros: all alike here)
       if (GENERAL) {
         tol = (a.sigmoid ? 16.0f : 16.0f + kOwn + 6) * 0x1p-24f * max_over<LANES>(smax) +
-              0x1p-23f * (cmax = max_over<LANES>(cmax));
+              0x1p-23f * (cmax = max_over<LANES>(cmax)) + 0x1p-125f;
         top_score = cmax;
       }
     }

@@ -482,7 +482,8 @@ fp8_status fp8_grad_norm(const fp8_grad_clip *plan, const void *table, float *no
  *   experts = the k largest c left, in descending order
  *   w_j = scale * s_j / sum of the chosen s (renormalize), else scale * s_j
  * Ties go to the lowest index, of groups and of experts; the order is that of the
- * exact scores (decided in fp64 where fp32 could err).  An expert whose logit or
+ * exact scores (decided in fp64 where fp32 could err; with a bias, and between sums of
+ * two, scores that are equal in fp64 are ties).  An expert whose logit or
  * bias is -inf is never chosen; slots left over get expert -1 and weight 0, so a
  * row of -inf (a padding token) has no expert.  A row with a NaN score (a NaN
  * logit or bias, or +inf under softmax) gets experts -1 and weights NaN.
