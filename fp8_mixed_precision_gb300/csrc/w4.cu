@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict
   }
   const float top = fmaxf(hi, -lo);
   float s = zero ? __fdiv_rn(hi - lo, 15.0f) : __fdiv_rn(top, 7.0f);
-  if (!(fabsf(s) < INFINITY)) s = 3.0e38f;  // hi - lo past fp32's range
+  if (s == INFINITY) s = __fdiv_rn(0.5f * hi - 0.5f * lo, 7.5f);  // hi - lo past fp32's range, halves are exact
   s = __bfloat162float(__float2bfloat16_rn(s));
   if (s == 0.0f) s = 1.0f;
   float z = 8.0f;
