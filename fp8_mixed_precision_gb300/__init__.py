@@ -21,7 +21,7 @@ __all__ = [
     "fp8_quantize", "fp8_scale_shape", "fp8_gemm", "fp8_linear_fwd", "fp8_linear_bwd",
     "fp8_gelu_fwd", "fp8_gelu_bwd", "fp8_grad_accumulate", "fp8_get_device_status",
     "fp8_launch_count", "fp8_profile_begin", "fp8_profile_end", "WeightCache", "LinearContext",
-    "fp8_quantize_delayed", "fp8_debug_wait_timeout", "fp8_debug_wait_together", "HostPipeline", "amax_partials_buffer",
+    "fp8_quantize_delayed", "fp8_debug_wait_timeout", "HostPipeline", "amax_partials_buffer",
     "fp8_amax_partials", "fp8_linear_fwd_after_amax", "fp8_linear_bwd_after_amax",
     "ACTIVATION", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "rmsnorm_buffers", "rmsnorm_workspace",
     "fp8_gated_fwd", "fp8_gated_fwd_quantized", "fp8_gated_bwd", "GatedContext", "gated_context",
@@ -79,7 +79,6 @@ _SIGS = {
     "fp8_get_device_status": (_c_int, [_c_p]),
     "fp8_profile_begin": (_c_int, []),
     "fp8_debug_wait_timeout": (_c_int, [ctypes.c_uint64, _c_p]),
-    "fp8_debug_wait_together": (_c_int, [ctypes.c_uint64, _c_p, _c_p]),
     "fp8_quantize_delayed": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p,
                                       ctypes.c_int32, _c_i64, _c_p, _c_sz, _c_p]),
     "fp8_weight_cache_register_delayed": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p,
@@ -556,15 +555,6 @@ def fp8_profile_end(by_shape: bool = False) -> list:
 def fp8_debug_wait_timeout(limit_ns: int, stream=None):
     """Enqueue the bounded-wait probe (a wait that nothing satisfies)."""
     _check(lib().fp8_debug_wait_timeout(int(limit_ns), _stream(stream)), "fp8_debug_wait_timeout")
-
-
-def fp8_debug_wait_together(limit_ns: int, device="cuda", stream=None) -> torch.Tensor:
-    """Failure-detection test hook: what the lanes of a warp that wait together
-    were told (int32 [32], the same for all) where half of them run out of time."""
-    with _on(stream):
-        answers = torch.empty(32, dtype=torch.int32, device=device)
-    _check(lib().fp8_debug_wait_together(int(limit_ns), answers.data_ptr(), _stream(stream)), "fp8_debug_wait_together")
-    return answers
 
 
 class QuantizedTensor:

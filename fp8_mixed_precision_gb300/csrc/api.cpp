@@ -1631,12 +1631,6 @@ fp8_status fp8_debug_wait_timeout(uint64_t limit_ns, fp8_stream_t stream) {
   return from_cuda(launch_wait_timeout_probe(limit_ns, cs(stream)));
 }
 
-fp8_status fp8_debug_wait_together(uint64_t limit_ns, int32_t *answers, fp8_stream_t stream) {
-  if (limit_ns == 0 || limit_ns > 50000000ull || !answers) return FP8_ERR_INVALID_ARG;
-  if (!words_aligned({answers})) return FP8_ERR_ALIGN;
-  return from_cuda(launch_wait_together_probe(limit_ns, answers, cs(stream)));
-}
-
 fp8_status fp8_get_device_status(fp8_stream_t stream) {
   unsigned s = 0, q = 0, n = 0, g = 0, w = 0;
   if (gemm_read_status(&s, cs(stream)) != cudaSuccess) return FP8_ERR_CUDA;

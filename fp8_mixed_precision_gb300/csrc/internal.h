@@ -130,8 +130,6 @@ cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const 
                         int scaling, void *C, void *ws, cudaStream_t st, int64_t a_rows = 0);
 // Launches the bounded-wait probe (a wait nobody satisfies; limit_ns <= 1 s).
 cudaError_t launch_wait_timeout_probe(uint64_t limit_ns, cudaStream_t st);
-// Test hook (w4_wide.cu): what 32 lanes that wait together were told, as 0 or 1.
-cudaError_t launch_wait_together_probe(uint64_t limit_ns, int *answers, cudaStream_t st);
 // Reads and clears the GEMM kernels' device status word (0 = ok).
 cudaError_t gemm_read_status(unsigned *status, cudaStream_t st);
 

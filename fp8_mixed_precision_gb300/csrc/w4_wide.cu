@@ -145,10 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_then_release();
   const uint32_t tmem = ctl->tmem_base, acc0 = tmem + kStages * kColsA;
   volatile int *abort = &ctl->abort;
-  const unsigned lanes = warp < 2 ? 0u : 0xffffffffu;  // warps 0 and 1 wait with one lane
-  const auto wait = [&](uint64_t *bar, uint32_t parity) {
-    return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status, lanes);
-  };
+  const auto wait = [&](uint64_t *bar, uint32_t parity) { return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status); };
   const Tokens tk = a.experts ? Tokens{(int)blockIdx.y, a.offsets[blockIdx.y], a.counts[blockIdx.y]} : Tokens{0, 0, a.T};
   const int per = a.gated ? 64 : 128, tiles = (a.N + per - 1) / per, units = tiles * parts;
   const int kbs = (a.K + kDepth - 1) / kDepth;
@@ -411,29 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Failure-detection test hook: the lanes of warp 0 wait together for a phase that warp 1
-// ends after four times limit_ns, the even lanes for limit_ns at most, the odd ones for
-// sixteen times as long, none told of another's giving up.
-__global__ void wait_together_probe_kernel(uint64_t limit_ns, int *__restrict__ answers) {
-  __shared__ uint64_t bar;
-  __shared__ int abort[32];
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(&bar, 1);
-    ptx::fence_mbar_init();
-  }
-  if (threadIdx.x < 32) abort[threadIdx.x] = 0;
-  __syncthreads();
-  pdl_wait_then_release();
-  if (threadIdx.x < 32) {
-    answers[threadIdx.x] = pipe::wait_bar(&bar, 0, &abort[threadIdx.x], &g_w4_wide_status, 0xffffffffu,
-                                          threadIdx.x & 1 ? 16 * limit_ns : limit_ns);
-  } else if (threadIdx.x == 32) {
-    const uint64_t t0 = ptx::globaltimer();
-    while (ptx::globaltimer() - t0 < 4 * limit_ns) __nanosleep(1000);
-    ptx::mbar_arrive(&bar);
-  }
-}
-
 template <int TN, int GROUP>
 cudaError_t launch_wide(const W4Args &a, const CUtensorMap &tm, const W4Plan &p, int lists, cudaStream_t st) {
   static bool set[64] = {};
@@ -487,11 +461,6 @@ cudaError_t launch_w4_wide(const W4Args &a, const W4Plan &p, int lists, cudaStre
   if (a.experts && !a.order) return cudaErrorInvalidValue;  // the kernel takes rows in the experts' order
   if (!make_bf16_slab_map(&tm, const_cast<void *>(a.x), a.P, a.K)) return cudaErrorInvalidValue;
   return p.nt == 4 ? by_group<32>(a, tm, p, lists, st) : by_group<64>(a, tm, p, lists, st);
-}
-
-cudaError_t launch_wait_together_probe(uint64_t limit_ns, int *answers, cudaStream_t st) {
-  LaunchScope ls("wait_together_probe", st, 128.0, 0.0);
-  return launch_kernel(wait_together_probe_kernel, dim3(1), dim3(64), 0, st, limit_ns, answers);
 }
 
 cudaError_t w4_wide_read_status(unsigned *status) {

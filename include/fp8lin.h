@@ -719,11 +719,6 @@ fp8_status fp8_get_device_status(fp8_stream_t stream);
  * status word and returns (no trap; the context stays usable).  Read the
  * outcome with fp8_get_device_status.  Errors: INVALID_ARG, CUDA. */
 fp8_status fp8_debug_wait_timeout(uint64_t limit_ns, fp8_stream_t stream);
-/* The same for lanes of a warp that wait together: half of them for limit_ns (1 .. 5e7),
- * half for sixteen times as long, on a barrier that completes after four times limit_ns.
- * answers: device int32 [32], 1 for a lane that was told that it had completed; all
- * lanes are told the same (0).  Errors: INVALID_ARG, ALIGN, CUDA. */
-fp8_status fp8_debug_wait_together(uint64_t limit_ns, int32_t *answers, fp8_stream_t stream);
 
 #ifdef __cplusplus
 }
