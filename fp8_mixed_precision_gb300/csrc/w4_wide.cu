@@ -146,6 +146,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base, acc0 = tmem + kStages * kColsA;
   volatile int *abort = &ctl->abort;
   const auto wait = [&](uint64_t *bar, uint32_t parity) { return pipe::wait_bar(bar, parity, abort, &g_w4_wide_status); };
+  // Warps 0 and 1 wait with one lane, and leave when a wait gives up.  The others wait with
+  // all: a lane whose wait gave up is `lost` and goes on with the rest of its warp (numbers
+  // that are then wrong, at addresses that are not), since TMEM's loads and stores are
+  // instructions of all lanes and another lane may have seen the phase end after all.  A unit
+  // later the warp leaves as one.
   const Tokens tk = a.experts ? Tokens{(int)blockIdx.y, a.offsets[blockIdx.y], a.counts[blockIdx.y]} : Tokens{0, 0, a.T};
   const int per = a.gated ? 64 : 128, tiles = (a.N + per - 1) / per, units = tiles * parts;
   const int kbs = (a.K + kDepth - 1) / kDepth;
@@ -234,29 +239,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       return bf16lo(a.scale[((int64_t)tk.e * a.rows + row_of(un)) * a.groups + un.kb0 * kGroups]);
     };
     uint32_t nacc = 0;
-    bool ok = true;
+    bool lost = false;
     float ahead = 0.0f;  // the next unit's first scale, a round trip to memory before its use
     if (tk.count > 0 && (int)blockIdx.x < units) ahead = first_scale(unit_of(blockIdx.x, parts, kbs, per_part));
-    for (int tb = 0; ok && tb < tk.count; tb += TN)
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        __syncwarp();
+    for (int tb = 0; tb < tk.count; tb += TN)
+      for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        if (__any_sync(0xffffffffu, lost)) break;
         const Unit un = unit_of(u, parts, kbs, per_part);
         const int out = un.tile * per + (a.gated ? row & 63 : row), wrow = row_of(un);
         const uint16_t *scale = a.scale + ((int64_t)tk.e * a.rows + wrow) * a.groups;
         float tot[TN] = {};
         float next = ahead;
         ahead = first_scale(unit_of(u + gridDim.x < units ? u + gridDim.x : blockIdx.x, parts, kbs, per_part));
-        for (int kb = un.kb0; ok && kb < un.kb0 + un.kbs; ++kb)
+        for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb)
 #pragma unroll 1
           for (int g = kb * kGroups; g < (kb + 1) * kGroups; ++g) {
             const float s = next;
             // (groups past the last one are products with zeros)
             next = bf16lo(scale[min(g + 1, a.groups - 1)]);
             const uint32_t ab = nacc % kAcc;
-            if (!wait(&ctl->acc_full[ab], nacc / kAcc & 1)) {
-              ok = false;
-              break;
-            }
+            lost = lost || !wait(&ctl->acc_full[ab], nacc / kAcc & 1);
             ptx::tc_fence_after();
 #pragma unroll
             for (int i = 0; i < TN; i += 32) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++nacc;
           }
-        if (!ok || out >= a.N) continue;
+        if (lost || out >= a.N) continue;
         // a part's sums: token by token, 32 rows at a time
         float *to = static_cast<float *>(a.part) + ((int64_t)un.part * a.P + tk.first + tb) * a.rows + wrow;
         const int count = min(TN, tk.count - tb);
@@ -355,9 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kColsA / 2);
     int stage = 0, held = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int tb = 0; ok && tb < tk.count; tb += TN)
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    bool lost = false;
+    for (int tb = 0; tb < tk.count; tb += TN)
+      for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        if (__any_sync(0xffffffffu, lost)) break;
         const Unit un = unit_of(u, parts, kbs, per_part);
         const int64_t zero = (first_row(un.tile, lane >> 4) + (lane & 15)) * a.groups;
         for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
@@ -383,10 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[4 * i + j] = two_codes(word, j, zz[i >> 2], mask, bias);
           }
-          if (!wait(&ctl->a_empty[stage], phase ^ 1)) {
-            ok = false;
-            break;
-          }
+          lost = lost || !wait(&ctl->a_empty[stage], phase ^ 1);
           __syncwarp();
           ptx::tc_fence_after();
           tmem_st32(ta + stage * kColsA, r);
