@@ -1114,7 +1114,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 template <typename Kernel>
-cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
+cudaError_t opt_in_smem(Kernel kernel, size_t bytes, std::atomic<bool> *done) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1128,7 +1128,7 @@ cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
 template <int SCALING, int ACT, bool SAVE>
 cudaError_t launch_fwd(const CUtensorMap (&m)[5], const GatedArgs &g, cudaStream_t st) {
   using C = GCfg;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = opt_in_smem(gated_fwd_kernel<SCALING, ACT, SAVE>, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(g.units, num_sms());
@@ -1159,7 +1159,7 @@ cudaError_t launch_small(const uint8_t *xq, const uint8_t *wq, int64_t K, SmallA
   a.ring_bytes = std::max(a.stages * stage_bytes + own, 2 * NT * BF * 4);
   a.idesc = ptx::idesc_f8f6f4(FP8_FORMAT_E4M3, FP8_FORMAT_E4M3, BM, NT);
   auto kernel = gated_small_kernel<SCALING, ACT, NT>;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = opt_in_smem(kernel, kSmallSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1198,7 +1198,7 @@ cudaError_t launch_cast_block(const GatedBwd &p, cudaStream_t st) {
       !make_bf16_tile_map(&m[1], p.g, p.N, p.F, 128, 128) ||
       !make_bf16_tile_map(&m[2], p.u, p.N, p.F, 128, 128))
     return cudaErrorInvalidValue;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = opt_in_smem(gated_bwd_cast_kernel<ACT>, sizeof(BSmem), done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((p.N + 127) / 128) * (p.F / 128);
@@ -1210,7 +1210,7 @@ cudaError_t launch_cast_block(const GatedBwd &p, cudaStream_t st) {
 
 // A grid of the kernel's resident CTAs, or as many as n8 vectors fill.
 template <typename Kernel>
-int64_t vector_grid(Kernel kernel, int threads, int64_t n8, int *bps) {
+int64_t vector_grid(Kernel kernel, int threads, int64_t n8, std::atomic<int> *bps) {
   const int64_t resident = (int64_t)blocks_per_sm(kernel, threads, bps) * num_sms();
   return std::max<int64_t>(1, std::min<int64_t>((n8 + threads - 1) / threads, resident));
 }
@@ -1218,7 +1218,7 @@ int64_t vector_grid(Kernel kernel, int threads, int64_t n8, int *bps) {
 template <int ACT>
 cudaError_t launch_cast_tensor(GatedBwd p, float *partials, cudaStream_t st) {
   const int64_t n8 = p.N * p.F / 8;
-  static int amax_bps[64], cast_bps[64];
+  static std::atomic<int> amax_bps[64], cast_bps[64];
   p.n_partials = (int)std::min<int64_t>(
       vector_grid(gated_bwd_amax_kernel<ACT>, kAmaxThreads, n8, amax_bps), kMaxPartials);
   {

@@ -993,14 +993,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> known{nullptr};
+  EncodeTiledFn fn = known;
   if (!fn) {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
                                          &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+      known = fn = reinterpret_cast<EncodeTiledFn>(p);
   }
   return fn;
 }
@@ -1138,7 +1139,7 @@ cudaError_t launch_variant(const CUtensorMap &ta, const CUtensorMap &tb, const C
   cfg.numAttrs = PR ? 1 : 0;  // the occupancy query below sees the cluster shape only
   // per device: the shared-memory opt-in, and how many CTAs can be resident
   // at once (whole clusters for pairs), which sizes the persistent grid
-  static int resident[64] = {0};
+  static std::atomic<int> resident[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1299,7 +1300,7 @@ cudaError_t launch_gemm(const uint8_t *A, int a_fmt, const float *a_sinv, const 
   }
   if (e != cudaSuccess || !split) return e;
   const int64_t mn = M * N;
-  static int reduce_bps[64];
+  static std::atomic<int> reduce_bps[64];
   const int64_t blocks = std::min<int64_t>(
       (mn / 4 + 255) / 256, (int64_t)num_sms() * blocks_per_sm(splitk_reduce_kernel, 256, reduce_bps));
   LaunchScope ls("gemm_splitk_reduce", st, 4.0 * p.splits * mn + 2.0 * mn, (double)p.splits * mn, M, N,

@@ -79,12 +79,12 @@ __global__ void grad_accumulate_kernel(float4 *__restrict__ acc, const uint2 *__
 // the occupancy calculator, per kernel and device), so that no block starts
 // after the others have finished their grid-stride share.
 template <typename Kernel>
-unsigned grid_resident(Kernel kernel, int64_t items, int *per_dev) {
+unsigned grid_resident(Kernel kernel, int64_t items, std::atomic<int> *per_dev) {
   const int bps = blocks_per_sm(kernel, kThreads, per_dev);
   const int64_t want = (items + kThreads - 1) / kThreads;
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)num_sms() * bps));
 }
-int g_gelu_fwd_bps[64], g_gelu_bwd_bps[64], g_acc_bps[64];
+std::atomic<int> g_gelu_fwd_bps[64], g_gelu_bwd_bps[64], g_acc_bps[64];
 
 }  // namespace
 

@@ -7,6 +7,7 @@
 #include <stdint.h>
 #include <stddef.h>
 #include <algorithm>
+#include <atomic>
 
 namespace fp8lin {
 
@@ -49,7 +50,7 @@ bool pdl_enabled();
 // launch the blocks are placed on SMs in the order the previous kernel frees
 // them, and a smaller grid would crowd onto the first SMs freed.
 template <typename Kernel>
-int blocks_per_sm(Kernel kernel, int threads, int *per_dev) {
+int blocks_per_sm(Kernel kernel, int threads, std::atomic<int> *per_dev) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return 1;

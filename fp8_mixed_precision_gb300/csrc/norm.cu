@@ -654,7 +654,7 @@ int row_warps(int64_t C, int vpt) {
 }
 
 template <typename Kernel>
-cudaError_t opt_in_smem(Kernel kernel, size_t bytes, bool *done) {
+cudaError_t opt_in_smem(Kernel kernel, size_t bytes, std::atomic<bool> *done) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -683,7 +683,7 @@ cudaError_t launch_rows(const NormFwd &a, cudaStream_t st) {
 template <int VPT, int WPR>
 cudaError_t launch_bwd(NormBwd a, int grid, cudaStream_t st) {
   constexpr int kWarps = ring_warps(WPR);
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = opt_in_smem(rmsnorm_bwd_kernel<VPT, WPR>, kRingSmem<WPR>, done);
   if (e != cudaSuccess) return e;
   const int stages = ring_stages(kRingSmem<WPR>, kWarps / WPR, a.C, 3);
@@ -731,7 +731,7 @@ cudaError_t launch_rmsnorm_cols(const void *r, const float *rstd, const float *r
                                 float *col_scale_inv, cudaStream_t st) {
   CUtensorMap tm;
   if (!make_bf16_tile_map(&tm, r, rows, cols, 128, kColTile)) return cudaErrorInvalidValue;
-  static bool attr_set[64] = {false};
+  static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {

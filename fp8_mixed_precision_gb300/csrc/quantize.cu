@@ -578,7 +578,7 @@ bool pdl_enabled() {
 }
 
 int num_sms() {
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return 148;
@@ -590,7 +590,7 @@ int num_sms() {
   return cached[dev];
 }
 
-static int g_amax_bps[64];
+static std::atomic<int> g_amax_bps[64];
 
 int tensorwise_partials_count(int64_t rows, int64_t cols) {
   const int64_t n16 = rows * cols / 8;
@@ -612,7 +612,7 @@ static cudaError_t launch_tile(const QParams &p, cudaStream_t st) {
   }
   static const char *names[3] = {"quant_cast_tensorwise", "quant_block_1x128", "quant_block_128x128"};
   static const char *pre_names[3] = {"", "gelu_quant_block_1x128", "gelu_bwd_quant_block_1x128"};
-  static bool attr_set[64] = {false};
+  static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {

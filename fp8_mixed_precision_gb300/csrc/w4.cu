@@ -613,7 +613,7 @@ constexpr size_t w4_bytes(int warps) {
 }
 template <int NT, int GROUP, bool ZERO>
 cudaError_t allow_bytes() {
-  static bool set[64] = {};
+  static std::atomic<bool> set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && set[dev]) return cudaSuccess;

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int TN, int GROUP>
 cudaError_t launch_wide(const W4Args &a, const CUtensorMap &tm, const W4Plan &p, int lists, cudaStream_t st) {
-  static bool set[64] = {};
+  static std::atomic<bool> set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
