@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(GCfg::kThreads, 1)
       };
       if constexpr (kTensor) {
         const uint32_t ab = nacc & 1;
-        if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) break;
+        if (__any_sync(0xffffffffu, !wait(&ctl->acc_full[ab], (nacc >> 1) & 1))) break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -331,7 +331,10 @@ __global__ void __launch_bounds__(GCfg::kThreads, 1)
         const float *xrow = g.x_sinv + (m < g.N ? m : g.N - 1) * g.lds;
         const float *wg = g.w_sinv + (int64_t)tf * g.lds;  // F is a multiple of 128
         const float *wu = wg + (g.F / BF) * g.lds;
-        bool ok = true;
+        // No lane leaves at a wait that gave up: TMEM loads are instructions of the whole
+        // warp, and another lane may have seen the phase end after all.  The warp leaves as
+        // one, by the abort flag, before it stores.  (A vote at each wait: 16384 x 4096 x
+        // 14336 1833 us for 1457.)
         float xs = xrow[0], gs = wg[0], us = wu[0];
         for (int kb = 0; kb < g.kbs; ++kb) {
           const uint32_t ab = nacc & 1;
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(GCfg::kThreads, 1)
             gs = wg[kb + 1];
             us = wu[kb + 1];
           }
-          if (!wait(&ctl->acc_full[ab], (nacc >> 1) & 1)) { ok = false; break; }
+          wait(&ctl->acc_full[ab], (nacc >> 1) & 1);
           ptx::tc_fence_after();
           // 16 columns at a time, G then U (loads kept in flight across chunks or
           // K blocks measured no faster: 1815 against 1787 us, and slower)
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(GCfg::kThreads, 1)
           }
           ++nacc;
         }
-        if (!ok) break;
+        if (__any_sync(0xffffffffu, *abort)) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float G[32], U[32];
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     for (int i = 0; i < uses; ++i) {
       const uint32_t ab = i & 1;
       const uint64_t ws = kTensor ? 0 : dup(wsc[a.split * i]);
-      if (!wait(&ctl->acc_full[ab], (i >> 1) & 1)) break;
+      wait(&ctl->acc_full[ab], (i >> 1) & 1);  // one that gave up: wrong sums, a warp still together
       ptx::tc_fence_after();
 #pragma unroll
       for (int c = 0; c < NT; c += 16) {

@@ -174,7 +174,8 @@ struct GemmArgs {
 };
 
 
-// Bounded wait on phase `parity` of `bar`; false on abort or timeout.
+// Bounded wait on phase `parity` of `bar`; false on abort or timeout, the abort flag then
+// being set.  (A probe of a phase that does not end takes about 4 us.)
 // CLUSTER: the barrier's arrivals may come from the other CTA of a pair.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
@@ -185,7 +186,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (probe()) return true;
-    if ((it & 63) == 0) {
+    if ((it & 7) == 0) {
       if (*abort) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
         atomicCAS(&g_gemm_status, 0u, (unsigned)FP8_ERR_TIMEOUT);
@@ -567,6 +568,10 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
     uint32_t nacc = 0;
     uint32_t ngrp = 0;  // scale-ring slots consumed (wide 1x128 x 1x128 tiles)
     uint32_t nout = 0;  // bf16 slabs this warp has handed to TMA stores
+    // Within a unit no lane leaves at a wait that gave up: TMEM loads are instructions of the
+    // whole warp, and another lane may have seen the phase end after all.  The sums are then
+    // wrong; the warp leaves as one, by the abort flag, before it stores them.  (A vote at
+    // each K block's wait took 1.7% of a 16384 x 14336 x 4096 backward pass, this nothing.)
     uint8_t *slabs = out_stage + (size_t)ew * C::kOutSlabs * C::kOutSlabBytes;
     float s_tensor = 0.0f;
     if (SCALING == FP8_SCALING_TENSOR) s_tensor = __fmul_rn(g.a_sinv[0], g.b_sinv[0]);
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
         for (int mh = 0; mh < MH; ++mh) {  // one accumulator buffer per M half
           const int64_t slab_y = slab_y0 + (int64_t)mh * BM;
           const uint32_t ab = nacc % NB, aph = (nacc / NB) & 1;
-          if (!wait_bar<PR>(&ctl->acc_full[ab], aph, abort)) { ok = false; break; }
+          if (__any_sync(0xffffffffu, !wait_bar<PR>(&ctl->acc_full[ab], aph, abort))) { ok = false; break; }
           ptx::tc_fence_after();
 #pragma unroll
           for (int s = 0; s < kSlabs; ++s) {
@@ -653,17 +658,16 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
         uint64_t acc[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[j] = 0;
-        bool ok = true;
-        for (int g0 = kb0; ok && g0 < kb1; g0 += kScaleGroup) {
+        for (int g0 = kb0; g0 < kb1; g0 += kScaleGroup) {
           const uint32_t slot = ngrp % kScaleSlots;
-          if (!wait_bar(&ctl->sfull[slot], (ngrp / kScaleSlots) & 1, abort)) { ok = false; break; }
+          wait_bar(&ctl->sfull[slot], (ngrp / kScaleSlots) & 1, abort);
           const float *srow = scale_ring + slot * kScaleSlotFloats + q * 32 + rr;
           const float *scol = scale_ring + slot * kScaleSlotFloats + BM + h * 64 + 2 * cc;
 #pragma unroll 1
           for (int kk = 0; kk < kScaleGroup; ++kk) {
             if (g0 + kk >= kb1) break;
             const uint32_t ab = nacc % NB, aph = (nacc / NB) & 1;
-            if (!wait_bar<PR>(&ctl->acc_full[ab], aph, abort)) { ok = false; break; }
+            wait_bar<PR>(&ctl->acc_full[ab], aph, abort);
             ptx::tc_fence_after();
             uint64_t sb[8];  // column-scale pairs of this thread's 8 column pairs
 #pragma unroll
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
           if (lane == 0) ptx::mbar_arrive(&ctl->sempty[slot]);
           ++ngrp;
         }
-        if (!ok) break;
+        if (__any_sync(0xffffffffu, *abort)) break;
         // results straight from registers (once per tile): rows
         // slab_y0 + rr + 8i, columns colbase + 8k + 2cc and +1 (N is a multiple
         // of 16, so n < N covers n + 1)
@@ -736,7 +740,6 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
         const float *bt = g.b_sinv + (int64_t)btile * g.lds_b;
         // Scales of K blocks kb .. kb+kPre-1 in a register ring (slot 0 = current):
         // the loads are issued kPre blocks before their use, hiding their latency.
-        bool ok = true;
         if constexpr (SCALING == FP8_SCALING_1x128_1x128) {
           // Every element's scale is (row scale) x (column scale) of its K
           // block.  The partial is read with the 16x256b TMEM shape: thread
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
             ptx::cp_async_commit();
           };
           fetch(kb0);
-          for (int g0 = kb0; ok && g0 < kb1; g0 += 4) {
+          for (int g0 = kb0; g0 < kb1; g0 += 4) {
             ptx::cp_async_wait_all();
             const float4 bv = stg[lane], av = stg[32 + lane];  // this lane's own slots
             if (g0 + 4 < kb1) fetch(g0 + 4);
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
             for (int kk = 0; kk < 4; ++kk) {
               if (g0 + kk >= kb1) break;
               const uint32_t ab = nacc % NB, aph = (nacc / NB) & 1;
-              if (!wait_bar<PR>(&ctl->acc_full[ab], aph, abort)) { ok = false; break; }
+              wait_bar<PR>(&ctl->acc_full[ab], aph, abort);
               ptx::tc_fence_after();
               uint64_t sb[4];  // column-scale pairs of this thread's 4 column pairs
 #pragma unroll
@@ -846,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
             rb[i] = rb[i + 1];
           }
           load_scales(kb + kPre, ra[kPre - 1], rb[kPre - 1]);
-          if (!wait_bar<PR>(&ctl->acc_full[ab], aph, abort)) { ok = false; break; }
+          wait_bar<PR>(&ctl->acc_full[ab], aph, abort);
           ptx::tc_fence_after();
           const uint64_t st2 = pk(__fmul_rn(sa_cur, sbt_cur), __fmul_rn(sa_cur, sbt_cur));
 #pragma unroll
@@ -870,7 +873,7 @@ __global__ void __launch_bounds__(Cfg<SCALING, SPLIT, BN, MH, PR>::kThreads, 1)
           ++nacc;
         }
         }
-        if (!ok) break;
+        if (__any_sync(0xffffffffu, *abort)) break;
         if constexpr (SCALING == FP8_SCALING_1x128_1x128) {
           // rows slab_y + rr + 8i, columns colbase + 8j + 2cc and +1
           const int rr = lane >> 2, cc = lane & 3;

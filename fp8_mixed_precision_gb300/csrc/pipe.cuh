@@ -13,14 +13,14 @@ namespace pipe {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr uint64_t kDrainLimitNs = 100000000ull;  // 0.1 s
 
-// Wait for phase `parity` of `bar`; false on abort or timeout.
+// Wait for phase `parity` of `bar`; false on abort or timeout, the abort flag then being set.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          unsigned *status) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 0) {
+    if ((it & 63) == 1) {
       if (*abort) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
         atomicCAS(status, 0u, (unsigned)FP8_ERR_TIMEOUT);

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (groups past the last one are products with zeros)
             next = bf16lo(scale[min(g + 1, a.groups - 1)]);
             const uint32_t ab = nacc % kAcc;
-            lost = lost || !wait(&ctl->acc_full[ab], nacc / kAcc & 1);
+            lost |= !wait(&ctl->acc_full[ab], nacc / kAcc & 1);
             ptx::tc_fence_after();
 #pragma unroll
             for (int i = 0; i < TN; i += 32) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[4 * i + j] = two_codes(word, j, zz[i >> 2], mask, bias);
           }
-          lost = lost || !wait(&ctl->a_empty[stage], phase ^ 1);
+          lost |= !wait(&ctl->a_empty[stage], phase ^ 1);
           __syncwarp();
           ptx::tc_fence_after();
           tmem_st32(ta + stage * kColsA, r);
