@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[c][q] *= f;
+      for (int q = 0; q < 4; ++q) v[c][q] = f == 0.0f ? 0.0f : v[c][q] * f;  // (v is NaN at a logit of +inf)
   } else {
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
