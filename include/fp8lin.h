@@ -34,6 +34,7 @@
  *     dimension need not be a multiple of 128: the last 128-block of a row,
  *     column or tile is then shorter ("ragged tail") and its amax covers the
  *     elements present.  A zero dimension makes the call a no-op (FP8_OK).
+ *     An output overlaps no other tensor of its call unless the call says so.
  *     Routing takes any number of tokens and experts; 4-bit weights say theirs.
  *     The norm and the gated feed-forward take any number of tokens; their
  *     transposed FP8 layouts have rows of the token count rounded up to a
@@ -52,8 +53,8 @@
  *   - Calls are not thread-safe with respect to one fp8_weight_cache object.
  *     Other calls may come from several host threads: the per-device launch
  *     settings the library fills in on first use (shared-memory opt-in,
- *     resident CTA counts, SM count) are idempotent, so concurrent first
- *     calls store the same values.  The kernel timing of fp8_profile_begin /
+ *     resident CTA counts, SM count) are atomic and the same for every
+ *     caller.  The kernel timing of fp8_profile_begin /
  *     fp8_profile_end and the launch counter are process-wide.
  *
  * Recipes
@@ -554,7 +555,8 @@ fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int6
  *   codes  device u8 [E, rows, K / 2]: the even k in the low four bits
  *   scale  device bf16 [E, rows, ceil(K / group)]
  *   zero   device u8, of the same shape, 0 .. 15; NULL: 8
- *   rows a multiple of 16, K of 32
+ *   rows a multiple of 16, K of 32 (products over no K at all are zeros, but
+ *   fp8_w4_experts wants K and F of 32 and more: SHAPE)
  * Products are exact but for values of x under 2^-27 of the largest of their 256
  * neighbours (k to k + 255, k a multiple of 256), which may be taken within 2^-34 of
  * that one; sums are fp32.  The products of a token with an infinity or a NaN are not
@@ -572,7 +574,8 @@ fp8_status fp8_expert_combine_bwd(const void *dy, const void *z, int64_t T, int6
  *   y[t] = sum_j weights[t, j] h_tj Wd_e^T, h_tj = bf16(act(x_t Wg_e^T) * (x_t Wu_e^T)), e = experts[t, j],
  *   gate_up a stack of E weights [2F, K], down one of E weights [N, F]; weights f32
  *   and experts int32 [T, k] (values outside 0 .. E - 1: no expert, which counts as
- *   the weight times zero); ws fp8_w4_experts_workspace_size bytes, of one call at a time.
+ *   the weight times zero; an expert may be named more than once, and k be more than E);
+ *   ws fp8_w4_experts_workspace_size bytes, of one call at a time.
  * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (E > 1024), WORKSPACE, CUDA. */
 typedef struct {
   const uint8_t *codes;
