@@ -697,11 +697,13 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 // tcgen05 from 17 tokens on, where it saves more than its second launch and workspace
 // cost the host (6 us): 32 tokens through [28672, 4096] 44.4 us here and 39.6 there, 64
 // tokens 79 and 42, 37 tokens through [2048, 512] 4.8 and 7.0.
-// Lists of uneven lengths from 24 tokens on in the mean (32 experts, [2 2048, 4096] and
-// [4096, 2048]: mean 16 250 and 330, 24 339 and 361, 32 398 and 367; 8 experts of
-// [28672, 4096]: 360 and 425, 451 and 437, 520 and 441).
+// Lists from 32 tokens on in the mean, with or without an expert (us, fp16 operands and
+// tcgen05: 32 experts, [2 2048, 4096] and [4096, 2048], mean 24 300 and 332, 32 366 and 336,
+// 64 661 and 483, 256 2402 and 1428; 8 experts of [2 14336, 4096] and [4096, 14336], 24 465
+// and 549, 32 577 and 551, 64 1074 and 803; shorter lists than the mean, 7 of 8 tokens of
+// 512 without an expert, 151 and 328).
 bool w4_is_wide(int64_t weights, int K, int64_t tokens, int lists) {
-  return tokens >= (lists > 1 ? 24 : 17) && K >= kChunk && weights >= 1 << 23;
+  return tokens >= (lists > 1 ? 32 : 17) && K >= kChunk && weights >= 1 << 23;
 }
 
 // As few as let all blocks run within two waves (a warp to 256 of K, 16 to an SM): a

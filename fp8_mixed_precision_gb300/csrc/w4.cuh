@@ -6,10 +6,6 @@
 
 namespace fp8lin {
 
-// The tokens of an expert: first row in the experts' order and count.
-struct Tokens {
-  int e, first, count;
-};
 // A list's work for one item of the weight's rows, as kernels of `tile` tokens (8, 16 or
 // 32) at a time take them: what a block does for the codes is worth as much as for eight
 // tokens' products.

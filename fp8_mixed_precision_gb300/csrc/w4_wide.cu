@@ -47,9 +47,10 @@ struct Control {
   int abort;
 };
 
+// lists: first token and tiles of tokens before each, and behind the last one.
 template <int TN>
-constexpr int smem_bytes() {
-  return 1024 + kStagesB * TN * kDepth * 2 + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control);
+constexpr int smem_bytes(int lists) {
+  return 1024 + kStagesB * TN * kDepth * 2 + kWorkers * kRing * (kCodes + kZeros) + (int)sizeof(Control) + 8 * (lists + 1);
 }
 
 // D[tmem] (+)= A[tmem] B[smem]^T on bf16 operands, issued by one thread.
@@ -93,15 +94,11 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, int j, uint32_t zz, ui
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// One unit of work: 128 weight rows (gated: 64 of the gate, 64 of the up projection)
-// by one part of K.
+// One unit of work: 128 weight rows (gated: 64 of the gate, 64 of the up projection) by
+// one part of K, for one tile of a list's tokens.
 struct Unit {
-  int tile, part, kb0, kbs;
+  int e, token, count, tile, part, kb0, kbs;  // first token, and the list's tokens from it on
 };
-__device__ __forceinline__ Unit unit_of(int u, int parts, int kbs, int per) {
-  const int tile = u / parts, part = u - tile * parts;
-  return {tile, part, part * per, min(per, kbs - part * per)};
-}
 
 template <int TN, int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -116,6 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *opB = smem;
   uint8_t *rings = opB + kStagesB * kOperandB;
   Control *ctl = reinterpret_cast<Control *>(rings + kWorkers * kRing * (kCodes + kZeros));
+  const int lists = a.experts ? a.E : 1;
+  int *first = reinterpret_cast<int *>(ctl + 1), *before = first + lists + 1;  // of each list, and behind the last
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -132,6 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(&ctl->mma_done, 1);
     ctl->abort = 0;
+    if (!a.experts) {
+      first[0] = before[0] = 0;
+      first[1] = a.T;
+      before[1] = (a.T + TN - 1) / TN;
+    }
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tmX);
   }
@@ -151,9 +155,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   // that are then wrong, at addresses that are not), since TMEM's loads and stores are
   // instructions of all lanes and another lane may have seen the phase end after all.  A unit
   // later the warp leaves as one.
-  const Tokens tk = a.experts ? Tokens{(int)blockIdx.y, a.offsets[blockIdx.y], a.counts[blockIdx.y]} : Tokens{0, 0, a.T};
-  const int per = a.gated ? 64 : 128, tiles = (a.N + per - 1) / per, units = tiles * parts;
-  const int kbs = (a.K + kDepth - 1) / kDepth;
+  const int per = a.gated ? 64 : 128, kbs = (a.K + kDepth - 1) / kDepth;
+  // The lists' units, one list's after the other's, are dealt out to the blocks, the tiles of
+  // tokens for the same weights in a row (so the codes come from memory once, from L2 then).
+  // With as many blocks for every list, 1024 tokens x 2 of 32 experts [2 2048, 4096] and
+  // [4096, 2048] took 711 us, and 5278 where two experts had them all; like this 483 and 348.
+  const int slices = (a.N + per - 1) / per * parts;
+  if (a.experts) {
+    for (int l = threadIdx.x; l <= lists; l += kThreads) first[l] = a.offsets[l];
+    __syncthreads();
+    if (warp == 0) {
+      int sum = 0;
+      for (int l0 = 0; l0 < lists; l0 += 32) {
+        const int l = l0 + lane, n = l < lists ? (first[l + 1] - first[l] + TN - 1) / TN : 0;
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += v;
+        }
+        if (l < lists) before[l] = sum + s - n;
+        sum += __shfl_sync(0xffffffffu, s, 31);
+      }
+      if (lane == 0) before[lists] = sum;
+    }
+    __syncthreads();
+  }
+  const int units = before[lists] * slices;
+  // Unit u < units, for u that only grow; l: its list, 0 at first.
+  const auto unit_of = [&](int u, int &l) {
+    while (u >= before[l + 1] * slices) ++l;
+    const int n = before[l + 1] - before[l], rest = u - before[l] * slices;
+    const int slice = n == 1 ? rest : rest / n, tb = (rest - slice * n) * TN;
+    const int tile = slice / parts, part = slice - tile * parts;
+    return Unit{l, first[l] + tb, first[l + 1] - first[l] - tb, tile, part, part * per_part, min(per_part, kbs - part * per_part)};
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -162,27 +198,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int last_phase[kStagesB];
       for (int s = 0; s < kStagesB; ++s) last_phase[s] = -1;
       bool ok = true;
-      for (int tb = 0; ok && tb < tk.count; tb += TN)
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-          const Unit un = unit_of(u, parts, kbs, per_part);
-          for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
-            if (!wait(&ctl->b_empty[stage], phase ^ 1)) {
-              ok = false;
-              break;
-            }
-            // (rows past the list's are read too, and not stored)
-            ptx::mbar_arrive_expect_tx(&ctl->b_full[stage], kOperandB);
-            uint8_t *b = opB + stage * kOperandB;
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-              for (int r = 0; r < TN; r += 32)
-                ptx::tma_load_2d(b + half * (TN * 128) + r * 128, &tmX, &ctl->b_full[stage], kb * kDepth + 64 * half,
-                                 tk.first + tb + r);
-            last_phase[stage] = (int)phase;
-            if (++stage == kStagesB) stage = 0, phase ^= 1;
+      int l = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit un = unit_of(u, l);
+        for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
+          if (!wait(&ctl->b_empty[stage], phase ^ 1)) {
+            ok = false;
+            break;
           }
+          // (rows past the list's are read too, and not stored)
+          ptx::mbar_arrive_expect_tx(&ctl->b_full[stage], kOperandB);
+          uint8_t *b = opB + stage * kOperandB;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int r = 0; r < TN; r += 32)
+              ptx::tma_load_2d(b + half * (TN * 128) + r * 128, &tmX, &ctl->b_full[stage], kb * kDepth + 64 * half,
+                               un.token + r);
+          last_phase[stage] = (int)phase;
+          if (++stage == kStagesB) stage = 0, phase ^= 1;
         }
+      }
       if (!ok)  // let every issued copy land before the CTA can exit
         for (int s = 0; s < kStagesB; ++s)
           if (last_phase[s] >= 0) pipe::drain_wait(&ctl->b_full[s], (uint32_t)last_phase[s], &g_w4_wide_status);
@@ -193,38 +229,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, stage_b = 0;
       uint32_t phase = 0, phase_b = 0, nacc = 0;
       bool ok = true;
-      for (int tb = 0; ok && tb < tk.count; tb += TN)
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-          const Unit un = unit_of(u, parts, kbs, per_part);
-          for (int kb = 0; ok && kb < un.kbs; ++kb) {
-            if (!wait(&ctl->b_full[stage_b], phase_b) || !wait(&ctl->a_full[stage], phase)) {
+      int l = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit un = unit_of(u, l);
+        for (int kb = 0; ok && kb < un.kbs; ++kb) {
+          if (!wait(&ctl->b_full[stage_b], phase_b) || !wait(&ctl->a_full[stage], phase)) {
+            ok = false;
+            break;
+          }
+          const uint32_t ta = tmem + stage * kColsA;
+          const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage_b * kOperandB));
+          for (int g = 0; g < kGroups; ++g) {
+            if (!wait(&ctl->acc_empty[nacc % kAcc], (nacc / kAcc & 1) ^ 1)) {
               ok = false;
               break;
             }
-            const uint32_t ta = tmem + stage * kColsA;
-            const uint64_t bd = ptx::smem_desc_sw128(ptx::smem_u32(opB + stage_b * kOperandB));
-            for (int g = 0; g < kGroups; ++g) {
-              if (!wait(&ctl->acc_empty[nacc % kAcc], (nacc / kAcc & 1) ^ 1)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
+            ptx::tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < kSteps; ++k) {
-                const int step = g * kSteps + k;  // 16 deep: 32 bytes of a panel of 64
-                mma_bf16(acc0 + nacc % kAcc * TN, ta + 8 * step, bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4),
-                         idesc, k > 0);
-              }
-              ptx::mma_commit(&ctl->acc_full[nacc % kAcc]);
-              ++nacc;
+            for (int k = 0; k < kSteps; ++k) {
+              const int step = g * kSteps + k;  // 16 deep: 32 bytes of a panel of 64
+              mma_bf16(acc0 + nacc % kAcc * TN, ta + 8 * step, bd + (step / 4) * (TN * 128 >> 4) + 2 * (step % 4),
+                       idesc, k > 0);
             }
-            if (!ok) break;
-            ptx::mma_commit(&ctl->a_empty[stage]);
-            ptx::mma_commit(&ctl->b_empty[stage_b]);
-            if (++stage == kStages) stage = 0, phase ^= 1;
-            if (++stage_b == kStagesB) stage_b = 0, phase_b ^= 1;
+            ptx::mma_commit(&ctl->acc_full[nacc % kAcc]);
+            ++nacc;
           }
+          if (!ok) break;
+          ptx::mma_commit(&ctl->a_empty[stage]);
+          ptx::mma_commit(&ctl->b_empty[stage_b]);
+          if (++stage == kStages) stage = 0, phase ^= 1;
+          if (++stage_b == kStagesB) stage_b = 0, phase_b ^= 1;
         }
+      }
       ptx::mma_commit(&ctl->mma_done);
       pipe::drain_wait(&ctl->mma_done, 0, &g_w4_wide_status);
     }
@@ -236,53 +272,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       return (a.gated && row >= 64 ? a.N : 0) + min(un.tile * per + (a.gated ? row & 63 : row), a.N - 1);
     };
     const auto first_scale = [&](const Unit &un) {
-      return bf16lo(a.scale[((int64_t)tk.e * a.rows + row_of(un)) * a.groups + un.kb0 * kGroups]);
+      return bf16lo(a.scale[((int64_t)un.e * a.rows + row_of(un)) * a.groups + un.kb0 * kGroups]);
     };
     uint32_t nacc = 0;
     bool lost = false;
+    int l = 0;
+    Unit un = {}, then;
     float ahead = 0.0f;  // the next unit's first scale, a round trip to memory before its use
-    if (tk.count > 0 && (int)blockIdx.x < units) ahead = first_scale(unit_of(blockIdx.x, parts, kbs, per_part));
-    for (int tb = 0; tb < tk.count; tb += TN)
-      for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        if (__any_sync(0xffffffffu, lost)) break;
-        const Unit un = unit_of(u, parts, kbs, per_part);
-        const int out = un.tile * per + (a.gated ? row & 63 : row), wrow = row_of(un);
-        const uint16_t *scale = a.scale + ((int64_t)tk.e * a.rows + wrow) * a.groups;
-        float tot[TN] = {};
-        float next = ahead;
-        ahead = first_scale(unit_of(u + gridDim.x < units ? u + gridDim.x : blockIdx.x, parts, kbs, per_part));
-        for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb)
+    if ((int)blockIdx.x < units) ahead = first_scale(un = unit_of(blockIdx.x, l));
+    for (int u = blockIdx.x; u < units; u += gridDim.x, un = then) {
+      if (__any_sync(0xffffffffu, lost)) break;
+      then = u + (int)gridDim.x < units ? unit_of(u + gridDim.x, l) : un;
+      const int out = un.tile * per + (a.gated ? row & 63 : row), wrow = row_of(un);
+      const uint16_t *scale = a.scale + ((int64_t)un.e * a.rows + wrow) * a.groups;
+      float tot[TN] = {};
+      float next = ahead;
+      ahead = first_scale(then);
+      for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb)
 #pragma unroll 1
-          for (int g = kb * kGroups; g < (kb + 1) * kGroups; ++g) {
-            const float s = next;
-            // (groups past the last one are products with zeros)
-            next = bf16lo(scale[min(g + 1, a.groups - 1)]);
-            const uint32_t ab = nacc % kAcc;
-            lost |= !wait(&ctl->acc_full[ab], nacc / kAcc & 1);
-            ptx::tc_fence_after();
+        for (int g = kb * kGroups; g < (kb + 1) * kGroups; ++g) {
+          const float s = next;
+          // (groups past the last one are products with zeros)
+          next = bf16lo(scale[min(g + 1, a.groups - 1)]);
+          const uint32_t ab = nacc % kAcc;
+          lost |= !wait(&ctl->acc_full[ab], nacc / kAcc & 1);
+          ptx::tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < TN; i += 32) {
-              uint32_t r[32];
-              ptx::tmem_ld32(tl + ab * TN + i, r);
-              ptx::tmem_ld_wait();
-              if (i + 32 == TN) {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
-              }
-#pragma unroll
-              for (int j = 0; j < 32; ++j) tot[i + j] = fmaf(__uint_as_float(r[j]), s, tot[i + j]);
+          for (int i = 0; i < TN; i += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tl + ab * TN + i, r);
+            ptx::tmem_ld_wait();
+            if (i + 32 == TN) {
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(&ctl->acc_empty[ab]);
             }
-            ++nacc;
-          }
-        if (lost || out >= a.N) continue;
-        // a part's sums: token by token, 32 rows at a time
-        float *to = static_cast<float *>(a.part) + ((int64_t)un.part * a.P + tk.first + tb) * a.rows + wrow;
-        const int count = min(TN, tk.count - tb);
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-          if (i < count) to[(int64_t)i * a.rows] = tot[i];
-      }
+            for (int j = 0; j < 32; ++j) tot[i + j] = fmaf(__uint_as_float(r[j]), s, tot[i + j]);
+          }
+          ++nacc;
+        }
+      if (lost || out >= a.N) continue;
+      // a part's sums: token by token, 32 rows at a time
+      float *to = static_cast<float *>(a.part) + ((int64_t)un.part * a.P + un.token) * a.rows + wrow;
+      const int count = min(TN, un.count);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        if (i < count) to[(int64_t)i * a.rows] = tot[i];
+    }
   } else {
     const int quarter = warp & 3, half = (warp - 6) >> 2;  // rows 32 quarter .. of the tile, codes 64 half ..
     uint8_t *ring = rings + (warp - 6) * kRing * (kCodes + kZeros);
@@ -297,19 +334,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cto = place(crow, cp);  // (16 rows on: 512 bytes)
     const int from0 = place(lane, 0), from1 = place(lane, 1);
     // the first row of a unit's sixteen rows `j` of this warp, within the stack
-    const auto first_row = [&](int tile, int j) {
-      const int r = (a.gated ? tile * 64 + (quarter & 1) * 32 : tile * 128 + quarter * 32) + 16 * j;
-      return (int64_t)tk.e * a.rows + (a.gated ? (quarter >> 1) * a.N : 0) + min(r, a.N - 16);  // past the last: not stored
+    const auto first_row = [&](const Unit &un, int j) {
+      const int r = (a.gated ? un.tile * 64 + (quarter & 1) * 32 : un.tile * 128 + quarter * 32) + 16 * j;
+      return (int64_t)un.e * a.rows + (a.gated ? (quarter >> 1) * a.N : 0) + min(r, a.N - 16);  // past the last: not stored
     };
     // the request that runs kRing - 1 stages ahead: its unit, and where that continues
-    int ru = blockIdx.x, rkb = 0, rkbs = 0, rtb = 0, into = 0;
+    int ru = blockIdx.x, rl = 0, rkb = 0, rkbs = 0, into = 0;
     const uint8_t *rsrc0 = nullptr, *rsrc1 = nullptr;  // this lane's next pieces
     int64_t rzero = 0;                                 // this lane's row's zero points
     const auto begin = [&] {
-      const Unit un = unit_of(ru, parts, kbs, per_part);
+      const Unit un = unit_of(ru, rl);
       rkb = un.kb0;
       rkbs = un.kbs;
-      const int64_t r0 = first_row(un.tile, 0), r1 = first_row(un.tile, 1);
+      const int64_t r0 = first_row(un, 0), r1 = first_row(un, 1);
       const int at = rkb * (kDepth / 2) + 32 * half + 16 * cp;
       rsrc0 = a.codes + (r0 + crow) * row_bytes + at;
       rsrc1 = a.codes + (r1 + crow) * row_bytes + at;
@@ -318,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ru < units) begin();
     const auto group_of = [&](int kb) { return kb * kGroups + (kGroups > 1 ? half * kHalfGroups : 0); };
     const auto request = [&] {
-      if (rtb < tk.count && ru < units) {
+      if (ru < units) {
         uint8_t *dst = ring + into * (kCodes + kZeros);
         if (rkb < a.K / kDepth) {
           ptx::cp_async16(dst + cto, rsrc0);
@@ -344,8 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rsrc1 += kDepth / 2;
         if (--rkbs == 0) {
           ru += gridDim.x;
-          if (ru >= units) ru = blockIdx.x, rtb += TN;
-          begin();
+          if (ru < units) begin();
         }
       }
       ptx::cp_async_commit();
@@ -358,45 +394,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, held = 0;
     uint32_t phase = 0;
     bool lost = false;
-    for (int tb = 0; tb < tk.count; tb += TN)
-      for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        if (__any_sync(0xffffffffu, lost)) break;
-        const Unit un = unit_of(u, parts, kbs, per_part);
-        const int64_t zero = (first_row(un.tile, lane >> 4) + (lane & 15)) * a.groups;
-        for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
-          cp_async_wait_group<kRing - 2>();
-          __syncwarp();
-          const uint8_t *src = ring + held * (kCodes + kZeros);
-          const uint4 w[2] = {*reinterpret_cast<const uint4 *>(src + from0), *reinterpret_cast<const uint4 *>(src + from1)};
-          uint32_t zz[2];  // of each piece's group
+    int l = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      if (__any_sync(0xffffffffu, lost)) break;
+      const Unit un = unit_of(u, l);
+      const int64_t zero = (first_row(un, lane >> 4) + (lane & 15)) * a.groups;
+      for (int kb = un.kb0; kb < un.kb0 + un.kbs; ++kb) {
+        cp_async_wait_group<kRing - 2>();
+        __syncwarp();
+        const uint8_t *src = ring + held * (kCodes + kZeros);
+        const uint4 w[2] = {*reinterpret_cast<const uint4 *>(src + from0), *reinterpret_cast<const uint4 *>(src + from1)};
+        uint32_t zz[2];  // of each piece's group
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t z = 8u;
-            if (a.zero) z = src[kCodes + 8 * lane + (int)((zero + group_of(kb)) & 3) + (GROUP == 32 ? i : 0)] & 15u;
-            zz[i] = (0x4300u | z) * 0x10001u;
-          }
-          __syncwarp();
-          request();  // into the tile before this one, which every lane has read
-          held = held == kRing - 1 ? 0 : held + 1;
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = w[i >> 2];
-            const uint32_t word = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[4 * i + j] = two_codes(word, j, zz[i >> 2], mask, bias);
-          }
-          lost |= !wait(&ctl->a_empty[stage], phase ^ 1);
-          __syncwarp();
-          ptx::tc_fence_after();
-          tmem_st32(ta + stage * kColsA, r);
-          tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl->a_full[stage]);
-          if (++stage == kStages) stage = 0, phase ^= 1;
+        for (int i = 0; i < 2; ++i) {
+          uint32_t z = 8u;
+          if (a.zero) z = src[kCodes + 8 * lane + (int)((zero + group_of(kb)) & 3) + (GROUP == 32 ? i : 0)] & 15u;
+          zz[i] = (0x4300u | z) * 0x10001u;
         }
+        __syncwarp();
+        request();  // into the tile before this one, which every lane has read
+        held = held == kRing - 1 ? 0 : held + 1;
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = w[i >> 2];
+          const uint32_t word = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[4 * i + j] = two_codes(word, j, zz[i >> 2], mask, bias);
+        }
+        lost |= !wait(&ctl->a_empty[stage], phase ^ 1);
+        __syncwarp();
+        ptx::tc_fence_after();
+        tmem_st32(ta + stage * kColsA, r);
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctl->a_full[stage]);
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
+    }
     cp_async_wait_group<0>();
   }
   __syncwarp();
@@ -415,13 +451,17 @@ cudaError_t launch_wide(const W4Args &a, const CUtensorMap &tm, const W4Plan &p,
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(w4_wide_kernel<TN, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem_bytes<TN>());
+                                               smem_bytes<TN>(kMaxExperts));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   const int kbs = (a.K + kDepth - 1) / kDepth;
-  return launch_kernel(w4_wide_kernel<TN, GROUP>, dim3((unsigned)p.blocks, (unsigned)lists), dim3(kThreads),
-                       (size_t)smem_bytes<TN>(), st, tm, a, p.parts, (kbs + p.parts - 1) / p.parts);
+  const int per = a.gated ? 64 : 128;
+  // no list has more tiles of tokens than this says, whatever the tokens' choice
+  const int64_t units = ((int64_t)a.P / TN + lists) * ((a.N + per - 1) / per) * p.parts;
+  if (units > INT32_MAX - (1 << 20)) return cudaErrorInvalidValue;  // units are counted in 32 bits
+  return launch_kernel(w4_wide_kernel<TN, GROUP>, dim3((unsigned)std::min<int64_t>(p.blocks, units)), dim3(kThreads),
+                       (size_t)smem_bytes<TN>(a.experts ? a.E : 1), st, tm, a, p.parts, (kbs + p.parts - 1) / p.parts);
 }
 template <int TN>
 cudaError_t by_group(const W4Args &a, const CUtensorMap &tm, const W4Plan &p, int lists, cudaStream_t st) {
@@ -437,19 +477,20 @@ W4Plan w4_wide_plan(int N, int K, bool gated, int tokens, int lists, int64_t P) 
   best.nt = tokens <= 32 ? 4 : 8;
   best.wide = true;
   const int64_t sms = num_sms(), per = gated ? 64 : 128, tiles = (N + per - 1) / per, kbs = (K + kDepth - 1) / kDepth;
+  // of tokens, if the lists are of one length
+  const int64_t each_list = (P + lists - 1) / lists, token_tiles = lists * ((each_list + 8 * best.nt - 1) / (8 * best.nt));
+  best.blocks = (int)sms;
   double least = 0.0;
   for (int64_t parts = 1; parts <= 8 && parts <= kbs; ++parts) {
-    const int64_t each = (kbs + parts - 1) / parts, units = tiles * ((kbs + each - 1) / each);
-    const int64_t blocks = std::max<int64_t>(1, std::min(units, sms / lists));
-    const int64_t rounds = (units + blocks - 1) / blocks, waves = (blocks * lists + sms - 1) / sms;
+    const int64_t each = (kbs + parts - 1) / parts, slices = tiles * ((kbs + each - 1) / each);
+    const int64_t rounds = (token_tiles * slices + sms - 1) / sms;
     // in times of an SM's share of memory bandwidth for a stage of 8 KB, 0.2 us: a unit's
     // beginning and end cost about 4; the sums' bytes are written and read
-    const double cost = (double)(waves * rounds * (each + 4)) +
+    const double cost = (double)(rounds * (each + 4)) +
                         8.0 * (double)P * N * (gated ? 2 : 1) * (double)parts / (8192.0 * (double)sms);
-    if (best.blocks == 0 || cost < least) {
+    if (best.parts == 0 || cost < least) {
       least = cost;
       best.parts = (int)((kbs + each - 1) / each);
-      best.blocks = (int)blocks;
     }
   }
   best.planes = best.parts;

@@ -26,7 +26,8 @@ def experts(x, e, w, vgu, vdn, act):
 
 
 @pytest.mark.parametrize("E,k,K,F,N", [
-    (1, 17, 2048, 2048, 2048), (2, 48, 2048, 2048, 1040), (1, 17, 256, 16384, 512), (1, 40, 32, 16384, 512),  # tcgen05 plans
+    (1, 17, 2048, 2048, 2048), (2, 64, 2048, 2048, 1040), (1, 17, 256, 16384, 512), (1, 40, 32, 16384, 512),  # tcgen05
+    (2, 48, 2048, 2048, 1040),
     (2, 60, 4096, 1024, 64), (1, 2, 512, 256, 512), (3, 4, 96, 64, 48), (4, 300, 256, 96, 64), (1, 70000, 32, 32, 16)])
 @pytest.mark.parametrize("group,zero,act", [(32, True, "silu"), (128, False, "gelu")])
 @pytest.mark.parametrize("kind", ["random", "one", "holes", "none"])
@@ -70,14 +71,16 @@ def test_prompt(fp, N, K, T):  # noqa: F811
         assert bool(((h - want).abs() <= (bound + want.abs() * UB) * 1.01 + 1e-38).all())
 
 
-@pytest.mark.parametrize("T,E,k,K,F,N", [(2500, 4, 2, 544, 1024, 1040), (3001, 16, 3, 128, 64, 64)])
+@pytest.mark.parametrize("T,E,k,K,F,N", [(2500, 4, 2, 544, 1024, 1040), (3001, 16, 3, 128, 64, 64), (700, 5, 3, 1056, 1024, 1040),
+                                         (4000, 200, 2, 256, 96, 160), (16500, 1000, 2, 256, 256, 32)])
 def test_prompt_of_experts(fp, T, E, k, K, F, N):  # noqa: F811
     gu, vgu = weight(fp, (E, 2 * F, K), 64, True, 1)
     dn, vdn = weight(fp, (E, N, F), 64, False, 2)
     g = torch.Generator().manual_seed(3)
     x = torch.randn((T, K), generator=g).bfloat16().cuda()
-    e = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    e = torch.randint(0, max(1, 3 * E // 4), (T, k), generator=g, dtype=torch.int32)  # the last quarter without a token
     e[: T // 3] = 1                                   # one long list, the same expert in each slot
+    e[T // 3:][e[T // 3:] % 5 == 2] = 0               # others without one between them
     e[torch.rand((T, k), generator=g) < 0.1] = -1
     e, w = e.cuda(), torch.rand((T, k), generator=g).cuda()
     y = fp.fp8_w4_experts(x, w, e, gu, dn)

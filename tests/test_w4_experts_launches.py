@@ -69,9 +69,11 @@ def launches(tmp_path_factory):
 
 
 @pytest.mark.parametrize("T,E,k,K,F,N", [
-    (1, 1, 17, 4096, 4096, 4096), (1, 2, 48, 4096, 4096, 4096), (1, 1, 17, 256, 32768, 16), (1, 1, 17, 32, 32768, 256),
+    (1, 1, 17, 4096, 4096, 4096), (1, 2, 48, 4096, 4096, 4096), (1, 2, 64, 4096, 4096, 4096), (1, 1, 17, 256, 32768, 16),
+    (1, 1, 17, 32, 32768, 256),
     (1, 4, 1000, 2048, 2048, 2048), (1, 3, 4, 96, 64, 48), (1, 8, 2, 4096, 14336, 4096), (1, 8, 8, 512, 512, 512),
-    (1, 1, 1, 4096, 4096, 4096), (2, 1, 17, 4096, 4096, 4096), (64, 32, 4, 4096, 2048, 4096), (600, 8, 2, 4096, 14336, 4096)])
+    (1, 1, 1, 4096, 4096, 4096), (2, 1, 17, 4096, 4096, 4096), (64, 32, 4, 4096, 2048, 4096),
+    (600, 8, 2, 4096, 14336, 4096)])
 def test_order_comes_before_what_takes_it(launches, T, E, k, K, F, N):
     calls = launches(T, E, k, K, F, N)
     assert [c[0] for c in calls if c[0] in ("product", "join")] == ["product", "product", "join"]
