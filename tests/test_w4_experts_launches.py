@@ -2,6 +2,7 @@
 loaded before it, writes down their arguments in place of launching.  Kernels that
 take the tokens' order (the copy of rows into it, and the products of many tokens)
 run only where the same call has made it."""
+import json
 import os
 import subprocess
 import sys
@@ -37,22 +38,31 @@ cudaError_t launch_w4_join(const float *, const int *, const int *position, cons
 }  // namespace fp8lin
 '''
 
+SHAPES = [
+    (1, 1, 17, 4096, 4096, 4096), (1, 2, 48, 4096, 4096, 4096), (1, 2, 64, 4096, 4096, 4096), (1, 1, 17, 256, 32768, 16),
+    (1, 1, 17, 32, 32768, 256),
+    (1, 4, 1000, 2048, 2048, 2048), (1, 3, 4, 96, 64, 48), (1, 8, 2, 4096, 14336, 4096), (1, 8, 8, 512, 512, 512),
+    (1, 1, 1, 4096, 4096, 4096), (2, 1, 17, 4096, 4096, 4096), (64, 32, 4, 4096, 2048, 4096),
+    (600, 8, 2, 4096, 14336, 4096)]
+
 CHILD = r'''
-import ctypes, sys
+import ctypes, json, sys
 import fp8_mixed_precision_gb300 as fp
-L = fp.lib()
-T, E, k, K, F, N = map(int, sys.argv[1:])
+L, libc = fp.lib(), ctypes.CDLL(None)
 A = 1 << 20  # never dereferenced
-b = ctypes.c_size_t()
-assert L.fp8_w4_experts_workspace_size(T, k, E, K, F, N, ctypes.byref(b)) == 0
-gu, dn = fp._W4(A, A, None, E, 2 * F, K, 128), fp._W4(A, A, None, E, N, F, 128)
-assert L.fp8_w4_experts(A, T, k, A, A, gu, dn, 0, A, A, b.value, None) == 0
-ctypes.CDLL(None).fflush(None)
+for T, E, k, K, F, N in json.loads(sys.argv[1]):
+    b = ctypes.c_size_t()
+    assert L.fp8_w4_experts_workspace_size(T, k, E, K, F, N, ctypes.byref(b)) == 0
+    gu, dn = fp._W4(A, A, None, E, 2 * F, K, 128), fp._W4(A, A, None, E, N, F, 128)
+    assert L.fp8_w4_experts(A, T, k, A, A, gu, dn, 0, A, A, b.value, None) == 0
+    libc.printf(b"end\n")
+libc.fflush(None)
 '''
 
 
 @pytest.fixture(scope="module")
 def launches(tmp_path_factory):
+    """The launches of each shape, as lists of words."""
     from fp8_mixed_precision_gb300 import build
     build.build()
     tmp = tmp_path_factory.mktemp("stub")
@@ -60,22 +70,17 @@ def launches(tmp_path_factory):
     so = str(tmp / "stub.so")
     subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I" + build.CSRC, "-I" + build.INCLUDE,
                     "-I" + os.path.join(build._cuda_home(), "include"), str(tmp / "stub.cpp"), "-o", so], check=True)
-    def run(*shape):
-        r = subprocess.run([sys.executable, "-c", CHILD, *map(str, shape)], cwd=ROOT, capture_output=True, text=True,
-                           env=dict(os.environ, LD_PRELOAD=so, PYTHONPATH=ROOT))
-        assert r.returncode == 0, r.stderr[-2000:]
-        return [line.split() for line in r.stdout.splitlines()]
-    return run
+    r = subprocess.run([sys.executable, "-c", CHILD, json.dumps(SHAPES)], cwd=ROOT, capture_output=True, text=True,
+                       env=dict(os.environ, LD_PRELOAD=so, PYTHONPATH=ROOT))
+    assert r.returncode == 0, r.stderr[-2000:]
+    parts = r.stdout.split("end\n")
+    assert len(parts) == len(SHAPES) + 1
+    return {s: [line.split() for line in p.splitlines()] for s, p in zip(SHAPES, parts)}
 
 
-@pytest.mark.parametrize("T,E,k,K,F,N", [
-    (1, 1, 17, 4096, 4096, 4096), (1, 2, 48, 4096, 4096, 4096), (1, 2, 64, 4096, 4096, 4096), (1, 1, 17, 256, 32768, 16),
-    (1, 1, 17, 32, 32768, 256),
-    (1, 4, 1000, 2048, 2048, 2048), (1, 3, 4, 96, 64, 48), (1, 8, 2, 4096, 14336, 4096), (1, 8, 8, 512, 512, 512),
-    (1, 1, 1, 4096, 4096, 4096), (2, 1, 17, 4096, 4096, 4096), (64, 32, 4, 4096, 2048, 4096),
-    (600, 8, 2, 4096, 14336, 4096)])
+@pytest.mark.parametrize("T,E,k,K,F,N", SHAPES)
 def test_order_comes_before_what_takes_it(launches, T, E, k, K, F, N):
-    calls = launches(T, E, k, K, F, N)
+    calls = launches[T, E, k, K, F, N]
     assert [c[0] for c in calls if c[0] in ("product", "join")] == ["product", "product", "join"]
     made = [c for c in calls if c[0] == "order"]
     assert len(made) <= 1 and (not made or calls[0] is made[0])
