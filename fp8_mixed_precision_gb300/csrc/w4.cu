@@ -561,7 +561,10 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const float *__restrict__ 
 //   without zero points  scale = bf16(max |w| / 7), code = 8 + round(w / scale) in 0..15
 //   with                 scale = bf16((max - min) / 15) over the group and 0,
 //                        zero = round(-min / scale) in 0..15, code = zero + round(w / scale) in 0..15
-// A group of zeros has scale 1.
+// A group of zeros has scale 1.  Once per weight that is loaded, so not tuned; bound by
+// the instructions of a warp's group (two maxima over 32 lanes, four divisions a lane):
+// [28672, 4096] in groups of 128 191 us, of 64 with zero points 631, of 32 1253, for
+// 44 at the copy rate.
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const void *__restrict__ w, int64_t rows, int K, int group,
                                                           int groups, uint8_t *__restrict__ codes,
                                                           uint16_t *__restrict__ scale, uint8_t *__restrict__ zero) {

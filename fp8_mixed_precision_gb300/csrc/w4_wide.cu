@@ -14,6 +14,8 @@
 // What bounds it is the chain of barriers for each 128-deep stage: without any MMA or
 // arithmetic on the codes it takes 30.
 //
+// Every 64 tokens convert the codes again: 2048 tokens take 1409 us, 44 for each 64.
+//
 // Warps: 0 requests the tokens' tiles, 1 issues the MMAs, 2-5 are the epilogue, 6-13
 // turn codes into operands: 32 rows (the TMEM lanes of the warp) by half a stage each.
 #include <algorithm>
