@@ -20,7 +20,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 1) {
+    if ((it & 7) == 0) {
       if (*abort) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
         atomicCAS(status, 0u, (unsigned)FP8_ERR_TIMEOUT);

@@ -697,9 +697,11 @@ cudaError_t by_zero(const W4Args &a, const W4Plan &p, int lists, cudaStream_t st
 
 }  // namespace
 
-// tcgen05 from 17 tokens on, where it saves more than its second launch and workspace
-// cost the host (6 us): 32 tokens through [28672, 4096] 44.4 us here and 39.6 there, 64
-// tokens 79 and 42, 37 tokens through [2048, 512] 4.8 and 7.0.
+// tcgen05 from 17 tokens and 2^23 weights on, where it saves more than its second launch
+// and workspace cost the host (6 us): 32 tokens through [28672, 4096] 44.4 us here and 38.7
+// there, 64 tokens 79 and 43; 32 and 64 tokens through [2048, 1024] 4.6 and 6.7, 6.5 and
+// 7.8, [2048, 2048] 6.7 and 7.2, 9.1 and 9.7, [4096, 1024] 6.6 and 7.3, 9.7 and 9.4, [4096,
+// 2048] 9.0 and 9.1, 10.6 and 10.6; 37 through [2048, 512] 4.8 and 7.0.
 // Lists from 32 tokens on in the mean, with or without an expert (us, fp16 operands and
 // tcgen05: 32 experts, [2 2048, 4096] and [4096, 2048], mean 24 300 and 332, 32 366 and 336,
 // 64 661 and 483, 256 2402 and 1428; 8 experts of [2 14336, 4096] and [4096, 14336], 24 465

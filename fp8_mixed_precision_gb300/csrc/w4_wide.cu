@@ -10,7 +10,7 @@
 // a part of K go to memory and are added by the kernel that follows.
 //
 // On mma.m16n8k16, which moves every product's operands through the register file, 64
-// tokens through [28672, 4096] took 88 us for the 42.4 here (1.4 TB/s of codes; 62 MB).
+// tokens through [28672, 4096] took 88 us for the 43.1 here (1.4 TB/s of codes; 62 MB).
 // What bounds it is the chain of barriers for each 128-deep stage: without any MMA or
 // arithmetic on the codes it takes 30.
 //
